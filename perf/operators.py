@@ -1,0 +1,369 @@
+"""The operators over 4-bit caches and selected chunks, as a serving program calls them.
+
+Four operators of the prefix-shared KV cache:
+
+  store   prompts join an fp4 cache (quantised on insert) and their rows are read back dequantised
+  decode  decode attention over an fp4 cache
+  select  the chunks that a cheap upper bound on the scores picks for each sequence and key/value head
+  sparse  decode attention over the selected chunks alone
+
+A case holds a batch of sequences: `shared` tokens that all of them begin with, then private tokens, `private` of them
+less (37 i) mod (spread + 1) for sequence i.  Their rows are cut into chunks of `chunk` tokens.
+
+fp4: blocks of 16 consecutive dims share one E4M3 scale.  With y = fp32(x) * fp32(1 / S) (S the cache's own scale of
+keys or values), scale = E4M3(max|y| * fp32(1/6)) and code = E2M1(y * fp32(1 / scale)), both to nearest even and
+saturating; the code stands for code * scale * S.
+
+With `own` false everything is elementary torch operations; with it true the calls are the framework's.
+"""
+import numpy as np
+import torch
+
+own = False
+
+DEV = "cuda"
+E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+
+
+# ---------------------------------------------------------------------------- cases
+def _case(name, op, *, batch, shared=0, private, spread=0, layers=1, heads, kv_heads, dim=128, chunk=64, dtype="fp4",
+          k_scale=1.0, v_scale=1.0, q_len=1, top_k=0, sink=1, recent=1):
+    c = dict(op=op, batch=batch, shared=shared, private=private, spread=spread, layers=layers, heads=heads, kv_heads=kv_heads,
+             dim=dim, chunk=chunk, dtype=dtype, k_scale=k_scale, v_scale=v_scale, q_len=q_len, top_k=top_k, sink=sink, recent=recent)
+    return dict(c, name=name) if name else c
+
+
+def listed():
+    return [
+        # four short requests join a small cache: the latency of one insert, one read and one remove
+        _case("store_tiny", "store", batch=4, shared=64, private=16, heads=2, kv_heads=2, dim=64, chunk=16),
+        # a batch of prompts with grouped-query heads joins, lengths that end inside a chunk
+        _case("store_gqa", "store", batch=32, shared=1024, private=511, spread=300, heads=32, kv_heads=8, k_scale=0.75, v_scale=1.25),
+        # 32 unrelated prompts of 2048 tokens, one layer of 32 heads: the bandwidth of quantising and of reading back
+        _case("store_no_sharing", "store", batch=32, private=2048, heads=32, kv_heads=32),
+        # one decode step of a small batch: the latency of one call
+        _case("decode_tiny", "decode", batch=4, shared=64, private=16, heads=2, kv_heads=2, dim=64, chunk=16),
+        # a decode step over a common system prompt, 32 query heads on 8 key/value heads, ragged suffixes
+        _case("decode_gqa", "decode", batch=32, shared=1024, private=511, spread=300, heads=32, kv_heads=8, k_scale=0.75, v_scale=1.25),
+        # 64 sequences on a 4096-token prompt, one key/value head per query head: the benchmark's headline shape
+        _case("decode_s4096_b64", "decode", batch=64, shared=4096, private=512, heads=32, kv_heads=32),
+        # four draft tokens of each of 32 sequences are verified (causal), the last context tokens
+        _case("decode_q4", "decode", batch=32, shared=1024, private=512, heads=32, kv_heads=32, q_len=4),
+        # selection for a batch of ordinary contexts of an fp16 cache
+        _case("select_batch", "select", batch=32, shared=1024, private=2047, spread=900, heads=32, kv_heads=8, dtype="fp16", top_k=16),
+        # selection in contexts of 128 K tokens, where reading all keys would dominate a step
+        _case("select_long", "select", batch=8, private=131072, spread=5000, heads=32, kv_heads=8, dtype="fp16", top_k=64, sink=1, recent=2),
+        # one sequence attends to a few chunks of a small cache: the latency of one call
+        _case("sparse_one", "sparse", batch=1, private=1000, heads=8, kv_heads=2, dim=64, chunk=32, dtype="fp16", top_k=8),
+        # a batch attends to 64 of its chunks of a long fp16 cache
+        _case("sparse_fp16", "sparse", batch=16, private=32768, spread=3000, heads=32, kv_heads=8, dtype="fp16", top_k=64),
+        # the same with one key/value head per query head and the cache held in 4 bits
+        _case("sparse_fp4", "sparse", batch=16, private=16384, spread=1500, heads=32, kv_heads=32, dtype="fp4", top_k=64),
+    ]
+
+
+def draw(rng):
+    op = rng.choice(("store", "decode", "select", "sparse"))
+
+    def log(lo, hi):
+        return max(lo, min(hi, int(round(lo * (hi / lo) ** rng.random()))))
+
+    dtype = "fp4" if op in ("store", "decode") else rng.choice(("fp16", "fp8", "fp4"))
+    dim = {"fp16": rng.choice((64, 128, 256)), "fp8": 128, "fp4": rng.choice((64, 128))}[dtype]
+    chunk = rng.choice((16, 32) if dim == 256 else (16, 32, 64))
+    kv_heads = rng.choice((1, 2, 4, 8, 16))
+    group = rng.choice((1, 1, 2, 3, 4, 8))
+    batch = log(1, 48)
+    # tokens of the batch: with 16 heads and two layers as many rows as the largest listed cases have
+    most = (1 << (17 if op in ("select", "sparse") else 16)) // batch
+    shared = rng.choice((0, log(1, min(most // 2, 2048)))) if op != "sparse" else 0
+    least = 24 * chunk if op == "select" else 1                                 # a choice among many more chunks than are asked for
+    private = log(least, min(most - shared, 65536 if op in ("select", "sparse") else 4096))
+    spread = rng.randrange(private - least + 1)
+    # causal queries need contexts of at least q_len tokens
+    q_len = rng.choice((1, 1, 1, 2, 3)) if op == "decode" and shared + private - spread >= 3 else 1
+    sink, recent = rng.choice((0, 1, 2)), rng.choice((1, 1, 2))
+    top_k = max(sink + recent, log(1, 96)) if op in ("select", "sparse") else 0
+    if op == "select":
+        top_k = sink + recent + log(3, min(96, (shared + private - spread) // chunk // 2))
+    return _case("", op, batch=batch, shared=shared, private=private, spread=spread, layers=rng.choice((1, 1, 2)),
+                 heads=kv_heads * group, kv_heads=kv_heads, dim=dim, chunk=chunk, dtype=dtype,
+                 k_scale=rng.choice((1.0, 0.5, 0.37)), v_scale=rng.choice((1.0, 2.0, 0.81)), q_len=q_len,
+                 top_k=top_k, sink=sink, recent=recent)
+
+
+def _lengths(c):
+    return [c["shared"] + c["private"] - (37 * i) % (c["spread"] + 1) for i in range(c["batch"])]
+
+
+def work(case):
+    c = case
+    lens, D, C, HK = _lengths(c), c["dim"], c["chunk"], c["kv_heads"]
+    per = {"fp16": 2.0, "fp8": 1.0, "fp4": 0.5 + 1 / 16}[c["dtype"]] * D        # bytes of a stored row of one head
+    whole = c["shared"] // C * C                                                # tokens that the cache holds once
+    unique = sum(lens) - (c["batch"] - 1) * whole
+    qo = c["batch"] * c["q_len"] * c["heads"] * D * 2
+    if c["op"] == "store":
+        rows = c["layers"] * HK * 2
+        return {"bytes": rows * (unique * (2 * D + 2 * per) + sum(lens) * 2 * D), "flops": rows * 4 * D * (unique + sum(lens))}
+    if c["op"] == "decode":
+        return {"bytes": unique * HK * 2 * per + 2 * qo, "flops": 4 * sum(lens) * c["q_len"] * c["heads"] * D}
+    chunks = sum(-(-n // C) for n in lens)
+    if c["op"] == "select":
+        held = chunks - (c["batch"] - 1) * (c["shared"] // C)
+        return {"bytes": held * HK * 2 * D * 2 + qo + c["batch"] * HK * c["top_k"] * 4, "flops": 4 * chunks * c["heads"] * D}
+    tokens = sum(min(n, c["top_k"] * C) for n in lens)
+    return {"bytes": min(tokens, unique) * HK * 2 * per + 2 * qo + c["batch"] * HK * c["top_k"] * 4, "flops": 4 * tokens * c["heads"] * D}
+
+
+# ---------------------------------------------------------------------------- inputs
+def _inputs(c, seed):
+    """Distinct rows k, v [L, U, Hkv, D] (U: shared rows, then each sequence's own), the batch's row indices [b, n] (padded
+    with 0), lengths, the queries and, for the sparse operator, lists of chunks."""
+    g = torch.Generator(DEV).manual_seed(int(seed))
+    L, HK, D, b = c["layers"], c["kv_heads"], c["dim"], c["batch"]
+    lens = _lengths(c)
+    U = sum(lens) - (b - 1) * c["shared"]
+    # keys carry an offset of each channel, values a size of each head, as a model's do
+    k = torch.randn((L, U, HK, D), generator=g, device=DEV, dtype=torch.float16)
+    k += torch.randn((L, 1, HK, D), generator=g, device=DEV, dtype=torch.float16)
+    v = torch.randn((L, U, HK, D), generator=g, device=DEV, dtype=torch.float16)
+    v *= torch.rand((L, 1, HK, 1), generator=g, device=DEV, dtype=torch.float16) + 0.25
+    q = torch.randn((b, c["q_len"], c["heads"], D), generator=g, device=DEV, dtype=torch.float16)
+    n = torch.tensor(lens, device=DEV)
+    at = torch.arange(max(lens), device=DEV)
+    first = torch.cumsum(n - c["shared"], 0) - (n - c["shared"])
+    index = torch.where(at < c["shared"], at, at + first[:, None]) * (at < n[:, None])
+    lists = None
+    if c["op"] == "sparse":
+        # distinct chunks in ascending order with the last one among them, the rest at random; a context with fewer chunks than
+        # asked for ends in -1
+        have = (n + c["chunk"] - 1) // c["chunk"]
+        m = int(have.max())
+        w = torch.rand((b, HK, m), generator=g, device=DEV)
+        of = torch.arange(m, device=DEV)
+        w = torch.where(of == have[:, None, None] - 1, 2.0, torch.where(of < have[:, None, None], w, -1.0))
+        top, pick = torch.topk(w, min(c["top_k"], m), dim=-1)
+        pick = torch.where(top < 0, m, pick).sort(-1).values
+        pick = torch.where(pick == m, -1, pick)
+        lists = torch.full((b, HK, c["top_k"]), -1, dtype=torch.int32, device=DEV)
+        lists[..., : pick.shape[-1]] = pick
+    return k, v, q, index, n, lens, lists
+
+
+def _tokens(c, lens):
+    """Token ids of the batch, sequence after sequence: the shared ones, then ids that no other sequence has."""
+    parts = [np.concatenate([np.arange(c["shared"]), (i + 1) * (1 << 20) + np.arange(n - c["shared"])]) for i, n in enumerate(lens)]
+    return np.concatenate(parts).astype(np.int32)
+
+
+# ---------------------------------------------------------------------------- the cache's formats, plainly
+def _to_e4m3(x):
+    return x.clamp(-448.0, 448.0).to(torch.float8_e4m3fn)
+
+
+def _quantise(x, dtype, S):
+    """What a cache of this type keeps of fp16 rows [..., D]: a list of tensors."""
+    if dtype == "fp16":
+        return [x]
+    inv = float(np.float32(1) / np.float32(S))
+    if dtype == "fp8":
+        return [_to_e4m3(x.float() * inv).view(torch.uint8)]
+    y = (x.float() * inv).unflatten(-1, (-1, 16))
+    scale = _to_e4m3(y.abs().amax(-1) * float(np.float32(1) / np.float32(6)))
+    s = scale.float()
+    z = y * torch.where(s > 0, 1 / s, 0.0)[..., None]
+    a = z.abs()
+    # to nearest, ties to the even code
+    code = ((a > 0.25).to(torch.uint8) + (a >= 0.75) + (a > 1.25) + (a >= 1.75) + (a > 2.5) + (a >= 3.5) + (a > 5.0)).to(torch.uint8)
+    code = (code | (torch.signbit(z).to(torch.uint8) << 3)).flatten(-2)
+    return [code[..., 0::2] | (code[..., 1::2] << 4), scale.view(torch.uint8)]
+
+
+def _dequantise(parts, dtype, S):
+    """fp32 rows of what the cache keeps."""
+    if dtype == "fp16":
+        return parts[0].float()
+    if dtype == "fp8":
+        return parts[0].view(torch.float8_e4m3fn).float() * S
+    table = torch.tensor(E2M1 + tuple(-x for x in E2M1), device=parts[0].device)
+    p = parts[0].int()
+    code = torch.stack((table[p & 15], table[p >> 4]), -1).flatten(-2).unflatten(-1, (-1, 16))
+    return (code * parts[1].view(torch.float8_e4m3fn).float()[..., None]).flatten(-2) * S
+
+
+def _bounds(parts, c, index, n):
+    """The largest and the smallest stored key of each dim over each chunk of each sequence, fp16 [b, chunks, 2, Hkv, D], in units
+    of the key scale.  Stored values are exact in fp16."""
+    rows = _dequantise(parts, c["dtype"], 1.0).half()
+    C = c["chunk"]
+    m = -(-index.shape[1] // C) * C
+    at = torch.arange(m, device=index.device)
+    there = at < n[:, None]
+    x = rows[torch.nn.functional.pad(index, (0, m - index.shape[1]))]
+    hi = torch.where(there[..., None, None], x, -torch.inf).unflatten(1, (-1, C)).amax(2)
+    lo = torch.where(there[..., None, None], x, torch.inf).unflatten(1, (-1, C)).amin(2)
+    return torch.stack((hi, lo), 2)
+
+
+def prepare(case, seed):
+    c = case
+    k, v, q, index, n, lens, lists = _inputs(c, seed)
+    s = {"case": c, "layer": c["layers"] - 1, "q": q.squeeze(1) if c["q_len"] == 1 else q, "lists": lists}
+    if c["op"] == "store":
+        flat = torch.cat([index[i, :m] for i, m in enumerate(lens)])
+        s.update(k=k[:, flat].contiguous(), v=v[:, flat].contiguous())
+    if own:
+        # the cache that a serving program keeps, its sequences inserted (all but for the store operator, which does that)
+        import prefix_shared_decode_gb300 as ps
+        slots = sum(-(-m // c["chunk"]) for m in lens) + 8
+        s["ps"] = ps
+        s["pool"] = ps.Pool(c["layers"], c["heads"], c["dim"], c["chunk"], slots, n_kv_heads=c["kv_heads"], kv_dtype=c["dtype"],
+                            k_scale=c["k_scale"], v_scale=c["v_scale"], chunk_bounds=c["op"] == "select")
+        s["ids"], s["tokens"], s["lens"] = list(range(len(lens))), _tokens(c, lens), np.array(lens, dtype=np.int32)
+        if c["op"] != "store":
+            a = 0
+            for i, m in enumerate(lens):
+                s["pool"].insert(i, s["tokens"][a:a + m], k[:, index[i, :m]], v[:, index[i, :m]])
+                a += m
+            s["sched"] = s["pool"].schedule(s["ids"], q_len=c["q_len"], causal=c["q_len"] > 1)
+        return s
+    s.update(index=index, n=n)
+    if c["op"] == "select":
+        s["bounds"] = _bounds([x[s["layer"]] for x in _quantise(k, c["dtype"], c["k_scale"])], c, index, n)
+    elif c["op"] != "store":
+        s.update(k=_quantise(k, c["dtype"], c["k_scale"]), v=_quantise(v, c["dtype"], c["v_scale"]))
+    return s
+
+
+# ---------------------------------------------------------------------------- one pass
+def run(state):
+    return _run_own(state) if own else _PLAIN[state["case"]["op"]](state, state["case"])
+
+
+def _run_own(s):
+    c, ps, pool = s["case"], s["ps"], s["pool"]
+    if c["op"] == "store":
+        pool.insert_batch(s["ids"], s["tokens"], s["k"], s["v"], lengths=s["lens"])
+        k, v = pool.read_batch(s["ids"])
+        pool.remove_batch(s["ids"])
+        return {"k": k, "v": v}
+    if c["op"] == "decode":
+        return ps.decode_attention(pool, s["sched"], s["q"], layer=s["layer"])
+    if c["op"] == "select":
+        return ps.select_chunks(pool, s["sched"], s["q"], c["top_k"], layer=s["layer"], sink=c["sink"], recent=c["recent"])
+    return ps.sparse_decode_attention(pool, s["sched"], s["q"], s["lists"], layer=s["layer"])
+
+
+def _store(s, c):
+    k = _dequantise(_quantise(s["k"], c["dtype"], c["k_scale"]), c["dtype"], c["k_scale"])
+    v = _dequantise(_quantise(s["v"], c["dtype"], c["v_scale"]), c["dtype"], c["v_scale"])
+    return {"k": k.half(), "v": v.half()}
+
+
+def _decode(s, c):
+    layer, HK, G = s["layer"], c["kv_heads"], c["heads"] // c["kv_heads"]
+    K = _dequantise([x[layer] for x in s["k"]], c["dtype"], c["k_scale"]).transpose(0, 1)[:, s["index"]]   # [Hkv, b, n, D]
+    V = _dequantise([x[layer] for x in s["v"]], c["dtype"], c["v_scale"]).transpose(0, 1)[:, s["index"]]
+    q = s["q"].float().view(c["batch"], c["q_len"], HK, G, -1).permute(2, 0, 1, 3, 4).flatten(2, 3)          # [Hkv, b, q_len * G, D]
+    x = torch.matmul(q, K.transpose(-1, -2)) * c["dim"] ** -0.5
+    last = s["n"][:, None] - c["q_len"] + torch.arange(c["q_len"], device=q.device)                         # [b, q_len]
+    seen = torch.arange(K.shape[2], device=q.device) <= last[..., None]
+    x = torch.where(seen.repeat_interleave(G, 1), x, -torch.inf)
+    p = torch.exp(x - x.amax(-1, keepdim=True))
+    o = torch.matmul(p / p.sum(-1, keepdim=True), V)
+    return o.unflatten(2, (c["q_len"], G)).permute(1, 2, 0, 3, 4).reshape(s["q"].shape).half()
+
+
+def _select(s, c):
+    # in 64 bits: the order of scores that differ by less than 32 bits hold decides which chunk is listed
+    b, HK, G, K = c["batch"], c["kv_heads"], c["heads"] // c["kv_heads"], c["top_k"]
+    q = s["q"].double().view(b, HK, G, -1)
+    hi, lo = s["bounds"].double().permute(2, 0, 3, 4, 1)                                                    # [b, Hkv, D, chunks]
+    have = ((s["n"] + c["chunk"] - 1) // c["chunk"])[:, None, None]
+    at = torch.arange(hi.shape[-1], device=q.device)
+    there = at < have
+    score = torch.matmul(q.clamp(min=0), torch.where(there[:, :, None], hi, 0.0)) + torch.matmul(q.clamp(max=0), torch.where(there[:, :, None], lo, 0.0))
+    score = score.amax(2)
+    score = torch.where((at < c["sink"]) | (at >= have - c["recent"]), torch.inf, score)
+    score = torch.where(there, score, -torch.inf)
+    order = torch.sort(score, dim=-1, descending=True, stable=True).indices[..., :K]                        # ties: the lower index
+    order = torch.where(order < have, order, 1 << 30).sort(-1).values
+    out = torch.full((b, HK, K), -1, dtype=torch.int32, device=q.device)
+    out[..., : order.shape[-1]] = torch.where(order == 1 << 30, -1, order)
+    return out
+
+
+def _sparse(s, c):
+    layer, HK, G, C = s["layer"], c["kv_heads"], c["heads"] // c["kv_heads"], c["chunk"]
+    at = (s["lists"].long()[..., None] * C + torch.arange(C, device=DEV)).flatten(-2)                       # [b, Hkv, K * C] positions
+    seen = (at >= 0) & (at < s["n"][:, None, None])
+    rows = torch.gather(s["index"], 1, torch.where(seen, at, 0).flatten(1)).view(at.shape)
+    of = torch.arange(HK, device=DEV)[:, None]
+    K = _dequantise([x[layer][rows, of] for x in s["k"]], c["dtype"], c["k_scale"])                        # [b, Hkv, K * C, D]
+    V = _dequantise([x[layer][rows, of] for x in s["v"]], c["dtype"], c["v_scale"])
+    q = s["q"].float().view(c["batch"], HK, G, -1)
+    x = torch.where(seen[:, :, None], torch.matmul(q, K.transpose(-1, -2)) * c["dim"] ** -0.5, -torch.inf)
+    p = torch.exp(x - x.amax(-1, keepdim=True))
+    return torch.matmul(p / p.sum(-1, keepdim=True), V).reshape(s["q"].shape).half()
+
+
+_PLAIN = {"store": _store, "decode": _decode, "select": _select, "sparse": _sparse}
+
+
+# ---------------------------------------------------------------------------- in 64 bits, from the definitions
+def _nearest(x, grid):
+    """The nearest value of an ascending grid of non-negative values in float64, ties to the even place, beyond it the last."""
+    mid = (grid[1:] + grid[:-1]) / 2
+    up, down = torch.searchsorted(mid, x, right=True), torch.searchsorted(mid, x)
+    return grid[torch.where(up % 2 == 0, up, down)]
+
+
+def _held(x, dtype, S):
+    """What a cache of this type holds of fp16 rows, in float64: from the format's definition (values of a grid, not codes)."""
+    if dtype == "fp16":
+        return x.double()
+    # non-negative E4M3: 8 subnormal steps of 2^-9, then 8 steps of each power of two up to 448
+    e = np.arange(127)
+    e4m3 = np.where(e < 8, e * 2.0**-9, np.ldexp(1 + (e % 8) / 8, e // 8 - 7))
+    e4m3 = torch.from_numpy(e4m3).to(x.device)
+    y = (x.double() * float(np.float32(1) / np.float32(S))).float().double()
+    if dtype == "fp8":
+        return torch.sign(y) * _nearest(y.abs(), e4m3) * S
+    y = y.unflatten(-1, (-1, 16))
+    scale = _nearest((y.abs().amax(-1, keepdim=True) * float(np.float32(1) / np.float32(6))).float().double(), e4m3)
+    by = torch.where(scale > 0, (1 / scale).float().double(), 0.0)
+    z = (y * by).float().double()
+    return (torch.sign(z) * _nearest(z.abs(), torch.tensor(E2M1, device=x.device, dtype=torch.float64)) * scale).flatten(-2) * S
+
+
+def exact(case, seed):
+    c = case
+    k, v, q, index, n, lens, lists = _inputs(c, seed)
+    G, C, layer = c["heads"] // c["kv_heads"], c["chunk"], c["layers"] - 1
+    if c["op"] == "store":
+        # piece by piece: the float64 of all rows at once is large
+        flat = torch.cat([index[i, :m] for i, m in enumerate(lens)])
+        out = []
+        for x, S in ((k, c["k_scale"]), (v, c["v_scale"])):
+            out.append(torch.cat([_held(part, c["dtype"], S).half() for part in x.split(4096, 1)], 1)[:, flat])
+        return {"k": out[0], "v": out[1]}
+    if c["op"] == "select":
+        return None                          # whole numbers: the plain form ranks in 64 bits already
+    out = []
+    for i, m in enumerate(lens):             # a sequence at a time, a key/value head at a time
+        rows = index[i, :m]
+        heads = []
+        for h in range(c["kv_heads"]):
+            at = rows
+            if c["op"] == "sparse":
+                at = torch.cat([rows[j * C:(j + 1) * C] for j in lists[i, h].tolist() if j >= 0])
+            K, V = _held(k[layer, at, h], c["dtype"], c["k_scale"]), _held(v[layer, at, h], c["dtype"], c["v_scale"])
+            x = q[i, :, h * G:(h + 1) * G].double() @ K.T / np.sqrt(c["dim"])
+            if c["op"] == "decode":
+                hide = torch.arange(m, device=DEV) > m - c["q_len"] + torch.arange(c["q_len"], device=DEV)[:, None]
+                x = x.masked_fill(hide[:, None], -torch.inf)
+            heads.append(torch.softmax(x, -1) @ V)
+        out.append(torch.cat(heads, 1))
+    out = torch.stack(out)
+    return out.squeeze(1) if c["q_len"] == 1 else out
