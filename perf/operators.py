@@ -226,7 +226,7 @@ def prepare(case, seed):
             for i, m in enumerate(lens):
                 s["pool"].insert(i, s["tokens"][a:a + m], k[:, index[i, :m]], v[:, index[i, :m]])
                 a += m
-            s["sched"] = s["pool"].schedule(s["ids"], q_len=c["q_len"], causal=c["q_len"] > 1)
+            s["sched"] = s["pool"].schedule(s["ids"], q_len=c["q_len"], causal=c["q_len"] > 1, chunk_lists=c["op"] != "decode")
         return s
     s.update(index=index, n=n)
     if c["op"] == "select":
