@@ -29,8 +29,8 @@
  *    stream).  All device work is enqueued asynchronously on it.
  *  - Objects are not thread-safe: serialise calls on one pool.
  *  - Element type of K, V, Q and out is IEEE fp16; accumulation is fp32.
- *    A pool created with CA_KV_FP8 stores K and V as 8-bit floats (below);
- *    its inputs and outputs stay fp16.
+ *    A pool created with CA_KV_FP8 or CA_KV_FP4 stores K and V as 8-bit or
+ *    4-bit floats (below); its inputs and outputs stay fp16.
  */
 #ifndef CHUNK_ATTENTION_H
 #define CHUNK_ATTENTION_H
@@ -72,6 +72,23 @@ extern "C" {
  * keep fp16; this is one of the variants their tuning discussion leaves open
  * [CA §7, Model and Hardware Compatibility]. */
 #define CA_KV_FP8            2u
+/* Store K and V in 4 bits: E2M1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign),
+ * each block of 16 consecutive dims of a row with one E4M3 scale (4.5 bits an
+ * element, 3.56 times fewer bytes than fp16).  Inserted rows are quantised on
+ * the device: with S the pool's k_scale or v_scale and every step in fp32,
+ *     y     = x * (1 / S)
+ *     scale = E4M3(max|y| over the block * (1/6))
+ *     code  = E2M1(y * (1 / scale))            (0 where scale is 0)
+ * both conversions to nearest even and saturating; a code reads back as
+ * code * scale * S, where code * scale is exact in fp16.  Attention is the
+ * plain definition over those values.  Rows must be finite: a block that holds
+ * a NaN or an infinity keeps finite but unspecified values.  Needs head_dim 64
+ * or 128; excludes CA_KV_FP8. */
+#define CA_KV_FP4            4u
+/* Keep the largest and smallest stored key of each dim for every chunk,
+ * key/value head and layer (2 x head_dim fp16 each; inserts and appends update
+ * them): what ca_select_chunks scores chunks by.  Keys must not be NaN. */
+#define CA_CHUNK_BOUNDS      8u
 
 /* ---- schedule flags ---------------------------------------------------- */
 /* Treat every chunk as sequence-first even when the batch shares it (no
@@ -82,6 +99,9 @@ extern "C" {
 /* Multi-token queries (ca_build_schedule_ex): query token j of a sequence
  * whose context holds n tokens sees only tokens [0, n - q_len + j]. */
 #define CA_SCHED_CAUSAL      2u
+/* Upload each sequence's chunk list with the schedule: ca_select_chunks and
+ * ca_sparse_attention need it (every other call ignores it). */
+#define CA_SCHED_CHUNK_LISTS 4u
 
 typedef struct ca_pool  ca_pool;
 typedef struct ca_sched ca_sched;
@@ -92,14 +112,15 @@ typedef struct ca_sched ca_sched;
  * [CA §4.1]); n_layers, n_heads and capacity_slots >= 1.  Other shapes give
  * CA_ERR_UNSUPPORTED, bad counts or unknown flags CA_ERR_INVALID.  A pool
  * made from this struct has one key/value head per query head and (with
- * CA_KV_FP8) scales of 1; ca_pool_config_ex sets those too. */
+ * CA_KV_FP8 or CA_KV_FP4) scales of 1; ca_pool_config_ex sets those too. */
 typedef struct {
     int32_t  n_layers;
     int32_t  n_heads;         /* query heads (q and out)                       */
     int32_t  head_dim;
     int32_t  chunk;           /* c: tokens per chunk                           */
     int32_t  capacity_slots;  /* chunk slots in the device pool                */
-    uint32_t flags;           /* CA_NO_SHARING | CA_KV_FP8, or 0               */
+    uint32_t flags;           /* CA_NO_SHARING | CA_KV_FP8 or CA_KV_FP4 |
+                                 CA_CHUNK_BOUNDS, or 0                         */
 } ca_pool_config;
 
 /* ca_pool_config plus the variants the summary's tuning discussion leaves
@@ -107,13 +128,13 @@ typedef struct {
  * heads stored in the pool (grouped-query attention: query head h reads
  * key/value head h / (n_heads / n_kv_heads)); 0 means n_heads; n_heads must
  * be a multiple of it and the group n_heads / n_kv_heads at most 64 (32 at
- * head_dim 256).  k_scale / v_scale: the CA_KV_FP8 scales (0 means 1.0;
- * ignored without CA_KV_FP8). */
+ * head_dim 256).  k_scale / v_scale: the CA_KV_FP8 or CA_KV_FP4 scales (0
+ * means 1.0; ignored without either). */
 typedef struct {
     ca_pool_config base;
     int32_t  n_kv_heads;      /* key/value heads (0: n_heads)                  */
-    float    k_scale;         /* CA_KV_FP8 only: key scale (0: 1.0)            */
-    float    v_scale;         /* CA_KV_FP8 only: value scale (0: 1.0)          */
+    float    k_scale;         /* CA_KV_FP8, CA_KV_FP4: key scale (0: 1.0)      */
+    float    v_scale;         /* CA_KV_FP8, CA_KV_FP4: value scale (0: 1.0)    */
 } ca_pool_config_ex;
 
 /* Occupancy of a pool (ca_pool_stats).  The storage model of prefix
@@ -133,9 +154,15 @@ typedef struct {
  * per element, head = key/value head)
  *     kv[slot][layer][K|V][head][c][head_dim]
  * so one chunk of one head is a contiguous c x head_dim tile (16 KiB at
- * c = 64, D = 128 in fp16) that the kernels fetch whole with TMA; then one int32 per
+ * c = 64, D = 128 in fp16) that the kernels fetch whole with TMA; with
+ * CA_KV_FP4 kv[slot][layer][head] tiles of c * head_dim * 9/8 bytes that hold
+ * the chunk's K and V of a head (key codes, value codes, key scales, value
+ * scales, each in the order of the kernels' fragments: an opaque format, read
+ * back by ca_read_batch).  Then one int32 per
  * slot holding the chunk's valid-token count (the kernels read it, so a
- * decode-time append can grow a partial chunk without a new schedule).
+ * decode-time append can grow a partial chunk without a new schedule), and
+ * with CA_CHUNK_BOUNDS, 256-byte aligned after those, the key bounds: fp16
+ * [slot][layer][head][largest|smallest][head_dim], in units of the key scale.
  */
 
 /* Bytes of device memory a pool with this shape needs (for kv_dev).
@@ -210,6 +237,21 @@ int ca_append_tokens(ca_pool* pool, int64_t seq_id, const int32_t* tokens,
                      int32_t n, const void* k_dev, const void* v_dev,
                      void* stream, int32_t* n_new_chunks_out);
 
+/* Read rows back: tokens [starts[i], starts[i] + lengths[i]) of each
+ * sequence, as the pool holds them (dequantised, rounded to fp16), into packed
+ * k_dev / v_dev: fp16 [n_layers][sum(lengths)][n_kv_heads][head_dim], 16-byte
+ * aligned, sequence after sequence, the layout that ca_insert_batch takes.
+ * For a prompt whose matched prefix must reach its prefill attention, or to
+ * move a sequence to another pool.  starts may be NULL (all 0); lengths may be
+ * 0; a sequence may be listed more than once.  Works for every pool type; one
+ * launch per 1024 chunks, enqueued on `stream` behind the inserts and appends
+ * before it there.  Errors: CA_ERR_NOT_FOUND; CA_ERR_INVALID (a range past the
+ * sequence's end, a host-only pool, NULL or misaligned pointers);
+ * CA_ERR_CUDA.  [CA §3.1: the chunks hold each sequence's K/V by token.] */
+int ca_read_batch(const ca_pool* pool, int32_t n_seqs, const int64_t* seq_ids,
+                  const int32_t* starts, const int32_t* lengths, void* k_dev, void* v_dev,
+                  void* stream);
+
 /* Remove a finished sequence [CA §3.1: completed sequences remove their
  * path].  Every chunk on its path loses one reference; chunks left with none
  * return their slot to the free list [CA-blog, 動的プレフィックス検出]. */
@@ -228,6 +270,9 @@ int ca_pool_stats(const ca_pool* pool, ca_stats* out);
 int ca_seq_slots(const ca_pool* pool, int64_t seq_id, int32_t* slots, int32_t cap,
                  int32_t* n_out);
 
+/* Context tokens of seq_id (CA_ERR_NOT_FOUND if it is not in the pool). */
+int ca_seq_length(const ca_pool* pool, int64_t seq_id, int32_t* n_out);
+
 /* ---- schedule -------------------------------------------------------------
  * The per-step context of the two-phase kernel [CA §3.2, §3.3] for the batch
  * seq_ids[0..b): which chunks are chunk-first and which sequences share each
@@ -243,7 +288,7 @@ int ca_seq_slots(const ca_pool* pool, int64_t seq_id, int32_t* slots, int32_t ca
 int ca_build_schedule(ca_pool* pool, const int64_t* seq_ids, int32_t b,
                       ca_sched** inout, void* stream);
 
-/* The same with flags (CA_SCHED_NO_TPP, CA_SCHED_CAUSAL; 0 is
+/* The same with flags (CA_SCHED_NO_TPP, CA_SCHED_CAUSAL, CA_SCHED_CHUNK_LISTS; 0 is
  * ca_build_schedule) and q_len query tokens per sequence (multi-token queries: draft
  * tokens to verify, or a chunk of prompt prefilled over the trie).  The
  * blog's two-phase function takes queries of any length [CA-blog, Two-Phase
@@ -388,6 +433,47 @@ int ca_decode_attention_host(const ca_pool* pool, const ca_sched* sched,
 int ca_decode_attention_static_ws(const ca_pool* pool, const ca_sched* sched,
                                   int32_t layer, const void* q_dev, void* out_dev,
                                   float scale, void* stream);
+
+/* ---- attention over selected chunks ----------------------------------------
+ * Decode attention that reads only some of each context's chunks: the first
+ * call picks them by a cheap score, the second attends to a list (that call's,
+ * or the caller's own).  Both take schedules of ca_build_schedule_ex with
+ * CA_SCHED_CHUNK_LISTS and q_len 1, of any pool type.  A list holds chunk
+ * numbers within the sequence's context (chunk j: tokens j*c to j*c + c - 1).
+ * The pages attend to every chunk; these calls serve contexts too long for it.
+ *
+ * ca_select_chunks: for each sequence i and key/value head h, lists_dev
+ * (int32 [b][n_kv_heads][top_k]) receives top_k chunks in ascending order, or
+ * all of them and then -1 where the context has fewer.  Always among them are
+ * the first `sink` and the last `recent` chunks; the others are those with the
+ * largest
+ *     score(j) = max over the group's query rows of
+ *                sum_d max(q_d * hi_jd, q_d * lo_jd)
+ * where hi and lo are the chunk's key bounds: no token of the chunk has a
+ * larger product with the row.  Chunks are ranked by their scores in 64 bits
+ * (scores in 32 decide wherever their error bound allows it), ties to the
+ * lower number; a score that is not a number ranks last.  Needs
+ * CA_CHUNK_BOUNDS.  Contexts of at most 49152 chunks (CA_ERR_UNSUPPORTED).
+ *
+ * ca_sparse_attention: out[i][h][:] = sum_t softmax_t(scale * q[i][h] . k_t) v_t
+ * over the tokens of the chunks in lists_dev[i][h / group] (-1 entries, and
+ * all below 0, are skipped; order is free; a chunk listed twice counts twice).
+ * A list without a token gives zeros.  An entry past the context's last chunk
+ * is skipped and reported as CA_ERR_DEVICE_BOUNDS by ca_sched_device_status.
+ *
+ * Each call is one kernel on `stream`, which allocates nothing and needs no
+ * workspace; calls on one schedule may overlap, and both may be captured into
+ * graphs, valid while the schedule is (ca_decode_attention).  q_dev / out_dev
+ * fp16 [b][n_heads][head_dim], 16-byte aligned.  Errors: CA_ERR_STALE;
+ * CA_ERR_INVALID (a schedule without lists, a pool without bounds, top_k < 1,
+ * sink + recent > top_k, bad layer, NULL or misaligned pointers);
+ * CA_ERR_UNSUPPORTED (q_len > 1, more than 2^31 list entries); CA_ERR_CUDA. */
+int ca_select_chunks(const ca_pool* pool, const ca_sched* sched, int32_t layer,
+                     const void* q_dev, int32_t top_k, int32_t sink, int32_t recent,
+                     int32_t* lists_dev, void* stream);
+int ca_sparse_attention(const ca_pool* pool, const ca_sched* sched, int32_t layer,
+                        const void* q_dev, const int32_t* lists_dev, int32_t top_k,
+                        void* out_dev, float scale, void* stream);
 
 /* Synchronise `stream` and read the schedule's device status word: CA_OK,
  * CA_ERR_DEVICE_BOUNDS or CA_ERR_TIMEOUT (or a code written by

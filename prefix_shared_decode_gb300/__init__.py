@@ -20,8 +20,8 @@ import numpy as np
 from . import capi
 from .capi import CAError, check
 
-__all__ = ["Pool", "Schedule", "DecodeGraph", "decode_attention", "decode_attention_host", "kernel_launches",
-           "CAError"]
+__all__ = ["Pool", "Schedule", "DecodeGraph", "decode_attention", "decode_attention_host", "select_chunks",
+           "sparse_decode_attention", "kernel_launches", "CAError"]
 
 
 _cuda_ok = None
@@ -53,16 +53,21 @@ class Pool:
 
     With ``host_only=True`` no GPU memory is touched (trie, allocator and
     schedule tables only).  ``kv_dtype="fp8"`` stores K and V as FP8 E4M3
-    with the given scales (inserted rows stay fp16; the library quantises)."""
+    with the given scales (inserted rows stay fp16; the library quantises),
+    ``kv_dtype="fp4"`` as E2M1 codes with an E4M3 scale for every 16 dims.
+    ``chunk_bounds=True`` also keeps every chunk's largest and smallest keys,
+    which ``select_chunks`` needs."""
 
     def __init__(self, n_layers: int, n_heads: int, head_dim: int, chunk: int,
                  capacity_slots: int, no_sharing: bool = False, host_only: bool = False,
                  device=None, n_kv_heads: int | None = None, kv_dtype: str = "fp16",
-                 k_scale: float = 1.0, v_scale: float = 1.0):
+                 k_scale: float = 1.0, v_scale: float = 1.0, chunk_bounds: bool = False):
         L = capi.lib()
-        if kv_dtype not in ("fp16", "fp8"):
-            raise ValueError("kv_dtype must be 'fp16' or 'fp8'")
-        flags = (capi.CA_NO_SHARING if no_sharing else 0) | (capi.CA_KV_FP8 if kv_dtype == "fp8" else 0)
+        kinds = {"fp16": 0, "fp8": capi.CA_KV_FP8, "fp4": capi.CA_KV_FP4}
+        if kv_dtype not in kinds:
+            raise ValueError("kv_dtype must be 'fp16', 'fp8' or 'fp4'")
+        flags = ((capi.CA_NO_SHARING if no_sharing else 0) | kinds[kv_dtype] |
+                 (capi.CA_CHUNK_BOUNDS if chunk_bounds else 0))
         self.cfg = capi.PoolConfigEx(capi.PoolConfig(n_layers, n_heads, head_dim, chunk, capacity_slots, flags),
                                      n_kv_heads or 0, float(k_scale), float(v_scale))
         self.kv_dtype, self.k_scale, self.v_scale = kv_dtype, float(k_scale), float(v_scale)
@@ -98,14 +103,19 @@ class Pool:
         return self._h
 
     def _tile_bytes(self) -> int:
-        eb = 1 if self.kv_dtype == "fp8" else 2
-        return self.capacity_slots * self.n_layers * 2 * self.n_kv_heads * self.chunk * self.head_dim * eb
+        e = self.chunk * self.head_dim
+        pair = {"fp16": 4 * e, "fp8": 2 * e, "fp4": 2 * (e // 2 + e // 16)}[self.kv_dtype]   # K and V of a head
+        return self.capacity_slots * self.n_layers * self.n_kv_heads * pair
 
     def kv_view(self):
         """The device pool's K/V tiles as [slots, L, 2, H, c, D] (a view):
-        fp16, or the E4M3 codes as uint8 for an fp8 pool."""
+        fp16, or the E4M3 codes as uint8 for an fp8 pool; an fp4 pool's tiles
+        as uint8 [slots, L, H, bytes], in the kernels' own order (``read``
+        gives their values)."""
         import torch
         t = self._kv[self._kv_offset:self._kv_offset + self._tile_bytes()]
+        if self.kv_dtype == "fp4":
+            return t.view(self.capacity_slots, self.n_layers, self.n_kv_heads, -1)
         if self.kv_dtype == "fp16":
             t = t.view(torch.float16)
         return t.view(self.capacity_slots, self.n_layers, 2, self.n_kv_heads, self.chunk, self.head_dim)
@@ -115,6 +125,18 @@ class Pool:
         import torch
         a = self._kv_offset + self._tile_bytes()
         return self._kv[a:a + 4 * self.capacity_slots].view(torch.int32)
+
+    def bounds_view(self):
+        """The chunks' key bounds, fp16 [slots, L, Hkv, 2, D] (a view): the
+        largest, then the smallest stored key of each dim, in units of the key
+        scale.  Rows of free slots are not defined."""
+        import torch
+        if not self.cfg.base.flags & capi.CA_CHUNK_BOUNDS:
+            raise ValueError("the pool was created without chunk_bounds")
+        a = self._kv_offset + self._tile_bytes() + (4 * self.capacity_slots + 255) // 256 * 256
+        n = self.capacity_slots * self.n_layers * self.n_kv_heads * 2 * self.head_dim * 2
+        return self._kv[a:a + n].view(torch.float16).view(self.capacity_slots, self.n_layers, self.n_kv_heads, 2,
+                                                          self.head_dim)
 
     def match_prefix(self, tokens) -> int:
         tok = _i32(tokens)
@@ -181,6 +203,72 @@ class Pool:
                                           C.byref(grown)), "ca_append_tokens")
         return grown.value
 
+    def read_batch(self, seq_ids, starts=None, lengths=None, out=None, stream=None):
+        """The K and V rows that the pool holds for tokens [start, start +
+        length) of each sequence (default: all of its tokens), dequantised:
+        fp16 tensors (k, v) [L, sum(lengths), Hkv, D], sequence after
+        sequence, the layout ``insert_batch`` takes.  ``out``: such a pair to
+        write into."""
+        import torch
+        if self.host_only:
+            raise ValueError("a host-only pool holds no rows")
+        ids = np.ascontiguousarray(np.asarray(seq_ids, dtype=np.int64))
+        first = None if starts is None else _i32(starts)
+        if lengths is None:
+            lens = np.array([self.seq_len(int(i)) for i in ids], dtype=np.int32)
+            if first is not None:
+                if first.shape != lens.shape:
+                    raise ValueError("starts and seq_ids differ in length")
+                lens = np.maximum(lens - first, 0).astype(np.int32)
+        else:
+            lens = _i32(lengths)
+        if ids.ndim != 1 or lens.shape != ids.shape or (first is not None and first.shape != ids.shape):
+            raise ValueError("seq_ids, starts and lengths differ in length")
+        if len(lens) and lens.min() < 0:
+            raise ValueError("lengths must not be negative")
+        shape = (self.n_layers, int(lens.sum(dtype=np.int64)), self.n_kv_heads, self.head_dim)
+        if out is None:
+            k = torch.empty(shape, dtype=torch.float16, device=self._kv.device)
+            v = torch.empty(shape, dtype=torch.float16, device=self._kv.device)
+        else:
+            k, v = out
+            for x in (k, v):
+                self._check_tensor(x, shape, torch.float16, "out")
+        if shape[1] == 0:
+            for i in ids:
+                self.seq_len(int(i))                 # unknown sequences are refused all the same
+            return k, v
+        P32 = C.POINTER(C.c_int32)
+        check(capi.lib().ca_read_batch(self._h, len(ids), ids.ctypes.data_as(C.POINTER(C.c_int64)),
+                                       None if first is None else first.ctypes.data_as(P32), lens.ctypes.data_as(P32),
+                                       k.data_ptr(), v.data_ptr(), self._stream(stream)), "ca_read_batch")
+        return k, v
+
+    def read(self, seq_id: int, start: int = 0, stop: int | None = None, out=None, stream=None):
+        """``read_batch`` of tokens [start, stop) of one sequence."""
+        n = self.seq_len(seq_id) if stop is None else int(stop)
+        return self.read_batch([seq_id], [start], [n - int(start)], out=out, stream=stream)
+
+    def seq_len(self, seq_id: int) -> int:
+        """Context tokens of a sequence."""
+        n = C.c_int32()
+        check(capi.lib().ca_seq_length(self._h, int(seq_id), C.byref(n)), "ca_seq_length")
+        return n.value
+
+    def _check_tensor(self, x, shape, dtype, what: str) -> None:
+        if x.dtype != dtype or not x.is_contiguous() or tuple(x.shape) != tuple(shape):
+            raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+        if x.device != self._kv.device:
+            raise ValueError(f"{what} is on {x.device}, the pool on {self._kv.device}")
+
+    def _stream(self, stream) -> int | None:
+        """The raw handle of ``stream`` (default: the current one of the
+        pool's device)."""
+        import torch
+        if stream is None:
+            stream = torch.cuda.current_stream(self._kv.device)
+        return int(getattr(stream, "cuda_stream", stream)) or None
+
     def remove(self, seq_id: int) -> None:
         check(capi.lib().ca_remove_seq(self._h, int(seq_id)), "ca_remove_seq")
 
@@ -207,12 +295,14 @@ class Pool:
         return list(buf)[:n.value]
 
     def schedule(self, seq_ids, no_tpp: bool = False, reuse: "Schedule | None" = None,
-                 stream=None, q_len: int = 1, causal: bool = False) -> "Schedule":
+                 stream=None, q_len: int = 1, causal: bool = False, chunk_lists: bool = False) -> "Schedule":
         """Per-step tables for the batch ``seq_ids`` (rows of q / out in that
         order).  Passing the previous schedule reuses it when nothing changed.
         ``q_len`` > 1: that many query tokens per sequence (q / out become
         [b, q_len, H, D]); ``causal``: token j sees context tokens
-        [0, len - q_len + j] only."""
+        [0, len - q_len + j] only.  ``chunk_lists``: also upload each
+        sequence's chunk list, for ``select_chunks`` and
+        ``sparse_decode_attention``."""
         s = reuse if reuse is not None else Schedule(self)
         # A decode loop passes the same batch list every step: its int64 copy
         # (and that copy's address) is kept, so the per-step call converts
@@ -222,7 +312,8 @@ class Pool:
         else:
             ids = np.ascontiguousarray(np.asarray(seq_ids, dtype=np.int64))
         h = s._h if s._h is not None else C.c_void_p()
-        flags = (capi.CA_SCHED_NO_TPP if no_tpp else 0) | (capi.CA_SCHED_CAUSAL if causal else 0)
+        flags = ((capi.CA_SCHED_NO_TPP if no_tpp else 0) | (capi.CA_SCHED_CAUSAL if causal else 0) |
+                 (capi.CA_SCHED_CHUNK_LISTS if chunk_lists else 0))
         check(capi.lib().ca_build_schedule_ex(self._h, ids.__array_interface__["data"][0] if ids is not s._ids
                                               else s._ids_ptr, len(ids), int(q_len), flags, C.byref(h),
                                               None if self.host_only else _stream_ptr(stream)),
@@ -356,6 +447,61 @@ def decode_attention_host(pool: Pool, sched: Schedule, q_host, out_host, layer: 
                                               ws.numel(), _stream_ptr(stream)),
           "ca_decode_attention_host")
     return out_host
+
+
+def select_chunks(pool: Pool, sched: Schedule, q, top_k: int, layer: int = 0, sink: int = 1, recent: int = 1,
+                  out=None, stream=None):
+    """The ``top_k`` chunks of each context to attend to, int32
+    [b, Hkv, top_k] in ascending order (all of a shorter context's, then -1):
+    its first ``sink`` and last ``recent`` chunks and those with the largest
+    upper bound on a product of the group's queries with a key of the chunk.
+    q: fp16 [b, H, D].  Needs a pool with ``chunk_bounds`` and a schedule with
+    ``chunk_lists``."""
+    import torch
+    _check_lists(pool, sched)
+    pool._check_tensor(q, (sched.b, pool.n_heads, pool.head_dim), torch.float16, "q")
+    shape = (sched.b, pool.n_kv_heads, int(top_k))
+    if min(shape) < 1 or not 0 <= int(sink) + int(recent) <= int(top_k) or min(int(sink), int(recent)) < 0:
+        raise ValueError("top_k must be at least 1 and cover sink + recent")
+    if out is None:
+        out = torch.empty(shape, dtype=torch.int32, device=q.device)
+    else:
+        pool._check_tensor(out, shape, torch.int32, "out")
+    check(capi.lib().ca_select_chunks(pool._h, sched._h, int(layer), q.data_ptr(), int(top_k), int(sink), int(recent),
+                                      out.data_ptr(), pool._stream(stream)), "ca_select_chunks")
+    return out
+
+
+def sparse_decode_attention(pool: Pool, sched: Schedule, q, chunks, out=None, layer: int = 0,
+                            scale: float | None = None, stream=None):
+    """out[i, h] = softmax(scale q[i, h] . K^T) V over the tokens of the
+    chunks listed in ``chunks[i, h // group]`` (int32 [b, Hkv, n]; entries
+    below 0 are skipped, a list without a token gives zeros).  q: fp16
+    [b, H, D].  Needs a schedule with ``chunk_lists``."""
+    import torch
+    _check_lists(pool, sched)
+    shape = (sched.b, pool.n_heads, pool.head_dim)
+    pool._check_tensor(q, shape, torch.float16, "q")
+    if chunks.dim() != 3 or chunks.shape[2] < 1:
+        raise ValueError("chunks must be an int32 tensor [b, Hkv, n] with n >= 1")
+    pool._check_tensor(chunks, (sched.b, pool.n_kv_heads, chunks.shape[2]), torch.int32, "chunks")
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        pool._check_tensor(out, shape, torch.float16, "out")
+    if scale is None:
+        scale = 1.0 / math.sqrt(pool.head_dim)
+    check(capi.lib().ca_sparse_attention(pool._h, sched._h, int(layer), q.data_ptr(), chunks.data_ptr(),
+                                         chunks.shape[2], out.data_ptr(), float(scale), pool._stream(stream)),
+          "ca_sparse_attention")
+    return out
+
+
+def _check_lists(pool: Pool, sched: Schedule) -> None:
+    if pool.host_only:
+        raise ValueError("a host-only pool holds no rows")
+    if not sched._flags & capi.CA_SCHED_CHUNK_LISTS:
+        raise ValueError("the schedule was built without chunk_lists")
 
 
 class DecodeGraph:

@@ -20,15 +20,19 @@ ERRORS = {
 CA_STATIC_WS_BYTES = 16 << 20
 CA_NO_SHARING = 1
 CA_KV_FP8 = 2
+CA_KV_FP4 = 4
+CA_CHUNK_BOUNDS = 8
 CA_SCHED_NO_TPP = 1
 CA_SCHED_CAUSAL = 2
+CA_SCHED_CHUNK_LISTS = 4
 
 # Every symbol the header declares, in header order.
 EXPORTS = [
     "ca_pool_bytes", "ca_pool_bytes_ex", "ca_pool_create", "ca_pool_create_ex", "ca_pool_destroy", "ca_match_prefix", "ca_insert_tokens",
-    "ca_insert_batch", "ca_append_tokens", "ca_remove_seq", "ca_remove_batch", "ca_pool_stats", "ca_seq_slots", "ca_build_schedule", "ca_build_schedule_ex", "ca_sched_destroy",
+    "ca_insert_batch", "ca_append_tokens", "ca_read_batch", "ca_remove_seq", "ca_remove_batch", "ca_pool_stats", "ca_seq_slots", "ca_seq_length", "ca_build_schedule", "ca_build_schedule_ex", "ca_sched_destroy",
     "ca_sched_counts", "ca_export_tables", "ca_export_plan", "ca_workspace_bytes", "ca_decode_attention",
     "ca_workspace_bytes_host", "ca_decode_attention_host", "ca_decode_attention_static_ws",
+    "ca_select_chunks", "ca_sparse_attention",
     "ca_sched_device_status", "ca_sched_inject_status", "ca_sched_inject_stall", "ca_pool_inject_alloc_failure",
     "ca_sched_set_profile_events", "ca_kernel_launches", "ca_error_string",
 ]
@@ -83,10 +87,12 @@ def lib() -> C.CDLL:
         "ca_insert_tokens": [vp, i64, P(i32), i32, vp, vp, vp, P(i32)],
         "ca_insert_batch": [vp, i32, P(i64), P(i32), P(i32), vp, vp, vp, P(i32)],
         "ca_append_tokens": [vp, i64, P(i32), i32, vp, vp, vp, P(i32)],
+        "ca_read_batch": [vp, i32, P(i64), P(i32), P(i32), vp, vp, vp],
         "ca_remove_seq": [vp, i64],
         "ca_remove_batch": [vp, i32, P(i64)],
         "ca_pool_stats": [vp, P(Stats)],
         "ca_seq_slots": [vp, i64, P(i32), i32, P(i32)],
+        "ca_seq_length": [vp, i64, P(i32)],
         "ca_build_schedule": [vp, P(i64), i32, P(vp), vp],
         "ca_build_schedule_ex": [vp, vp, i32, i32, u32, P(vp), vp],     # seq_ids: int64 array address
         "ca_sched_destroy": [vp],
@@ -98,6 +104,8 @@ def lib() -> C.CDLL:
         "ca_decode_attention": [vp, vp, i32, vp, vp, C.c_float, vp, sz, vp],
         "ca_decode_attention_host": [vp, vp, i32, vp, vp, C.c_float, vp, sz, vp],
         "ca_decode_attention_static_ws": [vp, vp, i32, vp, vp, C.c_float, vp],
+        "ca_select_chunks": [vp, vp, i32, vp, i32, i32, i32, vp, vp],
+        "ca_sparse_attention": [vp, vp, i32, vp, vp, i32, vp, C.c_float, vp],
         "ca_sched_device_status": [vp, vp],
         "ca_sched_inject_status": [vp, i32, vp],
         "ca_sched_inject_stall": [vp, i32],

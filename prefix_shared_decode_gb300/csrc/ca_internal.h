@@ -75,7 +75,9 @@ constexpr int kUnitInts = (int)(sizeof(Unit) / sizeof(int32_t));
 
 // Offsets (in bytes) of the arrays inside the device plan blob.
 struct PlanLayout {
-    size_t chunks, units, seq_perm, pbase, status, counter, chunk_tok0, ctx_len, cta_head, total;
+    size_t chunks, units, seq_perm, pbase, status, counter, chunk_tok0, ctx_len, cta_head;
+    size_t list_off, list_slots;   // CA_SCHED_CHUNK_LISTS: each batch row's chunk slots (CSR)
+    size_t total;
 };
 
 // One 128-byte line per CTA with what its producer needs to issue its first
@@ -112,6 +114,7 @@ struct AttnParams {
     const int32_t* ctx_len;      // [b] context tokens of each position
     float scale_log2;            // scale * log2(e) (times the key scale of an fp8 pool)
     float out_scale;             // value scale of an fp8 pool, else 1
+    const uint8_t* kv;           // the pool's tiles (read by bulk copies of an fp4 pool)
     int32_t n_stages;
     int32_t kv_stable;           // no insert/append wrote the pool since the last call
     int32_t test_stall;          // test hook: the producer first waits on a barrier nothing completes
@@ -185,6 +188,10 @@ struct Tables {
     // token offset of each chunk in its sequences' contexts (cf rows, then sf
     // chunks) and each position's context length: the causal mask's inputs
     std::vector<int32_t> row_tok0, sf_tok0, ctx_len;
+    // CA_SCHED_CHUNK_LISTS: the slots of seq_ids[i]'s chunks, root first, are
+    // list_slots[list_off[i] .. list_off[i + 1])
+    std::vector<int32_t> list_off, list_slots;
+    int32_t list_max = 0;          // the longest list
 };
 
 struct Plan {
@@ -243,14 +250,21 @@ struct ScatterChunk {
 // one per query head).
 inline int32_t kv_heads(const PoolCfg& c) { return c.n_kv_heads > 0 ? c.n_kv_heads : c.n_heads; }
 
-// Device bytes of the pool: the K/V tiles, then the per-slot token counts.
-// Bytes per stored K/V element (fp16, or 1 for an FP8 pool) and the
-// effective dequantisation scales.
-inline int kv_elem_bytes(const PoolCfg& c) { return (c.flags & CA_KV_FP8) ? 1 : 2; }
+// Device bytes of the pool: the K/V tiles, then the per-slot token counts,
+// then (CA_CHUNK_BOUNDS) the key bounds [slot][layer][head][2][head_dim] fp16.
+// Bytes per stored K/V element (fp16, 1 for an FP8 pool, 0 for the 4-bit
+// codes of an FP4 pool) and the effective dequantisation scales.
+inline int kv_elem_bytes(const PoolCfg& c) { return (c.flags & CA_KV_FP8) ? 1 : (c.flags & CA_KV_FP4) ? 0 : 2; }
+// Bytes of the K and V tiles of one chunk and head (fp4: codes and scales).
+inline size_t pair_tile_bytes(const PoolCfg& c) {
+    const size_t e = (size_t)c.chunk * c.head_dim;
+    return (c.flags & CA_KV_FP4) ? 2 * (e / 2 + e / 16) : 2 * e * (size_t)kv_elem_bytes(c);
+}
 inline float kv_scale_of(float s) { return s == 0.f ? 1.f : s; }
 // Query rows one tensor-core unit takes: 64, or 32 at head_dim 256.
 inline int32_t max_query_rows(const PoolCfg& c) { return c.head_dim == 256 ? 32 : 64; }
 size_t pool_tile_bytes(const PoolCfg& c);
+size_t pool_bounds_offset(const PoolCfg& c);   // of the key bounds
 size_t pool_total_bytes(const PoolCfg& c);
 
 // What an append changed, so that a failed copy launch can undo it.
@@ -295,5 +309,21 @@ AttnParams attn_params(const Pool& pool, const Sched& s, int32_t layer, const vo
                        float scale, void* ws_dev);
 // Kernels this process has launched through the library (all pools, all devices).
 uint64_t kernel_launches();
+void count_launch();
+
+// cache_rows.cu: quantising stores of an fp4 pool, key bounds, reading back
+// (a ScatterChunk there is rows [dst_row, dst_row + n_rows) of `slot` and the
+// packed rows from src_row)
+int launch_fp4_store(const Pool& p, const void* k, const void* v, int32_t total_rows,
+                     const std::vector<ScatterChunk>& chunks, void* stream);
+int launch_key_bounds(const Pool& p, const std::vector<ScatterChunk>& chunks, void* stream);
+int launch_read_rows(const Pool& p, void* k, void* v, int32_t total_rows, const std::vector<ScatterChunk>& chunks,
+                     void* stream);
+
+// sparse.cu: chunk selection and attention over listed chunks
+int launch_select(const Pool& p, const Sched& s, int32_t layer, const void* q, int32_t top_k, int32_t sink,
+                  int32_t recent, int32_t* lists, void* stream);
+int launch_sparse(const Pool& p, const Sched& s, int32_t layer, const void* q, const int32_t* lists, int32_t top_k,
+                  void* out, float scale, void* stream);
 
 }  // namespace ca

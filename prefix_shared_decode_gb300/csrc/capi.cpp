@@ -49,23 +49,42 @@ int check_cfg(const PoolCfg* c) {
     if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return CA_ERR_UNSUPPORTED;
     // head_dim 256: chunks of at most 32 tokens (two stages of K+V must fit
     // beside the query tile), fp16 only
-    if (c->head_dim == 256 && (c->chunk > 32 || (c->flags & CA_KV_FP8))) return CA_ERR_UNSUPPORTED;
+    if (c->head_dim == 256 && (c->chunk > 32 || (c->flags & (CA_KV_FP8 | CA_KV_FP4)))) return CA_ERR_UNSUPPORTED;
     if (c->chunk != 16 && c->chunk != 32 && c->chunk != 64) return CA_ERR_UNSUPPORTED;
-    if (c->flags & ~(CA_NO_SHARING | CA_KV_FP8)) return CA_ERR_INVALID;
-    if (c->flags & CA_KV_FP8) {
-        if (c->head_dim != 128) return CA_ERR_UNSUPPORTED;
+    if (c->flags & ~(CA_NO_SHARING | CA_KV_FP8 | CA_KV_FP4 | CA_CHUNK_BOUNDS)) return CA_ERR_INVALID;
+    if ((c->flags & CA_KV_FP8) && (c->flags & CA_KV_FP4)) return CA_ERR_INVALID;
+    if (c->flags & (CA_KV_FP8 | CA_KV_FP4)) {
+        if ((c->flags & CA_KV_FP8) && c->head_dim != 128) return CA_ERR_UNSUPPORTED;
         for (float sc : {c->k_scale, c->v_scale})
             if (!(sc == 0.f || (sc > 0.f && sc < 3.0e38f))) return CA_ERR_INVALID;
     }
     if (c->n_kv_heads < 0 || (c->n_kv_heads > 0 && c->n_heads % c->n_kv_heads)) return CA_ERR_INVALID;
     if (c->n_heads / kv_heads(*c) > max_query_rows(*c)) return CA_ERR_UNSUPPORTED;
-    // TMA row coordinates are 32-bit.
-    const long double rows = (long double)c->capacity_slots * c->n_layers * 2 * kv_heads(*c) * c->chunk;
+    // TMA row coordinates are 32-bit (an fp4 pool has no tensor map: its tiles are counted).
+    const long double tiles = (long double)c->capacity_slots * c->n_layers * kv_heads(*c);
+    const long double rows = (c->flags & CA_KV_FP4) ? tiles : tiles * 2 * c->chunk;
     if (rows > 2147483647.0L) return CA_ERR_UNSUPPORTED;
     return CA_OK;
 }
 
 size_t pool_bytes(const PoolCfg& c) { return pool_total_bytes(c); }
+
+// The pool's device made current for one call (its kernels run there whatever
+// device the caller has current), and the caller's put back after it.
+struct DeviceGuard {
+    int before = -1;
+    bool ok = false, changed = false;
+    explicit DeviceGuard(int device) {
+        if (cudaGetDevice(&before) != cudaSuccess) return;
+        changed = before != device;
+        ok = !changed || cudaSetDevice(device) == cudaSuccess;
+    }
+    ~DeviceGuard() {
+        if (changed) cudaSetDevice(before);
+    }
+    DeviceGuard(const DeviceGuard&) = delete;
+    DeviceGuard& operator=(const DeviceGuard&) = delete;
+};
 
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? CA_OK : CA_ERR_CUDA; }
 
@@ -249,6 +268,35 @@ int ca_append_tokens(ca_pool* pool, int64_t seq_id, const int32_t* tokens, int32
     });
 }
 
+int ca_read_batch(const ca_pool* pool, int32_t n_seqs, const int64_t* seq_ids, const int32_t* starts,
+                  const int32_t* lengths, void* k_dev, void* v_dev, void* stream) {
+    const Range range("ca_read");
+    if (!pool || !pool->kv || n_seqs < 1 || !seq_ids || !lengths) return CA_ERR_INVALID;
+    if (!k_dev || !v_dev || !aligned(k_dev, 16) || !aligned(v_dev, 16)) return CA_ERR_INVALID;
+    return guard([&] {
+        const int32_t c = pool->cfg.chunk;
+        std::vector<ScatterChunk> rows;
+        int64_t total = 0;
+        for (int32_t i = 0; i < n_seqs; ++i) {
+            auto it = pool->seqs.find(seq_ids[i]);
+            if (it == pool->seqs.end()) return CA_ERR_NOT_FOUND;
+            const Sequence& seq = it->second;
+            const int64_t a = starts ? starts[i] : 0, z = a + lengths[i];
+            if (a < 0 || lengths[i] < 0 || z > seq.length) return CA_ERR_INVALID;
+            for (int64_t t = a; t < z;) {
+                const int64_t j = t / c, upto = std::min<int64_t>(z, (j + 1) * c);
+                rows.push_back({(int32_t)(total + t - a), (int32_t)(upto - t), seq.path[j]->slot, (int32_t)(t - j * c)});
+                t = upto;
+            }
+            total += lengths[i];
+            if (total > INT32_MAX) return CA_ERR_INVALID;
+        }
+        const DeviceGuard dev(pool->device);
+        if (!dev.ok) return CA_ERR_CUDA;
+        return launch_read_rows(*pool, k_dev, v_dev, (int32_t)total, rows, stream);
+    });
+}
+
 int ca_remove_seq(ca_pool* pool, int64_t seq_id) {
     const Range range("ca_remove");
     if (!pool) return CA_ERR_INVALID;
@@ -293,6 +341,14 @@ int ca_seq_slots(const ca_pool* pool, int64_t seq_id, int32_t* slots, int32_t ca
     return CA_OK;
 }
 
+int ca_seq_length(const ca_pool* pool, int64_t seq_id, int32_t* n_out) {
+    if (!pool || !n_out) return CA_ERR_INVALID;
+    auto it = pool->seqs.find(seq_id);
+    if (it == pool->seqs.end()) return CA_ERR_NOT_FOUND;
+    *n_out = it->second.length;
+    return CA_OK;
+}
+
 int ca_build_schedule(ca_pool* pool, const int64_t* seq_ids, int32_t b, ca_sched** inout, void* stream) {
     return ca_build_schedule_ex(pool, seq_ids, b, 1, 0u, inout, stream);
 }
@@ -300,7 +356,7 @@ int ca_build_schedule(ca_pool* pool, const int64_t* seq_ids, int32_t b, ca_sched
 int ca_build_schedule_ex(ca_pool* pool, const int64_t* seq_ids, int32_t b, int32_t q_len, uint32_t flags,
                          ca_sched** inout, void* stream) {
     const Range range("ca_build_schedule");
-    if (!pool || !inout || !seq_ids || b < 1 || q_len < 1 || (flags & ~(CA_SCHED_NO_TPP | CA_SCHED_CAUSAL)))
+    if (!pool || !inout || !seq_ids || b < 1 || q_len < 1 || (flags & ~(CA_SCHED_NO_TPP | CA_SCHED_CAUSAL | CA_SCHED_CHUNK_LISTS)))
         return CA_ERR_INVALID;
     if ((int64_t)q_len * (pool->cfg.n_heads / kv_heads(pool->cfg)) > max_query_rows(pool->cfg))
         return CA_ERR_UNSUPPORTED;
@@ -473,9 +529,10 @@ AttnParams attn_params(const Pool& pool, const Sched& s, int32_t layer, const vo
     a.group = pool.cfg.n_heads / a.n_kv_heads;
     a.layer = layer;
     a.capacity = pool.cfg.capacity_slots;
-    const bool f8 = (pool.cfg.flags & CA_KV_FP8) != 0;
-    a.scale_log2 = scale * 1.4426950408889634f * (f8 ? kv_scale_of(pool.cfg.k_scale) : 1.f);
-    a.out_scale = f8 ? kv_scale_of(pool.cfg.v_scale) : 1.f;
+    a.kv = static_cast<const uint8_t*>(pool.kv);
+    const bool quant = (pool.cfg.flags & (CA_KV_FP8 | CA_KV_FP4)) != 0;
+    a.scale_log2 = scale * 1.4426950408889634f * (quant ? kv_scale_of(pool.cfg.k_scale) : 1.f);
+    a.out_scale = quant ? kv_scale_of(pool.cfg.v_scale) : 1.f;
     return a;
 }
 }  // namespace ca
@@ -523,6 +580,42 @@ int ca_decode_attention_host(const ca_pool* pool, const ca_sched* s, int32_t lay
     st = decode_launch(pool, s, layer, ws + s->ws.q_stage, ws + s->ws.out_stage, scale, ws_dev, stream);
     if (st) return st;
     return cuda_status(cudaMemcpyAsync(out_host, ws + s->ws.out_stage, bytes, cudaMemcpyDeviceToHost, cs));
+}
+
+// What both chunk-list calls ask of their pool and schedule.
+static int list_checks(const ca_pool* pool, const ca_sched* s, int32_t layer, const void* q_dev, int32_t top_k,
+                       const void* lists_dev) {
+    if (!pool || !s || !pool->kv || s->pool != pool || !s->dev) return CA_ERR_INVALID;
+    if (s->generation != pool->generation) return CA_ERR_STALE;
+    if (!(s->flags & CA_SCHED_CHUNK_LISTS)) return CA_ERR_INVALID;
+    if (s->q_len != 1) return CA_ERR_UNSUPPORTED;
+    if (layer < 0 || layer >= pool->cfg.n_layers || top_k < 1) return CA_ERR_INVALID;
+    if (!q_dev || !aligned(q_dev, 16) || !lists_dev || !aligned(lists_dev, 4)) return CA_ERR_INVALID;
+    if ((int64_t)s->t.b * kv_heads(pool->cfg) * top_k > INT32_MAX) return CA_ERR_UNSUPPORTED;
+    return CA_OK;
+}
+
+int ca_select_chunks(const ca_pool* pool, const ca_sched* s, int32_t layer, const void* q_dev, int32_t top_k,
+                     int32_t sink, int32_t recent, int32_t* lists_dev, void* stream) {
+    const Range range("ca_select_chunks");
+    const int st = list_checks(pool, s, layer, q_dev, top_k, lists_dev);
+    if (st) return st;
+    if (!(pool->cfg.flags & CA_CHUNK_BOUNDS)) return CA_ERR_INVALID;
+    if (sink < 0 || recent < 0 || (int64_t)sink + recent > top_k) return CA_ERR_INVALID;
+    const DeviceGuard dev(pool->device);
+    if (!dev.ok) return CA_ERR_CUDA;
+    return launch_select(*pool, *s, layer, q_dev, top_k, sink, recent, lists_dev, stream);
+}
+
+int ca_sparse_attention(const ca_pool* pool, const ca_sched* s, int32_t layer, const void* q_dev,
+                        const int32_t* lists_dev, int32_t top_k, void* out_dev, float scale, void* stream) {
+    const Range range("ca_sparse_attention");
+    const int st = list_checks(pool, s, layer, q_dev, top_k, lists_dev);
+    if (st) return st;
+    if (!out_dev || !aligned(out_dev, 16)) return CA_ERR_INVALID;
+    const DeviceGuard dev(pool->device);
+    if (!dev.ok) return CA_ERR_CUDA;
+    return launch_sparse(*pool, *s, layer, q_dev, lists_dev, top_k, out_dev, scale, stream);
 }
 
 int ca_sched_device_status(const ca_sched* s, void* stream) {

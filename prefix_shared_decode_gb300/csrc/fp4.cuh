@@ -1,0 +1,201 @@
+// The 4-bit pool's tile format and the device code that reads it into tensor
+// core fragments.
+//
+// Blocks of 16 consecutive dims of a row share one E4M3 scale; a code is an
+// E2M1 value (0, .5, 1, 1.5, 2, 3, 4, 6 and a sign).  code * scale has at
+// most 6 significant bits and lies between 2^-10 and 2688, so it is exact in
+// fp16: the products below are those of an fp16 pool holding these values.
+//
+// One chunk of one key/value head is a contiguous tile
+//     K codes [c x D/2 B] | V codes [c x D/2 B] | K scales [c x D/16 B] | V scales [c x D/16 B]
+// (9216 bytes at c = 64, D = 128) fetched by one bulk copy.  Inside it every
+// array is laid out for m16n8k16 fragments, so that a lane's operands come
+// with few wide shared-memory loads and no bank conflicts.  With lane
+// (g, t) = (lane / 4, lane % 4), tokens taken 16 at a time:
+//  * K (operand A of S = K q: rows tokens, columns dims).  Storage row
+//    m = f4_row(token) is fragment row m.  In a row, dim 16 kk + 4t + j is
+//    byte t * D/8 + 2 kk + j / 2, nibble j % 2: a lane's codes of all steps
+//    kk are D/8 consecutive bytes, each byte a pair of adjacent columns (the
+//    columns are permuted inside a step; the query fragments take the same
+//    order).
+//  * V (operand A of O^T += V^T p: rows dims, columns tokens).  Row = token;
+//    dim 16 db + 2g + h is byte db of unit g, nibble h: a lane's D/8 dims of a
+//    token are D/16 consecutive bytes.  Fragment columns 2t, 2t + 1, 2t + 8,
+//    2t + 9 are tokens t, t + 4, t + 8, t + 12 (the order in which S^T's rows
+//    reach the operand p); two tokens' words are interleaved by nibble masks
+//    into bytes that hold one dim of both.  At D = 128 unit g of a row sits
+//    at g ^ 4 when bit 1 of the token is set (two rows share 128 bytes).
+//  * K scales: row m, one byte per step kk.
+//  * V scales: tokens x and x + 4 (and x + 8, x + 12) paired, [pair][db][2],
+//    so that 16 bits convert to the pair of scales that a fragment register's
+//    two tokens need.
+#pragma once
+
+#include "device.cuh"
+
+namespace ca {
+namespace dev {
+
+template <int C, int D>
+struct F4Tile {
+    static constexpr int kCodes = C * D / 2;
+    static constexpr int kScales = C * D / 16;
+    static constexpr int kVCodes = kCodes;
+    static constexpr int kKScales = 2 * kCodes;
+    static constexpr int kVScales = 2 * kCodes + kScales;
+    static constexpr int kBytes = 2 * (kCodes + kScales);
+};
+
+// Storage row of a token's keys inside its block of 16 (and back).
+__host__ __device__ constexpr int f4_row(int tok) {
+    return (tok & ~7) | ((tok & 3) << 1) | ((tok >> 2) & 1);
+}
+__host__ __device__ constexpr int f4_token(int row) {
+    return (row & ~7) | ((row & 1) << 2) | ((row >> 1) & 3);
+}
+// Byte offsets inside the four arrays.  Keys: the pair of dims d, d + 1 (d even).
+template <int D>
+__host__ __device__ constexpr int f4_k_byte(int tok, int d) {
+    return f4_row(tok) * (D / 2) + ((d & 15) >> 2) * (D / 8) + (d >> 4) * 2 + ((d & 3) >> 1);
+}
+template <int D>
+__host__ __device__ constexpr int f4_v_unit(int tok, int g) {
+    return D == 128 ? (g ^ ((tok & 2) << 1)) : g;
+}
+template <int D>
+__host__ __device__ constexpr int f4_v_byte(int tok, int d) {
+    return tok * (D / 2) + f4_v_unit<D>(tok, (d & 15) >> 1) * (D / 16) + (d >> 4);
+}
+template <int D>
+__host__ __device__ constexpr int f4_k_scale(int tok, int blk) {
+    return f4_row(tok) * (D / 16) + blk;
+}
+template <int D>
+__host__ __device__ constexpr int f4_v_scale(int tok, int blk) {
+    return (tok & ~15) * (D / 16) + ((((tok >> 3) & 1) * 4 + (tok & 3)) * (D / 16) + blk) * 2 + ((tok >> 2) & 1);
+}
+
+// Two E2M1 codes (low nibble first) as an fp16 pair.
+__device__ __forceinline__ uint32_t f16x2_from_e2m1x2(uint32_t v8) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}" : "=r"(r) : "r"(v8));
+    return r;
+}
+// E2M1 codes of two fp32 values (nearest even, saturating): lo in the low nibble.
+__device__ __forceinline__ uint32_t e2m1x2_from_f32(float lo, float hi) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}"
+        : "=r"(r)
+        : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+template <int N>
+__device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
+    static_assert(N == 1 || N == 2 || N == 4, "one load");
+    if constexpr (N == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    } else if constexpr (N == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        w[0] = v.x; w[1] = v.y;
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+}
+
+// Scores of the 16 tokens of block `blk` against NB groups of 8 query rows:
+// s[nb] is the accumulator tile (rows g and g + 8 = tokens f4_token(g) and
+// f4_token(g + 8) of the block, columns 2t and 2t + 1 = query rows).  The
+// E4M3 scale of a row differs from step to step, so each step's product is
+// taken from zero and added times the scale in fp32 (two FMAs per row and
+// column pair instead of scaling four operand registers, and no rounding).
+// ONE: every column carries the same query (only columns 0 of s are formed).
+// qb[nb][kk]: query dims 16 kk + 4t, + 1 and 16 kk + 4t + 2, + 3.
+template <int C, int D, int NB, bool ONE>
+__device__ __forceinline__ void f4_scores(const uint8_t* tile, int blk, const uint32_t (&qb)[NB][D / 16][2],
+                                          float (&s)[NB][4], int lane) {
+    using T = F4Tile<C, D>;
+    const int g = lane >> 2, t = lane & 3;
+    const uint8_t* kc = tile + (blk * 16 + g) * (D / 2) + t * (D / 8);
+    const uint8_t* ks = tile + T::kKScales + (blk * 16 + g) * (D / 16);
+    uint32_t w0[D / 32], w1[D / 32], c0[D / 64], c1[D / 64];
+    lds_words<D / 32>(kc, w0);
+    lds_words<D / 32>(kc + 8 * (D / 2), w1);
+    lds_words<D / 64>(ks, c0);
+    lds_words<D / 64>(ks + 8 * (D / 16), c1);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.f;
+#pragma unroll
+    for (int kp = 0; kp < D / 32; ++kp) {                 // two steps: one word of codes, two scales
+        const uint32_t h0 = f16x2_from_e4m3x2(c0[kp >> 1] >> (16 * (kp & 1)));
+        const uint32_t h1 = f16x2_from_e4m3x2(c1[kp >> 1] >> (16 * (kp & 1)));
+        const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+        const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t x0 = w0[kp] >> (16 * e), x1 = w1[kp] >> (16 * e);
+            const uint32_t a[4] = {f16x2_from_e2m1x2(x0), f16x2_from_e2m1x2(x1), f16x2_from_e2m1x2(x0 >> 8),
+                                   f16x2_from_e2m1x2(x1 >> 8)};
+            const float r0 = e ? f0.y : f0.x, r1 = e ? f1.y : f1.x;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                mma16816(acc, a, qb[nb][2 * kp + e][0], qb[nb][2 * kp + e][1]);
+                s[nb][0] = fmaf(acc[0], r0, s[nb][0]);
+                s[nb][2] = fmaf(acc[2], r1, s[nb][2]);
+                if constexpr (!ONE) {
+                    s[nb][1] = fmaf(acc[1], r0, s[nb][1]);
+                    s[nb][3] = fmaf(acc[3], r1, s[nb][3]);
+                }
+            }
+        }
+    }
+}
+
+// O^T += V^T p for the 16 tokens of block `blk`: o[nb][db] holds dims
+// 16 db + 2g (c0, c1: query rows 2t, 2t + 1) and 16 db + 2g + 1 (c2, c3).
+// pb[nb]: p's operand, token pairs (t, t + 4) and (t + 8, t + 12).  The values
+// are scaled before the product (exact in fp16): a scale moved onto p would
+// round p, whose small weights are near fp16's smallest already.
+template <int C, int D, int NB>
+__device__ __forceinline__ void f4_pv(const uint8_t* tile, int blk, const uint32_t (&pb)[NB][2],
+                                      float (&o)[NB][D / 16][4], int lane) {
+    using T = F4Tile<C, D>;
+    const int g = lane >> 2, t = lane & 3;
+    const int tok = blk * 16 + t;
+    const uint8_t* vc = tile + T::kVCodes + tok * (D / 2) + f4_v_unit<D>(t, g) * (D / 16);
+    const uint8_t* vs = tile + T::kVScales + blk * 16 * (D / 16) + t * (D / 8);
+    constexpr int NW = D / 64;
+    uint32_t wa[NW], wb[NW], wc[NW], wd[NW], sab[D / 32], scd[D / 32];
+    lds_words<NW>(vc, wa);
+    lds_words<NW>(vc + 4 * (D / 2), wb);
+    lds_words<NW>(vc + 8 * (D / 2), wc);
+    lds_words<NW>(vc + 12 * (D / 2), wd);
+    lds_words<D / 32>(vs, sab);
+    lds_words<D / 32>(vs + 4 * (D / 8), scd);
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {                        // four blocks of dims per word
+        const uint32_t lo = 0x0f0f0f0fu, hi = 0xf0f0f0f0u;
+        const uint32_t e0 = (wa[i] & lo) | ((wb[i] << 4) & hi), e1 = ((wa[i] >> 4) & lo) | (wb[i] & hi);
+        const uint32_t e2 = (wc[i] & lo) | ((wd[i] << 4) & hi), e3 = ((wc[i] >> 4) & lo) | (wd[i] & hi);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int db = 4 * i + j;
+            const uint32_t x = f16x2_from_e4m3x2(sab[db >> 1] >> (16 * (db & 1)));
+            const uint32_t y = f16x2_from_e4m3x2(scd[db >> 1] >> (16 * (db & 1)));
+            const uint32_t a[4] = {mul_f16x2(f16x2_from_e2m1x2(e0 >> (8 * j)), x),
+                                   mul_f16x2(f16x2_from_e2m1x2(e1 >> (8 * j)), x),
+                                   mul_f16x2(f16x2_from_e2m1x2(e2 >> (8 * j)), y),
+                                   mul_f16x2(f16x2_from_e2m1x2(e3 >> (8 * j)), y)};
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma16816(o[nb][db], a, pb[nb][0], pb[nb][1]);
+        }
+    }
+}
+
+}  // namespace dev
+}  // namespace ca

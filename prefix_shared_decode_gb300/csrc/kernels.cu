@@ -47,6 +47,8 @@
 #include <cstring>
 
 #include "ca_internal.h"
+#include "device.cuh"
+#include "fp4.cuh"
 
 namespace ca {
 namespace dev {
@@ -62,179 +64,9 @@ constexpr int kRing = 16;                  // unit announcements (producer -> co
 // Merge CTAs: one warp per pair, 16 warps a CTA (fewer CTAs to retire at
 // the hand-over than 4-warp CTAs; measured 2% faster calls at 72 MB of KV)
 constexpr int kMergeWarps = 16;
-constexpr unsigned kFull = 0xffffffffu;
-constexpr unsigned long long kWaitLimitNs = 1000000000ull;  // 1 s
 
-// ---------------------------------------------------------------------------
-// PTX wrappers
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_expect_tx_only(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ unsigned long long global_ns() {
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-// Wait for an mbarrier phase; false after about a second (never hangs).
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = global_ns();
-    for (uint32_t spin = 0; spin < (1u << 28); ++spin) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((spin & 63) == 63 && global_ns() - t0 > kWaitLimitNs) return false;
-    }
-    return false;
-}
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y,
-                                            uint32_t bar, uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy)
-        : "memory");
-}
-__device__ __forceinline__ uint64_t policy_evict_first() {
-    uint64_t p;
-    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
-    return p;
-}
 __device__ __forceinline__ void consumer_sync() {   // named barrier over the 4 consumer warps
     asm volatile("bar.sync 1, %0;" ::"n"(kConsumerWarps * 32) : "memory");
-}
-__device__ __forceinline__ float ex2(float x) {      // 2^x, hardware approximation
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2,
-                                        uint32_t& r3) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
-                 : "r"(addr));
-}
-__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2,
-                                          uint32_t& r3) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
-                 : "r"(addr));
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-    uint32_t r;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(addr));
-    return r;
-}
-__device__ __forceinline__ void lds64(uint32_t addr, uint32_t& r0, uint32_t& r1) {
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(addr));
-}
-__device__ __forceinline__ void ldsm_x2(uint32_t addr, uint32_t& r0, uint32_t& r1) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(addr));
-}
-// The 8x8 b16 matrix held in fragment layout (lane L: row L/4, columns
-// 2(L%4), 2(L%4)+1) transposed across the warp.
-__device__ __forceinline__ uint32_t movm_trans(uint32_t a) {
-    uint32_t d;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
-    return d;
-}
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-    __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&h);
-}
-// FP8 E4M3 <-> fp16/fp32 conversions (hardware cvt, round to nearest even).
-// In a packed pair the byte at the lower address is the low half.
-__device__ __forceinline__ uint32_t f16x2_from_e4m3x2(uint32_t v16) {
-    uint32_t r;
-    const uint16_t v = (uint16_t)v16;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(v));
-    return r;
-}
-__device__ __forceinline__ uint32_t e4m3x2_from_f32(float lo, float hi) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-// A lane's DPL consecutive values: fp16 loads as packed pairs, fp32 loads and
-// stores (DPL = 2, 4 or 8).
-template <int DPL>
-__device__ __forceinline__ void ld_h(const void* src, uint32_t (&w)[DPL / 2]) {
-    if constexpr (DPL == 8) {
-        const uint4 v = *reinterpret_cast<const uint4*>(src);
-        w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-    } else if constexpr (DPL == 4) {
-        const uint2 v = *reinterpret_cast<const uint2*>(src);
-        w[0] = v.x; w[1] = v.y;
-    } else {
-        w[0] = *reinterpret_cast<const uint32_t*>(src);
-    }
-}
-template <int DPL>
-__device__ __forceinline__ void ldcg_f(const float* src, float (&v)[DPL]) {
-    if constexpr (DPL >= 4) {
-#pragma unroll
-        for (int i = 0; i < DPL; i += 4) {
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(src + i));
-            v[i] = x.x; v[i + 1] = x.y; v[i + 2] = x.z; v[i + 3] = x.w;
-        }
-    } else {
-        const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
-        v[0] = x.x; v[1] = x.y;
-    }
-}
-template <int DPL>
-__device__ __forceinline__ void st_f(float* dst, const float (&v)[DPL]) {
-    if constexpr (DPL >= 4) {
-#pragma unroll
-        for (int i = 0; i < DPL; i += 4)
-            *reinterpret_cast<float4*>(dst + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-    } else {
-        *reinterpret_cast<float2*>(dst) = make_float2(v[0], v[1]);
-    }
-}
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait_all() {
-    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
-}
-__device__ __forceinline__ void set_status(int32_t* status, int32_t code) {
-    atomicCAS(status, 0, code);
-}
-
-// Byte offset of 16-byte column chunk k of row r inside a tile stored as
-// boxes of `rows` x 128 B (a row's bytes split 128 at a time), each 128-byte
-// swizzled (TMA SWIZZLE_128B: chunk index XOR row mod 8).
-__device__ __forceinline__ uint32_t swz(int r, int k, int rows) {
-    return (uint32_t)((k >> 3) * rows * 128 + r * 128 + (((k & 7) ^ (r & 7)) << 4));
 }
 
 // ---------------------------------------------------------------------------
@@ -727,14 +559,93 @@ __device__ __forceinline__ void f8_tile_to_f16(const uint8_t* src, uint8_t* dst,
     }
 }
 
+// An fp4 chunk-head tile widened to the fp16 K and V tiles that the 16-row
+// blocks read (code * scale is exact in fp16).  All consumer threads take
+// part.  A thread takes 16 bytes (8 at D = 64) of a row's key codes: four
+// dims of every 16, and 8 (4) bytes of a token's value codes: two dims of
+// every 16; consecutive threads take rows whose swizzled 16-byte columns
+// differ.
+template <int C, int D>
+__device__ __forceinline__ void f4_tile_to_f16(const uint8_t* src, uint8_t* kd, uint8_t* vd, int tid) {
+    using T = F4Tile<C, D>;
+    constexpr int NK = D / 16;
+    for (int i = tid; i < C * 4; i += kConsumerWarps * 32) {
+        const int t = i & 3, r = i >> 2;
+        // rows of 8 in the order 0 1 4 5 2 3 6 7: tokens 0 4 2 6, then 1 5 3 7
+        const int m = (r & ~7) | (r & 1) | ((r & 2) << 1) | ((r & 4) >> 1);
+        const int tok = f4_token(m);
+        uint32_t w[D / 32], sc[D / 64];
+        lds_words<D / 32>(src + m * (D / 2) + t * (D / 8), w);
+        lds_words<D / 64>(src + T::kKScales + m * (D / 16), sc);
+#pragma unroll
+        for (int kk = 0; kk < NK; ++kk) {
+            const uint32_t x = w[kk >> 1] >> (16 * (kk & 1));
+            const uint32_t s2 = f16x2_from_e4m3x2(((sc[kk >> 2] >> (8 * (kk & 3))) & 0xffu) * 0x101u);
+            const uint2 o = make_uint2(mul_f16x2(f16x2_from_e2m1x2(x), s2), mul_f16x2(f16x2_from_e2m1x2(x >> 8), s2));
+            *reinterpret_cast<uint2*>(kd + swz(tok, 2 * kk + (t >> 1), C) + 8 * (t & 1)) = o;
+        }
+    }
+    for (int i = tid; i < C * 8; i += kConsumerWarps * 32) {
+        const int g = i & 7, r = i >> 3;
+        // four rows of a warp: tokens 0 2 4 6, then 1 3 5 7 of each 8
+        const int tok = (r & ~7) | ((r & 3) << 1) | ((r >> 2) & 1);
+        uint32_t w[D / 64];
+        lds_words<D / 64>(src + T::kVCodes + tok * (D / 2) + f4_v_unit<D>(tok, g) * (D / 16), w);
+#pragma unroll
+        for (int db = 0; db < NK; ++db) {
+            const uint32_t s2 = f16x2_from_e4m3x2(src[T::kVScales + f4_v_scale<D>(tok, db)] * 0x101u);
+            *reinterpret_cast<uint32_t*>(vd + swz(tok, 2 * db + (g >> 2), C) + 4 * (g & 3)) =
+                mul_f16x2(f16x2_from_e2m1x2(w[db >> 2] >> (8 * (db & 3))), s2);
+        }
+    }
+}
+
+// Sequence-first on an fp4 pool: one query row against the 16 tokens of
+// block `blk` of a tile, on the tensor cores with the query replicated over
+// the 8 columns (as sf_chunk_f8_tc does; on CUDA cores the widening alone
+// would outweigh the tile's bytes).  Only columns 0 (c0, c2) are formed.
+// The weights are held times 2^10 in their fp16 operand (p <= 1024), so that
+// they stay normal numbers down to 2^-24 of the largest; m is lowered to match.
+constexpr float kF4Lift = 10.f;
+template <int C, int D>
+__device__ __forceinline__ void sf_chunk_f4_tc(const uint8_t* tile, int blk, int ntok,
+                                               const uint32_t (&qb)[1][D / 16][2], float scale_log2, float& m,
+                                               float& s, float (&oc)[1][D / 16][4], int lane) {
+    const int g = lane >> 2;
+    float acc[1][4];
+    f4_scores<C, D, 1, true>(tile, blk, qb, acc, lane);
+    const int r0 = blk * 16 + f4_token(g);
+    const float x0 = (r0 < ntok) ? acc[0][0] * scale_log2 : -INFINITY;
+    const float x1 = (r0 + 8 < ntok) ? acc[0][2] * scale_log2 : -INFINITY;
+    float mx = fmaxf(x0, x1);
+#pragma unroll
+    for (int off = 4; off <= 16; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
+    const float mnew = fmaxf(m, mx - kF4Lift);
+    const float mu = (mnew == -INFINITY) ? 0.f : mnew;
+    const float alpha = ex2(m - mu);
+    const float p0 = ex2(x0 - mu), p1 = ex2(x1 - mu);
+    float ps = p0 + p1;
+#pragma unroll
+    for (int off = 4; off <= 16; off <<= 1) ps += __shfl_xor_sync(kFull, ps, off);
+    s = s * alpha + ps;
+    m = mnew;
+#pragma unroll
+    for (int db = 0; db < D / 16; ++db) {
+        oc[0][db][0] *= alpha;
+        oc[0][db][2] *= alpha;
+    }
+    const uint32_t pb[1][2] = {{movm_trans(pack_half2(p0, p0)), movm_trans(pack_half2(p1, p1))}};
+    f4_pv<C, D, 1>(tile, blk, pb, oc, lane);
+}
+
 // Shared-memory map of one CTA.  EB: bytes per stored K/V element (2 for
-// fp16, 1 for fp8, which adds an fp16 copy of one stage for the transposed
-// few-row products).
+// fp16; 1 for fp8, which adds an fp16 copy of one stage for the transposed
+// few-row products; 0 for fp4, which adds it for the 16-row blocks).
 template <int C, int D, int EB>
 struct Smem {
-    static constexpr int kTile = C * D * EB;    // one K or V tile of one chunk-head
+    static constexpr int kTile = EB ? C * D * EB : F4Tile<C, D>::kBytes / 2;   // one K or V tile of one chunk-head
     static constexpr int kStage = 2 * kTile;    // K then V
-    static constexpr int kConvBytes = EB == 1 ? 2 * C * D * 2 : 0;
+    static constexpr int kConvBytes = EB <= 1 ? 2 * C * D * 2 : 0;
     static constexpr int kQBytes = q_rows<D>() * D * 2;
     // head_dim 256: score halves exchanged by warp pairs, two chunk parities
     static constexpr int kXsBytes = D == 256 ? 2 * kConsumerWarps * (C / 8) * 4 * 32 * 4 : 0;
@@ -819,7 +730,20 @@ __device__ __forceinline__ bool sf_rows_transposed(
             }
             if (act) {
                 const int tok0 = 16 * w;
+                // token of the block in fragment row g (fp4 tiles: f4_token)
+                const int tg = EB == 0 ? f4_token(g) : g;
                 float sacc[4] = {0.f, 0.f, 0.f, 0.f};
+                if constexpr (EB == 0) {
+                    uint32_t qb[1][D / 16][2];
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        lds64(smem_u32(qreg) + swz(g, 2 * kk + (t >> 1), q_rows<D>()) + 8 * (t & 1), qb[0][kk][0],
+                              qb[0][kk][1]);
+                    float s4[1][4];
+                    f4_scores<C, D, 1, false>(stages + (size_t)st * SM::kStage, w, qb, s4, lane);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sacc[e] = s4[0][e];
+                } else {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     // Q^T as the B operand: n = query row (lane & 7), k = 16 dims
@@ -828,11 +752,12 @@ __device__ __forceinline__ bool sf_rows_transposed(
                     ldsm_x4(kt + swz(tok0 + (lane & 15), 2 * kk + (lane >> 4), C), a[0], a[1], a[2], a[3]);
                     mma16816(sacc, a, qb0, qb1);
                 }
-                // sacc: (token g, rows 2t, 2t+1), (token g + 8, rows 2t, 2t+1)
+                }
+                // sacc: (token tg, rows 2t, 2t+1), (token tg + 8, rows 2t, 2t+1)
                 float x[4], mx[2];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int tok = tok0 + g + 8 * (i >> 1), row = 2 * t + (i & 1);
+                    const int tok = tok0 + tg + 8 * (i >> 1), row = 2 * t + (i & 1);
                     const bool valid = tok < ntok && row < m_rows && ctx0 + tok <= limr[i & 1];
                     x[i] = valid ? sacc[i] * p.scale_log2 : -INFINITY;
                 }
@@ -872,6 +797,11 @@ __device__ __forceinline__ bool sf_rows_transposed(
                 // P^T fragments: k = tokens, n = query rows
                 const uint32_t b0 = movm_trans(pack_half2(p0, p1));   // tokens 0..7
                 const uint32_t b1 = movm_trans(pack_half2(p2, p3));   // tokens 8..15
+                if constexpr (EB == 0) {
+                    const uint32_t pb[1][2] = {{b0, b1}};
+                    f4_pv<C, D, 1>(stages + (size_t)st * SM::kStage, w, pb,
+                                   reinterpret_cast<float(&)[1][D / 16][4]>(ot), lane);
+                } else {
 #pragma unroll
                 for (int db = 0; db < D / 16; ++db) {
                     uint32_t a[4];
@@ -879,8 +809,9 @@ __device__ __forceinline__ bool sf_rows_transposed(
                               a[0], a[1], a[2], a[3]);
                     mma16816(ot[db], a, b0, b1);
                 }
+                }
             }
-            if constexpr (EB == 2) {
+            if constexpr (EB != 1) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty0 + 8 * st);
             }
@@ -933,8 +864,12 @@ __device__ __forceinline__ bool sf_rows_transposed(
                     float* dst = p.part_o + (size_t)pid * D;
 #pragma unroll
                     for (int db = 0; db < D / 16; ++db) {
-                        dst[16 * db + g] = ot[db][r];
-                        dst[16 * db + g + 8] = ot[db][r + 2];
+                        if constexpr (EB == 0) {          // dims 16db + 2g, 16db + 2g + 1
+                            *reinterpret_cast<float2*>(dst + 16 * db + 2 * g) = make_float2(ot[db][r], ot[db][r + 2]);
+                        } else {
+                            dst[16 * db + g] = ot[db][r];
+                            dst[16 * db + g + 8] = ot[db][r + 2];
+                        }
                     }
                     if (g == 0) p.part_ms[pid] = make_float2(m[r], s[r]);
                 }
@@ -957,7 +892,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 two_phase_attention_kernel(const __grid_constant__ CUtensorMap tmap, const AttnParams p) {
     using SM = Smem<C, D, EB>;
     constexpr int DPL = D / 32;
-    constexpr int BOXES = D * EB / 128;   // 128-byte boxes per tile row
+    constexpr int BOXES = EB ? D * EB / 128 : 1;   // 128-byte boxes per tile row (fp4: one bulk copy)
     // single-row sequence-first work of an fp8 pool with 64-token chunks
     // runs on the tensor cores (sf_chunk_f8_tc), elsewhere on CUDA cores
     constexpr bool kF8Tc = EB == 1 && C == 64 && D == 128;
@@ -1006,7 +941,8 @@ two_phase_attention_kernel(const __grid_constant__ CUtensorMap tmap, const AttnP
         // ------------------------------ producer ------------------------------
         if (lane != 0) return;
         // the tensor map's descriptor is fetched while the plan line loads
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap)) : "memory");
+        if constexpr (EB != 0)
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap)) : "memory");
         if (p.test_stall) {
             // Test hook (ca_sched_inject_stall): wait for stage 0's first
             // phase, which nothing completes since no copy has been issued;
@@ -1132,12 +1068,17 @@ two_phase_attention_kernel(const __grid_constant__ CUtensorMap tmap, const AttnP
                 // flight) has been written and the producer has arrived.
                 mbar_expect_tx_only(fb, SM::kStage);
                 const uint32_t dst = smem_u32(stages + (size_t)st * SM::kStage);
-                const int rowK = (((ch.slot * p.n_layers + p.layer) * 2 + 0) * HK + head) * C;
-                const int rowV = rowK + HK * C;
+                if constexpr (EB == 0) {
+                    bulk_load(dst, p.kv + (((long long)ch.slot * p.n_layers + p.layer) * HK + head) * SM::kStage,
+                              SM::kStage, fb, pol);
+                } else {
+                    const int rowK = (((ch.slot * p.n_layers + p.layer) * 2 + 0) * HK + head) * C;
+                    const int rowV = rowK + HK * C;
 #pragma unroll
-                for (int bx = 0; bx < BOXES; ++bx) {
-                    tma_load_2d(dst + bx * C * 128, &tmap, bx * (128 / EB), rowK, fb, pol);
-                    tma_load_2d(dst + SM::kTile + bx * C * 128, &tmap, bx * (128 / EB), rowV, fb, pol);
+                    for (int bx = 0; bx < BOXES; ++bx) {
+                        tma_load_2d(dst + bx * C * 128, &tmap, bx * (128 / EB), rowK, fb, pol);
+                        tma_load_2d(dst + SM::kTile + bx * C * 128, &tmap, bx * (128 / EB), rowV, fb, pol);
+                    }
                 }
                 stage_ntok[st] = min(max(ntok, 0), C);
                 stage_tok0[st] = tok0;
@@ -1236,7 +1177,50 @@ two_phase_attention_kernel(const __grid_constant__ CUtensorMap tmap, const AttnP
                 float* xo = reinterpret_cast<float*>(qreg) + (flush & 1) * kConsumerWarps * D;
                 float* xm = xms + (flush & 1) * 2 * kConsumerWarps;
                 float m = -INFINITY, s = 0.f;
-                if constexpr (kF8Tc) {
+                if constexpr (EB == 0) {
+                    // The query in fragment order: step kk wants dims
+                    // 16kk + 4t .. + 3, held by lane 4kk + t (D = 128) or in
+                    // pairs by lanes 8kk + 2t, + 1 (D = 64).
+                    uint32_t qb[1][D / 16][2];
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        if constexpr (D == 128) {
+                            qb[0][kk][0] = __shfl_sync(kFull, qraw.x, 4 * kk + (lane & 3));
+                            qb[0][kk][1] = __shfl_sync(kFull, qraw.y, 4 * kk + (lane & 3));
+                        } else {
+                            qb[0][kk][0] = __shfl_sync(kFull, qraw.x, 8 * kk + 2 * (lane & 3));
+                            qb[0][kk][1] = __shfl_sync(kFull, qraw.x, 8 * kk + 2 * (lane & 3) + 1);
+                        }
+                    }
+                    float oc[1][D / 16][4];
+#pragma unroll
+                    for (int db = 0; db < D / 16; ++db)
+                        oc[0][db][0] = oc[0][db][1] = oc[0][db][2] = oc[0][db][3] = 0.f;
+                    for (; L < seg_end; ++L, ++it) {
+                        const int st = it % S;
+                        if (!mbar_wait(full0 + 8 * st, (uint32_t)(it / S) & 1u)) {
+                            set_status(p.status, CA_ERR_TIMEOUT);
+                            return;
+                        }
+                        const int ntok = stage_ntok[st];
+                        // The tile's C / 16 blocks go to the warps in turn,
+                        // tile after tile (a 16-token tile to one warp).
+                        constexpr int NBLK = C / 16;
+                        const int blk = NBLK == 4 ? w : (w - it * NBLK) & 3;
+                        if (blk < NBLK && blk * 16 < ntok)
+                            sf_chunk_f4_tc<C, D>(stages + (size_t)st * SM::kStage, blk, ntok, qb, p.scale_log2, m, s,
+                                                 oc, lane);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(empty0 + 8 * st);
+                    }
+                    // lane (g, 0) holds dims 16db + 2g, + 1
+                    if ((lane & 3) == 0) {
+#pragma unroll
+                        for (int db = 0; db < D / 16; ++db)
+                            *reinterpret_cast<float2*>(xo + w * D + 16 * db + 2 * (lane >> 2)) =
+                                make_float2(oc[0][db][0], oc[0][db][2]);
+                    }
+                } else if constexpr (kF8Tc) {
                     // The query in fragment order: lane L holds dims 4L .. 4L + 3,
                     // step kk wants dims 16kk + 4t .. + 3, i.e. lane 4kk + t's.
                     uint32_t qb[8][2];
@@ -1405,7 +1389,17 @@ two_phase_attention_kernel(const __grid_constant__ CUtensorMap tmap, const AttnP
                     const int ntok = stage_ntok[st];
                     const int ctx0 = stage_tok0[st];
                     // an fp8 stage is read as E4M3 bytes, straight into the
-                    // fragments (cf_chunk<..., true>)
+                    // fragments (cf_chunk<..., true>); an fp4 stage is widened
+                    // once for all the warps
+                    if constexpr (EB == 0) {
+                        consumer_sync();
+                        f4_tile_to_f16<C, D>(stages + (size_t)st * SM::kStage, conv, conv + SM::kConvBytes / 2,
+                                             threadIdx.x);
+                        consumer_sync();
+                        if (lane == 0) mbar_arrive(empty0 + 8 * st);
+                        kt = smem_u32(conv);
+                        vt = kt + SM::kConvBytes / 2;
+                    }
                     if constexpr (kSplit) {
                         if (active) {
                             constexpr int kXs = (C / 8) * 4 * 32;     // floats per warp slot
@@ -1425,8 +1419,10 @@ two_phase_attention_kernel(const __grid_constant__ CUtensorMap tmap, const AttnP
                                                             p.scale_log2, m, s, o, lane);
                         }
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(empty0 + 8 * st);
+                    if constexpr (EB != 0) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(empty0 + 8 * st);
+                    }
                 }
                 // Row sums are per thread so far: reduce over the quad.
 #pragma unroll
@@ -1604,7 +1600,17 @@ void* kernel_ptr(bool rows) {
 // rows: the schedule brings 2..8 query rows per position and key/value head
 // (the few-row variant exists for head_dim <= 128).
 void* pick_kernel(const PoolCfg& c, bool rows = false) {
-    if (kv_elem_bytes(c) == 1) {
+    if (kv_elem_bytes(c) == 0) {
+        if (c.head_dim == 128) {
+            if (c.chunk == 64) return kernel_ptr<64, 128, 0>(rows);
+            if (c.chunk == 32) return kernel_ptr<32, 128, 0>(rows);
+            if (c.chunk == 16) return kernel_ptr<16, 128, 0>(rows);
+        } else if (c.head_dim == 64) {
+            if (c.chunk == 64) return kernel_ptr<64, 64, 0>(rows);
+            if (c.chunk == 32) return kernel_ptr<32, 64, 0>(rows);
+            if (c.chunk == 16) return kernel_ptr<16, 64, 0>(rows);
+        }
+    } else if (kv_elem_bytes(c) == 1) {
         if (c.head_dim != 128) return nullptr;
         if (c.chunk == 64) return kernel_ptr<64, 128, 1>(rows);
         if (c.chunk == 32) return kernel_ptr<32, 128, 1>(rows);
@@ -1626,10 +1632,10 @@ void* pick_kernel(const PoolCfg& c, bool rows = false) {
 // The kernel's dynamic shared memory (the Smem map above, computed here).
 size_t smem_for(const PoolCfg& c, int stages) {
     const size_t eb = (size_t)kv_elem_bytes(c), cd = (size_t)c.chunk * c.head_dim;
-    const size_t conv = eb == 1 ? 2 * cd * 2 : 0;
+    const size_t conv = eb <= 1 ? 2 * cd * 2 : 0;
     const size_t qrows = c.head_dim == 256 ? 32 : dev::kQRows;
     const size_t xs = c.head_dim == 256 ? (size_t)2 * dev::kConsumerWarps * (c.chunk / 8) * 4 * 32 * 4 : 0;
-    return (size_t)stages * 2 * cd * eb + conv + xs + qrows * c.head_dim * 2 + 512 +
+    return (size_t)stages * pair_tile_bytes(c) + conv + xs + qrows * c.head_dim * 2 + 512 +
            2 * dev::kMaxStages * 8 + 4 * dev::kRing + 2 * 4 * dev::kMaxStages;
 }
 }  // namespace
@@ -1666,6 +1672,10 @@ int kernel_ctas_per_sm(const PoolCfg& c, int* ctas) {
 }
 
 int make_tensor_map(Pool& p) {
+    if (p.cfg.flags & CA_KV_FP4) {                  // bulk copies of whole tiles: no map
+        std::memset(p.tmap, 0, sizeof p.tmap);
+        return CA_OK;
+    }
     using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -1699,6 +1709,8 @@ namespace {
 std::atomic<uint64_t> g_launches{0};
 }  // namespace
 
+void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
+
 uint64_t kernel_launches() { return g_launches.load(std::memory_order_relaxed); }
 
 int launch_scatter(const Pool& p, const void* k, const void* v, int32_t total_rows,
@@ -1708,6 +1720,11 @@ int launch_scatter(const Pool& p, const void* k, const void* v, int32_t total_ro
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
     if (cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &cap) != cudaSuccess) return CA_ERR_CUDA;
     if (cap != cudaStreamCaptureStatusNone) p.captured_writes = true;
+    if (c.flags & CA_KV_FP4) {
+        const int st = launch_fp4_store(p, k, v, total_rows, chunks, stream);
+        if (st) return st;
+        return (c.flags & CA_CHUNK_BOUNDS) ? launch_key_bounds(p, chunks, stream) : CA_OK;
+    }
     for (size_t i = 0; i < chunks.size(); i += dev::kScatterMaxChunks) {
         const size_t cnt = std::min<size_t>(dev::kScatterMaxChunks, chunks.size() - i);
         dev::ScatterArgs a;
@@ -1732,6 +1749,7 @@ int launch_scatter(const Pool& p, const void* k, const void* v, int32_t total_ro
         if (cudaGetLastError() != cudaSuccess) return CA_ERR_CUDA;
         g_launches.fetch_add(1, std::memory_order_relaxed);
     }
+    if (c.flags & CA_CHUNK_BOUNDS) return launch_key_bounds(p, chunks, stream);
     return CA_OK;
 }
 

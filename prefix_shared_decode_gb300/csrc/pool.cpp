@@ -212,11 +212,17 @@ int pool_insert(Pool& p, int64_t seq_id, const int32_t* tokens, int32_t n,
 }
 
 size_t pool_tile_bytes(const PoolCfg& c) {
-    return (size_t)c.capacity_slots * c.n_layers * 2 * kv_heads(c) * c.chunk * c.head_dim * kv_elem_bytes(c);
+    return (size_t)c.capacity_slots * c.n_layers * kv_heads(c) * pair_tile_bytes(c);
+}
+
+size_t pool_bounds_offset(const PoolCfg& c) {
+    return pool_tile_bytes(c) + (((size_t)c.capacity_slots * sizeof(int32_t) + 255) & ~size_t(255));
 }
 
 size_t pool_total_bytes(const PoolCfg& c) {
-    return pool_tile_bytes(c) + (((size_t)c.capacity_slots * sizeof(int32_t) + 255) & ~size_t(255));
+    const size_t bounds =
+        (c.flags & CA_CHUNK_BOUNDS) ? (size_t)c.capacity_slots * c.n_layers * kv_heads(c) * 2 * c.head_dim * 2 : 0;
+    return pool_bounds_offset(c) + bounds;
 }
 
 int pool_append(Pool& p, int64_t seq_id, const int32_t* tokens, int32_t n,

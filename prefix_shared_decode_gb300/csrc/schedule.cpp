@@ -79,8 +79,21 @@ int build_tables(const Pool& p, const int64_t* seq_ids, int32_t b, uint32_t flag
 
     t.b = b;
     for (auto* v : {&t.seq_perm, &t.cf_rows, &t.cf_runs, &t.sf_offsets, &t.sf_chunks, &t.merge_offsets,
-                    &t.merge_runs, &t.row_tok0, &t.sf_tok0, &t.ctx_len})
+                    &t.merge_runs, &t.row_tok0, &t.sf_tok0, &t.ctx_len, &t.list_off, &t.list_slots})
         v->clear();
+    t.list_max = 0;
+    if (flags & CA_SCHED_CHUNK_LISTS) {
+        t.list_off.reserve((size_t)b + 1);
+        t.list_off.push_back(0);
+        int64_t total = 0;
+        for (int32_t i = 0; i < b; ++i) total += (int64_t)seq_of[i]->path.size();
+        t.list_slots.reserve(total);
+        for (int32_t i = 0; i < b; ++i) {
+            for (const Node* n : seq_of[i]->path) t.list_slots.push_back(n->slot);
+            t.list_off.push_back((int32_t)t.list_slots.size());
+            t.list_max = std::max(t.list_max, (int32_t)seq_of[i]->path.size());
+        }
+    }
     const int32_t c = p.cfg.chunk;
     // Depth-first order over the shared nodes only: at a node, the sequences
     // ending there, then its children in insertion order; a child held by
@@ -193,6 +206,9 @@ constexpr double kCfComputePer16 = 0.2;
 // tile carries m query rows of work on half the bytes of an fp16 tile);
 // swept on GB300 (1.5 .. 2.8) for the fastest calls
 constexpr double kF8CfFactor = 2.0;
+// fp4 pools likewise: a chunk-first tile is widened to fp16 in shared memory
+// first, and a sequence-first one is 9/16 of an fp8 tile's bytes
+constexpr double kF4CfFactor = 3.0;
 
 // Share of the sequence-first tiles left to the tail queue that CTAs drain
 // dynamically once their static lists are done (absorbs the run-to-run rate
@@ -222,7 +238,10 @@ void build_plan(const Pool& p, const Tables& t, int32_t grid, int32_t q_len, Pla
     // An fp8 pool halves a tile's bytes while the chunk-first tensor work per
     // tile stays the same, so against single-row sequence-first tiles (and
     // only there) a chunk-first tile costs more.
-    const double cf_mult = ((p.cfg.flags & CA_KV_FP8) && RW == 1) ? kF8CfFactor : 1.0;
+    const double cf_mult = RW != 1                        ? 1.0
+                           : (p.cfg.flags & CA_KV_FP8) ? kF8CfFactor
+                           : (p.cfg.flags & CA_KV_FP4) ? kF4CfFactor
+                                                       : 1.0;
     auto rows_cost = [&](int32_t m_rows) {
         return cf_mult * (1.0 + kCfComputePer16 * ((m_rows + 15) / 16)) / sf_cost;
     };
@@ -533,8 +552,14 @@ void layout_plan(const Plan& plan, int32_t b, PlanLayout& lay, std::vector<unsig
     lay.chunk_tok0 = off; off = align256(off + plan.chunk_tok0.size() * sizeof(int32_t));
     lay.ctx_len = off;   off = align256(off + (size_t)b * sizeof(int32_t));
     lay.cta_head = off;  off = align256(off + (size_t)plan.grid * sizeof(CtaHead));
+    lay.list_off = off;   off = align256(off + t.list_off.size() * sizeof(int32_t));
+    lay.list_slots = off; off = align256(off + t.list_slots.size() * sizeof(int32_t));
     lay.total = off;
     blob.assign(off, 0);
+    if (!t.list_off.empty()) {
+        std::memcpy(blob.data() + lay.list_off, t.list_off.data(), t.list_off.size() * sizeof(int32_t));
+        std::memcpy(blob.data() + lay.list_slots, t.list_slots.data(), t.list_slots.size() * sizeof(int32_t));
+    }
     std::memcpy(blob.data() + lay.chunks, plan.chunks.data(), plan.chunks.size() * sizeof(ChunkRef));
     std::memcpy(blob.data() + lay.units, plan.units.data(), plan.units.size() * sizeof(Unit));
     std::memcpy(blob.data() + lay.seq_perm, t.seq_perm.data(), (size_t)b * sizeof(int32_t));

@@ -1,0 +1,995 @@
+// Attention over selected chunks: choosing each context's chunks by an upper
+// bound on their scores, and decode attention over listed chunks alone, for
+// every pool type.  Contexts of 10^5 tokens and more spend a decode step
+// reading keys and values that the softmax weights at nothing; the bounds are
+// 1 / (chunk length) of the keys and the lists a few of the chunks.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "ca_internal.h"
+#include "fp4.cuh"
+
+namespace ca {
+namespace dev {
+
+// ---------------------------------------------------------------------------
+// Clusters: the CTAs that share one (sequence, key/value head) meet in their
+// shared memories, so neither call needs a workspace, a second kernel or an
+// atomic whose order could change a result.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void st_peer(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ float ld_peer(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_peer4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// What both kernels read of the schedule and the pool.
+struct ListParams {
+    const uint16_t* q;            // fp16 [b][H][D]
+    const int32_t* list_off;      // chunk slots of batch row i: list_slots[list_off[i] ..)
+    const int32_t* list_slots;
+    const int32_t* slot_ntok;
+    const uint8_t* kv;
+    const uint16_t* bounds;       // [slot][L][Hkv][largest, smallest][D]
+    int32_t* status;
+    int32_t* lists;               // [b][Hkv][top_k] (read by the attention)
+    uint16_t* out;
+    int32_t n_layers, n_kv_heads, n_heads, group, layer, capacity, top_k;
+    int32_t sink, recent;         // selection
+    int32_t n_stages, splits;     // attention: ring stages; both: CTAs per cluster
+    float scale_log2, out_scale;
+};
+
+// ---------------------------------------------------------------------------
+// Selection.  score(chunk) = max over the group's rows of
+//     sum_d max(q_d hi_d, q_d lo_d) = sum_d q_d^+ hi_d + q_d^- lo_d,
+// a product of the bounds [chunks x 2D] with the rows' positive and negative
+// parts: tensor cores take it 16 chunks by 8 rows at a time, with the dims
+// permuted so that a lane's operand of a bounds row is 16 contiguous bytes
+// from global memory (nothing is staged; the kernel is bound by reading the
+// bounds once).  The CTAs of a cluster score their blocks of 16 chunks and
+// leave the scores, as order-preserving integers, in the first CTA's shared
+// memory; that CTA finds the top_k-th.
+//
+// Exact order: a 32-bit score is off by at most E (below), so with T the
+// top_k-th largest of them, a chunk above T + 2E is among the exact top_k, one
+// below T - 2E is not.  Where more chunks lie in between than places are left,
+// those few are scored again in 64 bits and ranked by (score, lower number).
+// ---------------------------------------------------------------------------
+constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
+constexpr uint32_t kSure = 0xffffffffu;   // key of a chunk that is taken
+constexpr uint32_t kTie = 0xfffffffeu;    // key of one that ties for the last places
+constexpr int kFewTies = 256;             // chunks ranked pairwise in 64 bits
+
+__device__ __forceinline__ uint32_t order_key(float x) {   // monotone; 0 for a NaN, never above kTie - 1
+    if (x != x) return 0u;
+    const uint32_t u = __float_as_uint(x + 0.f);           // -0 counts as 0
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ unsigned long long order_key(double x) {
+    if (x != x) return 0ull;
+    const unsigned long long u = (unsigned long long)__double_as_longlong(x + 0.0);
+    return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+__device__ __forceinline__ uint32_t part_f16x2(uint32_t x, bool positive) {   // max(x, 0) or min(x, 0)
+    const __half2 h = *reinterpret_cast<const __half2*>(&x), z = __float2half2_rn(0.f);
+    const __half2 r = positive ? __hmax2(h, z) : __hmin2(h, z);
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+struct SelShared {
+    uint32_t hist[256];
+    uint32_t top_abs[16];                 // largest |bound| of each CTA of the cluster (fp32 bits)
+    uint32_t red[kSelWarps][2];
+    float qsum[kSelWarps];
+    uint32_t pick_bin, pick_left;         // radix step: the digit, places left inside it
+    uint32_t n_list;
+    uint32_t list[kFewTies];
+    unsigned long long key64[kFewTies];
+};
+
+// The exact score of one chunk in 64 bits (a warp; every lane gets it).
+template <int D>
+__device__ __forceinline__ double exact_score(const ListParams& p, const uint16_t* q, const uint16_t* bounds,
+                                              int lane) {
+    double best = 0.0;
+    bool nan = false;
+    for (int r = 0; r < p.group; ++r) {
+        double s = 0.0;
+#pragma unroll
+        for (int d = lane; d < D; d += 32) {
+            const double x = (double)__half2float(__ushort_as_half(q[(size_t)r * D + d]));
+            const double hi = (double)__half2float(__ushort_as_half(bounds[d]));
+            const double lo = (double)__half2float(__ushort_as_half(bounds[D + d]));
+            s = fma(x, x > 0.0 ? hi : lo, s);
+        }
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(kFull, s, off);
+        nan = nan || s != s;
+        if (r == 0 || s > best) best = s;
+    }
+    return nan ? __longlong_as_double(0x7ff8000000000000ll) : best;
+}
+
+// Block-wide sums of two counts (every thread gets them).
+__device__ __forceinline__ uint2 sum2(SelShared& sh, uint32_t a, uint32_t b) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    a = __reduce_add_sync(kFull, a);
+    b = __reduce_add_sync(kFull, b);
+    __syncthreads();                      // earlier reads of red are done
+    if (lane == 0) { sh.red[warp][0] = a; sh.red[warp][1] = b; }
+    __syncthreads();
+    uint2 t = make_uint2(0u, 0u);
+#pragma unroll
+    for (int w = 0; w < kSelWarps; ++w) { t.x += sh.red[w][0]; t.y += sh.red[w][1]; }
+    return t;
+}
+
+// After a histogram of one digit: the digit that holds the `left`-th largest,
+// and how many places are left inside it.
+__device__ __forceinline__ void pick_digit(SelShared& sh, uint32_t left) {
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;     // lane 0 takes the eight largest digits
+        uint32_t c[8], sum = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) { c[j] = sh.hist[255 - (lane * 8 + j)]; sum += c[j]; }
+        uint32_t before = sum;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const uint32_t o = __shfl_up_sync(kFull, before, off);
+            if (lane >= off) before += o;
+        }
+        before -= sum;                    // larger digits' count
+        if (before < left && before + sum >= left) {
+            uint32_t at = before;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (at < left && at + c[j] >= left) {
+                    sh.pick_bin = 255 - (lane * 8 + j);
+                    sh.pick_left = left - at;
+                }
+                at += c[j];
+            }
+        }
+    }
+    __syncthreads();
+}
+__device__ __forceinline__ void hist_add(SelShared& sh, uint32_t digit, bool on) {   // one atomic per digit and warp
+    const uint32_t same = __match_any_sync(kFull, on ? digit : 256u);
+    if (on && (threadIdx.x & 31) == __ffs(same) - 1) atomicAdd(&sh.hist[digit], __popc(same));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const ListParams p) {
+    extern __shared__ __align__(16) uint32_t keys[];      // the first CTA's: one key per chunk
+    __shared__ SelShared sh;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int cs = p.splits, rank = blockIdx.x % cs, pair = blockIdx.x / cs;
+    const int i = pair / p.n_kv_heads, h = pair % p.n_kv_heads;
+    const int off = p.list_off[i], n = p.list_off[i + 1] - off, K = p.top_k, G = p.group;
+    int32_t* out = p.lists + (size_t)pair * K;
+    if (n <= K) {                                         // (the whole cluster: same n)
+        if (rank == 0)
+            for (int j = threadIdx.x; j < K; j += kSelThreads) out[j] = j < n ? j : -1;
+        return;
+    }
+    if (cs > 1) cluster_sync_all();                       // the first CTA's shared memory exists
+    const uint16_t* q = p.q + ((size_t)i * p.n_heads + (size_t)h * G) * D;
+    const int32_t* slots = p.list_slots + off;
+    auto bounds_of = [&](int slot) {
+        return p.bounds + (((size_t)slot * p.n_layers + p.layer) * p.n_kv_heads + h) * 2 * D;
+    };
+    const uint32_t keys0 = cs > 1 ? peer_addr(smem_u32(keys), 0) : 0u;
+    const uint32_t abs0 = cs > 1 ? peer_addr(smem_u32(sh.top_abs), 0) : 0u;
+
+    // scores of blocks of 16 chunks
+    __half2 top = __float2half2_rn(0.f);
+    bool bad = false;
+    for (int blk = rank * kSelWarps + warp; blk * 16 < n; blk += cs * kSelWarps) {
+        const int c0 = blk * 16 + g, c1 = c0 + 8;
+        int s0 = slots[min(c0, n - 1)], s1 = slots[min(c1, n - 1)];
+        if (s0 < 0 || s0 >= p.capacity) { s0 = 0; bad = true; }
+        if (s1 < 0 || s1 >= p.capacity) { s1 = 0; bad = true; }
+        const uint4* b0 = reinterpret_cast<const uint4*>(bounds_of(s0)) + t;
+        const uint4* b1 = reinterpret_cast<const uint4*>(bounds_of(s1)) + t;
+        float best0 = -INFINITY, best1 = -INFINITY;
+        bool nan0 = false, nan1 = false;
+        constexpr int J = D / 32;                         // 64-byte groups of a bounds row
+        uint4 x0[2][J], x1[2][J];
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                x0[part][j] = __ldg(b0 + part * (D / 8) + j * 4);
+                x1[part][j] = __ldg(b1 + part * (D / 8) + j * 4);
+            }
+        for (int r0 = 0; r0 < G; r0 += 8) {
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint4* qr = reinterpret_cast<const uint4*>(q + (size_t)min(r0 + g, G - 1) * D) + t;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const uint4 y = __ldg(qr + j * 4);
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    const uint4 u = x0[part][j], w = x1[part][j];
+                    const uint32_t a[4] = {u.x, w.x, u.y, w.y}, b[4] = {u.z, w.z, u.w, w.w};
+                    mma16816(acc, a, part_f16x2(y.x, part == 0), part_f16x2(y.y, part == 0));
+                    mma16816(acc, b, part_f16x2(y.z, part == 0), part_f16x2(y.w, part == 0));
+                }
+            }
+            // rows past the group repeat its last one: they change no maximum
+            best0 = fmaxf(best0, fmaxf(acc[0], acc[1]));
+            best1 = fmaxf(best1, fmaxf(acc[2], acc[3]));
+            nan0 = nan0 || acc[0] != acc[0] || acc[1] != acc[1];
+            nan1 = nan1 || acc[2] != acc[2] || acc[3] != acc[3];
+        }
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const uint32_t w[8] = {x0[part][j].x, x0[part][j].y, x0[part][j].z, x0[part][j].w,
+                                       x1[part][j].x, x1[part][j].y, x1[part][j].z, x1[part][j].w};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) top = __hmax2(top, __habs2(*reinterpret_cast<const __half2*>(&w[k])));
+            }
+#pragma unroll
+        for (int d = 1; d <= 2; d <<= 1) {
+            best0 = fmaxf(best0, __shfl_xor_sync(kFull, best0, d));
+            best1 = fmaxf(best1, __shfl_xor_sync(kFull, best1, d));
+            nan0 = __shfl_xor_sync(kFull, (int)nan0, d) || nan0;
+            nan1 = __shfl_xor_sync(kFull, (int)nan1, d) || nan1;
+        }
+        if (t < 2) {
+            const int c = t ? c1 : c0;
+            const bool forced = c < p.sink || c >= n - p.recent;
+            const uint32_t k = forced ? kSure : (t ? nan1 : nan0) ? 0u : order_key(t ? best1 : best0);
+            if (c < n) {
+                if (cs > 1) st_peer(keys0 + 4u * (uint32_t)c, k);
+                else keys[c] = k;
+            }
+        }
+    }
+    if (bad) set_status(p.status, CA_ERR_DEVICE_BOUNDS);
+    {
+        // the cluster's largest |bound|: a non-negative fp32's bits order as integers
+        const float2 f = __half22float2(top);
+        uint32_t m = __reduce_max_sync(kFull, __float_as_uint(fmaxf(f.x, f.y)));
+        if (lane == 0) sh.red[warp][0] = m;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < kSelWarps; ++w) m = max(m, sh.red[w][0]);
+            if (cs > 1) st_peer(abs0 + 4u * (uint32_t)rank, m);
+            else sh.top_abs[0] = m;
+        }
+    }
+    if (cs > 1) {
+        cluster_sync_all();
+        if (rank != 0) return;
+    } else {
+        __syncthreads();
+    }
+
+    const uint32_t places = (uint32_t)(K - p.sink - p.recent);   // n > K >= sink + recent: they do not overlap
+    uint32_t cut = kTie, ties = 0;                        // taken: keys above `cut`, and the first `ties` of kTie
+    if (places > 0) {
+        // E: with A = sum of |terms| <= max over rows of sum|q| times the largest |bound|, each of the
+        // D / 8 steps of mma (16 exact products and the running sum, aligned and cut at 2^-23 of the
+        // largest each, rounded once) is off by at most 18 * 2^-23 * A.
+        float qs = 0.f;
+        for (int r = warp; r < G; r += kSelWarps) {
+            float s = 0.f;
+            for (int d = lane; d < D; d += 32) s += fabsf(__half2float(__ushort_as_half(q[(size_t)r * D + d])));
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+            qs = fmaxf(qs, s);
+        }
+        if (lane == 0) sh.qsum[warp] = qs;
+
+        // T: the places-th largest key, digit by digit
+        uint32_t prefix = 0, left = places;
+        for (int shift = 24; shift >= 0; shift -= 8) {
+            __syncthreads();
+            for (int j = threadIdx.x; j < 256; j += kSelThreads) sh.hist[j] = 0u;
+            __syncthreads();
+            for (int j0 = 0; j0 < n; j0 += kSelThreads) {
+                const int j = j0 + threadIdx.x;
+                const uint32_t k = j < n ? keys[j] : kSure;
+                hist_add(sh, (k >> shift) & 255u, k != kSure && (shift == 24 || (k >> (shift + 8)) == prefix));
+            }
+            pick_digit(sh, left);
+            prefix = (prefix << 8) | sh.pick_bin;
+            left = sh.pick_left;
+        }
+        float A = 0.f, big = 0.f;
+#pragma unroll
+        for (int w = 0; w < kSelWarps; ++w) A = fmaxf(A, sh.qsum[w]);
+        for (int r = 0; r < cs; ++r) big = fmaxf(big, __uint_as_float(sh.top_abs[r]));
+        A *= big;
+        const float E = A * ((D / 8) * 18.2f / 8388608.f);
+        const float T = key_value(prefix);
+        uint32_t low = 0u, high = kTie - 1u;              // a band without bounds where E or T is not finite
+        if (prefix != 0u && E < 1e37f && fabsf(T) < 1e37f) {
+            const float w = 2.01f * E + fabsf(T) * 1e-6f;
+            low = max(order_key(T - w), 1u);
+            high = order_key(T + w);
+        }
+        uint32_t above = 0, band = 0;
+        for (int j = threadIdx.x; j < n; j += kSelThreads) {
+            const uint32_t k = keys[j];
+            above += k > high && k != kSure;
+            band += k >= low && k <= high;
+        }
+        const uint2 c = sum2(sh, above, band);
+        const uint32_t open = places - c.x;               // places left for the band
+        cut = high;
+        if (c.y == open) {
+            cut = low - 1u;                               // low is at least 1 here: NaN keys are 0
+            if (low == 0u) {                              // the unbounded band: every chunk is taken
+                for (int j = threadIdx.x; j < n; j += kSelThreads) keys[j] = kSure;
+                cut = kTie;
+            }
+        } else if (E == 0.f) {                            // every score in the band is the same
+            for (int j = threadIdx.x; j < n; j += kSelThreads)
+                if (keys[j] >= low && keys[j] <= high) keys[j] = kTie;
+            ties = open;
+            cut = high;
+        } else if (c.y <= (uint32_t)kFewTies) {
+            if (threadIdx.x == 0) sh.n_list = 0u;
+            __syncthreads();
+            for (int j = threadIdx.x; j < n; j += kSelThreads)
+                if (keys[j] >= low && keys[j] <= high) sh.list[atomicAdd(&sh.n_list, 1u)] = (uint32_t)j;
+            __syncthreads();
+            for (uint32_t x = warp; x < c.y; x += kSelWarps) {
+                const int s = slots[sh.list[x]];
+                const double v = exact_score<D>(p, q, bounds_of(s >= 0 && s < p.capacity ? s : 0), lane);
+                if (lane == 0) sh.key64[x] = order_key(v);
+            }
+            __syncthreads();
+            for (uint32_t x = threadIdx.x; x < c.y; x += kSelThreads) {
+                uint32_t before = 0;
+                for (uint32_t y = 0; y < c.y; ++y)
+                    before += sh.key64[y] > sh.key64[x] || (sh.key64[y] == sh.key64[x] && sh.list[y] < sh.list[x]);
+                keys[sh.list[x]] = before < open ? kSure : 0u;
+            }
+        } else {
+            // Many near-equal scores (contexts of equal chunks): a radix
+            // selection over the 64-bit keys, computed anew for each digit.
+            unsigned long long pre = 0;
+            uint32_t rest = open;
+            auto exact_key = [&](int j) {
+                const int s = slots[j];
+                return order_key(exact_score<D>(p, q, bounds_of(s >= 0 && s < p.capacity ? s : 0), lane));
+            };
+            for (int shift = 56; shift >= 0; shift -= 8) {
+                __syncthreads();
+                for (int j = threadIdx.x; j < 256; j += kSelThreads) sh.hist[j] = 0u;
+                __syncthreads();
+                for (int j = warp; j < n; j += kSelWarps) {
+                    if (keys[j] < low || keys[j] > high) continue;
+                    const unsigned long long k = exact_key(j);
+                    if (lane == 0 && (shift == 56 || (k >> (shift + 8)) == pre))
+                        atomicAdd(&sh.hist[(k >> shift) & 255u], 1u);
+                }
+                pick_digit(sh, rest);
+                pre = (pre << 8) | sh.pick_bin;
+                rest = sh.pick_left;
+            }
+            for (int j = warp; j < n; j += kSelWarps) {
+                const uint32_t k32 = keys[j];
+                __syncwarp();
+                if (k32 < low || k32 > high) continue;
+                const unsigned long long k = exact_key(j);
+                if (lane == 0) keys[j] = k > pre ? kSure : k == pre ? kTie : 0u;
+            }
+            ties = rest;
+        }
+    }
+    __syncthreads();
+
+    // The taken chunks in ascending order: a thread counts its stretch, a scan
+    // over the threads gives its first place, and it writes them.
+    const int per = (n + kSelThreads - 1) / kSelThreads, j0 = min(n, (int)threadIdx.x * per), j1 = min(n, j0 + per);
+    uint32_t took = 0, tied = 0;
+    for (int j = j0; j < j1; ++j) {
+        const uint32_t k = keys[j];
+        tied += k == kTie;
+        took += k > cut && k != kTie;
+    }
+    uint32_t a = took, b = tied;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t x = __shfl_up_sync(kFull, a, d), y = __shfl_up_sync(kFull, b, d);
+        if (lane >= d) { a += x; b += y; }
+    }
+    if (lane == 31) { sh.red[warp][0] = a; sh.red[warp][1] = b; }
+    __syncthreads();
+    a -= took;
+    b -= tied;
+    for (int w = 0; w < warp; ++w) { a += sh.red[w][0]; b += sh.red[w][1]; }
+    for (int j = j0; j < j1; ++j) {
+        const uint32_t k = keys[j];
+        const bool tie = k == kTie, take = tie ? b < ties : k > cut;
+        const uint32_t at = a + min(b, ties);
+        if (take && at < (uint32_t)K) out[at] = j;
+        a += take && !tie;
+        b += tie;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Tiles of the three pool types as tensor core fragments, the products taken
+// transposed (tokens on the rows, up to 8 NB query rows on the columns).
+// `tok(g)`: the token of the block in fragment row g (g + 8: 8 further).
+// `qdim(kk, t)`: first of a lane's dims of step kk, held in two registers
+// (kPair: four consecutive dims, else two and the two 8 further).
+// ---------------------------------------------------------------------------
+template <int EB, int C, int D, int NB>
+struct Frag;
+
+template <int C, int D, int NB>
+struct Frag<2, C, D, NB> {                       // fp16: ldmatrix from the swizzled tiles
+    static constexpr int kStage = 4 * C * D;
+    static constexpr bool kPair = false;
+    __device__ static int tok(int g) { return g; }
+    __device__ static int dim(int db, int half, int g) { return 16 * db + 8 * half + g; }
+    __device__ static void scores(const uint8_t* st, int blk, const uint32_t (&qb)[NB][D / 16][2], float (&s)[NB][4],
+                                  int lane) {
+        const uint32_t kt = smem_u32(st);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            uint32_t a[4];
+            ldsm_x4(kt + swz(blk * 16 + (lane & 15), 2 * kk + (lane >> 4), C), a[0], a[1], a[2], a[3]);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma16816(s[nb], a, qb[nb][kk][0], qb[nb][kk][1]);
+        }
+    }
+    __device__ static void pv(const uint8_t* st, int blk, const uint32_t (&pb)[NB][2], float (&o)[NB][D / 16][4],
+                              int lane) {
+        const uint32_t vt = smem_u32(st) + 2 * C * D;
+#pragma unroll
+        for (int db = 0; db < D / 16; ++db) {
+            uint32_t a[4];
+            ldsm_x4_t(vt + swz(blk * 16 + (lane & 7) + ((lane >> 4) << 3), 2 * db + ((lane >> 3) & 1), C), a[0], a[1],
+                      a[2], a[3]);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma16816(o[nb][db], a, pb[nb][0], pb[nb][1]);
+        }
+    }
+};
+
+template <int C, int D, int NB>
+struct Frag<1, C, D, NB> {                       // fp8: bytes widened into the fragments
+    static_assert(D == 128, "fp8 pools have head_dim 128");
+    static constexpr int kStage = 2 * C * D;
+    static constexpr bool kPair = true;
+    __device__ static int tok(int g) { return f4_token(g); }
+    // O^T rows: dims 32 qd + 4g + 2e (row g) and one further (row g + 8), db = 2 qd + e
+    __device__ static int dim(int db, int half, int g) { return 32 * (db >> 1) + 4 * g + 2 * (db & 1) + half; }
+    __device__ static uint32_t word(const uint8_t* tile, int row, int chunk, int off) {
+        return *reinterpret_cast<const uint32_t*>(tile + swz(row, chunk, C) + off);
+    }
+    __device__ static void scores(const uint8_t* st, int blk, const uint32_t (&qb)[NB][D / 16][2], float (&s)[NB][4],
+                                  int lane) {
+        const int g = lane >> 2, t = lane & 3, r0 = blk * 16 + tok(g), r1 = r0 + 8;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t w0 = word(st, r0, kk, 4 * t), w1 = word(st, r1, kk, 4 * t);
+            const uint32_t a[4] = {f16x2_from_e4m3x2(w0 & 0xffffu), f16x2_from_e4m3x2(w1 & 0xffffu),
+                                   f16x2_from_e4m3x2(w0 >> 16), f16x2_from_e4m3x2(w1 >> 16)};
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma16816(s[nb], a, qb[nb][kk][0], qb[nb][kk][1]);
+        }
+    }
+    __device__ static void pv(const uint8_t* st, int blk, const uint32_t (&pb)[NB][2], float (&o)[NB][D / 16][4],
+                              int lane) {
+        const int g = lane >> 2, t = lane & 3, t0 = blk * 16 + t;
+        const uint8_t* vt = st + C * D;
+#pragma unroll
+        for (int qd = 0; qd < D / 32; ++qd) {
+            const int kc = 2 * qd + (g >> 2), off = 4 * (g & 3);
+            const uint32_t a = word(vt, t0, kc, off), b = word(vt, t0 + 4, kc, off);
+            const uint32_t c = word(vt, t0 + 8, kc, off), d = word(vt, t0 + 12, kc, off);
+            const uint32_t ab0 = __byte_perm(a, b, 0x5140), cd0 = __byte_perm(c, d, 0x5140);
+            const uint32_t ab1 = __byte_perm(a, b, 0x7362), cd1 = __byte_perm(c, d, 0x7362);
+            const uint32_t x[4] = {f16x2_from_e4m3x2(ab0 & 0xffffu), f16x2_from_e4m3x2(ab0 >> 16),
+                                   f16x2_from_e4m3x2(cd0 & 0xffffu), f16x2_from_e4m3x2(cd0 >> 16)};
+            const uint32_t y[4] = {f16x2_from_e4m3x2(ab1 & 0xffffu), f16x2_from_e4m3x2(ab1 >> 16),
+                                   f16x2_from_e4m3x2(cd1 & 0xffffu), f16x2_from_e4m3x2(cd1 >> 16)};
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                mma16816(o[nb][2 * qd], x, pb[nb][0], pb[nb][1]);
+                mma16816(o[nb][2 * qd + 1], y, pb[nb][0], pb[nb][1]);
+            }
+        }
+    }
+};
+
+template <int C, int D, int NB>
+struct Frag<0, C, D, NB> {                       // fp4
+    static constexpr int kStage = F4Tile<C, D>::kBytes;
+    static constexpr bool kPair = true;
+    __device__ static int tok(int g) { return f4_token(g); }
+    __device__ static int dim(int db, int half, int g) { return 16 * db + 2 * g + half; }
+    __device__ static void scores(const uint8_t* st, int blk, const uint32_t (&qb)[NB][D / 16][2], float (&s)[NB][4],
+                                  int lane) {
+        f4_scores<C, D, NB, false>(st, blk, qb, s, lane);
+    }
+    __device__ static void pv(const uint8_t* st, int blk, const uint32_t (&pb)[NB][2], float (&o)[NB][D / 16][4],
+                              int lane) {
+        f4_pv<C, D, NB>(st, blk, pb, o, lane);
+    }
+};
+
+// ---------------------------------------------------------------------------
+// Attention over listed chunks.  A cluster takes one (sequence, key/value
+// head, up to 8 NB rows of its group); its CTAs take the list's entries in
+// turn.  In a CTA a producer warp looks 32 entries up at once (list -> slot ->
+// token count) and keeps a ring of tiles in flight; four consumer warps take
+// the tiles' blocks of 16 tokens with an online softmax.  At the end the
+// warps' states meet in shared memory, the CTAs' in the cluster's, and every
+// CTA writes its share of the output.
+// ---------------------------------------------------------------------------
+constexpr int kSpWarps = 4, kSpThreads = 32 * (kSpWarps + 1), kSpStages = 8;
+// The softmax reference is kept 5 below a running maximum and raised only when
+// a score passes it by 13: the weights stay below 2^13 in their fp16 operand
+// and normal numbers down to 2^-19 (or less) of the largest.
+constexpr float kSpLift = 5.f, kSpSlack = 8.f;
+
+template <int EB, int C, int D, int NB>
+struct SpShared {
+    using F = Frag<EB, C, D, NB>;
+    static constexpr int kRows = 8 * NB;
+    static constexpr int kMerge = kSpWarps * kRows * D * 4;       // the warps' outputs, in the ring's place
+    static size_t ring(int stages) {
+        const size_t r = (size_t)stages * F::kStage;
+        return r > (size_t)kMerge ? r : (size_t)kMerge;
+    }
+    // stage bars, token counts, (m, s) of the warps and of the CTA
+    static constexpr int kTail = 2 * kSpStages * 8 + kSpStages * 4 + (kSpWarps + 1) * kRows * 2 * 4;
+    static size_t bytes(int stages) { return ring(stages) + kTail; }
+};
+
+__device__ __forceinline__ void sp_consumers() { asm volatile("bar.sync 1, %0;" ::"n"(kSpWarps * 32) : "memory"); }
+
+template <int EB, int C, int D, int NB>
+__global__ void __launch_bounds__(kSpThreads, 2)
+sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListParams p, uint32_t ring_bytes) {
+    using F = Frag<EB, C, D, NB>;
+    using SM = SpShared<EB, C, D, NB>;
+    constexpr int R = SM::kRows, NBLK = C / 16;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + ring_bytes);
+    volatile int32_t* stage_ntok = reinterpret_cast<volatile int32_t*>(bars + 2 * kSpStages);
+    float* wms = const_cast<float*>(reinterpret_cast<volatile float*>(stage_ntok + kSpStages));   // [warp][row][m, s]
+    float* cms = wms + kSpWarps * R * 2;                                                           // [row][m, s]
+    const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + kSpStages);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int S = p.n_stages, cs = p.splits;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if ((smem_u32(smem) & 1023u) != 0 || S < 1 || S > kSpStages) {   // the same in every CTA
+        if (threadIdx.x == 0) set_status(p.status, CA_ERR_INVALID);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < S; ++k) {
+            mbar_init(full0 + 8 * k, 1);
+            mbar_init(empty0 + 8 * k, kSpWarps);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    __syncthreads();
+    const int rank = blockIdx.x % cs, unit = blockIdx.x / cs;
+    const int G = p.group, RB = (G + R - 1) / R;
+    const int rb = unit % RB, h = (unit / RB) % p.n_kv_heads, i = unit / (RB * p.n_kv_heads);
+    const int rows = min(R, G - rb * R);
+    const int row0 = h * G + rb * R;                       // the CTA's first query head
+
+    if (warp == kSpWarps) {
+        // ------------------------------ producer ------------------------------
+        const int off = p.list_off[i], n = p.list_off[i + 1] - off;
+        const int32_t* list = p.lists + ((size_t)i * p.n_kv_heads + h) * p.top_k;
+        const uint64_t pol = policy_evict_first();
+        int it = 0;
+        bool ok = true;
+        const int mine = (p.top_k - rank + cs - 1) / cs;   // entries rank, rank + cs, ...
+        for (int base = 0; base < mine && ok; base += 32) {
+            int slot = -1, ntok = 0;
+            if (base + lane < mine) {
+                const int j = list[rank + (size_t)(base + lane) * cs];
+                if (j >= n) {
+                    set_status(p.status, CA_ERR_DEVICE_BOUNDS);
+                } else if (j >= 0) {
+                    slot = p.list_slots[off + j];
+                    if (slot < 0 || slot >= p.capacity) {
+                        set_status(p.status, CA_ERR_DEVICE_BOUNDS);
+                        slot = -1;
+                    } else {
+                        ntok = min(max(p.slot_ntok[slot], 0), C);
+                    }
+                }
+            }
+            uint32_t todo = __ballot_sync(kFull, ntok > 0);
+            while (todo && ok) {
+                const int src = __ffs(todo) - 1;
+                todo &= todo - 1;
+                const int sl = __shfl_sync(kFull, slot, src), nt = __shfl_sync(kFull, ntok, src);
+                const int st = it % S;
+                if (lane == 0) {
+                    if (!mbar_wait(empty0 + 8 * st, ((uint32_t)(it / S) & 1u) ^ 1u)) {
+                        set_status(p.status, CA_ERR_TIMEOUT);
+                        ok = false;
+                    } else {
+                        const uint32_t fb = full0 + 8 * st, dst = smem_u32(smem) + st * F::kStage;
+                        mbar_expect_tx_only(fb, F::kStage);
+                        if constexpr (EB == 0) {
+                            bulk_load(dst, p.kv + (((long long)sl * p.n_layers + p.layer) * p.n_kv_heads + h) * F::kStage,
+                                      F::kStage, fb, pol);
+                        } else {
+                            const int rowK = (((sl * p.n_layers + p.layer) * 2) * p.n_kv_heads + h) * C;
+                            const int rowV = rowK + p.n_kv_heads * C;
+#pragma unroll
+                            for (int bx = 0; bx < D * EB / 128; ++bx) {
+                                tma_load_2d(dst + bx * C * 128, &tmap, bx * (128 / EB), rowK, fb, pol);
+                                tma_load_2d(dst + F::kStage / 2 + bx * C * 128, &tmap, bx * (128 / EB), rowV, fb, pol);
+                            }
+                        }
+                        stage_ntok[st] = nt;
+                        mbar_arrive(fb);
+                    }
+                }
+                ok = __shfl_sync(kFull, (int)ok, 0) != 0;
+                it += ok;
+            }
+        }
+        if (lane == 0) {
+            const int st = it % S;
+            if (ok && mbar_wait(empty0 + 8 * st, ((uint32_t)(it / S) & 1u) ^ 1u)) {
+                stage_ntok[st] = -1;                       // no more tiles
+                mbar_arrive(full0 + 8 * st);
+            } else {
+                set_status(p.status, CA_ERR_TIMEOUT);
+                // give the copies already issued a bounded chance to land
+                for (int k = (it > S ? it - S : 0); k < it; ++k)
+                    mbar_wait(full0 + 8 * (k % S), (uint32_t)(k / S) & 1u);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------ consumers ------------------------------
+        uint32_t qb[NB][D / 16][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            const bool there = nb * 8 + g < rows;
+            const uint16_t* q = p.q + ((size_t)i * p.n_heads + row0 + (there ? nb * 8 + g : 0)) * D;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                uint2 x;
+                if constexpr (F::kPair) {
+                    x = *reinterpret_cast<const uint2*>(q + 16 * kk + 4 * t);
+                } else {
+                    x.x = *reinterpret_cast<const uint32_t*>(q + 16 * kk + 2 * t);
+                    x.y = *reinterpret_cast<const uint32_t*>(q + 16 * kk + 2 * t + 8);
+                }
+                qb[nb][kk][0] = there ? x.x : 0u;
+                qb[nb][kk][1] = there ? x.y : 0u;
+            }
+        }
+        float o[NB][D / 16][4], m[NB][2], s[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            m[nb][0] = m[nb][1] = -INFINITY;
+            s[nb][0] = s[nb][1] = 0.f;
+#pragma unroll
+            for (int db = 0; db < D / 16; ++db) o[nb][db][0] = o[nb][db][1] = o[nb][db][2] = o[nb][db][3] = 0.f;
+        }
+        for (int it = 0;; ++it) {
+            const int st = it % S;
+            if (!mbar_wait(full0 + 8 * st, (uint32_t)(it / S) & 1u)) {
+                if (lane == 0) set_status(p.status, CA_ERR_TIMEOUT);
+                break;
+            }
+            const int ntok = stage_ntok[st];
+            if (ntok < 0) break;
+            // a tile's blocks of 16 tokens go to the warps in turn, tile after tile
+            const int blk = NBLK == 4 ? warp : (warp - it * NBLK) & 3;
+            if (blk < NBLK && blk * 16 < ntok) {
+                const uint8_t* tile = smem + (size_t)st * F::kStage;
+                float x[NB][4];
+                F::scores(tile, blk, qb, x, lane);
+                const int tk = blk * 16 + F::tok(g);
+                const bool in0 = tk < ntok, in1 = tk + 8 < ntok;
+                bool grow = false;
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[nb][e] = ((e >> 1) ? in1 : in0) ? x[nb][e] * p.scale_log2 : -INFINITY;
+                        grow = grow || x[nb][e] > m[nb][e & 1] + (kSpLift + kSpSlack);
+                    }
+                }
+                if (__any_sync(kFull, grow)) {
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            float mx = fmaxf(x[nb][r], x[nb][r + 2]);
+#pragma unroll
+                            for (int d = 4; d <= 16; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, d));
+                            const float mn = fmaxf(m[nb][r], mx - kSpLift);
+                            const float al = mn == -INFINITY ? 1.f : ex2(m[nb][r] - mn);
+                            m[nb][r] = mn;
+                            s[nb][r] *= al;
+#pragma unroll
+                            for (int db = 0; db < D / 16; ++db) {
+                                o[nb][db][r] *= al;
+                                o[nb][db][r + 2] *= al;
+                            }
+                        }
+                }
+                uint32_t pb[NB][2];
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    const float u0 = m[nb][0] == -INFINITY ? 0.f : m[nb][0], u1 = m[nb][1] == -INFINITY ? 0.f : m[nb][1];
+                    const float p0 = ex2(x[nb][0] - u0), p1 = ex2(x[nb][1] - u1);
+                    const float p2 = ex2(x[nb][2] - u0), p3 = ex2(x[nb][3] - u1);
+                    s[nb][0] += p0 + p2;                   // the lane's tokens; summed over g at the end
+                    s[nb][1] += p1 + p3;
+                    pb[nb][0] = movm_trans(pack_half2(p0, p1));
+                    pb[nb][1] = movm_trans(pack_half2(p2, p3));
+                }
+                F::pv(tile, blk, pb, o, lane);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty0 + 8 * st);
+        }
+        // Every copy has landed and every warp is past its last tile: the ring
+        // takes the warps' outputs, [warp][row][D].
+        sp_consumers();
+        float* ob = reinterpret_cast<float*>(smem);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+#pragma unroll
+                for (int d = 4; d <= 16; d <<= 1) s[nb][r] += __shfl_xor_sync(kFull, s[nb][r], d);
+                const int row = nb * 8 + 2 * t + r;
+                if (g == 0) {
+                    wms[(warp * R + row) * 2] = m[nb][r];
+                    wms[(warp * R + row) * 2 + 1] = s[nb][r];
+                }
+#pragma unroll
+                for (int db = 0; db < D / 16; ++db)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        ob[(warp * R + row) * D + F::dim(db, e, g)] = o[nb][db][r + 2 * e];
+            }
+        sp_consumers();
+        for (int idx = threadIdx.x; idx < rows * (D / 4); idx += kSpWarps * 32) {
+            const int row = idx / (D / 4), d4 = idx % (D / 4);
+            float M = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kSpWarps; ++w) M = fmaxf(M, wms[(w * R + row) * 2]);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kSpWarps; ++w) {
+                const float mw = wms[(w * R + row) * 2];
+                const float wt = mw == -INFINITY ? 0.f : ex2(mw - M);
+                sum += wt * wms[(w * R + row) * 2 + 1];
+                const float4 v = reinterpret_cast<const float4*>(ob + (size_t)(w * R + row) * D)[d4];
+                acc.x += wt * v.x; acc.y += wt * v.y; acc.z += wt * v.z; acc.w += wt * v.w;
+            }
+            if (cs == 1) {
+                const float inv = sum > 0.f ? p.out_scale / sum : 0.f;
+                *reinterpret_cast<uint2*>(p.out + ((size_t)i * p.n_heads + row0 + row) * D + d4 * 4) =
+                    make_uint2(pack_half2(acc.x * inv, acc.y * inv), pack_half2(acc.z * inv, acc.w * inv));
+            } else {
+                reinterpret_cast<float4*>(ob + (size_t)row * D)[d4] = acc;   // this thread's own place of warp 0's
+                if (d4 == 0) {
+                    cms[row * 2] = M;
+                    cms[row * 2 + 1] = sum;
+                }
+            }
+        }
+    }
+    if (cs == 1) return;
+    cluster_sync_all();
+    if (warp < kSpWarps) {
+        const uint32_t ob = smem_u32(smem), ms = smem_u32(cms);
+        for (int idx = rank * kSpWarps * 32 + threadIdx.x; idx < rows * (D / 4); idx += cs * kSpWarps * 32) {
+            const int row = idx / (D / 4), d4 = idx % (D / 4);
+            float M = -INFINITY, sum = 0.f;
+            for (int c = 0; c < cs; ++c) M = fmaxf(M, ld_peer(peer_addr(ms + row * 8, c)));
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int c = 0; c < cs; ++c) {
+                const uint32_t a = peer_addr(ms + row * 8, c);
+                const float mc = ld_peer(a), sc = ld_peer(a + 4);
+                const float wt = mc == -INFINITY ? 0.f : ex2(mc - M);
+                const float4 v = ld_peer4(peer_addr(ob + (uint32_t)(row * D + d4 * 4) * 4u, c));
+                sum += wt * sc;
+                acc.x += wt * v.x; acc.y += wt * v.y; acc.z += wt * v.z; acc.w += wt * v.w;
+            }
+            const float inv = sum > 0.f ? p.out_scale / sum : 0.f;
+            *reinterpret_cast<uint2*>(p.out + ((size_t)i * p.n_heads + row0 + row) * D + d4 * 4) =
+                make_uint2(pack_half2(acc.x * inv, acc.y * inv), pack_half2(acc.z * inv, acc.w * inv));
+        }
+    }
+    cluster_sync_all();                                    // the others may still read this CTA's share
+}
+
+}  // namespace dev
+
+namespace {
+
+constexpr int32_t kMostChunks = 49152;    // keys of one context in a CTA's shared memory (192 KB)
+
+dev::ListParams list_params(const Pool& p, const Sched& s, int32_t layer, const void* q, int32_t top_k) {
+    unsigned char* dev = static_cast<unsigned char*>(s.dev);
+    const PoolCfg& c = p.cfg;
+    dev::ListParams a{};
+    a.q = static_cast<const uint16_t*>(q);
+    a.list_off = reinterpret_cast<const int32_t*>(dev + s.layout.list_off);
+    a.list_slots = reinterpret_cast<const int32_t*>(dev + s.layout.list_slots);
+    a.kv = static_cast<const uint8_t*>(p.kv);
+    a.slot_ntok = reinterpret_cast<const int32_t*>(a.kv + pool_tile_bytes(c));
+    a.bounds = reinterpret_cast<const uint16_t*>(a.kv + pool_bounds_offset(c));
+    a.status = reinterpret_cast<int32_t*>(dev + s.layout.status);
+    a.n_layers = c.n_layers;
+    a.n_kv_heads = kv_heads(c);
+    a.n_heads = c.n_heads;
+    a.group = c.n_heads / a.n_kv_heads;
+    a.layer = layer;
+    a.capacity = c.capacity_slots;
+    a.top_k = top_k;
+    return a;
+}
+
+// One launch of `blocks` clusters of `cs` CTAs, a programmatic dependent of
+// the work before it (the kernels wait for that before anything else).
+int launch(const void* fn, unsigned blocks, int cs, int threads, size_t smem, void** args, cudaStream_t stream) {
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return CA_ERR_CUDA;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cs;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks * (unsigned)cs);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelExC(&cfg, fn, args) != cudaSuccess) return CA_ERR_CUDA;
+    count_launch();
+    return CA_OK;
+}
+
+using SparseFn = void (*)(const CUtensorMap, const dev::ListParams, uint32_t);
+struct SparseKernel {
+    SparseFn fn = nullptr;
+    int rows = 0, stage = 0, tail = 0, merge = 0;
+};
+template <int EB, int C, int D, int NB>
+SparseKernel sparse_of() {
+    using SM = dev::SpShared<EB, C, D, NB>;
+    return {dev::sparse_attention_kernel<EB, C, D, NB>, SM::kRows, SM::F::kStage, SM::kTail, SM::kMerge};
+}
+// Rows of a group per CTA: 8, or 16 for groups of more (at head_dim 256 the
+// accumulators of 16 rows do not fit the registers).
+template <int EB, int C, int D>
+SparseKernel pick_rows(int group) {
+    if constexpr (D <= 128) {
+        if (group > 8) return sparse_of<EB, C, D, 2>();
+    }
+    return sparse_of<EB, C, D, 1>();
+}
+template <int EB, int D>
+SparseKernel pick_sparse(const PoolCfg& c) {
+    const int G = c.n_heads / kv_heads(c);
+    if (c.chunk == 16) return pick_rows<EB, 16, D>(G);
+    if (c.chunk == 32) return pick_rows<EB, 32, D>(G);
+    if constexpr (D <= 128) {
+        if (c.chunk == 64) return pick_rows<EB, 64, D>(G);
+    }
+    return {};
+}
+SparseKernel pick_sparse(const PoolCfg& c) {
+    switch (kv_elem_bytes(c)) {
+        case 0: return c.head_dim == 64 ? pick_sparse<0, 64>(c) : pick_sparse<0, 128>(c);
+        case 1: return pick_sparse<1, 128>(c);
+        default:
+            return c.head_dim == 64 ? pick_sparse<2, 64>(c) : c.head_dim == 128 ? pick_sparse<2, 128>(c)
+                                                                               : pick_sparse<2, 256>(c);
+    }
+}
+
+int device_sms(const Pool& p) {
+    int n = 0;
+    return cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, p.device) == cudaSuccess ? n : 0;
+}
+
+}  // namespace
+
+int launch_select(const Pool& p, const Sched& s, int32_t layer, const void* q, int32_t top_k, int32_t sink,
+                  int32_t recent, int32_t* lists, void* stream) {
+    if (s.t.list_max > kMostChunks) return CA_ERR_UNSUPPORTED;
+    dev::ListParams a = list_params(p, s, layer, q, top_k);
+    a.lists = lists;
+    a.sink = sink;
+    a.recent = recent;
+    const int pairs = s.t.b * a.n_kv_heads, sms = device_sms(p);
+    // More CTAs per pair while the card is not full and each warp still has a block of 16 chunks.
+    int cs = 1;
+    while (cs < 8 && pairs * cs < 2 * sms && cs * dev::kSelWarps * 16 < s.t.list_max) cs *= 2;
+    a.splits = cs;
+    const size_t smem = (size_t)s.t.list_max * 4;
+    const void* fn = p.cfg.head_dim == 64    ? reinterpret_cast<const void*>(&dev::select_chunks_kernel<64>)
+                     : p.cfg.head_dim == 128 ? reinterpret_cast<const void*>(&dev::select_chunks_kernel<128>)
+                                             : reinterpret_cast<const void*>(&dev::select_chunks_kernel<256>);
+    void* args[] = {&a};
+    return launch(fn, (unsigned)pairs, cs, dev::kSelThreads, smem, args, static_cast<cudaStream_t>(stream));
+}
+
+int launch_sparse(const Pool& p, const Sched& s, int32_t layer, const void* q, const int32_t* lists, int32_t top_k,
+                  void* out, float scale, void* stream) {
+    const SparseKernel k = pick_sparse(p.cfg);
+    if (!k.fn) return CA_ERR_UNSUPPORTED;
+    dev::ListParams a = list_params(p, s, layer, q, top_k);
+    a.lists = const_cast<int32_t*>(lists);
+    a.out = static_cast<uint16_t*>(out);
+    const bool quant = (p.cfg.flags & (CA_KV_FP8 | CA_KV_FP4)) != 0;
+    a.scale_log2 = scale * 1.4426950408889634f * (quant ? kv_scale_of(p.cfg.k_scale) : 1.f);
+    a.out_scale = quant ? kv_scale_of(p.cfg.v_scale) : 1.f;
+    const int units = s.t.b * a.n_kv_heads * ((a.group + k.rows - 1) / k.rows), sms = device_sms(p);
+    const int most = std::min(top_k, s.t.list_max);        // entries that hold a chunk
+    int cs = 1;
+    while (cs < 8 && units * cs < 2 * sms && cs * 2 <= most) cs *= 2;
+    a.splits = cs;
+    // ring: what two CTAs per SM leave room for (113 KiB each)
+    int st = dev::kSpStages;
+    while (st > 2 && (size_t)st * k.stage + k.tail > 113 * 1024) --st;
+    a.n_stages = st;
+    uint32_t ring = (uint32_t)std::max(st * k.stage, k.merge);
+    const size_t smem = ring + (size_t)k.tail;
+    void* args[] = {const_cast<unsigned char*>(p.tmap), &a, &ring};
+    return launch(reinterpret_cast<const void*>(k.fn), (unsigned)units, cs, dev::kSpThreads, smem, args,
+                  static_cast<cudaStream_t>(stream));
+}
+
+}  // namespace ca
