@@ -270,8 +270,10 @@ int ca_pool_stats(const ca_pool* pool, ca_stats* out);
 int ca_seq_slots(const ca_pool* pool, int64_t seq_id, int32_t* slots, int32_t cap,
                  int32_t* n_out);
 
-/* Context tokens of seq_id (CA_ERR_NOT_FOUND if it is not in the pool). */
-int ca_seq_length(const ca_pool* pool, int64_t seq_id, int32_t* n_out);
+/* Context tokens of each sequence into lengths_out[n_seqs] (CA_ERR_NOT_FOUND
+ * if one is not in the pool). */
+int ca_seq_lengths(const ca_pool* pool, int32_t n_seqs, const int64_t* seq_ids,
+                   int32_t* lengths_out);
 
 /* ---- schedule -------------------------------------------------------------
  * The per-step context of the two-phase kernel [CA §3.2, §3.3] for the batch
@@ -450,10 +452,10 @@ int ca_decode_attention_static_ws(const ca_pool* pool, const ca_sched* sched,
  *     score(j) = max over the group's query rows of
  *                sum_d max(q_d * hi_jd, q_d * lo_jd)
  * where hi and lo are the chunk's key bounds: no token of the chunk has a
- * larger product with the row.  Chunks are ranked by their scores in 64 bits
+ * larger product with the row.  Chunks are ranked by their scores to 48 bits
  * (scores in 32 decide wherever their error bound allows it), ties to the
- * lower number; a score that is not a number ranks last.  Needs
- * CA_CHUNK_BOUNDS.  Contexts of at most 49152 chunks (CA_ERR_UNSUPPORTED).
+ * lower number.  A row whose sum is not a number is passed over, and a chunk
+ * with no other ranks last.  Needs CA_CHUNK_BOUNDS.  Contexts of at most 49152 chunks (CA_ERR_UNSUPPORTED).
  *
  * ca_sparse_attention: out[i][h][:] = sum_t softmax_t(scale * q[i][h] . k_t) v_t
  * over the tokens of the chunks in lists_dev[i][h / group] (-1 entries, and

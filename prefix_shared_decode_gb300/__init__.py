@@ -48,6 +48,15 @@ def _i32(a) -> np.ndarray:
     return np.ascontiguousarray(np.asarray(a, dtype=np.int32))
 
 
+def _i64(a) -> np.ndarray:
+    return np.ascontiguousarray(np.asarray(a, dtype=np.int64))
+
+
+def _at(a: np.ndarray) -> int:
+    """The address of an array's data."""
+    return a.__array_interface__["data"][0]
+
+
 class Pool:
     """A prefix-aware KV cache: the chunk trie and its device pool.
 
@@ -167,24 +176,21 @@ class Pool:
         for a host-only pool).  All or nothing.  Returns the shared tokens.
         ``token_lists`` is a list of token arrays, or (with ``lengths``) the
         already concatenated tokens."""
-        ids = np.ascontiguousarray(np.asarray(seq_ids, dtype=np.int64))
+        ids = _i64(seq_ids)
         if lengths is None:
             lens = np.ascontiguousarray(np.array([len(t) for t in token_lists], dtype=np.int32))
             tok = np.ascontiguousarray(np.concatenate([np.asarray(t, dtype=np.int32) for t in token_lists]))
         else:
-            lens = np.ascontiguousarray(np.asarray(lengths, dtype=np.int32))
-            tok = np.ascontiguousarray(np.asarray(token_lists, dtype=np.int32))
+            lens, tok = _i32(lengths), _i32(token_lists)
         kp = vp = None
         if k is not None:
             assert k.is_contiguous() and v.is_contiguous()
             assert tuple(k.shape) == (self.n_layers, int(lens.sum()), self.n_kv_heads, self.head_dim)
             kp, vp = k.data_ptr(), v.data_ptr()
         shared = np.zeros(len(ids), dtype=np.int32)
-        P32 = C.POINTER(C.c_int32)
-        check(capi.lib().ca_insert_batch(self._h, len(ids), ids.ctypes.data_as(C.POINTER(C.c_int64)),
-                                         tok.ctypes.data_as(P32), lens.ctypes.data_as(P32), kp, vp,
-                                         None if self.host_only else _stream_ptr(stream),
-                                         shared.ctypes.data_as(P32)), "ca_insert_batch")
+        check(capi.lib().ca_insert_batch(self._h, len(ids), _at(ids), _at(tok), _at(lens), kp, vp,
+                                         None if self.host_only else _stream_ptr(stream), _at(shared)),
+              "ca_insert_batch")
         return shared.tolist()
 
     def append(self, seq_id: int, tokens, k=None, v=None, stream=None) -> int:
@@ -212,19 +218,20 @@ class Pool:
         import torch
         if self.host_only:
             raise ValueError("a host-only pool holds no rows")
-        ids = np.ascontiguousarray(np.asarray(seq_ids, dtype=np.int64))
+        ids = _i64(seq_ids)
+        if ids.ndim != 1 or not len(ids):
+            raise ValueError("seq_ids must be a list of at least one sequence")
+        held = np.empty(len(ids), np.int32)
+        L = capi.lib()
+        check(L.ca_seq_lengths(self._h, len(ids), _at(ids), _at(held)), "ca_seq_lengths")
         first = None if starts is None else _i32(starts)
-        if lengths is None:
-            lens = np.array([self.seq_len(int(i)) for i in ids], dtype=np.int32)
-            if first is not None:
-                if first.shape != lens.shape:
-                    raise ValueError("starts and seq_ids differ in length")
-                lens = np.maximum(lens - first, 0).astype(np.int32)
-        else:
+        if lengths is not None:
             lens = _i32(lengths)
-        if ids.ndim != 1 or lens.shape != ids.shape or (first is not None and first.shape != ids.shape):
+        else:
+            lens = held if first is None else held - first
+        if lens.shape != ids.shape or (first is not None and first.shape != ids.shape):
             raise ValueError("seq_ids, starts and lengths differ in length")
-        if len(lens) and lens.min() < 0:
+        if lens.min() < 0:
             raise ValueError("lengths must not be negative")
         shape = (self.n_layers, int(lens.sum(dtype=np.int64)), self.n_kv_heads, self.head_dim)
         if out is None:
@@ -234,14 +241,9 @@ class Pool:
             k, v = out
             for x in (k, v):
                 self._check_tensor(x, shape, torch.float16, "out")
-        if shape[1] == 0:
-            for i in ids:
-                self.seq_len(int(i))                 # unknown sequences are refused all the same
-            return k, v
-        P32 = C.POINTER(C.c_int32)
-        check(capi.lib().ca_read_batch(self._h, len(ids), ids.ctypes.data_as(C.POINTER(C.c_int64)),
-                                       None if first is None else first.ctypes.data_as(P32), lens.ctypes.data_as(P32),
-                                       k.data_ptr(), v.data_ptr(), self._stream(stream)), "ca_read_batch")
+        if shape[1]:
+            check(L.ca_read_batch(self._h, len(ids), _at(ids), None if first is None else _at(first), _at(lens),
+                                  k.data_ptr(), v.data_ptr(), self._stream(stream)), "ca_read_batch")
         return k, v
 
     def read(self, seq_id: int, start: int = 0, stop: int | None = None, out=None, stream=None):
@@ -251,8 +253,8 @@ class Pool:
 
     def seq_len(self, seq_id: int) -> int:
         """Context tokens of a sequence."""
-        n = C.c_int32()
-        check(capi.lib().ca_seq_length(self._h, int(seq_id), C.byref(n)), "ca_seq_length")
+        i, n = C.c_int64(int(seq_id)), C.c_int32()
+        check(capi.lib().ca_seq_lengths(self._h, 1, C.addressof(i), C.addressof(n)), "ca_seq_lengths")
         return n.value
 
     def _check_tensor(self, x, shape, dtype, what: str) -> None:
@@ -266,6 +268,9 @@ class Pool:
         pool's device)."""
         import torch
         if stream is None:
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # no Stream object per call
+            if raw is not None:
+                return raw(self._kv.device.index) or None
             stream = torch.cuda.current_stream(self._kv.device)
         return int(getattr(stream, "cuda_stream", stream)) or None
 
@@ -273,9 +278,8 @@ class Pool:
         check(capi.lib().ca_remove_seq(self._h, int(seq_id)), "ca_remove_seq")
 
     def remove_batch(self, seq_ids) -> None:
-        ids = np.ascontiguousarray(np.asarray(seq_ids, dtype=np.int64))
-        check(capi.lib().ca_remove_batch(self._h, len(ids), ids.ctypes.data_as(C.POINTER(C.c_int64))),
-              "ca_remove_batch")
+        ids = _i64(seq_ids)
+        check(capi.lib().ca_remove_batch(self._h, len(ids), _at(ids)), "ca_remove_batch")
 
     def _generation(self) -> int:
         st = self.__dict__.setdefault("_stats_buf", capi.Stats())

@@ -29,7 +29,7 @@ CA_SCHED_CHUNK_LISTS = 4
 # Every symbol the header declares, in header order.
 EXPORTS = [
     "ca_pool_bytes", "ca_pool_bytes_ex", "ca_pool_create", "ca_pool_create_ex", "ca_pool_destroy", "ca_match_prefix", "ca_insert_tokens",
-    "ca_insert_batch", "ca_append_tokens", "ca_read_batch", "ca_remove_seq", "ca_remove_batch", "ca_pool_stats", "ca_seq_slots", "ca_seq_length", "ca_build_schedule", "ca_build_schedule_ex", "ca_sched_destroy",
+    "ca_insert_batch", "ca_append_tokens", "ca_read_batch", "ca_remove_seq", "ca_remove_batch", "ca_pool_stats", "ca_seq_slots", "ca_seq_lengths", "ca_build_schedule", "ca_build_schedule_ex", "ca_sched_destroy",
     "ca_sched_counts", "ca_export_tables", "ca_export_plan", "ca_workspace_bytes", "ca_decode_attention",
     "ca_workspace_bytes_host", "ca_decode_attention_host", "ca_decode_attention_static_ws",
     "ca_select_chunks", "ca_sparse_attention",
@@ -85,14 +85,14 @@ def lib() -> C.CDLL:
         "ca_pool_destroy": [vp],
         "ca_match_prefix": [vp, P(i32), i32, P(i32)],
         "ca_insert_tokens": [vp, i64, P(i32), i32, vp, vp, vp, P(i32)],
-        "ca_insert_batch": [vp, i32, P(i64), P(i32), P(i32), vp, vp, vp, P(i32)],
+        "ca_insert_batch": [vp, i32, vp, vp, vp, vp, vp, vp, vp],       # arrays by address
         "ca_append_tokens": [vp, i64, P(i32), i32, vp, vp, vp, P(i32)],
-        "ca_read_batch": [vp, i32, P(i64), P(i32), P(i32), vp, vp, vp],
+        "ca_read_batch": [vp, i32, vp, vp, vp, vp, vp, vp],             # arrays by address
         "ca_remove_seq": [vp, i64],
-        "ca_remove_batch": [vp, i32, P(i64)],
+        "ca_remove_batch": [vp, i32, vp],
         "ca_pool_stats": [vp, P(Stats)],
         "ca_seq_slots": [vp, i64, P(i32), i32, P(i32)],
-        "ca_seq_length": [vp, i64, P(i32)],
+        "ca_seq_lengths": [vp, i32, vp, vp],                            # arrays by address
         "ca_build_schedule": [vp, P(i64), i32, P(vp), vp],
         "ca_build_schedule_ex": [vp, vp, i32, i32, u32, P(vp), vp],     # seq_ids: int64 array address
         "ca_sched_destroy": [vp],

@@ -159,7 +159,11 @@ struct Pool {
     void* kv = nullptr;            // device pool (nullptr: host only)
     size_t kv_bytes = 0;
     int device = -1;
-    int num_sms = 0;
+    int num_sms = 0;               // CTAs of the attention grid (SMs x resident CTAs)
+    int sms = 0;                   // SMs of the device
+    // The kernels over chunk lists (selection, attention) whose shared-memory
+    // limit a call on this pool has raised.
+    mutable const void* list_fn[2] = {nullptr, nullptr};
     alignas(64) unsigned char tmap[128];  // CUtensorMap over the pool
     Node root;
     std::vector<Node> nodes;       // one per slot, reused; live iff refcount > 0

@@ -15,9 +15,12 @@ namespace ca {
 namespace dev {
 
 constexpr int kRowThreads = 256;
-// Chunk lists travel in the launch parameters (at most 32 KB): short lists
-// for decode-time appends, long ones for prompts.
-constexpr int kFewChunks = 16, kManyChunks = 1024;
+// Chunk lists travel in the launch parameters: short lists for decode-time
+// appends, longer ones for prompts.  Parameters above 4 KB cost the host some
+// 10 us a launch, so the longest list is taken only where several launches of
+// the next one would cost it as much and the card a tail each (1024 chunks of
+// 32 heads stored and read back: 459 us in one launch each, 518 in five).
+constexpr int kFewChunks = 16, kSomeChunks = 248, kManyChunks = 1024;
 
 template <int N>
 struct RowArgs {
@@ -29,6 +32,8 @@ struct RowArgs {
     float k_mul, v_mul;           // stores: 1 / scale; reads: scale
     ScatterChunk ch[N];
 };
+
+static_assert(sizeof(RowArgs<kSomeChunks>) <= 4096 && sizeof(RowArgs<kManyChunks>) <= 32764, "launch parameters");
 
 struct Where {
     ScatterChunk c;
@@ -336,9 +341,10 @@ int rows(const Pool& p, RowOp op, const void* k, const void* v, int32_t total_ro
     const size_t most = std::max<size_t>(1, std::min<size_t>(dev::kManyChunks, (size_t)INT32_MAX / per));
     for (size_t i = 0; i < chunks.size();) {
         const size_t n = std::min(most, chunks.size() - i);
-        const int st = n <= dev::kFewChunks
-                           ? run_rows<dev::kFewChunks>(p, op, k, v, total_rows, chunks.data() + i, n, s)
-                           : run_rows<dev::kManyChunks>(p, op, k, v, total_rows, chunks.data() + i, n, s);
+        const ScatterChunk* c = chunks.data() + i;
+        const int st = n <= dev::kFewChunks    ? run_rows<dev::kFewChunks>(p, op, k, v, total_rows, c, n, s)
+                       : n <= dev::kSomeChunks ? run_rows<dev::kSomeChunks>(p, op, k, v, total_rows, c, n, s)
+                                               : run_rows<dev::kManyChunks>(p, op, k, v, total_rows, c, n, s);
         if (st) return st;
         i += n;
     }

@@ -152,6 +152,7 @@ int ca_pool_create_ex(const ca_pool_config_ex* cfg_ex, void* kv_dev, size_t kv_b
             if (cudaGetDevice(&p->device) != cudaSuccess) return CA_ERR_CUDA;
             if (cudaDeviceGetAttribute(&p->num_sms, cudaDevAttrMultiProcessorCount, p->device) != cudaSuccess)
                 return CA_ERR_CUDA;
+            p->sms = p->num_sms;
             int ctas = 1;
             st = kernel_ctas_per_sm(*cfg, &ctas);
             if (st) return st;
@@ -276,6 +277,7 @@ int ca_read_batch(const ca_pool* pool, int32_t n_seqs, const int64_t* seq_ids, c
     return guard([&] {
         const int32_t c = pool->cfg.chunk;
         std::vector<ScatterChunk> rows;
+        rows.reserve((size_t)n_seqs * 4);
         int64_t total = 0;
         for (int32_t i = 0; i < n_seqs; ++i) {
             auto it = pool->seqs.find(seq_ids[i]);
@@ -341,11 +343,13 @@ int ca_seq_slots(const ca_pool* pool, int64_t seq_id, int32_t* slots, int32_t ca
     return CA_OK;
 }
 
-int ca_seq_length(const ca_pool* pool, int64_t seq_id, int32_t* n_out) {
-    if (!pool || !n_out) return CA_ERR_INVALID;
-    auto it = pool->seqs.find(seq_id);
-    if (it == pool->seqs.end()) return CA_ERR_NOT_FOUND;
-    *n_out = it->second.length;
+int ca_seq_lengths(const ca_pool* pool, int32_t n_seqs, const int64_t* seq_ids, int32_t* lengths_out) {
+    if (!pool || n_seqs < 0 || (n_seqs > 0 && (!seq_ids || !lengths_out))) return CA_ERR_INVALID;
+    for (int32_t i = 0; i < n_seqs; ++i) {
+        auto it = pool->seqs.find(seq_ids[i]);
+        if (it == pool->seqs.end()) return CA_ERR_NOT_FOUND;
+        lengths_out[i] = it->second.length;
+    }
     return CA_OK;
 }
 

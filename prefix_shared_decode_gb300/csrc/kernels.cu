@@ -578,11 +578,15 @@ __device__ __forceinline__ void f4_tile_to_f16(const uint8_t* src, uint8_t* kd, 
         lds_words<D / 32>(src + m * (D / 2) + t * (D / 8), w);
         lds_words<D / 64>(src + T::kKScales + m * (D / 16), sc);
 #pragma unroll
-        for (int kk = 0; kk < NK; ++kk) {
-            const uint32_t x = w[kk >> 1] >> (16 * (kk & 1));
-            const uint32_t s2 = f16x2_from_e4m3x2(((sc[kk >> 2] >> (8 * (kk & 3))) & 0xffu) * 0x101u);
-            const uint2 o = make_uint2(mul_f16x2(f16x2_from_e2m1x2(x), s2), mul_f16x2(f16x2_from_e2m1x2(x >> 8), s2));
-            *reinterpret_cast<uint2*>(kd + swz(tok, 2 * kk + (t >> 1), C) + 8 * (t & 1)) = o;
+        for (int kp = 0; kp < NK / 2; ++kp) {             // two steps: one word of codes, two scales
+            uint32_t x[4], h[2];
+            f16x2_from_e2m1x8(w[kp], x);
+            f16x2_from_e4m3x4(sc[kp >> 1], h);
+            const uint32_t sa = __byte_perm(h[kp & 1], 0u, 0x1010), sb = __byte_perm(h[kp & 1], 0u, 0x3232);
+            *reinterpret_cast<uint2*>(kd + swz(tok, 4 * kp + (t >> 1), C) + 8 * (t & 1)) =
+                make_uint2(mul_f16x2(x[0], sa), mul_f16x2(x[1], sa));
+            *reinterpret_cast<uint2*>(kd + swz(tok, 4 * kp + 2 + (t >> 1), C) + 8 * (t & 1)) =
+                make_uint2(mul_f16x2(x[2], sb), mul_f16x2(x[3], sb));
         }
     }
     for (int i = tid; i < C * 8; i += kConsumerWarps * 32) {
@@ -591,11 +595,25 @@ __device__ __forceinline__ void f4_tile_to_f16(const uint8_t* src, uint8_t* kd, 
         const int tok = (r & ~7) | ((r & 3) << 1) | ((r >> 2) & 1);
         uint32_t w[D / 64];
         lds_words<D / 64>(src + T::kVCodes + tok * (D / 2) + f4_v_unit<D>(tok, g) * (D / 16), w);
+        // the scale pairs of the token and its partner 4 on (or before)
+        uint32_t sc[D / 32];
+        lds_words<D / 32>(src + T::kVScales + (f4_v_scale<D>(tok, 0) & ~1), sc);
+        const uint32_t pick = (tok & 4) ? 0x3232u : 0x1010u;
 #pragma unroll
-        for (int db = 0; db < NK; ++db) {
-            const uint32_t s2 = f16x2_from_e4m3x2(src[T::kVScales + f4_v_scale<D>(tok, db)] * 0x101u);
-            *reinterpret_cast<uint32_t*>(vd + swz(tok, 2 * db + (g >> 2), C) + 4 * (g & 3)) =
-                mul_f16x2(f16x2_from_e2m1x2(w[db >> 2] >> (8 * (db & 3))), s2);
+        for (int i4 = 0; i4 < D / 64; ++i4) {
+            uint32_t x[4];
+            f16x2_from_e2m1x8(w[i4], x);
+#pragma unroll
+            for (int j2 = 0; j2 < 2; ++j2) {
+                uint32_t h[2];
+                f16x2_from_e4m3x4(sc[2 * i4 + j2], h);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int db = 4 * i4 + 2 * j2 + e;
+                    *reinterpret_cast<uint32_t*>(vd + swz(tok, 2 * db + (g >> 2), C) + 4 * (g & 3)) =
+                        mul_f16x2(x[2 * j2 + e], __byte_perm(h[e], 0u, pick));
+                }
+            }
         }
     }
 }
@@ -604,9 +622,13 @@ __device__ __forceinline__ void f4_tile_to_f16(const uint8_t* src, uint8_t* kd, 
 // block `blk` of a tile, on the tensor cores with the query replicated over
 // the 8 columns (as sf_chunk_f8_tc does; on CUDA cores the widening alone
 // would outweigh the tile's bytes).  Only columns 0 (c0, c2) are formed.
-// The weights are held times 2^10 in their fp16 operand (p <= 1024), so that
-// they stay normal numbers down to 2^-24 of the largest; m is lowered to match.
-constexpr float kF4Lift = 10.f;
+// The path is bound by issue slots, so a block costs no shuffle and no
+// rescaling as a rule: the reference m is a running maximum less kF4Lift,
+// raised only when some score passes it by kF4Lift + kF4Slack (a vote), and
+// s holds each lane's own tokens until the head ends.  The weights stay below
+// 2^13 in their fp16 operand and normal numbers down to 2^-19 (or less) of
+// the largest.
+constexpr float kF4Lift = 5.f, kF4Slack = 8.f;
 template <int C, int D>
 __device__ __forceinline__ void sf_chunk_f4_tc(const uint8_t* tile, int blk, int ntok,
                                                const uint32_t (&qb)[1][D / 16][2], float scale_log2, float& m,
@@ -618,22 +640,22 @@ __device__ __forceinline__ void sf_chunk_f4_tc(const uint8_t* tile, int blk, int
     const float x0 = (r0 < ntok) ? acc[0][0] * scale_log2 : -INFINITY;
     const float x1 = (r0 + 8 < ntok) ? acc[0][2] * scale_log2 : -INFINITY;
     float mx = fmaxf(x0, x1);
+    if (__any_sync(kFull, mx > m + (kF4Lift + kF4Slack))) {
 #pragma unroll
-    for (int off = 4; off <= 16; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
-    const float mnew = fmaxf(m, mx - kF4Lift);
-    const float mu = (mnew == -INFINITY) ? 0.f : mnew;
-    const float alpha = ex2(m - mu);
-    const float p0 = ex2(x0 - mu), p1 = ex2(x1 - mu);
-    float ps = p0 + p1;
+        for (int off = 4; off <= 16; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
+        const float mnew = fmaxf(m, mx - kF4Lift);
+        const float alpha = ex2(m - mnew);
+        m = mnew;
+        s *= alpha;
 #pragma unroll
-    for (int off = 4; off <= 16; off <<= 1) ps += __shfl_xor_sync(kFull, ps, off);
-    s = s * alpha + ps;
-    m = mnew;
-#pragma unroll
-    for (int db = 0; db < D / 16; ++db) {
-        oc[0][db][0] *= alpha;
-        oc[0][db][2] *= alpha;
+        for (int db = 0; db < D / 16; ++db) {
+            oc[0][db][0] *= alpha;
+            oc[0][db][2] *= alpha;
+        }
     }
+    const float mu = (m == -INFINITY) ? 0.f : m;
+    const float p0 = ex2(x0 - mu), p1 = ex2(x1 - mu);
+    s += p0 + p1;
     const uint32_t pb[1][2] = {{movm_trans(pack_half2(p0, p0)), movm_trans(pack_half2(p1, p1))}};
     f4_pv<C, D, 1>(tile, blk, pb, oc, lane);
 }
@@ -707,9 +729,10 @@ __device__ __forceinline__ bool sf_rows_transposed(
         float ot[D / 16][4], m[2] = {-INFINITY, -INFINITY}, s[2] = {0.f, 0.f};
 #pragma unroll
         for (int db = 0; db < D / 16; ++db) ot[db][0] = ot[db][1] = ot[db][2] = ot[db][3] = 0.f;
-        for (; L < seg_end; ++L, ++it) {
-            const int st = it % S;
-            if (!mbar_wait(full0 + 8 * st, (uint32_t)(it / S) & 1u)) {
+        int st = it % S;
+        uint32_t ph = (uint32_t)(it / S) & 1u;
+        for (; L < seg_end; ++L, ++it, st = st + 1 == S ? 0 : st + 1, ph ^= (uint32_t)(st == 0)) {
+            if (!mbar_wait(full0 + 8 * st, ph)) {
                 set_status(p.status, CA_ERR_TIMEOUT);
                 ok = false;
                 break;
@@ -765,10 +788,14 @@ __device__ __forceinline__ bool sf_rows_transposed(
                 mx[1] = fmaxf(x[1], x[3]);
                 bool grow = false;
                 float alpha[2] = {1.f, 1.f}, mu[2];
+                // fp4: one vote instead of the reductions, as in sf_chunk_f4_tc
+                if (EB != 0 || __any_sync(kFull, mx[0] > m[0] + (kF4Lift + kF4Slack) ||
+                                                     mx[1] > m[1] + (kF4Lift + kF4Slack)))
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
 #pragma unroll
                     for (int off = 4; off <= 16; off <<= 1) mx[r] = fmaxf(mx[r], __shfl_xor_sync(kFull, mx[r], off));
+                    if constexpr (EB == 0) mx[r] -= kF4Lift;
                     // the reference maximum is raised lazily, as in cf_softmax_pv
                     if (mx[r] > m[r] + 8.f) {
                         alpha[r] = ex2(m[r] - mx[r]);
@@ -776,8 +803,9 @@ __device__ __forceinline__ bool sf_rows_transposed(
                         s[r] *= alpha[r];
                         grow = true;
                     }
-                    mu[r] = (m[r] == -INFINITY) ? 0.f : m[r];
                 }
+                mu[0] = (m[0] == -INFINITY) ? 0.f : m[0];
+                mu[1] = (m[1] == -INFINITY) ? 0.f : m[1];
                 if (__any_sync(kFull, grow)) {
 #pragma unroll
                     for (int db = 0; db < D / 16; ++db) {
@@ -790,9 +818,10 @@ __device__ __forceinline__ bool sf_rows_transposed(
                 float ps[2] = {p0 + p2, p1 + p3};
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
+                    if constexpr (EB != 0)
 #pragma unroll
-                    for (int off = 4; off <= 16; off <<= 1) ps[r] += __shfl_xor_sync(kFull, ps[r], off);
-                    s[r] += ps[r];
+                        for (int off = 4; off <= 16; off <<= 1) ps[r] += __shfl_xor_sync(kFull, ps[r], off);
+                    s[r] += ps[r];               // fp4: the lane's own tokens
                 }
                 // P^T fragments: k = tokens, n = query rows
                 const uint32_t b0 = movm_trans(pack_half2(p0, p1));   // tokens 0..7
@@ -817,6 +846,12 @@ __device__ __forceinline__ bool sf_rows_transposed(
             }
         }
         if (!ok) break;
+        if constexpr (EB == 0)
+#pragma unroll
+            for (int off = 4; off <= 16; off <<= 1) {
+                s[0] += __shfl_xor_sync(kFull, s[0], off);
+                s[1] += __shfl_xor_sync(kFull, s[1], off);
+            }
         // Combine the Tr warps' states through the Q tile (free once every
         // warp has left the chunk loop: the barrier opening each round).
         float* xo = reinterpret_cast<float*>(qreg);
@@ -888,7 +923,7 @@ __device__ __forceinline__ bool sf_rows_transposed(
 // key/value head (head_dim <= 128): it has the transposed few-row path and
 // no single-row sequence-first path; the other variant the reverse.
 template <int C, int D, int EB, bool kRows>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, EB == 0 ? 3 : 2)
 two_phase_attention_kernel(const __grid_constant__ CUtensorMap tmap, const AttnParams p) {
     using SM = Smem<C, D, EB>;
     constexpr int DPL = D / 32;
@@ -1196,9 +1231,10 @@ two_phase_attention_kernel(const __grid_constant__ CUtensorMap tmap, const AttnP
 #pragma unroll
                     for (int db = 0; db < D / 16; ++db)
                         oc[0][db][0] = oc[0][db][1] = oc[0][db][2] = oc[0][db][3] = 0.f;
+                    int st = it % S;
+                    uint32_t ph = (uint32_t)(it / S) & 1u;
                     for (; L < seg_end; ++L, ++it) {
-                        const int st = it % S;
-                        if (!mbar_wait(full0 + 8 * st, (uint32_t)(it / S) & 1u)) {
+                        if (!mbar_wait(full0 + 8 * st, ph)) {
                             set_status(p.status, CA_ERR_TIMEOUT);
                             return;
                         }
@@ -1212,7 +1248,13 @@ two_phase_attention_kernel(const __grid_constant__ CUtensorMap tmap, const AttnP
                                                  oc, lane);
                         __syncwarp();
                         if (lane == 0) mbar_arrive(empty0 + 8 * st);
+                        if (++st == S) {
+                            st = 0;
+                            ph ^= 1u;
+                        }
                     }
+#pragma unroll
+                    for (int off = 4; off <= 16; off <<= 1) s += __shfl_xor_sync(kFull, s, off);
                     // lane (g, 0) holds dims 16db + 2g, + 1
                     if ((lane & 3) == 0) {
 #pragma unroll
@@ -1643,7 +1685,7 @@ size_t smem_for(const PoolCfg& c, int stages) {
 // Stages that fit two CTAs per SM (113 KiB each, at most 8).
 int kernel_smem_bytes(const PoolCfg& c, int* n_stages, size_t* bytes) {
     if (!pick_kernel(c)) return CA_ERR_UNSUPPORTED;
-    const size_t budget = 113 * 1024;
+    const size_t budget = (c.flags & CA_KV_FP4) ? 75 * 1024 : 113 * 1024;
     int st = dev::kMaxStages;
     while (st > 1 && smem_for(c, st) > budget) --st;
     *n_stages = st;

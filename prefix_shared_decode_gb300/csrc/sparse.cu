@@ -19,8 +19,13 @@ namespace dev {
 // shared memories, so neither call needs a workspace, a second kernel or an
 // atomic whose order could change a result.
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync_all() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
 __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
     uint32_t r;
@@ -74,15 +79,16 @@ struct ListParams {
 //
 // Exact order: a 32-bit score is off by at most E (below), so with T the
 // top_k-th largest of them, a chunk above T + 2E is among the exact top_k, one
-// below T - 2E is not.  Where more chunks lie in between than places are left,
-// those few are scored again in 64 bits and ranked by (score, lower number).
+// below T - 2E is not.  Where more chunks lie in between than places are left
+// (a handful as a rule), those are summed again to 48 bits and ranked by
+// (score, lower number).
 // ---------------------------------------------------------------------------
 constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
 constexpr uint32_t kSure = 0xffffffffu;   // key of a chunk that is taken
 constexpr uint32_t kTie = 0xfffffffeu;    // key of one that ties for the last places
 constexpr int kFewTies = 256;             // chunks ranked pairwise in 64 bits
 
-__device__ __forceinline__ uint32_t order_key(float x) {   // monotone; 0 for a NaN, never above kTie - 1
+__device__ __forceinline__ uint32_t order_key(float x) {   // monotone; 0 for a NaN, never as much as kTie
     if (x != x) return 0u;
     const uint32_t u = __float_as_uint(x + 0.f);           // -0 counts as 0
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
@@ -101,38 +107,53 @@ __device__ __forceinline__ uint32_t part_f16x2(uint32_t x, bool positive) {   //
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+constexpr int kBins = 2048, kPerBin = kBins / kSelThreads;
 struct SelShared {
-    uint32_t hist[256];
+    uint32_t hist[kBins];
     uint32_t top_abs[16];                 // largest |bound| of each CTA of the cluster (fp32 bits)
     uint32_t red[kSelWarps][2];
     float qsum[kSelWarps];
-    uint32_t pick_bin, pick_left;         // radix step: the digit, places left inside it
+    uint32_t bin, left, in_bin, T;        // histogram step: the digit, places left inside it, its count
     uint32_t n_list;
     uint32_t list[kFewTies];
     unsigned long long key64[kFewTies];
 };
 
-// The exact score of one chunk in 64 bits (a warp; every lane gets it).
+// s + e <- s + e + x, s the rounded sum and e what rounding lost.
+__device__ __forceinline__ void add_pair(float& s, float& e, float x, float y) {
+    const float t = __fadd_rn(s, x), z = __fsub_rn(t, s);
+    const float lost = __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(x, z));
+    s = t;
+    e = __fadd_rn(__fadd_rn(e, y), lost);
+}
+// One row's product with a chunk's bounds to 48 bits (a warp; every lane gets
+// it), as an ordered key.  Products of fp16 are exact in fp32 and their sums
+// are held as pairs of fp32: the card's fp64 pipe (2 FMAs a clock and SM) took
+// 8 us for five chunks of four rows where this takes 1.  The order of the sum
+// is fixed: equal bounds tie.
 template <int D>
-__device__ __forceinline__ double exact_score(const ListParams& p, const uint16_t* q, const uint16_t* bounds,
-                                              int lane) {
-    double best = 0.0;
-    bool nan = false;
-    for (int r = 0; r < p.group; ++r) {
-        double s = 0.0;
+__device__ __forceinline__ unsigned long long exact_row(const uint16_t* q, const uint16_t* bounds, int lane) {
+    float s = 0.f, e = 0.f;
 #pragma unroll
-        for (int d = lane; d < D; d += 32) {
-            const double x = (double)__half2float(__ushort_as_half(q[(size_t)r * D + d]));
-            const double hi = (double)__half2float(__ushort_as_half(bounds[d]));
-            const double lo = (double)__half2float(__ushort_as_half(bounds[D + d]));
-            s = fma(x, x > 0.0 ? hi : lo, s);
-        }
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(kFull, s, off);
-        nan = nan || s != s;
-        if (r == 0 || s > best) best = s;
+    for (int j = 0; j < D / 64; ++j) {
+        const int d = 64 * j + 2 * lane;
+        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(q + d));
+        const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(bounds + d));
+        const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(bounds + D + d));
+        add_pair(s, e, __fmul_rn(x.x, x.x > 0.f ? hi.x : lo.x), 0.f);
+        add_pair(s, e, __fmul_rn(x.y, x.y > 0.f ? hi.y : lo.y), 0.f);
     }
-    return nan ? __longlong_as_double(0x7ff8000000000000ll) : best;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) {
+        const float s2 = __shfl_xor_sync(kFull, s, off), e2 = __shfl_xor_sync(kFull, e, off);
+        // the same pair order in both lanes, so that every lane ends with the same sum
+        const bool up = (threadIdx.x & off) != 0;
+        float a = up ? s2 : s, ae = up ? e2 : e;
+        add_pair(a, ae, up ? s : s2, up ? e : e2);
+        s = a;
+        e = ae;
+    }
+    return order_key((double)s + (double)e);
 }
 
 // Block-wide sums of two counts (every thread gets them).
@@ -149,39 +170,95 @@ __device__ __forceinline__ uint2 sum2(SelShared& sh, uint32_t a, uint32_t b) {
     return t;
 }
 
-// After a histogram of one digit: the digit that holds the `left`-th largest,
-// and how many places are left inside it.
-__device__ __forceinline__ void pick_digit(SelShared& sh, uint32_t left) {
+// After a histogram: the bin that holds the `left`-th largest, its count and
+// how many places are left inside it.
+__device__ __forceinline__ void pick_bin(SelShared& sh, uint32_t left) {
     __syncthreads();
-    if (threadIdx.x < 32) {
-        const int lane = threadIdx.x;     // lane 0 takes the eight largest digits
-        uint32_t c[8], sum = 0;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t c[kPerBin], sum = 0;         // thread 0 takes the largest bins
 #pragma unroll
-        for (int j = 0; j < 8; ++j) { c[j] = sh.hist[255 - (lane * 8 + j)]; sum += c[j]; }
-        uint32_t before = sum;
+    for (int j = 0; j < kPerBin; ++j) {
+        c[j] = sh.hist[kBins - 1 - (threadIdx.x * kPerBin + j)];
+        sum += c[j];
+    }
+    uint32_t at = sum;
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const uint32_t o = __shfl_up_sync(kFull, before, off);
-            if (lane >= off) before += o;
-        }
-        before -= sum;                    // larger digits' count
-        if (before < left && before + sum >= left) {
-            uint32_t at = before;
+    for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t o = __shfl_up_sync(kFull, at, off);
+        if (lane >= off) at += o;
+    }
+    if (lane == 31) sh.red[warp][0] = at;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) at += sh.red[w][0];
+    at -= sum;                            // the larger bins' count
+    if (at < left && at + sum >= left) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (at < left && at + c[j] >= left) {
-                    sh.pick_bin = 255 - (lane * 8 + j);
-                    sh.pick_left = left - at;
-                }
-                at += c[j];
+        for (int j = 0; j < kPerBin; ++j) {
+            if (at < left && at + c[j] >= left) {
+                sh.bin = kBins - 1 - (threadIdx.x * kPerBin + j);
+                sh.left = left - at;
+                sh.in_bin = c[j];
             }
+            at += c[j];
         }
     }
     __syncthreads();
 }
-__device__ __forceinline__ void hist_add(SelShared& sh, uint32_t digit, bool on) {   // one atomic per digit and warp
-    const uint32_t same = __match_any_sync(kFull, on ? digit : 256u);
-    if (on && (threadIdx.x & 31) == __ffs(same) - 1) atomicAdd(&sh.hist[digit], __popc(same));
+
+// The `left`-th largest of the keys that are not kSure (at least `left` of them).
+__device__ __forceinline__ uint32_t kth_key(SelShared& sh, const uint32_t* keys, int n, uint32_t left) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t lo = 0xffffffffu, hi = 0u;
+    for (int j = threadIdx.x; j < n; j += kSelThreads)
+        if (keys[j] != kSure) {
+            lo = min(lo, keys[j]);
+            hi = max(hi, keys[j]);
+        }
+    lo = __reduce_min_sync(kFull, lo);
+    hi = __reduce_max_sync(kFull, hi);
+    __syncthreads();
+    if (lane == 0) { sh.red[warp][0] = lo; sh.red[warp][1] = hi; }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kSelWarps; ++w) { lo = min(lo, sh.red[w][0]); hi = max(hi, sh.red[w][1]); }
+    uint32_t some = (uint32_t)n;          // keys within [lo, hi], at most
+    while (lo != hi && some > (uint32_t)kFewTies) {
+        // 2048 bins over [lo, hi]
+        const int shift = max(0, 32 - __clz(hi - lo) - 11);
+        __syncthreads();
+        for (int j = threadIdx.x; j < kBins; j += kSelThreads) sh.hist[j] = 0u;
+        __syncthreads();
+        for (int j = threadIdx.x; j < n; j += kSelThreads) {
+            const uint32_t k = keys[j];
+            if (k != kSure && k >= lo && k <= hi) atomicAdd(&sh.hist[(k - lo) >> shift], 1u);
+        }
+        pick_bin(sh, left);
+        left = sh.left;
+        some = sh.in_bin;
+        lo += sh.bin << shift;
+        hi = min(hi, lo + ((1u << shift) - 1u));
+    }
+    if (lo == hi) return lo;
+    // few keys left: their order by pairs
+    if (threadIdx.x == 0) sh.n_list = 0u;
+    __syncthreads();
+    for (int j = threadIdx.x; j < n; j += kSelThreads) {
+        const uint32_t k = keys[j];
+        if (k != kSure && k >= lo && k <= hi) sh.list[atomicAdd(&sh.n_list, 1u)] = k;
+    }
+    __syncthreads();
+    const uint32_t m = sh.n_list;
+    for (uint32_t x = threadIdx.x; x < m; x += kSelThreads) {
+        const uint32_t k = sh.list[x];
+        uint32_t above = 0, same = 0;
+        for (uint32_t y = 0; y < m; ++y) {
+            above += sh.list[y] > k;
+            same += sh.list[y] == k;
+        }
+        if (above < left && above + same >= left) sh.T = k;
+    }
+    __syncthreads();
+    return sh.T;
 }
 
 template <int D>
@@ -190,17 +267,19 @@ __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const ListPa
     __shared__ SelShared sh;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int cs = p.splits, rank = blockIdx.x % cs, pair = blockIdx.x / cs;
     const int i = pair / p.n_kv_heads, h = pair % p.n_kv_heads;
+    // (the schedule's lists may be read before the dependency wait, as its plan is)
     const int off = p.list_off[i], n = p.list_off[i + 1] - off, K = p.top_k, G = p.group;
+    if (cs > 1) cluster_arrive();                         // waited for before the first remote store
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     int32_t* out = p.lists + (size_t)pair * K;
     if (n <= K) {                                         // (the whole cluster: same n)
         if (rank == 0)
             for (int j = threadIdx.x; j < K; j += kSelThreads) out[j] = j < n ? j : -1;
+        if (cs > 1) cluster_wait();
         return;
     }
-    if (cs > 1) cluster_sync_all();                       // the first CTA's shared memory exists
     const uint16_t* q = p.q + ((size_t)i * p.n_heads + (size_t)h * G) * D;
     const int32_t* slots = p.list_slots + off;
     auto bounds_of = [&](int slot) {
@@ -209,7 +288,23 @@ __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const ListPa
     const uint32_t keys0 = cs > 1 ? peer_addr(smem_u32(keys), 0) : 0u;
     const uint32_t abs0 = cs > 1 ? peer_addr(smem_u32(sh.top_abs), 0) : 0u;
 
+    if (rank == 0) {                                      // the largest sum|q| of the group's rows, for E
+        float qs = 0.f;
+        for (int r = warp; r < G; r += kSelWarps) {
+            float s = 0.f;
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) {
+                const float2 x = __half22float2(*reinterpret_cast<const __half2*>(q + (size_t)r * D + 64 * j + 2 * lane));
+                s += fabsf(x.x) + fabsf(x.y);
+            }
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+            qs = fmaxf(qs, s);
+        }
+        if (lane == 0) sh.qsum[warp] = qs;
+    }
     // scores of blocks of 16 chunks
+    bool met = cs == 1;                                   // the first CTA's shared memory exists
     __half2 top = __float2half2_rn(0.f);
     bool bad = false;
     for (int blk = rank * kSelWarps + warp; blk * 16 < n; blk += cs * kSelWarps) {
@@ -219,8 +314,7 @@ __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const ListPa
         if (s1 < 0 || s1 >= p.capacity) { s1 = 0; bad = true; }
         const uint4* b0 = reinterpret_cast<const uint4*>(bounds_of(s0)) + t;
         const uint4* b1 = reinterpret_cast<const uint4*>(bounds_of(s1)) + t;
-        float best0 = -INFINITY, best1 = -INFINITY;
-        bool nan0 = false, nan1 = false;
+        float best0 = __uint_as_float(0x7fffffffu), best1 = best0;   // NaN: a row that is not a number is passed over
         constexpr int J = D / 32;                         // 64-byte groups of a bounds row
         uint4 x0[2][J], x1[2][J];
 #pragma unroll
@@ -247,8 +341,6 @@ __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const ListPa
             // rows past the group repeat its last one: they change no maximum
             best0 = fmaxf(best0, fmaxf(acc[0], acc[1]));
             best1 = fmaxf(best1, fmaxf(acc[2], acc[3]));
-            nan0 = nan0 || acc[0] != acc[0] || acc[1] != acc[1];
-            nan1 = nan1 || acc[2] != acc[2] || acc[3] != acc[3];
         }
 #pragma unroll
         for (int part = 0; part < 2; ++part)
@@ -263,13 +355,15 @@ __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const ListPa
         for (int d = 1; d <= 2; d <<= 1) {
             best0 = fmaxf(best0, __shfl_xor_sync(kFull, best0, d));
             best1 = fmaxf(best1, __shfl_xor_sync(kFull, best1, d));
-            nan0 = __shfl_xor_sync(kFull, (int)nan0, d) || nan0;
-            nan1 = __shfl_xor_sync(kFull, (int)nan1, d) || nan1;
+        }
+        if (!met) {
+            cluster_wait();
+            met = true;
         }
         if (t < 2) {
             const int c = t ? c1 : c0;
             const bool forced = c < p.sink || c >= n - p.recent;
-            const uint32_t k = forced ? kSure : (t ? nan1 : nan0) ? 0u : order_key(t ? best1 : best0);
+            const uint32_t k = forced ? kSure : order_key(t ? best1 : best0);
             if (c < n) {
                 if (cs > 1) st_peer(keys0 + 4u * (uint32_t)c, k);
                 else keys[c] = k;
@@ -277,6 +371,7 @@ __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const ListPa
         }
     }
     if (bad) set_status(p.status, CA_ERR_DEVICE_BOUNDS);
+    if (!met) cluster_wait();
     {
         // the cluster's largest |bound|: a non-negative fp32's bits order as integers
         const float2 f = __half22float2(top);
@@ -302,40 +397,16 @@ __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const ListPa
         // E: with A = sum of |terms| <= max over rows of sum|q| times the largest |bound|, each of the
         // D / 8 steps of mma (16 exact products and the running sum, aligned and cut at 2^-23 of the
         // largest each, rounded once) is off by at most 18 * 2^-23 * A.
-        float qs = 0.f;
-        for (int r = warp; r < G; r += kSelWarps) {
-            float s = 0.f;
-            for (int d = lane; d < D; d += 32) s += fabsf(__half2float(__ushort_as_half(q[(size_t)r * D + d])));
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-            qs = fmaxf(qs, s);
-        }
-        if (lane == 0) sh.qsum[warp] = qs;
-
-        // T: the places-th largest key, digit by digit
-        uint32_t prefix = 0, left = places;
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            __syncthreads();
-            for (int j = threadIdx.x; j < 256; j += kSelThreads) sh.hist[j] = 0u;
-            __syncthreads();
-            for (int j0 = 0; j0 < n; j0 += kSelThreads) {
-                const int j = j0 + threadIdx.x;
-                const uint32_t k = j < n ? keys[j] : kSure;
-                hist_add(sh, (k >> shift) & 255u, k != kSure && (shift == 24 || (k >> (shift + 8)) == prefix));
-            }
-            pick_digit(sh, left);
-            prefix = (prefix << 8) | sh.pick_bin;
-            left = sh.pick_left;
-        }
+        const uint32_t kth = kth_key(sh, keys, n, places);
         float A = 0.f, big = 0.f;
 #pragma unroll
         for (int w = 0; w < kSelWarps; ++w) A = fmaxf(A, sh.qsum[w]);
         for (int r = 0; r < cs; ++r) big = fmaxf(big, __uint_as_float(sh.top_abs[r]));
         A *= big;
         const float E = A * ((D / 8) * 18.2f / 8388608.f);
-        const float T = key_value(prefix);
+        const float T = key_value(kth);
         uint32_t low = 0u, high = kTie - 1u;              // a band without bounds where E or T is not finite
-        if (prefix != 0u && E < 1e37f && fabsf(T) < 1e37f) {
+        if (kth != 0u && E < 1e37f && fabsf(T) < 1e37f) {
             const float w = 2.01f * E + fabsf(T) * 1e-6f;
             low = max(order_key(T - w), 1u);
             high = order_key(T + w);
@@ -362,14 +433,17 @@ __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const ListPa
             cut = high;
         } else if (c.y <= (uint32_t)kFewTies) {
             if (threadIdx.x == 0) sh.n_list = 0u;
+            for (int x = threadIdx.x; x < kFewTies; x += kSelThreads) sh.key64[x] = 0ull;
             __syncthreads();
             for (int j = threadIdx.x; j < n; j += kSelThreads)
                 if (keys[j] >= low && keys[j] <= high) sh.list[atomicAdd(&sh.n_list, 1u)] = (uint32_t)j;
             __syncthreads();
-            for (uint32_t x = warp; x < c.y; x += kSelWarps) {
-                const int s = slots[sh.list[x]];
-                const double v = exact_score<D>(p, q, bounds_of(s >= 0 && s < p.capacity ? s : 0), lane);
-                if (lane == 0) sh.key64[x] = order_key(v);
+            for (uint32_t x = warp; x < c.y * (uint32_t)G; x += kSelWarps) {   // (row, chunk) by (row, chunk)
+                const uint32_t e = x / (uint32_t)G, r = x % (uint32_t)G;
+                const int s = slots[sh.list[e]];
+                const unsigned long long k =
+                    exact_row<D>(q + (size_t)r * D, bounds_of(s >= 0 && s < p.capacity ? s : 0), lane);
+                if (lane == 0) atomicMax(&sh.key64[e], k);
             }
             __syncthreads();
             for (uint32_t x = threadIdx.x; x < c.y; x += kSelThreads) {
@@ -385,11 +459,14 @@ __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const ListPa
             uint32_t rest = open;
             auto exact_key = [&](int j) {
                 const int s = slots[j];
-                return order_key(exact_score<D>(p, q, bounds_of(s >= 0 && s < p.capacity ? s : 0), lane));
+                const uint16_t* b = bounds_of(s >= 0 && s < p.capacity ? s : 0);
+                unsigned long long k = 0ull;
+                for (int r = 0; r < G; ++r) k = max(k, exact_row<D>(q + (size_t)r * D, b, lane));
+                return k;
             };
             for (int shift = 56; shift >= 0; shift -= 8) {
                 __syncthreads();
-                for (int j = threadIdx.x; j < 256; j += kSelThreads) sh.hist[j] = 0u;
+                for (int j = threadIdx.x; j < kBins; j += kSelThreads) sh.hist[j] = 0u;
                 __syncthreads();
                 for (int j = warp; j < n; j += kSelWarps) {
                     if (keys[j] < low || keys[j] > high) continue;
@@ -397,9 +474,9 @@ __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const ListPa
                     if (lane == 0 && (shift == 56 || (k >> (shift + 8)) == pre))
                         atomicAdd(&sh.hist[(k >> shift) & 255u], 1u);
                 }
-                pick_digit(sh, rest);
-                pre = (pre << 8) | sh.pick_bin;
-                rest = sh.pick_left;
+                pick_bin(sh, rest);
+                pre = (pre << 8) | sh.bin;
+                rest = sh.left;
             }
             for (int j = warp; j < n; j += kSelWarps) {
                 const uint32_t k32 = keys[j];
@@ -715,9 +792,10 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
 #pragma unroll
             for (int db = 0; db < D / 16; ++db) o[nb][db][0] = o[nb][db][1] = o[nb][db][2] = o[nb][db][3] = 0.f;
         }
-        for (int it = 0;; ++it) {
-            const int st = it % S;
-            if (!mbar_wait(full0 + 8 * st, (uint32_t)(it / S) & 1u)) {
+        int st = 0;
+        uint32_t ph = 0;
+        for (int it = 0;; ++it, st = st + 1 == S ? 0 : st + 1, ph ^= (uint32_t)(st == 0)) {
+            if (!mbar_wait(full0 + 8 * st, ph)) {
                 if (lane == 0) set_status(p.status, CA_ERR_TIMEOUT);
                 break;
             }
@@ -877,11 +955,16 @@ dev::ListParams list_params(const Pool& p, const Sched& s, int32_t layer, const 
 }
 
 // One launch of `blocks` clusters of `cs` CTAs, a programmatic dependent of
-// the work before it (the kernels wait for that before anything else).
-int launch(const void* fn, unsigned blocks, int cs, int threads, size_t smem, void** args, cudaStream_t stream) {
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return CA_ERR_CUDA;
+// the work before it (the kernels wait for that before anything else).  `most`:
+// the kernel's largest dynamic shared memory, the same in every call, so that
+// pools which share a kernel never lower each other's limit.
+int launch(const Pool& p, int kind, const void* fn, unsigned blocks, int cs, int threads, size_t smem, size_t most,
+           void** args, cudaStream_t stream) {
+    if (smem > 48 * 1024 && p.list_fn[kind] != fn) {
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess)
+            return CA_ERR_CUDA;
+        p.list_fn[kind] = fn;
+    }
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -939,11 +1022,6 @@ SparseKernel pick_sparse(const PoolCfg& c) {
     }
 }
 
-int device_sms(const Pool& p) {
-    int n = 0;
-    return cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, p.device) == cudaSuccess ? n : 0;
-}
-
 }  // namespace
 
 int launch_select(const Pool& p, const Sched& s, int32_t layer, const void* q, int32_t top_k, int32_t sink,
@@ -953,17 +1031,17 @@ int launch_select(const Pool& p, const Sched& s, int32_t layer, const void* q, i
     a.lists = lists;
     a.sink = sink;
     a.recent = recent;
-    const int pairs = s.t.b * a.n_kv_heads, sms = device_sms(p);
-    // More CTAs per pair while the card is not full and each warp still has a block of 16 chunks.
+    const int pairs = s.t.b * a.n_kv_heads, sms = p.sms;
+    // More CTAs per pair while all are resident at once (two per SM) and each warp still has a block of 16 chunks.
     int cs = 1;
-    while (cs < 8 && pairs * cs < 2 * sms && cs * dev::kSelWarps * 16 < s.t.list_max) cs *= 2;
+    while (cs < 8 && pairs * cs * 2 <= 2 * sms && cs * dev::kSelWarps * 16 < s.t.list_max) cs *= 2;
     a.splits = cs;
     const size_t smem = (size_t)s.t.list_max * 4;
     const void* fn = p.cfg.head_dim == 64    ? reinterpret_cast<const void*>(&dev::select_chunks_kernel<64>)
                      : p.cfg.head_dim == 128 ? reinterpret_cast<const void*>(&dev::select_chunks_kernel<128>)
                                              : reinterpret_cast<const void*>(&dev::select_chunks_kernel<256>);
     void* args[] = {&a};
-    return launch(fn, (unsigned)pairs, cs, dev::kSelThreads, smem, args, static_cast<cudaStream_t>(stream));
+    return launch(p, 0, fn, (unsigned)pairs, cs, dev::kSelThreads, smem, (size_t)kMostChunks * 4, args, static_cast<cudaStream_t>(stream));
 }
 
 int launch_sparse(const Pool& p, const Sched& s, int32_t layer, const void* q, const int32_t* lists, int32_t top_k,
@@ -976,7 +1054,7 @@ int launch_sparse(const Pool& p, const Sched& s, int32_t layer, const void* q, c
     const bool quant = (p.cfg.flags & (CA_KV_FP8 | CA_KV_FP4)) != 0;
     a.scale_log2 = scale * 1.4426950408889634f * (quant ? kv_scale_of(p.cfg.k_scale) : 1.f);
     a.out_scale = quant ? kv_scale_of(p.cfg.v_scale) : 1.f;
-    const int units = s.t.b * a.n_kv_heads * ((a.group + k.rows - 1) / k.rows), sms = device_sms(p);
+    const int units = s.t.b * a.n_kv_heads * ((a.group + k.rows - 1) / k.rows), sms = p.sms;
     const int most = std::min(top_k, s.t.list_max);        // entries that hold a chunk
     int cs = 1;
     while (cs < 8 && units * cs < 2 * sms && cs * 2 <= most) cs *= 2;
@@ -988,7 +1066,7 @@ int launch_sparse(const Pool& p, const Sched& s, int32_t layer, const void* q, c
     uint32_t ring = (uint32_t)std::max(st * k.stage, k.merge);
     const size_t smem = ring + (size_t)k.tail;
     void* args[] = {const_cast<unsigned char*>(p.tmap), &a, &ring};
-    return launch(reinterpret_cast<const void*>(k.fn), (unsigned)units, cs, dev::kSpThreads, smem, args,
+    return launch(p, 1, reinterpret_cast<const void*>(k.fn), (unsigned)units, cs, dev::kSpThreads, smem, smem, args,
                   static_cast<cudaStream_t>(stream));
 }
 

@@ -106,7 +106,9 @@ def test_chunk_list_calls_refuse_without_a_device(lib):
     assert lib.ca_sparse_attention(p.handle, None, 0, a, a, 2, a, 1.0, None) == -1
     assert lib.ca_read_batch(p.handle, 1, ids, None, ln, a, a, None) == -1
     assert lib.ca_read_batch(None, 1, ids, None, ln, a, a, None) == -1
-    assert lib.ca_seq_length(p.handle, 1, None) == -1
+    assert lib.ca_seq_lengths(p.handle, 1, ids, None) == -1
+    assert lib.ca_seq_lengths(p.handle, 1, None, ln) == -1
+    assert lib.ca_seq_lengths(p.handle, 1, (C.c_int64 * 1)(7), ln) == -3
     # the lists change nothing in the tables, and a schedule is rebuilt when the flag changes
     for k, v in s.tables().items():
         np.testing.assert_array_equal(v, plain.tables()[k])
