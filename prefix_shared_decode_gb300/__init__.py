@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes as C
 import math
+from array import array
 
 import numpy as np
 
@@ -48,13 +49,15 @@ def _i32(a) -> np.ndarray:
     return np.ascontiguousarray(np.asarray(a, dtype=np.int32))
 
 
-def _i64(a) -> np.ndarray:
-    return np.ascontiguousarray(np.asarray(a, dtype=np.int64))
-
-
-def _at(a: np.ndarray) -> int:
+def _at(a) -> int:
     """The address of an array's data."""
-    return a.__array_interface__["data"][0]
+    return a.buffer_info()[0] if isinstance(a, array) else a.__array_interface__["data"][0]
+
+
+def _ints(kind: str, a) -> array:
+    """A short list of integers ("q": int64, "i": int32) with an address that
+    costs less to ask for than a numpy array's."""
+    return array(kind, a if isinstance(a, (list, tuple)) else np.asarray(a).tolist())
 
 
 class Pool:
@@ -176,18 +179,20 @@ class Pool:
         for a host-only pool).  All or nothing.  Returns the shared tokens.
         ``token_lists`` is a list of token arrays, or (with ``lengths``) the
         already concatenated tokens."""
-        ids = _i64(seq_ids)
+        ids = _ints("q", seq_ids)
         if lengths is None:
-            lens = np.ascontiguousarray(np.array([len(t) for t in token_lists], dtype=np.int32))
+            lens = _ints("i", [len(t) for t in token_lists])
             tok = np.ascontiguousarray(np.concatenate([np.asarray(t, dtype=np.int32) for t in token_lists]))
         else:
-            lens, tok = _i32(lengths), _i32(token_lists)
+            lens, tok = _ints("i", lengths), _i32(token_lists)
+        if len(lens) != len(ids) or tok.size < sum(lens):
+            raise ValueError("seq_ids, lengths and tokens do not go together")
         kp = vp = None
         if k is not None:
             assert k.is_contiguous() and v.is_contiguous()
-            assert tuple(k.shape) == (self.n_layers, int(lens.sum()), self.n_kv_heads, self.head_dim)
+            assert k.shape == (self.n_layers, sum(lens), self.n_kv_heads, self.head_dim)
             kp, vp = k.data_ptr(), v.data_ptr()
-        shared = np.zeros(len(ids), dtype=np.int32)
+        shared = array("i", bytes(4 * len(ids)))
         check(capi.lib().ca_insert_batch(self._h, len(ids), _at(ids), _at(tok), _at(lens), kp, vp,
                                          None if self.host_only else _stream_ptr(stream), _at(shared)),
               "ca_insert_batch")
@@ -218,31 +223,31 @@ class Pool:
         import torch
         if self.host_only:
             raise ValueError("a host-only pool holds no rows")
-        ids = _i64(seq_ids)
-        if ids.ndim != 1 or not len(ids):
+        ids, first = _ints("q", seq_ids), None if starts is None else _ints("i", starts)
+        b = len(ids)
+        if not b:
             raise ValueError("seq_ids must be a list of at least one sequence")
-        held = np.empty(len(ids), np.int32)
         L = capi.lib()
-        check(L.ca_seq_lengths(self._h, len(ids), _at(ids), _at(held)), "ca_seq_lengths")
-        first = None if starts is None else _i32(starts)
+        lens = array("i", bytes(4 * b))
+        check(L.ca_seq_lengths(self._h, b, _at(ids), _at(lens)), "ca_seq_lengths")
         if lengths is not None:
-            lens = _i32(lengths)
-        else:
-            lens = held if first is None else held - first
-        if lens.shape != ids.shape or (first is not None and first.shape != ids.shape):
+            lens = _ints("i", lengths)
+        elif first is not None and len(first) == b:
+            lens = _ints("i", [n - a for n, a in zip(lens, first)])
+        if len(lens) != b or (first is not None and len(first) != b):
             raise ValueError("seq_ids, starts and lengths differ in length")
-        if lens.min() < 0:
+        if min(lens) < 0:
             raise ValueError("lengths must not be negative")
-        shape = (self.n_layers, int(lens.sum(dtype=np.int64)), self.n_kv_heads, self.head_dim)
+        shape = (self.n_layers, sum(lens), self.n_kv_heads, self.head_dim)
         if out is None:
             k = torch.empty(shape, dtype=torch.float16, device=self._kv.device)
             v = torch.empty(shape, dtype=torch.float16, device=self._kv.device)
         else:
             k, v = out
-            for x in (k, v):
-                self._check_tensor(x, shape, torch.float16, "out")
+            self._check_tensor(k, shape, torch.float16, "out")
+            self._check_tensor(v, shape, torch.float16, "out")
         if shape[1]:
-            check(L.ca_read_batch(self._h, len(ids), _at(ids), None if first is None else _at(first), _at(lens),
+            check(L.ca_read_batch(self._h, b, _at(ids), None if first is None else _at(first), _at(lens),
                                   k.data_ptr(), v.data_ptr(), self._stream(stream)), "ca_read_batch")
         return k, v
 
@@ -258,7 +263,7 @@ class Pool:
         return n.value
 
     def _check_tensor(self, x, shape, dtype, what: str) -> None:
-        if x.dtype != dtype or not x.is_contiguous() or tuple(x.shape) != tuple(shape):
+        if x.dtype != dtype or not x.is_contiguous() or x.shape != shape:
             raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
         if x.device != self._kv.device:
             raise ValueError(f"{what} is on {x.device}, the pool on {self._kv.device}")
@@ -278,7 +283,7 @@ class Pool:
         check(capi.lib().ca_remove_seq(self._h, int(seq_id)), "ca_remove_seq")
 
     def remove_batch(self, seq_ids) -> None:
-        ids = _i64(seq_ids)
+        ids = _ints("q", seq_ids)
         check(capi.lib().ca_remove_batch(self._h, len(ids), _at(ids)), "ca_remove_batch")
 
     def _generation(self) -> int:
@@ -323,6 +328,7 @@ class Pool:
                                               None if self.host_only else _stream_ptr(stream)),
               "ca_build_schedule_ex")
         s._h = h
+        s._ws_need = None
         s.b = len(ids)
         s.q_len = int(q_len)
         if ids is not s._ids:
@@ -341,6 +347,7 @@ class Schedule:
         self.b = 0
         self.q_len = 1
         self._ws = None
+        self._ws_need = None            # bytes of the device workspace, until the next build
         self._ids, self._ids_ptr, self._ids_list, self._flags = None, None, None, 0
 
     def _key(self) -> tuple:
@@ -400,7 +407,9 @@ class Schedule:
         """A zero-filled device workspace large enough for this schedule
         (cached and grown on demand)."""
         import torch
-        need = self.workspace_bytes(host_io)
+        need = self.workspace_bytes(host_io) if host_io or self._ws_need is None else self._ws_need
+        if not host_io:
+            self._ws_need = need
         if self._ws is None or self._ws.numel() < need:
             self._ws = torch.zeros(max(need, 256), dtype=torch.uint8, device=self.pool._kv.device)
         return self._ws

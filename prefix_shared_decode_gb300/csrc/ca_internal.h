@@ -315,6 +315,11 @@ AttnParams attn_params(const Pool& pool, const Sched& s, int32_t layer, const vo
 uint64_t kernel_launches();
 void count_launch();
 
+// fp4_attention.cu: the two-phase kernel of an fp4 pool (the arguments and the
+// plan of the others') and its dynamic shared memory
+void* fp4_kernel(const PoolCfg& c);
+size_t fp4_smem_bytes(const PoolCfg& c, int stages);
+
 // cache_rows.cu: quantising stores of an fp4 pool, key bounds, reading back
 // (a ScatterChunk there is rows [dst_row, dst_row + n_rows) of `slot` and the
 // packed rows from src_row)

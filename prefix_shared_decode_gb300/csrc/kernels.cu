@@ -48,7 +48,7 @@
 
 #include "ca_internal.h"
 #include "device.cuh"
-#include "fp4.cuh"
+#include "row_blocks.cuh"
 
 namespace ca {
 namespace dev {
@@ -56,10 +56,6 @@ namespace dev {
 constexpr int kConsumerWarps = 4;
 constexpr int kThreads = 32 * (kConsumerWarps + 1);
 constexpr int kMaxStages = 8;
-constexpr int kQRows = 64;                 // query rows per tensor-core unit, max (D <= 128)
-// Query rows of the Q tile: 32 at head_dim 256 (the tile stays 16 KiB).
-template <int D>
-__host__ __device__ constexpr int q_rows() { return D == 256 ? 32 : kQRows; }
 constexpr int kRing = 16;                  // unit announcements (producer -> consumers)
 // Merge CTAs: one warp per pair, 16 warps a CTA (fewer CTAs to retire at
 // the hand-over than 4-warp CTAs; measured 2% faster calls at 72 MB of KV)
@@ -342,176 +338,6 @@ __device__ __forceinline__ void sf_chunk_f8_tc(const uint8_t* kt, const uint8_t*
     }
 }
 
-// ---------------------------------------------------------------------------
-// Tensor-core path (chunk-first units, and sequence-first units with several
-// query rows): one chunk-head tile against a 16-row block of the Q tile with
-// mma.sync m16n8k16 (fp16 in, fp32 accumulate).  The warp takes tokens
-// [tok0, tok0 + NT) of the chunk.  Row state per thread: rows g = lane/4 and
-// g + 8 of the block.
-// ---------------------------------------------------------------------------
-// Scores of a 16-row block against NT tokens [tok0, tok0 + NT) of a chunk
-// tile, over the head dims [16 kk0, 16 kk1): S = Q K^T with the Q fragments
-// read from the swizzled Q tile (row lane%16, 16-byte chunk 2kk + lane/16).
-template <int C, int D, int NT, bool F8 = false>
-__device__ __forceinline__ void cf_scores(uint32_t kt, int tok0, uint32_t qrow_addr_base, int kk0, int kk1,
-                                          float (&sacc)[NT / 8][4], int lane) {
-#pragma unroll
-    for (int i = 0; i < NT / 8; ++i) sacc[i][0] = sacc[i][1] = sacc[i][2] = sacc[i][3] = 0.f;
-    if constexpr (F8) {
-        // E4M3 keys (128-byte rows, 16-byte chunk kk of row r at chunk
-        // kk ^ (r % 8)).  Inside each 16-dim step the fragment columns are
-        // permuted, 2t (+1) <-> dim 16kk + 4t (+1) and 2t + 8 (+9) <->
-        // 16kk + 4t + 2 (+3), on both operands: one 32-bit load gives a
-        // lane's four key bytes of token g, one 64-bit load its four query
-        // dims of a row.  The scores come out in the usual layout.
-        const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-        for (int kk = kk0; kk < kk1; ++kk) {
-            uint32_t qa[4];
-            lds64(qrow_addr_base + swz(g, 2 * kk + (t >> 1), q_rows<D>()) + 8 * (t & 1), qa[0], qa[2]);
-            lds64(qrow_addr_base + swz(g + 8, 2 * kk + (t >> 1), q_rows<D>()) + 8 * (t & 1), qa[1], qa[3]);
-#pragma unroll
-            for (int j = 0; j < NT / 8; ++j) {
-                const int row = tok0 + 8 * j + g;
-                const uint32_t wd = lds32(kt + row * 128 + ((kk ^ (row & 7)) << 4) + 4 * t);
-                mma16816(sacc[j], qa, f16x2_from_e4m3x2(wd & 0xffffu), f16x2_from_e4m3x2(wd >> 16));
-            }
-        }
-        return;
-    }
-#pragma unroll
-    for (int kk = kk0; kk < kk1; ++kk) {
-        uint32_t qa[4];
-        {
-            const int qr = (lane & 15), qc = 2 * kk + (lane >> 4);
-            ldsm_x4(qrow_addr_base + swz(qr, qc, q_rows<D>()), qa[0], qa[1], qa[2], qa[3]);
-        }
-#pragma unroll
-        for (int np = 0; np < NT / 16; ++np) {
-            const int tok = tok0 + np * 16 + (lane & 7) + ((lane >> 4) << 3);
-            const int kc = 2 * kk + ((lane >> 3) & 1);
-            uint32_t b0, b1, b2, b3;
-            ldsm_x4(kt + swz(tok, kc, C), b0, b1, b2, b3);
-            mma16816(sacc[2 * np], qa, b0, b1);
-            mma16816(sacc[2 * np + 1], qa, b2, b3);
-        }
-    }
-}
-
-// Online softmax of a scored 16-row block (log2 units; columns past ntok,
-// and under the causal mask past each row's limit, are masked), then
-// O += P V for the OD output dims [16 dp0, 16 dp0 + OD).
-template <int C, int NT, int OD, bool F8 = false>
-__device__ __forceinline__ void cf_softmax_pv(uint32_t vt, int ntok, int tok0, int ctx0, int lim0, int lim1,
-                                              float scale_log2, float (&sacc)[NT / 8][4], int dp0,
-                                              float (&m)[2], float (&s)[2], float (&o)[OD / 8][4], int lane) {
-    float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-    for (int nt = 0; nt < NT / 8; ++nt) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int col = tok0 + nt * 8 + 2 * (lane & 3) + (e & 1);
-            // a column counts if it holds a token and, under the causal
-            // mask, that token is at or before the row's limit
-            const bool ok = col < ntok && ctx0 + col <= ((e >> 1) ? lim1 : lim0);
-            const float x = ok ? sacc[nt][e] * scale_log2 : -INFINITY;
-            sacc[nt][e] = x;
-            mx[e >> 1] = fmaxf(mx[e >> 1], x);
-        }
-    }
-    // The row's reference maximum m is raised lazily: only when the chunk's
-    // maximum exceeds it by more than 2^8 (P then stays below 256, exact in
-    // fp16), so most chunks leave O unscaled; o and s always refer to the
-    // same m, which the partial carries.
-    float alpha[2], mu[2];
-    bool grow = false;
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(kFull, mx[r], 1));
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(kFull, mx[r], 2));
-        alpha[r] = 1.f;
-        if (mx[r] > m[r] + 8.f) {                   // also the first finite maximum
-            alpha[r] = ex2(m[r] - mx[r]);           // 0 while m is -inf
-            m[r] = mx[r];
-            s[r] *= alpha[r];
-            grow = true;
-        }
-        mu[r] = (m[r] == -INFINITY) ? 0.f : m[r];
-    }
-    uint32_t pa[NT / 16][4];
-#pragma unroll
-    for (int nt = 0; nt < NT / 8; ++nt) {
-        const float p0 = ex2(sacc[nt][0] - mu[0]), p1 = ex2(sacc[nt][1] - mu[0]);
-        const float p2 = ex2(sacc[nt][2] - mu[1]), p3 = ex2(sacc[nt][3] - mu[1]);
-        s[0] += p0 + p1;
-        s[1] += p2 + p3;
-        // accumulator layout of n-tile nt == A-operand layout of k-step nt/2
-        pa[nt >> 1][(nt & 1) * 2 + 0] = pack_half2(p0, p1);
-        pa[nt >> 1][(nt & 1) * 2 + 1] = pack_half2(p2, p3);
-    }
-    if (__any_sync(kFull, grow)) {
-#pragma unroll
-        for (int dt = 0; dt < OD / 8; ++dt) {
-            o[dt][0] *= alpha[0]; o[dt][1] *= alpha[0];
-            o[dt][2] *= alpha[1]; o[dt][3] *= alpha[1];
-        }
-    }
-    if constexpr (F8) {
-        // E4M3 values: n-tile 4dq + i holds output dims 32dq + 4n + i
-        // (n = the fragment column), so a lane's B operand for dims
-        // 32dq + 4g .. + 3 of its four tokens (16j + 2t, + 1, + 8, + 9) is
-        // four 32-bit loads paired per dim by byte permutes.  The
-        // accumulator of lane (g, t) then holds dims 32dq + 8t .. + 7 of its
-        // rows: o[4dq + i][c] <-> dim 32dq + 8t + 4c' + i (c' = c % 2).
-        static_assert(OD == 128, "fp8 pools have head_dim 128");
-        const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-        for (int j = 0; j < NT / 16; ++j) {
-            const int r0 = tok0 + 16 * j + 2 * t;
-#pragma unroll
-            for (int dq = 0; dq < 4; ++dq) {
-                const int kc = 2 * dq + (g >> 2);
-                const uint32_t off = 4 * (g & 3);
-                const uint32_t wa = lds32(vt + r0 * 128 + ((kc ^ (r0 & 7)) << 4) + off);
-                const uint32_t wb = lds32(vt + (r0 + 1) * 128 + ((kc ^ ((r0 + 1) & 7)) << 4) + off);
-                const uint32_t wc = lds32(vt + (r0 + 8) * 128 + ((kc ^ (r0 & 7)) << 4) + off);
-                const uint32_t wd = lds32(vt + (r0 + 9) * 128 + ((kc ^ ((r0 + 1) & 7)) << 4) + off);
-                const uint32_t x01 = __byte_perm(wa, wb, 0x5140), x23 = __byte_perm(wa, wb, 0x7362);
-                const uint32_t y01 = __byte_perm(wc, wd, 0x5140), y23 = __byte_perm(wc, wd, 0x7362);
-                mma16816(o[4 * dq + 0], pa[j], f16x2_from_e4m3x2(x01 & 0xffffu), f16x2_from_e4m3x2(y01 & 0xffffu));
-                mma16816(o[4 * dq + 1], pa[j], f16x2_from_e4m3x2(x01 >> 16), f16x2_from_e4m3x2(y01 >> 16));
-                mma16816(o[4 * dq + 2], pa[j], f16x2_from_e4m3x2(x23 & 0xffffu), f16x2_from_e4m3x2(y23 & 0xffffu));
-                mma16816(o[4 * dq + 3], pa[j], f16x2_from_e4m3x2(x23 >> 16), f16x2_from_e4m3x2(y23 >> 16));
-            }
-        }
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < NT / 16; ++j) {
-#pragma unroll
-        for (int dq = 0; dq < OD / 16; ++dq) {
-            const int tok = tok0 + 16 * j + (lane & 7) + (((lane >> 3) & 1) << 3);
-            const int kc = 2 * (dp0 + dq) + (lane >> 4);
-            uint32_t b0, b1, b2, b3;
-            ldsm_x4_t(vt + swz(tok, kc, C), b0, b1, b2, b3);
-            mma16816(o[2 * dq], pa[j], b0, b1);
-            mma16816(o[2 * dq + 1], pa[j], b2, b3);
-        }
-    }
-}
-
-// One warp, one 16-row block, NT tokens, every head dim.
-// F8: K and V are the stage's E4M3 bytes (head_dim 128), and o comes out
-// with its dims permuted as cf_softmax_pv describes.
-template <int C, int D, int NT, bool F8 = false>
-__device__ __forceinline__ void cf_chunk(uint32_t kt, uint32_t vt, int ntok, int tok0, int ctx0, int lim0,
-                                         int lim1, uint32_t qrow_addr_base, float scale_log2,
-                                         float (&m)[2], float (&s)[2], float (&o)[D / 8][4], int lane) {
-    float sacc[NT / 8][4];
-    cf_scores<C, D, NT, F8>(kt, tok0, qrow_addr_base, 0, D / 16, sacc, lane);
-    cf_softmax_pv<C, NT, D, F8>(vt, ntok, tok0, ctx0, lim0, lim1, scale_log2, sacc, 0, m, s, o, lane);
-}
-
 // head_dim 256: two warps share a 16-row block, warp `half` owning head dims
 // [128 half, 128 half + 128) (128 fp32 accumulators per thread for all 256
 // would not fit the register budget).  Each scores the block over its dims,
@@ -559,115 +385,14 @@ __device__ __forceinline__ void f8_tile_to_f16(const uint8_t* src, uint8_t* dst,
     }
 }
 
-// An fp4 chunk-head tile widened to the fp16 K and V tiles that the 16-row
-// blocks read (code * scale is exact in fp16).  All consumer threads take
-// part.  A thread takes 16 bytes (8 at D = 64) of a row's key codes: four
-// dims of every 16, and 8 (4) bytes of a token's value codes: two dims of
-// every 16; consecutive threads take rows whose swizzled 16-byte columns
-// differ.
-template <int C, int D>
-__device__ __forceinline__ void f4_tile_to_f16(const uint8_t* src, uint8_t* kd, uint8_t* vd, int tid) {
-    using T = F4Tile<C, D>;
-    constexpr int NK = D / 16;
-    for (int i = tid; i < C * 4; i += kConsumerWarps * 32) {
-        const int t = i & 3, r = i >> 2;
-        // rows of 8 in the order 0 1 4 5 2 3 6 7: tokens 0 4 2 6, then 1 5 3 7
-        const int m = (r & ~7) | (r & 1) | ((r & 2) << 1) | ((r & 4) >> 1);
-        const int tok = f4_token(m);
-        uint32_t w[D / 32], sc[D / 64];
-        lds_words<D / 32>(src + m * (D / 2) + t * (D / 8), w);
-        lds_words<D / 64>(src + T::kKScales + m * (D / 16), sc);
-#pragma unroll
-        for (int kp = 0; kp < NK / 2; ++kp) {             // two steps: one word of codes, two scales
-            uint32_t x[4], h[2];
-            f16x2_from_e2m1x8(w[kp], x);
-            f16x2_from_e4m3x4(sc[kp >> 1], h);
-            const uint32_t sa = __byte_perm(h[kp & 1], 0u, 0x1010), sb = __byte_perm(h[kp & 1], 0u, 0x3232);
-            *reinterpret_cast<uint2*>(kd + swz(tok, 4 * kp + (t >> 1), C) + 8 * (t & 1)) =
-                make_uint2(mul_f16x2(x[0], sa), mul_f16x2(x[1], sa));
-            *reinterpret_cast<uint2*>(kd + swz(tok, 4 * kp + 2 + (t >> 1), C) + 8 * (t & 1)) =
-                make_uint2(mul_f16x2(x[2], sb), mul_f16x2(x[3], sb));
-        }
-    }
-    for (int i = tid; i < C * 8; i += kConsumerWarps * 32) {
-        const int g = i & 7, r = i >> 3;
-        // four rows of a warp: tokens 0 2 4 6, then 1 3 5 7 of each 8
-        const int tok = (r & ~7) | ((r & 3) << 1) | ((r >> 2) & 1);
-        uint32_t w[D / 64];
-        lds_words<D / 64>(src + T::kVCodes + tok * (D / 2) + f4_v_unit<D>(tok, g) * (D / 16), w);
-        // the scale pairs of the token and its partner 4 on (or before)
-        uint32_t sc[D / 32];
-        lds_words<D / 32>(src + T::kVScales + (f4_v_scale<D>(tok, 0) & ~1), sc);
-        const uint32_t pick = (tok & 4) ? 0x3232u : 0x1010u;
-#pragma unroll
-        for (int i4 = 0; i4 < D / 64; ++i4) {
-            uint32_t x[4];
-            f16x2_from_e2m1x8(w[i4], x);
-#pragma unroll
-            for (int j2 = 0; j2 < 2; ++j2) {
-                uint32_t h[2];
-                f16x2_from_e4m3x4(sc[2 * i4 + j2], h);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int db = 4 * i4 + 2 * j2 + e;
-                    *reinterpret_cast<uint32_t*>(vd + swz(tok, 2 * db + (g >> 2), C) + 4 * (g & 3)) =
-                        mul_f16x2(x[2 * j2 + e], __byte_perm(h[e], 0u, pick));
-                }
-            }
-        }
-    }
-}
-
-// Sequence-first on an fp4 pool: one query row against the 16 tokens of
-// block `blk` of a tile, on the tensor cores with the query replicated over
-// the 8 columns (as sf_chunk_f8_tc does; on CUDA cores the widening alone
-// would outweigh the tile's bytes).  Only columns 0 (c0, c2) are formed.
-// The path is bound by issue slots, so a block costs no shuffle and no
-// rescaling as a rule: the reference m is a running maximum less kF4Lift,
-// raised only when some score passes it by kF4Lift + kF4Slack (a vote), and
-// s holds each lane's own tokens until the head ends.  The weights stay below
-// 2^13 in their fp16 operand and normal numbers down to 2^-19 (or less) of
-// the largest.
-constexpr float kF4Lift = 5.f, kF4Slack = 8.f;
-template <int C, int D>
-__device__ __forceinline__ void sf_chunk_f4_tc(const uint8_t* tile, int blk, int ntok,
-                                               const uint32_t (&qb)[1][D / 16][2], float scale_log2, float& m,
-                                               float& s, float (&oc)[1][D / 16][4], int lane) {
-    const int g = lane >> 2;
-    float acc[1][4];
-    f4_scores<C, D, 1, true>(tile, blk, qb, acc, lane);
-    const int r0 = blk * 16 + f4_token(g);
-    const float x0 = (r0 < ntok) ? acc[0][0] * scale_log2 : -INFINITY;
-    const float x1 = (r0 + 8 < ntok) ? acc[0][2] * scale_log2 : -INFINITY;
-    float mx = fmaxf(x0, x1);
-    if (__any_sync(kFull, mx > m + (kF4Lift + kF4Slack))) {
-#pragma unroll
-        for (int off = 4; off <= 16; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
-        const float mnew = fmaxf(m, mx - kF4Lift);
-        const float alpha = ex2(m - mnew);
-        m = mnew;
-        s *= alpha;
-#pragma unroll
-        for (int db = 0; db < D / 16; ++db) {
-            oc[0][db][0] *= alpha;
-            oc[0][db][2] *= alpha;
-        }
-    }
-    const float mu = (m == -INFINITY) ? 0.f : m;
-    const float p0 = ex2(x0 - mu), p1 = ex2(x1 - mu);
-    s += p0 + p1;
-    const uint32_t pb[1][2] = {{movm_trans(pack_half2(p0, p0)), movm_trans(pack_half2(p1, p1))}};
-    f4_pv<C, D, 1>(tile, blk, pb, oc, lane);
-}
-
 // Shared-memory map of one CTA.  EB: bytes per stored K/V element (2 for
-// fp16; 1 for fp8, which adds an fp16 copy of one stage for the transposed
-// few-row products; 0 for fp4, which adds it for the 16-row blocks).
+// fp16, 1 for fp8, which adds an fp16 copy of one stage for the transposed
+// few-row products).
 template <int C, int D, int EB>
 struct Smem {
-    static constexpr int kTile = EB ? C * D * EB : F4Tile<C, D>::kBytes / 2;   // one K or V tile of one chunk-head
+    static constexpr int kTile = C * D * EB;    // one K or V tile of one chunk-head
     static constexpr int kStage = 2 * kTile;    // K then V
-    static constexpr int kConvBytes = EB <= 1 ? 2 * C * D * 2 : 0;
+    static constexpr int kConvBytes = EB == 1 ? 2 * C * D * 2 : 0;
     static constexpr int kQBytes = q_rows<D>() * D * 2;
     // head_dim 256: score halves exchanged by warp pairs, two chunk parities
     static constexpr int kXsBytes = D == 256 ? 2 * kConsumerWarps * (C / 8) * 4 * 32 * 4 : 0;
@@ -729,10 +454,9 @@ __device__ __forceinline__ bool sf_rows_transposed(
         float ot[D / 16][4], m[2] = {-INFINITY, -INFINITY}, s[2] = {0.f, 0.f};
 #pragma unroll
         for (int db = 0; db < D / 16; ++db) ot[db][0] = ot[db][1] = ot[db][2] = ot[db][3] = 0.f;
-        int st = it % S;
-        uint32_t ph = (uint32_t)(it / S) & 1u;
-        for (; L < seg_end; ++L, ++it, st = st + 1 == S ? 0 : st + 1, ph ^= (uint32_t)(st == 0)) {
-            if (!mbar_wait(full0 + 8 * st, ph)) {
+        for (; L < seg_end; ++L, ++it) {
+            const int st = it % S;
+            if (!mbar_wait(full0 + 8 * st, (uint32_t)(it / S) & 1u)) {
                 set_status(p.status, CA_ERR_TIMEOUT);
                 ok = false;
                 break;
@@ -753,20 +477,7 @@ __device__ __forceinline__ bool sf_rows_transposed(
             }
             if (act) {
                 const int tok0 = 16 * w;
-                // token of the block in fragment row g (fp4 tiles: f4_token)
-                const int tg = EB == 0 ? f4_token(g) : g;
                 float sacc[4] = {0.f, 0.f, 0.f, 0.f};
-                if constexpr (EB == 0) {
-                    uint32_t qb[1][D / 16][2];
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        lds64(smem_u32(qreg) + swz(g, 2 * kk + (t >> 1), q_rows<D>()) + 8 * (t & 1), qb[0][kk][0],
-                              qb[0][kk][1]);
-                    float s4[1][4];
-                    f4_scores<C, D, 1, false>(stages + (size_t)st * SM::kStage, w, qb, s4, lane);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sacc[e] = s4[0][e];
-                } else {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     // Q^T as the B operand: n = query row (lane & 7), k = 16 dims
@@ -775,12 +486,11 @@ __device__ __forceinline__ bool sf_rows_transposed(
                     ldsm_x4(kt + swz(tok0 + (lane & 15), 2 * kk + (lane >> 4), C), a[0], a[1], a[2], a[3]);
                     mma16816(sacc, a, qb0, qb1);
                 }
-                }
-                // sacc: (token tg, rows 2t, 2t+1), (token tg + 8, rows 2t, 2t+1)
+                // sacc: (token g, rows 2t, 2t+1), (token g + 8, rows 2t, 2t+1)
                 float x[4], mx[2];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int tok = tok0 + tg + 8 * (i >> 1), row = 2 * t + (i & 1);
+                    const int tok = tok0 + g + 8 * (i >> 1), row = 2 * t + (i & 1);
                     const bool valid = tok < ntok && row < m_rows && ctx0 + tok <= limr[i & 1];
                     x[i] = valid ? sacc[i] * p.scale_log2 : -INFINITY;
                 }
@@ -788,14 +498,10 @@ __device__ __forceinline__ bool sf_rows_transposed(
                 mx[1] = fmaxf(x[1], x[3]);
                 bool grow = false;
                 float alpha[2] = {1.f, 1.f}, mu[2];
-                // fp4: one vote instead of the reductions, as in sf_chunk_f4_tc
-                if (EB != 0 || __any_sync(kFull, mx[0] > m[0] + (kF4Lift + kF4Slack) ||
-                                                     mx[1] > m[1] + (kF4Lift + kF4Slack)))
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
 #pragma unroll
                     for (int off = 4; off <= 16; off <<= 1) mx[r] = fmaxf(mx[r], __shfl_xor_sync(kFull, mx[r], off));
-                    if constexpr (EB == 0) mx[r] -= kF4Lift;
                     // the reference maximum is raised lazily, as in cf_softmax_pv
                     if (mx[r] > m[r] + 8.f) {
                         alpha[r] = ex2(m[r] - mx[r]);
@@ -803,9 +509,8 @@ __device__ __forceinline__ bool sf_rows_transposed(
                         s[r] *= alpha[r];
                         grow = true;
                     }
+                    mu[r] = (m[r] == -INFINITY) ? 0.f : m[r];
                 }
-                mu[0] = (m[0] == -INFINITY) ? 0.f : m[0];
-                mu[1] = (m[1] == -INFINITY) ? 0.f : m[1];
                 if (__any_sync(kFull, grow)) {
 #pragma unroll
                     for (int db = 0; db < D / 16; ++db) {
@@ -818,19 +523,13 @@ __device__ __forceinline__ bool sf_rows_transposed(
                 float ps[2] = {p0 + p2, p1 + p3};
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    if constexpr (EB != 0)
 #pragma unroll
-                        for (int off = 4; off <= 16; off <<= 1) ps[r] += __shfl_xor_sync(kFull, ps[r], off);
-                    s[r] += ps[r];               // fp4: the lane's own tokens
+                    for (int off = 4; off <= 16; off <<= 1) ps[r] += __shfl_xor_sync(kFull, ps[r], off);
+                    s[r] += ps[r];
                 }
                 // P^T fragments: k = tokens, n = query rows
                 const uint32_t b0 = movm_trans(pack_half2(p0, p1));   // tokens 0..7
                 const uint32_t b1 = movm_trans(pack_half2(p2, p3));   // tokens 8..15
-                if constexpr (EB == 0) {
-                    const uint32_t pb[1][2] = {{b0, b1}};
-                    f4_pv<C, D, 1>(stages + (size_t)st * SM::kStage, w, pb,
-                                   reinterpret_cast<float(&)[1][D / 16][4]>(ot), lane);
-                } else {
 #pragma unroll
                 for (int db = 0; db < D / 16; ++db) {
                     uint32_t a[4];
@@ -838,20 +537,13 @@ __device__ __forceinline__ bool sf_rows_transposed(
                               a[0], a[1], a[2], a[3]);
                     mma16816(ot[db], a, b0, b1);
                 }
-                }
             }
-            if constexpr (EB != 1) {
+            if constexpr (EB == 2) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty0 + 8 * st);
             }
         }
         if (!ok) break;
-        if constexpr (EB == 0)
-#pragma unroll
-            for (int off = 4; off <= 16; off <<= 1) {
-                s[0] += __shfl_xor_sync(kFull, s[0], off);
-                s[1] += __shfl_xor_sync(kFull, s[1], off);
-            }
         // Combine the Tr warps' states through the Q tile (free once every
         // warp has left the chunk loop: the barrier opening each round).
         float* xo = reinterpret_cast<float*>(qreg);
@@ -899,12 +591,8 @@ __device__ __forceinline__ bool sf_rows_transposed(
                     float* dst = p.part_o + (size_t)pid * D;
 #pragma unroll
                     for (int db = 0; db < D / 16; ++db) {
-                        if constexpr (EB == 0) {          // dims 16db + 2g, 16db + 2g + 1
-                            *reinterpret_cast<float2*>(dst + 16 * db + 2 * g) = make_float2(ot[db][r], ot[db][r + 2]);
-                        } else {
-                            dst[16 * db + g] = ot[db][r];
-                            dst[16 * db + g + 8] = ot[db][r + 2];
-                        }
+                        dst[16 * db + g] = ot[db][r];
+                        dst[16 * db + g + 8] = ot[db][r + 2];
                     }
                     if (g == 0) p.part_ms[pid] = make_float2(m[r], s[r]);
                 }
@@ -923,11 +611,11 @@ __device__ __forceinline__ bool sf_rows_transposed(
 // key/value head (head_dim <= 128): it has the transposed few-row path and
 // no single-row sequence-first path; the other variant the reverse.
 template <int C, int D, int EB, bool kRows>
-__global__ void __launch_bounds__(kThreads, EB == 0 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, 2)
 two_phase_attention_kernel(const __grid_constant__ CUtensorMap tmap, const AttnParams p) {
     using SM = Smem<C, D, EB>;
     constexpr int DPL = D / 32;
-    constexpr int BOXES = EB ? D * EB / 128 : 1;   // 128-byte boxes per tile row (fp4: one bulk copy)
+    constexpr int BOXES = D * EB / 128;   // 128-byte boxes per tile row
     // single-row sequence-first work of an fp8 pool with 64-token chunks
     // runs on the tensor cores (sf_chunk_f8_tc), elsewhere on CUDA cores
     constexpr bool kF8Tc = EB == 1 && C == 64 && D == 128;
@@ -976,8 +664,7 @@ two_phase_attention_kernel(const __grid_constant__ CUtensorMap tmap, const AttnP
         // ------------------------------ producer ------------------------------
         if (lane != 0) return;
         // the tensor map's descriptor is fetched while the plan line loads
-        if constexpr (EB != 0)
-            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap)) : "memory");
         if (p.test_stall) {
             // Test hook (ca_sched_inject_stall): wait for stage 0's first
             // phase, which nothing completes since no copy has been issued;
@@ -1103,17 +790,12 @@ two_phase_attention_kernel(const __grid_constant__ CUtensorMap tmap, const AttnP
                 // flight) has been written and the producer has arrived.
                 mbar_expect_tx_only(fb, SM::kStage);
                 const uint32_t dst = smem_u32(stages + (size_t)st * SM::kStage);
-                if constexpr (EB == 0) {
-                    bulk_load(dst, p.kv + (((long long)ch.slot * p.n_layers + p.layer) * HK + head) * SM::kStage,
-                              SM::kStage, fb, pol);
-                } else {
-                    const int rowK = (((ch.slot * p.n_layers + p.layer) * 2 + 0) * HK + head) * C;
-                    const int rowV = rowK + HK * C;
+                const int rowK = (((ch.slot * p.n_layers + p.layer) * 2 + 0) * HK + head) * C;
+                const int rowV = rowK + HK * C;
 #pragma unroll
-                    for (int bx = 0; bx < BOXES; ++bx) {
-                        tma_load_2d(dst + bx * C * 128, &tmap, bx * (128 / EB), rowK, fb, pol);
-                        tma_load_2d(dst + SM::kTile + bx * C * 128, &tmap, bx * (128 / EB), rowV, fb, pol);
-                    }
+                for (int bx = 0; bx < BOXES; ++bx) {
+                    tma_load_2d(dst + bx * C * 128, &tmap, bx * (128 / EB), rowK, fb, pol);
+                    tma_load_2d(dst + SM::kTile + bx * C * 128, &tmap, bx * (128 / EB), rowV, fb, pol);
                 }
                 stage_ntok[st] = min(max(ntok, 0), C);
                 stage_tok0[st] = tok0;
@@ -1212,57 +894,7 @@ two_phase_attention_kernel(const __grid_constant__ CUtensorMap tmap, const AttnP
                 float* xo = reinterpret_cast<float*>(qreg) + (flush & 1) * kConsumerWarps * D;
                 float* xm = xms + (flush & 1) * 2 * kConsumerWarps;
                 float m = -INFINITY, s = 0.f;
-                if constexpr (EB == 0) {
-                    // The query in fragment order: step kk wants dims
-                    // 16kk + 4t .. + 3, held by lane 4kk + t (D = 128) or in
-                    // pairs by lanes 8kk + 2t, + 1 (D = 64).
-                    uint32_t qb[1][D / 16][2];
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        if constexpr (D == 128) {
-                            qb[0][kk][0] = __shfl_sync(kFull, qraw.x, 4 * kk + (lane & 3));
-                            qb[0][kk][1] = __shfl_sync(kFull, qraw.y, 4 * kk + (lane & 3));
-                        } else {
-                            qb[0][kk][0] = __shfl_sync(kFull, qraw.x, 8 * kk + 2 * (lane & 3));
-                            qb[0][kk][1] = __shfl_sync(kFull, qraw.x, 8 * kk + 2 * (lane & 3) + 1);
-                        }
-                    }
-                    float oc[1][D / 16][4];
-#pragma unroll
-                    for (int db = 0; db < D / 16; ++db)
-                        oc[0][db][0] = oc[0][db][1] = oc[0][db][2] = oc[0][db][3] = 0.f;
-                    int st = it % S;
-                    uint32_t ph = (uint32_t)(it / S) & 1u;
-                    for (; L < seg_end; ++L, ++it) {
-                        if (!mbar_wait(full0 + 8 * st, ph)) {
-                            set_status(p.status, CA_ERR_TIMEOUT);
-                            return;
-                        }
-                        const int ntok = stage_ntok[st];
-                        // The tile's C / 16 blocks go to the warps in turn,
-                        // tile after tile (a 16-token tile to one warp).
-                        constexpr int NBLK = C / 16;
-                        const int blk = NBLK == 4 ? w : (w - it * NBLK) & 3;
-                        if (blk < NBLK && blk * 16 < ntok)
-                            sf_chunk_f4_tc<C, D>(stages + (size_t)st * SM::kStage, blk, ntok, qb, p.scale_log2, m, s,
-                                                 oc, lane);
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(empty0 + 8 * st);
-                        if (++st == S) {
-                            st = 0;
-                            ph ^= 1u;
-                        }
-                    }
-#pragma unroll
-                    for (int off = 4; off <= 16; off <<= 1) s += __shfl_xor_sync(kFull, s, off);
-                    // lane (g, 0) holds dims 16db + 2g, + 1
-                    if ((lane & 3) == 0) {
-#pragma unroll
-                        for (int db = 0; db < D / 16; ++db)
-                            *reinterpret_cast<float2*>(xo + w * D + 16 * db + 2 * (lane >> 2)) =
-                                make_float2(oc[0][db][0], oc[0][db][2]);
-                    }
-                } else if constexpr (kF8Tc) {
+                if constexpr (kF8Tc) {
                     // The query in fragment order: lane L holds dims 4L .. 4L + 3,
                     // step kk wants dims 16kk + 4t .. + 3, i.e. lane 4kk + t's.
                     uint32_t qb[8][2];
@@ -1431,17 +1063,7 @@ two_phase_attention_kernel(const __grid_constant__ CUtensorMap tmap, const AttnP
                     const int ntok = stage_ntok[st];
                     const int ctx0 = stage_tok0[st];
                     // an fp8 stage is read as E4M3 bytes, straight into the
-                    // fragments (cf_chunk<..., true>); an fp4 stage is widened
-                    // once for all the warps
-                    if constexpr (EB == 0) {
-                        consumer_sync();
-                        f4_tile_to_f16<C, D>(stages + (size_t)st * SM::kStage, conv, conv + SM::kConvBytes / 2,
-                                             threadIdx.x);
-                        consumer_sync();
-                        if (lane == 0) mbar_arrive(empty0 + 8 * st);
-                        kt = smem_u32(conv);
-                        vt = kt + SM::kConvBytes / 2;
-                    }
+                    // fragments (cf_chunk<..., true>)
                     if constexpr (kSplit) {
                         if (active) {
                             constexpr int kXs = (C / 8) * 4 * 32;     // floats per warp slot
@@ -1461,10 +1083,8 @@ two_phase_attention_kernel(const __grid_constant__ CUtensorMap tmap, const AttnP
                                                             p.scale_log2, m, s, o, lane);
                         }
                     }
-                    if constexpr (EB != 0) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(empty0 + 8 * st);
-                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(empty0 + 8 * st);
                 }
                 // Row sums are per thread so far: reduce over the quad.
 #pragma unroll
@@ -1642,17 +1262,8 @@ void* kernel_ptr(bool rows) {
 // rows: the schedule brings 2..8 query rows per position and key/value head
 // (the few-row variant exists for head_dim <= 128).
 void* pick_kernel(const PoolCfg& c, bool rows = false) {
-    if (kv_elem_bytes(c) == 0) {
-        if (c.head_dim == 128) {
-            if (c.chunk == 64) return kernel_ptr<64, 128, 0>(rows);
-            if (c.chunk == 32) return kernel_ptr<32, 128, 0>(rows);
-            if (c.chunk == 16) return kernel_ptr<16, 128, 0>(rows);
-        } else if (c.head_dim == 64) {
-            if (c.chunk == 64) return kernel_ptr<64, 64, 0>(rows);
-            if (c.chunk == 32) return kernel_ptr<32, 64, 0>(rows);
-            if (c.chunk == 16) return kernel_ptr<16, 64, 0>(rows);
-        }
-    } else if (kv_elem_bytes(c) == 1) {
+    if (c.flags & CA_KV_FP4) return fp4_kernel(c);
+    if (kv_elem_bytes(c) == 1) {
         if (c.head_dim != 128) return nullptr;
         if (c.chunk == 64) return kernel_ptr<64, 128, 1>(rows);
         if (c.chunk == 32) return kernel_ptr<32, 128, 1>(rows);
@@ -1673,16 +1284,18 @@ void* pick_kernel(const PoolCfg& c, bool rows = false) {
 }
 // The kernel's dynamic shared memory (the Smem map above, computed here).
 size_t smem_for(const PoolCfg& c, int stages) {
+    if (c.flags & CA_KV_FP4) return fp4_smem_bytes(c, stages);
     const size_t eb = (size_t)kv_elem_bytes(c), cd = (size_t)c.chunk * c.head_dim;
-    const size_t conv = eb <= 1 ? 2 * cd * 2 : 0;
+    const size_t conv = eb == 1 ? 2 * cd * 2 : 0;
     const size_t qrows = c.head_dim == 256 ? 32 : dev::kQRows;
     const size_t xs = c.head_dim == 256 ? (size_t)2 * dev::kConsumerWarps * (c.chunk / 8) * 4 * 32 * 4 : 0;
-    return (size_t)stages * pair_tile_bytes(c) + conv + xs + qrows * c.head_dim * 2 + 512 +
+    return (size_t)stages * 2 * cd * eb + conv + xs + qrows * c.head_dim * 2 + 512 +
            2 * dev::kMaxStages * 8 + 4 * dev::kRing + 2 * 4 * dev::kMaxStages;
 }
 }  // namespace
 
-// Stages that fit two CTAs per SM (113 KiB each, at most 8).
+// Stages that fit two CTAs per SM (113 KiB each, at most 8); an fp4 pool's
+// kernel runs three.
 int kernel_smem_bytes(const PoolCfg& c, int* n_stages, size_t* bytes) {
     if (!pick_kernel(c)) return CA_ERR_UNSUPPORTED;
     const size_t budget = (c.flags & CA_KV_FP4) ? 75 * 1024 : 113 * 1024;

@@ -124,7 +124,17 @@ void walk_matched(const Pool& p, const int32_t* tokens, int32_t n, std::vector<N
     const int32_t c = p.cfg.chunk;
     const Node* node = &p.root;
     for (int32_t i = 0; i < n / c; ++i) {
-        Node* ch = find_child(p, node, tokens + (size_t)i * c, c, chunk_hash(tokens + (size_t)i * c, c));
+        const int32_t* t = tokens + (size_t)i * c;
+        Node* ch = nullptr;
+        if (node->children.size() <= 2) {       // along a common prompt: comparing costs less than hashing
+            for (Node* x : node->children)
+                if (x->matchable && std::equal(t, t + c, chunk_tokens(p, x))) {
+                    ch = x;
+                    break;
+                }
+        } else {
+            ch = find_child(p, node, t, c, chunk_hash(t, c));
+        }
         if (!ch) break;
         out.push_back(ch);
         node = ch;

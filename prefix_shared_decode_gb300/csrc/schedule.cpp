@@ -206,9 +206,12 @@ constexpr double kCfComputePer16 = 0.2;
 // tile carries m query rows of work on half the bytes of an fp16 tile);
 // swept on GB300 (1.5 .. 2.8) for the fastest calls
 constexpr double kF8CfFactor = 2.0;
-// fp4 pools likewise: a chunk-first tile is widened to fp16 in shared memory
-// first, and a sequence-first one is 9/16 of an fp8 tile's bytes
-constexpr double kF4CfFactor = 3.0;
+// fp4 pools: a chunk-first tile is widened to fp16 in shared memory first, a
+// sequence-first one straight into fragments whatever its rows (up to 8).
+// Swept on GB300 at three CTAs per SM: single rows over a 4096-token prompt
+// 69.6 / 62.2 / 62.4 / 67.6 us at 2 / 3 / 4 / 5; four query tokens over a
+// 1024-token one 50.7 / 44.8 / 42.3 / 39.3 us at 1 / 2 / 3 / 4.
+constexpr double kF4CfFactor = 3.0, kF4CfRowsFactor = 4.0;
 
 // Share of the sequence-first tiles left to the tail queue that CTAs drain
 // dynamically once their static lists are done (absorbs the run-to-run rate
@@ -237,11 +240,11 @@ void build_plan(const Pool& p, const Tables& t, int32_t grid, int32_t q_len, Pla
     const double sf_cost = (RW == 1) ? 1.0 : 1.0 + kCfComputePer16 * ((RW + 15) / 16);
     // An fp8 pool halves a tile's bytes while the chunk-first tensor work per
     // tile stays the same, so against single-row sequence-first tiles (and
-    // only there) a chunk-first tile costs more.
-    const double cf_mult = RW != 1                        ? 1.0
-                           : (p.cfg.flags & CA_KV_FP8) ? kF8CfFactor
-                           : (p.cfg.flags & CA_KV_FP4) ? kF4CfFactor
-                                                       : 1.0;
+    // only there) a chunk-first tile costs more.  An fp4 pool's sequence-first
+    // tiles of up to 8 rows all cost about the same.
+    double cf_mult = 1.0;
+    if (p.cfg.flags & CA_KV_FP4) cf_mult = RW == 1 ? kF4CfFactor : RW <= 8 ? kF4CfRowsFactor : 1.0;
+    else if ((p.cfg.flags & CA_KV_FP8) && RW == 1) cf_mult = kF8CfFactor;
     auto rows_cost = [&](int32_t m_rows) {
         return cf_mult * (1.0 + kCfComputePer16 * ((m_rows + 15) / 16)) / sf_cost;
     };
