@@ -463,9 +463,11 @@ int ca_decode_attention_static_ws(const ca_pool* pool, const ca_sched* sched,
  * A list without a token gives zeros.  An entry past the context's last chunk
  * is skipped and reported as CA_ERR_DEVICE_BOUNDS by ca_sched_device_status.
  *
- * Each call is one kernel on `stream`, which allocates nothing and needs no
- * workspace; calls on one schedule may overlap, and both may be captured into
- * graphs, valid while the schedule is (ca_decode_attention).  q_dev / out_dev
+ * Each call is one kernel on `stream`, which allocates nothing: the attention's
+ * partial results lie in a buffer that the schedule holds.  So, as for the
+ * decode calls, calls on one schedule must not overlap on the GPU (graphs that
+ * recorded them included); calls on different schedules may.  Both may be
+ * captured into graphs, valid while the schedule is (ca_decode_attention).  q_dev / out_dev
  * fp16 [b][n_heads][head_dim], 16-byte aligned.  Errors: CA_ERR_STALE;
  * CA_ERR_INVALID (a schedule without lists, a pool without bounds, top_k < 1,
  * sink + recent > top_k, bad layer, NULL or misaligned pointers);

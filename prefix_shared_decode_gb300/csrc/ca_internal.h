@@ -77,6 +77,7 @@ constexpr int kUnitInts = (int)(sizeof(Unit) / sizeof(int32_t));
 struct PlanLayout {
     size_t chunks, units, seq_perm, pbase, status, counter, chunk_tok0, ctx_len, cta_head;
     size_t list_off, list_slots;   // CA_SCHED_CHUNK_LISTS: each batch row's chunk slots (CSR)
+    size_t list_count, list_count_bytes;   // and a counter per unit of the listed chunks' attention
     size_t total;
 };
 
@@ -227,6 +228,8 @@ struct Sched {
     std::vector<unsigned char> blob;   // host copy of the device plan
     void* dev = nullptr;               // device plan blob
     size_t dev_bytes = 0;
+    void* list_parts = nullptr;        // CA_SCHED_CHUNK_LISTS: partials of the listed chunks' attention
+    size_t list_parts_size = 0;
     // Two pinned staging buffers used in turn for the upload, each with an
     // event marking when its last copy finished, so that building the next
     // context never waits for the GPU (only for a copy two builds back).
@@ -296,7 +299,7 @@ int32_t pool_match(const Pool& p, const int32_t* tokens, int32_t n);
 // schedule.cpp
 int build_tables(const Pool& p, const int64_t* seq_ids, int32_t b, uint32_t flags, Tables& t);
 void build_plan(const Pool& p, const Tables& t, int32_t grid, int32_t q_len, Plan& plan);
-void layout_plan(const Plan& plan, int32_t b, PlanLayout& lay, std::vector<unsigned char>& blob,
+void layout_plan(const Pool& p, const Plan& plan, int32_t b, PlanLayout& lay, std::vector<unsigned char>& blob,
                  const Tables& t);
 void layout_ws(const Plan& plan, const Pool& p, int32_t b, WsLayout& ws);
 
@@ -332,6 +335,7 @@ int launch_read_rows(const Pool& p, void* k, void* v, int32_t total_rows, const 
 // sparse.cu: chunk selection and attention over listed chunks
 int launch_select(const Pool& p, const Sched& s, int32_t layer, const void* q, int32_t top_k, int32_t sink,
                   int32_t recent, int32_t* lists, void* stream);
+size_t list_parts_bytes(const Pool& p);
 int launch_sparse(const Pool& p, const Sched& s, int32_t layer, const void* q, const int32_t* lists, int32_t top_k,
                   void* out, float scale, void* stream);
 

@@ -394,7 +394,7 @@ int ca_build_schedule_ex(ca_pool* pool, const int64_t* seq_ids, int32_t b, int32
         s->seq_ids.assign(seq_ids, seq_ids + b);
         alloc_point(*pool);                 // the plan's vectors may grow below
         build_plan(*pool, s->t, pool->kv ? pool->num_sms : kHostOnlyGrid, q_len, s->plan);
-        layout_plan(s->plan, b, s->layout, s->blob, s->t);
+        layout_plan(*pool, s->plan, b, s->layout, s->blob, s->t);
         layout_ws(s->plan, *pool, b, s->ws);
         if (pool->kv) {
             if (s->dev_bytes < s->blob.size()) {
@@ -406,6 +406,14 @@ int ca_build_schedule_ex(ca_pool* pool, const int64_t* seq_ids, int32_t b, int32
                     return CA_ERR_CUDA;
                 }
                 s->dev_bytes = s->blob.size();
+            }
+            const size_t parts = (flags & CA_SCHED_CHUNK_LISTS) ? list_parts_bytes(*pool) : 0;
+            if (s->list_parts_size < parts) {
+                if (s->list_parts) cudaFree(s->list_parts);
+                s->list_parts = nullptr;
+                s->list_parts_size = 0;
+                if (cudaMalloc(&s->list_parts, parts) != cudaSuccess) return CA_ERR_CUDA;
+                s->list_parts_size = parts;
             }
             st = upload_plan(*s, static_cast<cudaStream_t>(stream));
             if (st) {
@@ -429,6 +437,7 @@ int ca_sched_destroy(ca_sched* sched) {
         if (sched->pinned[i]) cudaFreeHost(sched->pinned[i]);
     }
     if (sched->dev) cudaFree(sched->dev);
+    if (sched->list_parts) cudaFree(sched->list_parts);
     delete sched;
     return CA_OK;
 }
@@ -638,10 +647,12 @@ int ca_sched_device_status(const ca_sched* s, void* stream) {
     int32_t* dev_word = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(s->dev) + s->layout.status);
     if (cudaMemcpy(&word, dev_word, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) return CA_ERR_CUDA;
     if (word != 0) {
-        // A call that stopped early may have left the queue counter
-        // mid-count: clear it with the word.
+        // A call that stopped early may have left the queue counter (or those
+        // of the listed chunks' attention) mid-count: cleared with the word.
         if (cudaMemset(dev_word, 0, sizeof(word)) != cudaSuccess ||
             cudaMemset(static_cast<unsigned char*>(s->dev) + s->layout.counter, 0, sizeof(int32_t)) !=
+                cudaSuccess ||
+            cudaMemset(static_cast<unsigned char*>(s->dev) + s->layout.list_count, 0, s->layout.list_count_bytes) !=
                 cudaSuccess)
             return CA_ERR_CUDA;
     }

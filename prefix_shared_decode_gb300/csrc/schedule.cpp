@@ -543,7 +543,7 @@ namespace {
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 }  // namespace
 
-void layout_plan(const Plan& plan, int32_t b, PlanLayout& lay, std::vector<unsigned char>& blob,
+void layout_plan(const Pool& p, const Plan& plan, int32_t b, PlanLayout& lay, std::vector<unsigned char>& blob,
                  const Tables& t) {
     size_t off = 0;
     lay.chunks = off;    off = align256(off + plan.chunks.size() * sizeof(ChunkRef));
@@ -557,6 +557,11 @@ void layout_plan(const Plan& plan, int32_t b, PlanLayout& lay, std::vector<unsig
     lay.cta_head = off;  off = align256(off + (size_t)plan.grid * sizeof(CtaHead));
     lay.list_off = off;   off = align256(off + t.list_off.size() * sizeof(int32_t));
     lay.list_slots = off; off = align256(off + t.list_slots.size() * sizeof(int32_t));
+    // (units take at least 8 heads of a group, or all of a smaller one)
+    const int32_t HK = kv_heads(p.cfg), G = p.cfg.n_heads / HK;
+    lay.list_count = off;
+    lay.list_count_bytes = t.list_off.empty() ? 0 : (size_t)b * HK * ((G + 7) / 8) * sizeof(int32_t);
+    off = align256(off + lay.list_count_bytes);
     lay.total = off;
     blob.assign(off, 0);
     if (!t.list_off.empty()) {

@@ -15,9 +15,8 @@ namespace ca {
 namespace dev {
 
 // ---------------------------------------------------------------------------
-// Clusters: the CTAs that share one (sequence, key/value head) meet in their
-// shared memories, so neither call needs a workspace, a second kernel or an
-// atomic whose order could change a result.
+// Clusters: the CTAs that score one context's chunks leave their scores in
+// the first one's shared memory.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void cluster_arrive() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -35,20 +34,6 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void st_peer(uint32_t addr, uint32_t v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-__device__ __forceinline__ float ld_peer(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
-__device__ __forceinline__ float4 ld_peer4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-
 // What both kernels read of the schedule and the pool.
 struct ListParams {
     const uint16_t* q;            // fp16 [b][H][D]
@@ -62,7 +47,10 @@ struct ListParams {
     uint16_t* out;
     int32_t n_layers, n_kv_heads, n_heads, group, layer, capacity, top_k;
     int32_t sink, recent;         // selection
-    int32_t n_stages, splits;     // attention: ring stages; both: CTAs per cluster
+    int32_t splits;               // selection: CTAs per cluster
+    int32_t n_stages, n_units;    // attention: ring stages, units
+    int32_t* counters;            // pieces of each unit that have arrived (0 between calls)
+    float* parts;                 // [2 per CTA] (m, s) of the rows, then their outputs
     float scale_log2, out_scale;
 };
 
@@ -629,13 +617,19 @@ struct Frag<0, C, D, NB> {                       // fp4
 };
 
 // ---------------------------------------------------------------------------
-// Attention over listed chunks.  A cluster takes one (sequence, key/value
-// head, up to 8 NB rows of its group); its CTAs take the list's entries in
-// turn.  In a CTA a producer warp looks 32 entries up at once (list -> slot ->
-// token count) and keeps a ring of tiles in flight; four consumer warps take
-// the tiles' blocks of 16 tokens with an online softmax.  At the end the
-// warps' states meet in shared memory, the CTAs' in the cluster's, and every
-// CTA writes its share of the output.
+// Attention over listed chunks.  A unit is one (sequence, key/value head, up to
+// 8 NB rows of its group) with its top_k list entries; the units' entries are
+// laid end to end and cut into equal stretches, one per resident CTA, so every
+// CTA streams the same number of tiles whatever the batch.  (Clusters of up to
+// eight CTAs per unit were measured first: 75 us where this takes 61, 512 units
+// on 456 resident CTAs.)  A producer warp looks 32 entries up at once (list ->
+// slot -> token count) and keeps a ring of tiles in flight, across units; four
+// consumer warps take the tiles' blocks of 16 tokens with an online softmax.
+// A unit cut between CTAs leaves its pieces' partial triples in the schedule's
+// buffer, and the CTA that finishes its last piece (a counter per unit, which
+// it clears again) merges them in the order of the pieces: nothing waits, and
+// results do not depend on the order of arrival.  One warp sees to that while
+// the others go on with the next unit; all four at the end of the stretch.
 // ---------------------------------------------------------------------------
 constexpr int kSpWarps = 4, kSpThreads = 32 * (kSpWarps + 1), kSpStages = 8;
 // The softmax reference is kept 5 below a running maximum and raised only when
@@ -647,35 +641,36 @@ template <int EB, int C, int D, int NB>
 struct SpShared {
     using F = Frag<EB, C, D, NB>;
     static constexpr int kRows = 8 * NB;
-    static constexpr int kMerge = kSpWarps * kRows * D * 4;       // the warps' outputs, in the ring's place
-    static size_t ring(int stages) {
-        const size_t r = (size_t)stages * F::kStage;
-        return r > (size_t)kMerge ? r : (size_t)kMerge;
-    }
-    // stage bars, token counts, (m, s) of the warps and of the CTA
-    static constexpr int kTail = 2 * kSpStages * 8 + kSpStages * 4 + (kSpWarps + 1) * kRows * 2 * 4;
-    static size_t bytes(int stages) { return ring(stages) + kTail; }
+    static constexpr int kRow = D + 4;                            // floats: no bank conflicts between rows
+    static constexpr int kExch = (kSpWarps - 1) * kRows * kRow * 4;   // outputs of warps 1, 2, 3
+    // stage bars, token counts, (m, s) of the warps, a flag
+    static constexpr int kTail = 2 * kSpStages * 8 + kSpStages * 4 + kSpWarps * kRows * 2 * 4 + 16;
+    static constexpr size_t bytes(int stages) { return (size_t)stages * F::kStage + kExch + kTail; }
 };
 
 __device__ __forceinline__ void sp_consumers() { asm volatile("bar.sync 1, %0;" ::"n"(kSpWarps * 32) : "memory"); }
 
+// Entries [first, last) of CTA c when `total` are cut into `grid` stretches.
+__device__ __forceinline__ long long cut_at(long long total, int grid, int c) { return total * c / grid; }
+
 template <int EB, int C, int D, int NB>
-__global__ void __launch_bounds__(kSpThreads, 2)
-sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListParams p, uint32_t ring_bytes) {
+__global__ void __launch_bounds__(kSpThreads, EB == 0 && NB == 1 ? 3 : 2)
+sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListParams p) {
     using F = Frag<EB, C, D, NB>;
     using SM = SpShared<EB, C, D, NB>;
-    constexpr int R = SM::kRows, NBLK = C / 16;
+    constexpr int R = SM::kRows, NBLK = C / 16, RS = SM::kRow;
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + ring_bytes);
+    const int S = p.n_stages;
+    float* exch = reinterpret_cast<float*>(smem + (size_t)S * F::kStage);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(exch) + SM::kExch);
     volatile int32_t* stage_ntok = reinterpret_cast<volatile int32_t*>(bars + 2 * kSpStages);
     float* wms = const_cast<float*>(reinterpret_cast<volatile float*>(stage_ntok + kSpStages));   // [warp][row][m, s]
-    float* cms = wms + kSpWarps * R * 2;                                                           // [row][m, s]
+    volatile int32_t* flag = reinterpret_cast<volatile int32_t*>(wms + kSpWarps * R * 2);
     const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + kSpStages);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int S = p.n_stages, cs = p.splits;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     if ((smem_u32(smem) & 1023u) != 0 || S < 1 || S > kSpStages) {   // the same in every CTA
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         if (threadIdx.x == 0) set_status(p.status, CA_ERR_INVALID);
         return;
     }
@@ -688,100 +683,128 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     __syncthreads();
-    const int rank = blockIdx.x % cs, unit = blockIdx.x / cs;
-    const int G = p.group, RB = (G + R - 1) / R;
-    const int rb = unit % RB, h = (unit / RB) % p.n_kv_heads, i = unit / (RB * p.n_kv_heads);
-    const int rows = min(R, G - rb * R);
-    const int row0 = h * G + rb * R;                       // the CTA's first query head
+    const int G = p.group, RB = (G + R - 1) / R, K = p.top_k, HK = p.n_kv_heads, grid = gridDim.x;
+    const long long total = (long long)p.n_units * K;
+    const long long e0 = cut_at(total, grid, blockIdx.x), e1 = cut_at(total, grid, blockIdx.x + 1);
+    // unit u: row block u % RB of head (u / RB) % HK of batch row u / (RB * HK)
 
     if (warp == kSpWarps) {
         // ------------------------------ producer ------------------------------
-        const int off = p.list_off[i], n = p.list_off[i + 1] - off;
-        const int32_t* list = p.lists + ((size_t)i * p.n_kv_heads + h) * p.top_k;
         const uint64_t pol = policy_evict_first();
-        int it = 0;
+        int st = 0, done = 0;                              // ring slot; slots filled so far
+        uint32_t ph = 1u;                                  // the empty barriers' phase: free at first
         bool ok = true;
-        const int mine = (p.top_k - rank + cs - 1) / cs;   // entries rank, rank + cs, ...
-        for (int base = 0; base < mine && ok; base += 32) {
-            int slot = -1, ntok = 0;
-            if (base + lane < mine) {
-                const int j = list[rank + (size_t)(base + lane) * cs];
-                if (j >= n) {
-                    set_status(p.status, CA_ERR_DEVICE_BOUNDS);
-                } else if (j >= 0) {
-                    slot = p.list_slots[off + j];
-                    if (slot < 0 || slot >= p.capacity) {
+        auto take = [&]() -> bool {                        // lane 0: the next ring slot
+            if (mbar_wait(empty0 + 8 * st, ph)) return true;
+            set_status(p.status, CA_ERR_TIMEOUT);
+            return false;
+        };
+        auto step = [&]() {
+            ++done;
+            if (++st == S) {
+                st = 0;
+                ph ^= 1u;
+            }
+        };
+        for (long long e = e0; e < e1 && ok;) {
+            const int u = (int)(e / K), pair = u / RB, h = pair % HK, i = pair / HK;
+            const int j1 = (int)min((long long)K, e1 - (long long)u * K);
+            const int off = p.list_off[i], n = p.list_off[i + 1] - off;
+            const int32_t* list = p.lists + (size_t)pair * K;
+            // Only a context's last chunk can be partial.  (The schedule's
+            // lists may be read before the dependency wait, as its plan is;
+            // token counts, the caller's lists and the pool after it.)
+            const int end_slot = p.list_slots[off + n - 1];
+            if (e == e0) asm volatile("griddepcontrol.wait;" ::: "memory");
+            const int end_ntok = end_slot >= 0 && end_slot < p.capacity ? min(max(p.slot_ntok[end_slot], 0), C) : 0;
+            for (int j0 = (int)(e - (long long)u * K); j0 < j1 && ok; j0 += 32) {
+                int slot = -1, ntok = 0;
+                if (j0 + lane < j1) {
+                    const int j = list[j0 + lane];
+                    if (j >= n) {
                         set_status(p.status, CA_ERR_DEVICE_BOUNDS);
-                        slot = -1;
-                    } else {
-                        ntok = min(max(p.slot_ntok[slot], 0), C);
+                    } else if (j >= 0) {
+                        slot = p.list_slots[off + j];
+                        if (slot < 0 || slot >= p.capacity) set_status(p.status, CA_ERR_DEVICE_BOUNDS);
+                        else ntok = j == n - 1 ? end_ntok : C;
                     }
                 }
-            }
-            uint32_t todo = __ballot_sync(kFull, ntok > 0);
-            while (todo && ok) {
-                const int src = __ffs(todo) - 1;
-                todo &= todo - 1;
-                const int sl = __shfl_sync(kFull, slot, src), nt = __shfl_sync(kFull, ntok, src);
-                const int st = it % S;
-                if (lane == 0) {
-                    if (!mbar_wait(empty0 + 8 * st, ((uint32_t)(it / S) & 1u) ^ 1u)) {
-                        set_status(p.status, CA_ERR_TIMEOUT);
-                        ok = false;
-                    } else {
-                        const uint32_t fb = full0 + 8 * st, dst = smem_u32(smem) + st * F::kStage;
-                        mbar_expect_tx_only(fb, F::kStage);
-                        if constexpr (EB == 0) {
-                            bulk_load(dst, p.kv + (((long long)sl * p.n_layers + p.layer) * p.n_kv_heads + h) * F::kStage,
-                                      F::kStage, fb, pol);
-                        } else {
-                            const int rowK = (((sl * p.n_layers + p.layer) * 2) * p.n_kv_heads + h) * C;
-                            const int rowV = rowK + p.n_kv_heads * C;
+                uint32_t todo = __ballot_sync(kFull, ntok > 0);
+                while (todo && ok) {
+                    const int src = __ffs(todo) - 1;
+                    todo &= todo - 1;
+                    const int sl = __shfl_sync(kFull, slot, src), nt = __shfl_sync(kFull, ntok, src);
+                    if (lane == 0) {
+                        ok = take();
+                        if (ok) {
+                            const uint32_t fb = full0 + 8 * st, dst = smem_u32(smem) + st * F::kStage;
+                            mbar_expect_tx_only(fb, F::kStage);
+                            if constexpr (EB == 0) {
+                                bulk_load(dst, p.kv + (((long long)sl * p.n_layers + p.layer) * HK + h) * F::kStage,
+                                          F::kStage, fb, pol);
+                            } else {
+                                const int rowK = (((sl * p.n_layers + p.layer) * 2) * HK + h) * C;
+                                const int rowV = rowK + HK * C;
 #pragma unroll
-                            for (int bx = 0; bx < D * EB / 128; ++bx) {
-                                tma_load_2d(dst + bx * C * 128, &tmap, bx * (128 / EB), rowK, fb, pol);
-                                tma_load_2d(dst + F::kStage / 2 + bx * C * 128, &tmap, bx * (128 / EB), rowV, fb, pol);
+                                for (int bx = 0; bx < D * EB / 128; ++bx) {
+                                    tma_load_2d(dst + bx * C * 128, &tmap, bx * (128 / EB), rowK, fb, pol);
+                                    tma_load_2d(dst + F::kStage / 2 + bx * C * 128, &tmap, bx * (128 / EB), rowV, fb,
+                                                pol);
+                                }
                             }
+                            stage_ntok[st] = nt;
+                            mbar_arrive(fb);
                         }
-                        stage_ntok[st] = nt;
-                        mbar_arrive(fb);
                     }
+                    ok = __shfl_sync(kFull, (int)ok, 0) != 0;
+                    if (ok) step();
                 }
-                ok = __shfl_sync(kFull, (int)ok, 0) != 0;
-                it += ok;
             }
-        }
-        if (lane == 0) {
-            const int st = it % S;
-            if (ok && mbar_wait(empty0 + 8 * st, ((uint32_t)(it / S) & 1u) ^ 1u)) {
-                stage_ntok[st] = -1;                       // no more tiles
-                mbar_arrive(full0 + 8 * st);
-            } else {
-                set_status(p.status, CA_ERR_TIMEOUT);
-                // give the copies already issued a bounded chance to land
-                for (int k = (it > S ? it - S : 0); k < it; ++k)
-                    mbar_wait(full0 + 8 * (k % S), (uint32_t)(k / S) & 1u);
+            if (ok && lane == 0) {                         // the piece ends: a slot without data
+                ok = take();
+                if (ok) {
+                    stage_ntok[st] = -1;
+                    mbar_arrive(full0 + 8 * st);
+                }
             }
+            ok = __shfl_sync(kFull, (int)ok, 0) != 0;
+            if (ok) step();
+            e = (long long)u * K + j1;
         }
-        __syncwarp();
-    } else {
-        // ------------------------------ consumers ------------------------------
+        if (!ok && lane == 0)                              // copies in flight get a bounded chance to land
+            for (int k = max(0, done - S); k < done; ++k)
+                mbar_wait(full0 + 8 * (k % S), (uint32_t)(k / S) & 1u);
+        return;
+    }
+
+    // ------------------------------ consumers ------------------------------
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    int st = 0, it = 0;
+    uint32_t ph = 0u;
+    for (long long e = e0; e < e1;) {
+        const int u = (int)(e / K), pair = u / RB, rb = u % RB, h = pair % HK, i = pair / HK;
+        const long long u0 = (long long)u * K, end = min(u0 + K, e1);
+        const bool whole = e == u0 && end == u0 + K;
+        const int rows = min(R, G - rb * R);
+        const size_t row0 = (size_t)i * p.n_heads + h * G + rb * R;      // the unit's first row of q and out
         uint32_t qb[NB][D / 16][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
             const bool there = nb * 8 + g < rows;
-            const uint16_t* q = p.q + ((size_t)i * p.n_heads + row0 + (there ? nb * 8 + g : 0)) * D;
+            const uint16_t* q = p.q + (row0 + (there ? nb * 8 + g : 0)) * D;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-                uint2 x;
-                if constexpr (F::kPair) {
-                    x = *reinterpret_cast<const uint2*>(q + 16 * kk + 4 * t);
-                } else {
-                    x.x = *reinterpret_cast<const uint32_t*>(q + 16 * kk + 2 * t);
-                    x.y = *reinterpret_cast<const uint32_t*>(q + 16 * kk + 2 * t + 8);
+                uint2 x = make_uint2(0u, 0u);
+                if (there) {
+                    if constexpr (F::kPair) {
+                        x = *reinterpret_cast<const uint2*>(q + 16 * kk + 4 * t);
+                    } else {
+                        x.x = *reinterpret_cast<const uint32_t*>(q + 16 * kk + 2 * t);
+                        x.y = *reinterpret_cast<const uint32_t*>(q + 16 * kk + 2 * t + 8);
+                    }
                 }
-                qb[nb][kk][0] = there ? x.x : 0u;
-                qb[nb][kk][1] = there ? x.y : 0u;
+                qb[nb][kk][0] = x.x;
+                qb[nb][kk][1] = x.y;
             }
         }
         float o[NB][D / 16][4], m[NB][2], s[NB][2];
@@ -792,15 +815,13 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
 #pragma unroll
             for (int db = 0; db < D / 16; ++db) o[nb][db][0] = o[nb][db][1] = o[nb][db][2] = o[nb][db][3] = 0.f;
         }
-        int st = 0;
-        uint32_t ph = 0;
-        for (int it = 0;; ++it, st = st + 1 == S ? 0 : st + 1, ph ^= (uint32_t)(st == 0)) {
+        for (bool more = true; more; ++it) {
             if (!mbar_wait(full0 + 8 * st, ph)) {
-                if (lane == 0) set_status(p.status, CA_ERR_TIMEOUT);
-                break;
+                set_status(p.status, CA_ERR_TIMEOUT);
+                return;
             }
             const int ntok = stage_ntok[st];
-            if (ntok < 0) break;
+            more = ntok >= 0;
             // a tile's blocks of 16 tokens go to the warps in turn, tile after tile
             const int blk = NBLK == 4 ? warp : (warp - it * NBLK) & 3;
             if (blk < NBLK && blk * 16 < ntok) {
@@ -813,9 +834,9 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        x[nb][e] = ((e >> 1) ? in1 : in0) ? x[nb][e] * p.scale_log2 : -INFINITY;
-                        grow = grow || x[nb][e] > m[nb][e & 1] + (kSpLift + kSpSlack);
+                    for (int k = 0; k < 4; ++k) {
+                        x[nb][k] = ((k >> 1) ? in1 : in0) ? x[nb][k] * p.scale_log2 : -INFINITY;
+                        grow = grow || x[nb][k] > m[nb][k & 1] + (kSpLift + kSpSlack);
                     }
                 }
                 if (__any_sync(kFull, grow)) {
@@ -840,9 +861,9 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
                 uint32_t pb[NB][2];
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
-                    const float u0 = m[nb][0] == -INFINITY ? 0.f : m[nb][0], u1 = m[nb][1] == -INFINITY ? 0.f : m[nb][1];
-                    const float p0 = ex2(x[nb][0] - u0), p1 = ex2(x[nb][1] - u1);
-                    const float p2 = ex2(x[nb][2] - u0), p3 = ex2(x[nb][3] - u1);
+                    const float u0_ = m[nb][0] == -INFINITY ? 0.f : m[nb][0], u1_ = m[nb][1] == -INFINITY ? 0.f : m[nb][1];
+                    const float p0 = ex2(x[nb][0] - u0_), p1 = ex2(x[nb][1] - u1_);
+                    const float p2 = ex2(x[nb][2] - u0_), p3 = ex2(x[nb][3] - u1_);
                     s[nb][0] += p0 + p2;                   // the lane's tokens; summed over g at the end
                     s[nb][1] += p1 + p3;
                     pb[nb][0] = movm_trans(pack_half2(p0, p1));
@@ -852,79 +873,164 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(empty0 + 8 * st);
+            if (++st == S) {
+                st = 0;
+                ph ^= 1u;
+            }
         }
-        // Every copy has landed and every warp is past its last tile: the ring
-        // takes the warps' outputs, [warp][row][D].
-        sp_consumers();
-        float* ob = reinterpret_cast<float*>(smem);
+        // The warps' states meet: warps 1 to 3 hand theirs to warp 0, which
+        // leaves the sum in the exchange area for all of them to write out.
+        auto put = [&](float* dst) {                       // [row][D] with the rows' stride
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-#pragma unroll
-                for (int d = 4; d <= 16; d <<= 1) s[nb][r] += __shfl_xor_sync(kFull, s[nb][r], d);
-                const int row = nb * 8 + 2 * t + r;
-                if (g == 0) {
-                    wms[(warp * R + row) * 2] = m[nb][r];
-                    wms[(warp * R + row) * 2 + 1] = s[nb][r];
-                }
+            for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int db = 0; db < D / 16; ++db)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        ob[(warp * R + row) * D + F::dim(db, e, g)] = o[nb][db][r + 2 * e];
-            }
+                    for (int k = 0; k < 4; ++k)
+                        dst[(nb * 8 + 2 * t + (k & 1)) * RS + F::dim(db, k >> 1, g)] = o[nb][db][k];
+        };
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int d = 4; d <= 16; d <<= 1) s[nb][r] += __shfl_xor_sync(kFull, s[nb][r], d);
+        sp_consumers();                                    // the last piece has been written out
+        if (warp > 0) {
+            put(exch + (size_t)(warp - 1) * R * RS);
+            if (g == 0)
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        *reinterpret_cast<float2*>(wms + (warp * R + nb * 8 + 2 * t + r) * 2) =
+                            make_float2(m[nb][r], s[nb][r]);
+        }
         sp_consumers();
+        if (warp == 0) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int row = nb * 8 + 2 * t + r;
+                    float2 q[kSpWarps - 1];
+                    float M = m[nb][r];
+#pragma unroll
+                    for (int k = 1; k < kSpWarps; ++k) {
+                        q[k - 1] = *reinterpret_cast<const float2*>(wms + (k * R + row) * 2);
+                        M = fmaxf(M, q[k - 1].x);
+                    }
+                    const float a0 = m[nb][r] == -INFINITY ? 0.f : ex2(m[nb][r] - M);
+                    float sum = s[nb][r] * a0;
+#pragma unroll
+                    for (int db = 0; db < D / 16; ++db) {
+                        o[nb][db][r] *= a0;
+                        o[nb][db][r + 2] *= a0;
+                    }
+#pragma unroll
+                    for (int k = 1; k < kSpWarps; ++k) {
+                        const float ak = q[k - 1].x == -INFINITY ? 0.f : ex2(q[k - 1].x - M);
+                        sum += q[k - 1].y * ak;
+                        const float* src = exch + ((size_t)(k - 1) * R + row) * RS;
+#pragma unroll
+                        for (int db = 0; db < D / 16; ++db) {
+                            o[nb][db][r] += ak * src[F::dim(db, 0, g)];
+                            o[nb][db][r + 2] += ak * src[F::dim(db, 1, g)];
+                        }
+                    }
+                    if (g == 0) *reinterpret_cast<float2*>(wms + row * 2) = make_float2(M, sum);
+                }
+            __syncwarp();
+            put(exch);
+        }
+        sp_consumers();
+        const int c = blockIdx.x;
+        float* part = p.parts + (size_t)(2 * c + (e != e0)) * R * (D + 2);
         for (int idx = threadIdx.x; idx < rows * (D / 4); idx += kSpWarps * 32) {
             const int row = idx / (D / 4), d4 = idx % (D / 4);
-            float M = -INFINITY, sum = 0.f;
-#pragma unroll
-            for (int w = 0; w < kSpWarps; ++w) M = fmaxf(M, wms[(w * R + row) * 2]);
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < kSpWarps; ++w) {
-                const float mw = wms[(w * R + row) * 2];
-                const float wt = mw == -INFINITY ? 0.f : ex2(mw - M);
-                sum += wt * wms[(w * R + row) * 2 + 1];
-                const float4 v = reinterpret_cast<const float4*>(ob + (size_t)(w * R + row) * D)[d4];
-                acc.x += wt * v.x; acc.y += wt * v.y; acc.z += wt * v.z; acc.w += wt * v.w;
-            }
-            if (cs == 1) {
-                const float inv = sum > 0.f ? p.out_scale / sum : 0.f;
-                *reinterpret_cast<uint2*>(p.out + ((size_t)i * p.n_heads + row0 + row) * D + d4 * 4) =
-                    make_uint2(pack_half2(acc.x * inv, acc.y * inv), pack_half2(acc.z * inv, acc.w * inv));
+            const float4 v = reinterpret_cast<const float4*>(exch + row * RS)[d4];
+            const float2 q = *reinterpret_cast<const float2*>(wms + row * 2);
+            if (whole) {
+                const float inv = q.y > 0.f ? p.out_scale / q.y : 0.f;
+                *reinterpret_cast<uint2*>(p.out + (row0 + row) * D + d4 * 4) =
+                    make_uint2(pack_half2(v.x * inv, v.y * inv), pack_half2(v.z * inv, v.w * inv));
             } else {
-                reinterpret_cast<float4*>(ob + (size_t)row * D)[d4] = acc;   // this thread's own place of warp 0's
-                if (d4 == 0) {
-                    cms[row * 2] = M;
-                    cms[row * 2 + 1] = sum;
+                reinterpret_cast<float4*>(part + R * 2)[row * (D / 4) + d4] = v;
+                if (d4 == 0) reinterpret_cast<float2*>(part)[row] = q;
+            }
+        }
+        // Warp 3 sees to a piece that is not a whole unit (the others have
+        // arrived when their stores are out; the ring's slack covers its
+        // detour), with all the others where nothing follows.
+        if (!whole) {
+            const bool over = end == e1;
+            if (warp < kSpWarps - 1) {
+                asm volatile("bar.arrive 2, %0;" ::"n"(kSpWarps * 32) : "memory");
+                if (!over) {
+                    e = end;
+                    continue;
+                }
+            } else {
+                asm volatile("bar.sync 2, %0;" ::"n"(kSpWarps * 32) : "memory");
+            }
+            // the unit's pieces lie in CTAs c0 .. c1; the last to arrive merges
+            int c0 = (int)((u0 * grid) / total), c1 = (int)(((u0 + K - 1) * grid) / total), last = 0;
+            while (cut_at(total, grid, c0 + 1) <= u0) ++c0;
+            while (cut_at(total, grid, c1 + 1) <= u0 + K - 1) ++c1;
+            if (warp == kSpWarps - 1) {
+                if (lane == 0) {
+                    __threadfence();
+                    last = atomicAdd(p.counters + u, 1) == c1 - c0;
+                    if (last) p.counters[u] = 0;
+                    __threadfence();
+                    *flag = last;
+                }
+                last = __shfl_sync(kFull, last, 0);
+            }
+            if (over) {
+                sp_consumers();
+                last = *flag;
+            }
+            if (last) {
+                const int first = over ? threadIdx.x : lane, stride = over ? kSpWarps * 32 : 32;
+                for (int idx = first; idx < rows * (D / 4); idx += stride) {
+                    const int row = idx / (D / 4), d4 = idx % (D / 4);
+                    float M = -INFINITY, sum = 0.f;
+                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                    constexpr int KB = 4;                  // pieces whose loads are in flight together
+                    for (int k0 = c0; k0 <= c1; k0 += KB) {
+                        float2 q[KB];
+                        float4 v[KB];
+                        float mn = M;
+#pragma unroll
+                        for (int k = 0; k < KB; ++k) {
+                            const int cc = min(k0 + k, c1);
+                            const float* src =
+                                p.parts + (size_t)(2 * cc + (cut_at(total, grid, cc) < u0)) * R * (D + 2);
+                            q[k] = __ldcg(reinterpret_cast<const float2*>(src) + row);
+                            v[k] = __ldcg(reinterpret_cast<const float4*>(src + R * 2) + row * (D / 4) + d4);
+                        }
+#pragma unroll
+                        for (int k = 0; k < KB; ++k) mn = fmaxf(mn, q[k].x);
+                        const float mu = mn == -INFINITY ? 0.f : mn, wa = ex2(M - mu);
+                        M = mn;
+                        sum *= wa;
+                        acc.x *= wa; acc.y *= wa; acc.z *= wa; acc.w *= wa;
+#pragma unroll
+                        for (int k = 0; k < KB; ++k) {
+                            const float w = k0 + k <= c1 ? ex2(q[k].x - mu) : 0.f;
+                            sum += q[k].y * w;
+                            acc.x += v[k].x * w; acc.y += v[k].y * w; acc.z += v[k].z * w; acc.w += v[k].w * w;
+                        }
+                    }
+                    const float inv = sum > 0.f ? p.out_scale / sum : 0.f;
+                    *reinterpret_cast<uint2*>(p.out + (row0 + row) * D + d4 * 4) =
+                        make_uint2(pack_half2(acc.x * inv, acc.y * inv), pack_half2(acc.z * inv, acc.w * inv));
                 }
             }
         }
+        e = end;
     }
-    if (cs == 1) return;
-    cluster_sync_all();
-    if (warp < kSpWarps) {
-        const uint32_t ob = smem_u32(smem), ms = smem_u32(cms);
-        for (int idx = rank * kSpWarps * 32 + threadIdx.x; idx < rows * (D / 4); idx += cs * kSpWarps * 32) {
-            const int row = idx / (D / 4), d4 = idx % (D / 4);
-            float M = -INFINITY, sum = 0.f;
-            for (int c = 0; c < cs; ++c) M = fmaxf(M, ld_peer(peer_addr(ms + row * 8, c)));
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int c = 0; c < cs; ++c) {
-                const uint32_t a = peer_addr(ms + row * 8, c);
-                const float mc = ld_peer(a), sc = ld_peer(a + 4);
-                const float wt = mc == -INFINITY ? 0.f : ex2(mc - M);
-                const float4 v = ld_peer4(peer_addr(ob + (uint32_t)(row * D + d4 * 4) * 4u, c));
-                sum += wt * sc;
-                acc.x += wt * v.x; acc.y += wt * v.y; acc.z += wt * v.z; acc.w += wt * v.w;
-            }
-            const float inv = sum > 0.f ? p.out_scale / sum : 0.f;
-            *reinterpret_cast<uint2*>(p.out + ((size_t)i * p.n_heads + row0 + row) * D + d4 * 4) =
-                make_uint2(pack_half2(acc.x * inv, acc.y * inv), pack_half2(acc.z * inv, acc.w * inv));
-        }
-    }
-    cluster_sync_all();                                    // the others may still read this CTA's share
 }
 
 }  // namespace dev
@@ -977,21 +1083,21 @@ int launch(const Pool& p, int kind, const void* fn, unsigned blocks, int cs, int
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = cs > 1 ? 2 : 1;
     if (cudaLaunchKernelExC(&cfg, fn, args) != cudaSuccess) return CA_ERR_CUDA;
     count_launch();
     return CA_OK;
 }
 
-using SparseFn = void (*)(const CUtensorMap, const dev::ListParams, uint32_t);
 struct SparseKernel {
-    SparseFn fn = nullptr;
-    int rows = 0, stage = 0, tail = 0, merge = 0;
+    const void* fn = nullptr;
+    int rows = 0, stage = 0, fixed = 0;      // rows of a unit; bytes of a stage, of the rest
 };
 template <int EB, int C, int D, int NB>
 SparseKernel sparse_of() {
     using SM = dev::SpShared<EB, C, D, NB>;
-    return {dev::sparse_attention_kernel<EB, C, D, NB>, SM::kRows, SM::F::kStage, SM::kTail, SM::kMerge};
+    return {reinterpret_cast<const void*>(&dev::sparse_attention_kernel<EB, C, D, NB>), SM::kRows, SM::F::kStage,
+            (int)SM::bytes(0)};
 }
 // Rows of a group per CTA: 8, or 16 for groups of more (at head_dim 256 the
 // accumulators of 16 rows do not fit the registers).
@@ -1054,20 +1160,27 @@ int launch_sparse(const Pool& p, const Sched& s, int32_t layer, const void* q, c
     const bool quant = (p.cfg.flags & (CA_KV_FP8 | CA_KV_FP4)) != 0;
     a.scale_log2 = scale * 1.4426950408889634f * (quant ? kv_scale_of(p.cfg.k_scale) : 1.f);
     a.out_scale = quant ? kv_scale_of(p.cfg.v_scale) : 1.f;
-    const int units = s.t.b * a.n_kv_heads * ((a.group + k.rows - 1) / k.rows), sms = p.sms;
-    const int most = std::min(top_k, s.t.list_max);        // entries that hold a chunk
-    int cs = 1;
-    while (cs < 8 && units * cs < 2 * sms && cs * 2 <= most) cs *= 2;
-    a.splits = cs;
-    // ring: what two CTAs per SM leave room for (113 KiB each)
+    a.n_units = s.t.b * a.n_kv_heads * ((a.group + k.rows - 1) / k.rows);
+    a.counters = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(s.dev) + s.layout.list_count);
+    a.parts = static_cast<float*>(s.list_parts);
+    // Ring: what the resident CTAs leave room for (three per SM for an fp4
+    // pool's groups of up to 8 heads, two otherwise).
+    const int per_sm = (p.cfg.flags & CA_KV_FP4) && k.rows == 8 ? 3 : 2;
+    const size_t room = (size_t)(per_sm == 3 ? 75 : 113) * 1024;
     int st = dev::kSpStages;
-    while (st > 2 && (size_t)st * k.stage + k.tail > 113 * 1024) --st;
+    while (st > 2 && (size_t)st * k.stage + k.fixed > room) --st;
     a.n_stages = st;
-    uint32_t ring = (uint32_t)std::max(st * k.stage, k.merge);
-    const size_t smem = ring + (size_t)k.tail;
-    void* args[] = {const_cast<unsigned char*>(p.tmap), &a, &ring};
-    return launch(p, 1, reinterpret_cast<const void*>(k.fn), (unsigned)units, cs, dev::kSpThreads, smem, smem, args,
-                  static_cast<cudaStream_t>(stream));
+    const size_t smem = (size_t)st * k.stage + k.fixed;
+    // Two entries per CTA at least: a piece costs its queries, a partial and a place in the merge.
+    const int64_t entries = (int64_t)a.n_units * top_k;
+    const int grid = (int)std::min<int64_t>((int64_t)per_sm * p.sms, (entries + 1) / 2);
+    void* args[] = {const_cast<unsigned char*>(p.tmap), &a};
+    return launch(p, 1, k.fn, (unsigned)grid, 1, dev::kSpThreads, smem, smem, args, static_cast<cudaStream_t>(stream));
+}
+
+size_t list_parts_bytes(const Pool& p) {
+    const int rows = p.cfg.head_dim <= 128 && p.cfg.n_heads / kv_heads(p.cfg) > 8 ? 16 : 8;
+    return (size_t)3 * p.sms * 2 * rows * (p.cfg.head_dim + 2) * sizeof(float);
 }
 
 }  // namespace ca

@@ -225,7 +225,7 @@ def test_lists_of_any_order(torch_cuda):
 
 def test_graph_and_streams(torch_cuda):
     """Both calls captured and replayed over appends in place; the same calls
-    issued on two other streams at once."""
+    issued on two other streams at once, each on a schedule of its own."""
     from prefix_shared_decode_gb300 import select_chunks, sparse_decode_attention
     torch = torch_cuda
     x = Cache(torch, 5, "fp8", 64, 128, 4, 2, [3000, 5003, 64 * 30 + 1])
@@ -256,16 +256,17 @@ def test_graph_and_streams(torch_cuda):
         np.testing.assert_array_equal(lists.cpu().numpy(), want)
         x.check_attention(out.cpu().numpy(), ids, 0, q, want)
     streams = [torch.cuda.Stream() for _ in range(2)]
+    scheds = [x.pool.schedule(ids, chunk_lists=True) for _ in streams]
     got = []
     torch.cuda.synchronize()
     for _ in range(10):
-        for s in streams:
-            a = select_chunks(x.pool, sched, qd, 6, stream=s)
-            got.append((a, sparse_decode_attention(x.pool, sched, qd, a, stream=s)))
+        for s, sc in zip(streams, scheds):
+            a = select_chunks(x.pool, sc, qd, 6, stream=s)
+            got.append((a, sparse_decode_attention(x.pool, sc, qd, a, stream=s)))
     torch.cuda.synchronize()
     for a, o in got:
         assert torch.equal(a, lists) and torch.equal(o, out)
-    assert sched.device_status() == 0
+    assert all(s.device_status() == 0 for s in [sched, *scheds])
 
 
 def test_refusals(torch_cuda, lib):
