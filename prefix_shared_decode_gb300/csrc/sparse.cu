@@ -623,15 +623,20 @@ struct Frag<0, C, D, NB> {                       // fp4
 // CTA streams the same number of tiles whatever the batch.  (Clusters of up to
 // eight CTAs per unit were measured first: 75 us where this takes 61, 512 units
 // on 456 resident CTAs.)  A producer warp looks 32 entries up at once (list ->
-// slot -> token count) and keeps a ring of tiles in flight, across units; four
+// slot -> token count) and keeps a ring of tiles in flight, across units; the
 // consumer warps take the tiles' blocks of 16 tokens with an online softmax.
+// Each ring slot belongs to the warps of one group, a warp per block of a tile.
+// An fp4 tile costs more to widen than to fetch (some 300 issue slots of each
+// SM partition, the ALU's half of them, against 260 for its bytes): three CTAs
+// per SM, 69 us for 512 units of 64 tiles; two of eight warps 69, four of four
+// 70, one of twelve 83.
 // A unit cut between CTAs leaves its pieces' partial triples in the schedule's
 // buffer, and the CTA that finishes its last piece (a counter per unit, which
 // it clears again) merges them in the order of the pieces: nothing waits, and
 // results do not depend on the order of arrival.  One warp sees to that while
 // the others go on with the next unit; all four at the end of the stretch.
 // ---------------------------------------------------------------------------
-constexpr int kSpWarps = 4, kSpThreads = 32 * (kSpWarps + 1), kSpStages = 8;
+constexpr int kSpWarps = 4, kSpThreads = 32 * (kSpWarps + 1), kSpStages = 12;
 // The softmax reference is kept 5 below a running maximum and raised only when
 // a score passes it by 13: the weights stay below 2^13 in their fp16 operand
 // and normal numbers down to 2^-19 (or less) of the largest.
@@ -640,6 +645,8 @@ constexpr float kSpLift = 5.f, kSpSlack = 8.f;
 template <int EB, int C, int D, int NB>
 struct SpShared {
     using F = Frag<EB, C, D, NB>;
+    static constexpr int kGroups = kSpWarps / (C / 16);           // of warps; the ring is a multiple of them
+    static constexpr int kPerSm = EB == 0 && NB == 1 ? 3 : 2;     // resident CTAs
     static constexpr int kRows = 8 * NB;
     static constexpr int kRow = D + 4;                            // floats: no bank conflicts between rows
     static constexpr int kExch = (kSpWarps - 1) * kRows * kRow * 4;   // outputs of warps 1, 2, 3
@@ -654,22 +661,22 @@ __device__ __forceinline__ void sp_consumers() { asm volatile("bar.sync 1, %0;" 
 __device__ __forceinline__ long long cut_at(long long total, int grid, int c) { return total * c / grid; }
 
 template <int EB, int C, int D, int NB>
-__global__ void __launch_bounds__(kSpThreads, EB == 0 && NB == 1 ? 3 : 2)
+__global__ void __launch_bounds__(kSpThreads, SpShared<EB, C, D, NB>::kPerSm)
 sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListParams p) {
     using F = Frag<EB, C, D, NB>;
     using SM = SpShared<EB, C, D, NB>;
-    constexpr int R = SM::kRows, NBLK = C / 16, RS = SM::kRow;
+    constexpr int R = SM::kRows, NBLK = C / 16, RS = SM::kRow, W = kSpWarps, NG = SM::kGroups;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int S = p.n_stages;
     float* exch = reinterpret_cast<float*>(smem + (size_t)S * F::kStage);
     uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(exch) + SM::kExch);
     volatile int32_t* stage_ntok = reinterpret_cast<volatile int32_t*>(bars + 2 * kSpStages);
     float* wms = const_cast<float*>(reinterpret_cast<volatile float*>(stage_ntok + kSpStages));   // [warp][row][m, s]
-    volatile int32_t* flag = reinterpret_cast<volatile int32_t*>(wms + kSpWarps * R * 2);
+    volatile int32_t* flag = reinterpret_cast<volatile int32_t*>(wms + W * R * 2);
     const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + kSpStages);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if ((smem_u32(smem) & 1023u) != 0 || S < 1 || S > kSpStages) {   // the same in every CTA
+    if ((smem_u32(smem) & 1023u) != 0 || S < NG || S > kSpStages || S % NG) {   // the same in every CTA
         asm volatile("griddepcontrol.wait;" ::: "memory");
         if (threadIdx.x == 0) set_status(p.status, CA_ERR_INVALID);
         return;
@@ -677,7 +684,7 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
     if (threadIdx.x == 0) {
         for (int k = 0; k < S; ++k) {
             mbar_init(full0 + 8 * k, 1);
-            mbar_init(empty0 + 8 * k, kSpWarps);
+            mbar_init(empty0 + 8 * k, NBLK);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -688,21 +695,21 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
     const long long e0 = cut_at(total, grid, blockIdx.x), e1 = cut_at(total, grid, blockIdx.x + 1);
     // unit u: row block u % RB of head (u / RB) % HK of batch row u / (RB * HK)
 
-    if (warp == kSpWarps) {
+    if (warp == W) {
         // ------------------------------ producer ------------------------------
         const uint64_t pol = policy_evict_first();
         int st = 0, done = 0;                              // ring slot; slots filled so far
         uint32_t ph = 1u;                                  // the empty barriers' phase: free at first
         bool ok = true;
-        auto take = [&]() -> bool {                        // lane 0: the next ring slot
-            if (mbar_wait(empty0 + 8 * st, ph)) return true;
+        auto take = [&](int slot, uint32_t phase) -> bool {
+            if (mbar_wait(empty0 + 8 * slot, phase)) return true;
             set_status(p.status, CA_ERR_TIMEOUT);
             return false;
         };
-        auto step = [&]() {
-            ++done;
-            if (++st == S) {
-                st = 0;
+        auto step = [&](int n) {
+            done += n;
+            if ((st += n) >= S) {
+                st -= S;
                 ph ^= 1u;
             }
         };
@@ -729,21 +736,25 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
                         else ntok = j == n - 1 ? end_ntok : C;
                     }
                 }
+                // The lanes that hold a tile take the next ring slots in their
+                // order, a third of the ring at a time (one lane at a time was
+                // too slow for 16-token tiles), each waiting for its own.
                 uint32_t todo = __ballot_sync(kFull, ntok > 0);
                 while (todo && ok) {
-                    const int src = __ffs(todo) - 1;
-                    todo &= todo - 1;
-                    const int sl = __shfl_sync(kFull, slot, src), nt = __shfl_sync(kFull, ntok, src);
-                    if (lane == 0) {
-                        ok = take();
-                        if (ok) {
-                            const uint32_t fb = full0 + 8 * st, dst = smem_u32(smem) + st * F::kStage;
+                    const int r = __popc(todo & ((1u << lane) - 1u)), some = min(__popc(todo), max(1, S / 3));
+                    const bool mine = (todo >> lane & 1u) && r < some;
+                    bool good = true;
+                    if (mine) {
+                        const int sl = st + r < S ? st + r : st + r - S;
+                        good = take(sl, st + r < S ? ph : ph ^ 1u);
+                        if (good) {
+                            const uint32_t fb = full0 + 8 * sl, dst = smem_u32(smem) + sl * F::kStage;
                             mbar_expect_tx_only(fb, F::kStage);
                             if constexpr (EB == 0) {
-                                bulk_load(dst, p.kv + (((long long)sl * p.n_layers + p.layer) * HK + h) * F::kStage,
+                                bulk_load(dst, p.kv + (((long long)slot * p.n_layers + p.layer) * HK + h) * F::kStage,
                                           F::kStage, fb, pol);
                             } else {
-                                const int rowK = (((sl * p.n_layers + p.layer) * 2) * HK + h) * C;
+                                const int rowK = (((slot * p.n_layers + p.layer) * 2) * HK + h) * C;
                                 const int rowV = rowK + HK * C;
 #pragma unroll
                                 for (int bx = 0; bx < D * EB / 128; ++bx) {
@@ -752,23 +763,26 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
                                                 pol);
                                 }
                             }
-                            stage_ntok[st] = nt;
+                            stage_ntok[sl] = ntok;
                             mbar_arrive(fb);
                         }
                     }
-                    ok = __shfl_sync(kFull, (int)ok, 0) != 0;
-                    if (ok) step();
+                    ok = __all_sync(kFull, good);
+                    todo &= ~__ballot_sync(kFull, mine);
+                    step(some);
                 }
             }
-            if (ok && lane == 0) {                         // the piece ends: a slot without data
-                ok = take();
-                if (ok) {
-                    stage_ntok[st] = -1;
-                    mbar_arrive(full0 + 8 * st);
+            for (int k = 0; k < NG && ok; ++k) {           // the piece ends: a slot without data for each group
+                if (lane == 0) {
+                    ok = take(st, ph);
+                    if (ok) {
+                        stage_ntok[st] = -1;
+                        mbar_arrive(full0 + 8 * st);
+                    }
                 }
+                ok = __shfl_sync(kFull, (int)ok, 0) != 0;
+                step(1);
             }
-            ok = __shfl_sync(kFull, (int)ok, 0) != 0;
-            if (ok) step();
             e = (long long)u * K + j1;
         }
         if (!ok && lane == 0)                              // copies in flight get a bounded chance to land
@@ -779,8 +793,11 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
 
     // ------------------------------ consumers ------------------------------
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    int st = 0, it = 0;
+    int st = warp / NBLK;                                  // the warp's next slot: its group's
+    const int blk = warp % NBLK;                           // its block of that group's tiles
     uint32_t ph = 0u;
+    // (every piece moves the ring on by its tiles and a slot for each group, so
+    // the groups' turns shift from piece to piece; a group's own slots do not)
     for (long long e = e0; e < e1;) {
         const int u = (int)(e / K), pair = u / RB, rb = u % RB, h = pair % HK, i = pair / HK;
         const long long u0 = (long long)u * K, end = min(u0 + K, e1);
@@ -815,16 +832,14 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
 #pragma unroll
             for (int db = 0; db < D / 16; ++db) o[nb][db][0] = o[nb][db][1] = o[nb][db][2] = o[nb][db][3] = 0.f;
         }
-        for (bool more = true; more; ++it) {
+        for (bool more = true; more;) {
             if (!mbar_wait(full0 + 8 * st, ph)) {
                 set_status(p.status, CA_ERR_TIMEOUT);
                 return;
             }
             const int ntok = stage_ntok[st];
             more = ntok >= 0;
-            // a tile's blocks of 16 tokens go to the warps in turn, tile after tile
-            const int blk = NBLK == 4 ? warp : (warp - it * NBLK) & 3;
-            if (blk < NBLK && blk * 16 < ntok) {
+            if (blk * 16 < ntok) {
                 const uint8_t* tile = smem + (size_t)st * F::kStage;
                 float x[NB][4];
                 F::scores(tile, blk, qb, x, lane);
@@ -873,13 +888,14 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(empty0 + 8 * st);
-            if (++st == S) {
-                st = 0;
+            if ((st += NG) >= S) {
+                st -= S;
                 ph ^= 1u;
             }
         }
         // The warps' states meet: warps 1 to 3 hand theirs to warp 0, which
-        // leaves the sum in the exchange area for all of them to write out.
+        // leaves the sum in the exchange area for all of them to write out
+        // (three copies there leave room for a third tile of 32 KB).
         auto put = [&](float* dst) {                       // [row][D] with the rows' stride
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
@@ -895,7 +911,7 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
             for (int r = 0; r < 2; ++r)
 #pragma unroll
                 for (int d = 4; d <= 16; d <<= 1) s[nb][r] += __shfl_xor_sync(kFull, s[nb][r], d);
-        sp_consumers();                                    // the last piece has been written out
+        sp_consumers();                                 // the last piece has been written out
         if (warp > 0) {
             put(exch + (size_t)(warp - 1) * R * RS);
             if (g == 0)
@@ -913,10 +929,10 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const int row = nb * 8 + 2 * t + r;
-                    float2 q[kSpWarps - 1];
+                    float2 q[W - 1];
                     float M = m[nb][r];
 #pragma unroll
-                    for (int k = 1; k < kSpWarps; ++k) {
+                    for (int k = 1; k < W; ++k) {
                         q[k - 1] = *reinterpret_cast<const float2*>(wms + (k * R + row) * 2);
                         M = fmaxf(M, q[k - 1].x);
                     }
@@ -928,7 +944,7 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
                         o[nb][db][r + 2] *= a0;
                     }
 #pragma unroll
-                    for (int k = 1; k < kSpWarps; ++k) {
+                    for (int k = 1; k < W; ++k) {
                         const float ak = q[k - 1].x == -INFINITY ? 0.f : ex2(q[k - 1].x - M);
                         sum += q[k - 1].y * ak;
                         const float* src = exch + ((size_t)(k - 1) * R + row) * RS;
@@ -946,7 +962,7 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
         sp_consumers();
         const int c = blockIdx.x;
         float* part = p.parts + (size_t)(2 * c + (e != e0)) * R * (D + 2);
-        for (int idx = threadIdx.x; idx < rows * (D / 4); idx += kSpWarps * 32) {
+        for (int idx = threadIdx.x; idx < rows * (D / 4); idx += W * 32) {
             const int row = idx / (D / 4), d4 = idx % (D / 4);
             const float4 v = reinterpret_cast<const float4*>(exch + row * RS)[d4];
             const float2 q = *reinterpret_cast<const float2*>(wms + row * 2);
@@ -959,25 +975,25 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
                 if (d4 == 0) reinterpret_cast<float2*>(part)[row] = q;
             }
         }
-        // Warp 3 sees to a piece that is not a whole unit (the others have
+        // The last warp sees to a piece that is not a whole unit (the others have
         // arrived when their stores are out; the ring's slack covers its
         // detour), with all the others where nothing follows.
         if (!whole) {
             const bool over = end == e1;
-            if (warp < kSpWarps - 1) {
-                asm volatile("bar.arrive 2, %0;" ::"n"(kSpWarps * 32) : "memory");
+            if (warp < W - 1) {
+                asm volatile("bar.arrive 2, %0;" ::"n"(W * 32) : "memory");
                 if (!over) {
                     e = end;
                     continue;
                 }
             } else {
-                asm volatile("bar.sync 2, %0;" ::"n"(kSpWarps * 32) : "memory");
+                asm volatile("bar.sync 2, %0;" ::"n"(W * 32) : "memory");
             }
             // the unit's pieces lie in CTAs c0 .. c1; the last to arrive merges
             int c0 = (int)((u0 * grid) / total), c1 = (int)(((u0 + K - 1) * grid) / total), last = 0;
             while (cut_at(total, grid, c0 + 1) <= u0) ++c0;
             while (cut_at(total, grid, c1 + 1) <= u0 + K - 1) ++c1;
-            if (warp == kSpWarps - 1) {
+            if (warp == W - 1) {
                 if (lane == 0) {
                     __threadfence();
                     last = atomicAdd(p.counters + u, 1) == c1 - c0;
@@ -992,7 +1008,7 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
                 last = *flag;
             }
             if (last) {
-                const int first = over ? threadIdx.x : lane, stride = over ? kSpWarps * 32 : 32;
+                const int first = over ? threadIdx.x : lane, stride = over ? W * 32 : 32;
                 for (int idx = first; idx < rows * (D / 4); idx += stride) {
                     const int row = idx / (D / 4), d4 = idx % (D / 4);
                     float M = -INFINITY, sum = 0.f;
@@ -1092,12 +1108,13 @@ int launch(const Pool& p, int kind, const void* fn, unsigned blocks, int cs, int
 struct SparseKernel {
     const void* fn = nullptr;
     int rows = 0, stage = 0, fixed = 0;      // rows of a unit; bytes of a stage, of the rest
+    int groups = 0, per_sm = 0;              // the ring's slots come in multiples of `groups`; CTAs per SM
 };
 template <int EB, int C, int D, int NB>
 SparseKernel sparse_of() {
     using SM = dev::SpShared<EB, C, D, NB>;
     return {reinterpret_cast<const void*>(&dev::sparse_attention_kernel<EB, C, D, NB>), SM::kRows, SM::F::kStage,
-            (int)SM::bytes(0)};
+            (int)SM::bytes(0), SM::kGroups, SM::kPerSm};
 }
 // Rows of a group per CTA: 8, or 16 for groups of more (at head_dim 256 the
 // accumulators of 16 rows do not fit the registers).
@@ -1163,17 +1180,15 @@ int launch_sparse(const Pool& p, const Sched& s, int32_t layer, const void* q, c
     a.n_units = s.t.b * a.n_kv_heads * ((a.group + k.rows - 1) / k.rows);
     a.counters = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(s.dev) + s.layout.list_count);
     a.parts = static_cast<float*>(s.list_parts);
-    // Ring: what the resident CTAs leave room for (three per SM for an fp4
-    // pool's groups of up to 8 heads, two otherwise).
-    const int per_sm = (p.cfg.flags & CA_KV_FP4) && k.rows == 8 ? 3 : 2;
-    const size_t room = (size_t)(per_sm == 3 ? 75 : 113) * 1024;
-    int st = dev::kSpStages;
-    while (st > 2 && (size_t)st * k.stage + k.fixed > room) --st;
+    // Ring: what the resident CTAs (two or three per SM) leave room for.
+    const size_t room = (size_t)(k.per_sm == 2 ? 113 : 75) * 1024;
+    int st = dev::kSpStages / k.groups * k.groups;
+    while (st > k.groups && (size_t)st * k.stage + k.fixed > room) st -= k.groups;
     a.n_stages = st;
     const size_t smem = (size_t)st * k.stage + k.fixed;
     // Two entries per CTA at least: a piece costs its queries, a partial and a place in the merge.
     const int64_t entries = (int64_t)a.n_units * top_k;
-    const int grid = (int)std::min<int64_t>((int64_t)per_sm * p.sms, (entries + 1) / 2);
+    const int grid = (int)std::min<int64_t>((int64_t)k.per_sm * p.sms, (entries + 1) / 2);
     void* args[] = {const_cast<unsigned char*>(p.tmap), &a};
     return launch(p, 1, k.fn, (unsigned)grid, 1, dev::kSpThreads, smem, smem, args, static_cast<cudaStream_t>(stream));
 }
