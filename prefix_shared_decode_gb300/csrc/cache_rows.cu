@@ -67,15 +67,13 @@ __global__ void __launch_bounds__(kRowThreads) fp4_store_kernel(const __grid_con
         __syncthreads();
     }
     constexpr int NB = D / 16;                       // blocks per row
-    const int half = c.n_rows * NB;                  // K's blocks, then V's
-    for (int i = threadIdx.x; i < 2 * half; i += kRowThreads) {
-        const bool isv = i >= half;
-        const int r = (isv ? i - half : i) / NB, blk = i % NB;
+    uint8_t* dst = a.pool + (((long long)c.slot * a.n_layers + at.l) * a.n_heads + at.h) * T::kBytes;
+    // one block of a row: its codes, two to a byte, and its scale
+    auto quantise = [&](const uint16_t* rows, int r, int blk, float mul, uint32_t (&b)[8]) -> uint32_t {
         const long long src = (((long long)at.l * a.total_rows + c.src_row + r) * a.n_heads + at.h) * D + blk * 16;
-        const uint4* p = reinterpret_cast<const uint4*>((isv ? a.v : a.k) + src);
+        const uint4* p = reinterpret_cast<const uint4*>(rows + src);
         const uint4 x0 = __ldcs(p), x1 = __ldcs(p + 1);
         const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-        const float mul = isv ? a.v_mul : a.k_mul;
         float y[16], top = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -88,36 +86,64 @@ __global__ void __launch_bounds__(kRowThreads) fp4_store_kernel(const __grid_con
         const uint32_t sh = f16x2_from_e4m3x2(sc);
         const float s = __low2float(*reinterpret_cast<const __half2*>(&sh));
         const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
-        uint32_t b[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) b[j] = e2m1x2_from_f32(y[2 * j] * inv, y[2 * j + 1] * inv);
-        const int tok = c.dst_row + r;
-        if (!isv) {
+        return sc;
+    };
+    for (int i = threadIdx.x; i < c.n_rows * NB; i += kRowThreads) {
+        const int r = i / NB, blk = i % NB, tok = c.dst_row + r;
+        uint32_t b[8];
+        tile[T::kKScales + f4_k_scale<D>(tok, blk)] = (uint8_t)quantise(a.k, r, blk, a.k_mul, b);
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-                *reinterpret_cast<uint16_t*>(tile + f4_k_byte<D>(tok, blk * 16 + 4 * t)) =
-                    (uint16_t)(b[2 * t] | (b[2 * t + 1] << 8));
-            tile[T::kKScales + f4_k_scale<D>(tok, blk)] = (uint8_t)sc;
-        } else {
+        for (int t = 0; t < 4; ++t)
+            *reinterpret_cast<uint16_t*>(tile + f4_k_byte<D>(tok, blk * 16 + 4 * t)) =
+                (uint16_t)(b[2 * t] | (b[2 * t + 1] << 8));
+    }
+    // Values: a thread takes a pair of tokens' block.  A token that is not among
+    // the new rows keeps what the pool holds (nothing, in a new chunk).
+    const int z = c.dst_row + c.n_rows;
+    for (int i = threadIdx.x; i < C / 2 * NB; i += kRowThreads) {
+        const int pair = i / NB, blk = i % NB, tok = (pair >> 2) * 8 + (pair & 3);
+        const bool has0 = tok >= c.dst_row && tok < z, has1 = tok + 4 >= c.dst_row && tok + 4 < z;
+        if (!has0 && !has1) continue;
+        uint32_t b0[8], b1[8];
+        if (has0) tile[T::kVScales + f4_v_scale<D>(tok, blk)] = (uint8_t)quantise(a.v, tok - c.dst_row, blk, a.v_mul, b0);
+        if (has1)
+            tile[T::kVScales + f4_v_scale<D>(tok + 4, blk)] =
+                (uint8_t)quantise(a.v, tok + 4 - c.dst_row, blk, a.v_mul, b1);
 #pragma unroll
-            for (int g = 0; g < 8; ++g) tile[T::kVCodes + f4_v_byte<D>(tok, blk * 16 + 2 * g)] = (uint8_t)b[g];
-            tile[T::kVScales + f4_v_scale<D>(tok, blk)] = (uint8_t)sc;
+        for (int g = 0; g < 8; ++g) {
+            const int at0 = T::kVCodes + f4_v_byte<D>(pair, blk * 16 + 2 * g), at1 = at0 + D / 16;
+            uint32_t x, y;                            // dims 2g, 2g + 1: (tok, tok + 4)
+            if (has0 && has1) {
+                x = (b0[g] & 15u) | (b1[g] << 4);
+                y = (b0[g] >> 4) | (b1[g] & 0xf0u);
+            } else {
+                const uint32_t ox = c.dst_row ? dst[at0] : 0u, oy = c.dst_row ? dst[at1] : 0u;
+                x = has0 ? (b0[g] & 15u) | (ox & 0xf0u) : (ox & 15u) | (b1[g] << 4);
+                y = has0 ? (b0[g] >> 4) | (oy & 0xf0u) : (oy & 15u) | (b1[g] & 0xf0u);
+            }
+            tile[at0] = (uint8_t)x;
+            tile[at1] = (uint8_t)y;
         }
     }
     __syncthreads();
-    uint8_t* dst = a.pool + (((long long)c.slot * a.n_layers + at.l) * a.n_heads + at.h) * T::kBytes;
     if (c.dst_row == 0) {
         for (int i = threadIdx.x; i < T::kBytes / 16; i += kRowThreads)
             reinterpret_cast<uint4*>(dst)[i] = reinterpret_cast<const uint4*>(tile)[i];
         return;
     }
-    // the new rows alone: code rows in 16-byte pieces, then the scales
-    constexpr int RP = D / 32;
-    for (int i = threadIdx.x; i < 2 * c.n_rows * RP; i += kRowThreads) {
-        const int r = i / RP % c.n_rows, piece = i % RP;
-        const int off = (i < c.n_rows * RP) ? f4_row(c.dst_row + r) * (D / 2)
-                                            : T::kVCodes + (c.dst_row + r) * (D / 2);
-        reinterpret_cast<uint4*>(dst + off)[piece] = reinterpret_cast<const uint4*>(tile + off)[piece];
+    // the new rows alone: key rows and pairs of value rows in 16-byte pieces,
+    // then the scales
+    for (int i = threadIdx.x; i < c.n_rows * (D / 32); i += kRowThreads) {
+        const int off = f4_row(c.dst_row + i / (D / 32)) * (D / 2) + i % (D / 32) * 16;
+        *reinterpret_cast<uint4*>(dst + off) = *reinterpret_cast<const uint4*>(tile + off);
+    }
+    for (int i = threadIdx.x; i < C / 2 * (D / 16); i += kRowThreads) {
+        const int pair = i / (D / 16), tok = (pair >> 2) * 8 + (pair & 3);
+        if (!(tok >= c.dst_row && tok < z) && !(tok + 4 >= c.dst_row && tok + 4 < z)) continue;
+        const int off = T::kVCodes + i * 16;
+        *reinterpret_cast<uint4*>(dst + off) = *reinterpret_cast<const uint4*>(tile + off);
     }
     for (int i = threadIdx.x; i < 2 * c.n_rows * NB; i += kRowThreads) {
         const int r = i / NB % c.n_rows, blk = i % NB;
@@ -253,8 +279,11 @@ __global__ void __launch_bounds__(kRowThreads) read_rows_kernel(const __grid_con
                 sc = tile[T::kKScales + f4_k_scale<D>(tok, blk)];
             } else {
 #pragma unroll
-                for (int g = 0; g < 8; ++g)
-                    w[g] = f16x2_from_e2m1x2(tile[T::kVCodes + f4_v_byte<D>(tok, blk * 16 + 2 * g)]);
+                for (int g = 0; g < 8; ++g) {
+                    const uint8_t* b = tile + T::kVCodes + f4_v_byte<D>(f4_pair(tok), blk * 16 + 2 * g);
+                    const int nib = tok & 4;
+                    w[g] = f16x2_from_e2m1x2((b[0] >> nib & 15u) | (b[D / 16] >> nib << 4));
+                }
                 sc = tile[T::kVScales + f4_v_scale<D>(tok, blk)];
             }
             const uint32_t s2 = f16x2_from_e4m3x2(sc * 0x101u);

@@ -18,13 +18,14 @@
 //    kk are D/8 consecutive bytes, each byte a pair of adjacent columns (the
 //    columns are permuted inside a step; the query fragments take the same
 //    order).
-//  * V (operand A of O^T += V^T p: rows dims, columns tokens).  Row = token;
-//    dim 16 db + 2g + h is byte db of unit g, nibble h: a lane's D/8 dims of a
-//    token are D/16 consecutive bytes.  Fragment columns 2t, 2t + 1, 2t + 8,
-//    2t + 9 are tokens t, t + 4, t + 8, t + 12 (the order in which S^T's rows
-//    reach the operand p); two tokens' words are interleaved by nibble masks
-//    into bytes that hold one dim of both.  At D = 128 unit g of a row sits
-//    at g ^ 4 when bit 1 of the token is set (two rows share 128 bytes).
+//  * V (operand A of O^T += V^T p: rows dims, columns tokens).  Fragment
+//    columns 2t, 2t + 1, 2t + 8, 2t + 9 are tokens t, t + 4, t + 8, t + 12 (the
+//    order in which S^T's rows reach the operand p), so tokens x and x + 4 of
+//    each 8 share bytes, low and high nibble: a byte converts to a fragment
+//    register's pair.  Row = pair of tokens, D bytes; in it unit g holds dims
+//    16 db + 2g of all db, then dims 16 db + 2g + 1: a lane's dims of both
+//    tokens are D/8 consecutive bytes.  Unit g of a row sits at
+//    f4_v_unit(row, g), which keeps the loads of four rows apart.
 //  * K scales: row m, one byte per step kk.
 //  * V scales: tokens x and x + 4 (and x + 8, x + 12) paired, [pair][db][2],
 //    so that 16 bits convert to the pair of scales that a fragment register's
@@ -58,13 +59,15 @@ template <int D>
 __host__ __device__ constexpr int f4_k_byte(int tok, int d) {
     return f4_row(tok) * (D / 2) + ((d & 15) >> 2) * (D / 8) + (d >> 4) * 2 + ((d & 3) >> 1);
 }
+// Values: the row of a token's pair, and the byte of its dim d in the array.
+__host__ __device__ constexpr int f4_pair(int tok) { return (tok >> 3) * 4 + (tok & 3); }
 template <int D>
-__host__ __device__ constexpr int f4_v_unit(int tok, int g) {
-    return D == 128 ? (g ^ ((tok & 2) << 1)) : g;
+__host__ __device__ constexpr int f4_v_unit(int pair, int g) {
+    return D == 128 ? (g ^ ((pair & 3) << 1)) : (g ^ ((pair & 2) << 1));
 }
 template <int D>
-__host__ __device__ constexpr int f4_v_byte(int tok, int d) {
-    return tok * (D / 2) + f4_v_unit<D>(tok, (d & 15) >> 1) * (D / 16) + (d >> 4);
+__host__ __device__ constexpr int f4_v_byte(int pair, int d) {
+    return pair * D + f4_v_unit<D>(pair, (d & 15) >> 1) * (D / 8) + (d & 1) * (D / 16) + (d >> 4);
 }
 template <int D>
 __host__ __device__ constexpr int f4_k_scale(int tok, int blk) {
@@ -72,7 +75,7 @@ __host__ __device__ constexpr int f4_k_scale(int tok, int blk) {
 }
 template <int D>
 __host__ __device__ constexpr int f4_v_scale(int tok, int blk) {
-    return (tok & ~15) * (D / 16) + ((((tok >> 3) & 1) * 4 + (tok & 3)) * (D / 16) + blk) * 2 + ((tok >> 2) & 1);
+    return (f4_pair(tok) * (D / 16) + blk) * 2 + ((tok >> 2) & 1);
 }
 
 // Two E2M1 codes (low nibble first) as an fp16 pair.
@@ -188,27 +191,22 @@ __device__ __forceinline__ void f4_pv(const uint8_t* tile, int blk, const uint32
                                       float (&o)[NB][D / 16][4], int lane) {
     using T = F4Tile<C, D>;
     const int g = lane >> 2, t = lane & 3;
-    const int tok = blk * 16 + t;
-    const uint8_t* vc = tile + T::kVCodes + tok * (D / 2) + f4_v_unit<D>(t, g) * (D / 16);
-    const uint8_t* vs = tile + T::kVScales + blk * 16 * (D / 16) + t * (D / 8);
+    // pairs (t, t + 4) and (t + 8, t + 12) of the block: rows 8 blk + t and 4 on
+    const uint8_t* vc = tile + T::kVCodes + (blk * 8 + t) * D + f4_v_unit<D>(t, g) * (D / 8);
+    const uint8_t* vs = tile + T::kVScales + (blk * 8 + t) * (D / 8);
     constexpr int NW = D / 64;
-    uint32_t wa[NW], wb[NW], wc[NW], wd[NW], sab[D / 32], scd[D / 32];
-    lds_words<NW>(vc, wa);
-    lds_words<NW>(vc + 4 * (D / 2), wb);
-    lds_words<NW>(vc + 8 * (D / 2), wc);
-    lds_words<NW>(vc + 12 * (D / 2), wd);
+    uint32_t ab[2 * NW], cd[2 * NW], sab[D / 32], scd[D / 32];
+    lds_words<2 * NW>(vc, ab);                            // dims 16 db + 2g: words 0 .. NW - 1, then + 1
+    lds_words<2 * NW>(vc + 4 * D, cd);
     lds_words<D / 32>(vs, sab);
     lds_words<D / 32>(vs + 4 * (D / 8), scd);
 #pragma unroll
     for (int i = 0; i < NW; ++i) {                        // four blocks of dims per word
-        const uint32_t lo = 0x0f0f0f0fu, hi = 0xf0f0f0f0u;
-        const uint32_t e0 = (wa[i] & lo) | ((wb[i] << 4) & hi), e1 = ((wa[i] >> 4) & lo) | (wb[i] & hi);
-        const uint32_t e2 = (wc[i] & lo) | ((wd[i] << 4) & hi), e3 = ((wc[i] >> 4) & lo) | (wd[i] & hi);
         uint32_t v0[4], v1[4], v2[4], v3[4];
-        f16x2_from_e2m1x8(e0, v0);
-        f16x2_from_e2m1x8(e1, v1);
-        f16x2_from_e2m1x8(e2, v2);
-        f16x2_from_e2m1x8(e3, v3);
+        f16x2_from_e2m1x8(ab[i], v0);
+        f16x2_from_e2m1x8(ab[NW + i], v1);
+        f16x2_from_e2m1x8(cd[i], v2);
+        f16x2_from_e2m1x8(cd[NW + i], v3);
 #pragma unroll
         for (int j2 = 0; j2 < 2; ++j2) {
             uint32_t x[2], y[2];

@@ -188,9 +188,9 @@ __device__ __forceinline__ bool f4_tiles_own(F4Ctx& c, int tiles, const uint32_t
 
 // The tile widened once for all warps, into the fp16 K and V tiles that the
 // 16-row blocks read (code * scale is exact in fp16).  A thread takes 16 bytes
-// (8 at D = 64) of a row's key codes: four dims of every 16, and 8 (4) bytes
-// of a token's value codes: two dims of every 16; consecutive threads take
-// rows whose swizzled 16-byte columns differ.
+// (8 at D = 64) of a row's key codes: four dims of every 16, and as many of a
+// pair's value codes: two dims of every 16 of both tokens; consecutive threads
+// take rows whose swizzled 16-byte columns differ.
 template <int C, int D>
 __device__ __forceinline__ void f4_tile_to_f16(const uint8_t* src, uint8_t* kd, uint8_t* vd, int tid) {
     using T = F4Tile<C, D>;
@@ -215,28 +215,29 @@ __device__ __forceinline__ void f4_tile_to_f16(const uint8_t* src, uint8_t* kd, 
                 make_uint2(mul_f16x2(x[2], sb), mul_f16x2(x[3], sb));
         }
     }
-    for (int i = tid; i < C * 8; i += kF4Warps * 32) {
-        const int g = i & 7, r = i >> 3;
-        // four rows of a warp: tokens 0 2 4 6, then 1 3 5 7 of each 8
-        const int tok = (r & ~7) | ((r & 3) << 1) | ((r >> 2) & 1);
-        uint32_t w[D / 64], sc[D / 32];
-        lds_words<D / 64>(src + T::kVCodes + tok * (D / 2) + f4_v_unit<D>(tok, g) * (D / 16), w);
-        // the scale pairs of the token and its partner 4 on (or before)
-        lds_words<D / 32>(src + T::kVScales + (f4_v_scale<D>(tok, 0) & ~1), sc);
-        const uint32_t pick = (tok & 4) ? 0x3232u : 0x1010u;
+    for (int i = tid; i < C * 4; i += kF4Warps * 32) {
+        // four pairs of tokens a warp: (0, 4), (1, 5), ... of each 8; their rows
+        // two apart in turn
+        const int g = i & 7, q = i >> 3, pair = (q & ~3) | ((q & 1) << 1) | ((q >> 1) & 1);
+        const int tok = (pair >> 2) * 8 + (pair & 3);
+        uint32_t w[D / 32], sc[D / 32];
+        lds_words<D / 32>(src + T::kVCodes + pair * D + f4_v_unit<D>(pair, g) * (D / 8), w);
+        lds_words<D / 32>(src + T::kVScales + pair * (D / 8), sc);
 #pragma unroll
         for (int i4 = 0; i4 < D / 64; ++i4) {
-            uint32_t x[4];
+            uint32_t x[4], y[4];
             f16x2_from_e2m1x8(w[i4], x);
+            f16x2_from_e2m1x8(w[D / 64 + i4], y);
 #pragma unroll
             for (int j2 = 0; j2 < 2; ++j2) {
                 uint32_t h[2];
                 f16x2_from_e4m3x4(sc[2 * i4 + j2], h);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int db = 4 * i4 + 2 * j2 + e;
-                    *reinterpret_cast<uint32_t*>(vd + swz(tok, 2 * db + (g >> 2), C) + 4 * (g & 3)) =
-                        mul_f16x2(x[2 * j2 + e], __byte_perm(h[e], 0u, pick));
+                    const int k = 2 * j2 + e, kc = 2 * (4 * i4 + k) + (g >> 2), off = 4 * (g & 3);
+                    const uint32_t a = mul_f16x2(x[k], h[e]), b = mul_f16x2(y[k], h[e]);   // (tok, tok + 4)
+                    *reinterpret_cast<uint32_t*>(vd + swz(tok, kc, C) + off) = __byte_perm(a, b, 0x5410);
+                    *reinterpret_cast<uint32_t*>(vd + swz(tok + 4, kc, C) + off) = __byte_perm(a, b, 0x7632);
                 }
             }
         }
