@@ -68,12 +68,18 @@ __global__ void __launch_bounds__(kRowThreads) fp4_store_kernel(const __grid_con
     }
     constexpr int NB = D / 16;                       // blocks per row
     uint8_t* dst = a.pool + (((long long)c.slot * a.n_layers + at.l) * a.n_heads + at.h) * T::kBytes;
-    // one block of a row: its codes, two to a byte, and its scale
-    auto quantise = [&](const uint16_t* rows, int r, int blk, float mul, uint32_t (&b)[8]) -> uint32_t {
+    // A thread takes one block of two tokens that share value bytes (x and
+    // x + 4), keys and values: all 128 bytes are on their way before the first
+    // is looked at.
+    struct Block { uint4 a, b; };
+    auto fetch = [&](const uint16_t* rows, int r, int blk) -> Block {
         const long long src = (((long long)at.l * a.total_rows + c.src_row + r) * a.n_heads + at.h) * D + blk * 16;
         const uint4* p = reinterpret_cast<const uint4*>(rows + src);
-        const uint4 x0 = __ldcs(p), x1 = __ldcs(p + 1);
-        const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+        return {__ldcs(p), __ldcs(p + 1)};
+    };
+    // its codes, two to a byte, and its scale
+    auto quantise = [&](const Block& x, float mul, uint32_t (&b)[8]) -> uint32_t {
+        const uint32_t w[8] = {x.a.x, x.a.y, x.a.z, x.a.w, x.b.x, x.b.y, x.b.z, x.b.w};
         float y[16], top = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -90,27 +96,29 @@ __global__ void __launch_bounds__(kRowThreads) fp4_store_kernel(const __grid_con
         for (int j = 0; j < 8; ++j) b[j] = e2m1x2_from_f32(y[2 * j] * inv, y[2 * j + 1] * inv);
         return sc;
     };
-    for (int i = threadIdx.x; i < c.n_rows * NB; i += kRowThreads) {
-        const int r = i / NB, blk = i % NB, tok = c.dst_row + r;
+    auto put_key = [&](const Block& x, int tok, int blk) {
         uint32_t b[8];
-        tile[T::kKScales + f4_k_scale<D>(tok, blk)] = (uint8_t)quantise(a.k, r, blk, a.k_mul, b);
+        tile[T::kKScales + f4_k_scale<D>(tok, blk)] = (uint8_t)quantise(x, a.k_mul, b);
 #pragma unroll
         for (int t = 0; t < 4; ++t)
             *reinterpret_cast<uint16_t*>(tile + f4_k_byte<D>(tok, blk * 16 + 4 * t)) =
                 (uint16_t)(b[2 * t] | (b[2 * t + 1] << 8));
-    }
-    // Values: a thread takes a pair of tokens' block.  A token that is not among
-    // the new rows keeps what the pool holds (nothing, in a new chunk).
+    };
     const int z = c.dst_row + c.n_rows;
     for (int i = threadIdx.x; i < C / 2 * NB; i += kRowThreads) {
         const int pair = i / NB, blk = i % NB, tok = (pair >> 2) * 8 + (pair & 3);
         const bool has0 = tok >= c.dst_row && tok < z, has1 = tok + 4 >= c.dst_row && tok + 4 < z;
         if (!has0 && !has1) continue;
+        Block k0, k1, v0, v1;
+        if (has0) { k0 = fetch(a.k, tok - c.dst_row, blk); v0 = fetch(a.v, tok - c.dst_row, blk); }
+        if (has1) { k1 = fetch(a.k, tok + 4 - c.dst_row, blk); v1 = fetch(a.v, tok + 4 - c.dst_row, blk); }
+        if (has0) put_key(k0, tok, blk);
+        if (has1) put_key(k1, tok + 4, blk);
         uint32_t b0[8], b1[8];
-        if (has0) tile[T::kVScales + f4_v_scale<D>(tok, blk)] = (uint8_t)quantise(a.v, tok - c.dst_row, blk, a.v_mul, b0);
-        if (has1)
-            tile[T::kVScales + f4_v_scale<D>(tok + 4, blk)] =
-                (uint8_t)quantise(a.v, tok + 4 - c.dst_row, blk, a.v_mul, b1);
+        if (has0) tile[T::kVScales + f4_v_scale<D>(tok, blk)] = (uint8_t)quantise(v0, a.v_mul, b0);
+        if (has1) tile[T::kVScales + f4_v_scale<D>(tok + 4, blk)] = (uint8_t)quantise(v1, a.v_mul, b1);
+        // The token that is not among the new rows keeps what the pool holds
+        // (nothing, in a new chunk).
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
             const int at0 = T::kVCodes + f4_v_byte<D>(pair, blk * 16 + 2 * g), at1 = at0 + D / 16;
@@ -225,6 +233,7 @@ __global__ void __launch_bounds__(kRowThreads) key_bounds_kernel(const __grid_co
 // memory (its rows are permuted) and a thread takes a block of 16 dims.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t scaled(uint32_t h, float mul) {
+    if (mul == 1.f) return h;                          // (the same for the whole launch)
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
     return pack_half2(f.x * mul, f.y * mul);
 }
@@ -263,36 +272,41 @@ __global__ void __launch_bounds__(kRowThreads) read_rows_kernel(const __grid_con
             reinterpret_cast<uint4*>(tile)[i] = __ldcs(reinterpret_cast<const uint4*>(src) + i);
         __syncthreads();
         constexpr int NB = D / 16;
-        const int half = c.n_rows * NB;
-        for (int i = threadIdx.x; i < 2 * half; i += kRowThreads) {
-            const bool isv = i >= half;
-            const int r = (isv ? i - half : i) / NB, blk = i % NB, tok = c.dst_row + r;
-            uint32_t w[8];
-            uint32_t sc;
-            if (!isv) {
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const uint32_t b = *reinterpret_cast<const uint16_t*>(tile + f4_k_byte<D>(tok, blk * 16 + 4 * t));
-                    w[2 * t] = f16x2_from_e2m1x2(b);
-                    w[2 * t + 1] = f16x2_from_e2m1x2(b >> 8);
-                }
-                sc = tile[T::kKScales + f4_k_scale<D>(tok, blk)];
-            } else {
-#pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                    const uint8_t* b = tile + T::kVCodes + f4_v_byte<D>(f4_pair(tok), blk * 16 + 2 * g);
-                    const int nib = tok & 4;
-                    w[g] = f16x2_from_e2m1x2((b[0] >> nib & 15u) | (b[D / 16] >> nib << 4));
-                }
-                sc = tile[T::kVScales + f4_v_scale<D>(tok, blk)];
-            }
-            const uint32_t s2 = f16x2_from_e4m3x2(sc * 0x101u);
-            const float mul = isv ? a.v_mul : a.k_mul;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = scaled(mul_f16x2(w[j], s2), mul);
-            uint4* o = reinterpret_cast<uint4*>((isv ? ov : ok) + ((row0 + r) * a.n_heads + at.h) * D + blk * 16);
+        const int z = c.dst_row + c.n_rows;
+        auto write = [&](uint16_t* rows, int tok, int blk, const uint32_t (&w)[8]) {
+            if (tok < c.dst_row || tok >= z) return;
+            uint4* o = reinterpret_cast<uint4*>(rows + ((row0 + tok - c.dst_row) * a.n_heads + at.h) * D + blk * 16);
             __stcs(o, make_uint4(w[0], w[1], w[2], w[3]));
             __stcs(o + 1, make_uint4(w[4], w[5], w[6], w[7]));
+        };
+        // keys token by token, values by the pairs of tokens that share bytes
+        for (int i = threadIdx.x; i < c.n_rows * NB; i += kRowThreads) {
+            const int blk = i % NB, tok = c.dst_row + i / NB;
+            const uint32_t s2 = f16x2_from_e4m3x2(tile[T::kKScales + f4_k_scale<D>(tok, blk)] * 0x101u);
+            uint32_t w[8];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const uint32_t b = *reinterpret_cast<const uint16_t*>(tile + f4_k_byte<D>(tok, blk * 16 + 4 * t));
+                w[2 * t] = scaled(mul_f16x2(f16x2_from_e2m1x2(b), s2), a.k_mul);
+                w[2 * t + 1] = scaled(mul_f16x2(f16x2_from_e2m1x2(b >> 8), s2), a.k_mul);
+            }
+            write(ok, tok, blk, w);
+        }
+        for (int i = threadIdx.x; i < C / 2 * NB; i += kRowThreads) {
+            const int pair = i / NB, blk = i % NB, tok = (pair >> 2) * 8 + (pair & 3);
+            if ((tok < c.dst_row || tok >= z) && (tok + 4 < c.dst_row || tok + 4 >= z)) continue;
+            const uint32_t s2 = f16x2_from_e4m3x2(
+                *reinterpret_cast<const uint16_t*>(tile + T::kVScales + f4_v_scale<D>(tok, blk)));
+            uint32_t w0[8], w1[8];
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+                const uint8_t* b = tile + T::kVCodes + f4_v_byte<D>(pair, blk * 16 + 2 * g);
+                const uint32_t x = mul_f16x2(f16x2_from_e2m1x2(b[0]), s2), y = mul_f16x2(f16x2_from_e2m1x2(b[D / 16]), s2);
+                w0[g] = scaled(__byte_perm(x, y, 0x5410), a.v_mul);
+                w1[g] = scaled(__byte_perm(x, y, 0x7632), a.v_mul);
+            }
+            write(ov, tok, blk, w0);
+            write(ov, tok + 4, blk, w1);
         }
     }
 }

@@ -39,18 +39,21 @@ constexpr int kF4Stages = 8, kF4Ring = 16;
 // their fp16 operand and normal numbers down to 2^-19 (or less) of the largest.
 constexpr float kLift = 5.f, kSlack = 8.f;
 
-// Shared memory: the ring, the exchange area (operand images of a shared tile,
-// or the warps' outputs at the end of a head: rows of D + 4 floats, which keep
-// the fragments' stores free of bank conflicts), (m, s) per warp and row.
+// Shared memory: the ring, two areas, (m, s) per warp and row.  For units of up
+// to 8 rows the areas hold the warps' outputs at the end of a head, in turn; for
+// others a shared tile widened to fp16 (32 tokens at a time: with all 64 the
+// ring had two slots instead of four, and the other units' tiles took 1.91 ns
+// each instead of 1.67 over the card) and the queries.
 template <int C, int D>
 struct F4Smem {
     static constexpr int kStage = F4Tile<C, D>::kBytes;
-    static constexpr int kImage = C * D * 2;                    // operand images of K (and of V)
-    static constexpr int kRow = D + 4;
-    static constexpr int kOut8 = kF4Warps * 8 * kRow * 4;       // 8 rows of each warp
-    static constexpr int kExch = 2 * kImage > 2 * kOut8 ? 2 * kImage : 2 * kOut8;
+    static constexpr int kTok = C < 32 ? C : 32;                // tokens widened at a time
+    static constexpr int kImage = kTok * D * 2;                 // their keys (and their values)
+    static constexpr int kOut8 = kF4Warps * 8 * D * 4;          // 8 rows of each warp
+    static constexpr int kExch = 2 * kImage > kOut8 ? 2 * kImage : kOut8;
     static constexpr int kMs = 2 * kF4Warps * 8 * 2 * 4;
-    static constexpr int kQ = kQRows * D * 2;                   // query rows of a shared tile
+    static constexpr int kQ = kQRows * D * 2;                   // query rows of a shared tile (= kOut8)
+    static_assert(kQ >= kOut8, "the second area");
     static constexpr int kTail = kMs + 2 * kF4Stages * 8 + kF4Ring * 4 + 2 * kF4Stages * 4 + kQRows * 4;
     static size_t bytes(int stages) { return (size_t)stages * kStage + kExch + kQ + kTail; }
 };
@@ -60,7 +63,7 @@ __device__ __forceinline__ void f4_sync() { asm volatile("bar.sync 1, %0;" ::"n"
 // What the consumers' loops share.
 struct F4Ctx {
     const uint8_t* stages;
-    uint8_t* exch;
+    uint8_t *exch, *qreg;
     float* ms;
     uint32_t full0, empty0;
     const volatile int32_t *ntok, *tok0;
@@ -186,43 +189,43 @@ __device__ __forceinline__ bool f4_tiles_own(F4Ctx& c, int tiles, const uint32_t
     return true;
 }
 
-// The tile widened once for all warps, into the fp16 K and V tiles that the
-// 16-row blocks read (code * scale is exact in fp16).  A thread takes 16 bytes
+// Tokens [base, base + N) of a tile widened once for all warps, into the fp16 K
+// and V tiles that the 16-row blocks read (code * scale is exact in fp16).  A thread takes 16 bytes
 // (8 at D = 64) of a row's key codes: four dims of every 16, and as many of a
 // pair's value codes: two dims of every 16 of both tokens; consecutive threads
 // take rows whose swizzled 16-byte columns differ.
-template <int C, int D>
-__device__ __forceinline__ void f4_tile_to_f16(const uint8_t* src, uint8_t* kd, uint8_t* vd, int tid) {
+template <int C, int D, int N>
+__device__ __forceinline__ void f4_tile_to_f16(const uint8_t* src, int base, uint8_t* kd, uint8_t* vd, int tid) {
     using T = F4Tile<C, D>;
     constexpr int NK = D / 16;
-    for (int i = tid; i < C * 4; i += kF4Warps * 32) {
+    for (int i = tid; i < N * 4; i += kF4Warps * 32) {
         const int t = i & 3, r = i >> 2;
         // rows of 8 in the order 0 1 4 5 2 3 6 7: tokens 0 4 2 6, then 1 5 3 7
         const int m = (r & ~7) | (r & 1) | ((r & 2) << 1) | ((r & 4) >> 1);
         const int tok = f4_token(m);
         uint32_t w[D / 32], sc[D / 64];
-        lds_words<D / 32>(src + m * (D / 2) + t * (D / 8), w);
-        lds_words<D / 64>(src + T::kKScales + m * (D / 16), sc);
+        lds_words<D / 32>(src + (base + m) * (D / 2) + t * (D / 8), w);
+        lds_words<D / 64>(src + T::kKScales + (base + m) * (D / 16), sc);
 #pragma unroll
         for (int kp = 0; kp < NK / 2; ++kp) {             // two steps: one word of codes, two scales
             uint32_t x[4], h[2];
             f16x2_from_e2m1x8(w[kp], x);
             f16x2_from_e4m3x4(sc[kp >> 1], h);
             const uint32_t sa = __byte_perm(h[kp & 1], 0u, 0x1010), sb = __byte_perm(h[kp & 1], 0u, 0x3232);
-            *reinterpret_cast<uint2*>(kd + swz(tok, 4 * kp + (t >> 1), C) + 8 * (t & 1)) =
+            *reinterpret_cast<uint2*>(kd + swz(tok, 4 * kp + (t >> 1), N) + 8 * (t & 1)) =
                 make_uint2(mul_f16x2(x[0], sa), mul_f16x2(x[1], sa));
-            *reinterpret_cast<uint2*>(kd + swz(tok, 4 * kp + 2 + (t >> 1), C) + 8 * (t & 1)) =
+            *reinterpret_cast<uint2*>(kd + swz(tok, 4 * kp + 2 + (t >> 1), N) + 8 * (t & 1)) =
                 make_uint2(mul_f16x2(x[2], sb), mul_f16x2(x[3], sb));
         }
     }
-    for (int i = tid; i < C * 4; i += kF4Warps * 32) {
+    for (int i = tid; i < N * 4; i += kF4Warps * 32) {
         // four pairs of tokens a warp: (0, 4), (1, 5), ... of each 8; their rows
         // two apart in turn
         const int g = i & 7, q = i >> 3, pair = (q & ~3) | ((q & 1) << 1) | ((q >> 1) & 1);
         const int tok = (pair >> 2) * 8 + (pair & 3);
         uint32_t w[D / 32], sc[D / 32];
-        lds_words<D / 32>(src + T::kVCodes + pair * D + f4_v_unit<D>(pair, g) * (D / 8), w);
-        lds_words<D / 32>(src + T::kVScales + pair * (D / 8), sc);
+        lds_words<D / 32>(src + T::kVCodes + (base / 2 + pair) * D + f4_v_unit<D>(pair, g) * (D / 8), w);
+        lds_words<D / 32>(src + T::kVScales + (base / 2 + pair) * (D / 8), sc);
 #pragma unroll
         for (int i4 = 0; i4 < D / 64; ++i4) {
             uint32_t x[4], y[4];
@@ -236,8 +239,8 @@ __device__ __forceinline__ void f4_tile_to_f16(const uint8_t* src, uint8_t* kd, 
                 for (int e = 0; e < 2; ++e) {
                     const int k = 2 * j2 + e, kc = 2 * (4 * i4 + k) + (g >> 2), off = 4 * (g & 3);
                     const uint32_t a = mul_f16x2(x[k], h[e]), b = mul_f16x2(y[k], h[e]);   // (tok, tok + 4)
-                    *reinterpret_cast<uint32_t*>(vd + swz(tok, kc, C) + off) = __byte_perm(a, b, 0x5410);
-                    *reinterpret_cast<uint32_t*>(vd + swz(tok + 4, kc, C) + off) = __byte_perm(a, b, 0x7632);
+                    *reinterpret_cast<uint32_t*>(vd + swz(tok, kc, N) + off) = __byte_perm(a, b, 0x5410);
+                    *reinterpret_cast<uint32_t*>(vd + swz(tok + 4, kc, N) + off) = __byte_perm(a, b, 0x7632);
                 }
             }
         }
@@ -251,9 +254,10 @@ __device__ __forceinline__ void f4_tile_to_f16(const uint8_t* src, uint8_t* kd, 
 // here, so that the id's load, begun with the head, is first waited for here.
 template <int C, int D, bool ONE>
 __device__ __forceinline__ void f4_finish(F4Ctx& c, const AttnParams& p, F4State<D, 1>& a, int rows, int pid, int part) {
-    constexpr int RS = F4Smem<C, D>::kRow;
     const int g = c.lane >> 2, t = c.lane & 3;
-    float* ob = reinterpret_cast<float*>(c.exch + (c.flush & 1) * F4Smem<C, D>::kOut8);
+    float* ob = reinterpret_cast<float*>((c.flush & 1) ? c.qreg : c.exch);
+    // column of a row's dim: the fragments' stores of four rows stay apart
+    auto col = [](int row, int d) { return d ^ ((row >> 1 & 3) << 3); };
     float* ms = c.ms + (c.flush & 1) * kF4Warps * 8 * 2;
     ++c.flush;
 #pragma unroll
@@ -266,7 +270,7 @@ __device__ __forceinline__ void f4_finish(F4Ctx& c, const AttnParams& p, F4State
             if (g == 0) *reinterpret_cast<float2*>(ms + (c.w * 8 + row) * 2) = make_float2(a.m[0][r], s);
 #pragma unroll
             for (int db = 0; db < D / 16; ++db)
-                *reinterpret_cast<float2*>(ob + (c.w * 8 + row) * RS + 16 * db + 2 * g) =
+                *reinterpret_cast<float2*>(ob + (c.w * 8 + row) * D + col(row, 16 * db + 2 * g)) =
                     make_float2(a.o[0][db][r], a.o[0][db][r + 2]);
         }
     }
@@ -286,7 +290,7 @@ __device__ __forceinline__ void f4_finish(F4Ctx& c, const AttnParams& p, F4State
             const float wt = q[k].x == -INFINITY ? 0.f : ex2(q[k].x - M);
             sum += wt * q[k].y;
             if (c.lane < D / 4) {
-                const float4 v = reinterpret_cast<const float4*>(ob + (k * 8 + row) * RS)[c.lane];
+                const float4 v = *reinterpret_cast<const float4*>(ob + (k * 8 + row) * D + col(row, 4 * c.lane));
                 acc.x += wt * v.x; acc.y += wt * v.y; acc.z += wt * v.z; acc.w += wt * v.w;
             }
         }
@@ -462,7 +466,7 @@ fp4_attention_kernel(const __grid_constant__ CUtensorMap, const AttnParams p) {
         return lane < kUnitInts ? reinterpret_cast<const int32_t*>(p.units + u)[lane] : 0;
     };
     auto fld = [&](int32_t d, int i) -> int32_t { return __shfl_sync(kFull, d, i); };
-    F4Ctx c{stages, exch, ms, full0, empty0, stage_ntok, stage_tok0, S, 0, 0, 0u, warp, lane, 0};
+    F4Ctx c{stages, exch, qreg, ms, full0, empty0, stage_ntok, stage_tok0, S, 0, 0, 0u, warp, lane, 0};
     const int w = warp, g = lane >> 2, t = lane & 3;
     auto tab_pos = [](int32_t e) { return e >> 16; };
     auto tab_tok = [](int32_t e) { return e >> 8 & 0xff; };
@@ -574,7 +578,8 @@ fp4_attention_kernel(const __grid_constant__ CUtensorMap, const AttnParams p) {
             // More rows: the tile widened once for all warps, each taking a
             // 16-row block and (fewer than 4 blocks) a share of the tokens.
             const int rblocks = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-            const int T = min(kF4Warps / rblocks, C / 16), rb = w / T, tp = w % T;
+            constexpr int N = SM::kTok;
+            const int T = min(kF4Warps / rblocks, N / 16), rb = w / T, tp = w % T;
             const bool act = rb < rblocks && rb * 16 < rows;
             int lim[2] = {INT_MAX, INT_MAX};
             if (p.causal) {
@@ -601,21 +606,22 @@ fp4_attention_kernel(const __grid_constant__ CUtensorMap, const AttnParams p) {
                         return;
                     }
                     const int ntok = c.ntok[c.st], ctx0 = c.tok0[c.st];
-                    f4_sync();                 // the last tile has been read (and the queries are there)
-                    f4_tile_to_f16<C, D>(stages + (size_t)c.st * SM::kStage, exch, exch + SM::kImage, threadIdx.x);
-                    f4_sync();
-                    if (lane == 0) mbar_arrive(empty0 + 8 * c.st);
-                    c.next();
-                    if (!act) continue;
-                    constexpr int kStep = C >= 32 ? 32 : 16;
-                    if (T * 16 == C) {
-                        cf_chunk<C, D, 16>(kt, vt, ntok, tp * 16, ctx0, lim[0], lim[1], qblock, p.scale_log2, m, s, o,
-                                           lane);
-                    } else {
-                        for (int t0 = tp * (C / T); t0 < (tp + 1) * (C / T); t0 += kStep)
-                            cf_chunk<C, D, kStep>(kt, vt, ntok, t0, ctx0, lim[0], lim[1], qblock, p.scale_log2, m, s,
-                                                  o, lane);
+                    const uint8_t* tile = stages + (size_t)c.st * SM::kStage;
+#pragma unroll 1
+                    for (int base = 0; base < C && (base == 0 || base < ntok); base += N) {
+                        f4_sync();             // the last tokens have been read (and the queries are there)
+                        f4_tile_to_f16<C, D, N>(tile, base, exch, exch + SM::kImage, threadIdx.x);
+                        f4_sync();
+                        if (lane == 0 && (base + N >= C || base + N >= ntok)) mbar_arrive(empty0 + 8 * c.st);
+                        if (!act) continue;
+                        if (T * 16 == N)
+                            cf_chunk<N, D, 16>(kt, vt, ntok - base, tp * 16, ctx0 + base, lim[0], lim[1], qblock,
+                                               p.scale_log2, m, s, o, lane);
+                        else
+                            cf_chunk<N, D, N>(kt, vt, ntok - base, 0, ctx0 + base, lim[0], lim[1], qblock,
+                                              p.scale_log2, m, s, o, lane);
                     }
+                    c.next();
                 }
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {

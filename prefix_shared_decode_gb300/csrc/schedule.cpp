@@ -208,10 +208,10 @@ constexpr double kCfComputePer16 = 0.2;
 constexpr double kF8CfFactor = 2.0;
 // fp4 pools: a chunk-first tile is widened to fp16 in shared memory first, a
 // sequence-first one straight into fragments whatever its rows (up to 8).
-// Swept on GB300 at three CTAs per SM: single rows over a 4096-token prompt
-// 69.6 / 62.2 / 62.4 / 67.6 us at 2 / 3 / 4 / 5; four query tokens over a
-// 1024-token one 50.7 / 44.8 / 42.3 / 39.3 us at 1 / 2 / 3 / 4.
-constexpr double kF4CfFactor = 3.0, kF4CfRowsFactor = 4.0;
+// Swept on GB300 at three CTAs per SM, single rows over prompts of 4096 tokens
+// (64 sequences) and 1024 (32): 64.1 / 62.0 / 61.0 and 31.9 / 30.7 / 27.3 us at
+// 2.5 / 3.5 / 4.5; four query tokens over 1024: 42.1 / 37.3 / 41.4 us at 3 / 4 / 5.
+constexpr double kF4CfFactor = 4.5, kF4CfRowsFactor = 4.0;
 
 // Share of the sequence-first tiles left to the tail queue that CTAs drain
 // dynamically once their static lists are done (absorbs the run-to-run rate
