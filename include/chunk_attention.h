@@ -454,8 +454,9 @@ int ca_decode_attention_static_ws(const ca_pool* pool, const ca_sched* sched,
  * where hi and lo are the chunk's key bounds: no token of the chunk has a
  * larger product with the row.  Chunks are ranked by their scores to 48 bits
  * (scores in 32 decide wherever their error bound allows it), ties to the
- * lower number.  A row whose sum is not a number is passed over, and a chunk
- * with no other ranks last.  Needs CA_CHUNK_BOUNDS.  Contexts of at most 49152 chunks (CA_ERR_UNSUPPORTED).
+ * lower number.  Keys and queries must be finite (with others the chunks
+ * beside the forced ones are unspecified, but still top_k different ones).
+ * Needs CA_CHUNK_BOUNDS.  Contexts of at most 49152 chunks (CA_ERR_UNSUPPORTED).
  *
  * ca_sparse_attention: out[i][h][:] = sum_t softmax_t(scale * q[i][h] . k_t) v_t
  * over the tokens of the chunks in lists_dev[i][h / group] (-1 entries, and
@@ -467,7 +468,8 @@ int ca_decode_attention_static_ws(const ca_pool* pool, const ca_sched* sched,
  * partial results lie in a buffer that the schedule holds.  So, as for the
  * decode calls, calls on one schedule must not overlap on the GPU (graphs that
  * recorded them included); calls on different schedules may.  Both may be
- * captured into graphs, valid while the schedule is (ca_decode_attention).  q_dev / out_dev
+ * captured into graphs, valid while the schedule is (ca_decode_attention).
+ * out_dev must not overlap q_dev.  q_dev / out_dev
  * fp16 [b][n_heads][head_dim], 16-byte aligned.  Errors: CA_ERR_STALE;
  * CA_ERR_INVALID (a schedule without lists, a pool without bounds, top_k < 1,
  * sink + recent > top_k, bad layer, NULL or misaligned pointers);

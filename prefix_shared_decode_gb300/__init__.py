@@ -28,9 +28,9 @@ __all__ = ["Pool", "Schedule", "DecodeGraph", "decode_attention", "decode_attent
 _cuda_ok = None
 
 
-def _stream_ptr(stream) -> int | None:
-    """The raw handle of ``stream`` (default: torch's current stream on the
-    current device; 0 / None is the legacy default stream)."""
+def _stream_ptr(stream, device: int | None = None) -> int | None:
+    """The raw handle of ``stream`` (default: torch's current stream on device
+    ``device``, or on the current one; 0 / None is the legacy default stream)."""
     if stream is None:
         global _cuda_ok
         import torch
@@ -40,8 +40,8 @@ def _stream_ptr(stream) -> int | None:
             return None
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # no Stream object per call
         if raw is not None:
-            return raw(torch.cuda.current_device()) or None
-        stream = torch.cuda.current_stream()
+            return raw(torch.cuda.current_device() if device is None else device) or None
+        stream = torch.cuda.current_stream(device)
     return int(getattr(stream, "cuda_stream", stream)) or None
 
 
@@ -169,7 +169,7 @@ class Pool:
         shared = C.c_int32()
         check(capi.lib().ca_insert_tokens(self._h, int(seq_id), tok.ctypes.data_as(C.POINTER(C.c_int32)),
                                           len(tok), kp, vp,
-                                          None if self.host_only else _stream_ptr(stream),
+                                          None if self.host_only else self._stream(stream),
                                           C.byref(shared)), "ca_insert_tokens")
         return shared.value
 
@@ -194,7 +194,7 @@ class Pool:
             kp, vp = k.data_ptr(), v.data_ptr()
         shared = array("i", bytes(4 * len(ids)))
         check(capi.lib().ca_insert_batch(self._h, len(ids), _at(ids), _at(tok), _at(lens), kp, vp,
-                                         None if self.host_only else _stream_ptr(stream), _at(shared)),
+                                         None if self.host_only else self._stream(stream), _at(shared)),
               "ca_insert_batch")
         return shared.tolist()
 
@@ -210,7 +210,7 @@ class Pool:
             kp, vp = k.data_ptr(), v.data_ptr()
         grown = C.c_int32()
         check(capi.lib().ca_append_tokens(self._h, int(seq_id), tok.ctypes.data_as(C.POINTER(C.c_int32)),
-                                          len(tok), kp, vp, None if self.host_only else _stream_ptr(stream),
+                                          len(tok), kp, vp, None if self.host_only else self._stream(stream),
                                           C.byref(grown)), "ca_append_tokens")
         return grown.value
 
@@ -271,13 +271,7 @@ class Pool:
     def _stream(self, stream) -> int | None:
         """The raw handle of ``stream`` (default: the current one of the
         pool's device)."""
-        import torch
-        if stream is None:
-            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # no Stream object per call
-            if raw is not None:
-                return raw(self._kv.device.index) or None
-            stream = torch.cuda.current_stream(self._kv.device)
-        return int(getattr(stream, "cuda_stream", stream)) or None
+        return _stream_ptr(stream, None if self._kv is None else self._kv.device.index)
 
     def remove(self, seq_id: int) -> None:
         check(capi.lib().ca_remove_seq(self._h, int(seq_id)), "ca_remove_seq")
@@ -325,7 +319,7 @@ class Pool:
                  (capi.CA_SCHED_CHUNK_LISTS if chunk_lists else 0))
         check(capi.lib().ca_build_schedule_ex(self._h, ids.__array_interface__["data"][0] if ids is not s._ids
                                               else s._ids_ptr, len(ids), int(q_len), flags, C.byref(h),
-                                              None if self.host_only else _stream_ptr(stream)),
+                                              None if self.host_only else self._stream(stream)),
               "ca_build_schedule_ex")
         s._h = h
         s._ws_need = None
@@ -415,7 +409,7 @@ class Schedule:
         return self._ws
 
     def device_status(self, stream=None) -> int:
-        return capi.lib().ca_sched_device_status(self._h, _stream_ptr(stream))
+        return capi.lib().ca_sched_device_status(self._h, self.pool._stream(stream))
 
     def set_profile_events(self, begin=None, end=None) -> None:
         bp = begin.cuda_event if begin is not None else None
@@ -443,7 +437,7 @@ def decode_attention(pool: Pool, sched: Schedule, q, out=None, layer: int = 0, s
         scale = 1.0 / math.sqrt(pool.head_dim)
     ws = workspace if workspace is not None else sched.workspace()
     check(capi.lib().ca_decode_attention(pool._h, sched._h, layer, q.data_ptr(), out.data_ptr(),
-                                         float(scale), ws.data_ptr(), ws.numel(), _stream_ptr(stream)),
+                                         float(scale), ws.data_ptr(), ws.numel(), pool._stream(stream)),
           "ca_decode_attention")
     return out
 
@@ -457,7 +451,7 @@ def decode_attention_host(pool: Pool, sched: Schedule, q_host, out_host, layer: 
     ws = workspace if workspace is not None else sched.workspace(host_io=True)
     check(capi.lib().ca_decode_attention_host(pool._h, sched._h, layer, q_host.data_ptr(),
                                               out_host.data_ptr(), float(scale), ws.data_ptr(),
-                                              ws.numel(), _stream_ptr(stream)),
+                                              ws.numel(), pool._stream(stream)),
           "ca_decode_attention_host")
     return out_host
 

@@ -162,9 +162,7 @@ struct Pool {
     int device = -1;
     int num_sms = 0;               // CTAs of the attention grid (SMs x resident CTAs)
     int sms = 0;                   // SMs of the device
-    // The kernels over chunk lists (selection, attention) whose shared-memory
-    // limit a call on this pool has raised.
-    mutable const void* list_fn[2] = {nullptr, nullptr};
+    bool lists_ready = false;      // the kernels over chunk lists may use their shared memory
     alignas(64) unsigned char tmap[128];  // CUtensorMap over the pool
     Node root;
     std::vector<Node> nodes;       // one per slot, reused; live iff refcount > 0
@@ -336,6 +334,7 @@ int launch_read_rows(const Pool& p, void* k, void* v, int32_t total_rows, const 
 int launch_select(const Pool& p, const Sched& s, int32_t layer, const void* q, int32_t top_k, int32_t sink,
                   int32_t recent, int32_t* lists, void* stream);
 size_t list_parts_bytes(const Pool& p);
+int prepare_lists(Pool& p);
 int launch_sparse(const Pool& p, const Sched& s, int32_t layer, const void* q, const int32_t* lists, int32_t top_k,
                   void* out, float scale, void* stream);
 

@@ -232,7 +232,10 @@ int ca_insert_batch(ca_pool* pool, int32_t n_seqs, const int64_t* seq_ids, const
                 if (n_shared_out) n_shared_out[i] = shared;
                 row0 += lengths[i];
             }
-            if (!st && pool->kv) st = launch_scatter(*pool, k_dev, v_dev, (int32_t)total, copies, stream);
+            if (!st && pool->kv) {
+                const DeviceGuard dev(pool->device);
+                st = dev.ok ? launch_scatter(*pool, k_dev, v_dev, (int32_t)total, copies, stream) : CA_ERR_CUDA;
+            }
         } catch (...) {
             undo();
             throw;
@@ -258,7 +261,8 @@ int ca_append_tokens(ca_pool* pool, int64_t seq_id, const int32_t* tokens, int32
         int st = pool_append(*pool, seq_id, tokens, n, &copies, &undo);
         if (st) return st;
         if (pool->kv) {
-            st = launch_scatter(*pool, k_dev, v_dev, n, copies, stream);
+            const DeviceGuard dev(pool->device);
+            st = dev.ok ? launch_scatter(*pool, k_dev, v_dev, n, copies, stream) : CA_ERR_CUDA;
             if (st) {
                 pool_undo_append(*pool, seq_id, undo);
                 return st;
@@ -397,6 +401,8 @@ int ca_build_schedule_ex(ca_pool* pool, const int64_t* seq_ids, int32_t b, int32
         layout_plan(*pool, s->plan, b, s->layout, s->blob, s->t);
         layout_ws(s->plan, *pool, b, s->ws);
         if (pool->kv) {
+            const DeviceGuard dev(pool->device);
+            if (!dev.ok) return CA_ERR_CUDA;
             if (s->dev_bytes < s->blob.size()) {
                 if (s->dev) cudaFree(s->dev);
                 s->dev = nullptr;
@@ -414,6 +420,10 @@ int ca_build_schedule_ex(ca_pool* pool, const int64_t* seq_ids, int32_t b, int32
                 s->list_parts_size = 0;
                 if (cudaMalloc(&s->list_parts, parts) != cudaSuccess) return CA_ERR_CUDA;
                 s->list_parts_size = parts;
+            }
+            if (parts) {
+                st = prepare_lists(*pool);
+                if (st) return st;
             }
             st = upload_plan(*s, static_cast<cudaStream_t>(stream));
             if (st) {
@@ -554,6 +564,8 @@ extern "C" {
 
 static int decode_launch(const ca_pool* pool, const ca_sched* s, int32_t layer, const void* q,
                          void* out, float scale, void* ws_dev, void* stream) {
+    const DeviceGuard dev(pool->device);
+    if (!dev.ok) return CA_ERR_CUDA;
     const AttnParams a = attn_params(*pool, *s, layer, q, out, scale, ws_dev);
     return launch_attention(*pool, *s, a, stream);
 }

@@ -98,7 +98,7 @@ __device__ __forceinline__ uint32_t part_f16x2(uint32_t x, bool positive) {   //
 constexpr int kBins = 2048, kPerBin = kBins / kSelThreads;
 struct SelShared {
     uint32_t hist[kBins];
-    uint32_t top_abs[16];                 // largest |bound| of each CTA of the cluster (fp32 bits)
+    uint32_t top_abs[8][128];             // largest |bound| of each pair of dims: per warp, then per CTA of the cluster
     uint32_t red[kSelWarps][2];
     float qsum[kSelWarps];
     uint32_t bin, left, in_bin, T;        // histogram step: the digit, places left inside it, its count
@@ -253,6 +253,7 @@ template <int D>
 __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const ListParams p) {
     extern __shared__ __align__(16) uint32_t keys[];      // the first CTA's: one key per chunk
     __shared__ SelShared sh;
+    __shared__ uint32_t wtop[kSelWarps][D / 2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int cs = p.splits, rank = blockIdx.x % cs, pair = blockIdx.x / cs;
@@ -276,24 +277,11 @@ __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const ListPa
     const uint32_t keys0 = cs > 1 ? peer_addr(smem_u32(keys), 0) : 0u;
     const uint32_t abs0 = cs > 1 ? peer_addr(smem_u32(sh.top_abs), 0) : 0u;
 
-    if (rank == 0) {                                      // the largest sum|q| of the group's rows, for E
-        float qs = 0.f;
-        for (int r = warp; r < G; r += kSelWarps) {
-            float s = 0.f;
-#pragma unroll
-            for (int j = 0; j < D / 64; ++j) {
-                const float2 x = __half22float2(*reinterpret_cast<const __half2*>(q + (size_t)r * D + 64 * j + 2 * lane));
-                s += fabsf(x.x) + fabsf(x.y);
-            }
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-            qs = fmaxf(qs, s);
-        }
-        if (lane == 0) sh.qsum[warp] = qs;
-    }
+    // each warp's own row of the largest |bound| per pair of dims (for E)
+    for (int d = lane; d < D / 2; d += 32) wtop[warp][d] = 0u;
+    __syncwarp();
     // scores of blocks of 16 chunks
     bool met = cs == 1;                                   // the first CTA's shared memory exists
-    __half2 top = __float2half2_rn(0.f);
     bool bad = false;
     for (int blk = rank * kSelWarps + warp; blk * 16 < n; blk += cs * kSelWarps) {
         const int c0 = blk * 16 + g, c1 = c0 + 8;
@@ -330,15 +318,27 @@ __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const ListPa
             best0 = fmaxf(best0, fmaxf(acc[0], acc[1]));
             best1 = fmaxf(best1, fmaxf(acc[2], acc[3]));
         }
+        auto larger = [](uint32_t a, uint32_t b) {        // max(|a|, |b|) of fp16 pairs
+            const __half2 m = __hmax2(__habs2(*reinterpret_cast<const __half2*>(&a)),
+                                      __habs2(*reinterpret_cast<const __half2*>(&b)));
+            return *reinterpret_cast<const uint32_t*>(&m);
+        };
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
+        for (int j = 0; j < J; ++j) {
+            uint32_t m[4] = {larger(x0[0][j].x, x1[0][j].x), larger(x0[0][j].y, x1[0][j].y),
+                             larger(x0[0][j].z, x1[0][j].z), larger(x0[0][j].w, x1[0][j].w)};
+            m[0] = larger(m[0], larger(x0[1][j].x, x1[1][j].x));
+            m[1] = larger(m[1], larger(x0[1][j].y, x1[1][j].y));
+            m[2] = larger(m[2], larger(x0[1][j].z, x1[1][j].z));
+            m[3] = larger(m[3], larger(x0[1][j].w, x1[1][j].w));
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const uint32_t w[8] = {x0[part][j].x, x0[part][j].y, x0[part][j].z, x0[part][j].w,
-                                       x1[part][j].x, x1[part][j].y, x1[part][j].z, x1[part][j].w};
+            for (int k = 0; k < 4; ++k) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) top = __hmax2(top, __habs2(*reinterpret_cast<const __half2*>(&w[k])));
+                for (int d = 4; d <= 16; d <<= 1) m[k] = larger(m[k], __shfl_xor_sync(kFull, m[k], d));
+                uint32_t* to = &wtop[warp][j * 16 + t * 4 + k];
+                if (g == 0) *to = larger(*to, m[k]);
             }
+        }
 #pragma unroll
         for (int d = 1; d <= 2; d <<= 1) {
             best0 = fmaxf(best0, __shfl_xor_sync(kFull, best0, d));
@@ -360,17 +360,14 @@ __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const ListPa
     }
     if (bad) set_status(p.status, CA_ERR_DEVICE_BOUNDS);
     if (!met) cluster_wait();
-    {
-        // the cluster's largest |bound|: a non-negative fp32's bits order as integers
-        const float2 f = __half22float2(top);
-        uint32_t m = __reduce_max_sync(kFull, __float_as_uint(fmaxf(f.x, f.y)));
-        if (lane == 0) sh.red[warp][0] = m;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            for (int w = 1; w < kSelWarps; ++w) m = max(m, sh.red[w][0]);
-            if (cs > 1) st_peer(abs0 + 4u * (uint32_t)rank, m);
-            else sh.top_abs[0] = m;
-        }
+    __syncthreads();
+    for (int d = threadIdx.x; d < D / 2; d += kSelThreads) {
+        __half2 m = *reinterpret_cast<const __half2*>(&wtop[0][d]);
+#pragma unroll
+        for (int w = 1; w < kSelWarps; ++w) m = __hmax2(m, *reinterpret_cast<const __half2*>(&wtop[w][d]));
+        const uint32_t bits = *reinterpret_cast<const uint32_t*>(&m);
+        if (cs > 1) st_peer(abs0 + 4u * (uint32_t)(rank * 128 + d), bits);
+        else sh.top_abs[0][d] = bits;
     }
     if (cs > 1) {
         cluster_sync_all();
@@ -382,15 +379,38 @@ __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const ListPa
     const uint32_t places = (uint32_t)(K - p.sink - p.recent);   // n > K >= sink + recent: they do not overlap
     uint32_t cut = kTie, ties = 0;                        // taken: keys above `cut`, and the first `ties` of kTie
     if (places > 0) {
-        // E: with A = sum of |terms| <= max over rows of sum|q| times the largest |bound|, each of the
-        // D / 8 steps of mma (16 exact products and the running sum, aligned and cut at 2^-23 of the
-        // largest each, rounded once) is off by at most 18 * 2^-23 * A.
-        const uint32_t kth = kth_key(sh, keys, n, places);
-        float A = 0.f, big = 0.f;
+        // E: with A the sum of |terms|, at most max over rows of sum_d |q_d| * (the largest |bound| of
+        // dim d), each of the D / 8 steps of mma (16 exact products and the running sum, aligned and cut
+        // at 2^-23 of the largest each, rounded once) is off by at most 18 * 2^-23 * A.  (A bound by the
+        // largest |bound| of all dims would count a channel of large keys in every dim.)
+        {
+            __half2 m[D / 64];
 #pragma unroll
-        for (int w = 0; w < kSelWarps; ++w) A = fmaxf(A, sh.qsum[w]);
-        for (int r = 0; r < cs; ++r) big = fmaxf(big, __uint_as_float(sh.top_abs[r]));
-        A *= big;
+            for (int j = 0; j < D / 64; ++j) {
+                m[j] = *reinterpret_cast<const __half2*>(&sh.top_abs[0][j * 32 + lane]);
+                for (int r = 1; r < cs; ++r)
+                    m[j] = __hmax2(m[j], *reinterpret_cast<const __half2*>(&sh.top_abs[r][j * 32 + lane]));
+            }
+            float qs = 0.f;
+            for (int r = warp; r < G; r += kSelWarps) {
+                float s = 0.f;
+#pragma unroll
+                for (int j = 0; j < D / 64; ++j) {
+                    const float2 x =
+                        __half22float2(*reinterpret_cast<const __half2*>(q + (size_t)r * D + 64 * j + 2 * lane));
+                    const float2 b = __half22float2(m[j]);
+                    s += fabsf(x.x) * b.x + fabsf(x.y) * b.y;
+                }
+#pragma unroll
+                for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+                qs = s > qs || s != s ? s : qs;          // a NaN stays: no bound then
+            }
+            if (lane == 0) sh.qsum[warp] = qs;
+        }
+        const uint32_t kth = kth_key(sh, keys, n, places);
+        float A = 0.f;
+#pragma unroll
+        for (int w = 0; w < kSelWarps; ++w) A = sh.qsum[w] > A || sh.qsum[w] != sh.qsum[w] ? sh.qsum[w] : A;
         const float E = A * ((D / 8) * 18.2f / 8388608.f);
         const float T = key_value(kth);
         uint32_t low = 0u, high = kTie - 1u;              // a band without bounds where E or T is not finite
@@ -1077,16 +1097,9 @@ dev::ListParams list_params(const Pool& p, const Sched& s, int32_t layer, const 
 }
 
 // One launch of `blocks` clusters of `cs` CTAs, a programmatic dependent of
-// the work before it (the kernels wait for that before anything else).  `most`:
-// the kernel's largest dynamic shared memory, the same in every call, so that
-// pools which share a kernel never lower each other's limit.
-int launch(const Pool& p, int kind, const void* fn, unsigned blocks, int cs, int threads, size_t smem, size_t most,
-           void** args, cudaStream_t stream) {
-    if (smem > 48 * 1024 && p.list_fn[kind] != fn) {
-        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess)
-            return CA_ERR_CUDA;
-        p.list_fn[kind] = fn;
-    }
+// the work before it (the kernels wait for that before they read or write what
+// it may have written).
+int launch(const void* fn, unsigned blocks, int cs, int threads, size_t smem, void** args, cudaStream_t stream) {
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1145,6 +1158,21 @@ SparseKernel pick_sparse(const PoolCfg& c) {
     }
 }
 
+// The ring: what the resident CTAs (two or three per SM) leave room for.
+int sparse_stages(const SparseKernel& k, size_t* smem) {
+    const size_t room = (size_t)(k.per_sm == 2 ? 113 : 75) * 1024;
+    int st = dev::kSpStages / k.groups * k.groups;
+    while (st > k.groups && (size_t)st * k.stage + k.fixed > room) st -= k.groups;
+    *smem = (size_t)st * k.stage + k.fixed;
+    return st;
+}
+
+const void* select_fn(const PoolCfg& c) {
+    return c.head_dim == 64    ? reinterpret_cast<const void*>(&dev::select_chunks_kernel<64>)
+           : c.head_dim == 128 ? reinterpret_cast<const void*>(&dev::select_chunks_kernel<128>)
+                               : reinterpret_cast<const void*>(&dev::select_chunks_kernel<256>);
+}
+
 }  // namespace
 
 int launch_select(const Pool& p, const Sched& s, int32_t layer, const void* q, int32_t top_k, int32_t sink,
@@ -1160,11 +1188,8 @@ int launch_select(const Pool& p, const Sched& s, int32_t layer, const void* q, i
     while (cs < 8 && pairs * cs * 2 <= 2 * sms && cs * dev::kSelWarps * 16 < s.t.list_max) cs *= 2;
     a.splits = cs;
     const size_t smem = (size_t)s.t.list_max * 4;
-    const void* fn = p.cfg.head_dim == 64    ? reinterpret_cast<const void*>(&dev::select_chunks_kernel<64>)
-                     : p.cfg.head_dim == 128 ? reinterpret_cast<const void*>(&dev::select_chunks_kernel<128>)
-                                             : reinterpret_cast<const void*>(&dev::select_chunks_kernel<256>);
     void* args[] = {&a};
-    return launch(p, 0, fn, (unsigned)pairs, cs, dev::kSelThreads, smem, (size_t)kMostChunks * 4, args, static_cast<cudaStream_t>(stream));
+    return launch(select_fn(p.cfg), (unsigned)pairs, cs, dev::kSelThreads, smem, args, static_cast<cudaStream_t>(stream));
 }
 
 int launch_sparse(const Pool& p, const Sched& s, int32_t layer, const void* q, const int32_t* lists, int32_t top_k,
@@ -1180,17 +1205,30 @@ int launch_sparse(const Pool& p, const Sched& s, int32_t layer, const void* q, c
     a.n_units = s.t.b * a.n_kv_heads * ((a.group + k.rows - 1) / k.rows);
     a.counters = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(s.dev) + s.layout.list_count);
     a.parts = static_cast<float*>(s.list_parts);
-    // Ring: what the resident CTAs (two or three per SM) leave room for.
-    const size_t room = (size_t)(k.per_sm == 2 ? 113 : 75) * 1024;
-    int st = dev::kSpStages / k.groups * k.groups;
-    while (st > k.groups && (size_t)st * k.stage + k.fixed > room) st -= k.groups;
-    a.n_stages = st;
-    const size_t smem = (size_t)st * k.stage + k.fixed;
+    size_t smem;
+    a.n_stages = sparse_stages(k, &smem);
     // Two entries per CTA at least: a piece costs its queries, a partial and a place in the merge.
     const int64_t entries = (int64_t)a.n_units * top_k;
     const int grid = (int)std::min<int64_t>((int64_t)k.per_sm * p.sms, (entries + 1) / 2);
     void* args[] = {const_cast<unsigned char*>(p.tmap), &a};
-    return launch(p, 1, k.fn, (unsigned)grid, 1, dev::kSpThreads, smem, smem, args, static_cast<cudaStream_t>(stream));
+    return launch(k.fn, (unsigned)grid, 1, dev::kSpThreads, smem, args, static_cast<cudaStream_t>(stream));
+}
+
+// Once per pool, when a schedule is built with chunk lists (outside stream
+// capture): the kernels' shared-memory limits, which load them too.  Every pool
+// asks the same of a kernel.
+int prepare_lists(Pool& p) {
+    if (p.lists_ready) return CA_OK;
+    const SparseKernel k = pick_sparse(p.cfg);
+    if (!k.fn) return CA_ERR_UNSUPPORTED;
+    size_t smem;
+    sparse_stages(k, &smem);
+    if (cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
+        cudaFuncSetAttribute(select_fn(p.cfg), cudaFuncAttributeMaxDynamicSharedMemorySize, kMostChunks * 4) !=
+            cudaSuccess)
+        return CA_ERR_CUDA;
+    p.lists_ready = true;
+    return CA_OK;
 }
 
 size_t list_parts_bytes(const Pool& p) {

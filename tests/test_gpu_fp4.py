@@ -58,7 +58,7 @@ class Cache:
 
     def check_rows(self):
         """Every sequence's rows, read back, are the oracle's values rounded to fp16."""
-        ids = sorted(self.trie.seqs) if hasattr(self.trie, "seqs") else list(range(len(self.seqs)))
+        ids = list(range(len(self.seqs)))
         k, v = self.pool.read_batch(ids)
         at = 0
         for i in ids:
@@ -302,3 +302,62 @@ def test_prompts_longer_than_one_launch(torch_cuda):
     pool.remove_batch([0, 1, 2, 3])
     pool.insert(7, np.arange(100, 8100), k[:, :8000].contiguous(), v[:, :8000].contiguous())
     np.testing.assert_array_equal(pool.read(7)[0].cpu().numpy(), half(F4.roundtrip(k[:, :8000].cpu().numpy(), 1.0)))
+
+
+def test_offsets_past_32_bits(torch_cuda):
+    """A pool of 5.5 GB: the last slots' rows are stored, bounded, read back and
+    attended to (whole and by lists) as the first ones'."""
+    from prefix_shared_decode_gb300 import Pool, decode_attention, select_chunks, sparse_decode_attention
+    torch = torch_cuda
+    L, H, D, c, n = 64, 32, 128, 64, 640
+    pool = Pool(L, H, D, c, 300, kv_dtype="fp4", chunk_bounds=True)
+    g = torch.Generator("cuda").manual_seed(2)
+    k, v = (torch.randn((L, n, H, D), generator=g, device="cuda", dtype=torch.float16) for _ in range(2))
+    for i in range(30):
+        pool.insert(i, np.arange(n) + 1000 * i, k, v)
+    assert min(pool.seq_slots(29)) * L * H * 9216 > 2 ** 32
+    last, first = pool.read(29), pool.read(0)
+    assert torch.equal(last[0], first[0]) and torch.equal(last[1], first[1])
+    wk, wv = (F4.roundtrip(t[-1].cpu().numpy(), 1.0) for t in (k, v))
+    np.testing.assert_array_equal(last[0][-1].cpu().numpy(), half(wk))
+    np.testing.assert_array_equal(last[1][-1].cpu().numpy(), half(wv))
+    q = torch.randn((2, H, D), generator=g, device="cuda", dtype=torch.float16)
+    qn = q.cpu().numpy()
+    sched = pool.schedule([29, 3], chunk_lists=True)
+    a = np.stack([A.softmax_attention(x, wk, np.abs(wv), D ** -0.5) for x in qn])
+    want = np.stack([A.softmax_attention(x, wk, wv, D ** -0.5) for x in qn])
+    near(decode_attention(pool, sched, q, layer=L - 1).cpu().numpy(), want, a)
+    lists = select_chunks(pool, sched, q, 10, layer=L - 1)
+    near(sparse_decode_attention(pool, sched, q, lists, layer=L - 1).cpu().numpy(), want, a)
+    hi = torch.from_numpy(wk.reshape(10, c, H, D).max(1)).half()
+    assert torch.equal(pool.bounds_view()[pool.seq_slots(29), L - 1, :, 0].cpu(), hi)
+    assert sched.device_status() == 0
+
+
+def test_a_stalled_producer_times_out(torch_cuda, lib):
+    """The waits of the fp4 kernel are bounded: a call whose producer never
+    issues a copy reports CA_ERR_TIMEOUT, the next one runs."""
+    from prefix_shared_decode_gb300 import decode_attention
+    torch = torch_cuda
+    x = Cache(torch, 17, 16, 64, L=1)
+    q = x.rng.standard_normal((12, 2, 64)).astype(np.float16)
+    qd = torch.from_numpy(q).cuda()
+    sched = x.pool.schedule(list(range(12)))
+    assert lib.ca_sched_inject_stall(sched.handle, 1) == 0
+    decode_attention(x.pool, sched, qd)
+    assert sched.device_status() == -8
+    x.check(decode_attention(x.pool, sched, qd).cpu().numpy(), list(range(12)), 0, q, 1 / 8)
+    assert sched.device_status() == 0
+
+
+def test_appends_one_token_at_a_time(torch_cuda):
+    """Every place in a chunk, and the first of the next, filled alone: a value
+    byte holds two tokens, and the one that was there stays."""
+    torch = torch_cuda
+    for c, D in ((16, 128), (64, 64)):
+        x = Cache(torch, 33 + c, c, D, G=1, Hkv=1, L=2, v_scale=0.5, n_seqs=1, seqs=[list(range(3))])
+        for j in range(c + 2):
+            x.append(0, [1000 + j])
+            if j % 7 == 0 or j > c - 4:
+                x.check_rows()
+        x.check_rows()

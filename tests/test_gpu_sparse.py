@@ -269,6 +269,108 @@ def test_graph_and_streams(torch_cuda):
     assert all(s.device_status() == 0 for s in [sched, *scheds])
 
 
+@pytest.mark.parametrize("kv_dtype,G,D", [("fp16", 4, 128), ("fp4", 64, 64), ("fp16", 32, 256)])
+def test_channels_of_large_keys(torch_cuda, kv_dtype, G, D):
+    """A few channels a hundred times the others', as models' keys have: the
+    order among the chunks is still that of the exact scores."""
+    from prefix_shared_decode_gb300 import select_chunks
+    c = 16
+    x = Cache(torch_cuda, 40 + G, kv_dtype, c, D, G, 1, [1], rows=[(np.zeros((1, 1, 1, D), np.float16),) * 2])
+    k = x.draw(900 * c)
+    k[..., 3] += 300
+    k[..., D // 2] *= 60
+    x = Cache(torch_cuda, 41 + G, kv_dtype, c, D, G, 1, [900 * c], rows=[(k, k)])
+    q = x.queries(1, G)
+    sched = x.pool.schedule([0], chunk_lists=True)
+    for top_k in (5, 64, 400):
+        got = select_chunks(x.pool, sched, x.dev(q), top_k).cpu().numpy()
+        np.testing.assert_array_equal(got, x.want_lists([0], 0, q, top_k, 1, 1))
+
+
+def test_the_longest_contexts(torch_cuda):
+    """49152 chunks are scored; one more is refused, while lists of the
+    caller's own still reach every chunk."""
+    from prefix_shared_decode_gb300 import CAError, Pool, select_chunks, sparse_decode_attention
+    torch = torch_cuda
+    c, D, n = 16, 64, 49152 * 16
+    g = torch.Generator("cuda").manual_seed(3)
+    k, v = (torch.randn((1, n + 1, 1, D), generator=g, device="cuda", dtype=torch.float16) for _ in range(2))
+    pool = Pool(1, 1, D, c, 49160, chunk_bounds=True)
+    pool.insert(0, np.arange(n), k[:, :n].contiguous(), v[:, :n].contiguous())
+    q = torch.randn((1, 1, D), generator=g, device="cuda", dtype=torch.float16)
+    sched = pool.schedule([0], chunk_lists=True)
+    got = select_chunks(pool, sched, q, 100, sink=2, recent=3).cpu().numpy()[0, 0]
+    bnd = k[0, :n, 0].view(-1, c, D).double()
+    qd = q[0, 0].double()
+    score = torch.maximum(qd * bnd.amax(1), qd * bnd.amin(1)).sum(-1).cpu().numpy()
+    np.testing.assert_array_equal(got, SP.select(score, 100, 2, 3))
+    pool.append(0, [n], k[:, n:].contiguous(), v[:, n:].contiguous())
+    sched = pool.schedule([0], chunk_lists=True)
+    with pytest.raises(CAError) as e:
+        select_chunks(pool, sched, q, 100)
+    assert e.value.name == "CA_ERR_UNSUPPORTED"
+    lists = torch.tensor([[[49152, 7]]], dtype=torch.int32, device="cuda")
+    out = sparse_decode_attention(pool, sched, q, lists).cpu().numpy()
+    rows = list(range(7 * c, 8 * c)) + [n]
+    kk, vv = (t[0, rows].cpu().numpy().astype(np.float64) for t in (k, v))
+    want = SP.attention(q[0].cpu().numpy(), kk, vv, [[0, 1]], c, D ** -0.5)
+    near(out[0], want, SP.attention(q[0].cpu().numpy(), kk, np.abs(vv), [[0, 1]], c, D ** -0.5))
+    assert sched.device_status() == 0
+
+
+def test_captured_before_any_call(torch_cuda):
+    """A graph whose capture is the pool's first use of both calls, and two
+    runs of the same lists that agree bit for bit however the pieces arrive."""
+    from prefix_shared_decode_gb300 import select_chunks, sparse_decode_attention
+    torch = torch_cuda
+    x = Cache(torch, 8, "fp4", 32, 64, 2, 1, [2000, 1777])
+    q = x.queries(2, 2)
+    qd = x.dev(q)
+    sched = x.pool.schedule([1, 0], chunk_lists=True)
+    lists = torch.empty((2, 1, 40), dtype=torch.int32, device="cuda")
+    out = torch.empty_like(qd)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        select_chunks(x.pool, sched, qd, 40, out=lists)
+        sparse_decode_attention(x.pool, sched, qd, lists, out=out)
+    graph.replay()
+    want = x.want_lists([1, 0], 0, q, 40, 1, 1)
+    np.testing.assert_array_equal(lists.cpu().numpy(), want)
+    x.check_attention(out.cpu().numpy(), [1, 0], 0, q, want)
+    first = out.clone()
+    for _ in range(20):
+        graph.replay()
+        assert torch.equal(out, first)
+
+
+def test_flat_pools_and_wide_lists(torch_cuda):
+    """A pool without sharing; lists wider than any context; one entry."""
+    from prefix_shared_decode_gb300 import Pool, select_chunks, sparse_decode_attention
+    torch = torch_cuda
+    rng = np.random.default_rng(9)
+    c, D, L = 16, 128, 3
+    pool = Pool(L, 2, D, c, 60, no_sharing=True, kv_dtype="fp8", chunk_bounds=True)
+    k, v = rng.standard_normal((2, L, 200, 2, D)).astype(np.float16)
+    dk, dv = torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda()
+    for i in range(3):
+        pool.insert(i, list(range(200)), dk, dv)
+    sched = pool.schedule([2, 0, 1], chunk_lists=True)
+    q = rng.standard_normal((3, 2, D)).astype(np.float16)
+    qd = torch.from_numpy(q).cuda()
+    hk, hv = held(k, "fp8", 1.0), held(v, "fp8", 1.0)
+    for top_k in (1000, 13, 1):
+        lists = select_chunks(pool, sched, qd, top_k, layer=2, sink=0)
+        got = sparse_decode_attention(pool, sched, qd, lists, layer=2).cpu().numpy()
+        lists = lists.cpu().numpy()
+        for r in range(3):
+            want = [SP.select(s, top_k, 0, 1) for s in SP.scores(q[r], SP.bounds(hk[2], c))]
+            np.testing.assert_array_equal(lists[r], want)
+            near(got[r], SP.attention(q[r], hk[2], hv[2], want, c, D ** -0.5),
+                 SP.attention(q[r], hk[2], np.abs(hv[2]), want, c, D ** -0.5))
+    assert sched.device_status() == 0
+
+
 def test_refusals(torch_cuda, lib):
     from prefix_shared_decode_gb300 import CAError, Pool, select_chunks, sparse_decode_attention
     torch = torch_cuda
