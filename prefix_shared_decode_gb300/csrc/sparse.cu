@@ -535,11 +535,11 @@ __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const ListPa
 // `qdim(kk, t)`: first of a lane's dims of step kk, held in two registers
 // (kPair: four consecutive dims, else two and the two 8 further).
 // ---------------------------------------------------------------------------
-template <int EB, int C, int D, int NB>
+template <int EB, int C, int D, int NB, bool ONE>
 struct Frag;
 
 template <int C, int D, int NB>
-struct Frag<2, C, D, NB> {                       // fp16: ldmatrix from the swizzled tiles
+struct Frag<2, C, D, NB, false> {                       // fp16: ldmatrix from the swizzled tiles
     static constexpr int kStage = 4 * C * D;
     static constexpr bool kPair = false;
     __device__ static int tok(int g) { return g; }
@@ -572,7 +572,7 @@ struct Frag<2, C, D, NB> {                       // fp16: ldmatrix from the swiz
 };
 
 template <int C, int D, int NB>
-struct Frag<1, C, D, NB> {                       // fp8: bytes widened into the fragments
+struct Frag<1, C, D, NB, false> {                       // fp8: bytes widened into the fragments
     static_assert(D == 128, "fp8 pools have head_dim 128");
     static constexpr int kStage = 2 * C * D;
     static constexpr bool kPair = true;
@@ -620,15 +620,15 @@ struct Frag<1, C, D, NB> {                       // fp8: bytes widened into the 
     }
 };
 
-template <int C, int D, int NB>
-struct Frag<0, C, D, NB> {                       // fp4
+template <int C, int D, int NB, bool ONE>
+struct Frag<0, C, D, NB, ONE> {                  // fp4; ONE: a single query row, in every column
     static constexpr int kStage = F4Tile<C, D>::kBytes;
     static constexpr bool kPair = true;
     __device__ static int tok(int g) { return f4_token(g); }
     __device__ static int dim(int db, int half, int g) { return 16 * db + 2 * g + half; }
     __device__ static void scores(const uint8_t* st, int blk, const uint32_t (&qb)[NB][D / 16][2], float (&s)[NB][4],
                                   int lane) {
-        f4_scores<C, D, NB, false>(st, blk, qb, s, lane);
+        f4_scores<C, D, NB, ONE>(st, blk, qb, s, lane);
     }
     __device__ static void pv(const uint8_t* st, int blk, const uint32_t (&pb)[NB][2], float (&o)[NB][D / 16][4],
                               int lane) {
@@ -641,15 +641,17 @@ struct Frag<0, C, D, NB> {                       // fp4
 // 8 NB rows of its group) with its top_k list entries; the units' entries are
 // laid end to end and cut into equal stretches, one per resident CTA, so every
 // CTA streams the same number of tiles whatever the batch.  (Clusters of up to
-// eight CTAs per unit were measured first: 75 us where this takes 61, 512 units
-// on 456 resident CTAs.)  A producer warp looks 32 entries up at once (list ->
+// eight CTAs per unit took 75 us where the stretches took 69, with the same
+// code for a tile: 512 units of 64 fp4 tiles on 456 resident CTAs.)  A producer warp looks 32 entries up at once (list ->
 // slot -> token count) and keeps a ring of tiles in flight, across units; the
 // consumer warps take the tiles' blocks of 16 tokens with an online softmax.
 // Each ring slot belongs to the warps of one group, a warp per block of a tile.
-// An fp4 tile costs more to widen than to fetch (some 300 issue slots of each
-// SM partition, the ALU's half of them, against 260 for its bytes): three CTAs
-// per SM, 69 us for 512 units of 64 tiles; two of eight warps 69, four of four
-// 70, one of twelve 83.
+// Units of 64 tiles of 64 tokens, head_dim 128: 128 of fp16 45 us, 89% of the
+// copy rate, bound by DRAM; 128 of fp8 31 us (65%); 512 of fp4 59 us (77%),
+// bound by the instructions that widen a tile (58% of the issue slots, 52% of
+// the ALU) in the shadow of its loads: three CTAs per SM hide most of them
+// (three of four warps and two of eight 69 us before the values' codes lay in
+// pairs, four of four 70, one of twelve 83).
 // A unit cut between CTAs leaves its pieces' partial triples in the schedule's
 // buffer, and the CTA that finishes its last piece (a counter per unit, which
 // it clears again) merges them in the order of the pieces: nothing waits, and
@@ -662,9 +664,9 @@ constexpr int kSpWarps = 4, kSpThreads = 32 * (kSpWarps + 1), kSpStages = 12;
 // and normal numbers down to 2^-19 (or less) of the largest.
 constexpr float kSpLift = 5.f, kSpSlack = 8.f;
 
-template <int EB, int C, int D, int NB>
+template <int EB, int C, int D, int NB, bool ONE>
 struct SpShared {
-    using F = Frag<EB, C, D, NB>;
+    using F = Frag<EB, C, D, NB, ONE>;
     static constexpr int kGroups = kSpWarps / (C / 16);           // of warps; the ring is a multiple of them
     static constexpr int kPerSm = EB == 0 && NB == 1 ? 3 : 2;     // resident CTAs
     static constexpr int kRows = 8 * NB;
@@ -680,11 +682,12 @@ __device__ __forceinline__ void sp_consumers() { asm volatile("bar.sync 1, %0;" 
 // Entries [first, last) of CTA c when `total` are cut into `grid` stretches.
 __device__ __forceinline__ long long cut_at(long long total, int grid, int c) { return total * c / grid; }
 
-template <int EB, int C, int D, int NB>
-__global__ void __launch_bounds__(kSpThreads, SpShared<EB, C, D, NB>::kPerSm)
+template <int EB, int C, int D, int NB, bool ONE>
+__global__ void __launch_bounds__(kSpThreads, SpShared<EB, C, D, NB, ONE>::kPerSm)
 sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListParams p) {
-    using F = Frag<EB, C, D, NB>;
-    using SM = SpShared<EB, C, D, NB>;
+    using F = Frag<EB, C, D, NB, ONE>;
+    using SM = SpShared<EB, C, D, NB, ONE>;
+    constexpr int NR = ONE ? 1 : 2;                        // query rows among a lane's two columns
     constexpr int R = SM::kRows, NBLK = C / 16, RS = SM::kRow, W = kSpWarps, NG = SM::kGroups;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int S = p.n_stages;
@@ -827,8 +830,8 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
         uint32_t qb[NB][D / 16][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-            const bool there = nb * 8 + g < rows;
-            const uint16_t* q = p.q + (row0 + (there ? nb * 8 + g : 0)) * D;
+            const bool there = ONE || nb * 8 + g < rows;
+            const uint16_t* q = p.q + (row0 + (!ONE && there ? nb * 8 + g : 0)) * D;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 uint2 x = make_uint2(0u, 0u);
@@ -869,7 +872,7 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < 4; k += 3 - NR) {
                         x[nb][k] = ((k >> 1) ? in1 : in0) ? x[nb][k] * p.scale_log2 : -INFINITY;
                         grow = grow || x[nb][k] > m[nb][k & 1] + (kSpLift + kSpSlack);
                     }
@@ -878,7 +881,7 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) {
+                        for (int r = 0; r < NR; ++r) {
                             float mx = fmaxf(x[nb][r], x[nb][r + 2]);
 #pragma unroll
                             for (int d = 4; d <= 16; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, d));
@@ -896,11 +899,17 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
                 uint32_t pb[NB][2];
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
-                    const float u0_ = m[nb][0] == -INFINITY ? 0.f : m[nb][0], u1_ = m[nb][1] == -INFINITY ? 0.f : m[nb][1];
-                    const float p0 = ex2(x[nb][0] - u0_), p1 = ex2(x[nb][1] - u1_);
-                    const float p2 = ex2(x[nb][2] - u0_), p3 = ex2(x[nb][3] - u1_);
-                    s[nb][0] += p0 + p2;                   // the lane's tokens; summed over g at the end
-                    s[nb][1] += p1 + p3;
+                    // (the sums are of the lane's tokens, until the piece ends)
+                    const float u0_ = m[nb][0] == -INFINITY ? 0.f : m[nb][0];
+                    const float p0 = ex2(x[nb][0] - u0_), p2 = ex2(x[nb][2] - u0_);
+                    float p1 = p0, p3 = p2;
+                    s[nb][0] += p0 + p2;
+                    if constexpr (!ONE) {
+                        const float u1_ = m[nb][1] == -INFINITY ? 0.f : m[nb][1];
+                        p1 = ex2(x[nb][1] - u1_);
+                        p3 = ex2(x[nb][3] - u1_);
+                        s[nb][1] += p1 + p3;
+                    }
                     pb[nb][0] = movm_trans(pack_half2(p0, p1));
                     pb[nb][1] = movm_trans(pack_half2(p2, p3));
                 }
@@ -917,28 +926,29 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
         // leaves the sum in the exchange area for all of them to write out
         // (three copies there leave room for a third tile of 32 KB).
         auto put = [&](float* dst) {                       // [row][D] with the rows' stride
+            if (ONE && t != 0) return;
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int db = 0; db < D / 16; ++db)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
+                    for (int k = 0; k < 4; k += 3 - NR)
                         dst[(nb * 8 + 2 * t + (k & 1)) * RS + F::dim(db, k >> 1, g)] = o[nb][db][k];
         };
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+            for (int r = 0; r < NR; ++r)
 #pragma unroll
                 for (int d = 4; d <= 16; d <<= 1) s[nb][r] += __shfl_xor_sync(kFull, s[nb][r], d);
         sp_consumers();                                 // the last piece has been written out
         if (warp > 0) {
             put(exch + (size_t)(warp - 1) * R * RS);
-            if (g == 0)
+            if (g == 0 && (!ONE || t == 0))
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                    for (int r = 0; r < 2; ++r)
+                    for (int r = 0; r < NR; ++r)
                         *reinterpret_cast<float2*>(wms + (warp * R + nb * 8 + 2 * t + r) * 2) =
                             make_float2(m[nb][r], s[nb][r]);
         }
@@ -947,8 +957,8 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int row = nb * 8 + 2 * t + r;
+                for (int r = 0; r < NR; ++r) {
+                    const int row = nb * 8 + (ONE ? 0 : 2 * t + r);
                     float2 q[W - 1];
                     float M = m[nb][r];
 #pragma unroll
@@ -974,7 +984,7 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
                             o[nb][db][r + 2] += ak * src[F::dim(db, 1, g)];
                         }
                     }
-                    if (g == 0) *reinterpret_cast<float2*>(wms + row * 2) = make_float2(M, sum);
+                    if (g == 0 && (!ONE || t == 0)) *reinterpret_cast<float2*>(wms + row * 2) = make_float2(M, sum);
                 }
             __syncwarp();
             put(exch);
@@ -1123,18 +1133,22 @@ struct SparseKernel {
     int rows = 0, stage = 0, fixed = 0;      // rows of a unit; bytes of a stage, of the rest
     int groups = 0, per_sm = 0;              // the ring's slots come in multiples of `groups`; CTAs per SM
 };
-template <int EB, int C, int D, int NB>
+template <int EB, int C, int D, int NB, bool ONE = false>
 SparseKernel sparse_of() {
-    using SM = dev::SpShared<EB, C, D, NB>;
-    return {reinterpret_cast<const void*>(&dev::sparse_attention_kernel<EB, C, D, NB>), SM::kRows, SM::F::kStage,
+    using SM = dev::SpShared<EB, C, D, NB, ONE>;
+    return {reinterpret_cast<const void*>(&dev::sparse_attention_kernel<EB, C, D, NB, ONE>), SM::kRows, SM::F::kStage,
             (int)SM::bytes(0), SM::kGroups, SM::kPerSm};
 }
 // Rows of a group per CTA: 8, or 16 for groups of more (at head_dim 256 the
-// accumulators of 16 rows do not fit the registers).
+// accumulators of 16 rows do not fit the registers); a single one by itself in
+// an fp4 pool, which is bound by instructions.
 template <int EB, int C, int D>
 SparseKernel pick_rows(int group) {
     if constexpr (D <= 128) {
         if (group > 8) return sparse_of<EB, C, D, 2>();
+    }
+    if constexpr (EB == 0) {                   // 512 units of one row: 58.8 us, with eight columns 62.3
+        if (group == 1) return sparse_of<EB, C, D, 1, true>();
     }
     return sparse_of<EB, C, D, 1>();
 }

@@ -93,7 +93,8 @@ class Cache:
 POOLS = [("fp16", 16, 64, 1, 2), ("fp16", 64, 128, 4, 2), ("fp16", 32, 256, 2, 1), ("fp16", 16, 256, 12, 1),
          ("fp16", 64, 128, 16, 1), ("fp16", 32, 128, 64, 1), ("fp8", 64, 128, 1, 3), ("fp8", 16, 128, 8, 1),
          ("fp8", 32, 128, 9, 1), ("fp4", 64, 128, 1, 3), ("fp4", 16, 64, 4, 2), ("fp4", 32, 128, 16, 1),
-         ("fp4", 64, 64, 3, 2), ("fp16", 32, 64, 8, 2)]
+         ("fp4", 64, 64, 3, 2), ("fp16", 32, 64, 8, 2), ("fp4", 16, 64, 1, 2),
+         ("fp4", 32, 128, 1, 1)]
 
 
 @pytest.mark.parametrize("kv_dtype,c,D,G,Hkv", POOLS)
