@@ -311,11 +311,11 @@ def measured_peak():
     return FALLBACK_HBM_GBS, "fallback"
 
 
-def source_fingerprint(path: str) -> str:
-    """sha256[:16] of a C++/CUDA source with comments and whitespace removed,
+def source_fingerprint(*paths: str) -> str:
+    """sha256[:16] of C++/CUDA sources with comments and whitespace removed,
     so that only code changes (not comment edits) change it."""
     import re
-    text = open(path).read()
+    text = "\n".join(open(p).read() for p in paths)
     text = re.sub(r"/\*.*?\*/", " ", text, flags=re.S)
     text = re.sub(r"//[^\n]*", " ", text)
     text = re.sub(r"\s+", " ", text)
@@ -325,7 +325,8 @@ def source_fingerprint(path: str) -> str:
 def profile_record(key: str):
     """The committed ncu record for a kernel on a workload, if it was taken on
     the current kernel code (None otherwise)."""
-    h = source_fingerprint(os.path.join(ROOT, "prefix_shared_decode_gb300", "csrc", "kernels.cu"))
+    csrc = os.path.join(ROOT, "prefix_shared_decode_gb300", "csrc")
+    h = source_fingerprint(*(os.path.join(csrc, f) for f in ("kernels.cu", "device.cuh", "row_blocks.cuh")))
     path = os.path.join(ROOT, "profiles", "traffic.json")
     if not os.path.exists(path):
         return None
@@ -334,7 +335,7 @@ def profile_record(key: str):
     except ValueError:
         return None
     e = d.get(key)
-    if not e or e.get("kernels_cu_code_sha256_16") != h:
+    if not e or e.get("code_sha256_16") != h:
         return None
     return e
 

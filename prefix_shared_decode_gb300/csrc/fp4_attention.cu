@@ -7,19 +7,23 @@
 //  * All products are taken transposed, tokens on the rows and query rows on
 //    the columns (S^T = K Q^T, O^T += V^T P^T), 16 tokens at a time: the
 //    tile's bytes widen straight into operand registers (fp4.cuh).
-//  * Units of up to 16 query rows (every sequence-first unit of ordinary head
-//    groups, chunk-first ones of few sharers): each of the four warps takes
-//    its own 16 tokens of a tile and nothing is exchanged until the head ends.
-//  * Units of more rows: the warps widen the tile once into operand images in
-//    shared memory and split the rows 16 by 16 (at most 32 rows: two warps
-//    share them and split the tokens).
+//  * Units of up to 8 query rows (every sequence-first unit of head groups up
+//    to 8, chunk-first ones of few sharers): each of the four warps takes its
+//    own 16 tokens of a tile and nothing is exchanged until the head ends.
+//  * Units of more rows: the warps widen the tile once into fp16 tiles in
+//    shared memory, 32 tokens at a time, and take a 16-row block each (with
+//    fewer than four blocks also a share of the tokens).
 //
 // What bounds it: the widening (two ALU cycles for each pair of values, and a
 // multiply for its scale), not the bytes: a single-row tile costs its four
 // warps about 250 instructions each.  So the path is written for issue slots:
 // a vote decides whether the softmax reference must rise, sums stay per lane
 // until the head ends, queries of the next head are fetched a head ahead, and
-// three CTAs per SM (128 registers a thread) cover the latencies.
+// three CTAs per SM (128 registers a thread) cover the latencies.  65536 tiles
+// of single rows alone take 114 us, 80% of the copy rate; 64 sequences of 512
+// tokens of their own under 4096 shared ones, 32 heads of 128 dims, 61 us (50%
+// of the issue slots, 43% of the ALU, 36% of DRAM), where the shared tiles'
+// trip through shared memory and its waits take the rest.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -42,8 +46,8 @@ constexpr float kLift = 5.f, kSlack = 8.f;
 // Shared memory: the ring, two areas, (m, s) per warp and row.  For units of up
 // to 8 rows the areas hold the warps' outputs at the end of a head, in turn; for
 // others a shared tile widened to fp16 (32 tokens at a time: with all 64 the
-// ring had two slots instead of four, and the other units' tiles took 1.91 ns
-// each instead of 1.67 over the card) and the queries.
+// ring had two slots instead of four, and single-row tiles took 1.91 ns each
+// over the card instead of 1.73) and the queries.
 template <int C, int D>
 struct F4Smem {
     static constexpr int kStage = F4Tile<C, D>::kBytes;
@@ -190,10 +194,10 @@ __device__ __forceinline__ bool f4_tiles_own(F4Ctx& c, int tiles, const uint32_t
 }
 
 // Tokens [base, base + N) of a tile widened once for all warps, into the fp16 K
-// and V tiles that the 16-row blocks read (code * scale is exact in fp16).  A thread takes 16 bytes
-// (8 at D = 64) of a row's key codes: four dims of every 16, and as many of a
-// pair's value codes: two dims of every 16 of both tokens; consecutive threads
-// take rows whose swizzled 16-byte columns differ.
+// and V tiles that the 16-row blocks read (code * scale is exact in fp16).  A
+// thread takes 16 bytes (8 at D = 64) of a row's key codes: four dims of every
+// 16, and as many of a pair's value codes: two dims of every 16 of both tokens;
+// consecutive threads take rows whose swizzled 16-byte columns differ.
 template <int C, int D, int N>
 __device__ __forceinline__ void f4_tile_to_f16(const uint8_t* src, int base, uint8_t* kd, uint8_t* vd, int tid) {
     using T = F4Tile<C, D>;
