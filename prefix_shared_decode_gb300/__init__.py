@@ -57,7 +57,11 @@ def _at(a) -> int:
 def _ints(kind: str, a) -> array:
     """A short list of integers ("q": int64, "i": int32) with an address that
     costs less to ask for than a numpy array's."""
-    return array(kind, a if isinstance(a, (list, tuple)) else np.asarray(a).tolist())
+    a = a if isinstance(a, (list, tuple)) else np.asarray(a).tolist()
+    try:
+        return array(kind, a)
+    except TypeError:                   # floats, say: cut as numpy cuts them
+        return array(kind, np.asarray(a, dtype=np.int64).tolist())
 
 
 class Pool:
@@ -185,7 +189,7 @@ class Pool:
             tok = np.ascontiguousarray(np.concatenate([np.asarray(t, dtype=np.int32) for t in token_lists]))
         else:
             lens, tok = _ints("i", lengths), _i32(token_lists)
-        if len(lens) != len(ids) or tok.size < sum(lens):
+        if len(lens) < len(ids) or tok.size < sum(lens[:len(ids)]):
             raise ValueError("seq_ids, lengths and tokens do not go together")
         kp = vp = None
         if k is not None:
