@@ -473,7 +473,8 @@ int ca_decode_attention_static_ws(const ca_pool* pool, const ca_sched* sched,
  * fp16 [b][n_heads][head_dim], 16-byte aligned.  Errors: CA_ERR_STALE;
  * CA_ERR_INVALID (a schedule without lists, a pool without bounds, top_k < 1,
  * sink + recent > top_k, bad layer, NULL or misaligned pointers);
- * CA_ERR_UNSUPPORTED (q_len > 1, more than 2^31 list entries); CA_ERR_CUDA. */
+ * CA_ERR_UNSUPPORTED (q_len > 1, more than 2^31 - 257 list entries in all);
+ * CA_ERR_CUDA. */
 int ca_select_chunks(const ca_pool* pool, const ca_sched* sched, int32_t layer,
                      const void* q_dev, int32_t top_k, int32_t sink, int32_t recent,
                      int32_t* lists_dev, void* stream);

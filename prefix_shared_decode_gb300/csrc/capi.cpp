@@ -149,7 +149,14 @@ int ca_pool_create_ex(const ca_pool_config_ex* cfg_ex, void* kv_dev, size_t kv_b
         p->heap.resize(cfg->capacity_slots);
         for (int32_t i = 0; i < cfg->capacity_slots; ++i) p->heap[i] = i;   // sorted = min-heap
         if (kv_dev) {
-            if (cudaGetDevice(&p->device) != cudaSuccess) return CA_ERR_CUDA;
+            // The pool's device is its memory's, whatever device is current here
+            // (memory that belongs to no one device: the current one).
+            cudaPointerAttributes at{};
+            if (cudaGetDevice(&p->device) != cudaSuccess || cudaPointerGetAttributes(&at, kv_dev) != cudaSuccess)
+                return CA_ERR_CUDA;
+            if (at.type == cudaMemoryTypeDevice) p->device = at.device;
+            const DeviceGuard dev(p->device);
+            if (!dev.ok) return CA_ERR_CUDA;
             if (cudaDeviceGetAttribute(&p->num_sms, cudaDevAttrMultiProcessorCount, p->device) != cudaSuccess)
                 return CA_ERR_CUDA;
             p->sms = p->num_sms;
@@ -364,8 +371,8 @@ int ca_build_schedule(ca_pool* pool, const int64_t* seq_ids, int32_t b, ca_sched
 int ca_build_schedule_ex(ca_pool* pool, const int64_t* seq_ids, int32_t b, int32_t q_len, uint32_t flags,
                          ca_sched** inout, void* stream) {
     const Range range("ca_build_schedule");
-    if (!pool || !inout || !seq_ids || b < 1 || q_len < 1 || (flags & ~(CA_SCHED_NO_TPP | CA_SCHED_CAUSAL | CA_SCHED_CHUNK_LISTS)))
-        return CA_ERR_INVALID;
+    if (!pool || !inout || !seq_ids || b < 1 || q_len < 1) return CA_ERR_INVALID;
+    if (flags & ~(CA_SCHED_NO_TPP | CA_SCHED_CAUSAL | CA_SCHED_CHUNK_LISTS)) return CA_ERR_INVALID;
     if ((int64_t)q_len * (pool->cfg.n_heads / kv_heads(pool->cfg)) > max_query_rows(pool->cfg))
         return CA_ERR_UNSUPPORTED;
     if (q_len == 1) flags &= ~CA_SCHED_CAUSAL;       // one query token sees its whole context
@@ -616,7 +623,8 @@ static int list_checks(const ca_pool* pool, const ca_sched* s, int32_t layer, co
     if (s->q_len != 1) return CA_ERR_UNSUPPORTED;
     if (layer < 0 || layer >= pool->cfg.n_layers || top_k < 1) return CA_ERR_INVALID;
     if (!q_dev || !aligned(q_dev, 16) || !lists_dev || !aligned(lists_dev, 4)) return CA_ERR_INVALID;
-    if ((int64_t)s->t.b * kv_heads(pool->cfg) * top_k > INT32_MAX) return CA_ERR_UNSUPPORTED;
+    // (the kernels step through a list by up to 256 entries at a time, in 32 bits)
+    if ((int64_t)s->t.b * kv_heads(pool->cfg) * top_k > INT32_MAX - 256) return CA_ERR_UNSUPPORTED;
     return CA_OK;
 }
 

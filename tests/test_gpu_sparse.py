@@ -421,3 +421,18 @@ def test_refusals(torch_cuda, lib):
     x.append(0, 40)
     refused("CA_ERR_STALE", lambda: select_chunks(x.pool, sched, q, 3))
     refused("CA_ERR_STALE", lambda: sparse_decode_attention(x.pool, sched, q, lists))
+
+
+def test_lists_whose_indexes_would_overflow(torch_cuda, lib):
+    """Refused on the host: a single row's list within a step of 2^31 entries."""
+    from prefix_shared_decode_gb300 import kernel_launches
+    x = Cache(torch_cuda, 7, "fp16", 16, 64, 1, 1, [100])
+    sched = x.pool.schedule([0], chunk_lists=True)
+    q = x.dev(x.queries(1, 1))
+    stream = torch_cuda.cuda.current_stream().cuda_stream
+    a = (x.pool.handle, sched.handle, 0, q.data_ptr())
+    before = kernel_launches()
+    for k in (2**31 - 1, 2**31 - 256):
+        assert lib.ca_select_chunks(*a, k, 0, 0, q.data_ptr(), stream) == -9
+        assert lib.ca_sparse_attention(*a, q.data_ptr(), k, q.data_ptr(), 1.0, stream) == -9
+    assert kernel_launches() == before
