@@ -95,6 +95,12 @@ __device__ __forceinline__ void f16x2_from_e2m1x8(uint32_t w, uint32_t (&r)[4]) 
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
         : "r"(w));
 }
+__device__ __forceinline__ void f16x2_from_e2m1x4(uint16_t w, uint32_t (&r)[2]) {
+    asm("{\n\t.reg .b8 a, b;\n\tmov.b16 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t}"
+        : "=r"(r[0]), "=r"(r[1])
+        : "h"(w));
+}
 __device__ __forceinline__ void f16x2_from_e4m3x4(uint32_t w, uint32_t (&r)[2]) {
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
         "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"

@@ -10,9 +10,9 @@
 //  * Units of up to 8 query rows (every sequence-first unit of head groups up
 //    to 8, chunk-first ones of few sharers): each of the four warps takes its
 //    own 16 tokens of a tile and nothing is exchanged until the head ends.
-//  * Units of more rows: the warps widen the tile once into fp16 tiles in
-//    shared memory, 32 tokens at a time, and take a 16-row block each (with
-//    fewer than four blocks also a share of the tokens).
+//  * Units of more rows: 64 tokens at a time, the warps split the tokens for the
+//    scores and the dims for the outputs, so that each code is widened once;
+//    the weights pass through shared memory.
 //
 // What bounds it: the widening (two ALU cycles for each pair of values, and a
 // multiply for its scale), not the bytes: a single-row tile costs its four
@@ -21,12 +21,14 @@
 // until the head ends, queries of the next head are fetched a head ahead, and
 // three CTAs per SM (128 registers a thread) cover the latencies.  65536 tiles
 // of single rows alone take 114 us, 80% of the copy rate; 64 sequences of 512
-// tokens of their own under 4096 shared ones, 32 heads of 128 dims, 61 us (50%
-// of the issue slots, 43% of the ALU, 36% of DRAM), where the shared tiles'
-// trip through shared memory and its waits take the rest.
+// tokens of their own under 4096 shared ones, 32 heads of 128 dims, 55 us, of
+// which the single rows' tiles are half; a step of a shared tile (64 rows) takes
+// some 2100 cycles of an SM, 1150 of them its tensor products.  (Widening shared
+// tiles into fp16 in shared memory first, 16 rows a warp: 61 us.)
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <climits>
 
 #include "ca_internal.h"
@@ -44,17 +46,21 @@ constexpr int kF4Stages = 8, kF4Ring = 16;
 constexpr float kLift = 5.f, kSlack = 8.f;
 
 // Shared memory: the ring, two areas, (m, s) per warp and row.  For units of up
-// to 8 rows the areas hold the warps' outputs at the end of a head, in turn; for
-// others a shared tile widened to fp16 (32 tokens at a time: with all 64 the
-// ring had two slots instead of four, and single-row tiles took 1.91 ns each
-// over the card instead of 1.73) and the queries.
+// to 8 rows the areas hold the warps' outputs at the end of a head, in turn;
+// for others the weights of 64 tokens with their tables, and the queries.
+constexpr int kWideTok = 64;                                    // tokens of a step
+struct WideTables {
+    float ref[kQRows], thr[kQRows], fall[kQRows];               // softmax references; scores that raise them; 2^(old - new)
+    float top[kF4Warps][kQRows];                                // largest scores of each warp's tokens
+    int32_t qrow[kQRows], lim[kQRows], pid[kQRows];             // rows of q (of head 0); causal limits; partial ids
+};
 template <int C, int D>
 struct F4Smem {
     static constexpr int kStage = F4Tile<C, D>::kBytes;
-    static constexpr int kTok = C < 32 ? C : 32;                // tokens widened at a time
-    static constexpr int kImage = kTok * D * 2;                 // their keys (and their values)
     static constexpr int kOut8 = kF4Warps * 8 * D * 4;          // 8 rows of each warp
-    static constexpr int kExch = 2 * kImage > kOut8 ? 2 * kImage : kOut8;
+    static constexpr int kP = kQRows * kWideTok * 2;            // weights [row][token]
+    static constexpr int kWide = kP + (int)sizeof(WideTables);
+    static constexpr int kExch = kOut8 > kWide ? kOut8 : (kWide + 127) / 128 * 128;
     static constexpr int kMs = 2 * kF4Warps * 8 * 2 * 4;
     static constexpr int kQ = kQRows * D * 2;                   // query rows of a shared tile (= kOut8)
     static_assert(kQ >= kOut8, "the second area");
@@ -63,6 +69,15 @@ struct F4Smem {
 };
 
 __device__ __forceinline__ void f4_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kF4Warps * 32) : "memory"); }
+__device__ __forceinline__ bool f4_sync_any(bool x) {      // the same barrier: does x hold anywhere?
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, %2, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"((uint32_t)x), "n"(kF4Warps * 32)
+                 : "memory");
+    return r != 0u;
+}
 
 // What the consumers' loops share.
 struct F4Ctx {
@@ -169,6 +184,7 @@ __device__ __forceinline__ bool f4_tiles_own(F4Ctx& c, int tiles, const uint32_t
                                              F4State<D, NB>& a) {
     constexpr int NBLK = C / 16;
     const int tg = f4_token(c.lane >> 2);
+    // tiles up to the first of the rows' causal limits need no mask
     for (; tiles > 0; --tiles) {
         if (!mbar_wait(c.full0 + 8 * c.st, c.ph)) {
             set_status(status, CA_ERR_TIMEOUT);
@@ -182,7 +198,8 @@ __device__ __forceinline__ bool f4_tiles_own(F4Ctx& c, int tiles, const uint32_t
             float x[NB][4];
             uint32_t pb[NB][2];
             f4_scores<C, D, NB, ONE>(tile, blk, qb, x, c.lane);
-            f4_mask<NB>(x, blk * 16 + tg, ntok, causal ? c.tok0[c.st] : 0, causal, lim, scale_log2);
+            const int tok0 = causal ? c.tok0[c.st] : 0;
+            f4_mask<NB>(x, blk * 16 + tg, ntok, tok0, causal, lim, scale_log2);
             f4_softmax<D, NB, ONE>(x, a, pb);
             f4_pv<C, D, NB>(tile, blk, pb, a.o, c.lane);
         }
@@ -193,62 +210,288 @@ __device__ __forceinline__ bool f4_tiles_own(F4Ctx& c, int tiles, const uint32_t
     return true;
 }
 
-// Tokens [base, base + N) of a tile widened once for all warps, into the fp16 K
-// and V tiles that the 16-row blocks read (code * scale is exact in fp16).  A
-// thread takes 16 bytes (8 at D = 64) of a row's key codes: four dims of every
-// 16, and as many of a pair's value codes: two dims of every 16 of both tokens;
-// consecutive threads take rows whose swizzled 16-byte columns differ.
-template <int C, int D, int N>
-__device__ __forceinline__ void f4_tile_to_f16(const uint8_t* src, int base, uint8_t* kd, uint8_t* vd, int tid) {
+// Units of more than 8 rows (to 64).  A step takes 64 tokens: warp w the scores
+// of 16 of them for all rows, then, with the weights of all 64 in shared
+// memory, 16 D / 64 dims of all rows' outputs.  So every code is widened by one
+// warp only, straight into its operand (code * scale is exact in fp16), and a
+// row's output needs no meeting of warps at the end.  A row's softmax reference
+// is the same for all warps: a barrier that is also a vote tells whether any
+// score passes it by more than the slack.
+template <int C, int D, int NP>
+__device__ __forceinline__ void f4_wide_scores(const uint8_t* tile, int blk, uint32_t qa, float (&s)[2 * NP][4],
+                                               int lane) {
     using T = F4Tile<C, D>;
-    constexpr int NK = D / 16;
-    for (int i = tid; i < N * 4; i += kF4Warps * 32) {
-        const int t = i & 3, r = i >> 2;
-        // rows of 8 in the order 0 1 4 5 2 3 6 7: tokens 0 4 2 6, then 1 5 3 7
-        const int m = (r & ~7) | (r & 1) | ((r & 2) << 1) | ((r & 4) >> 1);
-        const int tok = f4_token(m);
-        uint32_t w[D / 32], sc[D / 64];
-        lds_words<D / 32>(src + (base + m) * (D / 2) + t * (D / 8), w);
-        lds_words<D / 64>(src + T::kKScales + (base + m) * (D / 16), sc);
+    const int g = lane >> 2, t = lane & 3, i = lane >> 3, j = lane & 7;
+    const uint8_t* kc = tile + (blk * 16 + g) * (D / 2) + t * (D / 8);
+    const uint8_t* ks = tile + T::kKScales + (blk * 16 + g) * (D / 16);
+    const uint32_t row = qa + ((i >> 1) * 8 + j) * (2 * D), at = (uint32_t)((i & 1) ^ j);
 #pragma unroll
-        for (int kp = 0; kp < NK / 2; ++kp) {             // two steps: one word of codes, two scales
-            uint32_t x[4], h[2];
-            f16x2_from_e2m1x8(w[kp], x);
-            f16x2_from_e4m3x4(sc[kp >> 1], h);
-            const uint32_t sa = __byte_perm(h[kp & 1], 0u, 0x1010), sb = __byte_perm(h[kp & 1], 0u, 0x3232);
-            *reinterpret_cast<uint2*>(kd + swz(tok, 4 * kp + (t >> 1), N) + 8 * (t & 1)) =
-                make_uint2(mul_f16x2(x[0], sa), mul_f16x2(x[1], sa));
-            *reinterpret_cast<uint2*>(kd + swz(tok, 4 * kp + 2 + (t >> 1), N) + 8 * (t & 1)) =
-                make_uint2(mul_f16x2(x[2], sb), mul_f16x2(x[3], sb));
-        }
-    }
-    for (int i = tid; i < N * 4; i += kF4Warps * 32) {
-        // four pairs of tokens a warp: (0, 4), (1, 5), ... of each 8; their rows
-        // two apart in turn
-        const int g = i & 7, q = i >> 3, pair = (q & ~3) | ((q & 1) << 1) | ((q >> 1) & 1);
-        const int tok = (pair >> 2) * 8 + (pair & 3);
-        uint32_t w[D / 32], sc[D / 32];
-        lds_words<D / 32>(src + T::kVCodes + (base / 2 + pair) * D + f4_v_unit<D>(pair, g) * (D / 8), w);
-        lds_words<D / 32>(src + T::kVScales + (base / 2 + pair) * (D / 8), sc);
+    for (int nb = 0; nb < 8; ++nb) s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.f;
 #pragma unroll
-        for (int i4 = 0; i4 < D / 64; ++i4) {
-            uint32_t x[4], y[4];
-            f16x2_from_e2m1x8(w[i4], x);
-            f16x2_from_e2m1x8(w[D / 64 + i4], y);
+    for (int sp = 0; sp < D / 64; ++sp) {                 // four steps of 16 dims
+        uint32_t w0[2], w1[2], c0[1], c1[1], h0[2], h1[2];
+        lds_words<2>(kc + sp * 8, w0);
+        lds_words<2>(kc + 8 * (D / 2) + sp * 8, w1);
+        lds_words<1>(ks + sp * 4, c0);
+        lds_words<1>(ks + 8 * (D / 16) + sp * 4, c1);
+        f16x2_from_e4m3x4(c0[0], h0);
+        f16x2_from_e4m3x4(c1[0], h1);
 #pragma unroll
-            for (int j2 = 0; j2 < 2; ++j2) {
-                uint32_t h[2];
-                f16x2_from_e4m3x4(sc[2 * i4 + j2], h);
+        for (int kp = 0; kp < 2; ++kp) {
+            uint32_t x0[4], x1[4];
+            f16x2_from_e2m1x8(w0[kp], x0);
+            f16x2_from_e2m1x8(w1[kp], x1);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int k = 2 * j2 + e, kc = 2 * (4 * i4 + k) + (g >> 2), off = 4 * (g & 3);
-                    const uint32_t a = mul_f16x2(x[k], h[e]), b = mul_f16x2(y[k], h[e]);   // (tok, tok + 4)
-                    *reinterpret_cast<uint32_t*>(vd + swz(tok, kc, N) + off) = __byte_perm(a, b, 0x5410);
-                    *reinterpret_cast<uint32_t*>(vd + swz(tok + 4, kc, N) + off) = __byte_perm(a, b, 0x7632);
+            for (int e = 0; e < 2; ++e) {
+                const int kk = 4 * sp + 2 * kp + e;
+                const uint32_t s0 = __byte_perm(h0[kp], 0u, e ? 0x3232 : 0x1010);
+                const uint32_t s1 = __byte_perm(h1[kp], 0u, e ? 0x3232 : 0x1010);
+                const uint32_t a[4] = {mul_f16x2(x0[2 * e], s0), mul_f16x2(x1[2 * e], s1),
+                                       mul_f16x2(x0[2 * e + 1], s0), mul_f16x2(x1[2 * e + 1], s1)};
+                const uint32_t col = row + ((at ^ (uint32_t)(2 * kk)) << 4);
+#pragma unroll
+                for (int n = 0; n < NP; ++n) {            // 16 rows at a time
+                    uint32_t b[4];
+                    ldsm_x4(col + n * 16 * 2 * D, b[0], b[1], b[2], b[3]);
+                    mma16816(s[2 * n], a, b[0], b[1]);
+                    mma16816(s[2 * n + 1], a, b[2], b[3]);
                 }
             }
         }
     }
+}
+
+// Address of 16 rows' weights for the 16 tokens of block b of the step, as
+// four 8 x 8 matrices (rows 0-7 and 8-15 of the first, then the next 8 tokens
+// of each: the order of two operands); lane l addresses row l % 8 of matrix l / 8.
+__device__ __forceinline__ uint32_t f4_p_addr(uint32_t pa, int n, int b, int lane) {
+    const int i = lane >> 3, j = lane & 7;
+    return pa + (uint32_t)((n * 16 + (i >> 1) * 8 + j) * (kWideTok * 2)) +
+           (uint32_t)(((2 * b + (i & 1)) ^ j) << 4);
+}
+__device__ __forceinline__ void stsm_x4_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+                 "r"(c), "r"(d)
+                 : "memory");
+}
+
+// O^T += V^T p for block b of the step (block `blk` of its tile): warp w's dims,
+// all rows.  o[nb][d] as f4_pv's, d-th of the warp's groups of 16 dims.
+template <int C, int D, int NP>
+__device__ __forceinline__ void f4_wide_pv(const uint8_t* tile, int blk, int b, uint32_t pa,
+                                           float (&o)[2 * NP][D / 64][4], int w, int lane) {
+    using T = F4Tile<C, D>;
+    constexpr int N = D / 64;
+    const int g = lane >> 2, t = lane & 3;
+    const uint8_t* vc = tile + T::kVCodes + (blk * 8 + t) * D + f4_v_unit<D>(t, g) * (D / 8) + N * w;
+    const uint8_t* vs = tile + T::kVScales + (blk * 8 + t) * (D / 8) + 2 * N * w;
+    uint32_t a[N][4];
+    if constexpr (N == 2) {
+        uint32_t v0[2], v1[2], v2[2], v3[2], x[2], y[2];
+        f16x2_from_e2m1x4(*reinterpret_cast<const uint16_t*>(vc), v0);
+        f16x2_from_e2m1x4(*reinterpret_cast<const uint16_t*>(vc + D / 16), v1);
+        f16x2_from_e2m1x4(*reinterpret_cast<const uint16_t*>(vc + 4 * D), v2);
+        f16x2_from_e2m1x4(*reinterpret_cast<const uint16_t*>(vc + 4 * D + D / 16), v3);
+        f16x2_from_e4m3x4(*reinterpret_cast<const uint32_t*>(vs), x);
+        f16x2_from_e4m3x4(*reinterpret_cast<const uint32_t*>(vs + 4 * (D / 8)), y);
+#pragma unroll
+        for (int d = 0; d < N; ++d) {
+            a[d][0] = mul_f16x2(v0[d], x[d]);
+            a[d][1] = mul_f16x2(v1[d], x[d]);
+            a[d][2] = mul_f16x2(v2[d], y[d]);
+            a[d][3] = mul_f16x2(v3[d], y[d]);
+        }
+    } else {
+        const uint32_t x = f16x2_from_e4m3x2(*reinterpret_cast<const uint16_t*>(vs));
+        const uint32_t y = f16x2_from_e4m3x2(*reinterpret_cast<const uint16_t*>(vs + 4 * (D / 8)));
+        a[0][0] = mul_f16x2(f16x2_from_e2m1x2(vc[0]), x);
+        a[0][1] = mul_f16x2(f16x2_from_e2m1x2(vc[D / 16]), x);
+        a[0][2] = mul_f16x2(f16x2_from_e2m1x2(vc[4 * D]), y);
+        a[0][3] = mul_f16x2(f16x2_from_e2m1x2(vc[4 * D + D / 16]), y);
+    }
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+        uint32_t pb[4];
+        ldsm_x4(f4_p_addr(pa, n, b, lane), pb[0], pb[1], pb[2], pb[3]);
+#pragma unroll
+        for (int d = 0; d < N; ++d) {
+            mma16816(o[2 * n][d], a[d], pb[0], pb[1]);
+            mma16816(o[2 * n + 1][d], a[d], pb[2], pb[3]);
+        }
+    }
+}
+
+// One head of such a unit: its `tiles` tiles over NP blocks of 16 rows (a loop
+// to a number known at run time would wait for every load of operands), whose
+// queries lie in qreg (word 2t of a row's 16 dims before word 2t + 1 of all t:
+// the operand order of the widened keys), to the partials of its rows.
+// scale_log2 > 0.  False on a timeout.
+template <int C, int D, int NP>
+__device__ __forceinline__ bool f4_wide_head(F4Ctx& c, const AttnParams& p, WideTables* tab, int tiles, int rows,
+                                             float scale_log2) {
+    constexpr int N = D / 64, NBLK = C / 16, TP = 4 / NBLK;     // tiles of a step
+    const int lane = c.lane, g = lane >> 2, t = lane & 3, w = c.w;
+    const uint32_t qa = smem_u32(c.qreg), pa = smem_u32(c.exch);
+    float o[2 * NP][N][4], sum[2][4];
+#pragma unroll
+    for (int nb = 0; nb < 2 * NP; ++nb)
+#pragma unroll
+        for (int d = 0; d < N; ++d) o[nb][d][0] = o[nb][d][1] = o[nb][d][2] = o[nb][d][3] = 0.f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) sum[k][0] = sum[k][1] = sum[k][2] = sum[k][3] = 0.f;
+    // (tiles up to the first of the rows' causal limits need no mask)
+    const int first_lim = p.causal ? __reduce_min_sync(kFull, min(tab->lim[lane], tab->lim[lane + 32])) : 0;
+    bool first = true;
+#pragma unroll 1
+    for (; tiles > 0; tiles -= TP, first = false) {
+        const int nt = min(tiles, TP);
+        auto slot_of = [&](int k) { return c.st + k < c.S ? c.st + k : c.st + k - c.S; };
+        for (int k = 0; k < nt; ++k) {
+            const int sl = slot_of(k);
+            if (!mbar_wait(c.full0 + 8 * sl, c.st + k < c.S ? c.ph : c.ph ^ 1u)) {
+                set_status(p.status, CA_ERR_TIMEOUT);
+                return false;
+            }
+        }
+        float s[2 * NP][4];
+        {
+            const int k = w / NBLK, blk = w % NBLK, sl = slot_of(k);
+            const int left = k < nt ? c.ntok[sl] - blk * 16 : 0;      // tokens of the warp's block
+            if (left > 0) {
+                f4_wide_scores<C, D, NP>(c.stages + (size_t)sl * F4Tile<C, D>::kBytes, blk, qa, s, lane);
+                const int tg = f4_token(g);
+                if (left < 16) {
+#pragma unroll
+                    for (int nb = 0; nb < 2 * NP; ++nb)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (tg + 8 * (e >> 1) >= left) s[nb][e] = -INFINITY;
+                }
+                if (p.causal && c.tok0[sl] + C - 1 > first_lim) {
+                    const int tok = c.tok0[sl] + blk * 16 + tg;
+#pragma unroll
+                    for (int nb = 0; nb < 2 * NP; ++nb) {
+                        const int2 lim = *reinterpret_cast<const int2*>(tab->lim + nb * 8 + 2 * t);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (tok + 8 * (e >> 1) > ((e & 1) ? lim.y : lim.x)) s[nb][e] = -INFINITY;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int nb = 0; nb < 2 * NP; ++nb) s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = -INFINITY;
+            }
+        }
+        bool grow = false;
+        if (!first) {
+#pragma unroll
+            for (int nb = 0; nb < 2 * NP; ++nb) {
+                const float2 thr = *reinterpret_cast<const float2*>(&tab->thr[nb * 8 + 2 * t]);
+                grow = grow | (fmaxf(s[nb][0], s[nb][2]) > thr.x) | (fmaxf(s[nb][1], s[nb][3]) > thr.y);
+            }
+        }
+        // (past the vote every warp has read the last step's weights, too)
+        if (first || f4_sync_any(grow)) {
+#pragma unroll
+            for (int nb = 0; nb < 2 * NP; ++nb) {
+                float2 mx = make_float2(fmaxf(s[nb][0], s[nb][2]), fmaxf(s[nb][1], s[nb][3]));
+#pragma unroll
+                for (int d = 4; d <= 16; d <<= 1) {
+                    mx.x = fmaxf(mx.x, __shfl_xor_sync(kFull, mx.x, d));
+                    mx.y = fmaxf(mx.y, __shfl_xor_sync(kFull, mx.y, d));
+                }
+                if (g == 0) *reinterpret_cast<float2*>(&tab->top[w][nb * 8 + 2 * t]) = mx;
+            }
+            f4_sync();
+            if (const int row = threadIdx.x; row < NP * 16) {
+                const float old = first ? -FLT_MAX : tab->ref[row];      // (any finite score raises it)
+                const float mx = fmaxf(fmaxf(tab->top[0][row], tab->top[1][row]),
+                                       fmaxf(tab->top[2][row], tab->top[3][row]));
+                const float ref = fmaxf(old, mx * scale_log2 - kLift);
+                tab->ref[row] = ref;
+                tab->thr[row] = (ref + (kLift + kSlack)) / scale_log2;
+                tab->fall[row] = ex2(old - ref);
+            }
+            f4_sync();
+            if (!first) {
+#pragma unroll
+                for (int nb = 0; nb < 2 * NP; ++nb) {
+                    const float2 f = *reinterpret_cast<const float2*>(&tab->fall[nb * 8 + 2 * t]);
+#pragma unroll
+                    for (int d = 0; d < N; ++d) {
+                        o[nb][d][0] *= f.x;
+                        o[nb][d][1] *= f.y;
+                        o[nb][d][2] *= f.x;
+                        o[nb][d][3] *= f.y;
+                    }
+                    if (nb >> 1 == w) {
+                        sum[nb & 1][0] *= f.x;
+                        sum[nb & 1][1] *= f.y;
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int nb = 2 * n + k;
+                const float2 ref = *reinterpret_cast<const float2*>(&tab->ref[nb * 8 + 2 * t]);
+                pk[2 * k] = pack_half2(ex2(fmaf(s[nb][0], scale_log2, -ref.x)),
+                                       ex2(fmaf(s[nb][1], scale_log2, -ref.y)));
+                pk[2 * k + 1] = pack_half2(ex2(fmaf(s[nb][2], scale_log2, -ref.x)),
+                                           ex2(fmaf(s[nb][3], scale_log2, -ref.y)));
+            }
+            stsm_x4_t(f4_p_addr(pa, n, w, lane), pk[0], pk[1], pk[2], pk[3]);
+        }
+        f4_sync();
+        // A tile is zero past its tokens, so one test for each is enough, and the
+        // loads of its four blocks need not wait for one another.
+#pragma unroll
+        for (int k = 0; k < TP; ++k) {
+            const int sl = slot_of(k);
+            if (k < nt && c.ntok[sl] > 0) {
+                const uint8_t* tile = c.stages + (size_t)sl * F4Tile<C, D>::kBytes;
+#pragma unroll
+                for (int blk = 0; blk < NBLK; ++blk)
+                    f4_wide_pv<C, D, NP>(tile, blk, k * NBLK + blk, pa, o, w, lane);
+                if (w < NP) {                              // the sums of 16 rows: a product with ones
+                    const uint32_t ones[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
+#pragma unroll
+                    for (int blk = 0; blk < NBLK; ++blk) {
+                        uint32_t pb[4];
+                        ldsm_x4(f4_p_addr(pa, w, k * NBLK + blk, lane), pb[0], pb[1], pb[2], pb[3]);
+                        mma16816(sum[0], ones, pb[0], pb[1]);
+                        mma16816(sum[1], ones, pb[2], pb[3]);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        for (int k = 0; k < nt; ++k) {
+            if (lane == 0) mbar_arrive(c.empty0 + 8 * c.st);
+            c.next();
+        }
+    }
+#pragma unroll
+    for (int nb = 0; nb < 2 * NP; ++nb)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int row = nb * 8 + 2 * t + r;
+            if (row < rows) {
+                const int id = tab->pid[row];
+#pragma unroll
+                for (int d = 0; d < N; ++d)
+                    *reinterpret_cast<float2*>(p.part_o + (size_t)id * D + 16 * (N * w + d) + 2 * g) =
+                        make_float2(o[nb][d][r], o[nb][d][r + 2]);
+                if (nb >> 1 == w && g == 0) {
+                    const float all = sum[nb & 1][r];      // 0: no token of the unit is the row's
+                    p.part_ms[id] = make_float2(all == 0.f ? -INFINITY : tab->ref[row], all);
+                }
+            }
+        }
+    return true;
 }
 
 // The end of a head of at most 8 rows: the warps' states meet in the exchange
@@ -324,7 +567,7 @@ fp4_attention_kernel(const __grid_constant__ CUtensorMap, const AttnParams p) {
     const int H = p.n_heads, HK = p.n_kv_heads, G = p.group, QL = p.q_len, RW = QL * G;
     // The merge kernel may be scheduled now; it waits for this grid itself.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (S < 1 || S > kF4Stages) {                          // uniform across the CTA
+    if (S < 64 / C || S > kF4Stages) {                     // uniform across the CTA
         if (threadIdx.x == 0) set_status(p.status, CA_ERR_INVALID);
         return;
     }
@@ -505,6 +748,18 @@ fp4_attention_kernel(const __grid_constant__ CUtensorMap, const AttnParams p) {
 
     const int n_static = u_end - u_begin;
     int32_t dn = (n_static > 0) ? load_desc(u_begin) : 0;
+    // What a unit of more rows asks of the plan: its rows' places in q, causal
+    // limits and partial ids.
+    WideTables* const tab = reinterpret_cast<WideTables*>(exch + SM::kP);
+    auto wide_rows = [&](int q_lo, int rows, int kvh, int upart) {
+        if (threadIdx.x >= kQRows) return;
+        const int r = threadIdx.x, e = row_tab[r], at = q_lo + tab_pos(e);
+        if (r < rows) {
+            tab->qrow[r] = (p.seq_perm[at] * QL + tab_tok(e)) * H + tab_head(e);
+            tab->pid[r] = p.pbase[((size_t)at * QL + tab_tok(e)) * H + kvh * G + tab_head(e)] + upart;
+        }
+        tab->lim[r] = p.causal && r < rows ? p.ctx_len[at] - QL + tab_tok(e) : INT_MAX;
+    };
     asm volatile("griddepcontrol.wait;" ::: "memory");     // q and the pool after this
     if (n_static > 0 && RW <= 8 && fld(dn, F_KIND) == UNIT_SF) prefetch(fld(dn, F_QROW), fld(dn, F_HEAD));
     for (int seq = 0;; ++seq) {
@@ -579,112 +834,49 @@ fp4_attention_kernel(const __grid_constant__ CUtensorMap, const AttnParams p) {
             qn_row = -1;                       // (its registers are wanted here)
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) qn[0][kk][0] = qn[0][kk][1] = 0u;
-            // More rows: the tile widened once for all warps, each taking a
-            // 16-row block and (fewer than 4 blocks) a share of the tokens.
-            const int rblocks = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-            constexpr int N = SM::kTok;
-            const int T = min(kF4Warps / rblocks, N / 16), rb = w / T, tp = w % T;
-            const bool act = rb < rblocks && rb * 16 < rows;
-            int lim[2] = {INT_MAX, INT_MAX};
-            if (p.causal) {
-                lim[0] = limit_of(rb * 16 + g);
-                lim[1] = limit_of(rb * 16 + g + 8);
-            }
-            const uint32_t kt = smem_u32(exch), vt = kt + SM::kImage, qblock = smem_u32(qreg) + rb * 16 * 128;
+            // The scale's sign goes to the queries, and a scale of zero makes
+            // them zero, so that larger products are larger scores below.
+            const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u, keep = p.scale_log2 == 0.f ? 0u : 0xffffffffu;
+            const float scale_log2 = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
+            const int np = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
             for (; L < L_end; ++kvh, upart = part_rest) {
                 const int seg_end = min(L_end, (kvh + 1) * n);
-                f4_sync();                     // the last head's exchange has been read
-                // Rows past `rows` are left as they are: every mma row is
-                // independent and such rows are never written out.
-                for (int i = threadIdx.x; i < rows * (D / 8); i += kF4Warps * 32) {
-                    const int r = i / (D / 8), k = i % (D / 8);
-                    cp_async16(smem_u32(qreg + swz(r, k, kQRows)), q_of(r) + (size_t)kvh * G * D + k * 8);
-                }
-                cp_async_wait_all();
-                float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, s[2] = {0.f, 0.f};
+                f4_sync();                     // the last head's queries and tables have been read
+                wide_rows(q_lo, rows, kvh, upart);
+                f4_sync();
+                constexpr int M = kQRows * (D / 16) / (kF4Warps * 32);   // 16 dims of a row at a time
+                uint4 a[M], b[M];
 #pragma unroll
-                for (int dt = 0; dt < D / 8; ++dt) o[dt][0] = o[dt][1] = o[dt][2] = o[dt][3] = 0.f;
-                for (; L < seg_end; ++L) {
-                    if (!mbar_wait(full0 + 8 * c.st, c.ph)) {
-                        set_status(p.status, CA_ERR_TIMEOUT);
-                        return;
-                    }
-                    const int ntok = c.ntok[c.st], ctx0 = c.tok0[c.st];
-                    const uint8_t* tile = stages + (size_t)c.st * SM::kStage;
-#pragma unroll 1
-                    for (int base = 0; base < C && (base == 0 || base < ntok); base += N) {
-                        f4_sync();             // the last tokens have been read (and the queries are there)
-                        f4_tile_to_f16<C, D, N>(tile, base, exch, exch + SM::kImage, threadIdx.x);
-                        f4_sync();
-                        if (lane == 0 && (base + N >= C || base + N >= ntok)) mbar_arrive(empty0 + 8 * c.st);
-                        if (!act) continue;
-                        if (T * 16 == N)
-                            cf_chunk<N, D, 16>(kt, vt, ntok - base, tp * 16, ctx0 + base, lim[0], lim[1], qblock,
-                                               p.scale_log2, m, s, o, lane);
-                        else
-                            cf_chunk<N, D, N>(kt, vt, ntok - base, 0, ctx0 + base, lim[0], lim[1], qblock,
-                                              p.scale_log2, m, s, o, lane);
-                    }
-                    c.next();
-                }
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    s[r] += __shfl_xor_sync(kFull, s[r], 1);
-                    s[r] += __shfl_xor_sync(kFull, s[r], 2);
-                }
-                // The T warps of a block meet two by two in the exchange area
-                // (the last tile's place): warps [half, 2 half) hand over.
-                float* xo = reinterpret_cast<float*>(exch);
-                for (int half = T / 2; half >= 1; half /= 2) {
-                    f4_sync();
-                    if (act && tp >= half && tp < 2 * half) {
-                        const int slot = rb * (T / 2) + tp - half;
-                        float* dst = xo + (size_t)slot * (16 * D);
-#pragma unroll
-                        for (int dt = 0; dt < D / 8; ++dt)
-                            reinterpret_cast<float4*>(dst)[dt * 32 + lane] =
-                                make_float4(o[dt][0], o[dt][1], o[dt][2], o[dt][3]);
-                        if (t == 0)
-                            reinterpret_cast<float4*>(ms)[slot * 8 + g] = make_float4(m[0], s[0], m[1], s[1]);
-                    }
-                    f4_sync();
-                    if (act && tp < half) {
-                        const int slot = rb * (T / 2) + tp;
-                        const float4* so = reinterpret_cast<const float4*>(xo + (size_t)slot * (16 * D));
-                        const float4 q = reinterpret_cast<const float4*>(ms)[slot * 8 + g];
-                        float a1[2], a2[2];
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const float m2 = r ? q.z : q.x, s2 = r ? q.w : q.y;
-                            const float M = fmaxf(m[r], m2), Mu = M == -INFINITY ? 0.f : M;
-                            a1[r] = ex2(m[r] - Mu);
-                            a2[r] = ex2(m2 - Mu);
-                            s[r] = s[r] * a1[r] + s2 * a2[r];
-                            m[r] = M;
-                        }
-#pragma unroll
-                        for (int dt = 0; dt < D / 8; ++dt) {
-                            const float4 v = so[dt * 32 + lane];
-                            o[dt][0] = o[dt][0] * a1[0] + v.x * a2[0];
-                            o[dt][1] = o[dt][1] * a1[0] + v.y * a2[0];
-                            o[dt][2] = o[dt][2] * a1[1] + v.z * a2[1];
-                            o[dt][3] = o[dt][3] * a1[1] + v.w * a2[1];
-                        }
+                for (int k = 0; k < M; ++k) {
+                    const int i = threadIdx.x + k * kF4Warps * 32, r = i / (D / 16), kk = i % (D / 16);
+                    a[k] = b[k] = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < rows) {
+                        const uint4* q =
+                            reinterpret_cast<const uint4*>(p.q + ((size_t)tab->qrow[r] + kvh * G) * D + kk * 16);
+                        a[k] = q[0];
+                        b[k] = q[1];
                     }
                 }
-                if (act && tp == 0) {
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const int row = rb * 16 + g + 8 * r;
-                        if (row >= rows) continue;
-                        const int id = pid_of(row, kvh) + upart;
-                        float* dst = p.part_o + (size_t)id * D;
-#pragma unroll
-                        for (int dt = 0; dt < D / 8; ++dt)
-                            *reinterpret_cast<float2*>(dst + dt * 8 + 2 * t) = make_float2(o[dt][2 * r], o[dt][2 * r + 1]);
-                        if (t == 0) p.part_ms[id] = make_float2(m[r], s[r]);
+                for (int k = 0; k < M; ++k) {
+                    const int i = threadIdx.x + k * kF4Warps * 32, r = i / (D / 16), kk = i % (D / 16);
+                    auto put = [&](int x, uint4 v) {
+                        *reinterpret_cast<uint4*>(qreg + r * (2 * D) + (((2 * kk + x) ^ (r & 7)) << 4)) =
+                            make_uint4((v.x ^ flip) & keep, (v.y ^ flip) & keep, (v.z ^ flip) & keep,
+                                       (v.w ^ flip) & keep);
+                    };
+                    if (r < np * 16) {
+                        put(0, make_uint4(a[k].x, a[k].z, b[k].x, b[k].z));
+                        put(1, make_uint4(a[k].y, a[k].w, b[k].y, b[k].w));
                     }
                 }
+                f4_sync();
+                const int tiles = seg_end - L;
+                if (!(np == 1   ? f4_wide_head<C, D, 1>(c, p, tab, tiles, rows, scale_log2)
+                      : np == 2 ? f4_wide_head<C, D, 2>(c, p, tab, tiles, rows, scale_log2)
+                                : f4_wide_head<C, D, 4>(c, p, tab, tiles, rows, scale_log2)))
+                    return;
+                L = seg_end;
             }
         }
     }

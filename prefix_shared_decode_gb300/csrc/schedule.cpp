@@ -206,12 +206,21 @@ constexpr double kCfComputePer16 = 0.2;
 // tile carries m query rows of work on half the bytes of an fp16 tile);
 // swept on GB300 (1.5 .. 2.8) for the fastest calls
 constexpr double kF8CfFactor = 2.0;
-// fp4 pools: a chunk-first tile is widened to fp16 in shared memory first, a
-// sequence-first one straight into fragments whatever its rows (up to 8).
-// Swept on GB300 at three CTAs per SM, single rows over prompts of 4096 tokens
-// (64 sequences) and 1024 (32): 64.1 / 62.0 / 61.0 and 31.9 / 30.7 / 27.3 us at
-// 2.5 / 3.5 / 4.5; four query tokens over 1024: 42.1 / 37.3 / 41.4 us at 3 / 4 / 5.
-constexpr double kF4CfFactor = 4.5, kF4CfRowsFactor = 4.0;
+// fp4 pools: what a chunk-first tile costs against a sequence-first one (whose
+// cost hardly depends on its rows, up to 8), for one row per position and for
+// several, and what a head of a chunk-first unit costs whatever its tiles (its
+// queries, first softmax reference and partials).  Swept on GB300 (2.5 .. 4,
+// 1.5 .. 3 and 1 .. 3.5): 64 sequences over 4096 shared tokens 58.4 / 55.7 /
+// 55.5 / 59.9 us at 2.5 / 3 / 3.5 / 4; grouped heads (4) over 1024 tokens 17.3 /
+// 15.6 / 15.6 us at 2 / 2.5 / 3, four query tokens 37.1 / 37.6 / 40.2; without a
+// unit's cost of its own the pieces of small calls came out too long (grouped
+// heads 17.2 us at 1).
+constexpr double kF4CfFactor = 3.5, kF4CfRowsFactor = 2.5, kF4CfUnit = 2.0;
+// Rows of such a unit where positions bring several: with 64 the registers of
+// its outputs spill and small calls have few units (grouped heads over 4096
+// tokens 30.3 us where 32 take 24.9, two query tokens 35.8 and 33.0; four level).
+// With one row per position 64 are better (64 sequences: 59 us, with 32 61).
+constexpr int32_t kF4GroupRows = 32;
 
 // Share of the sequence-first tiles left to the tail queue that CTAs drain
 // dynamically once their static lists are done (absorbs the run-to-run rate
@@ -274,6 +283,11 @@ void build_plan(const Pool& p, const Tables& t, int32_t grid, int32_t q_len, Pla
     // chunk-first work no longer finish long after the rest.
     const double sf_total = (double)(t.sf_chunks.size() / 2) * H;
     int32_t group_rows = max_query_rows(p.cfg);
+    double cf_unit = 0.0;                   // of a head of a unit, whatever its chunks
+    if (p.cfg.flags & CA_KV_FP4) {
+        if (RW > 1) group_rows = kF4GroupRows;
+        cf_unit = kF4CfUnit / sf_cost;
+    }
     auto cf_cost_total = [&] {
         double total = 0;
         for (int32_t u = 0; u < U; ++u) {
@@ -296,13 +310,14 @@ void build_plan(const Pool& p, const Tables& t, int32_t grid, int32_t q_len, Pla
     plan.grid = grid;
     const int64_t tail_tiles = (int64_t)(kTailShare * sf_total);
     const double sf_static = sf_total - (double)tail_tiles;
-    const double avg = (sf_static + cf_total) / grid;
+    double avg = (sf_static + cf_total) / grid;
 
     // Chunk-first units: pieces per run.
     std::vector<int32_t> pieces(U, 0);
     struct CfUnit { Unit u; double cost; };
     std::vector<CfUnit> cf;
     cf.reserve((size_t)U * 8);
+    int64_t cf_heads = 0;                   // heads of all units
     for (int32_t u = 0; u < U; ++u) {
         const int32_t row0 = t.cf_runs[4 * u], nrows = t.cf_runs[4 * u + 1];
         const int32_t lo = t.cf_runs[4 * u + 2], hi = t.cf_runs[4 * u + 3], m = hi - lo;
@@ -317,8 +332,8 @@ void build_plan(const Pool& p, const Tables& t, int32_t grid, int32_t q_len, Pla
         // longest unit bounds the kernel, while extra partials are spread
         // over every CTA and the merge.
         const int32_t rmin = std::max(1, (int32_t)((16.0 * mg * RW * (D + 2)) / ((double)c * D) + 0.999));
-        const int32_t rpar = std::max(1, (int32_t)(avg / row_cost));
-        const int32_t rcap = std::max(1, (int32_t)(1.25 * avg / row_cost));
+        const int32_t rpar = std::max(1, (int32_t)((avg - cf_unit) / row_cost));
+        const int32_t rcap = std::max(1, (int32_t)((1.25 * avg - cf_unit) / row_cost));
         const int32_t per = std::max(rpar, std::min(rmin, rcap));
         const int32_t np = std::max(1, (nrows + per - 1) / per);
         pieces[u] = np;
@@ -330,7 +345,7 @@ void build_plan(const Pool& p, const Tables& t, int32_t grid, int32_t q_len, Pla
                 const int32_t rb = row0 + (int32_t)((int64_t)nrows * (k + 1) / np);
                 // A unit covers a range of heads (the kernel reloads the query
                 // tile per head), as many as keep it within a CTA's share.
-                const double head_cost = (rb - ra) * rows_cost((qb - qa) * RW);
+                const double head_cost = (rb - ra) * rows_cost((qb - qa) * RW) + cf_unit;
                 const int32_t hp = std::max(1, std::min(H, (int32_t)(avg / head_cost)));
                 const int32_t nparts = (H + hp - 1) / hp;
                 for (int32_t hk = 0; hk < nparts; ++hk) {
@@ -338,10 +353,14 @@ void build_plan(const Pool& p, const Tables& t, int32_t grid, int32_t q_len, Pla
                     const int32_t h1 = (int32_t)((int64_t)H * (hk + 1) / nparts);
                     Unit x{UNIT_CF, h0, qa, qb, ra, rb, k, 0, h1 - h0, 0, 0, 0};
                     cf.push_back({x, (h1 - h0) * head_cost});
+                    cf_heads += h1 - h0;
                 }
             }
         }
     }
+    // The units' fixed costs are known now; shares of the sequence-first work
+    // are what is left of the whole.
+    avg += cf_unit * cf_heads / grid;
     // Partial index base of a run for its positions: the pieces of the runs
     // before it on the same path (its ancestors), which are exactly the runs
     // preceding it in any covered position's merge list.

@@ -9,6 +9,8 @@ step, 2^-11 of the value), the weights p held in fp16 (2^-11 of each, so
 products of magnitude below 2^6 leave below 2^-14 in the exponent; exp2 is
 good to 2^-22; weights below fp16's normal range are off by 2^-25 each, 2^-13
 over 4096 tokens)."""
+import sys
+
 import numpy as np
 import pytest
 
@@ -361,3 +363,29 @@ def test_appends_one_token_at_a_time(torch_cuda):
             if j % 7 == 0 or j > c - 4:
                 x.check_rows()
         x.check_rows()
+
+
+@pytest.mark.parametrize("scale", [128 ** -0.5, -0.05, 0.0, 0.1])
+@pytest.mark.parametrize("c,D,G,b", [(64, 128, 1, 70), (16, 64, 3, 21), (32, 128, 20, 3), (64, 64, 40, 2)])
+def test_scores_that_rise_along_the_context(torch_cuda, monkeypatch, c, D, G, b, scale):
+    """Keys twice as large chunk after chunk, so that a row's softmax reference
+    has to follow, in units of 9 to 64 rows; scales of either sign and zero.
+
+    (Scores to base 2: at most 8 steps of mma, each off by at most 16 * 2^-23 of
+    its largest term, 0.1 * 1.45 * 8 * 4 * 4 = 18.6 here: 2.9e-4, times ln 2 =
+    2.0e-4 of a weight, below the 2^-12 that the bound has for it.)"""
+    from prefix_shared_decode_gb300 import decode_attention
+    torch = torch_cuda
+
+    def rising(rng, L, n, H, D):
+        x = rng.standard_normal((L, n, H, D))
+        return (x * np.exp2(np.minimum(np.arange(n) // c, 3))[None, :, None, None]).astype(np.float16)
+
+    monkeypatch.setattr(sys.modules[__name__], "rows", rising)
+    seqs = [list(range(6 * c + 5)) + [10**6 + 1000 * i + j for j in range(3 + i % 2 * c)] for i in range(b)]
+    x = Cache(torch, 77 + b, c, D, G, seqs=seqs, L=1)
+    q = x.rng.standard_normal((b, 2 * G, D)).astype(np.float16)
+    sched = x.pool.schedule(list(range(b)))
+    got = decode_attention(x.pool, sched, torch.from_numpy(q).cuda(), scale=scale).cpu().numpy()
+    assert sched.device_status() == 0
+    x.check(got, list(range(b)), 0, q, scale)
