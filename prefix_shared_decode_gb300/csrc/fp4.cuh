@@ -139,9 +139,9 @@ __device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
 // E4M3 scale of a row differs from step to step, so each step's product is
 // taken from zero and added times the scale in fp32 (two FMAs per row and
 // column pair instead of scaling four operand registers, and no rounding).
-// ONE: every column carries the same query (only columns 0 of s are formed).
+// FEW: columns 2t and 2t + 1 are the same row (only the first of s is formed).
 // qb[nb][kk]: query dims 16 kk + 4t, + 1 and 16 kk + 4t + 2, + 3.
-template <int C, int D, int NB, bool ONE>
+template <int C, int D, int NB, bool FEW>
 __device__ __forceinline__ void f4_scores(const uint8_t* tile, int blk, const uint32_t (&qb)[NB][D / 16][2],
                                           float (&s)[NB][4], int lane) {
     using T = F4Tile<C, D>;
@@ -177,7 +177,7 @@ __device__ __forceinline__ void f4_scores(const uint8_t* tile, int blk, const ui
                     mma16816(acc, a, qb[nb][2 * kp + e][0], qb[nb][2 * kp + e][1]);
                     s[nb][0] = fmaf(acc[0], r0, s[nb][0]);
                     s[nb][2] = fmaf(acc[2], r1, s[nb][2]);
-                    if constexpr (!ONE) {
+                    if constexpr (!FEW) {
                         s[nb][1] = fmaf(acc[1], r0, s[nb][1]);
                         s[nb][3] = fmaf(acc[3], r1, s[nb][3]);
                     }

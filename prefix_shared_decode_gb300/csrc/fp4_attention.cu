@@ -9,7 +9,9 @@
 //    tile's bytes widen straight into operand registers (fp4.cuh).
 //  * Units of up to 8 query rows (every sequence-first unit of head groups up
 //    to 8, chunk-first ones of few sharers): each of the four warps takes its
-//    own 16 tokens of a tile and nothing is exchanged until the head ends.
+//    own 16 tokens of a tile and nothing is exchanged until the head ends.  Up
+//    to 4 rows lie twice in the 8 columns, which halves a lane's softmax (four
+//    query tokens over 2048 tokens of their own: 71.4 -> 66.7 us).
 //  * Units of more rows: 64 tokens at a time, the warps split the tokens for the
 //    scores and the dims for the outputs, so that each code is widened once;
 //    the weights pass through shared memory.
@@ -21,7 +23,7 @@
 // until the head ends, queries of the next head are fetched a head ahead, and
 // three CTAs per SM (128 registers a thread) cover the latencies.  65536 tiles
 // of single rows alone take 114 us, 80% of the copy rate; 64 sequences of 512
-// tokens of their own under 4096 shared ones, 32 heads of 128 dims, 55 us, of
+// tokens of their own under 4096 shared ones, 32 heads of 128 dims, 56 us, of
 // which the single rows' tiles are half; a step of a shared tile (64 rows) takes
 // some 2100 cycles of an SM, 1150 of them its tensor products.  (Widening shared
 // tiles into fp16 in shared memory first, 16 rows a warp: 61 us.)
@@ -113,19 +115,20 @@ struct F4State {
 };
 
 // Scaled and masked scores x of a 16-token block -> the operand p and the
-// state's sums (ONE: a single query in every column).
-template <int D, int NB, bool ONE>
+// state's sums.  FEW (up to 4 rows): row r is in columns 2r and 2r + 1, so that a
+// lane's two columns are one row and half the work is left.
+template <int D, int NB, bool FEW>
 __device__ __forceinline__ void f4_softmax(float (&x)[NB][4], F4State<D, NB>& a, uint32_t (&pb)[NB][2]) {
     bool grow = false;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int e = 0; e < 4; e += ONE ? 2 : 1) grow = grow || x[nb][e] > a.m[nb][e & 1] + (kLift + kSlack);
+        for (int e = 0; e < 4; e += FEW ? 2 : 1) grow = grow || x[nb][e] > a.m[nb][e & 1] + (kLift + kSlack);
     if (__any_sync(kFull, grow)) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int r = 0; r < (ONE ? 1 : 2); ++r) {
+            for (int r = 0; r < (FEW ? 1 : 2); ++r) {
                 float mx = fmaxf(x[nb][r], x[nb][r + 2]);
 #pragma unroll
                 for (int d = 4; d <= 16; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, d));
@@ -145,7 +148,7 @@ __device__ __forceinline__ void f4_softmax(float (&x)[NB][4], F4State<D, NB>& a,
         const float u0 = a.m[nb][0] == -INFINITY ? 0.f : a.m[nb][0];
         const float p0 = ex2(x[nb][0] - u0), p2 = ex2(x[nb][2] - u0);
         a.s[nb][0] += p0 + p2;                 // the lane's tokens; summed over the lanes at the end
-        if constexpr (ONE) {
+        if constexpr (FEW) {
             pb[nb][0] = movm_trans(pack_half2(p0, p0));
             pb[nb][1] = movm_trans(pack_half2(p2, p2));
         } else {
@@ -159,32 +162,32 @@ __device__ __forceinline__ void f4_softmax(float (&x)[NB][4], F4State<D, NB>& a,
 }
 
 // Scale, the chunk's token count and (lim: per row) the causal limit.
-template <int NB>
+template <int NB, bool FEW>
 __device__ __forceinline__ void f4_mask(float (&x)[NB][4], int tok, int ntok, int ctx0, bool causal,
                                         const int (&lim)[NB][2], float scale_log2) {
     const bool in0 = tok < ntok, in1 = tok + 8 < ntok;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[nb][e] = ((e >> 1) ? in1 : in0) ? x[nb][e] * scale_log2 : -INFINITY;
+        for (int e = 0; e < 4; e += FEW ? 2 : 1)
+            x[nb][e] = ((e >> 1) ? in1 : in0) ? x[nb][e] * scale_log2 : -INFINITY;
     if (causal) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < 4; e += FEW ? 2 : 1)
                 if (ctx0 + tok + 8 * (e >> 1) > lim[nb][e & 1]) x[nb][e] = -INFINITY;
     }
 }
 
 // One head's `tiles` tiles, each warp taking 16 tokens of its own; false on a
 // timeout.
-template <int C, int D, int NB, bool ONE>
+template <int C, int D, int NB, bool FEW>
 __device__ __forceinline__ bool f4_tiles_own(F4Ctx& c, int tiles, const uint32_t (&qb)[NB][D / 16][2],
-                                             const int (&lim)[NB][2], bool causal, float scale_log2, int32_t* status,
+                                             const int (&lim)[NB][2], int first_lim, float scale_log2, int32_t* status,
                                              F4State<D, NB>& a) {
     constexpr int NBLK = C / 16;
     const int tg = f4_token(c.lane >> 2);
-    // tiles up to the first of the rows' causal limits need no mask
     for (; tiles > 0; --tiles) {
         if (!mbar_wait(c.full0 + 8 * c.st, c.ph)) {
             set_status(status, CA_ERR_TIMEOUT);
@@ -197,10 +200,10 @@ __device__ __forceinline__ bool f4_tiles_own(F4Ctx& c, int tiles, const uint32_t
             const uint8_t* tile = c.stages + (size_t)c.st * F4Tile<C, D>::kBytes;
             float x[NB][4];
             uint32_t pb[NB][2];
-            f4_scores<C, D, NB, ONE>(tile, blk, qb, x, c.lane);
-            const int tok0 = causal ? c.tok0[c.st] : 0;
-            f4_mask<NB>(x, blk * 16 + tg, ntok, tok0, causal, lim, scale_log2);
-            f4_softmax<D, NB, ONE>(x, a, pb);
+            f4_scores<C, D, NB, FEW>(tile, blk, qb, x, c.lane);
+            const int tok0 = c.tok0[c.st];
+            f4_mask<NB, FEW>(x, blk * 16 + tg, ntok, tok0, tok0 + (C - 1) > first_lim, lim, scale_log2);
+            f4_softmax<D, NB, FEW>(x, a, pb);
             f4_pv<C, D, NB>(tile, blk, pb, a.o, c.lane);
         }
         __syncwarp();
@@ -499,7 +502,7 @@ __device__ __forceinline__ bool f4_wide_head(F4Ctx& c, const AttnParams& p, Wide
 // loads) and warp w writes the partials of rows w and w + 4.  Lane j holds the
 // first partial id of row w + 4 j's pieces, this one is `part` further: added
 // here, so that the id's load, begun with the head, is first waited for here.
-template <int C, int D, bool ONE>
+template <int C, int D, bool FEW>
 __device__ __forceinline__ void f4_finish(F4Ctx& c, const AttnParams& p, F4State<D, 1>& a, int rows, int pid, int part) {
     const int g = c.lane >> 2, t = c.lane & 3;
     float* ob = reinterpret_cast<float*>((c.flush & 1) ? c.qreg : c.exch);
@@ -508,12 +511,12 @@ __device__ __forceinline__ void f4_finish(F4Ctx& c, const AttnParams& p, F4State
     float* ms = c.ms + (c.flush & 1) * kF4Warps * 8 * 2;
     ++c.flush;
 #pragma unroll
-    for (int r = 0; r < (ONE ? 1 : 2); ++r) {
+    for (int r = 0; r < (FEW ? 1 : 2); ++r) {
         float s = a.s[0][r];
 #pragma unroll
         for (int d = 4; d <= 16; d <<= 1) s += __shfl_xor_sync(kFull, s, d);
-        const int row = ONE ? 0 : 2 * t + r;
-        if (!ONE || t == 0) {
+        const int row = FEW ? t : 2 * t + r;
+        if (!FEW || t < rows) {
             if (g == 0) *reinterpret_cast<float2*>(ms + (c.w * 8 + row) * 2) = make_float2(a.m[0][r], s);
 #pragma unroll
             for (int db = 0; db < D / 16; ++db)
@@ -718,7 +721,9 @@ fp4_attention_kernel(const __grid_constant__ CUtensorMap, const AttnParams p) {
     auto tab_pos = [](int32_t e) { return e >> 16; };
     auto tab_tok = [](int32_t e) { return e >> 8 & 0xff; };
     auto tab_head = [](int32_t e) { return e & 0xff; };
-    const int gt = tab_tok(row_tab[g]), gh = tab_head(row_tab[g]);   // of row g of one position
+    const bool few = RW <= 4;                  // rows of a position twice over, see f4_softmax
+    const int gr = few ? g >> 1 : g;           // the row in column g of a position's rows
+    const int gt = tab_tok(row_tab[gr]), gh = tab_head(row_tab[gr]);
 
     // Query rows in operand order.  One position's rows g < RW (its row of q
     // known from the unit), and any unit's rows.
@@ -732,11 +737,9 @@ fp4_attention_kernel(const __grid_constant__ CUtensorMap, const AttnParams p) {
             dst[kk][1] = x.y;
         }
     };
-    const bool one = RW == 1;                  // a single row: in every column
     auto load_own = [&](Q1& dst, int qrow, int kvh) {
-        const bool there = one || g < RW;
-        const int tk = one ? 0 : gt, hh = one ? 0 : gh;
-        put_row(dst[0], p.q + (((size_t)qrow * QL + tk) * H + kvh * G + hh) * D, there);
+        const bool there = gr < RW;
+        put_row(dst[0], p.q + (((size_t)qrow * QL + (there ? gt : 0)) * H + kvh * G + (there ? gh : 0)) * D, there);
     };
     Q1 qn;                                     // the next head's queries ...
     int qn_row = -1, qn_head = -1;             // ... and which they are
@@ -800,7 +803,10 @@ fp4_attention_kernel(const __grid_constant__ CUtensorMap, const AttnParams p) {
         };
         int kvh = L / n;
         if (rows <= 8) {
-            int lim[1][2] = {{limit_of(one ? 0 : 2 * t), limit_of(one ? 0 : 2 * t + 1)}};
+            const bool half = rows <= 4;
+            int lim[1][2] = {{limit_of(half ? t : 2 * t), limit_of(half ? t : 2 * t + 1)}};
+            // (tiles up to the first of the rows' causal limits need no mask)
+            const int first_lim = p.causal ? __reduce_min_sync(kFull, min(lim[0][0], lim[0][1])) : INT_MAX;
             for (; L < L_end; ++kvh, upart = part_rest) {
                 const int seg_end = min(L_end, (kvh + 1) * n);
                 Q1 qb;
@@ -814,17 +820,18 @@ fp4_attention_kernel(const __grid_constant__ CUtensorMap, const AttnParams p) {
                     if (seg_end < L_end) prefetch(qrow, kvh + 1);
                     else if (next_own) prefetch(fld(dn, F_QROW), fld(dn, F_HEAD));
                 } else {
-                    const bool there = g < rows;
-                    put_row(qb[0], q_of(there ? g : 0) + (size_t)kvh * G * D, there);
+                    const int r = half ? g >> 1 : g;
+                    put_row(qb[0], q_of(r < rows ? r : 0) + (size_t)kvh * G * D, r < rows);
                 }
                 const int pid = (lane < 2 && w + 4 * lane < rows) ? pid_of(w + 4 * lane, kvh) : 0;
                 F4State<D, 1> a;
                 a.clear();
-                if (one && is_sf) {
-                    if (!f4_tiles_own<C, D, 1, true>(c, seg_end - L, qb, lim, false, p.scale_log2, p.status, a)) return;
+                if (half) {
+                    if (!f4_tiles_own<C, D, 1, true>(c, seg_end - L, qb, lim, first_lim, p.scale_log2, p.status, a))
+                        return;
                     f4_finish<C, D, true>(c, p, a, rows, pid, upart);
                 } else {
-                    if (!f4_tiles_own<C, D, 1, false>(c, seg_end - L, qb, lim, p.causal, p.scale_log2, p.status, a))
+                    if (!f4_tiles_own<C, D, 1, false>(c, seg_end - L, qb, lim, first_lim, p.scale_log2, p.status, a))
                         return;
                     f4_finish<C, D, false>(c, p, a, rows, pid, upart);
                 }

@@ -210,9 +210,9 @@ constexpr double kF8CfFactor = 2.0;
 // cost hardly depends on its rows, up to 8), for one row per position and for
 // several, and what a head of a chunk-first unit costs whatever its tiles (its
 // queries, first softmax reference and partials).  Swept on GB300 (2.5 .. 4,
-// 1.5 .. 3 and 1 .. 3.5): 64 sequences over 4096 shared tokens 58.4 / 55.7 /
-// 55.5 / 59.9 us at 2.5 / 3 / 3.5 / 4; grouped heads (4) over 1024 tokens 17.3 /
-// 15.6 / 15.6 us at 2 / 2.5 / 3, four query tokens 37.1 / 37.6 / 40.2; without a
+// 1.5 .. 3 and 1 .. 3.5): 64 sequences over 4096 shared tokens 58.4 / 57.3 /
+// 56.5 / 59.9 us at 2.5 / 3 / 3.5 / 4; grouped heads (4) over 1024 tokens 17.1 /
+// 15.4 / 15.4 us at 2 / 2.5 / 3, four query tokens 35.2 / 35.5 / 37.9; without a
 // unit's cost of its own the pieces of small calls came out too long (grouped
 // heads 17.2 us at 1).
 constexpr double kF4CfFactor = 3.5, kF4CfRowsFactor = 2.5, kF4CfUnit = 2.0;

@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const ListPa
 // `qdim(kk, t)`: first of a lane's dims of step kk, held in two registers
 // (kPair: four consecutive dims, else two and the two 8 further).
 // ---------------------------------------------------------------------------
-template <int EB, int C, int D, int NB, bool ONE>
+template <int EB, int C, int D, int NB, bool FEW>
 struct Frag;
 
 template <int C, int D, int NB>
@@ -620,15 +620,15 @@ struct Frag<1, C, D, NB, false> {                       // fp8: bytes widened in
     }
 };
 
-template <int C, int D, int NB, bool ONE>
-struct Frag<0, C, D, NB, ONE> {                  // fp4; ONE: a single query row, in every column
+template <int C, int D, int NB, bool FEW>
+struct Frag<0, C, D, NB, FEW> {                  // fp4
     static constexpr int kStage = F4Tile<C, D>::kBytes;
     static constexpr bool kPair = true;
     __device__ static int tok(int g) { return f4_token(g); }
     __device__ static int dim(int db, int half, int g) { return 16 * db + 2 * g + half; }
     __device__ static void scores(const uint8_t* st, int blk, const uint32_t (&qb)[NB][D / 16][2], float (&s)[NB][4],
                                   int lane) {
-        f4_scores<C, D, NB, ONE>(st, blk, qb, s, lane);
+        f4_scores<C, D, NB, FEW>(st, blk, qb, s, lane);
     }
     __device__ static void pv(const uint8_t* st, int blk, const uint32_t (&pb)[NB][2], float (&o)[NB][D / 16][4],
                               int lane) {
@@ -664,9 +664,9 @@ constexpr int kSpWarps = 4, kSpThreads = 32 * (kSpWarps + 1), kSpStages = 12;
 // and normal numbers down to 2^-19 (or less) of the largest.
 constexpr float kSpLift = 5.f, kSpSlack = 8.f;
 
-template <int EB, int C, int D, int NB, bool ONE>
+template <int EB, int C, int D, int NB, bool FEW>
 struct SpShared {
-    using F = Frag<EB, C, D, NB, ONE>;
+    using F = Frag<EB, C, D, NB, FEW>;
     static constexpr int kGroups = kSpWarps / (C / 16);           // of warps; the ring is a multiple of them
     static constexpr int kPerSm = EB == 0 && NB == 1 ? 3 : 2;     // resident CTAs
     static constexpr int kRows = 8 * NB;
@@ -682,12 +682,13 @@ __device__ __forceinline__ void sp_consumers() { asm volatile("bar.sync 1, %0;" 
 // Entries [first, last) of CTA c when `total` are cut into `grid` stretches.
 __device__ __forceinline__ long long cut_at(long long total, int grid, int c) { return total * c / grid; }
 
-template <int EB, int C, int D, int NB, bool ONE>
-__global__ void __launch_bounds__(kSpThreads, SpShared<EB, C, D, NB, ONE>::kPerSm)
+template <int EB, int C, int D, int NB, bool FEW>
+__global__ void __launch_bounds__(kSpThreads, SpShared<EB, C, D, NB, FEW>::kPerSm)
 sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListParams p) {
-    using F = Frag<EB, C, D, NB, ONE>;
-    using SM = SpShared<EB, C, D, NB, ONE>;
-    constexpr int NR = ONE ? 1 : 2;                        // query rows among a lane's two columns
+    using F = Frag<EB, C, D, NB, FEW>;
+    using SM = SpShared<EB, C, D, NB, FEW>;
+    // FEW (up to 4 rows): row r is in columns 2r and 2r + 1, one row for a lane
+    constexpr int NR = FEW ? 1 : 2;                        // query rows among a lane's two columns
     constexpr int R = SM::kRows, NBLK = C / 16, RS = SM::kRow, W = kSpWarps, NG = SM::kGroups;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int S = p.n_stages;
@@ -830,8 +831,9 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
         uint32_t qb[NB][D / 16][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-            const bool there = ONE || nb * 8 + g < rows;
-            const uint16_t* q = p.q + (row0 + (!ONE && there ? nb * 8 + g : 0)) * D;
+            const int r = FEW ? g >> 1 : nb * 8 + g;
+            const bool there = r < rows;
+            const uint16_t* q = p.q + (row0 + (there ? r : 0)) * D;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 uint2 x = make_uint2(0u, 0u);
@@ -904,7 +906,7 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
                     const float p0 = ex2(x[nb][0] - u0_), p2 = ex2(x[nb][2] - u0_);
                     float p1 = p0, p3 = p2;
                     s[nb][0] += p0 + p2;
-                    if constexpr (!ONE) {
+                    if constexpr (!FEW) {
                         const float u1_ = m[nb][1] == -INFINITY ? 0.f : m[nb][1];
                         p1 = ex2(x[nb][1] - u1_);
                         p3 = ex2(x[nb][3] - u1_);
@@ -925,15 +927,15 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
         // The warps' states meet: warps 1 to 3 hand theirs to warp 0, which
         // leaves the sum in the exchange area for all of them to write out
         // (three copies there leave room for a third tile of 32 KB).
+        auto row_of = [&](int nb, int r) { return FEW ? t : nb * 8 + 2 * t + r; };
         auto put = [&](float* dst) {                       // [row][D] with the rows' stride
-            if (ONE && t != 0) return;
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int db = 0; db < D / 16; ++db)
 #pragma unroll
                     for (int k = 0; k < 4; k += 3 - NR)
-                        dst[(nb * 8 + 2 * t + (k & 1)) * RS + F::dim(db, k >> 1, g)] = o[nb][db][k];
+                        dst[row_of(nb, k & 1) * RS + F::dim(db, k >> 1, g)] = o[nb][db][k];
         };
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
@@ -944,12 +946,12 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
         sp_consumers();                                 // the last piece has been written out
         if (warp > 0) {
             put(exch + (size_t)(warp - 1) * R * RS);
-            if (g == 0 && (!ONE || t == 0))
+            if (g == 0)
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                     for (int r = 0; r < NR; ++r)
-                        *reinterpret_cast<float2*>(wms + (warp * R + nb * 8 + 2 * t + r) * 2) =
+                        *reinterpret_cast<float2*>(wms + (warp * R + row_of(nb, r)) * 2) =
                             make_float2(m[nb][r], s[nb][r]);
         }
         sp_consumers();
@@ -958,7 +960,7 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int r = 0; r < NR; ++r) {
-                    const int row = nb * 8 + (ONE ? 0 : 2 * t + r);
+                    const int row = row_of(nb, r);
                     float2 q[W - 1];
                     float M = m[nb][r];
 #pragma unroll
@@ -984,7 +986,7 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
                             o[nb][db][r + 2] += ak * src[F::dim(db, 1, g)];
                         }
                     }
-                    if (g == 0 && (!ONE || t == 0)) *reinterpret_cast<float2*>(wms + row * 2) = make_float2(M, sum);
+                    if (g == 0) *reinterpret_cast<float2*>(wms + row * 2) = make_float2(M, sum);
                 }
             __syncwarp();
             put(exch);
@@ -1133,22 +1135,24 @@ struct SparseKernel {
     int rows = 0, stage = 0, fixed = 0;      // rows of a unit; bytes of a stage, of the rest
     int groups = 0, per_sm = 0;              // the ring's slots come in multiples of `groups`; CTAs per SM
 };
-template <int EB, int C, int D, int NB, bool ONE = false>
+template <int EB, int C, int D, int NB, bool FEW = false>
 SparseKernel sparse_of() {
-    using SM = dev::SpShared<EB, C, D, NB, ONE>;
-    return {reinterpret_cast<const void*>(&dev::sparse_attention_kernel<EB, C, D, NB, ONE>), SM::kRows, SM::F::kStage,
+    using SM = dev::SpShared<EB, C, D, NB, FEW>;
+    return {reinterpret_cast<const void*>(&dev::sparse_attention_kernel<EB, C, D, NB, FEW>), SM::kRows, SM::F::kStage,
             (int)SM::bytes(0), SM::kGroups, SM::kPerSm};
 }
 // Rows of a group per CTA: 8, or 16 for groups of more (at head_dim 256 the
-// accumulators of 16 rows do not fit the registers); a single one by itself in
-// an fp4 pool, which is bound by instructions.
+// accumulators of 16 rows do not fit the registers).  In an fp4 pool, which is
+// bound by instructions, up to 4 rows lie twice in the 8 columns and a lane's
+// softmax is of one row, not two: 512 units of 64 tiles 58.8 us for 62.3 with
+// one row, 57.8 for 62.3 with four (an fp8 pool gains 1%, and has no such form).
 template <int EB, int C, int D>
 SparseKernel pick_rows(int group) {
     if constexpr (D <= 128) {
         if (group > 8) return sparse_of<EB, C, D, 2>();
     }
-    if constexpr (EB == 0) {                   // 512 units of one row: 58.8 us, with eight columns 62.3
-        if (group == 1) return sparse_of<EB, C, D, 1, true>();
+    if constexpr (EB == 0) {
+        if (group <= 4) return sparse_of<EB, C, D, 1, true>();
     }
     return sparse_of<EB, C, D, 1>();
 }

@@ -131,7 +131,8 @@ def test_rows_and_every_output(torch_cuda, c, D, G):
 
 
 @pytest.mark.parametrize("q_len,causal,G,c,D", [(2, False, 1, 16, 64), (4, True, 1, 64, 128), (3, True, 2, 32, 128),
-                                               (8, True, 1, 32, 64), (5, True, 4, 64, 128), (16, True, 4, 16, 128)])
+                                               (8, True, 1, 32, 64), (5, True, 4, 64, 128), (16, True, 4, 16, 128),
+                                               (3, True, 1, 16, 128), (2, True, 2, 64, 64)])
 def test_several_query_tokens(torch_cuda, q_len, causal, G, c, D):
     from prefix_shared_decode_gb300 import decode_attention
     torch = torch_cuda
