@@ -114,34 +114,57 @@ __device__ __forceinline__ void add_pair(float& s, float& e, float x, float y) {
     s = t;
     e = __fadd_rn(__fadd_rn(e, y), lost);
 }
-// One row's product with a chunk's bounds to 48 bits (a warp; every lane gets
-// it), as an ordered key.  Products of fp16 are exact in fp32 and their sums
-// are held as pairs of fp32: the card's fp64 pipe (2 FMAs a clock and SM) took
-// 8 us for five chunks of four rows where this takes 1.  The order of the sum
-// is fixed: equal bounds tie.
-template <int D>
-__device__ __forceinline__ unsigned long long exact_row(const uint16_t* q, const uint16_t* bounds, int lane) {
-    float s = 0.f, e = 0.f;
+// The largest of N rows' products with a chunk's bounds, each to 48 bits
+// (a warp; every lane gets it), as an ordered key.  Products of fp16 are exact
+// in fp32 and their sums are held as pairs of fp32: on the card's fp64 pipe (2
+// FMAs a clock and SM) five chunks of four rows took 8 us; 8 sequences of 2048
+// chunks lose some 3.5 us to all of the exact ranking now.  The order of a sum is
+// fixed: equal bounds tie.  (Four rows share the chunk's loads and overlap their
+// sums: 0.5 us less there than row by row.)
+constexpr int kExactRows = 4;
+template <int D, int N>
+__device__ __forceinline__ unsigned long long exact_rows(const uint16_t* q, const uint16_t* bounds, int lane) {
+    float s[N], e[N];
+#pragma unroll
+    for (int r = 0; r < N; ++r) s[r] = e[r] = 0.f;
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) {
         const int d = 64 * j + 2 * lane;
-        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(q + d));
         const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(bounds + d));
         const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(bounds + D + d));
-        add_pair(s, e, __fmul_rn(x.x, x.x > 0.f ? hi.x : lo.x), 0.f);
-        add_pair(s, e, __fmul_rn(x.y, x.y > 0.f ? hi.y : lo.y), 0.f);
-    }
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) {
-        const float s2 = __shfl_xor_sync(kFull, s, off), e2 = __shfl_xor_sync(kFull, e, off);
-        // the same pair order in both lanes, so that every lane ends with the same sum
-        const bool up = (threadIdx.x & off) != 0;
-        float a = up ? s2 : s, ae = up ? e2 : e;
-        add_pair(a, ae, up ? s : s2, up ? e : e2);
-        s = a;
-        e = ae;
+        for (int r = 0; r < N; ++r) {
+            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(q + r * D + d));
+            add_pair(s[r], e[r], __fmul_rn(x.x, x.x > 0.f ? hi.x : lo.x), 0.f);
+            add_pair(s[r], e[r], __fmul_rn(x.y, x.y > 0.f ? hi.y : lo.y), 0.f);
+        }
     }
-    return order_key((double)s + (double)e);
+    unsigned long long k = 0ull;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1)
+#pragma unroll
+        for (int r = 0; r < N; ++r) {
+            const float s2 = __shfl_xor_sync(kFull, s[r], off), e2 = __shfl_xor_sync(kFull, e[r], off);
+            // the same pair order in both lanes, so that every lane ends with the same sum
+            const bool up = (threadIdx.x & off) != 0;
+            float a = up ? s2 : s[r], ae = up ? e2 : e[r];
+            add_pair(a, ae, up ? s[r] : s2, up ? e[r] : e2);
+            s[r] = a;
+            e[r] = ae;
+        }
+#pragma unroll
+    for (int r = 0; r < N; ++r) k = max(k, order_key((double)s[r] + (double)e[r]));
+    return k;
+}
+
+// The same over rows [0, n) of q.
+template <int D>
+__device__ __forceinline__ unsigned long long exact_key(const uint16_t* q, int n, const uint16_t* bounds, int lane) {
+    unsigned long long k = 0ull;
+    int r = 0;
+    for (; r + kExactRows <= n; r += kExactRows) k = max(k, exact_rows<D, kExactRows>(q + r * D, bounds, lane));
+    for (; r < n; ++r) k = max(k, exact_rows<D, 1>(q + r * D, bounds, lane));
+    return k;
 }
 
 // Block-wide sums of two counts (every thread gets them).
@@ -369,6 +392,10 @@ __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const ListPa
         if (cs > 1) st_peer(abs0 + 4u * (uint32_t)(rank * 128 + d), bits);
         else sh.top_abs[0][d] = bits;
     }
+    uint32_t q0[D / 64];                                  // the bound's first row (below), on its way meanwhile
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j)
+        q0[j] = *reinterpret_cast<const uint32_t*>(q + (size_t)min(warp, G - 1) * D + 64 * j + 2 * lane);
     if (cs > 1) {
         cluster_sync_all();
         if (rank != 0) return;
@@ -396,8 +423,9 @@ __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const ListPa
                 float s = 0.f;
 #pragma unroll
                 for (int j = 0; j < D / 64; ++j) {
-                    const float2 x =
-                        __half22float2(*reinterpret_cast<const __half2*>(q + (size_t)r * D + 64 * j + 2 * lane));
+                    if (r != warp)
+                        q0[j] = *reinterpret_cast<const uint32_t*>(q + (size_t)r * D + 64 * j + 2 * lane);
+                    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&q0[j]));
                     const float2 b = __half22float2(m[j]);
                     s += fabsf(x.x) * b.x + fabsf(x.y) * b.y;
                 }
@@ -446,11 +474,12 @@ __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const ListPa
             for (int j = threadIdx.x; j < n; j += kSelThreads)
                 if (keys[j] >= low && keys[j] <= high) sh.list[atomicAdd(&sh.n_list, 1u)] = (uint32_t)j;
             __syncthreads();
-            for (uint32_t x = warp; x < c.y * (uint32_t)G; x += kSelWarps) {   // (row, chunk) by (row, chunk)
-                const uint32_t e = x / (uint32_t)G, r = x % (uint32_t)G;
+            const uint32_t RB = (uint32_t)(G + kExactRows - 1) / kExactRows;
+            for (uint32_t x = warp; x < c.y * RB; x += kSelWarps) {            // (rows, chunk) by (rows, chunk)
+                const uint32_t e = x / RB, r = x % RB * kExactRows;
                 const int s = slots[sh.list[e]];
-                const unsigned long long k =
-                    exact_row<D>(q + (size_t)r * D, bounds_of(s >= 0 && s < p.capacity ? s : 0), lane);
+                const unsigned long long k = exact_key<D>(q + (size_t)r * D, min(kExactRows, G - (int)r),
+                                                          bounds_of(s >= 0 && s < p.capacity ? s : 0), lane);
                 if (lane == 0) atomicMax(&sh.key64[e], k);
             }
             __syncthreads();
@@ -465,12 +494,9 @@ __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const ListPa
             // selection over the 64-bit keys, computed anew for each digit.
             unsigned long long pre = 0;
             uint32_t rest = open;
-            auto exact_key = [&](int j) {
+            auto key_of = [&](int j) {
                 const int s = slots[j];
-                const uint16_t* b = bounds_of(s >= 0 && s < p.capacity ? s : 0);
-                unsigned long long k = 0ull;
-                for (int r = 0; r < G; ++r) k = max(k, exact_row<D>(q + (size_t)r * D, b, lane));
-                return k;
+                return exact_key<D>(q, G, bounds_of(s >= 0 && s < p.capacity ? s : 0), lane);
             };
             for (int shift = 56; shift >= 0; shift -= 8) {
                 __syncthreads();
@@ -478,7 +504,7 @@ __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const ListPa
                 __syncthreads();
                 for (int j = warp; j < n; j += kSelWarps) {
                     if (keys[j] < low || keys[j] > high) continue;
-                    const unsigned long long k = exact_key(j);
+                    const unsigned long long k = key_of(j);
                     if (lane == 0 && (shift == 56 || (k >> (shift + 8)) == pre))
                         atomicAdd(&sh.hist[(k >> shift) & 255u], 1u);
                 }
@@ -490,7 +516,7 @@ __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const ListPa
                 const uint32_t k32 = keys[j];
                 __syncwarp();
                 if (k32 < low || k32 > high) continue;
-                const unsigned long long k = exact_key(j);
+                const unsigned long long k = key_of(j);
                 if (lane == 0) keys[j] = k > pre ? kSure : k == pre ? kTie : 0u;
             }
             ties = rest;
