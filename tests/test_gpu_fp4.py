@@ -390,3 +390,24 @@ def test_scores_that_rise_along_the_context(torch_cuda, monkeypatch, c, D, G, b,
     got = decode_attention(x.pool, sched, torch.from_numpy(q).cuda(), scale=scale).cpu().numpy()
     assert sched.device_status() == 0
     x.check(got, list(range(b)), 0, q, scale)
+
+
+@pytest.mark.parametrize("G", [1, 4, 24])
+def test_flat_pools_and_a_sequence_twice_in_a_batch(torch_cuda, G):
+    """A pool without sharing; a batch that holds one sequence in several rows."""
+    from prefix_shared_decode_gb300 import CAError, decode_attention
+    torch = torch_cuda
+    seqs = [[1000 * i + j for j in range(n)] for i, n in enumerate((1, 200, 64, 33, 513))]
+    for kw in (dict(no_sharing=True), {}):
+        x = Cache(torch, 91 + G, 32, 128, G, seqs=seqs, **kw)
+        x.check_rows()
+        for batch in ([4, 1, 0, 3, 2], [1, 4, 1]):
+            try:
+                sched = x.pool.schedule(batch)
+            except CAError as e:
+                assert len(set(batch)) < len(batch) and e.name == "CA_ERR_INVALID"
+                continue
+            q = x.rng.standard_normal((len(batch), 2 * G, 128)).astype(np.float16)
+            got = decode_attention(x.pool, sched, torch.from_numpy(q).cuda(), layer=1).cpu().numpy()
+            assert sched.device_status() == 0
+            x.check(got, batch, 1, q, 1 / np.sqrt(128))
