@@ -94,12 +94,14 @@ class Pool:
         check(L.ca_pool_bytes_ex(C.byref(self.cfg), C.byref(nbytes)), "ca_pool_bytes_ex")
         self.kv_bytes = nbytes.value
         self._kv = None
+        self._device, self._device_index = None, None
         ptr = None
         if not host_only:
             import torch
             dev = torch.device(device if device is not None else "cuda")
             # over-allocate so the pool can start on a 1024-byte boundary
             self._kv = torch.empty(self.kv_bytes + 1024, dtype=torch.uint8, device=dev)
+            self._device, self._device_index = self._kv.device, self._kv.device.index
             base = self._kv.data_ptr()
             ptr = (base + 1023) // 1024 * 1024
             self._kv_offset = ptr - base
@@ -269,13 +271,13 @@ class Pool:
     def _check_tensor(self, x, shape, dtype, what: str) -> None:
         if x.dtype != dtype or not x.is_contiguous() or x.shape != shape:
             raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
-        if x.device != self._kv.device:
-            raise ValueError(f"{what} is on {x.device}, the pool on {self._kv.device}")
+        if x.device != self._device:
+            raise ValueError(f"{what} is on {x.device}, the pool on {self._device}")
 
     def _stream(self, stream) -> int | None:
         """The raw handle of ``stream`` (default: the current one of the
         pool's device)."""
-        return _stream_ptr(stream, None if self._kv is None else self._kv.device.index)
+        return _stream_ptr(stream, self._device_index)
 
     def remove(self, seq_id: int) -> None:
         check(capi.lib().ca_remove_seq(self._h, int(seq_id)), "ca_remove_seq")
@@ -471,14 +473,15 @@ def select_chunks(pool: Pool, sched: Schedule, q, top_k: int, layer: int = 0, si
     import torch
     _check_lists(pool, sched)
     pool._check_tensor(q, (sched.b, pool.n_heads, pool.head_dim), torch.float16, "q")
-    shape = (sched.b, pool.n_kv_heads, int(top_k))
-    if min(shape) < 1 or not 0 <= int(sink) + int(recent) <= int(top_k) or min(int(sink), int(recent)) < 0:
+    top_k, sink, recent = int(top_k), int(sink), int(recent)
+    shape = (sched.b, pool.n_kv_heads, top_k)
+    if top_k < 1 or sink < 0 or recent < 0 or sink + recent > top_k:
         raise ValueError("top_k must be at least 1 and cover sink + recent")
     if out is None:
-        out = torch.empty(shape, dtype=torch.int32, device=q.device)
+        out = torch.empty(shape, dtype=torch.int32, device=pool._device)
     else:
         pool._check_tensor(out, shape, torch.int32, "out")
-    check(capi.lib().ca_select_chunks(pool._h, sched._h, int(layer), q.data_ptr(), int(top_k), int(sink), int(recent),
+    check(capi.lib().ca_select_chunks(pool._h, sched._h, int(layer), q.data_ptr(), top_k, sink, recent,
                                       out.data_ptr(), pool._stream(stream)), "ca_select_chunks")
     return out
 
@@ -493,9 +496,10 @@ def sparse_decode_attention(pool: Pool, sched: Schedule, q, chunks, out=None, la
     _check_lists(pool, sched)
     shape = (sched.b, pool.n_heads, pool.head_dim)
     pool._check_tensor(q, shape, torch.float16, "q")
-    if chunks.dim() != 3 or chunks.shape[2] < 1:
+    n = chunks.shape[-1] if chunks.dim() == 3 else 0
+    if n < 1:
         raise ValueError("chunks must be an int32 tensor [b, Hkv, n] with n >= 1")
-    pool._check_tensor(chunks, (sched.b, pool.n_kv_heads, chunks.shape[2]), torch.int32, "chunks")
+    pool._check_tensor(chunks, (sched.b, pool.n_kv_heads, n), torch.int32, "chunks")
     if out is None:
         out = torch.empty_like(q)
     else:
@@ -503,7 +507,7 @@ def sparse_decode_attention(pool: Pool, sched: Schedule, q, chunks, out=None, la
     if scale is None:
         scale = 1.0 / math.sqrt(pool.head_dim)
     check(capi.lib().ca_sparse_attention(pool._h, sched._h, int(layer), q.data_ptr(), chunks.data_ptr(),
-                                         chunks.shape[2], out.data_ptr(), float(scale), pool._stream(stream)),
+                                         n, out.data_ptr(), float(scale), pool._stream(stream)),
           "ca_sparse_attention")
     return out
 
