@@ -219,7 +219,9 @@ __device__ __forceinline__ bool f4_tiles_own(F4Ctx& c, int tiles, const uint32_t
 // warp only, straight into its operand (code * scale is exact in fp16), and a
 // row's output needs no meeting of warps at the end.  A row's softmax reference
 // is the same for all warps: a barrier that is also a vote tells whether any
-// score passes it by more than the slack.
+// score passes it by more than the slack.  The weights are rounded to fp16 for
+// the product (half a step, 2^-11 of each), and summed in fp32 as rounded, by the
+// tensor cores too: an output stays an average of its values exactly.
 template <int C, int D, int NP>
 __device__ __forceinline__ void f4_wide_scores(const uint8_t* tile, int blk, uint32_t qa, float (&s)[2 * NP][4],
                                                int lane) {

@@ -5,7 +5,8 @@ through every entry point against the fp64 definition over those values.
 Tolerance of an attention output, from its roundings: the fp16 output (half a
 step, 2^-11 of the value), the weights p held in fp16 (2^-11 of each, so
 2^-11 * A with A = sum p|v| over the softmax), and 2^-12 * A for everything in
-32 bits (scores: products of fp16 are exact, 128 sums and the scales' fp32
+32 bits (in units of more than 8 rows the weights' sum is of the rounded ones:
+an output then moves by at most 2^-11 * sum p|v - out|; scores: products of fp16 are exact, 128 sums and the scales' fp32
 products of magnitude below 2^6 leave below 2^-14 in the exponent; exp2 is
 good to 2^-22; weights below fp16's normal range are off by 2^-25 each, 2^-13
 over 4096 tokens)."""
