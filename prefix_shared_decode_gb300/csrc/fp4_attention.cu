@@ -231,7 +231,7 @@ __device__ __forceinline__ void f4_wide_scores(const uint8_t* tile, int blk, uin
     const uint8_t* ks = tile + T::kKScales + (blk * 16 + g) * (D / 16);
     const uint32_t row = qa + ((i >> 1) * 8 + j) * (2 * D), at = (uint32_t)((i & 1) ^ j);
 #pragma unroll
-    for (int nb = 0; nb < 8; ++nb) s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.f;
+    for (int nb = 0; nb < 2 * NP; ++nb) s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.f;
 #pragma unroll
     for (int sp = 0; sp < D / 64; ++sp) {                 // four steps of 16 dims
         uint32_t w0[2], w1[2], c0[1], c1[1], h0[2], h1[2];
