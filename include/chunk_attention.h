@@ -500,11 +500,14 @@ int ca_sched_device_status(const ca_sched* sched, void* stream);
  * a host-only pool's schedule keeps a host word (ca_sched_device_status then
  * reads that one).  CA_ERR_INVALID for a non-negative or unknown code.
  *
- * ca_sched_inject_stall: the next n_calls decode calls on this schedule run
- * with their producer warps first waiting for a barrier phase that nothing
- * completes.  No copy is issued; that wait and the consumers' first waits
- * give up after their limit (~1 s), the call's results are undefined and
- * ca_sched_device_status() returns CA_ERR_TIMEOUT.  Later calls run normally.
+ * ca_sched_inject_stall: the next n_calls decode or ca_sparse_attention calls
+ * on this schedule run with waits that run out.  A producer warp first waits
+ * for a barrier phase that nothing completes and issues no copy; that wait and
+ * the consumers' first waits give up after their limit (~1 s).  (In CTAs of odd
+ * number of ca_sparse_attention one consumer warp gives up at once instead,
+ * while its tiles come.)  The call ends within a few such limits, its results
+ * are undefined and ca_sched_device_status() returns CA_ERR_TIMEOUT.  Later
+ * calls run normally.
  *
  * ca_pool_inject_alloc_failure: the host allocation points of the coming
  * inserts and appends pass after_n times, then one fails as if the host were

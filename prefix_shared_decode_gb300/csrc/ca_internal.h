@@ -238,8 +238,8 @@ struct Sched {
     void* ev_begin = nullptr;
     void* ev_end = nullptr;
     // Test hooks: the status word of a host-only pool's schedule, and the
-    // number of coming decode calls whose producer stalls (every wait then
-    // gives up after its limit and the call reports CA_ERR_TIMEOUT).
+    // number of coming decode or listed-chunk calls whose producer stalls (every
+    // wait then gives up after its limit and the call reports CA_ERR_TIMEOUT).
     mutable int32_t host_status = 0;
     mutable int32_t stall_calls = 0;
 };

@@ -52,6 +52,7 @@ struct ListParams {
     int32_t* counters;            // pieces of each unit that have arrived (0 between calls)
     float* parts;                 // [2 per CTA] (m, s) of the rows, then their outputs
     float scale_log2, out_scale;
+    int32_t test_stall;           // attention, test hook: waits that run out (below)
 };
 
 // ---------------------------------------------------------------------------
@@ -683,6 +684,13 @@ struct Frag<0, C, D, NB, FEW> {                  // fp4
 // it clears again) merges them in the order of the pieces: nothing waits, and
 // results do not depend on the order of arrival.  One warp sees to that while
 // the others go on with the next unit; all four at the end of the stretch.
+//
+// A consumer whose wait for a tile runs out reports it and waits for no tile
+// any more, but goes through the rest of its CTA's pieces with the others: the
+// named barriers at a piece's end count all four warps and have no limit of
+// their own.  So each warp gives up once at most, the CTA ends within a few of
+// the waits' limits, and the units' counters end at 0 as always; the outputs
+// of its units are undefined.
 // ---------------------------------------------------------------------------
 constexpr int kSpWarps = 4, kSpThreads = 32 * (kSpWarps + 1), kSpStages = 12;
 // The softmax reference is kept 5 below a running maximum and raised only when
@@ -748,6 +756,20 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
     if (warp == W) {
         // ------------------------------ producer ------------------------------
         const uint64_t pol = policy_evict_first();
+        if (p.test_stall && !(blockIdx.x & 1)) {
+            // Test hook (ca_sched_inject_stall): no tile is copied, and of several
+            // groups the first alone is told that its piece ends, so that it stands
+            // at the piece's barriers while the others' waits run out.
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            if (lane == 0) {
+                if (NG > 1) {
+                    stage_ntok[0] = -1;
+                    mbar_arrive(full0);
+                }
+                if (!mbar_wait(full0 + 8 * (NG > 1), 0u)) set_status(p.status, CA_ERR_TIMEOUT);
+            }
+            return;
+        }
         int st = 0, done = 0;                              // ring slot; slots filled so far
         uint32_t ph = 1u;                                  // the empty barriers' phase: free at first
         bool ok = true;
@@ -846,6 +868,10 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
     int st = warp / NBLK;                                  // the warp's next slot: its group's
     const int blk = warp % NBLK;                           // its block of that group's tiles
     uint32_t ph = 0u;
+    // (the test hook's other half, in CTAs of odd number: one warp of the four
+    // gives up while its tiles come)
+    bool alive = !(p.test_stall && (blockIdx.x & 1) && warp == 0);
+    if (!alive) set_status(p.status, CA_ERR_TIMEOUT);
     // (every piece moves the ring on by its tiles and a slot for each group, so
     // the groups' turns shift from piece to piece; a group's own slots do not)
     for (long long e = e0; e < e1;) {
@@ -883,10 +909,11 @@ sparse_attention_kernel(const __grid_constant__ CUtensorMap tmap, const ListPara
 #pragma unroll
             for (int db = 0; db < D / 16; ++db) o[nb][db][0] = o[nb][db][1] = o[nb][db][2] = o[nb][db][3] = 0.f;
         }
-        for (bool more = true; more;) {
-            if (!mbar_wait(full0 + 8 * st, ph)) {
+        for (bool more = alive; more;) {
+            if (!warp_wait(full0 + 8 * st, ph)) {
                 set_status(p.status, CA_ERR_TIMEOUT);
-                return;
+                alive = false;
+                break;
             }
             const int ntok = stage_ntok[st];
             more = ntok >= 0;
@@ -1251,6 +1278,10 @@ int launch_sparse(const Pool& p, const Sched& s, int32_t layer, const void* q, c
     a.parts = static_cast<float*>(s.list_parts);
     size_t smem;
     a.n_stages = sparse_stages(k, &smem);
+    if (s.stall_calls > 0) {
+        a.test_stall = 1;
+        --s.stall_calls;
+    }
     // Two entries per CTA at least: a piece costs its queries, a partial and a place in the merge.
     const int64_t entries = (int64_t)a.n_units * top_k;
     const int grid = (int)std::min<int64_t>((int64_t)k.per_sm * p.sms, (entries + 1) / 2);
