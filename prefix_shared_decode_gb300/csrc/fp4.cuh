@@ -119,8 +119,11 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
     return *reinterpret_cast<const uint32_t*>(&r);
 }
-// mbar_wait by a whole warp: its lanes agree on whether the wait ran out.
+// mbar_wait by a whole warp: its lanes agree on whether the wait ran out.  (A
+// vote on the first try, before any loop: 64 sequences of fp4 tiles under a
+// shared prompt 58.7 us, with the one vote behind the loop 59.5.)
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+    if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
     return __all_sync(kFull, mbar_wait(bar, parity));
 }
 template <int N>

@@ -81,6 +81,15 @@ __device__ __forceinline__ bool f4_sync_any(bool x) {      // the same barrier: 
     return r != 0u;
 }
 
+// A wait for a tile that runs out: the warp reports it, takes no tile any more
+// and goes on to the next barrier, which is a vote (at a unit's begin, where a
+// small head's warps meet, where a wide step raises its references): the
+// consumers leave together.  (A warp that left alone would have the others stand
+// at a barrier that has no limit: a tile that lands at the end of the limit is
+// seen by some warps only.)  So each warp gives up once at most, and the
+// producer, which gets no slot back from it, after its own limit; the call's
+// outputs are undefined.
+
 // What the consumers' loops share.
 struct F4Ctx {
     const uint8_t* stages;
@@ -91,6 +100,12 @@ struct F4Ctx {
     int S, st, it;            // ring slots, the next one, tiles taken
     uint32_t ph;
     int w, lane, flush;       // flush: heads ended (exchange parity)
+    // The test hook's other half, in CTAs of odd number: warp 0 behaves as if its
+    // wait had run out while the tiles come, at a unit's first (in CTAs 4i + 1) or
+    // inside a head (4i + 3).
+    __device__ __forceinline__ bool gives_up(const AttnParams& p, uint32_t cta) const {
+        return p.test_stall && (blockIdx.x & 3u) == cta && w == 0;
+    }
     __device__ __forceinline__ void next() {
         ++it;
         if (++st == S) {
@@ -180,17 +195,21 @@ __device__ __forceinline__ void f4_mask(float (&x)[NB][4], int tok, int ntok, in
     }
 }
 
-// One head's `tiles` tiles, each warp taking 16 tokens of its own; false on a
-// timeout.
+// One head's `tiles` tiles, each warp taking 16 tokens of its own; false where
+// its wait ran out.
 template <int C, int D, int NB, bool FEW>
-__device__ __forceinline__ bool f4_tiles_own(F4Ctx& c, int tiles, const uint32_t (&qb)[NB][D / 16][2],
-                                             const int (&lim)[NB][2], int first_lim, float scale_log2, int32_t* status,
-                                             F4State<D, NB>& a) {
+__device__ __forceinline__ bool f4_tiles_own(F4Ctx& c, const AttnParams& p, int tiles,
+                                             const uint32_t (&qb)[NB][D / 16][2], const int (&lim)[NB][2],
+                                             int first_lim, F4State<D, NB>& a) {
     constexpr int NBLK = C / 16;
     const int tg = f4_token(c.lane >> 2);
+    if (c.gives_up(p, 3)) {
+        set_status(p.status, CA_ERR_TIMEOUT);
+        return false;
+    }
     for (; tiles > 0; --tiles) {
-        if (!mbar_wait(c.full0 + 8 * c.st, c.ph)) {
-            set_status(status, CA_ERR_TIMEOUT);
+        if (!warp_wait(c.full0 + 8 * c.st, c.ph)) {
+            set_status(p.status, CA_ERR_TIMEOUT);
             return false;
         }
         const int ntok = c.ntok[c.st];
@@ -202,7 +221,7 @@ __device__ __forceinline__ bool f4_tiles_own(F4Ctx& c, int tiles, const uint32_t
             uint32_t pb[NB][2];
             f4_scores<C, D, NB, FEW>(tile, blk, qb, x, c.lane);
             const int tok0 = c.tok0[c.st];
-            f4_mask<NB, FEW>(x, blk * 16 + tg, ntok, tok0, tok0 + (C - 1) > first_lim, lim, scale_log2);
+            f4_mask<NB, FEW>(x, blk * 16 + tg, ntok, tok0, tok0 + (C - 1) > first_lim, lim, p.scale_log2);
             f4_softmax<D, NB, FEW>(x, a, pb);
             f4_pv<C, D, NB>(tile, blk, pb, a.o, c.lane);
         }
@@ -330,7 +349,7 @@ __device__ __forceinline__ void f4_wide_pv(const uint8_t* tile, int blk, int b, 
 // to a number known at run time would wait for every load of operands), whose
 // queries lie in qreg (word 2t of a row's 16 dims before word 2t + 1 of all t:
 // the operand order of the widened keys), to the partials of its rows.
-// scale_log2 > 0.  False on a timeout.
+// scale_log2 > 0.  False, for all warps, where a wait ran out.
 template <int C, int D, int NP>
 __device__ __forceinline__ bool f4_wide_head(F4Ctx& c, const AttnParams& p, WideTables* tab, int tiles, int rows,
                                              float scale_log2) {
@@ -351,17 +370,16 @@ __device__ __forceinline__ bool f4_wide_head(F4Ctx& c, const AttnParams& p, Wide
     for (; tiles > 0; tiles -= TP, first = false) {
         const int nt = min(tiles, TP);
         auto slot_of = [&](int k) { return c.st + k < c.S ? c.st + k : c.st + k - c.S; };
-        for (int k = 0; k < nt; ++k) {
+        bool late = c.gives_up(p, 3);          // a wait ran out: on to the vote
+        for (int k = 0; k < nt && !late; ++k) {
             const int sl = slot_of(k);
-            if (!mbar_wait(c.full0 + 8 * sl, c.st + k < c.S ? c.ph : c.ph ^ 1u)) {
-                set_status(p.status, CA_ERR_TIMEOUT);
-                return false;
-            }
+            late = !warp_wait(c.full0 + 8 * sl, c.st + k < c.S ? c.ph : c.ph ^ 1u);
         }
+        if (late) set_status(p.status, CA_ERR_TIMEOUT);
         float s[2 * NP][4];
         {
             const int k = w / NBLK, blk = w % NBLK, sl = slot_of(k);
-            const int left = k < nt ? c.ntok[sl] - blk * 16 : 0;      // tokens of the warp's block
+            const int left = k < nt && !late ? c.ntok[sl] - blk * 16 : 0;      // tokens of the warp's block
             if (left > 0) {
                 f4_wide_scores<C, D, NP>(c.stages + (size_t)sl * F4Tile<C, D>::kBytes, blk, qa, s, lane);
                 const int tg = f4_token(g);
@@ -387,7 +405,7 @@ __device__ __forceinline__ bool f4_wide_head(F4Ctx& c, const AttnParams& p, Wide
                 for (int nb = 0; nb < 2 * NP; ++nb) s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = -INFINITY;
             }
         }
-        bool grow = false;
+        bool grow = late;
         if (!first) {
 #pragma unroll
             for (int nb = 0; nb < 2 * NP; ++nb) {
@@ -407,7 +425,7 @@ __device__ __forceinline__ bool f4_wide_head(F4Ctx& c, const AttnParams& p, Wide
                 }
                 if (g == 0) *reinterpret_cast<float2*>(&tab->top[w][nb * 8 + 2 * t]) = mx;
             }
-            f4_sync();
+            if (f4_sync_any(late)) return false;
             if (const int row = threadIdx.x; row < NP * 16) {
                 const float old = first ? -FLT_MAX : tab->ref[row];      // (any finite score raises it)
                 const float mx = fmaxf(fmaxf(tab->top[0][row], tab->top[1][row]),
@@ -505,7 +523,8 @@ __device__ __forceinline__ bool f4_wide_head(F4Ctx& c, const AttnParams& p, Wide
 // first partial id of row w + 4 j's pieces, this one is `part` further: added
 // here, so that the id's load, begun with the head, is first waited for here.
 template <int C, int D, bool FEW>
-__device__ __forceinline__ void f4_finish(F4Ctx& c, const AttnParams& p, F4State<D, 1>& a, int rows, int pid, int part) {
+__device__ __forceinline__ bool f4_finish(F4Ctx& c, const AttnParams& p, F4State<D, 1>& a, int rows, int pid, int part,
+                                          bool late) {
     const int g = c.lane >> 2, t = c.lane & 3;
     float* ob = reinterpret_cast<float*>((c.flush & 1) ? c.qreg : c.exch);
     // column of a row's dim: the fragments' stores of four rows stay apart
@@ -526,7 +545,7 @@ __device__ __forceinline__ void f4_finish(F4Ctx& c, const AttnParams& p, F4State
                     make_float2(a.o[0][db][r], a.o[0][db][r + 2]);
         }
     }
-    f4_sync();
+    if (f4_sync_any(late)) return false;
     for (int row = c.w, j = 0; row < rows; row += kF4Warps, ++j) {
         const int id = __shfl_sync(kFull, pid, j) + part;
         float2 q[kF4Warps];
@@ -549,6 +568,7 @@ __device__ __forceinline__ void f4_finish(F4Ctx& c, const AttnParams& p, F4State
         if (c.lane < D / 4) reinterpret_cast<float4*>(p.part_o + (size_t)id * D)[c.lane] = acc;
         if (c.lane == 0) p.part_ms[id] = make_float2(M, sum);
     }
+    return true;
 }
 
 template <int C, int D>
@@ -599,7 +619,7 @@ fp4_attention_kernel(const __grid_constant__ CUtensorMap, const AttnParams p) {
         // one claim ahead; the pool before the dependency wait only where
         // kv_stable says so); a step is one bulk copy.
         if (lane != 0) return;
-        if (p.test_stall) {
+        if (p.test_stall && !(blockIdx.x & 1)) {
             if (!mbar_wait(full0, 0u)) set_status(p.status, CA_ERR_TIMEOUT);
             return;
         }
@@ -769,17 +789,15 @@ fp4_attention_kernel(const __grid_constant__ CUtensorMap, const AttnParams p) {
     if (n_static > 0 && RW <= 8 && fld(dn, F_KIND) == UNIT_SF) prefetch(fld(dn, F_QROW), fld(dn, F_HEAD));
     for (int seq = 0;; ++seq) {
         // The unit's first stage (or the closing one) carries its id.
-        if (!mbar_wait(full0 + 8 * c.st, c.ph)) {
-            set_status(p.status, CA_ERR_TIMEOUT);
-            return;
-        }
-        const int cur = ring[seq % kF4Ring];
-        if (cur < 0) break;
-        const int32_t dc = (seq < n_static) ? dn : load_desc(cur);
+        const bool in = !c.gives_up(p, 1) && warp_wait(full0 + 8 * c.st, c.ph);
+        if (!in) set_status(p.status, CA_ERR_TIMEOUT);
+        const int cur = ring[seq % kF4Ring];   // (anything, if that ran out)
+        const int32_t dc = (seq < n_static) ? dn : (in && cur >= 0) ? load_desc(cur) : 0;
         const bool next_static = seq + 1 < n_static;
         if (next_static) dn = load_desc(u_begin + seq + 1);
         const bool next_own = next_static && RW <= 8 && fld(dn, F_KIND) == UNIT_SF;
-        f4_sync();                             // the previous unit's exchange has been read
+        if (f4_sync_any(!in)) return;          // (the previous unit's exchange has been read, too)
+        if (cur < 0) break;
         const bool is_sf = fld(dc, F_KIND) == UNIT_SF;
         const int q_lo = fld(dc, F_QLO), q_hi = fld(dc, F_QHI), cb = fld(dc, F_CB), ce = fld(dc, F_CE);
         const int qrow = fld(dc, F_QROW);
@@ -829,13 +847,11 @@ fp4_attention_kernel(const __grid_constant__ CUtensorMap, const AttnParams p) {
                 F4State<D, 1> a;
                 a.clear();
                 if (half) {
-                    if (!f4_tiles_own<C, D, 1, true>(c, seg_end - L, qb, lim, first_lim, p.scale_log2, p.status, a))
-                        return;
-                    f4_finish<C, D, true>(c, p, a, rows, pid, upart);
+                    const bool all = f4_tiles_own<C, D, 1, true>(c, p, seg_end - L, qb, lim, first_lim, a);
+                    if (!f4_finish<C, D, true>(c, p, a, rows, pid, upart, !all)) return;
                 } else {
-                    if (!f4_tiles_own<C, D, 1, false>(c, seg_end - L, qb, lim, first_lim, p.scale_log2, p.status, a))
-                        return;
-                    f4_finish<C, D, false>(c, p, a, rows, pid, upart);
+                    const bool all = f4_tiles_own<C, D, 1, false>(c, p, seg_end - L, qb, lim, first_lim, a);
+                    if (!f4_finish<C, D, false>(c, p, a, rows, pid, upart, !all)) return;
                 }
                 L = seg_end;
             }
