@@ -12,6 +12,7 @@ memory and streams.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import math
 from array import array
@@ -246,8 +247,7 @@ class Pool:
             raise ValueError("lengths must not be negative")
         shape = (self.n_layers, sum(lens), self.n_kv_heads, self.head_dim)
         if out is None:
-            k = torch.empty(shape, dtype=torch.float16, device=self._kv.device)
-            v = torch.empty(shape, dtype=torch.float16, device=self._kv.device)
+            k, v = (self._empty(shape, torch.float16, stream) for _ in range(2))
         else:
             k, v = out
             self._check_tensor(k, shape, torch.float16, "out")
@@ -278,6 +278,26 @@ class Pool:
         """The raw handle of ``stream`` (default: the current one of the
         pool's device)."""
         return _stream_ptr(stream, self._device_index)
+
+    def _empty(self, shape, dtype, stream):
+        """A tensor on the pool's device for work on ``stream``."""
+        import torch
+        with self._under(stream):
+            return torch.empty(shape, dtype=dtype, device=self._device)
+
+    def _under(self, stream):
+        """``torch.cuda.stream`` of a stream in any form.  What a call on it
+        allocates is allocated under it: torch hands freed memory on in the
+        order of the stream it was allocated on, so a block of another stream
+        could still be in use there, or be given away while ``stream`` works."""
+        import torch
+        if stream is None:
+            return contextlib.nullcontext()
+        if not isinstance(stream, torch.cuda.Stream):
+            raw = _stream_ptr(stream)
+            stream = (torch.cuda.ExternalStream(raw, device=self._device) if raw
+                      else torch.cuda.default_stream(self._device))
+        return torch.cuda.stream(stream)
 
     def remove(self, seq_id: int) -> None:
         check(capi.lib().ca_remove_seq(self._h, int(seq_id)), "ca_remove_seq")
@@ -346,7 +366,7 @@ class Schedule:
         self._h = None
         self.b = 0
         self.q_len = 1
-        self._ws = None
+        self._ws, self._ws_stream = None, None
         self._ws_need = None            # bytes of the device workspace, until the next build
         self._ids, self._ids_ptr, self._ids_list, self._flags = None, None, None, 0
 
@@ -403,15 +423,26 @@ class Schedule:
         check(fn(self._h, C.byref(n)), "ca_workspace_bytes")
         return n.value
 
-    def workspace(self, host_io: bool = False):
+    def workspace(self, host_io: bool = False, stream=None):
         """A zero-filled device workspace large enough for this schedule
-        (cached and grown on demand)."""
-        import torch
+        (cached and grown on demand), for work on ``stream``."""
+        return self._workspace(host_io, stream, self.pool._stream(stream))
+
+    def _workspace(self, host_io: bool, stream, raw):
         need = self.workspace_bytes(host_io) if host_io or self._ws_need is None else self._ws_need
         if not host_io:
             self._ws_need = need
         if self._ws is None or self._ws.numel() < need:
-            self._ws = torch.zeros(max(need, 256), dtype=torch.uint8, device=self.pool._kv.device)
+            import torch
+            with self.pool._under(stream):
+                self._ws = torch.zeros(max(need, 256), dtype=torch.uint8, device=self.pool._device)
+            self._ws_stream = raw
+        elif self._ws_stream != raw:
+            # another stream than before: not to be given away while that one works
+            import torch
+            with self.pool._under(stream):
+                self._ws.record_stream(torch.cuda.current_stream(self.pool._device))
+            self._ws_stream = raw
         return self._ws
 
     def device_status(self, stream=None) -> int:
@@ -429,7 +460,9 @@ def decode_attention(pool: Pool, sched: Schedule, q, out=None, layer: int = 0, s
                      workspace=None, stream=None):
     """out[i, h] = softmax(scale q[i, h] . K^T) V over sequence seq_ids[i]'s
     context, via the two-phase kernel.  q: fp16 [b, H, D] on the GPU
-    ([b, q_len, H, D] for a multi-token schedule)."""
+    ([b, q_len, H, D] for a multi-token schedule).  With ``stream``, a result
+    that the call allocates is that stream's, as under ``torch.cuda.stream``
+    (so too in the calls below and in ``Pool.read_batch``)."""
     import torch
     if q.dtype != torch.float16 or not q.is_contiguous():
         raise ValueError("q must be a contiguous fp16 tensor")
@@ -438,12 +471,13 @@ def decode_attention(pool: Pool, sched: Schedule, q, out=None, layer: int = 0, s
     if q.shape != want:
         raise ValueError(f"q has shape {tuple(q.shape)}, the schedule needs {want}")
     if out is None:
-        out = torch.empty_like(q)
+        out = torch.empty_like(q) if stream is None else pool._empty(want, torch.float16, stream)
     if scale is None:
         scale = 1.0 / math.sqrt(pool.head_dim)
-    ws = workspace if workspace is not None else sched.workspace()
+    raw = pool._stream(stream)
+    ws = workspace if workspace is not None else sched._workspace(False, stream, raw)
     check(capi.lib().ca_decode_attention(pool._h, sched._h, layer, q.data_ptr(), out.data_ptr(),
-                                         float(scale), ws.data_ptr(), ws.numel(), pool._stream(stream)),
+                                         float(scale), ws.data_ptr(), ws.numel(), raw),
           "ca_decode_attention")
     return out
 
@@ -454,10 +488,11 @@ def decode_attention_host(pool: Pool, sched: Schedule, q_host, out_host, layer: 
     copies out on ``stream``; the caller synchronises."""
     if scale is None:
         scale = 1.0 / math.sqrt(pool.head_dim)
-    ws = workspace if workspace is not None else sched.workspace(host_io=True)
+    raw = pool._stream(stream)
+    ws = workspace if workspace is not None else sched._workspace(True, stream, raw)
     check(capi.lib().ca_decode_attention_host(pool._h, sched._h, layer, q_host.data_ptr(),
                                               out_host.data_ptr(), float(scale), ws.data_ptr(),
-                                              ws.numel(), pool._stream(stream)),
+                                              ws.numel(), raw),
           "ca_decode_attention_host")
     return out_host
 
@@ -478,7 +513,8 @@ def select_chunks(pool: Pool, sched: Schedule, q, top_k: int, layer: int = 0, si
     if top_k < 1 or sink < 0 or recent < 0 or sink + recent > top_k:
         raise ValueError("top_k must be at least 1 and cover sink + recent")
     if out is None:
-        out = torch.empty(shape, dtype=torch.int32, device=pool._device)
+        out = (torch.empty(shape, dtype=torch.int32, device=pool._device) if stream is None
+               else pool._empty(shape, torch.int32, stream))
     else:
         pool._check_tensor(out, shape, torch.int32, "out")
     check(capi.lib().ca_select_chunks(pool._h, sched._h, int(layer), q.data_ptr(), top_k, sink, recent,
@@ -501,7 +537,7 @@ def sparse_decode_attention(pool: Pool, sched: Schedule, q, chunks, out=None, la
         raise ValueError("chunks must be an int32 tensor [b, Hkv, n] with n >= 1")
     pool._check_tensor(chunks, (sched.b, pool.n_kv_heads, n), torch.int32, "chunks")
     if out is None:
-        out = torch.empty_like(q)
+        out = torch.empty_like(q) if stream is None else pool._empty(shape, torch.float16, stream)
     else:
         pool._check_tensor(out, shape, torch.float16, "out")
     if scale is None:
