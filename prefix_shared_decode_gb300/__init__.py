@@ -575,14 +575,15 @@ class DecodeGraph:
         self.workspace = workspace if workspace is not None else sched.workspace()
         self.scale = scale
         self._key = sched._key()
-        side = torch.cuda.Stream()
-        side.wait_stream(torch.cuda.current_stream())
-        with torch.cuda.stream(side):
-            self._record()                       # one uncaptured pass first
-        torch.cuda.current_stream().wait_stream(side)
-        self.graph = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(self.graph):
-            self._record()
+        with torch.cuda.device(pool._device):    # (the calls run there, whatever device is current)
+            side = torch.cuda.Stream()
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                self._record()                   # one uncaptured pass first
+            torch.cuda.current_stream().wait_stream(side)
+            self.graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(self.graph):
+                self._record()
 
     def _record(self):
         for layer, q, out in self.calls:
@@ -590,10 +591,12 @@ class DecodeGraph:
                              workspace=self.workspace)
 
     def replay(self) -> None:
-        """Run every recorded call on the current stream."""
+        """Run every recorded call on the pool's device's current stream."""
+        import torch
         if self.sched._key() != self._key:
             raise CAError(capi.CA_ERR_STALE, "DecodeGraph: the pool or the schedule changed after capture")
-        self.graph.replay()
+        with torch.cuda.device(self.pool._device):
+            self.graph.replay()
 
 
 def kernel_launches() -> int:
