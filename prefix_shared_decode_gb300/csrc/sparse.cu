@@ -458,11 +458,9 @@ __global__ void __launch_bounds__(kSelThreads) select_chunks_kernel(const ListPa
         const uint32_t open = places - c.x;               // places left for the band
         cut = high;
         if (c.y == open) {
-            cut = low - 1u;                               // low is at least 1 here: NaN keys are 0
-            if (low == 0u) {                              // the unbounded band: every chunk is taken
-                for (int j = threadIdx.x; j < n; j += kSelThreads) keys[j] = kSure;
-                cut = kTie;
-            }
+            // (low is at least 1 here: an unbounded band holds every chunk that is
+            // not forced, and those are more than the places, as n > K)
+            cut = low - 1u;
         } else if (E == 0.f) {                            // every score in the band is the same
             for (int j = threadIdx.x; j < n; j += kSelThreads)
                 if (keys[j] >= low && keys[j] <= high) keys[j] = kTie;
