@@ -70,11 +70,14 @@ int check_cfg(const PoolCfg* c) {
 size_t pool_bytes(const PoolCfg& c) { return pool_total_bytes(c); }
 
 // The pool's device made current for one call (its kernels run there whatever
-// device the caller has current), and the caller's put back after it.
+// device the caller has current), and the caller's put back after it.  An error
+// that an earlier call met and reported is dropped, so that this call's launches
+// are not taken for failed (one that the device does not recover from comes back).
 struct DeviceGuard {
     int before = -1;
     bool ok = false, changed = false;
     explicit DeviceGuard(int device) {
+        (void)cudaGetLastError();
         if (cudaGetDevice(&before) != cudaSuccess) return;
         changed = before != device;
         ok = !changed || cudaSetDevice(device) == cudaSuccess;
