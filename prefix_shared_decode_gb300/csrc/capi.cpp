@@ -89,6 +89,11 @@ struct DeviceGuard {
     DeviceGuard& operator=(const DeviceGuard&) = delete;
 };
 
+// A schedule that could not be built gives back its buffers too.
+struct SchedFree {
+    void operator()(ca_sched* s) const { ca_sched_destroy(s); }
+};
+
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? CA_OK : CA_ERR_CUDA; }
 
 // Copy the plan blob to the device through the next pinned staging buffer.
@@ -390,7 +395,7 @@ int ca_build_schedule_ex(ca_pool* pool, const int64_t* seq_ids, int32_t b, int32
                 auto it = pool->seqs.find(seq_ids[i]);
                 if (it != pool->seqs.end() && it->second.length < q_len) return CA_ERR_INVALID;
             }
-        std::unique_ptr<ca_sched> fresh;
+        std::unique_ptr<ca_sched, SchedFree> fresh;
         if (!s) {
             fresh.reset(new ca_sched());
             s = fresh.get();
