@@ -4,7 +4,7 @@
 // All three are bound by DRAM bytes; a CTA takes one chunk of one key/value
 // head and layer, and goes through shared memory where the tile's order is
 // not the rows'.  1024 chunks of 64 tokens, 32 heads of 128 dims: 215 us to
-// store as fp4 (1.32 GB moved, 6.1 TB/s), 227 us to read back (5.8 TB/s), 91% and
+// store as fp4 (1.32 GB moved, 6.1 TB/s), 225 us to read back (5.8 TB/s), 91% and
 // 87% of the copy rate; bounds read the rows just written from L2.
 #include <cuda_runtime.h>
 

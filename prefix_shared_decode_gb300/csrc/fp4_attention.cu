@@ -21,12 +21,14 @@
 // warps about 250 instructions each.  So the path is written for issue slots:
 // a vote decides whether the softmax reference must rise, sums stay per lane
 // until the head ends, queries of the next head are fetched a head ahead, and
-// three CTAs per SM (128 registers a thread) cover the latencies.  65536 tiles
-// of single rows alone take 114 us, 80% of the copy rate; 64 sequences of 512
-// tokens of their own under 4096 shared ones, 32 heads of 128 dims, 56 us, of
-// which the single rows' tiles are half; a step of a shared tile (64 rows) takes
-// some 2100 cycles of an SM, 1150 of them its tensor products.  (Widening shared
-// tiles into fp16 in shared memory first, 16 rows a warp: 61 us.)
+// three CTAs per SM cover the latencies (at their 128 registers a thread the
+// instances of 128 dims spill 196 to 288 bytes, those of 64 dims 16 to 28).
+// 65536 tiles of single rows alone take 114 us, 79% of the copy rate; 64
+// sequences of 512 tokens of their own under 4096 shared ones, 32 heads of 128
+// dims, 55 us, where the own tiles by themselves take 38: the shared ones' 13.5
+// steps of 64 rows an SM are the other 17, and their 544 products a step, at the
+// 0.5 a cycle that an SM issues, some 7.5 of these.  (Widening shared tiles into
+// fp16 in shared memory first, 16 rows a warp: 61 us.)
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -130,7 +132,10 @@ struct F4State {
 };
 
 // Scaled and masked scores x of a 16-token block -> the operand p and the
-// state's sums.  FEW (up to 4 rows): row r is in columns 2r and 2r + 1, so that a
+// state's sums.  The weights are rounded to fp16 for the product with the values
+// alone, as in the other pools' kernels (mma takes 16-bit operands; half a step,
+// 2^-11 of each weight, so at most 2^-11 * sum p|v| of an output); their sum is
+// of the unrounded ones, in fp32.  FEW (up to 4 rows): row r is in columns 2r and 2r + 1, so that a
 // lane's two columns are one row and half the work is left.
 template <int D, int NB, bool FEW>
 __device__ __forceinline__ void f4_softmax(float (&x)[NB][4], F4State<D, NB>& a, uint32_t (&pb)[NB][2]) {

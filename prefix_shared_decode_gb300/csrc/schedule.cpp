@@ -219,6 +219,7 @@ constexpr double kF4CfFactor = 3.5, kF4CfRowsFactor = 2.5, kF4CfUnit = 2.0;
 // Rows of such a unit where positions bring several: with 64 the registers of
 // its outputs spill and small calls have few units (grouped heads over 4096
 // tokens 30.3 us where 32 take 24.9, two query tokens 35.8 and 33.0; four level).
+// A tile that 128 rows share is then widened four times.
 // With one row per position 64 are better (64 sequences: 59 us, with 32 61).
 constexpr int32_t kF4GroupRows = 32;
 

@@ -671,9 +671,11 @@ struct Frag<0, C, D, NB, FEW> {                  // fp4
 // slot -> token count) and keeps a ring of tiles in flight, across units; the
 // consumer warps take the tiles' blocks of 16 tokens with an online softmax.
 // Each ring slot belongs to the warps of one group, a warp per block of a tile.
-// Units of 64 tiles of 64 tokens, head_dim 128: 128 of fp16 45 us, 89% of the
-// copy rate, bound by DRAM; 128 of fp8 31 us (65%); 512 of fp4 59 us (77%),
-// bound by the instructions that widen a tile (58% of the issue slots, 52% of
+// Units of 64 tiles of 64 tokens, head_dim 128: 128 of fp16 46 us, 88% of the
+// copy rate, bound by DRAM; 128 of fp8 30 us (67%), two CTAs per SM at 162
+// registers, whose word loads and byte permutes bring two tokens beside each
+// other for every 32 dims; 512 of fp4 59 us (77%),
+// bound by the instructions that widen a tile (55% of the issue slots, 50% of
 // the ALU) in the shadow of its loads: three CTAs per SM hide most of them
 // (three of four warps and two of eight 69 us before the values' codes lay in
 // pairs, four of four 70, one of twelve 83).
@@ -693,7 +695,9 @@ struct Frag<0, C, D, NB, FEW> {                  // fp4
 constexpr int kSpWarps = 4, kSpThreads = 32 * (kSpWarps + 1), kSpStages = 12;
 // The softmax reference is kept 5 below a running maximum and raised only when
 // a score passes it by 13: the weights stay below 2^13 in their fp16 operand
-// and normal numbers down to 2^-19 (or less) of the largest.
+// and normal numbers down to 2^-19 (or less) of the largest.  They are rounded for
+// the product with the values alone (2^-11 of each, so at most 2^-11 * sum p|v| of
+// an output); their sum is of the unrounded ones, in fp32.
 constexpr float kSpLift = 5.f, kSpSlack = 8.f;
 
 template <int EB, int C, int D, int NB, bool FEW>
