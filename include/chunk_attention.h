@@ -505,9 +505,9 @@ int ca_sched_device_status(const ca_sched* sched, void* stream);
  * for a barrier phase that nothing completes and issues no copy; that wait and
  * the consumers' first waits give up after their limit (~1 s).  (In CTAs of odd
  * number of ca_sparse_attention, and of the decode calls of a CA_KV_FP4 pool, one
- * consumer warp gives up instead while its tiles come.)  The call ends within a few such limits, its results
- * are undefined and ca_sched_device_status() returns CA_ERR_TIMEOUT.  Later
- * calls run normally.
+ * consumer warp gives up instead while its tiles come.)  The call ends within a
+ * few such limits, its results are undefined and ca_sched_device_status()
+ * returns CA_ERR_TIMEOUT.  Later calls run normally.
  *
  * ca_pool_inject_alloc_failure: the host allocation points of the coming
  * inserts and appends pass after_n times, then one fails as if the host were
