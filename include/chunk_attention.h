@@ -482,6 +482,96 @@ int ca_sparse_attention(const ca_pool* pool, const ca_sched* sched, int32_t laye
                         const void* q_dev, const int32_t* lists_dev, int32_t top_k,
                         void* out_dev, float scale, void* stream);
 
+/* ---- attention of query blocks -------------------------------------------------
+ * Blocks of queries of any lengths, one for each sequence listed, attend to
+ * the sequences' contexts: a decoder's targets (or beams) to an encoder's states
+ * that the pool holds, or with CA_SCHED_CAUSAL a prompt's new tokens, whose rows
+ * have been inserted, to their whole context behind whatever prefix it shares.
+ *     out[r] = sum_t softmax_t(scale * q[r] . k_t) v_t
+ * over the context's tokens; under the mask, row j of a block of m sees tokens
+ * t <= n - m + j of a context of n (as the schedule found it; n may be less
+ * than m), and a row that sees none gives zeros.  The decode calls take up to
+ * 64 / group query tokens, the same number for each sequence, and read a shared
+ * chunk once for all sharers; these take the rest.
+ *
+ * ca_build_schedule_blocks: seq_ids[0..b) may repeat; q_lens[i] >= 0 query tokens
+ * each.  flags: CA_SCHED_CAUSAL or 0.  Reuse, upload and errors as
+ * ca_build_schedule (CA_ERR_INVALID also for a negative length,
+ * CA_ERR_UNSUPPORTED for more than 2^31 rows).  Such a schedule serves
+ * ca_cross_attention, ca_workspace_bytes and the status calls alone; the others
+ * refuse it (CA_ERR_INVALID).
+ *
+ * ca_cross_attention: q_dev / out_dev fp16 [sum of q_lens][n_heads][head_dim], block
+ * after block, 16-byte aligned, not overlapping.  ws_dev as for ca_decode_attention
+ * (ca_workspace_bytes may give 0; then it may be NULL).  One or two kernels on
+ * `stream`, capturable as the decode calls are: replays see what appends have
+ * put into the partial last chunks (the mask's n stays the schedule's).  The
+ * contexts' keys and values must be finite: weights of 0 are multiplied too.
+ * Errors: as ca_decode_attention. */
+int ca_build_schedule_blocks(ca_pool* pool, const int64_t* seq_ids, int32_t b,
+                             const int32_t* q_lens, uint32_t flags, ca_sched** inout,
+                             void* stream);
+int ca_cross_attention(const ca_pool* pool, const ca_sched* sched, int32_t layer,
+                       const void* q_dev, void* out_dev, float scale, void* ws_dev,
+                       size_t ws_bytes, void* stream);
+
+/* ---- accumulated attention weights ------------------------------------------
+ * What a decode step's queries weigh each token of their contexts with, added
+ * to running sums: the tokens that ca_evict keeps are those of largest sum.
+ * For batch row i, key/value head h and token t of the context
+ *     out[i][h][t] = weights[i][h][t] + sum over query tokens j and heads x of
+ *                    the group of softmax_t(scale * q[i][j][x] . k_t),
+ * for any schedule of ca_build_schedule(_ex), its causal mask included; past the
+ * context out is what weights is.  Keys alone are read.
+ *   weights_dev, out_dev  fp32 [b][n_kv_heads][room], the same or apart (not
+ *            overlapping otherwise); room at least the longest context (a
+ *            context that has outgrown it when a captured call is replayed is
+ *            reported as CA_ERR_DEVICE_BOUNDS by ca_sched_device_status)
+ *   ws_dev   >= ca_workspace_bytes_weights(sched) bytes (the scores, fp32), used
+ *            as ca_decode_attention's is
+ * Two kernels on `stream`; the same inputs give the same sums bit for bit.
+ * Errors: as ca_decode_attention; CA_ERR_UNSUPPORTED for more than 2^31 chunks
+ * of all the batch's contexts. */
+int ca_workspace_bytes_weights(const ca_sched* sched, size_t* bytes_out);
+int ca_accumulate_attention(const ca_pool* pool, const ca_sched* sched, int32_t layer,
+                            const void* q_dev, const float* weights_dev, float* out_dev,
+                            int32_t room, float scale, void* ws_dev, size_t ws_bytes,
+                            void* stream);
+
+/* ---- eviction -----------------------------------------------------------------
+ * Cut the contexts of a schedule's batch (one built with CA_SCHED_CHUNK_LISTS)
+ * to at most `budget` tokens each.  Every layer, sequence and key/value head keeps
+ * tokens of its own: the first `sink`, the last `recent`, and between them those of
+ * largest weights (ca_accumulate_attention's sums; ties go to the lower
+ * position, -0 is 0, NaN ranks below everything).  Contexts within the budget
+ * keep all their tokens.
+ *   weights_dev  fp32 [n_layers][b][n_kv_heads][room], room at least the longest
+ *            context
+ *   kept_dev int32 [n_layers][b][n_kv_heads][budget]: the positions kept, in
+ *            ascending order (all of a shorter context's, then -1)
+ *   out_dev  as weights_dev, the same or apart (not overlapping otherwise): the
+ *            kept tokens' weights in their new places, then zeros
+ * Kept rows move, as the pool holds them (nothing is quantised again), into new
+ * private chunks, lowest free slots first; the sink's whole chunks stay where they
+ * are, shared as before.  With into_ids (b ids that are not in the pool) the kept
+ * rows form new sequences of those ids and the old ones stay as they are: the
+ * new ones share the chunks that stay (all whole chunks of a context within its
+ * budget; a CA_NO_SHARING pool shares none).  NULL: in place; then the old
+ * chunks' references are dropped, and the new chunks must be free beforehand.
+ * Positions within a context are counted anew; keys keep whatever position they
+ * were made with.  What joins a cut sequence later never matches a prompt, since
+ * it follows tokens that are gone.
+ * Schedules go stale unless every context was within its budget and stayed in
+ * place.  Enqueued on `stream` behind the appends and calls before it there; not
+ * capturable (CA_ERR_INVALID).  A host-only pool changes its tree alone (NULL
+ * pointers).  Errors: CA_ERR_STALE; CA_ERR_OOM, CA_ERR_EXISTS, CA_ERR_CUDA;
+ * CA_ERR_INVALID (a schedule without lists, budget < 1 or < sink + recent, a
+ * room shorter than a context, repeated new ids, NULL or misaligned pointers).
+ * On any error the pool is unchanged. */
+int ca_evict(ca_pool* pool, const ca_sched* sched, const float* weights_dev, int32_t room,
+             int32_t budget, int32_t sink, int32_t recent, const int64_t* into_ids,
+             int32_t* kept_dev, float* out_dev, void* stream);
+
 /* Synchronise `stream` and read the schedule's device status word: CA_OK,
  * CA_ERR_DEVICE_BOUNDS or CA_ERR_TIMEOUT (or a code written by
  * ca_sched_inject_status); a non-zero word is then cleared, together with

@@ -23,7 +23,7 @@ from . import capi
 from .capi import CAError, check
 
 __all__ = ["Pool", "Schedule", "DecodeGraph", "decode_attention", "decode_attention_host", "select_chunks",
-           "sparse_decode_attention", "kernel_launches", "CAError"]
+           "sparse_decode_attention", "cross_attention", "accumulate_attention", "kernel_launches", "CAError"]
 
 
 _cuda_ok = None
@@ -44,6 +44,11 @@ def _stream_ptr(stream, device: int | None = None) -> int | None:
             return raw(torch.cuda.current_device() if device is None else device) or None
         stream = torch.cuda.current_stream(device)
     return int(getattr(stream, "cuda_stream", stream)) or None
+
+
+def _torch():
+    import torch
+    return torch
 
 
 def _i32(a) -> np.ndarray:
@@ -306,6 +311,49 @@ class Pool:
         ids = _ints("q", seq_ids)
         check(capi.lib().ca_remove_batch(self._h, len(ids), _at(ids)), "ca_remove_batch")
 
+    def evict(self, sched: "Schedule", weights=None, budget: int = 0, sink: int = 0, recent: int = 0, into=None,
+              out=None, stream=None):
+        """Cut the contexts of a batch to at most ``budget`` tokens each: every
+        layer, sequence and key/value head keeps the first ``sink`` tokens, the
+        last ``recent`` ones, and between them those of largest ``weights``
+        (``accumulate_attention``'s sums, fp32 [L, b, Hkv, room], rows in the
+        schedule's order).  Kept rows move into chunks of their own; the sink's
+        whole chunks stay where they are, shared as before.  ``into``: ids of
+        new sequences that take the kept rows while the old ones stay as they
+        are.  Needs a schedule with ``chunk_lists``; like every schedule it is
+        out of date afterwards.  Returns the kept positions, int32
+        [L, b, Hkv, budget] ascending, -1 behind a shorter context's, and the
+        weights in their new places, then zeros (a new tensor, or ``out``,
+        which may be ``weights``).  A host-only pool takes and gives None."""
+        if not sched._flags & capi.CA_SCHED_CHUNK_LISTS:
+            raise ValueError("the schedule was built without chunk_lists")
+        budget, sink, recent = int(budget), int(sink), int(recent)
+        if budget < 1 or sink < 0 or recent < 0 or sink + recent > budget:
+            raise ValueError("budget must be at least 1 and cover sink + recent")
+        new = None if into is None else _ints("q", into)
+        if new is not None and len(new) != sched.b:
+            raise ValueError(f"into must have an id for each of the {sched.b} sequences")
+        kept, room = None, 0
+        if not self.host_only:
+            import torch
+            rows = (self.n_layers, sched.b, self.n_kv_heads)
+            room = weights.shape[-1] if weights is not None and weights.dim() == 4 else 0
+            if room < 1:
+                raise ValueError("weights must be an fp32 tensor [L, b, Hkv, room] with room >= 1")
+            self._check_tensor(weights, rows + (room,), torch.float32, "weights")
+            if out is None:
+                out = self._empty(weights.shape, torch.float32, stream)
+            else:
+                self._check_tensor(out, weights.shape, torch.float32, "out")
+            kept = self._empty(rows + (budget,), torch.int32, stream)
+        elif weights is not None or out is not None:
+            raise ValueError("a host-only pool holds no rows")
+        check(capi.lib().ca_evict(self._h, sched._h, None if weights is None else weights.data_ptr(), room, budget, sink,
+                                  recent, None if new is None else _at(new), None if kept is None else kept.data_ptr(),
+                                  None if out is None else out.data_ptr(),
+                                  None if self.host_only else self._stream(stream)), "ca_evict")
+        return kept, out
+
     def _generation(self) -> int:
         st = self.__dict__.setdefault("_stats_buf", capi.Stats())
         check(capi.lib().ca_pool_stats(self._h, C.byref(st)), "ca_pool_stats")
@@ -324,15 +372,22 @@ class Pool:
         return list(buf)[:n.value]
 
     def schedule(self, seq_ids, no_tpp: bool = False, reuse: "Schedule | None" = None,
-                 stream=None, q_len: int = 1, causal: bool = False, chunk_lists: bool = False) -> "Schedule":
+                 stream=None, q_len: int = 1, causal: bool = False, chunk_lists: bool = False,
+                 q_lens=None) -> "Schedule":
         """Per-step tables for the batch ``seq_ids`` (rows of q / out in that
         order).  Passing the previous schedule reuses it when nothing changed.
         ``q_len`` > 1: that many query tokens per sequence (q / out become
         [b, q_len, H, D]); ``causal``: token j sees context tokens
         [0, len - q_len + j] only.  ``chunk_lists``: also upload each
-        sequence's chunk list, for ``select_chunks`` and
-        ``sparse_decode_attention``."""
+        sequence's chunk list, for ``select_chunks``,
+        ``sparse_decode_attention`` and ``evict``.  ``q_lens``: a block of
+        that many queries for each sequence (0 and more; an id may repeat),
+        for ``cross_attention`` alone."""
         s = reuse if reuse is not None else Schedule(self)
+        if q_lens is not None:
+            if no_tpp or chunk_lists or q_len != 1:
+                raise ValueError("q_lens goes with causal alone")
+            return self._schedule_blocks(s, seq_ids, q_lens, causal, stream)
         # A decode loop passes the same batch list every step: its int64 copy
         # (and that copy's address) is kept, so the per-step call converts
         # nothing; the library itself decides whether the tables are current.
@@ -354,7 +409,23 @@ class Pool:
         if ids is not s._ids:
             s._ids, s._ids_ptr = ids, ids.__array_interface__["data"][0]
             s._ids_list = list(seq_ids) if isinstance(seq_ids, list) else None
-        s._flags = flags
+        s._flags, s.q_lens = flags, None
+        return s
+
+    def _schedule_blocks(self, s: "Schedule", seq_ids, q_lens, causal: bool, stream) -> "Schedule":
+        ids = np.ascontiguousarray(np.asarray(seq_ids, dtype=np.int64))
+        lens = _ints("i", q_lens)
+        if len(lens) != len(ids):
+            raise ValueError("seq_ids and q_lens differ in length")
+        if len(lens) and min(lens) < 0:
+            raise ValueError("q_lens must not be negative")
+        h = s._h if s._h is not None else C.c_void_p()
+        flags = capi.CA_SCHED_CAUSAL if causal else 0
+        check(capi.lib().ca_build_schedule_blocks(self._h, _at(ids), len(ids), _at(lens), flags, C.byref(h),
+                                                  None if self.host_only else self._stream(stream)),
+              "ca_build_schedule_blocks")
+        s._h, s._ws_need, s.b, s.q_len, s.q_lens = h, None, len(ids), 1, lens.tolist()
+        s._ids, s._ids_ptr, s._ids_list, s._flags = ids, _at(ids), None, flags
         return s
 
 
@@ -366,14 +437,18 @@ class Schedule:
         self._h = None
         self.b = 0
         self.q_len = 1
+        self.q_lens = None              # query blocks: the blocks' lengths
         self._ws, self._ws_stream = None, None
         self._ws_need = None            # bytes of the device workspace, until the next build
+        # of its own, so that growing it never takes decode's from a captured graph
+        self._weights_ws, self._weights_ws_stream = None, None
         self._ids, self._ids_ptr, self._ids_list, self._flags = None, None, None, 0
 
     def _key(self) -> tuple:
         """What the library's tables depend on: the batch, the flags, q_len and
         the pool's generation (the library rebuilds them when one changes)."""
-        return (self._ids.tobytes(), self._flags, self.q_len, self.pool._generation())
+        return (self._ids.tobytes(), self._flags, self.q_len, None if self.q_lens is None else tuple(self.q_lens),
+                self.pool._generation())
 
     def __del__(self):
         if getattr(self, "_h", None) is not None and self._h.value:
@@ -444,6 +519,18 @@ class Schedule:
                 self._ws.record_stream(torch.cuda.current_stream(self.pool._device))
             self._ws_stream = raw
         return self._ws
+
+    def _weights_workspace(self, stream, raw):
+        n = C.c_size_t()
+        check(capi.lib().ca_workspace_bytes_weights(self._h, C.byref(n)), "ca_workspace_bytes_weights")
+        if self._weights_ws is None or self._weights_ws.numel() < n.value:
+            self._weights_ws = self.pool._empty((max(n.value, 256),), _torch().uint8, stream)
+            self._weights_ws_stream = raw
+        elif self._weights_ws_stream != raw:
+            with self.pool._under(stream):
+                self._weights_ws.record_stream(_torch().cuda.current_stream(self.pool._device))
+            self._weights_ws_stream = raw
+        return self._weights_ws
 
     def device_status(self, stream=None) -> int:
         return capi.lib().ca_sched_device_status(self._h, self.pool._stream(stream))
@@ -545,6 +632,68 @@ def sparse_decode_attention(pool: Pool, sched: Schedule, q, chunks, out=None, la
     check(capi.lib().ca_sparse_attention(pool._h, sched._h, int(layer), q.data_ptr(), chunks.data_ptr(),
                                          n, out.data_ptr(), float(scale), pool._stream(stream)),
           "ca_sparse_attention")
+    return out
+
+
+def cross_attention(pool: Pool, sched: Schedule, q, out=None, layer: int = 0, scale: float | None = None,
+                    workspace=None, stream=None):
+    """Blocks of queries of their own lengths, each over the whole context of
+    its sequence: out[r] = softmax(scale q[r] . K^T) V.  q: fp16
+    [sum(q_lens), H, D], block after block, of a schedule with ``q_lens``.
+    With ``causal``, row j of a block of m sees tokens [0, n - m + j] of a
+    context of n (none: zeros), the form for a prompt's tokens whose rows are in
+    the pool; without, every row sees all of it, as a decoder's targets see an
+    encoder's states."""
+    import torch
+    if pool.host_only:
+        raise ValueError("a host-only pool holds no rows")
+    if sched.q_lens is None:
+        raise ValueError("the schedule was built without q_lens")
+    shape = (sum(sched.q_lens), pool.n_heads, pool.head_dim)
+    pool._check_tensor(q, shape, torch.float16, "q")
+    if out is None:
+        out = torch.empty_like(q) if stream is None else pool._empty(shape, torch.float16, stream)
+    else:
+        pool._check_tensor(out, shape, torch.float16, "out")
+    if scale is None:
+        scale = 1.0 / math.sqrt(pool.head_dim)
+    raw = pool._stream(stream)
+    ws = workspace if workspace is not None else sched._workspace(False, stream, raw)
+    check(capi.lib().ca_cross_attention(pool._h, sched._h, int(layer), q.data_ptr(), out.data_ptr(), float(scale),
+                                        ws.data_ptr(), ws.numel(), raw), "ca_cross_attention")
+    return out
+
+
+def accumulate_attention(pool: Pool, sched: Schedule, q, weights, out=None, layer: int = 0,
+                         scale: float | None = None, workspace=None, stream=None):
+    """Adds a decode step's attention weights to running sums per token:
+    weights[i, h, t] += the sum over sequence i's query tokens and the heads
+    of group h of softmax_t(scale q . k_t), for the tokens t of its context.
+    q: as for ``decode_attention``, of any schedule of ``Pool.schedule``
+    without ``q_lens``; weights: fp32 [b, Hkv, room] (a layer's, contiguous),
+    room at least the longest context.  In place, or into ``out``.  Returns
+    the sums; ``Pool.evict`` keeps the tokens of largest ones."""
+    import torch
+    if pool.host_only:
+        raise ValueError("a host-only pool holds no rows")
+    want = ((sched.b, pool.n_heads, pool.head_dim) if sched.q_len == 1
+            else (sched.b, sched.q_len, pool.n_heads, pool.head_dim))
+    pool._check_tensor(q, want, torch.float16, "q")
+    room = weights.shape[-1] if weights.dim() == 3 else 0
+    if room < 1:
+        raise ValueError("weights must be an fp32 tensor [b, Hkv, room] with room >= 1")
+    pool._check_tensor(weights, (sched.b, pool.n_kv_heads, room), torch.float32, "weights")
+    if out is None:
+        out = weights
+    else:
+        pool._check_tensor(out, weights.shape, torch.float32, "out")
+    if scale is None:
+        scale = 1.0 / math.sqrt(pool.head_dim)
+    raw = pool._stream(stream)
+    ws = workspace if workspace is not None else sched._weights_workspace(stream, raw)
+    check(capi.lib().ca_accumulate_attention(pool._h, sched._h, int(layer), q.data_ptr(), weights.data_ptr(),
+                                             out.data_ptr(), room, float(scale), ws.data_ptr(), ws.numel(), raw),
+          "ca_accumulate_attention")
     return out
 
 

@@ -32,7 +32,7 @@ EXPORTS = [
     "ca_insert_batch", "ca_append_tokens", "ca_read_batch", "ca_remove_seq", "ca_remove_batch", "ca_pool_stats", "ca_seq_slots", "ca_seq_lengths", "ca_build_schedule", "ca_build_schedule_ex", "ca_sched_destroy",
     "ca_sched_counts", "ca_export_tables", "ca_export_plan", "ca_workspace_bytes", "ca_decode_attention",
     "ca_workspace_bytes_host", "ca_decode_attention_host", "ca_decode_attention_static_ws",
-    "ca_select_chunks", "ca_sparse_attention",
+    "ca_select_chunks", "ca_sparse_attention", "ca_build_schedule_blocks", "ca_cross_attention", "ca_workspace_bytes_weights", "ca_accumulate_attention", "ca_evict",
     "ca_sched_device_status", "ca_sched_inject_status", "ca_sched_inject_stall", "ca_pool_inject_alloc_failure",
     "ca_sched_set_profile_events", "ca_kernel_launches", "ca_error_string",
 ]
@@ -106,6 +106,11 @@ def lib() -> C.CDLL:
         "ca_decode_attention_static_ws": [vp, vp, i32, vp, vp, C.c_float, vp],
         "ca_select_chunks": [vp, vp, i32, vp, i32, i32, i32, vp, vp],
         "ca_sparse_attention": [vp, vp, i32, vp, vp, i32, vp, C.c_float, vp],
+        "ca_build_schedule_blocks": [vp, vp, i32, vp, u32, P(vp), vp],  # arrays by address
+        "ca_cross_attention": [vp, vp, i32, vp, vp, C.c_float, vp, sz, vp],
+        "ca_workspace_bytes_weights": [vp, P(sz)],
+        "ca_accumulate_attention": [vp, vp, i32, vp, vp, vp, i32, C.c_float, vp, sz, vp],
+        "ca_evict": [vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp],     # into_ids: int64 array address
         "ca_sched_device_status": [vp, vp],
         "ca_sched_inject_status": [vp, i32, vp],
         "ca_sched_inject_stall": [vp, i32],

@@ -78,6 +78,8 @@ struct PlanLayout {
     size_t chunks, units, seq_perm, pbase, status, counter, chunk_tok0, ctx_len, cta_head;
     size_t list_off, list_slots;   // CA_SCHED_CHUNK_LISTS: each batch row's chunk slots (CSR)
     size_t list_count, list_count_bytes;   // and a counter per unit of the listed chunks' attention
+    size_t tok_base;               // [b + 1] chunks of the positions before each one (CSR)
+    size_t q_off, items, joins;    // schedules of query blocks (BlockItem, BlockJoin)
     size_t total;
 };
 
@@ -125,6 +127,28 @@ struct AttnParams {
 struct WsLayout {
     size_t part_o, part_ms, total;                  // device-resident inputs
     size_t q_stage, out_stage, total_host;          // + staging for host I/O
+    size_t weights_ms, weights_scores, weights_total;   // accumulated weights: (m, s) partials, then the scores
+};
+
+// ---------------------------------------------------------------------------
+// Query blocks (cross attention).  A block's rows of one key/value head are
+// its (query token, query head of the group) pairs, token by token: row r is
+// token r / G, query head kvh * G + r % G.  An item is one tile of them over a
+// stretch of the sequence's chunks.  A tile whose chunks are split among items
+// leaves partial triples, joined by a BlockJoin.
+// ---------------------------------------------------------------------------
+struct BlockItem {
+    int32_t seq;               // batch row
+    int32_t head;              // key/value head
+    int32_t row0, rows;        // rows [row0, row0 + rows) of the block and head
+    int32_t c_begin, c_end;    // chunks of the sequence (equal: the rows see nothing)
+    int32_t part;              // partial tile, or -1: the item is the tile's only one
+    int32_t pad;
+};
+struct BlockJoin {
+    int32_t seq, head, row0, rows;
+    int32_t part, n_parts;     // partial tiles [part, part + n_parts)
+    int32_t pad0, pad1;
 };
 
 // ---------------------------------------------------------------------------
@@ -153,6 +177,9 @@ struct Node {
 struct Sequence {
     std::vector<Node*> path;
     int32_t length = 0;
+    // An eviction cut it: rows that join it follow tokens that are gone, so no
+    // chunk that it fills or grows may match a prompt.
+    bool cut = false;
 };
 
 struct Pool {
@@ -191,6 +218,7 @@ struct Tables {
     // token offset of each chunk in its sequences' contexts (cf rows, then sf
     // chunks) and each position's context length: the causal mask's inputs
     std::vector<int32_t> row_tok0, sf_tok0, ctx_len;
+    std::vector<int32_t> tok_base;   // [b + 1] chunks of the positions before each one
     // CA_SCHED_CHUNK_LISTS: the slots of seq_ids[i]'s chunks, root first, are
     // list_slots[list_off[i] .. list_off[i + 1])
     std::vector<int32_t> list_off, list_slots;
@@ -217,7 +245,13 @@ struct Sched {
     int64_t generation = -1;
     uint32_t flags = 0;
     int32_t q_len = 1;
+    bool blocks = false;               // of query blocks: q_lens, items and joins instead of q_len, t and plan
     std::vector<int64_t> seq_ids;
+    std::vector<int32_t> q_lens;
+    std::vector<BlockItem> items;
+    std::vector<BlockJoin> joins;
+    int64_t q_rows = 0;                // query tokens of all blocks
+    int32_t n_parts = 0, tile_rows = 0;
     Tables t;
     Tables t_next;                     // rebuilt into, then swapped with t
     Plan plan;
@@ -292,6 +326,19 @@ int pool_insert(Pool& p, int64_t seq_id, const int32_t* tokens, int32_t n,
                 std::vector<std::pair<int32_t, int32_t>>* new_chunks,  // (first token, slot)
                 int32_t* n_shared);
 int pool_remove(Pool& p, int64_t seq_id);
+// One sequence's eviction: what its path becomes.
+struct EvictSeq {
+    int64_t id = 0;                // the sequence, and the one that takes the kept rows (itself, in place)
+    int64_t into = 0;
+    int32_t n = 0, kept = 0;       // context tokens before and after
+    int32_t stay = 0;              // chunks of the old path that stay in the new one
+    bool changed = false;
+    Sequence next;
+};
+int pool_evict_prepare(Pool& p, const std::vector<int64_t>& seq_ids, int32_t budget, int32_t sink, const int64_t* into,
+                       std::vector<EvictSeq>& out);
+void pool_evict_undo(Pool& p, std::vector<EvictSeq>& seqs);
+void pool_evict_commit(Pool& p, std::vector<EvictSeq>& seqs);
 int32_t pool_match(const Pool& p, const int32_t* tokens, int32_t n);
 
 // schedule.cpp
@@ -299,7 +346,10 @@ int build_tables(const Pool& p, const int64_t* seq_ids, int32_t b, uint32_t flag
 void build_plan(const Pool& p, const Tables& t, int32_t grid, int32_t q_len, Plan& plan);
 void layout_plan(const Pool& p, const Plan& plan, int32_t b, PlanLayout& lay, std::vector<unsigned char>& blob,
                  const Tables& t);
-void layout_ws(const Plan& plan, const Pool& p, int32_t b, WsLayout& ws);
+void layout_ws(const Plan& plan, const Pool& p, int32_t b, const Tables& t, WsLayout& ws);
+
+// blocks.cpp: schedules of query blocks
+int build_blocks(const Pool& p, const int64_t* seq_ids, int32_t b, const int32_t* q_lens, uint32_t flags, Sched& s);
 
 // kernels.cu
 int kernel_smem_bytes(const PoolCfg& c, int* n_stages, size_t* bytes);
@@ -337,5 +387,19 @@ size_t list_parts_bytes(const Pool& p);
 int prepare_lists(Pool& p);
 int launch_sparse(const Pool& p, const Sched& s, int32_t layer, const void* q, const int32_t* lists, int32_t top_k,
                   void* out, float scale, void* stream);
+
+
+// weights.cu: a step's attention weights added to running sums
+int launch_weights(const Pool& p, const Sched& s, int32_t layer, const void* q, const float* in, float* out, int32_t room,
+                   float scale, void* ws, void* stream);
+
+// evict.cu: the tokens to keep, and their rows moved into the new chunks
+int launch_evict(const Pool& p, const Sched& s, const std::vector<EvictSeq>& seqs, const float* weights, int32_t room,
+                 int32_t budget, int32_t sink, int32_t recent, int32_t* kept, float* weights_out, void* stream);
+
+// cross.cu: attention of query blocks
+int cross_tile_rows(const PoolCfg& c);    // rows of a tile
+int cross_places(const Pool& p);           // items that run at a time
+int launch_cross(const Pool& p, const Sched& s, int32_t layer, const void* q, void* out, float scale, void* ws, void* stream);
 
 }  // namespace ca

@@ -117,6 +117,24 @@ int upload_plan(Sched& s, cudaStream_t stream) {
     return cuda_status(cudaEventRecord(done, stream));
 }
 
+// Device memory for the schedule's plan.
+bool room_for_plan(Sched& s) {
+    if (s.dev_bytes >= s.blob.size()) return true;
+    if (s.dev) cudaFree(s.dev);
+    s.dev = nullptr;
+    s.dev_bytes = 0;
+    if (cudaMalloc(&s.dev, s.blob.size()) != cudaSuccess) return false;
+    s.dev_bytes = s.blob.size();
+    return true;
+}
+
+// Whether the contexts of a schedule of query blocks are as long as when it was built.
+bool same_lengths(const Pool& p, const Sched& s) {
+    for (size_t i = 0; i < s.seq_ids.size(); ++i)
+        if (p.seqs.at(s.seq_ids[i]).length != s.t.ctx_len[i]) return false;
+    return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -386,7 +404,7 @@ int ca_build_schedule_ex(ca_pool* pool, const int64_t* seq_ids, int32_t b, int32
     if (q_len == 1) flags &= ~CA_SCHED_CAUSAL;       // one query token sees its whole context
     return guard([&] {
         ca_sched* s = *inout;
-        if (s && s->pool == pool && s->generation == pool->generation && s->flags == flags &&
+        if (s && s->pool == pool && !s->blocks && s->generation == pool->generation && s->flags == flags &&
             s->q_len == q_len && (int32_t)s->seq_ids.size() == b &&
             std::equal(seq_ids, seq_ids + b, s->seq_ids.begin()))
             return CA_OK;                   // context unchanged since the tree last changed
@@ -410,24 +428,15 @@ int ca_build_schedule_ex(ca_pool* pool, const int64_t* seq_ids, int32_t b, int32
         s->pool = pool;
         s->flags = flags;
         s->q_len = q_len;
+        s->blocks = false;
         s->seq_ids.assign(seq_ids, seq_ids + b);
         alloc_point(*pool);                 // the plan's vectors may grow below
         build_plan(*pool, s->t, pool->kv ? pool->num_sms : kHostOnlyGrid, q_len, s->plan);
         layout_plan(*pool, s->plan, b, s->layout, s->blob, s->t);
-        layout_ws(s->plan, *pool, b, s->ws);
+        layout_ws(s->plan, *pool, b, s->t, s->ws);
         if (pool->kv) {
             const DeviceGuard dev(pool->device);
-            if (!dev.ok) return CA_ERR_CUDA;
-            if (s->dev_bytes < s->blob.size()) {
-                if (s->dev) cudaFree(s->dev);
-                s->dev = nullptr;
-                s->dev_bytes = 0;
-                if (cudaMalloc(&s->dev, s->blob.size()) != cudaSuccess) {
-                    s->generation = -1;
-                    return CA_ERR_CUDA;
-                }
-                s->dev_bytes = s->blob.size();
-            }
+            if (!dev.ok || !room_for_plan(*s)) return CA_ERR_CUDA;
             const size_t parts = (flags & CA_SCHED_CHUNK_LISTS) ? list_parts_bytes(*pool) : 0;
             if (s->list_parts_size < parts) {
                 if (s->list_parts) cudaFree(s->list_parts);
@@ -441,10 +450,50 @@ int ca_build_schedule_ex(ca_pool* pool, const int64_t* seq_ids, int32_t b, int32
                 if (st) return st;
             }
             st = upload_plan(*s, static_cast<cudaStream_t>(stream));
-            if (st) {
-                s->generation = -1;
-                return st;
-            }
+            if (st) return st;
+        }
+        s->generation = pool->generation;
+        if (fresh) *inout = fresh.release();
+        return CA_OK;
+    });
+}
+
+int ca_build_schedule_blocks(ca_pool* pool, const int64_t* seq_ids, int32_t b, const int32_t* q_lens, uint32_t flags,
+                             ca_sched** inout, void* stream) {
+    const Range range("ca_build_schedule");
+    if (!pool || !inout || !seq_ids || !q_lens || b < 1) return CA_ERR_INVALID;
+    if (flags & ~CA_SCHED_CAUSAL) return CA_ERR_INVALID;
+    return guard([&] {
+        ca_sched* s = *inout;
+        if (s && s->pool == pool && s->blocks && s->generation == pool->generation && s->flags == flags &&
+            (int32_t)s->seq_ids.size() == b && std::equal(seq_ids, seq_ids + b, s->seq_ids.begin()) &&
+            std::equal(q_lens, q_lens + b, s->q_lens.begin()) &&
+            // (the mask counts from the contexts' ends, which appends in place move)
+            (!(flags & CA_SCHED_CAUSAL) || same_lengths(*pool, *s)))
+            return CA_OK;
+        std::unique_ptr<ca_sched, SchedFree> fresh;
+        if (!s) {
+            fresh.reset(new ca_sched());
+            s = fresh.get();
+        }
+        const int64_t was = s->generation;
+        s->generation = -1;                 // (as above)
+        alloc_point(*pool);
+        int st = build_blocks(*pool, seq_ids, b, q_lens, flags, *s);
+        if (st) {
+            s->generation = was;            // its previous tables are untouched
+            return st;
+        }
+        s->pool = pool;
+        s->flags = flags;
+        s->q_len = 1;
+        s->blocks = true;
+        s->seq_ids.assign(seq_ids, seq_ids + b);
+        if (pool->kv) {
+            const DeviceGuard dev(pool->device);
+            if (!dev.ok || !room_for_plan(*s)) return CA_ERR_CUDA;
+            st = upload_plan(*s, static_cast<cudaStream_t>(stream));
+            if (st) return st;
         }
         s->generation = pool->generation;
         if (fresh) *inout = fresh.release();
@@ -468,7 +517,7 @@ int ca_sched_destroy(ca_sched* sched) {
 }
 
 int ca_sched_counts(const ca_sched* s, int32_t counts[6]) {
-    if (!s || !counts) return CA_ERR_INVALID;
+    if (!s || !counts || s->blocks) return CA_ERR_INVALID;
     counts[0] = s->t.b;
     counts[1] = (int32_t)(s->t.cf_rows.size() / 4);
     counts[2] = (int32_t)(s->t.cf_runs.size() / 4);
@@ -481,7 +530,7 @@ int ca_sched_counts(const ca_sched* s, int32_t counts[6]) {
 int ca_export_tables(const ca_sched* s, int32_t* seq_perm, int32_t* cf_rows, int32_t* cf_runs,
                      int32_t* sf_offsets, int32_t* sf_chunks, int32_t* merge_offsets,
                      int32_t* merge_runs) {
-    if (!s) return CA_ERR_INVALID;
+    if (!s || s->blocks) return CA_ERR_INVALID;
     auto put = [](int32_t* dst, const std::vector<int32_t>& v) {
         if (dst && !v.empty()) std::memcpy(dst, v.data(), v.size() * sizeof(int32_t));
     };
@@ -497,7 +546,7 @@ int ca_export_tables(const ca_sched* s, int32_t* seq_perm, int32_t* cf_rows, int
 
 int ca_export_plan(const ca_sched* s, int32_t counts[4], int32_t* units, int32_t* cta_begin,
                    int32_t* pbase, int32_t* chunks) {
-    if (!s || !counts) return CA_ERR_INVALID;
+    if (!s || !counts || s->blocks) return CA_ERR_INVALID;
     counts[0] = (int32_t)s->plan.units.size();
     counts[1] = s->plan.grid;
     counts[2] = (int32_t)s->plan.pbase.size();
@@ -526,11 +575,11 @@ int ca_workspace_bytes_host(const ca_sched* s, size_t* bytes_out) {
 }
 
 static int decode_checks(const ca_pool* pool, const ca_sched* s, int32_t layer, void* ws_dev,
-                         size_t ws_bytes, size_t need) {
-    if (!pool || !s || !pool->kv || s->pool != pool || !s->dev) return CA_ERR_INVALID;
+                         size_t ws_bytes, size_t need, bool blocks = false) {
+    if (!pool || !s || !pool->kv || s->pool != pool || !s->dev || s->blocks != blocks) return CA_ERR_INVALID;
     if (s->generation != pool->generation) return CA_ERR_STALE;
     if (layer < 0 || layer >= pool->cfg.n_layers) return CA_ERR_INVALID;
-    if (!ws_dev || !aligned(ws_dev, 256) || ws_bytes < need) return CA_ERR_INVALID;
+    if (need && (!ws_dev || !aligned(ws_dev, 256) || ws_bytes < need)) return CA_ERR_INVALID;
     return CA_OK;
 }
 
@@ -657,6 +706,102 @@ int ca_sparse_attention(const ca_pool* pool, const ca_sched* s, int32_t layer, c
     const DeviceGuard dev(pool->device);
     if (!dev.ok) return CA_ERR_CUDA;
     return launch_sparse(*pool, *s, layer, q_dev, lists_dev, top_k, out_dev, scale, stream);
+}
+
+int ca_workspace_bytes_weights(const ca_sched* s, size_t* bytes_out) {
+    if (!s || !bytes_out) return CA_ERR_INVALID;
+    *bytes_out = s->ws.weights_total;
+    return CA_OK;
+}
+
+int ca_accumulate_attention(const ca_pool* pool, const ca_sched* s, int32_t layer, const void* q_dev,
+                            const float* weights_dev, float* out_dev, int32_t room, float scale, void* ws_dev,
+                            size_t ws_bytes, void* stream) {
+    const Range range("ca_accumulate_attention");
+    int st = decode_checks(pool, s, layer, ws_dev, ws_bytes, s ? s->ws.weights_total : 0);
+    if (st) return st;
+    if (!q_dev || !aligned(q_dev, 16) || !weights_dev || !out_dev || !aligned(weights_dev, 4) || !aligned(out_dev, 4) ||
+        room < 1)
+        return CA_ERR_INVALID;
+    if (s->t.tok_base[s->t.b] < 0) return CA_ERR_UNSUPPORTED;      // more than 2^31 chunks, sharers counted
+    // in place or apart
+    const size_t bytes = (size_t)s->t.b * kv_heads(pool->cfg) * room * sizeof(float);
+    const char* in = reinterpret_cast<const char*>(weights_dev);
+    const char* out = reinterpret_cast<const char*>(out_dev);
+    if (in != out && in < out + bytes && out < in + bytes) return CA_ERR_INVALID;
+    return guard([&] {
+        for (int64_t id : s->seq_ids)
+            if (pool->seqs.at(id).length > room) return CA_ERR_INVALID;
+        const DeviceGuard dev(pool->device);
+        if (!dev.ok) return CA_ERR_CUDA;
+        return launch_weights(*pool, *s, layer, q_dev, weights_dev, out_dev, room, scale, ws_dev, stream);
+    });
+}
+
+int ca_evict(ca_pool* pool, const ca_sched* s, const float* weights_dev, int32_t room, int32_t budget, int32_t sink,
+             int32_t recent, const int64_t* into_ids, int32_t* kept_dev, float* out_dev, void* stream) {
+    const Range range("ca_evict");
+    if (!pool || !s || s->pool != pool) return CA_ERR_INVALID;
+    if (s->generation != pool->generation) return CA_ERR_STALE;
+    if (!(s->flags & CA_SCHED_CHUNK_LISTS)) return CA_ERR_INVALID;
+    if (budget < 1 || sink < 0 || recent < 0 || (int64_t)sink + recent > budget) return CA_ERR_INVALID;
+    if (pool->kv) {
+        if (!s->dev || room < 1 || !weights_dev || !kept_dev || !out_dev || !aligned(weights_dev, 4) ||
+            !aligned(kept_dev, 4) || !aligned(out_dev, 4))
+            return CA_ERR_INVALID;
+        const size_t bytes =
+            (size_t)pool->cfg.n_layers * s->t.b * kv_heads(pool->cfg) * room * sizeof(float);
+        const char* in = reinterpret_cast<const char*>(weights_dev);
+        const char* out = reinterpret_cast<const char*>(out_dev);
+        if (in != out && in < out + bytes && out < in + bytes) return CA_ERR_INVALID;
+    } else if (weights_dev || kept_dev || out_dev) {
+        return CA_ERR_INVALID;
+    }
+    return guard([&] {
+        if (pool->kv)
+            for (int64_t id : s->seq_ids)
+                if (pool->seqs.at(id).length > room) return CA_ERR_INVALID;
+        std::vector<EvictSeq> seqs;
+        if (pool->kv) {
+            // a replay would move rows of slots that have found other uses
+            cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+            const DeviceGuard dev(pool->device);
+            if (!dev.ok || cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &cap) != cudaSuccess) return CA_ERR_CUDA;
+            if (cap != cudaStreamCaptureStatusNone) return CA_ERR_INVALID;
+        }
+        int st = pool_evict_prepare(*pool, s->seq_ids, budget, sink, into_ids, seqs);
+        if (st) return st;
+        if (pool->kv) {
+            try {
+                const DeviceGuard dev(pool->device);
+                st = dev.ok ? launch_evict(*pool, *s, seqs, weights_dev, room, budget, sink, recent, kept_dev, out_dev, stream)
+                            : CA_ERR_CUDA;
+            } catch (...) {
+                pool_evict_undo(*pool, seqs);
+                throw;
+            }
+            if (st) {
+                pool_evict_undo(*pool, seqs);
+                return st;
+            }
+        }
+        pool_evict_commit(*pool, seqs);
+        return CA_OK;
+    });
+}
+
+int ca_cross_attention(const ca_pool* pool, const ca_sched* s, int32_t layer, const void* q_dev, void* out_dev,
+                       float scale, void* ws_dev, size_t ws_bytes, void* stream) {
+    const Range range("ca_cross_attention");
+    const int st = decode_checks(pool, s, layer, ws_dev, ws_bytes, s ? s->ws.total : 0, true);
+    if (st) return st;
+    if (s->q_rows == 0) return CA_OK;
+    if (!q_dev || !out_dev || !aligned(q_dev, 16) || !aligned(out_dev, 16)) return CA_ERR_INVALID;
+    return guard([&] {
+        const DeviceGuard dev(pool->device);
+        if (!dev.ok) return CA_ERR_CUDA;
+        return launch_cross(*pool, *s, layer, q_dev, out_dev, scale, ws_dev, stream);
+    });
 }
 
 int ca_sched_device_status(const ca_sched* s, void* stream) {

@@ -242,7 +242,7 @@ int pool_append(Pool& p, int64_t seq_id, const int32_t* tokens, int32_t n,
     if (it == p.seqs.end()) return CA_ERR_NOT_FOUND;
     Sequence& seq = it->second;
     const int32_t c = p.cfg.chunk;
-    const bool share = !(p.cfg.flags & CA_NO_SHARING);
+    const bool share = !(p.cfg.flags & CA_NO_SHARING) && !seq.cut;
     Node* last = seq.path.back();
     const int32_t fill = std::min(c - last->ntok, n);
     const int32_t n_new = (n - fill + c - 1) / c;
@@ -336,13 +336,10 @@ void pool_undo_append(Pool& p, int64_t seq_id, const AppendUndo& u) {
     p.generation = u.generation;
 }
 
-int pool_remove(Pool& p, int64_t seq_id) {
-    auto it = p.seqs.find(seq_id);
-    if (it == p.seqs.end()) return CA_ERR_NOT_FOUND;
-    std::vector<Node*> path = std::move(it->second.path);
-    p.seqs.erase(it);
-    // Refcounts never grow along a path, so the chunks that drop to zero form
-    // a suffix of it; detach its first node and free the whole suffix.
+// Drop one reference of a path's chunks.  Refcounts never grow along a path, so
+// the chunks that drop to zero form a suffix of it; detach its first node and
+// free the whole suffix.
+static void release_path(Pool& p, const std::vector<Node*>& path) {
     size_t first_free = path.size();
     for (size_t i = 0; i < path.size(); ++i) {
         path[i]->refcount -= 1;
@@ -360,8 +357,115 @@ int pool_remove(Pool& p, int64_t seq_id) {
             x->matchable = false;
         }
     }
+}
+
+int pool_remove(Pool& p, int64_t seq_id) {
+    auto it = p.seqs.find(seq_id);
+    if (it == p.seqs.end()) return CA_ERR_NOT_FOUND;
+    const std::vector<Node*> path = std::move(it->second.path);
+    p.seqs.erase(it);
+    release_path(p, path);
     p.generation += 1;
     return CA_OK;
+}
+
+// The paths that an eviction gives: the chunks wholly inside the sink stay
+// where they are (all whole chunks, of a sequence within its budget), new private
+// chunks take the rest of the kept rows.  With `into` the old sequences stay too
+// and share those chunks (a CA_NO_SHARING pool copies them).  All or nothing: new
+// slots are taken and new sequences entered here, references are given up only
+// by the commit.
+int pool_evict_prepare(Pool& p, const std::vector<int64_t>& seq_ids, int32_t budget, int32_t sink, const int64_t* into,
+                       std::vector<EvictSeq>& out) {
+    const int32_t c = p.cfg.chunk;
+    const bool apart = into && (p.cfg.flags & CA_NO_SHARING);
+    out.clear();
+    alloc_point(p);
+    out.resize(seq_ids.size());
+    size_t fresh = 0;
+    for (size_t i = 0; i < out.size(); ++i) {
+        auto it = p.seqs.find(seq_ids[i]);
+        if (it == p.seqs.end()) return CA_ERR_NOT_FOUND;
+        EvictSeq& e = out[i];
+        e.id = seq_ids[i];
+        e.into = into ? into[i] : e.id;
+        if (into) {
+            if (p.seqs.count(e.into)) return CA_ERR_EXISTS;
+            for (size_t j = 0; j < i; ++j)
+                if (out[j].into == e.into) return CA_ERR_INVALID;
+        }
+        e.n = it->second.length;
+        e.kept = std::min(e.n, budget);
+        const bool cut = e.n > budget;
+        e.stay = apart ? 0 : cut ? sink / c : e.n / c;
+        if (!into && !cut) continue;                // as it was
+        e.next.length = e.kept;
+        e.next.cut = cut || it->second.cut;
+        fresh += (size_t)((e.kept + c - 1) / c - e.stay);
+    }
+    if (fresh > p.heap.size()) return CA_ERR_OOM;
+    try {
+        for (EvictSeq& e : out) {
+            if (!into && e.n <= budget) continue;
+            if (into) {
+                alloc_point(p);
+                p.seqs.try_emplace(e.into);
+            }
+            e.changed = true;                       // (from here on the undo takes it back)
+            const std::vector<Node*>& old = p.seqs.at(e.id).path;
+            const int32_t pieces = (e.kept + c - 1) / c;
+            alloc_point(p);
+            e.next.path.reserve((size_t)pieces);    // nothing below pushes past it
+            for (int32_t k = 0; k < e.stay; ++k) {
+                old[k]->refcount += 1;
+                e.next.path.push_back(old[k]);
+            }
+            for (int32_t k = e.stay; k < pieces; ++k) {
+                const int32_t slot = heap_pop(p.heap);
+                Node* node = e.next.path.empty() ? &p.root : e.next.path.back();
+                Node* ch = &p.nodes[slot];
+                ch->slot = slot;
+                ch->ntok = std::min(c, e.kept - k * c);
+                // (a copy of a whole sequence keeps its tokens: its last chunk may fill up and match later)
+                if (e.n <= budget) std::copy_n(chunk_tokens(p, old[k]), ch->ntok, p.tokens.begin() + (size_t)slot * c);
+                ch->matchable = false;
+                ch->hash = 0;
+                ch->parent = node;
+                ch->children.clear();
+                ch->index.reset();
+                ch->refcount = 1;
+                e.next.path.push_back(ch);          // reserved: cannot throw
+                alloc_point(p);
+                add_child(node, ch);
+            }
+        }
+    } catch (...) {
+        pool_evict_undo(p, out);
+        throw;
+    }
+    return CA_OK;
+}
+
+void pool_evict_undo(Pool& p, std::vector<EvictSeq>& seqs) {
+    for (size_t i = seqs.size(); i-- > 0;) {
+        EvictSeq& e = seqs[i];
+        if (!e.changed) continue;
+        release_path(p, e.next.path);
+        if (e.into != e.id) p.seqs.erase(e.into);
+        e.changed = false;
+    }
+}
+
+void pool_evict_commit(Pool& p, std::vector<EvictSeq>& seqs) {
+    bool any = false;
+    for (EvictSeq& e : seqs) {
+        if (!e.changed) continue;
+        any = true;
+        Sequence& seq = p.seqs.at(e.into);
+        std::swap(seq, e.next);
+        if (e.into == e.id) release_path(p, e.next.path);   // the old path (staying chunks are held by the new one)
+    }
+    if (any) p.generation += 1;
 }
 
 }  // namespace ca

@@ -79,7 +79,7 @@ int build_tables(const Pool& p, const int64_t* seq_ids, int32_t b, uint32_t flag
 
     t.b = b;
     for (auto* v : {&t.seq_perm, &t.cf_rows, &t.cf_runs, &t.sf_offsets, &t.sf_chunks, &t.merge_offsets,
-                    &t.merge_runs, &t.row_tok0, &t.sf_tok0, &t.ctx_len, &t.list_off, &t.list_slots})
+                    &t.merge_runs, &t.row_tok0, &t.sf_tok0, &t.ctx_len, &t.tok_base, &t.list_off, &t.list_slots})
         v->clear();
     t.list_max = 0;
     if (flags & CA_SCHED_CHUNK_LISTS) {
@@ -158,6 +158,7 @@ int build_tables(const Pool& p, const int64_t* seq_ids, int32_t b, uint32_t flag
     t.sf_chunks.resize(2 * (size_t)t.sf_offsets[b]);
     t.sf_tok0.resize((size_t)t.sf_offsets[b]);
     t.ctx_len.resize(b);
+    t.tok_base.assign((size_t)b + 1, 0);
     for (int32_t pos = 0; pos < b; ++pos) {
         const int32_t i = order[pos];
         const auto& path = seq_of[i]->path;
@@ -169,6 +170,10 @@ int build_tables(const Pool& p, const int64_t* seq_ids, int32_t b, uint32_t flag
             *tok0++ = (int32_t)k * c;        // every chunk before the last is full
         }
         t.ctx_len[pos] = seq_of[i]->length;
+        // (a position's chunks count once for each of its sharers here: too many for
+        // 32 bits are told by a negative sum, which the weights' call refuses)
+        const int64_t chunks = (int64_t)t.tok_base[pos] + (int64_t)path.size();
+        t.tok_base[pos + 1] = t.tok_base[pos] < 0 || chunks > INT32_MAX ? -1 : (int32_t)chunks;
     }
 
     // Merge lists: runs are nested intervals listed in pre-order, so a
@@ -574,6 +579,7 @@ void layout_plan(const Pool& p, const Plan& plan, int32_t b, PlanLayout& lay, st
     lay.counter = off;   off = align256(off + sizeof(int32_t));
     lay.chunk_tok0 = off; off = align256(off + plan.chunk_tok0.size() * sizeof(int32_t));
     lay.ctx_len = off;   off = align256(off + (size_t)b * sizeof(int32_t));
+    lay.tok_base = off;  off = align256(off + t.tok_base.size() * sizeof(int32_t));
     lay.cta_head = off;  off = align256(off + (size_t)plan.grid * sizeof(CtaHead));
     lay.list_off = off;   off = align256(off + t.list_off.size() * sizeof(int32_t));
     lay.list_slots = off; off = align256(off + t.list_slots.size() * sizeof(int32_t));
@@ -594,6 +600,7 @@ void layout_plan(const Pool& p, const Plan& plan, int32_t b, PlanLayout& lay, st
     std::memcpy(blob.data() + lay.pbase, plan.pbase.data(), plan.pbase.size() * sizeof(int32_t));
     std::memcpy(blob.data() + lay.chunk_tok0, plan.chunk_tok0.data(), plan.chunk_tok0.size() * sizeof(int32_t));
     std::memcpy(blob.data() + lay.ctx_len, t.ctx_len.data(), (size_t)b * sizeof(int32_t));
+    std::memcpy(blob.data() + lay.tok_base, t.tok_base.data(), t.tok_base.size() * sizeof(int32_t));
     // Each CTA's first work, with the chunk refs of its first unit's steps
     // (a unit walks the linear (head, chunk) range [L0, L1); step L reads
     // chunk base + L % n, as the kernel's producer does).
@@ -616,7 +623,7 @@ void layout_plan(const Pool& p, const Plan& plan, int32_t b, PlanLayout& lay, st
     }
 }
 
-void layout_ws(const Plan& plan, const Pool& p, int32_t b, WsLayout& ws) {
+void layout_ws(const Plan& plan, const Pool& p, int32_t b, const Tables& t, WsLayout& ws) {
     const size_t H = p.cfg.n_heads, D = p.cfg.head_dim;   // q and out use the query heads
     size_t off = 0;
     ws.part_o = off;   off = align256(off + (size_t)plan.n_partials * D * sizeof(float));
@@ -625,6 +632,11 @@ void layout_ws(const Plan& plan, const Pool& p, int32_t b, WsLayout& ws) {
     ws.q_stage = off;  off = align256(off + (size_t)b * plan.q_len * H * D * 2);
     ws.out_stage = off; off = align256(off + (size_t)b * plan.q_len * H * D * 2);
     ws.total_host = off;
+    off = 0;
+    ws.weights_ms = off;     off = align256(off + (size_t)plan.n_partials * 2 * sizeof(float));
+    ws.weights_scores = off;
+    if (t.tok_base[b] >= 0) off = align256(off + (size_t)t.tok_base[b] * p.cfg.chunk * plan.q_len * H * sizeof(float));
+    ws.weights_total = off;
 }
 
 }  // namespace ca

@@ -77,11 +77,6 @@ constexpr uint32_t kSure = 0xffffffffu;   // key of a chunk that is taken
 constexpr uint32_t kTie = 0xfffffffeu;    // key of one that ties for the last places
 constexpr int kFewTies = 256;             // chunks ranked pairwise in 64 bits
 
-__device__ __forceinline__ uint32_t order_key(float x) {   // monotone; 0 for a NaN, never as much as kTie
-    if (x != x) return 0u;
-    const uint32_t u = __float_as_uint(x + 0.f);           // -0 counts as 0
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
 __device__ __forceinline__ unsigned long long order_key(double x) {
     if (x != x) return 0ull;
     const unsigned long long u = (unsigned long long)__double_as_longlong(x + 0.0);

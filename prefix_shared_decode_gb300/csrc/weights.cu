@@ -1,0 +1,430 @@
+// A decode step's attention weights, added to running sums per token:
+//     out[i][h][t] = in[i][h][t] + sum over the rows r of sequence i and
+//     key/value head h of  exp(x_rt) / sum_t' exp(x_rt'),  x_rt = scale q_r . k_t.
+// Keys alone are read, once for all sharers of a chunk: the first kernel walks
+// the two-phase plan of the schedule (units of shared chunks against the
+// queries of all their sharers, then each sequence's own chunks) and leaves the
+// scores, fp32 in log2 units, and each unit's (maximum, sum) of each row; the
+// second joins those per row and adds the weights up.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+
+#include "ca_internal.h"
+#include "fp4.cuh"
+#include "row_blocks.cuh"
+
+namespace ca {
+namespace dev {
+
+constexpr int kWtWarps = 4, kWtThreads = 32 * (kWtWarps + 1);
+constexpr int kWtTokens = 64;             // tokens of a stage: 16 a warp
+constexpr int kWtStages = 4;
+constexpr int kAddThreads = 256, kAddTokens = 4 * kAddThreads;
+
+struct WeightParams {
+    AttnParams a;                 // the schedule's plan, the pool, q (part_ms: the units' (m, s))
+    const int32_t* tok_base;      // [b + 1] chunks of the positions before each one
+    float* scores;                // position by position: [Hkv][rows][its chunks' tokens]
+    const float* in;
+    float* out;
+    int32_t room;                 // tokens per row of in and out
+    int32_t chunk;
+    int32_t blocks;               // second kernel: blocks of tokens per row
+};
+
+template <int C, int D, int EB>
+struct WtSmem {
+    static constexpr int kPer = kWtTokens / C;            // chunk tiles of a stage
+    static constexpr int kTile = EB == 0 ? F4Tile<C, D>::kBytes : C * D * EB;
+    static constexpr int kStage = kPer * kTile;
+    static constexpr int kQ = q_rows<D>() * D * 2;
+    static constexpr int kRows = kWtStages * kStage + kQ;           // score rows' addresses
+    static constexpr int kMs = kRows + kQRows * 8;                   // (m, s) of each warp's rows
+    static constexpr int kInfo = kMs + kWtWarps * kQRows * 8;        // ntok and first token of each chunk tile
+    static constexpr int kBars = kInfo + kWtStages * kPer * 8;
+    static constexpr int kBytes = kBars + 2 * kWtStages * 8;
+};
+
+__device__ __forceinline__ void wt_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWtWarps * 32) : "memory"); }
+
+// One unit per CTA.  Rows of the query tile are (position, query token, query
+// head) as in the two-phase kernel; a warp takes 16 tokens of a stage against
+// every 16 of them.  A thread keeps the running maximum and sum of its own
+// columns of each of its rows; they meet at the end of a head.
+template <int C, int D, int EB>
+__global__ void __launch_bounds__(kWtThreads) weight_scores_kernel(const __grid_constant__ CUtensorMap tmap,
+                                                                   const WeightParams wp) {
+    using SM = WtSmem<C, D, EB>;
+    constexpr int kPer = SM::kPer;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const AttnParams& p = wp.a;
+    uint8_t* qt = smem + kWtStages * SM::kStage;
+    float** row_at = reinterpret_cast<float**>(smem + SM::kRows);
+    float2* ms = reinterpret_cast<float2*>(smem + SM::kMs);
+    volatile int2* info = reinterpret_cast<volatile int2*>(smem + SM::kInfo);
+    const uint32_t full0 = smem_u32(smem + SM::kBars), empty0 = full0 + 8 * kWtStages;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kWtStages; ++i) {
+            mbar_init(full0 + 8 * i, 1);
+            mbar_init(empty0 + 8 * i, kWtWarps);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    __syncthreads();
+    // the plan may be read before the dependency wait; q and the pool after it
+    const Unit U = p.units[blockIdx.x];
+    const bool sf = U.kind == UNIT_SF;
+    const int n = sf ? U.n_per_head : U.c_end - U.c_begin, base = sf ? U.base : U.c_begin;
+    const int L0 = sf ? U.c_begin : U.head * n, L1 = sf ? U.c_end : (U.head + U.n_per_head) * n;
+    const int HK = p.n_kv_heads, G = p.group, QL = p.q_len, RW = QL * G, H = p.n_heads;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    if (warp == kWtWarps) {
+        // ------------------------------ producer ------------------------------
+        if (lane != 0) return;
+        if (p.test_stall) {               // test hook: a wait that nothing ends
+            if (!mbar_wait(full0, 0u)) set_status(p.status, CA_ERR_TIMEOUT);
+            return;
+        }
+        const uint64_t pol = policy_evict_first();
+        int it = 0;
+        bool ok = true;
+        for (int L = L0; L < L1 && ok;) {
+            const int head = L / n, seg_end = min(L1, (head + 1) * n);
+            for (; L < seg_end && ok; ++it) {
+                const int st = it % kWtStages, cnt = min(kPer, seg_end - L);
+                const uint32_t fb = full0 + 8 * st;
+                if (!mbar_wait(empty0 + 8 * st, ((uint32_t)(it / kWtStages) & 1u) ^ 1u)) {
+                    set_status(p.status, CA_ERR_TIMEOUT);
+                    ok = false;
+                    break;
+                }
+                uint32_t bytes = 0;
+                int slots[kPer];
+#pragma unroll
+                for (int x = 0; x < kPer; ++x) {
+                    slots[x] = -1;
+                    if (x >= cnt) continue;
+                    const int at = base + (L + x) % n;
+                    const ChunkRef ch = p.chunks[at];
+                    if (ch.slot < 0 || ch.slot >= p.capacity || head >= HK) {
+                        set_status(p.status, CA_ERR_DEVICE_BOUNDS);
+                    } else {
+                        slots[x] = ch.slot;
+                        bytes += EB == 0 ? C * D / 2 + C * D / 16 : C * D * EB;
+                    }
+                    const int ntok = slots[x] >= 0 ? min(max(p.slot_ntok[slots[x]], 0), C) : 0;
+                    info[st * kPer + x].x = ntok;
+                    info[st * kPer + x].y = p.chunk_tok0[at];
+                }
+                if (bytes) mbar_expect_tx_only(fb, bytes);
+#pragma unroll
+                for (int x = 0; x < kPer; ++x) {
+                    if (slots[x] < 0) continue;
+                    const uint32_t dst = smem_u32(smem + st * SM::kStage + x * SM::kTile);
+                    if constexpr (EB == 0) {
+                        using T = F4Tile<C, D>;
+                        const uint8_t* src =
+                            p.kv + (((long long)slots[x] * p.n_layers + p.layer) * HK + head) * T::kBytes;
+                        bulk_load(dst, src, T::kCodes, fb, pol);
+                        bulk_load(dst + T::kKScales, src + T::kKScales, T::kScales, fb, pol);
+                    } else {
+                        const int row = ((slots[x] * p.n_layers + p.layer) * 2 * HK + head) * C;
+#pragma unroll
+                        for (int bx = 0; bx < D * EB / 128; ++bx)
+                            tma_load_2d(dst + bx * C * 128, &tmap, bx * (128 / (EB == 0 ? 1 : EB)), row, fb, pol);
+                    }
+                }
+                mbar_arrive(fb);
+                L += cnt;
+            }
+        }
+        if (!ok)                          // let the copies in flight land before the CTA can end
+            for (int k = max(0, it - kWtStages); k < it; ++k)
+                mbar_wait(full0 + 8 * (k % kWtStages), (uint32_t)(k / kWtStages) & 1u);
+        return;
+    }
+
+    // ------------------------------ consumers --------------------------------
+    constexpr int RS = EB == 0 ? 4 : 2;               // rows of a 16-row block that a thread holds columns of
+    constexpr int RB = q_rows<D>() / 16;
+    const int g = lane >> 2, t = lane & 3;
+    const int m_rows = (U.q_hi - U.q_lo) * RW;
+    const int sub = warp * 16 / C, tok0 = warp * 16 % C;
+    auto row_of = [&](int rb, int k) { return rb * 16 + (EB == 0 ? (k >> 1) * 8 + 2 * t + (k & 1) : g + 8 * k); };
+    int lim[RB][RS];                                  // causal mask: the last token that a row sees
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+        for (int k = 0; k < RS; ++k) {
+            const int row = row_of(rb, k);
+            lim[rb][k] = p.causal && row < m_rows ? p.ctx_len[U.q_lo + row / RW] - QL + (row % RW) / G : INT_MAX;
+        }
+    int it = 0;
+    bool ok = true;                                   // (a warp whose wait ran out still meets the others at their barriers)
+    for (int L = L0; L < L1;) {
+        const int head = L / n, seg_end = min(L1, (head + 1) * n);
+        const int part = L == L0 || !sf ? U.part : U.part_next;
+        for (int i = threadIdx.x; i < m_rows * (D / 8); i += kWtWarps * 32) {
+            const int r = i / (D / 8), k = i % (D / 8);
+            const size_t tok = (size_t)p.seq_perm[U.q_lo + r / RW] * QL + (r % RW) / G;
+            cp_async16(smem_u32(qt + swz(r, k, q_rows<D>())), p.q + (tok * H + head * G + r % G) * D + k * 8);
+        }
+        for (int r = threadIdx.x; r < m_rows; r += kWtWarps * 32) {
+            const int pos = U.q_lo + r / RW;
+            const long long c0 = wp.tok_base[pos], tokens = (wp.tok_base[pos + 1] - c0) * C;
+            row_at[r] = wp.scores + c0 * C * ((long long)QL * H) + (long long)(head * RW + r % RW) * tokens;
+        }
+        cp_async_wait_all();
+        wt_sync();
+        float m[RB][RS], s[RB][RS];
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+            for (int k = 0; k < RS; ++k) {
+                m[rb][k] = -INFINITY;
+                s[rb][k] = 0.f;
+            }
+        for (; L < seg_end; ++it) {
+            const int st = it % kWtStages, cnt = min(kPer, seg_end - L);
+            if (ok && !mbar_wait(full0 + 8 * st, (uint32_t)(it / kWtStages) & 1u)) {
+                set_status(p.status, CA_ERR_TIMEOUT);
+                ok = false;
+            }
+            ok = __all_sync(kFull, ok);
+            L += cnt;
+            if (!ok) continue;
+            if (sub < cnt) {
+                const uint8_t* tile = smem + st * SM::kStage + sub * SM::kTile;
+                const int ntok = info[st * kPer + sub].x, ctx0 = info[st * kPer + sub].y;
+#pragma unroll
+                for (int rb = 0; rb < RB; ++rb) {
+                    if (rb * 16 >= m_rows) break;
+                    float acc[2][4];
+                    if constexpr (EB == 0) {
+                        uint32_t qb[2][D / 16][2];
+#pragma unroll
+                        for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk)
+                                lds64(smem_u32(qt) + swz(rb * 16 + nb * 8 + g, 2 * kk + (t >> 1), q_rows<D>()) + 8 * (t & 1),
+                                      qb[nb][kk][0], qb[nb][kk][1]);
+                        f4_scores<C, D, 2, false>(tile, tok0 / 16, qb, acc, lane);
+                    } else {
+                        cf_scores<C, D, 16, EB == 1>(smem_u32(tile), tok0, smem_u32(qt) + rb * 16 * 128, 0, D / 16, acc, lane);
+                    }
+#pragma unroll
+                    for (int k = 0; k < RS; ++k) {
+                        const int row = row_of(rb, k);
+                        if (row >= m_rows) continue;
+                        // this thread's columns of the row, in the order of x
+                        constexpr int N = 8 / RS;
+                        float x[N], top = m[rb][k];
+#pragma unroll
+                        for (int j = 0; j < N; ++j) {
+                            const int col = tok0 + (EB == 0 ? f4_token(g) + 8 * j : (j >> 1) * 8 + 2 * t + (j & 1));
+                            const float v = (EB == 0 ? acc[k >> 1][2 * j + (k & 1)] : acc[j >> 1][2 * k + (j & 1)]) * p.scale_log2;
+                            x[j] = col < ntok && ctx0 + col <= lim[rb][k] ? v : -INFINITY;
+                            top = fmaxf(top, x[j]);
+                        }
+                        const float mu = top == -INFINITY ? 0.f : top;
+                        float sum = s[rb][k] * ex2(m[rb][k] - mu);
+#pragma unroll
+                        for (int j = 0; j < N; ++j) sum += ex2(x[j] - mu);
+                        m[rb][k] = top;
+                        s[rb][k] = sum;
+                        float* dst = row_at[row] + ctx0 + tok0;
+                        if constexpr (EB == 0) {
+                            dst[f4_token(g)] = x[0];
+                            dst[f4_token(g) + 8] = x[1];
+                        } else {
+                            *reinterpret_cast<float2*>(dst + 2 * t) = make_float2(x[0], x[1]);
+                            *reinterpret_cast<float2*>(dst + 8 + 2 * t) = make_float2(x[2], x[3]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty0 + 8 * st);
+        }
+        // the row's columns of the other lanes, then of the other warps
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+            for (int k = 0; k < RS; ++k) {
+                float mk = m[rb][k], sk = s[rb][k];
+#pragma unroll
+                for (int off = EB == 0 ? 4 : 1; off <= (EB == 0 ? 16 : 2); off <<= 1) {
+                    const float m2 = __shfl_xor_sync(kFull, mk, off), s2 = __shfl_xor_sync(kFull, sk, off);
+                    const float M = fmaxf(mk, m2), mu = M == -INFINITY ? 0.f : M;
+                    sk = sk * ex2(mk - mu) + s2 * ex2(m2 - mu);
+                    mk = M;
+                }
+                const int row = row_of(rb, k);
+                if (row < m_rows && (EB == 0 ? g : t) == 0) ms[warp * kQRows + row] = make_float2(mk, sk);
+            }
+        wt_sync();
+        for (int row = threadIdx.x; row < m_rows; row += kWtWarps * 32) {
+            float M = -INFINITY, S = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWtWarps; ++w) M = fmaxf(M, ms[w * kQRows + row].x);
+            const float mu = M == -INFINITY ? 0.f : M;
+#pragma unroll
+            for (int w = 0; w < kWtWarps; ++w) S += ms[w * kQRows + row].y * ex2(ms[w * kQRows + row].x - mu);
+            const int pos = U.q_lo + row / RW, jq = (row % RW) / G;
+            p.part_ms[p.pbase[((size_t)pos * QL + jq) * H + head * G + row % G] + part] = make_float2(M, S);
+        }
+    }
+}
+
+// Joins the units' (m, s) of each row of a position and head, then adds the
+// rows' weights of four tokens per thread.
+__global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const WeightParams wp) {
+    __shared__ float lse[kQRows];                     // log2 of each row's sum
+    const AttnParams& p = wp.a;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int blk = blockIdx.x % wp.blocks, pair = blockIdx.x / wp.blocks;
+    const int pos = pair / p.n_kv_heads, h = pair % p.n_kv_heads;
+    const int G = p.group, QL = p.q_len, RW = QL * G, H = p.n_heads;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long c0 = wp.tok_base[pos], tokens = (wp.tok_base[pos + 1] - c0) * wp.chunk;
+    const int t0 = blk * kAddTokens + 4 * threadIdx.x;
+    const size_t row = ((size_t)p.seq_perm[pos] * p.n_kv_heads + h) * wp.room;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (blk * (long long)kAddTokens >= tokens && (wp.in == wp.out || blk * (long long)kAddTokens >= wp.room)) return;
+    for (int r = warp; r < RW; r += kAddThreads / 32) {
+        const size_t id = ((size_t)pos * QL + r / G) * H + h * G + r % G;
+        const int a = p.pbase[id], n = p.pbase[id + 1] - a;
+        float M = -INFINITY, S = 0.f;
+        for (int j = lane; j < n; j += 32) {
+            const float2 x = __ldcg(&p.part_ms[a + j]);
+            const float top = fmaxf(M, x.x), mu = top == -INFINITY ? 0.f : top;
+            S = S * ex2(M - mu) + x.y * ex2(x.x - mu);
+            M = top;
+        }
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) {
+            const float m2 = __shfl_xor_sync(kFull, M, off), s2 = __shfl_xor_sync(kFull, S, off);
+            const float top = fmaxf(M, m2), mu = top == -INFINITY ? 0.f : top;
+            // (the same order in both lanes, so that they agree)
+            const float a1 = S * ex2(M - mu), a2 = s2 * ex2(m2 - mu);
+            S = (lane & off) ? a2 + a1 : a1 + a2;
+            M = top;
+        }
+        if (lane == 0) lse[r] = S > 0.f || S != S ? M + log2f(S) : INFINITY;   // (a row that sees nothing weighs nothing)
+    }
+    __syncthreads();
+    float w[4] = {0.f, 0.f, 0.f, 0.f};
+    if (t0 < tokens) {                                // (a position's tokens are a multiple of 16)
+        const float* x = wp.scores + c0 * wp.chunk * ((long long)QL * H) + (long long)h * RW * tokens + t0;
+        for (int r = 0; r < RW; ++r, x += tokens) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(x));
+            const float l = lse[r];
+            w[0] += ex2(v.x - l);
+            w[1] += ex2(v.y - l);
+            w[2] += ex2(v.z - l);
+            w[3] += ex2(v.w - l);
+            if (r == 0 && ((t0 >= wp.room && v.x != -INFINITY) || (t0 + 1 >= wp.room && v.y != -INFINITY) ||
+                           (t0 + 2 >= wp.room && v.z != -INFINITY) || (t0 + 3 >= wp.room && v.w != -INFINITY)))
+                set_status(p.status, CA_ERR_DEVICE_BOUNDS);   // the context has outgrown its row
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (t0 + j < wp.room && (t0 < tokens || wp.in != wp.out)) wp.out[row + t0 + j] = wp.in[row + t0 + j] + w[j];
+}
+
+}  // namespace dev
+
+namespace {
+
+template <int C, int D, int EB>
+int run_scores(const CUtensorMap* map, const dev::WeightParams& w, unsigned grid, cudaLaunchAttribute* attr, cudaStream_t s) {
+    constexpr int bytes = dev::WtSmem<C, D, EB>::kBytes;
+    if (cudaFuncSetAttribute(dev::weight_scores_kernel<C, D, EB>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+        return CA_ERR_CUDA;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3(grid);
+    c.blockDim = dim3(dev::kWtThreads);
+    c.dynamicSmemBytes = bytes;
+    c.stream = s;
+    c.attrs = attr;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, dev::weight_scores_kernel<C, D, EB>, *map, w) == cudaSuccess ? CA_OK : CA_ERR_CUDA;
+}
+
+template <int D, int EB>
+int pick_scores(int chunk, const CUtensorMap* map, const dev::WeightParams& w, unsigned grid, cudaLaunchAttribute* attr,
+                cudaStream_t s) {
+    if (chunk == 16) return run_scores<16, D, EB>(map, w, grid, attr, s);
+    if (chunk == 32) return run_scores<32, D, EB>(map, w, grid, attr, s);
+    if constexpr (D <= 128)
+        if (chunk == 64) return run_scores<64, D, EB>(map, w, grid, attr, s);
+    return CA_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+int launch_weights(const Pool& p, const Sched& s, int32_t layer, const void* q, const float* in, float* out, int32_t room,
+                   float scale, void* ws, void* stream) {
+    const PoolCfg& c = p.cfg;
+    unsigned char* w8 = static_cast<unsigned char*>(ws);
+    dev::WeightParams w{};
+    w.a = attn_params(p, s, layer, q, nullptr, scale, ws);
+    w.a.part_o = nullptr;
+    w.a.part_ms = reinterpret_cast<float2*>(w8 + s.ws.weights_ms);
+    w.a.test_stall = 0;
+    if (s.stall_calls > 0) {
+        w.a.test_stall = 1;
+        --s.stall_calls;
+    }
+    w.tok_base = reinterpret_cast<const int32_t*>(static_cast<unsigned char*>(s.dev) + s.layout.tok_base);
+    w.scores = reinterpret_cast<float*>(w8 + s.ws.weights_scores);
+    w.in = in;
+    w.out = out;
+    w.room = room;
+    w.chunk = c.chunk;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    // Both are programmatic dependents of what precedes them in the stream.
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    const CUtensorMap* map = reinterpret_cast<const CUtensorMap*>(p.tmap);
+    const unsigned units = (unsigned)s.plan.units.size();
+    int st = CA_ERR_UNSUPPORTED;
+    if (c.flags & CA_KV_FP4) {
+        if (c.head_dim == 64) st = pick_scores<64, 0>(c.chunk, map, w, units, attr, cs);
+        else if (c.head_dim == 128) st = pick_scores<128, 0>(c.chunk, map, w, units, attr, cs);
+    } else if (c.flags & CA_KV_FP8) {
+        if (c.head_dim == 128) st = pick_scores<128, 1>(c.chunk, map, w, units, attr, cs);
+    } else {
+        if (c.head_dim == 64) st = pick_scores<64, 2>(c.chunk, map, w, units, attr, cs);
+        else if (c.head_dim == 128) st = pick_scores<128, 2>(c.chunk, map, w, units, attr, cs);
+        else if (c.head_dim == 256) st = pick_scores<256, 2>(c.chunk, map, w, units, attr, cs);
+    }
+    if (st) return st;
+    count_launch();
+    int64_t most = in == out ? 0 : room;
+    for (int32_t pos = 0; pos < s.t.b; ++pos)
+        most = std::max<int64_t>(most, (int64_t)(s.t.tok_base[pos + 1] - s.t.tok_base[pos]) * c.chunk);
+    w.blocks = (int32_t)((most + dev::kAddTokens - 1) / dev::kAddTokens);
+    const int64_t grid = (int64_t)w.blocks * s.t.b * kv_heads(c);
+    if (grid > INT32_MAX) return CA_ERR_UNSUPPORTED;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3((unsigned)grid);
+    lc.blockDim = dim3(dev::kAddThreads);
+    lc.stream = cs;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    if (cudaLaunchKernelEx(&lc, dev::add_weights_kernel, w) != cudaSuccess) return CA_ERR_CUDA;
+    count_launch();
+    return CA_OK;
+}
+
+}  // namespace ca

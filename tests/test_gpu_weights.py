@@ -1,0 +1,236 @@
+"""Accumulated attention weights on the GPU, for every pool type, against the
+fp64 definition over the stored keys.
+
+Tolerance.  A score is a sum of D products, exact in fp32, in 32 bits: off by at
+most (D + 8) 2^-23 times the sum S of their sizes (scale included; a step of
+2^-23 for each sum, since the tensor cores may cut instead of rounding).  The
+weight exp(x) / sum exp(x) then moves by at most twice that, relatively; its own
+exponentials, sum, logarithm and the exponent's rounding (of at most 2^8 in log2
+units: 2^-17 absolute) by 2^-15.  The sums of the rows and the running sum add
+half a step each."""
+import numpy as np
+import pytest
+
+from oracle import weights as OW
+from tests.test_gpu_sparse import POOLS, Cache, held
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def torch_cuda(lib):
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    return torch
+
+
+def queries(x, b, q_len, H):
+    q = x.rng.standard_normal((b, q_len, H, x.D)).astype(np.float16)
+    return q, x.dev(q if q_len > 1 else q[:, 0])
+
+
+def check(x, ids, q, layer, before, got, scale=None, causal=False):
+    """got = before + weights, and before itself past each context."""
+    scale = scale or 1 / np.sqrt(x.D)
+    G = q.shape[2] // x.Hkv
+    before, got = before.astype(np.float64), got.astype(np.float64)
+    for r, i in enumerate(ids):
+        n = x.k[i].shape[1]
+        keys = held(x.k[i][layer], x.kv_dtype, x.ks)
+        for h in range(x.Hkv):
+            w, size = OW.step_weights(q[r, :, h * G:(h + 1) * G], keys[:, h], scale, causal)
+            want = before[r, h, :n] + w
+            tol = w * (2 * (x.D + 8) * 2.0**-23 * size + 2.0**-15) + (np.abs(want) + w) * 2.0**-24 * (q.shape[1] * G + 1) + 1e-30
+            err = np.abs(got[r, h, :n] - want)
+            assert (err <= tol).all(), (i, h, float((err / tol).max()))
+            np.testing.assert_array_equal(got[r, h, n:], before[r, h, n:])
+
+
+@pytest.mark.parametrize("kv_dtype,c,D,G,Hkv", POOLS)
+def test_sums_over_steps(torch_cuda, kv_dtype, c, D, G, Hkv):
+    """Steps over contexts from one token on with a shared prefix, in place and
+    apart, before and after appends that fill partial chunks."""
+    from prefix_shared_decode_gb300 import accumulate_attention
+    torch = torch_cuda
+    lens = [1, c, 5 * c + 3, 17 * c, 40 * c + 7, 3 * c - 1, 33 * c + 1]
+    x = Cache(torch, c + D + G, kv_dtype, c, D, G, Hkv, lens, L=2, ks=0.75, vs=1.25, shared=2 * c + 5)
+    ids = [4, 0, 2, 6, 1, 5, 3]
+    room = 41 * c + 3
+    start = x.rng.random((2, len(ids), Hkv, room)).astype(np.float32)
+    w = x.dev(start)
+    sched = x.pool.schedule(ids)
+    for layer in (0, 1):
+        q, qd = queries(x, len(ids), 1, Hkv * G)
+        assert accumulate_attention(x.pool, sched, qd, w[layer], layer=layer) is not None
+        check(x, ids, q, layer, start[layer], w[layer].cpu().numpy())
+    # the last chunks grow in place: the same schedule sees the new tokens
+    for i in (2, 4, 5, 6):
+        x.append(i, 1)
+    q, qd = queries(x, len(ids), 1, Hkv * G)
+    out = torch.full_like(w[1], -1.0)
+    before = w[1].cpu().numpy()
+    again = torch.empty_like(out)
+    accumulate_attention(x.pool, sched, qd, w[1], out=out, layer=1, scale=0.3)
+    accumulate_attention(x.pool, sched, qd, w[1], out=again, layer=1, scale=0.3)
+    np.testing.assert_array_equal(w[1].cpu().numpy(), before)
+    check(x, ids, q, 1, before, out.cpu().numpy(), scale=0.3)
+    assert torch.equal(out, again)
+    assert sched.device_status() == 0
+
+
+@pytest.mark.parametrize("kv_dtype,c,D,G,Hkv,q_len", [("fp16", 16, 64, 2, 2, 3), ("fp16", 64, 128, 4, 2, 4), ("fp16", 32, 256, 2, 1, 16),
+                                                      ("fp8", 32, 128, 3, 2, 5), ("fp4", 64, 128, 4, 1, 16), ("fp4", 16, 64, 1, 3, 2)])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("no_tpp", [False, True])
+def test_several_query_tokens(torch_cuda, kv_dtype, c, D, G, Hkv, q_len, causal, no_tpp):
+    from prefix_shared_decode_gb300 import accumulate_attention
+    torch = torch_cuda
+    lens = [20 * c + 3, q_len, 3 * c + q_len, 9 * c, 20 * c + 1, 20 * c + 2]
+    x = Cache(torch, c + q_len, kv_dtype, c, D, G, Hkv, lens, L=1, shared=3 * c)
+    ids = [3, 5, 0, 1, 2, 4]
+    sched = x.pool.schedule(ids, q_len=q_len, causal=causal, no_tpp=no_tpp)
+    q, qd = queries(x, len(ids), q_len, Hkv * G)
+    start = np.zeros((len(ids), Hkv, 21 * c), np.float32)
+    w = x.dev(start)
+    accumulate_attention(x.pool, sched, qd, w)
+    check(x, ids, q, 0, start, w.cpu().numpy(), causal=causal)
+    assert sched.device_status() == 0
+
+
+@pytest.mark.parametrize("kv_dtype", ["fp16", "fp8", "fp4"])
+def test_one_long_context_and_odd_rooms(torch_cuda, kv_dtype):
+    """Many units per context, a room that is the context, and one whose rows
+    start off 16 bytes."""
+    from prefix_shared_decode_gb300 import accumulate_attention
+    x = Cache(torch_cuda, 5, kv_dtype, 16, 128, 4, 2, [20011], L=1)
+    sched = x.pool.schedule([0])
+    q, qd = queries(x, 1, 1, 8)
+    for room in (20011, 20013, 30000):
+        w = torch_cuda.ones(1, 2, room, device="cuda")
+        accumulate_attention(x.pool, sched, qd, w)
+        check(x, [0], q, 0, np.ones((1, 2, room), np.float32), w.cpu().numpy())
+
+
+def test_scores_of_every_size(torch_cuda):
+    """Keys that leave all the weight to one token, and keys that are all alike."""
+    from prefix_shared_decode_gb300 import accumulate_attention
+    rng = np.random.default_rng(3)
+    k = np.zeros((1, 200, 1, 64), np.float16)
+    k[0, 77, 0] = 60.0
+    k2 = np.ones((1, 130, 1, 64), np.float16) * np.float16(-3.0)
+    rows = [(k, k.copy()), (k2, k2.copy())]
+    x = Cache(torch_cuda, 5, "fp16", 32, 64, 2, 1, [200, 130], rows=rows)
+    q = np.ones((2, 1, 2, 64), np.float16)
+    q[:, :, 1] = rng.standard_normal((2, 1, 64)).astype(np.float16)
+    w = torch_cuda.zeros(2, 1, 256, device="cuda")
+    accumulate_attention(x.pool, x.pool.schedule([0, 1]), x.dev(q[:, 0]), w)
+    check(x, [0, 1], q, 0, np.zeros((2, 1, 256), np.float32), w.cpu().numpy())
+
+
+def test_streams_and_replays(torch_cuda):
+    """On another stream; captured, then replayed with other queries and after
+    an append; next to a captured decode call, whose workspace stays its own."""
+    from prefix_shared_decode_gb300 import accumulate_attention, decode_attention
+    torch = torch_cuda
+    x = Cache(torch, 9, "fp16", 32, 128, 4, 2, [700, 90, 333], shared=64)
+    ids = [2, 0, 1]
+    sched = x.pool.schedule(ids)
+    q, qd = queries(x, 3, 1, 8)
+    side = torch.cuda.Stream()
+    w = torch.zeros(3, 2, 800, device="cuda")
+    out = torch.empty_like(qd)
+    side.wait_stream(torch.cuda.current_stream())
+    accumulate_attention(x.pool, sched, qd, w, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    check(x, ids, q, 0, np.zeros((3, 2, 800), np.float32), w.cpu().numpy())
+    plain = decode_attention(x.pool, sched, qd)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        decode_attention(x.pool, sched, qd, out=out)
+        accumulate_attention(x.pool, sched, qd, w)
+    for step in range(3):
+        if step == 2:
+            x.append(0, 3)
+        q, new = queries(x, 3, 1, 8)
+        qd.copy_(new)
+        plain = decode_attention(x.pool, sched, qd)
+        before = w.cpu().numpy()
+        graph.replay()
+        torch.cuda.synchronize()
+        check(x, ids, q, 0, before, w.cpu().numpy())
+        assert torch.equal(out, plain)
+    assert sched.device_status() == 0
+
+
+def test_a_context_that_outgrows_its_room_is_reported(torch_cuda):
+    from prefix_shared_decode_gb300 import accumulate_attention
+    torch = torch_cuda
+    x = Cache(torch, 9, "fp16", 32, 64, 1, 2, [70, 33])
+    sched = x.pool.schedule([0, 1])
+    q, qd = queries(x, 2, 1, 2)
+    w = torch.zeros(2, 2, 70, device="cuda")
+    accumulate_attention(x.pool, sched, qd, w)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        accumulate_attention(x.pool, sched, qd, w)
+    graph.replay()
+    assert sched.device_status() == 0
+    before = w.cpu().numpy()[1]
+    x.append(0, 1)
+    graph.replay()
+    assert sched.device_status() == -7 and sched.device_status() == 0
+    got = w.cpu().numpy()
+    k = held(x.k[1][0], "fp16", 1.0)
+    for h in range(2):                    # the next row was not written into
+        want, _ = OW.step_weights(q[1, :, h:h + 1], k[:, h], 1 / 8)
+        np.testing.assert_allclose(got[1, h, :33], before[h, :33] + want, rtol=1e-4)
+
+
+def test_a_wait_that_runs_out_is_reported(torch_cuda):
+    from prefix_shared_decode_gb300 import accumulate_attention
+    torch = torch_cuda
+    for kv_dtype in ("fp16", "fp4"):
+        x = Cache(torch, 9, kv_dtype, 32, 128, 4, 2, [300, 200], shared=100)
+        sched = x.pool.schedule([0, 1])
+        q, qd = queries(x, 2, 1, 8)
+        w = torch.zeros(2, 2, 320, device="cuda")
+        assert x.pool and __import__("prefix_shared_decode_gb300").capi.lib().ca_sched_inject_stall(sched.handle, 1) == 0
+        accumulate_attention(x.pool, sched, qd, w)
+        assert sched.device_status() == -8
+        w.zero_()
+        accumulate_attention(x.pool, sched, qd, w)
+        check(x, [0, 1], q, 0, np.zeros((2, 2, 320), np.float32), w.cpu().numpy())
+        assert sched.device_status() == 0
+
+
+def test_refusals(torch_cuda):
+    from prefix_shared_decode_gb300 import CAError, accumulate_attention
+    torch = torch_cuda
+    x = Cache(torch, 9, "fp16", 32, 64, 2, 2, [70, 33])
+    sched = x.pool.schedule([0, 1])
+    q, qd = queries(x, 2, 1, 4)
+    w = torch.zeros(2, 2, 100, device="cuda")
+    for bad in (w[:, :1], w.double(), w[..., ::2], w[0], w.cpu(), torch.zeros(2, 2, 0, device="cuda")):
+        with pytest.raises(ValueError):
+            accumulate_attention(x.pool, sched, qd, bad)
+    for bad in (w[..., :99].contiguous(), w.half()):
+        with pytest.raises(ValueError):
+            accumulate_attention(x.pool, sched, qd, w, out=bad)
+    with pytest.raises(ValueError):
+        accumulate_attention(x.pool, sched, qd[:1], w)
+    with pytest.raises(CAError, match="INVALID"):          # a context of 70 tokens
+        accumulate_attention(x.pool, sched, qd, torch.zeros(2, 2, 69, device="cuda"))
+    with pytest.raises(CAError, match="INVALID"):
+        accumulate_attention(x.pool, sched, qd, w, layer=1)
+    both = torch.zeros(2 * 2 * 100 + 4, device="cuda")
+    with pytest.raises(CAError, match="INVALID"):          # overlapping, not the same
+        accumulate_attention(x.pool, sched, qd, both[:400].view(2, 2, 100), out=both[4:].view(2, 2, 100))
+    with pytest.raises(CAError, match="INVALID"):
+        accumulate_attention(x.pool, sched, qd, w, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    x.append(0, 64)
+    with pytest.raises(CAError, match="STALE"):
+        accumulate_attention(x.pool, sched, qd, torch.zeros(2, 2, 200, device="cuda"))
+    assert float(w.abs().max()) == 0
