@@ -59,13 +59,20 @@ int build_blocks(const Pool& p, const int64_t* seq_ids, int32_t b, const int32_t
     std::vector<BlockItem> items;
     std::vector<BlockJoin> joins;
     int64_t parts = 0;
+    std::vector<int32_t> list0(1, 0), q_off(1, 0);
+    for (int32_t i = 0; i < b; ++i) {
+        list0.push_back(list0.back() + (int32_t)seq[i]->path.size());
+        q_off.push_back(q_off.back() + q_lens[i]);
+    }
     for (const Tile& t : tiles) {
+        const Sequence& of = *seq[t.seq];
         const int64_t n = std::max<int64_t>(1, (t.chunks + per - 1) / per);
         for (int32_t h = 0; h < HK; ++h) {
             if (n > 1) joins.push_back({t.seq, h, t.row0, t.rows, (int32_t)parts, (int32_t)n, 0, 0});
             for (int64_t x = 0; x < n; ++x)
                 items.push_back({t.seq, h, t.row0, t.rows, (int32_t)(t.chunks * x / n), (int32_t)(t.chunks * (x + 1) / n),
-                                 n > 1 ? (int32_t)parts++ : -1, 0});
+                                 n > 1 ? (int32_t)parts++ : -1, q_off[t.seq], q_lens[t.seq], of.length,
+                                 (int32_t)of.path.size(), list0[t.seq], of.path.back()->slot, {0, 0, 0}});
         }
         if (parts > INT32_MAX / 2) return CA_ERR_UNSUPPORTED;
     }
@@ -77,13 +84,9 @@ int build_blocks(const Pool& p, const int64_t* seq_ids, int32_t b, const int32_t
     s.t = Tables{};
     s.plan = Plan{};
     s.t.b = b;
-    s.t.list_off.push_back(0);
-    std::vector<int32_t> q_off(1, 0);
     for (int32_t i = 0; i < b; ++i) {
         for (const Node* x : seq[i]->path) s.t.list_slots.push_back(x->slot);
-        s.t.list_off.push_back((int32_t)s.t.list_slots.size());
         s.t.ctx_len.push_back(seq[i]->length);
-        q_off.push_back(q_off.back() + q_lens[i]);
     }
     s.q_lens.assign(q_lens, q_lens + b);
     s.q_rows = rows;
@@ -102,8 +105,6 @@ int build_blocks(const Pool& p, const int64_t* seq_ids, int32_t b, const int32_t
     place(lay.status, sizeof(int32_t));
     place(lay.counter, sizeof(int32_t));
     place(lay.list_count, 0);
-    place(lay.ctx_len, s.t.ctx_len.size() * sizeof(int32_t));
-    place(lay.list_off, s.t.list_off.size() * sizeof(int32_t));
     place(lay.list_slots, s.t.list_slots.size() * sizeof(int32_t));
     place(lay.q_off, q_off.size() * sizeof(int32_t));
     place(lay.items, s.items.size() * sizeof(BlockItem));
@@ -113,8 +114,6 @@ int build_blocks(const Pool& p, const int64_t* seq_ids, int32_t b, const int32_t
     auto put = [&s](size_t at, const void* src, size_t bytes) {
         if (bytes) std::memcpy(s.blob.data() + at, src, bytes);
     };
-    put(lay.ctx_len, s.t.ctx_len.data(), s.t.ctx_len.size() * sizeof(int32_t));
-    put(lay.list_off, s.t.list_off.data(), s.t.list_off.size() * sizeof(int32_t));
     put(lay.list_slots, s.t.list_slots.data(), s.t.list_slots.size() * sizeof(int32_t));
     put(lay.q_off, q_off.data(), q_off.size() * sizeof(int32_t));
     put(lay.items, s.items.data(), s.items.size() * sizeof(BlockItem));

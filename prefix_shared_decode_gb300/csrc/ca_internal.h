@@ -143,8 +143,12 @@ struct BlockItem {
     int32_t row0, rows;        // rows [row0, row0 + rows) of the block and head
     int32_t c_begin, c_end;    // chunks of the sequence (equal: the rows see nothing)
     int32_t part;              // partial tile, or -1: the item is the tile's only one
-    int32_t pad;
+    int32_t q0, m;             // the block's first row of q / out, and its query tokens
+    int32_t ctx, n_chunks;     // context tokens (at the build) and chunks
+    int32_t list0, last_slot;  // the sequence's chunk slots: list_slots[list0 ..), and the last of them
+    int32_t pad[3];
 };
+static_assert(sizeof(BlockItem) == 64, "two items a line");
 struct BlockJoin {
     int32_t seq, head, row0, rows;
     int32_t part, n_parts;     // partial tiles [part, part + n_parts)
@@ -398,7 +402,7 @@ int launch_evict(const Pool& p, const Sched& s, const std::vector<EvictSeq>& seq
                  int32_t budget, int32_t sink, int32_t recent, int32_t* kept, float* weights_out, void* stream);
 
 // cross.cu: attention of query blocks
-int cross_tile_rows(const PoolCfg& c);    // rows of a tile
+int cross_tile_rows(const PoolCfg& c);     // rows of a tile
 int cross_places(const Pool& p);           // items that run at a time
 int launch_cross(const Pool& p, const Sched& s, int32_t layer, const void* q, void* out, float scale, void* ws, void* stream);
 

@@ -10,37 +10,12 @@
 #include <algorithm>
 #include <climits>
 
-#include "ca_internal.h"
+#include "cross.cuh"
 #include "fp4.cuh"
 #include "row_blocks.cuh"
 
 namespace ca {
 namespace dev {
-
-struct CrossParams {
-    const uint16_t* q;            // [rows of all blocks][H][D]
-    uint16_t* out;
-    const BlockItem* items;
-    const BlockJoin* joins;
-    const int32_t* q_off;         // [b + 1] first row of each block
-    const int32_t* ctx_len;
-    const int32_t* list_off;
-    const int32_t* list_slots;
-    const int32_t* slot_ntok;
-    const uint8_t* kv;
-    int32_t* status;
-    float* part_o;                // [parts][tile rows][D]
-    float2* part_ms;              // [parts][tile rows]
-    int32_t n_layers, n_heads, n_kv_heads, group, layer, capacity, causal, tile_rows;
-    float scale_log2, out_scale;
-};
-
-// Context tokens of batch row i as the pool holds it now.
-__device__ __forceinline__ int tokens_now(const CrossParams& p, int i, int chunk) {
-    const int a = p.list_off[i], n = p.list_off[i + 1] - a, last = p.list_slots[a + n - 1];
-    if (last < 0 || last >= p.capacity) return 0;
-    return (n - 1) * chunk + min(max(p.slot_ntok[last], 0), chunk);
-}
 
 constexpr int kCrossRows = 64, kCrossKeys = 64, kCrossThreads = 128;
 
@@ -138,14 +113,11 @@ __global__ void __launch_bounds__(kCrossThreads) cross_rows_kernel(const CrossPa
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const BlockItem it = p.items[blockIdx.x];
-    const int G = p.group, H = p.n_heads;
-    const int q0 = p.q_off[it.seq], m = p.q_off[it.seq + 1] - q0, ctx = p.ctx_len[it.seq];
+    const int G = p.group;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int n = min(tokens_now(p, it.seq, C), it.c_end * C);
-    const int32_t* slots = p.list_slots + p.list_off[it.seq];
-    auto row_at = [&](int r) {                        // element of q and out where row r of the tile begins
-        return ((size_t)(q0 + (it.row0 + r) / G) * H + it.head * G + (it.row0 + r) % G) * D;
-    };
+    const int n = min(tokens_now(p, it, C), it.c_end * C);
+    const int32_t* slots = p.list_slots + it.list0;
+    auto row_at = [&](int r) { return block_row(p, it, r, D); };
     for (int i = threadIdx.x; i < kCrossRows * (D / 8); i += kCrossThreads) {
         const int r = i / (D / 8), k = i % (D / 8);
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -156,7 +128,7 @@ __global__ void __launch_bounds__(kCrossThreads) cross_rows_kernel(const CrossPa
     const uint32_t qblock = smem_u32(qt) + r0 / QR * (QR * D * 2) + r0 % QR * 128;
     int lim[2];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) lim[k] = p.causal ? ctx - m + (it.row0 + r0 + g + 8 * k) / G : INT_MAX;
+    for (int k = 0; k < 2; ++k) lim[k] = p.causal ? it.ctx - it.m + (it.row0 + r0 + g + 8 * k) / G : INT_MAX;
     float o[D / 8][4], mx[2] = {-INFINITY, -INFINITY}, s[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -228,8 +200,10 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const CrossParams p) {
 
 }  // namespace dev
 
-int cross_tile_rows(const PoolCfg&) { return dev::kCrossRows; }
-int cross_places(const Pool& p) { return (p.sms > 0 ? p.sms : 152) * 2; }
+// fp16 pools: tiles for the 5th-generation tensor cores, an SM each.
+static bool on_tiles(const PoolCfg& c) { return !(c.flags & (CA_KV_FP8 | CA_KV_FP4)); }
+int cross_tile_rows(const PoolCfg& c) { return !on_tiles(c) ? dev::kCrossRows : c.head_dim == 256 ? 128 : 256; }
+int cross_places(const Pool& p) { return (p.sms > 0 ? p.sms : 152) * (on_tiles(p.cfg) ? 1 : 2); }
 
 namespace {
 
@@ -276,8 +250,6 @@ int launch_cross(const Pool& p, const Sched& s, int32_t layer, const void* q, vo
     a.items = reinterpret_cast<const BlockItem*>(dev8 + s.layout.items);
     a.joins = reinterpret_cast<const BlockJoin*>(dev8 + s.layout.joins);
     a.q_off = reinterpret_cast<const int32_t*>(dev8 + s.layout.q_off);
-    a.ctx_len = reinterpret_cast<const int32_t*>(dev8 + s.layout.ctx_len);
-    a.list_off = reinterpret_cast<const int32_t*>(dev8 + s.layout.list_off);
     a.list_slots = reinterpret_cast<const int32_t*>(dev8 + s.layout.list_slots);
     a.slot_ntok = reinterpret_cast<const int32_t*>(static_cast<const unsigned char*>(p.kv) + pool_tile_bytes(c));
     a.kv = static_cast<const uint8_t*>(p.kv);
@@ -294,7 +266,12 @@ int launch_cross(const Pool& p, const Sched& s, int32_t layer, const void* q, vo
     a.tile_rows = s.tile_rows;
     a.scale_log2 = scale * 1.4426950408889634f * (quant ? kv_scale_of(c.k_scale) : 1.f);
     a.out_scale = quant ? kv_scale_of(c.v_scale) : 1.f;
+    a.n_items = (int32_t)s.items.size();
     if (s.items.empty()) return CA_OK;
+    if (s.stall_calls > 0) {
+        a.test_stall = 1;
+        --s.stall_calls;
+    }
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const unsigned grid = (unsigned)s.items.size();
     int st = CA_ERR_UNSUPPORTED;
@@ -304,9 +281,7 @@ int launch_cross(const Pool& p, const Sched& s, int32_t layer, const void* q, vo
     } else if (c.flags & CA_KV_FP8) {
         if (c.head_dim == 128) st = pick<128, 1>(c.chunk, grid, a, cs);
     } else {
-        if (c.head_dim == 64) st = pick<64, 2>(c.chunk, grid, a, cs);
-        else if (c.head_dim == 128) st = pick<128, 2>(c.chunk, grid, a, cs);
-        else if (c.head_dim == 256) st = pick<256, 2>(c.chunk, grid, a, cs);
+        st = launch_cross_tiles(p, a, cs);
     }
     if (st || s.joins.empty()) return st;
     const unsigned jg = (unsigned)(s.joins.size() * ((s.tile_rows + 7) / 8));

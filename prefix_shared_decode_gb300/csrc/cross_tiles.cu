@@ -1,0 +1,430 @@
+// Query blocks of an fp16 pool on the 5th-generation tensor cores: tiles of 256
+// rows (128 at head_dim 256) against 128 (64) keys at a time.
+//
+// One CTA per SM walks the schedule's items.  Its warps:
+//   0-3, 4-7  the softmax of the tile's two halves of 128 rows, one thread a row
+//   8         issues every product: S = Q K^T and O += P V
+//   9         brings chunks' keys and values in (TMA)
+//   10, 11    bring the next tile's queries in
+// S, P and O stay in tensor memory; P takes the place of the scores it came from.
+// While one half is in its softmax, the other half's products run: per step of
+// 128 keys and half, 2 x 128 x 128 x D multiply-adds and 16 K exponentials.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+
+#include "cross.cuh"
+#include "tcgen05.cuh"
+
+namespace ca {
+namespace dev {
+
+constexpr int kTileThreads = 384, kTmemColumns = 512;
+constexpr int kMmaWarp = 8, kChunkWarp = 9, kQueryWarp = 10, kQueryWarps = 2;
+
+template <int D>
+struct TileShape {
+    static constexpr int kHalves = D == 256 ? 1 : 2;
+    static constexpr int kKeys = D == 256 ? 64 : 128;             // of a step
+    static constexpr int kSlab = kKeys * 128, kStage = D / 64 * kSlab;   // K or V of a step
+    static constexpr int kQSlab = 128 * 128, kQHalf = D / 64 * kQSlab;
+    static constexpr int kStages = D == 64 ? 8 : 5;
+    static constexpr int kO = 0, kS = kHalves * D;                // columns: outputs, then scores, half by half
+    static constexpr int kBytes = kHalves * kQHalf + kStages * kStage + 256;
+    static_assert(kS + kHalves * kKeys <= kTmemColumns && kBytes <= 227 * 1024, "fits an SM");
+};
+
+struct TileBars {
+    uint64_t full[8], empty[8];           // a stage's K or V
+    uint64_t q_full, q_empty;
+    uint64_t s_full[2], p_full[2];        // a half's scores are there; its weights are
+    uint64_t o_full[2];
+    uint64_t drain;
+    uint32_t tmem;
+};
+static_assert(sizeof(TileBars) <= 256, "room behind the stages");
+
+// What every role reads of an item.
+struct TileItem {
+    BlockItem b;
+    int n, steps;                         // tokens up to the item's last chunk, steps from c_begin on
+};
+template <int C, int D>
+__device__ __forceinline__ TileItem tile_item(const CrossParams& p, int idx) {
+    TileItem t;
+    t.b = p.items[idx];
+    t.n = min(tokens_now(p, t.b, C), t.b.c_end * C);
+    t.steps = max(0, (t.n - t.b.c_begin * C + TileShape<D>::kKeys - 1) / TileShape<D>::kKeys);
+    return t;
+}
+
+template <int C, int D>
+__global__ void __launch_bounds__(kTileThreads, 1) cross_tiles_kernel(const __grid_constant__ CUtensorMap tmap,
+                                                                      const CrossParams p) {
+    using T = TileShape<D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t* stages = smem + T::kHalves * T::kQHalf;
+    TileBars* bars = reinterpret_cast<TileBars*>(stages + T::kStages * T::kStage);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if ((smem_u32(smem) & 1023u) != 0) {                  // (the same for the whole CTA)
+        if (threadIdx.x == 0) set_status(p.status, CA_ERR_INVALID);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < T::kStages; ++i) {
+            mbar_init(smem_u32(&bars->full[i]), 1);
+            mbar_init(smem_u32(&bars->empty[i]), 1);
+        }
+        mbar_init(smem_u32(&bars->q_full), kQueryWarps);
+        mbar_init(smem_u32(&bars->q_empty), 1);
+        for (int h = 0; h < 2; ++h) {
+            mbar_init(smem_u32(&bars->s_full[h]), 1);
+            mbar_init(smem_u32(&bars->p_full[h]), 4);
+            mbar_init(smem_u32(&bars->o_full[h]), 1);
+        }
+        mbar_init(smem_u32(&bars->drain), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == kMmaWarp) tmem_alloc(smem_u32(&bars->tmem), kTmemColumns);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    // Every wait is bounded; a role whose wait runs out says so and ends, and
+    // the others' waits for it then run out too.
+    auto timed_out = [&]() { set_status(p.status, CA_ERR_TIMEOUT); };
+
+    // Items in turn, every other round backwards: they are listed by falling length.
+    auto item_of = [&](int round) {
+        const long long i = (long long)round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        return i < p.n_items ? (int)i : -1;
+    };
+    constexpr int kPer = T::kKeys / C;                    // chunks of a step
+
+    if (warp == kChunkWarp) {
+        // ------------------------------ keys and values ------------------------------
+        int it = 0;
+        bool ok = true;
+        if (p.test_stall) {                               // test hook: a wait that nothing ends
+            if (lane == 0 && !mbar_wait(smem_u32(&bars->full[0]), 0u)) timed_out();
+            ok = false;
+        }
+        for (int round = 0; ok; ++round) {
+            const int idx = item_of(round);
+            if (idx < 0) break;
+            const TileItem t = tile_item<C, D>(p, idx);
+            const int32_t* slots = p.list_slots + t.b.list0;
+            // A lane per chunk.  Past the item's last chunk that one comes again: its
+            // keys are masked, and its values, whose weights are 0, are finite.
+            auto slot_at = [&](int step) {
+                return lane < kPer && step < t.steps ? slots[min(t.b.c_begin + step * kPer + lane, t.b.c_end - 1)] : 0;
+            };
+            int slot = slot_at(0);
+            for (int x = 0; x < 2 * t.steps; ++x, ++it) { // K and V of each step
+                const int st = it % T::kStages;
+                if (!mbar_wait(smem_u32(&bars->empty[st]), ((uint32_t)(it / T::kStages) & 1u) ^ 1u)) ok = false;
+                ok = __all_sync(kFull, ok);
+                if (!ok) {
+                    if (lane == 0) timed_out();
+                    break;
+                }
+                if (slot < 0 || slot >= p.capacity) {
+                    set_status(p.status, CA_ERR_DEVICE_BOUNDS);
+                    slot = 0;
+                }
+                const int row = ((slot * p.n_layers + p.layer) * 2 * p.n_kv_heads + (x & 1) * p.n_kv_heads + t.b.head) * C;
+                const uint32_t fb = smem_u32(&bars->full[st]);
+                if (lane == 0) mbar_expect_tx_only(fb, T::kStage);
+                __syncwarp();
+                if (lane < kPer) {
+                    const uint32_t dst = smem_u32(stages) + st * T::kStage + lane * C * 128;
+#pragma unroll
+                    for (int s = 0; s < D / 64; ++s) tma_load_2d(dst + s * T::kSlab, &tmap, 64 * s, row, fb);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(fb);
+                if (x & 1) slot = slot_at((x >> 1) + 1);
+            }
+        }
+        if (!ok)                                          // copies in flight land before the CTA can end
+            for (int k = max(0, it - T::kStages); k < it; ++k)
+                mbar_wait(smem_u32(&bars->full[k % T::kStages]), (uint32_t)(k / T::kStages) & 1u);
+    } else if (warp >= kQueryWarp && warp < kQueryWarp + kQueryWarps) {
+        // ------------------------------ queries ------------------------------
+        uint32_t ph = 0u;
+        for (int round = 0;; ++round) {
+            const int idx = item_of(round);
+            if (idx < 0) break;
+            const TileItem t = tile_item<C, D>(p, idx);
+            if (t.steps == 0) continue;
+            if (!__all_sync(kFull, mbar_wait(smem_u32(&bars->q_empty), ph ^ 1u))) {
+                if (lane == 0) timed_out();
+                break;
+            }
+            ph ^= 1u;
+            const int rows = t.b.rows > 128 ? 256 : 128;  // of the halves that have any
+            for (int i = threadIdx.x - 32 * kQueryWarp; i < rows * (D / 8); i += 32 * kQueryWarps) {
+                const int r = i / (D / 8), k = i % (D / 8);
+                cp_async16_or_zero(smem_u32(smem) + r / 128 * T::kQHalf + swz(r % 128, k, 128),
+                                   p.q + block_row(p, t.b, min(r, t.b.rows - 1), D) + k * 8, r < t.b.rows);
+            }
+            cp_async_wait_all();
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->q_full));
+        }
+    } else if (warp == kMmaWarp) {
+        // ------------------------------ products ------------------------------
+        if (lane == 0) {
+            constexpr uint32_t kShapeS = f16_shape(T::kKeys, false), kShapeO = f16_shape(D, true);
+            const uint32_t q_at = smem_u32(smem), st_at = smem_u32(stages);
+            int it = 0;
+            uint32_t q_ph = 0u, p_ph = 0u;                // (both halves' barriers: one bit each)
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                if (ok && !mbar_wait(smem_u32(bar), parity)) {
+                    timed_out();
+                    ok = false;
+                }
+                tc_fence_after();
+                return ok;
+            };
+            auto scores = [&](int h, int st) {
+                const uint32_t a = q_at + h * T::kQHalf, b = st_at + st * T::kStage, d = tmem + T::kS + h * T::kKeys;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    mma_ss(d, desc_along_row(a + k / 4 * T::kQSlab + k % 4 * 32), desc_along_row(b + k / 4 * T::kSlab + k % 4 * 32),
+                           kShapeS, k > 0);
+                mma_commit(smem_u32(&bars->s_full[h]));
+            };
+            for (int round = 0; ok; ++round) {
+                const int idx = item_of(round);
+                if (idx < 0) break;
+                const TileItem t = tile_item<C, D>(p, idx);
+                if (t.steps == 0) continue;
+                const int halves = t.b.rows > 128 ? 2 : 1;
+                if (!wait(&bars->q_full, q_ph)) break;
+                q_ph ^= 1u;
+                if (!wait(&bars->full[it % T::kStages], (uint32_t)(it / T::kStages) & 1u)) break;
+                for (int h = 0; h < halves; ++h) scores(h, it % T::kStages);
+                mma_commit(smem_u32(&bars->empty[it % T::kStages]));
+                if (t.steps == 1) mma_commit(smem_u32(&bars->q_empty));
+                ++it;
+                for (int j = 0; j < t.steps; ++j) {
+                    const int sv = it % T::kStages, sk = (it + 1) % T::kStages;
+                    const bool more = j + 1 < t.steps;
+                    for (int h = 0; h < halves; ++h) {
+                        if (!wait(&bars->p_full[h], (p_ph >> h) & 1u)) break;
+                        p_ph ^= 1u << h;
+                        if (h == 0 && !wait(&bars->full[sv], (uint32_t)(it / T::kStages) & 1u)) break;
+                        const uint32_t a = tmem + T::kS + h * T::kKeys, b = st_at + sv * T::kStage, d = tmem + T::kO + h * D;
+#pragma unroll
+                        for (int k = 0; k < T::kKeys / 16; ++k)
+                            mma_ts(d, a + 8 * k, desc_along_rows(b + k * 2048, T::kSlab), kShapeO, j > 0 || k > 0);
+                        if (more) {
+                            if (h == 0 && !wait(&bars->full[sk], (uint32_t)((it + 1) / T::kStages) & 1u)) break;
+                            scores(h, sk);
+                        } else {
+                            mma_commit(smem_u32(&bars->o_full[h]));
+                        }
+                    }
+                    if (!ok) break;
+                    mma_commit(smem_u32(&bars->empty[sv]));
+                    if (more) mma_commit(smem_u32(&bars->empty[sk]));
+                    if (j + 2 == t.steps) mma_commit(smem_u32(&bars->q_empty));
+                    it += more ? 2 : 1;
+                }
+            }
+            // everything issued is done before the CTA can end
+            mma_commit(smem_u32(&bars->drain));
+            mbar_wait(smem_u32(&bars->drain), 0u);
+        }
+        __syncwarp();
+    } else if (warp < 4 * T::kHalves) {
+        // ------------------------------ softmax ------------------------------
+        const int h = warp >> 2;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;          // 32 (warp % 4), in an address's upper half
+        const uint32_t s_at = tmem + lanes + T::kS + h * T::kKeys, o_at = tmem + lanes + T::kO + h * D;
+        const int r = threadIdx.x & (128 * T::kHalves - 1);
+        // a negative scale turns the scores' signs; with 0 all scores are alike
+        const float scale = fmaxf(fabsf(p.scale_log2), 1e-37f);
+        const bool turned = p.scale_log2 < 0.f;
+        uint32_t s_ph = 0u, o_ph = 0u;
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            ok = __all_sync(kFull, mbar_wait(smem_u32(bar), parity));
+            if (!ok && lane == 0) timed_out();
+            tc_fence_after();
+            return ok;
+        };
+        for (int round = 0; ok; ++round) {
+            const int idx = item_of(round);
+            if (idx < 0) break;
+            const TileItem t = tile_item<C, D>(p, idx);
+            if (128 * h >= t.b.rows) continue;
+            // the last token that the row sees (a row past the tile's last: all)
+            int last = t.n - 1;
+            if (p.causal && r < t.b.rows) last = min(last, t.b.ctx - t.b.m + (t.b.row0 + r) / p.group);
+            const int all_see = __reduce_min_sync(kFull, last);
+            float m = -INFINITY, sum = 0.f;
+            for (int j = 0; j < t.steps; ++j) {
+                if (!wait(&bars->s_full[h], s_ph)) break;
+                s_ph ^= 1u;
+                constexpr int NC = T::kKeys / 32;
+                uint32_t x[NC][32];
+#pragma unroll
+                for (int c = 0; c < NC; ++c) tmem_ld32(s_at + 32 * c, x[c]);
+                tmem_wait_ld();
+                const int t0 = t.b.c_begin * C + j * T::kKeys;
+                if (turned) {
+#pragma unroll
+                    for (int c = 0; c < NC; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[c][e] ^= 0x80000000u;
+                }
+                if (t0 + T::kKeys - 1 > all_see) {
+                    const int see = last - t0;
+#pragma unroll
+                    for (int c = 0; c < NC; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (32 * c + e > see) x[c][e] = 0xff800000u;
+                }
+                float top = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(x[c][e]));
+                // The reference maximum rises only when it falls short by more than 2^8
+                // (weights then stay below 256, exact enough in fp16), so that the
+                // outputs are hardly ever scaled.
+                top *= scale;
+                const bool rise = top > m + 8.f;
+                if (__any_sync(kFull, rise)) {
+                    const float a = rise ? ex2(m - top) : 1.f;
+                    if (rise) m = top;
+                    sum *= a;
+                    if (j > 0) {                          // (the scores' barrier says that the step before is in)
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_ld32(o_at + 32 * c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+                            tmem_st32(o_at + 32 * c, o);
+                        }
+                    }
+                }
+                const float mu = m == -INFINITY ? 0.f : m;
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[c][e] = __float_as_uint(ex2(fmaf(__uint_as_float(x[c][e]), scale, -mu)));
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) w[e] = pack_half2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1]));
+                    tmem_st16(s_at + 16 * c, w);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[h]));
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) sum += __uint_as_float(x[c][e]);
+            }
+            if (!ok) break;
+            if (t.steps > 0) {
+                if (!wait(&bars->o_full[h], o_ph)) break;
+                o_ph ^= 1u;
+            }
+            const float inv = sum == 0.f ? 0.f : p.out_scale / sum;
+            const size_t id = (size_t)t.b.part * p.tile_rows + r;
+            const size_t at = r < t.b.rows ? block_row(p, t.b, r, D) : 0;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                if (t.steps > 0) {
+                    tmem_ld32(o_at + 32 * c, o);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0u;
+                }
+                if (r >= t.b.rows) {
+                } else if (t.b.part >= 0) {
+                    uint4* dst = reinterpret_cast<uint4*>(p.part_o + id * D + 32 * c);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                } else {
+                    uint4* dst = reinterpret_cast<uint4*>(p.out + at + 32 * c);
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        w[e] = pack_half2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                }
+                __syncwarp();
+            }
+            if (t.b.part >= 0 && r < t.b.rows) p.part_ms[id] = make_float2(m, sum);
+            tc_fence_before();                            // (the next tile's first product overwrites the outputs)
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_free(tmem, kTmemColumns);
+}
+
+}  // namespace dev
+
+namespace {
+
+template <int C, int D>
+int run(const Pool& p, const dev::CrossParams& a, cudaStream_t s) {
+    constexpr int bytes = dev::TileShape<D>::kBytes;
+    if (cudaFuncSetAttribute(dev::cross_tiles_kernel<C, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+        return CA_ERR_CUDA;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3((unsigned)(a.n_items < p.sms ? a.n_items : p.sms));
+    c.blockDim = dim3(dev::kTileThreads);
+    c.dynamicSmemBytes = bytes;
+    c.stream = s;
+    c.attrs = attr;
+    c.numAttrs = 1;
+    if (cudaLaunchKernelEx(&c, dev::cross_tiles_kernel<C, D>, *reinterpret_cast<const CUtensorMap*>(p.tmap), a) != cudaSuccess)
+        return CA_ERR_CUDA;
+    count_launch();
+    return CA_OK;
+}
+
+template <int D>
+int pick(const Pool& p, const dev::CrossParams& a, cudaStream_t s) {
+    if (p.cfg.chunk == 16) return run<16, D>(p, a, s);
+    if (p.cfg.chunk == 32) return run<32, D>(p, a, s);
+    if constexpr (D <= 128)
+        if (p.cfg.chunk == 64) return run<64, D>(p, a, s);
+    return CA_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+int launch_cross_tiles(const Pool& p, const dev::CrossParams& a, cudaStream_t s) {
+    if (p.cfg.head_dim == 64) return pick<64>(p, a, s);
+    if (p.cfg.head_dim == 128) return pick<128>(p, a, s);
+    if (p.cfg.head_dim == 256) return pick<256>(p, a, s);
+    return CA_ERR_UNSUPPORTED;
+}
+
+}  // namespace ca

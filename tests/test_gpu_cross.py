@@ -222,3 +222,32 @@ def test_refusals(torch_cuda):
     x.append(0, 64)
     with pytest.raises(CAError, match="STALE"):
         cross_attention(x.pool, sched, qd)
+
+
+def test_scales_of_every_sign(torch_cuda):
+    from prefix_shared_decode_gb300 import cross_attention
+    x = Cache(torch_cuda, 13, "fp16", 32, 128, 2, 2, [300, 37])
+    blocks = [140, 9]
+    for causal in (False, True):
+        sched = x.pool.schedule([0, 1], q_lens=blocks, causal=causal)
+        q, qd = queries(x, blocks, 4)
+        for scale in (-0.1, 0.0, 1e-3):
+            out = cross_attention(x.pool, sched, qd, scale=scale).cpu().numpy()
+            at = 0
+            for i, m in enumerate(blocks):
+                k, v = x.k[i][0].astype(np.float64), x.v[i][0].astype(np.float64)
+                near(out[at:at + m], OC.attention(q[at:at + m], k, v, scale, causal), OC.attention(q[at:at + m], k, np.abs(v), scale, causal))
+                at += m
+
+
+def test_a_wait_that_runs_out_is_reported(torch_cuda):
+    from prefix_shared_decode_gb300 import capi, cross_attention
+    x = Cache(torch_cuda, 9, "fp16", 32, 128, 4, 2, [300, 200], shared=100)
+    blocks = [100, 50]
+    sched = x.pool.schedule([0, 1], q_lens=blocks)
+    q, qd = queries(x, blocks, 8)
+    assert capi.lib().ca_sched_inject_stall(sched.handle, 1) == 0
+    cross_attention(x.pool, sched, qd)
+    assert sched.device_status() == -8
+    check(x, [0, 1], blocks, q, 0, cross_attention(x.pool, sched, qd))
+    assert sched.device_status() == 0
