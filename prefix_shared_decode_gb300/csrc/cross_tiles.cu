@@ -59,6 +59,29 @@ __device__ __forceinline__ TileItem tile_item(const CrossParams& p, int idx) {
     return t;
 }
 
+// A CTA's items in turn, every other round backwards (they are listed by falling
+// length); what there is to know of the next one is on its way beforehand.
+template <int C, int D>
+struct ItemWalk {
+    const CrossParams& p;
+    int round = 0, idx, next_idx;
+    TileItem t, next;
+    __device__ __forceinline__ explicit ItemWalk(const CrossParams& p_) : p(p_), idx(at(0)), next_idx(at(1)) {
+        if (idx >= 0) t = tile_item<C, D>(p, idx);
+        if (next_idx >= 0) next = tile_item<C, D>(p, next_idx);
+    }
+    __device__ __forceinline__ int at(int r) const {
+        const long long i = (long long)r * gridDim.x + ((r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        return i < p.n_items ? (int)i : -1;
+    }
+    __device__ __forceinline__ void advance() {
+        idx = next_idx;
+        t = next;
+        next_idx = at(++round + 1);
+        if (next_idx >= 0) next = tile_item<C, D>(p, next_idx);
+    }
+};
+
 template <int C, int D>
 __global__ void __launch_bounds__(kTileThreads, 1) cross_tiles_kernel(const __grid_constant__ CUtensorMap tmap,
                                                                       const CrossParams p) {
@@ -99,11 +122,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) cross_tiles_kernel(const __gr
     // the others' waits for it then run out too.
     auto timed_out = [&]() { set_status(p.status, CA_ERR_TIMEOUT); };
 
-    // Items in turn, every other round backwards: they are listed by falling length.
-    auto item_of = [&](int round) {
-        const long long i = (long long)round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        return i < p.n_items ? (int)i : -1;
-    };
     constexpr int kPer = T::kKeys / C;                    // chunks of a step
 
     if (warp == kChunkWarp) {
@@ -114,10 +132,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) cross_tiles_kernel(const __gr
             if (lane == 0 && !mbar_wait(smem_u32(&bars->full[0]), 0u)) timed_out();
             ok = false;
         }
-        for (int round = 0; ok; ++round) {
-            const int idx = item_of(round);
-            if (idx < 0) break;
-            const TileItem t = tile_item<C, D>(p, idx);
+        for (ItemWalk<C, D> walk(p); ok && walk.idx >= 0; walk.advance()) {
+            const TileItem& t = walk.t;
             const int32_t* slots = p.list_slots + t.b.list0;
             // A lane per chunk.  Past the item's last chunk that one comes again: its
             // keys are masked, and its values, whose weights are 0, are finite.
@@ -157,21 +173,25 @@ __global__ void __launch_bounds__(kTileThreads, 1) cross_tiles_kernel(const __gr
     } else if (warp >= kQueryWarp && warp < kQueryWarp + kQueryWarps) {
         // ------------------------------ queries ------------------------------
         uint32_t ph = 0u;
-        for (int round = 0;; ++round) {
-            const int idx = item_of(round);
-            if (idx < 0) break;
-            const TileItem t = tile_item<C, D>(p, idx);
+        for (ItemWalk<C, D> walk(p); walk.idx >= 0; walk.advance()) {
+            const TileItem& t = walk.t;
             if (t.steps == 0) continue;
             if (!__all_sync(kFull, mbar_wait(smem_u32(&bars->q_empty), ph ^ 1u))) {
                 if (lane == 0) timed_out();
                 break;
             }
             ph ^= 1u;
-            const int rows = t.b.rows > 128 ? 256 : 128;  // of the halves that have any
-            for (int i = threadIdx.x - 32 * kQueryWarp; i < rows * (D / 8); i += 32 * kQueryWarps) {
-                const int r = i / (D / 8), k = i % (D / 8);
+            // a lane has one 16-byte piece of every kStep-th row of the halves that have any
+            constexpr int kPieces = D / 8, kStep = 32 * kQueryWarps / kPieces;
+            const int id = threadIdx.x - 32 * kQueryWarp, k = id % kPieces, rows = t.b.rows > 128 ? 256 : 128;
+            int row = t.b.row0 + id / kPieces, tok = row / p.group, x = row % p.group;
+            const uint16_t* src = p.q + ((size_t)t.b.q0 * p.n_heads + (size_t)t.b.head * p.group) * D + k * 8;
+#pragma unroll 4
+            for (int r = id / kPieces; r < rows; r += kStep) {
+                const bool there = r < t.b.rows;
                 cp_async16_or_zero(smem_u32(smem) + r / 128 * T::kQHalf + swz(r % 128, k, 128),
-                                   p.q + block_row(p, t.b, min(r, t.b.rows - 1), D) + k * 8, r < t.b.rows);
+                                   src + (there ? ((size_t)tok * p.n_heads + x) * D : 0), there);
+                for (x += kStep; x >= p.group; x -= p.group) ++tok;
             }
             cp_async_wait_all();
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -180,70 +200,68 @@ __global__ void __launch_bounds__(kTileThreads, 1) cross_tiles_kernel(const __gr
         }
     } else if (warp == kMmaWarp) {
         // ------------------------------ products ------------------------------
-        if (lane == 0) {
-            constexpr uint32_t kShapeS = f16_shape(T::kKeys, false), kShapeO = f16_shape(D, true);
-            const uint32_t q_at = smem_u32(smem), st_at = smem_u32(stages);
-            int it = 0;
-            uint32_t q_ph = 0u, p_ph = 0u;                // (both halves' barriers: one bit each)
-            bool ok = true;
-            auto wait = [&](uint64_t* bar, uint32_t parity) {
-                if (ok && !mbar_wait(smem_u32(bar), parity)) {
-                    timed_out();
-                    ok = false;
-                }
-                tc_fence_after();
-                return ok;
-            };
-            auto scores = [&](int h, int st) {
-                const uint32_t a = q_at + h * T::kQHalf, b = st_at + st * T::kStage, d = tmem + T::kS + h * T::kKeys;
+        // (the whole warp runs this: mma_ss)
+        constexpr uint32_t kShapeS = f16_shape(T::kKeys, false), kShapeO = f16_shape(D, true);
+        const uint32_t q_desc = desc_along_row(smem_u32(smem)), k_desc = desc_along_row(smem_u32(stages)),
+                       v_desc = desc_along_rows(smem_u32(stages), T::kSlab);
+        int st = 0;                                       // the stage whose turn it is, and its parity
+        uint32_t st_ph = 0u, q_ph = 0u, p_ph = 0u;        // (p_ph: a bit for each half)
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            ok = __all_sync(kFull, mbar_wait(smem_u32(bar), parity));
+            if (!ok && lane == 0) timed_out();
+            tc_fence_after();
+            return ok;
+        };
+        auto scores = [&](int h, int stage) {
+            const uint32_t a = q_desc + h * (T::kQHalf >> 4), b = k_desc + stage * (T::kStage >> 4);
+            const uint32_t d = tmem + T::kS + h * T::kKeys;
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    mma_ss(d, desc_along_row(a + k / 4 * T::kQSlab + k % 4 * 32), desc_along_row(b + k / 4 * T::kSlab + k % 4 * 32),
-                           kShapeS, k > 0);
-                mma_commit(smem_u32(&bars->s_full[h]));
-            };
-            for (int round = 0; ok; ++round) {
-                const int idx = item_of(round);
-                if (idx < 0) break;
-                const TileItem t = tile_item<C, D>(p, idx);
-                if (t.steps == 0) continue;
-                const int halves = t.b.rows > 128 ? 2 : 1;
-                if (!wait(&bars->q_full, q_ph)) break;
-                q_ph ^= 1u;
-                if (!wait(&bars->full[it % T::kStages], (uint32_t)(it / T::kStages) & 1u)) break;
-                for (int h = 0; h < halves; ++h) scores(h, it % T::kStages);
-                mma_commit(smem_u32(&bars->empty[it % T::kStages]));
-                if (t.steps == 1) mma_commit(smem_u32(&bars->q_empty));
-                ++it;
-                for (int j = 0; j < t.steps; ++j) {
-                    const int sv = it % T::kStages, sk = (it + 1) % T::kStages;
-                    const bool more = j + 1 < t.steps;
-                    for (int h = 0; h < halves; ++h) {
-                        if (!wait(&bars->p_full[h], (p_ph >> h) & 1u)) break;
-                        p_ph ^= 1u << h;
-                        if (h == 0 && !wait(&bars->full[sv], (uint32_t)(it / T::kStages) & 1u)) break;
-                        const uint32_t a = tmem + T::kS + h * T::kKeys, b = st_at + sv * T::kStage, d = tmem + T::kO + h * D;
+            for (int k = 0; k < D / 16; ++k)
+                mma_ss<kShapeS>(d, a + k / 4 * (T::kQSlab >> 4) + k % 4 * 2, b + k / 4 * (T::kSlab >> 4) + k % 4 * 2, k > 0);
+            mma_commit(smem_u32(&bars->s_full[h]));
+        };
+        for (ItemWalk<C, D> walk(p); ok && walk.idx >= 0; walk.advance()) {
+            const TileItem& t = walk.t;
+            if (t.steps == 0) continue;
+            const int halves = t.b.rows > 128 ? 2 : 1;
+            if (!wait(&bars->q_full, q_ph)) break;
+            q_ph ^= 1u;
+            if (!wait(&bars->full[st], st_ph)) break;
+            for (int h = 0; h < halves; ++h) scores(h, st);
+            mma_commit(smem_u32(&bars->empty[st]));
+            if (t.steps == 1) mma_commit(smem_u32(&bars->q_empty));
+            for (int j = 0; j < t.steps; ++j) {
+                const bool more = j + 1 < t.steps;
+                if (++st == T::kStages) { st = 0; st_ph ^= 1u; }
+                const int sv = st;                        // this step's values, then the next one's keys
+                const uint32_t sv_ph = st_ph;
+                if (more && ++st == T::kStages) { st = 0; st_ph ^= 1u; }
+                for (int h = 0; h < halves; ++h) {
+                    if (!wait(&bars->p_full[h], (p_ph >> h) & 1u)) break;
+                    p_ph ^= 1u << h;
+                    if (h == 0 && !wait(&bars->full[sv], sv_ph)) break;
+                    const uint32_t b = v_desc + sv * (T::kStage >> 4);
+                    const uint32_t a = tmem + T::kS + h * T::kKeys, d = tmem + T::kO + h * D;
 #pragma unroll
-                        for (int k = 0; k < T::kKeys / 16; ++k)
-                            mma_ts(d, a + 8 * k, desc_along_rows(b + k * 2048, T::kSlab), kShapeO, j > 0 || k > 0);
-                        if (more) {
-                            if (h == 0 && !wait(&bars->full[sk], (uint32_t)((it + 1) / T::kStages) & 1u)) break;
-                            scores(h, sk);
-                        } else {
-                            mma_commit(smem_u32(&bars->o_full[h]));
-                        }
+                    for (int k = 0; k < T::kKeys / 16; ++k) mma_ts<kShapeO>(d, a + 8 * k, b + k * (2048 >> 4), j > 0 || k > 0);
+                    if (more) {
+                        if (h == 0 && !wait(&bars->full[st], st_ph)) break;
+                        scores(h, st);
+                    } else {
+                        mma_commit(smem_u32(&bars->o_full[h]));
                     }
-                    if (!ok) break;
-                    mma_commit(smem_u32(&bars->empty[sv]));
-                    if (more) mma_commit(smem_u32(&bars->empty[sk]));
-                    if (j + 2 == t.steps) mma_commit(smem_u32(&bars->q_empty));
-                    it += more ? 2 : 1;
                 }
+                if (!ok) break;
+                mma_commit(smem_u32(&bars->empty[sv]));
+                if (more) mma_commit(smem_u32(&bars->empty[st]));
+                if (j + 2 == t.steps) mma_commit(smem_u32(&bars->q_empty));
             }
-            // everything issued is done before the CTA can end
-            mma_commit(smem_u32(&bars->drain));
-            mbar_wait(smem_u32(&bars->drain), 0u);
+            if (ok && ++st == T::kStages) { st = 0; st_ph ^= 1u; }
         }
+        // everything issued is done before the CTA can end
+        mma_commit(smem_u32(&bars->drain));
+        mbar_wait(smem_u32(&bars->drain), 0u);
         __syncwarp();
     } else if (warp < 4 * T::kHalves) {
         // ------------------------------ softmax ------------------------------
@@ -254,6 +272,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) cross_tiles_kernel(const __gr
         // a negative scale turns the scores' signs; with 0 all scores are alike
         const float scale = fmaxf(fabsf(p.scale_log2), 1e-37f);
         const bool turned = p.scale_log2 < 0.f;
+        const uint64_t scale2 = pair_of(__float_as_uint(scale), __float_as_uint(scale));
+        auto largest = [](const uint32_t (&x)[32]) {
+            float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int e = 0; e < 32; e += 2)
+                a[(e >> 1) & 3] = fmaxf(a[(e >> 1) & 3], fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
+            return fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
+        };
         uint32_t s_ph = 0u, o_ph = 0u;
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -262,10 +288,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) cross_tiles_kernel(const __gr
             tc_fence_after();
             return ok;
         };
-        for (int round = 0; ok; ++round) {
-            const int idx = item_of(round);
-            if (idx < 0) break;
-            const TileItem t = tile_item<C, D>(p, idx);
+        for (ItemWalk<C, D> walk(p); ok && walk.idx >= 0; walk.advance()) {
+            const TileItem& t = walk.t;
             if (128 * h >= t.b.rows) continue;
             // the last token that the row sees (a row past the tile's last: all)
             int last = t.n - 1;
@@ -275,70 +299,89 @@ __global__ void __launch_bounds__(kTileThreads, 1) cross_tiles_kernel(const __gr
             for (int j = 0; j < t.steps; ++j) {
                 if (!wait(&bars->s_full[h], s_ph)) break;
                 s_ph ^= 1u;
-                constexpr int NC = T::kKeys / 32;
-                uint32_t x[NC][32];
+                constexpr int NC = T::kKeys / 32;         // 32 columns at a time
+                if (turned || t.b.c_begin * C + (j + 1) * T::kKeys - 1 > all_see) {
+                    // few steps need it: signs turned and hidden tokens masked in place
+                    const int see = last - (t.b.c_begin * C + j * T::kKeys);
+#pragma unroll 1
+                    for (int c = 0; c < NC; ++c) {
+                        uint32_t x[32];
+                        tmem_ld32(s_at + 32 * c, x);
+                        tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < NC; ++c) tmem_ld32(s_at + 32 * c, x[c]);
-                tmem_wait_ld();
-                const int t0 = t.b.c_begin * C + j * T::kKeys;
-                if (turned) {
-#pragma unroll
-                    for (int c = 0; c < NC; ++c)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) x[c][e] ^= 0x80000000u;
+                        for (int e = 0; e < 32; ++e) x[e] = 32 * c + e > see ? 0xff800000u : turned ? x[e] ^ 0x80000000u : x[e];
+                        tmem_st32(s_at + 32 * c, x);
+                    }
+                    tmem_wait_st();
                 }
-                if (t0 + T::kKeys - 1 > all_see) {
-                    const int see = last - t0;
+                // The weights 2^(x - m), with the reference m that the steps before have
+                // left, and beside them the largest score.  Only where that exceeds m by
+                // more than 8 (weights stay below 256, exact enough in fp16) the reference
+                // rises, by a whole number, so that scaling the outputs rounds nothing, and
+                // the weights are taken again: the scores are overwritten after this check.
+                uint64_t add[2] = {0ull, 0ull};
+                auto weigh = [&](const uint32_t (&x)[32], uint32_t* w) {
+                    const float mu = m == -INFINITY ? 0.f : m;
+                    const uint64_t mu2 = pair_of(__float_as_uint(-mu), __float_as_uint(-mu));
 #pragma unroll
-                    for (int c = 0; c < NC; ++c)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (32 * c + e > see) x[c][e] = 0xff800000u;
-                }
+                    for (int e = 0; e < 16; ++e) {
+                        uint32_t lo, hi;
+                        halves_of(fma2(pair_of(x[2 * e], x[2 * e + 1]), scale2, mu2), lo, hi);
+                        const float a = ex2(__uint_as_float(lo)), b = ex2(__uint_as_float(hi));
+                        w[e] = pack_half2(a, b);
+                        add[e & 1] = add2(add[e & 1], pair_of(__float_as_uint(a), __float_as_uint(b)));
+                    }
+                };
+                uint32_t w[NC / 2][32];
                 float top = -INFINITY;
+                {
+                    uint32_t x[2][32];
+                    tmem_ld32(s_at, x[0]);
 #pragma unroll
-                for (int c = 0; c < NC; ++c)
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(x[c][e]));
-                // The reference maximum rises only when it falls short by more than 2^8
-                // (weights then stay below 256, exact enough in fp16), so that the
-                // outputs are hardly ever scaled.
+                    for (int c = 0; c < NC; ++c) {
+                        tmem_wait_ld();
+                        if (c + 1 < NC) tmem_ld32(s_at + 32 * (c + 1), x[(c + 1) & 1]);
+                        top = fmaxf(top, largest(x[c & 1]));
+                        weigh(x[c & 1], &w[c / 2][c % 2 * 16]);
+                    }
+                }
                 top *= scale;
                 const bool rise = top > m + 8.f;
-                if (__any_sync(kFull, rise)) {
-                    const float a = rise ? ex2(m - top) : 1.f;
-                    if (rise) m = top;
+                if (!__any_sync(kFull, rise)) {
+#pragma unroll
+                    for (int c = 0; c < NC / 2; ++c) tmem_st32(s_at + 32 * c, w[c]);
+                } else {
+                    const float up = ceilf(top), a = rise ? ex2(m - up) : 1.f;
+                    if (rise) m = up;
                     sum *= a;
                     if (j > 0) {                          // (the scores' barrier says that the step before is in)
 #pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
+                        for (int d = 0; d < D / 32; ++d) {
                             uint32_t o[32];
-                            tmem_ld32(o_at + 32 * c, o);
+                            tmem_ld32(o_at + 32 * d, o);
                             tmem_wait_ld();
 #pragma unroll
                             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-                            tmem_st32(o_at + 32 * c, o);
+                            tmem_st32(o_at + 32 * d, o);
                         }
                     }
-                }
-                const float mu = m == -INFINITY ? 0.f : m;
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) x[c][e] = __float_as_uint(ex2(fmaf(__uint_as_float(x[c][e]), scale, -mu)));
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) w[e] = pack_half2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1]));
-                    tmem_st16(s_at + 16 * c, w);
+                    add[0] = add[1] = 0ull;
+#pragma unroll 1
+                    for (int c = 0; c < NC; ++c) {        // (P's columns 16 c .. + 15 held scores that have been read)
+                        uint32_t x[32], y[16];
+                        tmem_ld32(s_at + 32 * c, x);
+                        tmem_wait_ld();
+                        weigh(x, y);
+                        tmem_st16(s_at + 16 * c, y);
+                    }
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[h]));
-#pragma unroll
-                for (int c = 0; c < NC; ++c)
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) sum += __uint_as_float(x[c][e]);
+                uint32_t lo, hi;
+                halves_of(add2(add[0], add[1]), lo, hi);
+                sum += __uint_as_float(lo) + __uint_as_float(hi);
             }
             if (!ok) break;
             if (t.steps > 0) {

@@ -36,6 +36,14 @@ __device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t (&r)[32]) {
         : "r"(at)
         : "memory");
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at)
+        : "memory");
+}
 __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
@@ -55,48 +63,78 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) 
         : "memory");
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair_of(uint32_t lo, uint32_t hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ void halves_of(uint64_t v, uint32_t& lo, uint32_t& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 // ---------------------------------------------------------------------------
 // Operands.  A tile in shared memory is one or more slabs of 64 columns (128
 // bytes a row, rows behind one another), each swizzled as TMA's SWIZZLE_128B
 // leaves it (swz above), 1024-byte aligned.
 // ---------------------------------------------------------------------------
-// Descriptor: address, leading and stride offsets in 16-byte units, version 1,
-// 128-byte swizzle.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t leading, uint32_t stride) {
-    return (uint64_t)((addr & 0x3ffffu) >> 4) | ((uint64_t)(leading >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) |
-           (1ull << 46) | (2ull << 61);
-}
-// The product runs along a row (keys against queries): 16 columns are 32 bytes
-// on, groups of 8 rows 1024 bytes apart.
-__device__ __forceinline__ uint64_t desc_along_row(uint32_t addr) { return smem_desc(addr, 16, 1024); }
+// Descriptors.  Their upper words are constants: stride between groups of 8 rows
+// 1024 bytes, version 1, 128-byte swizzle; the lower word is the address and the
+// leading offset in 16-byte units.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+// The product runs along a row (keys against queries): 16 columns are 32 bytes on.
+__device__ __forceinline__ uint32_t desc_along_row(uint32_t addr) { return (addr >> 4) | (1u << 16); }
 // It runs along the rows (values, by tokens): slabs of 64 columns are `slab`
-// bytes apart, groups of 8 rows 1024; 16 rows are 2048 bytes on.
-__device__ __forceinline__ uint64_t desc_along_rows(uint32_t addr, uint32_t slab) { return smem_desc(addr, slab, 1024); }
+// bytes apart; 16 rows are 2048 bytes on.
+__device__ __forceinline__ uint32_t desc_along_rows(uint32_t addr, uint32_t slab) { return (addr >> 4) | (slab >> 4 << 16); }
 
 // fp16 operands, fp32 accumulator, 128 rows by n columns; b_rows: B's product
 // runs along its rows.
 __host__ __device__ constexpr uint32_t f16_shape(int n, bool b_rows) {
     return (1u << 4) | (b_rows ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
-// d (tensor memory) = a b, or d + a b; a and b in shared memory.  One thread issues.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add) {
+// d (tensor memory) = a b, or d + a b (add); a and b in shared memory.  A whole
+// warp runs these with the same arguments, and one of its threads, always the
+// same, issues.
+template <uint32_t SHAPE>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(shape), "r"((uint32_t)add)
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 x, y;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %3, 0;\n\t"
+        "mov.b64 x, {%1, %4};\n\tmov.b64 y, {%2, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"((uint32_t)add), "n"(kDescHigh), "n"(SHAPE)
         : "memory");
 }
 // The same with a in tensor memory, two fp16 values to a column.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t shape, bool add) {
+template <uint32_t SHAPE>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(shape), "r"((uint32_t)add)
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 y;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %3, 0;\n\t"
+        "mov.b64 y, {%2, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %5, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"((uint32_t)add), "n"(kDescHigh), "n"(SHAPE)
         : "memory");
 }
-// The barrier is arrived at once when everything this thread issued before is done.
+// The barrier is arrived at once when everything that thread issued before is done.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+        : "memory");
 }
 
 }  // namespace dev
