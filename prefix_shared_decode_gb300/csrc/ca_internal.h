@@ -79,7 +79,7 @@ struct PlanLayout {
     size_t list_off, list_slots;   // CA_SCHED_CHUNK_LISTS: each batch row's chunk slots (CSR)
     size_t list_count, list_count_bytes;   // and a counter per unit of the listed chunks' attention
     size_t tok_base;               // [b + 1] chunks of the positions before each one (CSR)
-    size_t q_off, items, joins;    // schedules of query blocks (BlockItem, BlockJoin)
+    size_t q_off, items, joins, cta_begin;   // schedules of query blocks (BlockItem, BlockJoin)
     size_t total;
 };
 
@@ -255,7 +255,7 @@ struct Sched {
     std::vector<BlockItem> items;
     std::vector<BlockJoin> joins;
     int64_t q_rows = 0;                // query tokens of all blocks
-    int32_t n_parts = 0, tile_rows = 0;
+    int32_t n_parts = 0, tile_rows = 0, n_places = 0;
     Tables t;
     Tables t_next;                     // rebuilt into, then swapped with t
     Plan plan;

@@ -266,7 +266,8 @@ int launch_cross(const Pool& p, const Sched& s, int32_t layer, const void* q, vo
     a.tile_rows = s.tile_rows;
     a.scale_log2 = scale * 1.4426950408889634f * (quant ? kv_scale_of(c.k_scale) : 1.f);
     a.out_scale = quant ? kv_scale_of(c.v_scale) : 1.f;
-    a.n_items = (int32_t)s.items.size();
+    a.cta_begin = reinterpret_cast<const int32_t*>(dev8 + s.layout.cta_begin);
+    a.n_places = s.n_places;
     if (s.items.empty()) return CA_OK;
     if (s.stall_calls > 0) {
         a.test_stall = 1;

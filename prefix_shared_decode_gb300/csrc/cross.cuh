@@ -15,6 +15,7 @@ struct CrossParams {
     uint16_t* out;
     const BlockItem* items;
     const BlockJoin* joins;
+    const int32_t* cta_begin;     // [places + 1] items of each place
     const int32_t* q_off;         // [b + 1] first row of each block
     const int32_t* list_slots;
     const int32_t* slot_ntok;
@@ -22,7 +23,7 @@ struct CrossParams {
     int32_t* status;
     float* part_o;                // [parts][tile rows][D]
     float2* part_ms;              // [parts][tile rows]
-    int32_t n_layers, n_heads, n_kv_heads, group, layer, capacity, causal, tile_rows, n_items;
+    int32_t n_layers, n_heads, n_kv_heads, group, layer, capacity, causal, tile_rows, n_places;
     int32_t test_stall;           // test hook: waits that run out (kernels that wait)
     float scale_log2, out_scale;
 };

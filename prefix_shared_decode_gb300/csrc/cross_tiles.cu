@@ -59,26 +59,22 @@ __device__ __forceinline__ TileItem tile_item(const CrossParams& p, int idx) {
     return t;
 }
 
-// A CTA's items in turn, every other round backwards (they are listed by falling
-// length); what there is to know of the next one is on its way beforehand.
+// A CTA's items in turn; what there is to know of the next one is on its way
+// beforehand.
 template <int C, int D>
 struct ItemWalk {
     const CrossParams& p;
-    int round = 0, idx, next_idx;
+    int idx, end;
     TileItem t, next;
-    __device__ __forceinline__ explicit ItemWalk(const CrossParams& p_) : p(p_), idx(at(0)), next_idx(at(1)) {
-        if (idx >= 0) t = tile_item<C, D>(p, idx);
-        if (next_idx >= 0) next = tile_item<C, D>(p, next_idx);
+    __device__ __forceinline__ explicit ItemWalk(const CrossParams& p_)
+        : p(p_), idx(p_.cta_begin[blockIdx.x]), end(p_.cta_begin[blockIdx.x + 1]) {
+        if (idx < end) t = tile_item<C, D>(p, idx);
+        if (idx + 1 < end) next = tile_item<C, D>(p, idx + 1);
     }
-    __device__ __forceinline__ int at(int r) const {
-        const long long i = (long long)r * gridDim.x + ((r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        return i < p.n_items ? (int)i : -1;
-    }
+    __device__ __forceinline__ bool more() const { return idx < end; }
     __device__ __forceinline__ void advance() {
-        idx = next_idx;
         t = next;
-        next_idx = at(++round + 1);
-        if (next_idx >= 0) next = tile_item<C, D>(p, next_idx);
+        if (++idx + 1 < end) next = tile_item<C, D>(p, idx + 1);
     }
 };
 
@@ -132,7 +128,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cross_tiles_kernel(const __gr
             if (lane == 0 && !mbar_wait(smem_u32(&bars->full[0]), 0u)) timed_out();
             ok = false;
         }
-        for (ItemWalk<C, D> walk(p); ok && walk.idx >= 0; walk.advance()) {
+        for (ItemWalk<C, D> walk(p); ok && walk.more(); walk.advance()) {
             const TileItem& t = walk.t;
             const int32_t* slots = p.list_slots + t.b.list0;
             // A lane per chunk.  Past the item's last chunk that one comes again: its
@@ -173,7 +169,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cross_tiles_kernel(const __gr
     } else if (warp >= kQueryWarp && warp < kQueryWarp + kQueryWarps) {
         // ------------------------------ queries ------------------------------
         uint32_t ph = 0u;
-        for (ItemWalk<C, D> walk(p); walk.idx >= 0; walk.advance()) {
+        for (ItemWalk<C, D> walk(p); walk.more(); walk.advance()) {
             const TileItem& t = walk.t;
             if (t.steps == 0) continue;
             if (!__all_sync(kFull, mbar_wait(smem_u32(&bars->q_empty), ph ^ 1u))) {
@@ -221,7 +217,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cross_tiles_kernel(const __gr
                 mma_ss<kShapeS>(d, a + k / 4 * (T::kQSlab >> 4) + k % 4 * 2, b + k / 4 * (T::kSlab >> 4) + k % 4 * 2, k > 0);
             mma_commit(smem_u32(&bars->s_full[h]));
         };
-        for (ItemWalk<C, D> walk(p); ok && walk.idx >= 0; walk.advance()) {
+        for (ItemWalk<C, D> walk(p); ok && walk.more(); walk.advance()) {
             const TileItem& t = walk.t;
             if (t.steps == 0) continue;
             const int halves = t.b.rows > 128 ? 2 : 1;
@@ -288,7 +284,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cross_tiles_kernel(const __gr
             tc_fence_after();
             return ok;
         };
-        for (ItemWalk<C, D> walk(p); ok && walk.idx >= 0; walk.advance()) {
+        for (ItemWalk<C, D> walk(p); ok && walk.more(); walk.advance()) {
             const TileItem& t = walk.t;
             if (128 * h >= t.b.rows) continue;
             // the last token that the row sees (a row past the tile's last: all)
@@ -440,7 +436,7 @@ int run(const Pool& p, const dev::CrossParams& a, cudaStream_t s) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t c = {};
-    c.gridDim = dim3((unsigned)(a.n_items < p.sms ? a.n_items : p.sms));
+    c.gridDim = dim3((unsigned)a.n_places);
     c.blockDim = dim3(dev::kTileThreads);
     c.dynamicSmemBytes = bytes;
     c.stream = s;
