@@ -1,11 +1,13 @@
-// Query blocks of an fp16 pool on the 5th-generation tensor cores: tiles of 256
-// rows (128 at head_dim 256) against 128 (64) keys at a time.
+// Query blocks on the 5th-generation tensor cores: tiles of 256 rows (128 at
+// head_dim 256) against 128 (64) keys at a time.
 //
-// One CTA per SM walks the schedule's items.  Its warps:
+// One CTA per SM walks its items.  Its warps:
 //   0-3, 4-7  the softmax of the tile's two halves of 128 rows, one thread a row
 //   8         issues every product: S = Q K^T and O += P V
 //   9         brings chunks' keys and values in (TMA)
 //   10, 11    bring the next tile's queries in
+//   12-15     pools of 8 and 4 bits: widen the chunks to fp16 (values in units of
+//             the pool's scales, exact), from a ring of their own
 // S, P and O stay in tensor memory; P takes the place of the scores it came from.
 // While one half is in its softmax, the other half's products run: per step of
 // 128 keys and half, 2 x 128 x 128 x D multiply-adds and 16 K exponentials.
@@ -15,76 +17,170 @@
 #include <climits>
 
 #include "cross.cuh"
+#include "fp4.cuh"
 #include "tcgen05.cuh"
 
 namespace ca {
 namespace dev {
 
-constexpr int kTileThreads = 384, kTmemColumns = 512;
-constexpr int kMmaWarp = 8, kChunkWarp = 9, kQueryWarp = 10, kQueryWarps = 2;
-
-template <int D>
+constexpr int kTmemColumns = 512;
+constexpr int kMmaWarp = 8, kChunkWarp = 9, kQueryWarp = 10, kQueryWarps = 2, kWidenWarp = 12, kWidenWarps = 4;
+// EB: bytes of a stored element (0: the 4-bit codes).
+template <int D, int EB>
 struct TileShape {
+    static constexpr bool kWiden = EB != 2;
+    static constexpr int kThreads = kWiden ? 512 : 384;
+    // Registers: 128 a thread at launch (168 with 12 warps); the softmax's warps take
+    // what the others give.
+    static constexpr int kLaunchRegs = kWiden ? 128 : 168, kSoftmaxRegs = kWiden ? 168 : 200, kOtherRegs = kWiden ? 88 : 104;
+    static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs == kThreads * kLaunchRegs, "as many as at launch");
     static constexpr int kHalves = D == 256 ? 1 : 2;
     static constexpr int kKeys = D == 256 ? 64 : 128;             // of a step
-    static constexpr int kSlab = kKeys * 128, kStage = D / 64 * kSlab;   // K or V of a step
+    static constexpr int kSlab = kKeys * 128, kStage = D / 64 * kSlab;   // K or V of a step, fp16
     static constexpr int kQSlab = 128 * 128, kQHalf = D / 64 * kQSlab;
-    static constexpr int kStages = D == 64 ? 8 : 5;
+    static constexpr int kStages = D == 64 ? 8 : kWiden ? 4 : 5;
+    // as the pool holds them: E4M3 rows, swizzled; codes, then scales
+    static constexpr int kRaw = EB == 1 ? kKeys * D : EB == 0 ? kKeys * (D / 2 + D / 16) : 0;
+    static constexpr int kRawStages = EB == 1 ? 2 : EB == 0 ? 3 : 0;
     static constexpr int kO = 0, kS = kHalves * D;                // columns: outputs, then scores, half by half
-    static constexpr int kBytes = kHalves * kQHalf + kStages * kStage + 256;
+    static constexpr int kBytes = kHalves * kQHalf + kStages * kStage + kRawStages * kRaw + 512;
     static_assert(kS + kHalves * kKeys <= kTmemColumns && kBytes <= 227 * 1024, "fits an SM");
 };
 
 struct TileBars {
     uint64_t full[8], empty[8];           // a stage's K or V
+    uint64_t raw_full[4], raw_empty[4];   // the same as the pool holds it
     uint64_t q_full, q_empty;
     uint64_t s_full[2], p_full[2];        // a half's scores are there; its weights are
     uint64_t o_full[2];
     uint64_t drain;
     uint32_t tmem;
 };
-static_assert(sizeof(TileBars) <= 256, "room behind the stages");
+static_assert(sizeof(TileBars) <= 512, "room behind the stages");
 
 // What every role reads of an item.
 struct TileItem {
     BlockItem b;
     int n, steps;                         // tokens up to the item's last chunk, steps from c_begin on
 };
-template <int C, int D>
+template <int C, int KEYS>
 __device__ __forceinline__ TileItem tile_item(const CrossParams& p, int idx) {
     TileItem t;
     t.b = p.items[idx];
     t.n = min(tokens_now(p, t.b, C), t.b.c_end * C);
-    t.steps = max(0, (t.n - t.b.c_begin * C + TileShape<D>::kKeys - 1) / TileShape<D>::kKeys);
+    t.steps = max(0, (t.n - t.b.c_begin * C + KEYS - 1) / KEYS);
     return t;
 }
 
 // A CTA's items in turn; what there is to know of the next one is on its way
 // beforehand.
-template <int C, int D>
+template <int C, int KEYS>
 struct ItemWalk {
     const CrossParams& p;
     int idx, end;
     TileItem t, next;
     __device__ __forceinline__ explicit ItemWalk(const CrossParams& p_)
         : p(p_), idx(p_.cta_begin[blockIdx.x]), end(p_.cta_begin[blockIdx.x + 1]) {
-        if (idx < end) t = tile_item<C, D>(p, idx);
-        if (idx + 1 < end) next = tile_item<C, D>(p, idx + 1);
+        if (idx < end) t = tile_item<C, KEYS>(p, idx);
+        if (idx + 1 < end) next = tile_item<C, KEYS>(p, idx + 1);
     }
     __device__ __forceinline__ bool more() const { return idx < end; }
     __device__ __forceinline__ void advance() {
         t = next;
-        if (++idx + 1 < end) next = tile_item<C, D>(p, idx + 1);
+        if (++idx + 1 < end) next = tile_item<C, KEYS>(p, idx + 1);
     }
 };
 
-template <int C, int D>
-__global__ void __launch_bounds__(kTileThreads, 1) cross_tiles_kernel(const __grid_constant__ CUtensorMap tmap,
-                                                                      const CrossParams p) {
-    using T = TileShape<D>;
+// A stage as the pool holds it, widened into swizzled fp16 slabs by the threads
+// of kWidenWarps warps.  Which lane has which piece keeps loads and stores of
+// 8-bit rows free of bank conflicts (rows r and r ^ 5 beside each other) and those
+// of 4-bit ones two to a bank at most.
+template <int D, int EB, int KEYS>
+__device__ __forceinline__ void widen(const uint8_t* raw, uint8_t* dst, bool values, int warp, int lane) {
+    if constexpr (EB == 1) {
+        const int r0 = (lane >> 3) ^ ((lane >> 2 & 1) * 5), k0 = lane & 3;
+#pragma unroll 4
+        for (int i = warp; i < KEYS / 8 * (D / 64); i += kWidenWarps) {
+            const int r = i / (D / 64) * 8 + r0, k = i % (D / 64) * 4 + k0;     // 16 dims of a row
+            const uint4 x = *reinterpret_cast<const uint4*>(raw + swz(r, k, KEYS));
+            uint32_t w[8];
+            const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t y[2];
+                f16x2_from_e4m3x4(in[j], y);
+                w[2 * j] = y[0];
+                w[2 * j + 1] = y[1];
+            }
+            *reinterpret_cast<uint4*>(dst + swz(r, 2 * k, KEYS)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(dst + swz(r, 2 * k + 1, KEYS)) = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+    } else if (!values) {
+        // codes of a row: its dims 16 b + 4 t + 0 .. 3 of all blocks b are D / 8 bytes
+        const int t = lane & 3;
+#pragma unroll 2
+        for (int m = warp * 8 + (lane >> 2); m < KEYS; m += 8 * kWidenWarps) {
+            const int r = f4_token(m);
+            uint32_t c[D / 32], s[D / 64];
+            lds_words<D / 32>(raw + m * (D / 2) + t * (D / 8), c);
+            lds_words<D / 64>(raw + KEYS * (D / 2) + m * (D / 16), s);
+#pragma unroll
+            for (int b4 = 0; b4 < D / 64; ++b4) {
+                uint32_t h[2];
+                f16x2_from_e4m3x4(s[b4], h);
+#pragma unroll
+                for (int b2 = 0; b2 < 2; ++b2) {          // two blocks: a word of codes
+                    uint32_t x[4];
+                    f16x2_from_e2m1x8(c[2 * b4 + b2], x);
+                    const uint32_t lo = __byte_perm(h[b2], h[b2], 0x1010), hi = __byte_perm(h[b2], h[b2], 0x3232);
+                    const int k = 2 * (4 * b4 + 2 * b2) + (t >> 1);
+                    *reinterpret_cast<uint2*>(dst + swz(r, k, KEYS) + 8 * (t & 1)) = make_uint2(mul_f16x2(x[0], lo), mul_f16x2(x[1], lo));
+                    *reinterpret_cast<uint2*>(dst + swz(r, k + 2, KEYS) + 8 * (t & 1)) =
+                        make_uint2(mul_f16x2(x[2], hi), mul_f16x2(x[3], hi));
+                }
+            }
+        }
+    } else {
+        // pairs of tokens r, r + 4 to a byte: dims 16 b + 2 g of all blocks b, then 16 b + 2 g + 1
+        const int u = lane & 7;
+#pragma unroll 2
+        for (int pair = warp * 4 + (lane >> 3); pair < KEYS / 2; pair += 4 * kWidenWarps) {
+            const int g = f4_v_unit<D>(pair, u), r = (pair >> 2) * 8 + (pair & 3);
+            constexpr int NW = D / 64;
+            uint32_t c[2 * NW], s[D / 32];
+            lds_words<2 * NW>(raw + pair * D + u * (D / 8), c);
+            lds_words<D / 32>(raw + KEYS * (D / 2) + pair * (D / 8), s);
+#pragma unroll
+            for (int i = 0; i < NW; ++i) {                // four blocks to a word
+                uint32_t a[4], b[4];
+                f16x2_from_e2m1x8(c[i], a);
+                f16x2_from_e2m1x8(c[NW + i], b);
+#pragma unroll
+                for (int j2 = 0; j2 < 2; ++j2) {
+                    uint32_t h[2];
+                    f16x2_from_e4m3x4(s[2 * i + j2], h);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int j = 2 * j2 + e, k = 2 * (4 * i + j) + (g >> 2);
+                        const uint32_t x = mul_f16x2(a[j], h[e]), y = mul_f16x2(b[j], h[e]);
+                        *reinterpret_cast<uint32_t*>(dst + swz(r, k, KEYS) + 4 * (g & 3)) = __byte_perm(x, y, 0x5410);
+                        *reinterpret_cast<uint32_t*>(dst + swz(r + 4, k, KEYS) + 4 * (g & 3)) = __byte_perm(x, y, 0x7632);
+                    }
+                }
+            }
+        }
+    }
+}
+
+template <int C, int D, int EB>
+__global__ void __launch_bounds__(TileShape<D, EB>::kThreads, 1)
+cross_tiles_kernel(const __grid_constant__ CUtensorMap tmap, const CrossParams p) {
+    using T = TileShape<D, EB>;
+    using Walk = ItemWalk<C, T::kKeys>;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* stages = smem + T::kHalves * T::kQHalf;
-    TileBars* bars = reinterpret_cast<TileBars*>(stages + T::kStages * T::kStage);
+    uint8_t* raw = stages + T::kStages * T::kStage;
+    TileBars* bars = reinterpret_cast<TileBars*>(raw + T::kRawStages * T::kRaw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if ((smem_u32(smem) & 1023u) != 0) {                  // (the same for the whole CTA)
@@ -93,8 +189,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) cross_tiles_kernel(const __gr
     }
     if (threadIdx.x == 0) {
         for (int i = 0; i < T::kStages; ++i) {
-            mbar_init(smem_u32(&bars->full[i]), 1);
+            mbar_init(smem_u32(&bars->full[i]), T::kWiden ? kWidenWarps : 1);
             mbar_init(smem_u32(&bars->empty[i]), 1);
+        }
+        for (int i = 0; i < T::kRawStages; ++i) {
+            mbar_init(smem_u32(&bars->raw_full[i]), 1);
+            mbar_init(smem_u32(&bars->raw_empty[i]), kWidenWarps);
         }
         mbar_init(smem_u32(&bars->q_full), kQueryWarps);
         mbar_init(smem_u32(&bars->q_empty), 1);
@@ -120,15 +220,20 @@ __global__ void __launch_bounds__(kTileThreads, 1) cross_tiles_kernel(const __gr
 
     constexpr int kPer = T::kKeys / C;                    // chunks of a step
 
+    if (warp >= kMmaWarp) {
+    give_registers<T::kOtherRegs>();
     if (warp == kChunkWarp) {
         // ------------------------------ keys and values ------------------------------
+        constexpr int N = T::kWiden ? T::kRawStages : T::kStages;
+        uint64_t* const full = T::kWiden ? bars->raw_full : bars->full;
+        uint64_t* const empty = T::kWiden ? bars->raw_empty : bars->empty;
         int it = 0;
         bool ok = true;
         if (p.test_stall) {                               // test hook: a wait that nothing ends
-            if (lane == 0 && !mbar_wait(smem_u32(&bars->full[0]), 0u)) timed_out();
+            if (lane == 0 && !mbar_wait(smem_u32(&full[0]), 0u)) timed_out();
             ok = false;
         }
-        for (ItemWalk<C, D> walk(p); ok && walk.more(); walk.advance()) {
+        for (Walk walk(p); ok && walk.more(); walk.advance()) {
             const TileItem& t = walk.t;
             const int32_t* slots = p.list_slots + t.b.list0;
             // A lane per chunk.  Past the item's last chunk that one comes again: its
@@ -138,8 +243,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) cross_tiles_kernel(const __gr
             };
             int slot = slot_at(0);
             for (int x = 0; x < 2 * t.steps; ++x, ++it) { // K and V of each step
-                const int st = it % T::kStages;
-                if (!mbar_wait(smem_u32(&bars->empty[st]), ((uint32_t)(it / T::kStages) & 1u) ^ 1u)) ok = false;
+                const int st = it % N;
+                if (!mbar_wait(smem_u32(&empty[st]), ((uint32_t)(it / N) & 1u) ^ 1u)) ok = false;
                 ok = __all_sync(kFull, ok);
                 if (!ok) {
                     if (lane == 0) timed_out();
@@ -149,14 +254,22 @@ __global__ void __launch_bounds__(kTileThreads, 1) cross_tiles_kernel(const __gr
                     set_status(p.status, CA_ERR_DEVICE_BOUNDS);
                     slot = 0;
                 }
-                const int row = ((slot * p.n_layers + p.layer) * 2 * p.n_kv_heads + (x & 1) * p.n_kv_heads + t.b.head) * C;
-                const uint32_t fb = smem_u32(&bars->full[st]);
-                if (lane == 0) mbar_expect_tx_only(fb, T::kStage);
+                const uint32_t fb = smem_u32(&full[st]);
+                if (lane == 0) mbar_expect_tx_only(fb, T::kWiden ? T::kRaw : T::kStage);
                 __syncwarp();
                 if (lane < kPer) {
-                    const uint32_t dst = smem_u32(stages) + st * T::kStage + lane * C * 128;
+                    if constexpr (EB == 0) {
+                        using F = F4Tile<C, D>;
+                        const uint8_t* src = p.kv + (((long long)slot * p.n_layers + p.layer) * p.n_kv_heads + t.b.head) * F::kBytes;
+                        const uint32_t dst = smem_u32(raw) + st * T::kRaw;
+                        bulk_load(dst + lane * F::kCodes, src + (x & 1) * F::kCodes, F::kCodes, fb);
+                        bulk_load(dst + T::kKeys * (D / 2) + lane * F::kScales, src + F::kKScales + (x & 1) * F::kScales, F::kScales, fb);
+                    } else {
+                        const int row = ((slot * p.n_layers + p.layer) * 2 * p.n_kv_heads + (x & 1) * p.n_kv_heads + t.b.head) * C;
+                        const uint32_t dst = (T::kWiden ? smem_u32(raw) + st * T::kRaw : smem_u32(stages) + st * T::kStage) + lane * C * 128;
 #pragma unroll
-                    for (int s = 0; s < D / 64; ++s) tma_load_2d(dst + s * T::kSlab, &tmap, 64 * s, row, fb);
+                        for (int s = 0; s < D * EB / 128; ++s) tma_load_2d(dst + s * T::kSlab, &tmap, s * (128 / EB), row, fb);
+                    }
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(fb);
@@ -164,12 +277,38 @@ __global__ void __launch_bounds__(kTileThreads, 1) cross_tiles_kernel(const __gr
             }
         }
         if (!ok)                                          // copies in flight land before the CTA can end
-            for (int k = max(0, it - T::kStages); k < it; ++k)
-                mbar_wait(smem_u32(&bars->full[k % T::kStages]), (uint32_t)(k / T::kStages) & 1u);
+            for (int k = max(0, it - N); k < it; ++k) mbar_wait(smem_u32(&full[k % N]), (uint32_t)(k / N) & 1u);
+    } else if (T::kWiden && warp >= kWidenWarp) {
+        // ------------------------------ widening ------------------------------
+        if constexpr (T::kWiden) {
+            int st = 0, rs = 0;
+            uint32_t st_ph = 0u, rs_ph = 0u;
+            bool ok = true;
+            for (Walk walk(p); ok && walk.more(); walk.advance()) {
+                const int steps = walk.t.steps;
+                for (int x = 0; x < 2 * steps; ++x) {
+                    ok = __all_sync(kFull, mbar_wait(smem_u32(&bars->empty[st]), st_ph ^ 1u) &&
+                                               mbar_wait(smem_u32(&bars->raw_full[rs]), rs_ph));
+                    if (!ok) {
+                        if (lane == 0) timed_out();
+                        break;
+                    }
+                    widen<D, EB, T::kKeys>(raw + rs * T::kRaw, stages + st * T::kStage, (x & 1) != 0, warp - kWidenWarp, lane);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(smem_u32(&bars->full[st]));
+                        mbar_arrive(smem_u32(&bars->raw_empty[rs]));
+                    }
+                    if (++st == T::kStages) { st = 0; st_ph ^= 1u; }
+                    if (++rs == T::kRawStages) { rs = 0; rs_ph ^= 1u; }
+                }
+            }
+        }
     } else if (warp >= kQueryWarp && warp < kQueryWarp + kQueryWarps) {
         // ------------------------------ queries ------------------------------
         uint32_t ph = 0u;
-        for (ItemWalk<C, D> walk(p); walk.more(); walk.advance()) {
+        for (Walk walk(p); walk.more(); walk.advance()) {
             const TileItem& t = walk.t;
             if (t.steps == 0) continue;
             if (!__all_sync(kFull, mbar_wait(smem_u32(&bars->q_empty), ph ^ 1u))) {
@@ -217,7 +356,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cross_tiles_kernel(const __gr
                 mma_ss<kShapeS>(d, a + k / 4 * (T::kQSlab >> 4) + k % 4 * 2, b + k / 4 * (T::kSlab >> 4) + k % 4 * 2, k > 0);
             mma_commit(smem_u32(&bars->s_full[h]));
         };
-        for (ItemWalk<C, D> walk(p); ok && walk.more(); walk.advance()) {
+        for (Walk walk(p); ok && walk.more(); walk.advance()) {
             const TileItem& t = walk.t;
             if (t.steps == 0) continue;
             const int halves = t.b.rows > 128 ? 2 : 1;
@@ -259,7 +398,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) cross_tiles_kernel(const __gr
         mma_commit(smem_u32(&bars->drain));
         mbar_wait(smem_u32(&bars->drain), 0u);
         __syncwarp();
-    } else if (warp < 4 * T::kHalves) {
+    }
+    } else {
+    take_registers<T::kSoftmaxRegs>();
+    if (warp < 4 * T::kHalves) {
         // ------------------------------ softmax ------------------------------
         const int h = warp >> 2;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;          // 32 (warp % 4), in an address's upper half
@@ -284,7 +426,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cross_tiles_kernel(const __gr
             tc_fence_after();
             return ok;
         };
-        for (ItemWalk<C, D> walk(p); ok && walk.more(); walk.advance()) {
+        for (Walk walk(p); ok && walk.more(); walk.advance()) {
             const TileItem& t = walk.t;
             if (128 * h >= t.b.rows) continue;
             // the last token that the row sees (a row past the tile's last: all)
@@ -311,10 +453,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) cross_tiles_kernel(const __gr
                     tmem_wait_st();
                 }
                 // The weights 2^(x - m), with the reference m that the steps before have
-                // left, and beside them the largest score.  Only where that exceeds m by
-                // more than 8 (weights stay below 256, exact enough in fp16) the reference
-                // rises, by a whole number, so that scaling the outputs rounds nothing, and
-                // the weights are taken again: the scores are overwritten after this check.
+                // left, and beside them the largest score.  m is set 8 below a largest
+                // score (rounded up), and rises only where one exceeds it by more than 15:
+                // weights in fp16 stay below 2^15, and those that lose bits below 2^-14 are
+                // at most 2^-21 of the largest.  It rises by whole numbers, so that scaling
+                // the outputs rounds nothing; the step's weights are then taken again (the
+                // scores are overwritten after this check).
                 uint64_t add[2] = {0ull, 0ull};
                 auto weigh = [&](const uint32_t (&x)[32], uint32_t* w) {
                     const float mu = m == -INFINITY ? 0.f : m;
@@ -342,12 +486,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) cross_tiles_kernel(const __gr
                     }
                 }
                 top *= scale;
-                const bool rise = top > m + 8.f;
+                const bool rise = top > m + 15.f;
                 if (!__any_sync(kFull, rise)) {
 #pragma unroll
                     for (int c = 0; c < NC / 2; ++c) tmem_st32(s_at + 32 * c, w[c]);
                 } else {
-                    const float up = ceilf(top), a = rise ? ex2(m - up) : 1.f;
+                    const float up = ceilf(top) - 8.f, a = rise ? ex2(m - up) : 1.f;
                     if (rise) m = up;
                     sum *= a;
                     if (j > 0) {                          // (the scores' barrier says that the step before is in)
@@ -417,6 +561,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) cross_tiles_kernel(const __gr
             tc_fence_before();                            // (the next tile's first product overwrites the outputs)
         }
     }
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -427,43 +572,46 @@ __global__ void __launch_bounds__(kTileThreads, 1) cross_tiles_kernel(const __gr
 
 namespace {
 
-template <int C, int D>
+template <int C, int D, int EB>
 int run(const Pool& p, const dev::CrossParams& a, cudaStream_t s) {
-    constexpr int bytes = dev::TileShape<D>::kBytes;
-    if (cudaFuncSetAttribute(dev::cross_tiles_kernel<C, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    using T = dev::TileShape<D, EB>;
+    if (cudaFuncSetAttribute(dev::cross_tiles_kernel<C, D, EB>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kBytes) != cudaSuccess)
         return CA_ERR_CUDA;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3((unsigned)a.n_places);
-    c.blockDim = dim3(dev::kTileThreads);
-    c.dynamicSmemBytes = bytes;
+    c.blockDim = dim3(T::kThreads);
+    c.dynamicSmemBytes = T::kBytes;
     c.stream = s;
     c.attrs = attr;
     c.numAttrs = 1;
-    if (cudaLaunchKernelEx(&c, dev::cross_tiles_kernel<C, D>, *reinterpret_cast<const CUtensorMap*>(p.tmap), a) != cudaSuccess)
+    if (cudaLaunchKernelEx(&c, dev::cross_tiles_kernel<C, D, EB>, *reinterpret_cast<const CUtensorMap*>(p.tmap), a) != cudaSuccess)
         return CA_ERR_CUDA;
     count_launch();
     return CA_OK;
 }
 
-template <int D>
+template <int D, int EB>
 int pick(const Pool& p, const dev::CrossParams& a, cudaStream_t s) {
-    if (p.cfg.chunk == 16) return run<16, D>(p, a, s);
-    if (p.cfg.chunk == 32) return run<32, D>(p, a, s);
+    if (p.cfg.chunk == 16) return run<16, D, EB>(p, a, s);
+    if (p.cfg.chunk == 32) return run<32, D, EB>(p, a, s);
     if constexpr (D <= 128)
-        if (p.cfg.chunk == 64) return run<64, D>(p, a, s);
+        if (p.cfg.chunk == 64) return run<64, D, EB>(p, a, s);
     return CA_ERR_UNSUPPORTED;
 }
 
 }  // namespace
 
+int cross_tile_rows(const PoolCfg& c) { return c.head_dim == 256 ? 128 : 256; }
+int cross_places(const Pool& p) { return p.sms > 0 ? p.sms : 152; }
+
 int launch_cross_tiles(const Pool& p, const dev::CrossParams& a, cudaStream_t s) {
-    if (p.cfg.head_dim == 64) return pick<64>(p, a, s);
-    if (p.cfg.head_dim == 128) return pick<128>(p, a, s);
-    if (p.cfg.head_dim == 256) return pick<256>(p, a, s);
-    return CA_ERR_UNSUPPORTED;
+    const int D = p.cfg.head_dim;
+    if (p.cfg.flags & CA_KV_FP4) return D == 64 ? pick<64, 0>(p, a, s) : D == 128 ? pick<128, 0>(p, a, s) : CA_ERR_UNSUPPORTED;
+    if (p.cfg.flags & CA_KV_FP8) return D == 128 ? pick<128, 1>(p, a, s) : CA_ERR_UNSUPPORTED;
+    return D == 64 ? pick<64, 2>(p, a, s) : D == 128 ? pick<128, 2>(p, a, s) : D == 256 ? pick<256, 2>(p, a, s) : CA_ERR_UNSUPPORTED;
 }
 
 }  // namespace ca
