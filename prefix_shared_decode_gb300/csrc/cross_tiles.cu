@@ -38,19 +38,21 @@ struct TileShape {
     static constexpr int kKeys = D == 256 ? 64 : 128;             // of a step
     static constexpr int kSlab = kKeys * 128, kStage = D / 64 * kSlab;   // K or V of a step, fp16
     static constexpr int kQSlab = 128 * 128, kQHalf = D / 64 * kQSlab;
+    static constexpr int kQBuffers = D == 64 ? 2 : 1;             // the next tile's queries beside this one's
+    static constexpr int kQBytes = kHalves * kQHalf;
     static constexpr int kStages = D == 64 ? 8 : kWiden ? 4 : 5;
     // as the pool holds them: E4M3 rows, swizzled; codes, then scales
     static constexpr int kRaw = EB == 1 ? kKeys * D : EB == 0 ? kKeys * (D / 2 + D / 16) : 0;
     static constexpr int kRawStages = EB == 1 ? 2 : EB == 0 ? 3 : 0;
     static constexpr int kO = 0, kS = kHalves * D;                // columns: outputs, then scores, half by half
-    static constexpr int kBytes = kHalves * kQHalf + kStages * kStage + kRawStages * kRaw + 512;
+    static constexpr int kBytes = kQBuffers * kQBytes + kStages * kStage + kRawStages * kRaw + 512;
     static_assert(kS + kHalves * kKeys <= kTmemColumns && kBytes <= 227 * 1024, "fits an SM");
 };
 
 struct TileBars {
     uint64_t full[8], empty[8];           // a stage's K or V
     uint64_t raw_full[4], raw_empty[4];   // the same as the pool holds it
-    uint64_t q_full, q_empty;
+    uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], p_full[2];        // a half's scores are there; its weights are
     uint64_t o_full[2];
     uint64_t drain;
@@ -178,7 +180,7 @@ cross_tiles_kernel(const __grid_constant__ CUtensorMap tmap, const CrossParams p
     using T = TileShape<D, EB>;
     using Walk = ItemWalk<C, T::kKeys>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint8_t* stages = smem + T::kHalves * T::kQHalf;
+    uint8_t* stages = smem + T::kQBuffers * T::kQBytes;
     uint8_t* raw = stages + T::kStages * T::kStage;
     TileBars* bars = reinterpret_cast<TileBars*>(raw + T::kRawStages * T::kRaw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -196,8 +198,10 @@ cross_tiles_kernel(const __grid_constant__ CUtensorMap tmap, const CrossParams p
             mbar_init(smem_u32(&bars->raw_full[i]), 1);
             mbar_init(smem_u32(&bars->raw_empty[i]), kWidenWarps);
         }
-        mbar_init(smem_u32(&bars->q_full), kQueryWarps);
-        mbar_init(smem_u32(&bars->q_empty), 1);
+        for (int i = 0; i < T::kQBuffers; ++i) {
+            mbar_init(smem_u32(&bars->q_full[i]), kQueryWarps);
+            mbar_init(smem_u32(&bars->q_empty[i]), 1);
+        }
         for (int h = 0; h < 2; ++h) {
             mbar_init(smem_u32(&bars->s_full[h]), 1);
             mbar_init(smem_u32(&bars->p_full[h]), 4);
@@ -307,15 +311,15 @@ cross_tiles_kernel(const __grid_constant__ CUtensorMap tmap, const CrossParams p
         }
     } else if (warp >= kQueryWarp && warp < kQueryWarp + kQueryWarps) {
         // ------------------------------ queries ------------------------------
+        int qb = 0;
         uint32_t ph = 0u;
         for (Walk walk(p); walk.more(); walk.advance()) {
             const TileItem& t = walk.t;
             if (t.steps == 0) continue;
-            if (!__all_sync(kFull, mbar_wait(smem_u32(&bars->q_empty), ph ^ 1u))) {
+            if (!__all_sync(kFull, mbar_wait(smem_u32(&bars->q_empty[qb]), ph ^ 1u))) {
                 if (lane == 0) timed_out();
                 break;
             }
-            ph ^= 1u;
             // a lane has one 16-byte piece of every kStep-th row of the halves that have any
             constexpr int kPieces = D / 8, kStep = 32 * kQueryWarps / kPieces;
             const int id = threadIdx.x - 32 * kQueryWarp, k = id % kPieces, rows = t.b.rows > 128 ? 256 : 128;
@@ -324,14 +328,23 @@ cross_tiles_kernel(const __grid_constant__ CUtensorMap tmap, const CrossParams p
 #pragma unroll 4
             for (int r = id / kPieces; r < rows; r += kStep) {
                 const bool there = r < t.b.rows;
-                cp_async16_or_zero(smem_u32(smem) + r / 128 * T::kQHalf + swz(r % 128, k, 128),
+                cp_async16_or_zero(smem_u32(smem) + qb * T::kQBytes + r / 128 * T::kQHalf + swz(r % 128, k, 128),
                                    src + (there ? ((size_t)tok * p.n_heads + x) * D : 0), there);
                 for (x += kStep; x >= p.group; x -= p.group) ++tok;
+            }
+            if constexpr (T::kQBuffers == 1) {            // the next tile's into L2 meanwhile
+                if (walk.idx + 1 < walk.end) {
+                    const BlockItem& n = walk.next.b;
+                    constexpr int kLines = D / 64;        // 128 bytes each
+                    for (int i = id; i < n.rows * kLines; i += 32 * kQueryWarps)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + block_row(p, n, i / kLines, D) + i % kLines * 64));
+                }
             }
             cp_async_wait_all();
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars->q_full));
+            if (lane == 0) mbar_arrive(smem_u32(&bars->q_full[qb]));
+            if (++qb == T::kQBuffers) { qb = 0; ph ^= 1u; }
         }
     } else if (warp == kMmaWarp) {
         // ------------------------------ products ------------------------------
@@ -340,6 +353,7 @@ cross_tiles_kernel(const __grid_constant__ CUtensorMap tmap, const CrossParams p
         const uint32_t q_desc = desc_along_row(smem_u32(smem)), k_desc = desc_along_row(smem_u32(stages)),
                        v_desc = desc_along_rows(smem_u32(stages), T::kSlab);
         int st = 0;                                       // the stage whose turn it is, and its parity
+        int qb = 0;                                       // the same of the queries' buffers
         uint32_t st_ph = 0u, q_ph = 0u, p_ph = 0u;        // (p_ph: a bit for each half)
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -349,7 +363,7 @@ cross_tiles_kernel(const __grid_constant__ CUtensorMap tmap, const CrossParams p
             return ok;
         };
         auto scores = [&](int h, int stage) {
-            const uint32_t a = q_desc + h * (T::kQHalf >> 4), b = k_desc + stage * (T::kStage >> 4);
+            const uint32_t a = q_desc + qb * (T::kQBytes >> 4) + h * (T::kQHalf >> 4), b = k_desc + stage * (T::kStage >> 4);
             const uint32_t d = tmem + T::kS + h * T::kKeys;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
@@ -360,12 +374,11 @@ cross_tiles_kernel(const __grid_constant__ CUtensorMap tmap, const CrossParams p
             const TileItem& t = walk.t;
             if (t.steps == 0) continue;
             const int halves = t.b.rows > 128 ? 2 : 1;
-            if (!wait(&bars->q_full, q_ph)) break;
-            q_ph ^= 1u;
+            if (!wait(&bars->q_full[qb], q_ph)) break;
             if (!wait(&bars->full[st], st_ph)) break;
             for (int h = 0; h < halves; ++h) scores(h, st);
             mma_commit(smem_u32(&bars->empty[st]));
-            if (t.steps == 1) mma_commit(smem_u32(&bars->q_empty));
+            if (t.steps == 1) mma_commit(smem_u32(&bars->q_empty[qb]));
             for (int j = 0; j < t.steps; ++j) {
                 const bool more = j + 1 < t.steps;
                 if (++st == T::kStages) { st = 0; st_ph ^= 1u; }
@@ -390,9 +403,10 @@ cross_tiles_kernel(const __grid_constant__ CUtensorMap tmap, const CrossParams p
                 if (!ok) break;
                 mma_commit(smem_u32(&bars->empty[sv]));
                 if (more) mma_commit(smem_u32(&bars->empty[st]));
-                if (j + 2 == t.steps) mma_commit(smem_u32(&bars->q_empty));
+                if (j + 2 == t.steps) mma_commit(smem_u32(&bars->q_empty[qb]));
             }
             if (ok && ++st == T::kStages) { st = 0; st_ph ^= 1u; }
+            if (++qb == T::kQBuffers) { qb = 0; q_ph ^= 1u; }
         }
         // everything issued is done before the CTA can end
         mma_commit(smem_u32(&bars->drain));
@@ -459,6 +473,18 @@ cross_tiles_kernel(const __grid_constant__ CUtensorMap tmap, const CrossParams p
                 // at most 2^-21 of the largest.  It rises by whole numbers, so that scaling
                 // the outputs rounds nothing; the step's weights are then taken again (the
                 // scores are overwritten after this check).
+                if (j == 0) {
+                    float top = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < NC; ++c) {
+                        uint32_t x[32];
+                        tmem_ld32(s_at + 32 * c, x);
+                        tmem_wait_ld();
+                        top = fmaxf(top, largest(x));
+                    }
+                    top *= scale;
+                    if (top > -INFINITY) m = ceilf(top) - 8.f;
+                }
                 uint64_t add[2] = {0ull, 0ull};
                 auto weigh = [&](const uint32_t (&x)[32], uint32_t* w) {
                     const float mu = m == -INFINITY ? 0.f : m;
