@@ -320,17 +320,21 @@ cross_tiles_kernel(const __grid_constant__ CUtensorMap tmap, const CrossParams p
                 if (lane == 0) timed_out();
                 break;
             }
-            // a lane has one 16-byte piece of every kStep-th row of the halves that have any
+            // A lane has one 16-byte piece of every kStep-th row of the halves that have
+            // any.  Row r is token (x0 + r) / group behind the tile's first; that quotient
+            // of a number below 320 by one up to 64 is exact in 16 fraction bits, and
+            // every row's address is on its own (a running one took 15000 clocks a tile).
             constexpr int kPieces = D / 8, kStep = 32 * kQueryWarps / kPieces;
             const int id = threadIdx.x - 32 * kQueryWarp, k = id % kPieces, rows = t.b.rows > 128 ? 256 : 128;
-            int row = t.b.row0 + id / kPieces, tok = row / p.group, x = row % p.group;
-            const uint16_t* src = p.q + ((size_t)t.b.q0 * p.n_heads + (size_t)t.b.head * p.group) * D + k * 8;
-#pragma unroll 4
+            const uint32_t x0 = t.b.row0 % p.group, inverse = (65535u + p.group) / p.group;
+            const uint16_t* src = p.q + ((size_t)(t.b.q0 + t.b.row0 / p.group) * p.n_heads + (size_t)t.b.head * p.group) * D + k * 8;
+            const uint32_t dst = smem_u32(smem) + qb * T::kQBytes;
+#pragma unroll 8
             for (int r = id / kPieces; r < rows; r += kStep) {
+                const uint32_t tok = (x0 + r) * inverse >> 16, x = x0 + r - tok * p.group;
                 const bool there = r < t.b.rows;
-                cp_async16_or_zero(smem_u32(smem) + qb * T::kQBytes + r / 128 * T::kQHalf + swz(r % 128, k, 128),
+                cp_async16_or_zero(dst + r / 128 * T::kQHalf + swz(r % 128, k, 128),
                                    src + (there ? ((size_t)tok * p.n_heads + x) * D : 0), there);
-                for (x += kStep; x >= p.group; x -= p.group) ++tok;
             }
             if constexpr (T::kQBuffers == 1) {            // the next tile's into L2 meanwhile
                 if (walk.idx + 1 < walk.end) {
@@ -385,20 +389,18 @@ cross_tiles_kernel(const __grid_constant__ CUtensorMap tmap, const CrossParams p
                 const int sv = st;                        // this step's values, then the next one's keys
                 const uint32_t sv_ph = st_ph;
                 if (more && ++st == T::kStages) { st = 0; st_ph ^= 1u; }
+                // (stages first: as a rule they are there, and asking costs time that the
+                // weights' wait hides)
+                if (!wait(&bars->full[sv], sv_ph) || (more && !wait(&bars->full[st], st_ph))) break;
                 for (int h = 0; h < halves; ++h) {
                     if (!wait(&bars->p_full[h], (p_ph >> h) & 1u)) break;
                     p_ph ^= 1u << h;
-                    if (h == 0 && !wait(&bars->full[sv], sv_ph)) break;
                     const uint32_t b = v_desc + sv * (T::kStage >> 4);
                     const uint32_t a = tmem + T::kS + h * T::kKeys, d = tmem + T::kO + h * D;
 #pragma unroll
                     for (int k = 0; k < T::kKeys / 16; ++k) mma_ts<kShapeO>(d, a + 8 * k, b + k * (2048 >> 4), j > 0 || k > 0);
-                    if (more) {
-                        if (h == 0 && !wait(&bars->full[st], st_ph)) break;
-                        scores(h, st);
-                    } else {
-                        mma_commit(smem_u32(&bars->o_full[h]));
-                    }
+                    if (more) scores(h, st);
+                    else mma_commit(smem_u32(&bars->o_full[h]));
                 }
                 if (!ok) break;
                 mma_commit(smem_u32(&bars->empty[sv]));
@@ -424,6 +426,7 @@ cross_tiles_kernel(const __grid_constant__ CUtensorMap tmap, const CrossParams p
         // a negative scale turns the scores' signs; with 0 all scores are alike
         const float scale = fmaxf(fabsf(p.scale_log2), 1e-37f);
         const bool turned = p.scale_log2 < 0.f;
+        const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
         const uint64_t scale2 = pair_of(__float_as_uint(scale), __float_as_uint(scale));
         auto largest = [](const uint32_t (&x)[32]) {
             float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -567,19 +570,26 @@ cross_tiles_kernel(const __grid_constant__ CUtensorMap tmap, const CrossParams p
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = 0u;
                 }
+                // (32 bytes a store where the rows allow it: whole sectors, half as many)
                 if (r >= t.b.rows) {
                 } else if (t.b.part >= 0) {
-                    uint4* dst = reinterpret_cast<uint4*>(p.part_o + id * D + 32 * c);
+                    float* dst = p.part_o + id * D + 32 * c;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    for (int e = 0; e < 32; e += 8) st_32b(dst + e, o[e], o[e + 1], o[e + 2], o[e + 3], o[e + 4], o[e + 5], o[e + 6], o[e + 7]);
                 } else {
-                    uint4* dst = reinterpret_cast<uint4*>(p.out + at + 32 * c);
+                    uint16_t* dst = p.out + at + 32 * c;
                     uint32_t w[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
                         w[e] = pack_half2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                    if (wide) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                        for (int e = 0; e < 16; e += 8) st_32b(dst + 2 * e, w[e], w[e + 1], w[e + 2], w[e + 3], w[e + 4], w[e + 5], w[e + 6], w[e + 7]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4)
+                            *reinterpret_cast<uint4*>(dst + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+                    }
                 }
                 __syncwarp();
             }
