@@ -361,10 +361,12 @@ cross_tiles_kernel(const __grid_constant__ CUtensorMap tmap, const CrossParams p
         uint32_t st_ph = 0u, q_ph = 0u, p_ph = 0u;        // (p_ph: a bit for each half)
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
-            ok = __all_sync(kFull, mbar_wait(smem_u32(bar), parity));
+            ok = warp_wait(smem_u32(bar), parity);
             if (!ok && lane == 0) timed_out();
-            tc_fence_after();
             return ok;
+        };
+        auto next_stage = [&]() {
+            if (++st == T::kStages) { st = 0; st_ph ^= 1u; }
         };
         auto scores = [&](int h, int stage) {
             const uint32_t a = q_desc + qb * (T::kQBytes >> 4) + h * (T::kQHalf >> 4), b = k_desc + stage * (T::kStage >> 4);
@@ -383,31 +385,43 @@ cross_tiles_kernel(const __grid_constant__ CUtensorMap tmap, const CrossParams p
             for (int h = 0; h < halves; ++h) scores(h, st);
             mma_commit(smem_u32(&bars->empty[st]));
             if (t.steps == 1) mma_commit(smem_u32(&bars->q_empty[qb]));
+            // Each step: its values, then the next one's keys.  What a step waits for is
+            // asked for while products are still queued: a wait takes some 150 clocks
+            // even where nothing is missing, and the queue is not deep.
+            next_stage();
+            int sv = st;
+            if (!wait(&bars->full[st], st_ph)) break;
             for (int j = 0; j < t.steps; ++j) {
                 const bool more = j + 1 < t.steps;
-                if (++st == T::kStages) { st = 0; st_ph ^= 1u; }
-                const int sv = st;                        // this step's values, then the next one's keys
-                const uint32_t sv_ph = st_ph;
-                if (more && ++st == T::kStages) { st = 0; st_ph ^= 1u; }
-                // (stages first: as a rule they are there, and asking costs time that the
-                // weights' wait hides)
-                if (!wait(&bars->full[sv], sv_ph) || (more && !wait(&bars->full[st], st_ph))) break;
+                if (more) {
+                    next_stage();
+                    if (!wait(&bars->full[st], st_ph)) break;
+                }
+                const int sk = st;
                 for (int h = 0; h < halves; ++h) {
                     if (!wait(&bars->p_full[h], (p_ph >> h) & 1u)) break;
+                    tc_fence_after();
                     p_ph ^= 1u << h;
                     const uint32_t b = v_desc + sv * (T::kStage >> 4);
                     const uint32_t a = tmem + T::kS + h * T::kKeys, d = tmem + T::kO + h * D;
 #pragma unroll
                     for (int k = 0; k < T::kKeys / 16; ++k) mma_ts<kShapeO>(d, a + 8 * k, b + k * (2048 >> 4), j > 0 || k > 0);
-                    if (more) scores(h, st);
+                    if (more) scores(h, sk);
                     else mma_commit(smem_u32(&bars->o_full[h]));
+                    if (h + 1 == halves) {
+                        mma_commit(smem_u32(&bars->empty[sv]));
+                        if (more) mma_commit(smem_u32(&bars->empty[sk]));
+                        if (j + 2 == t.steps) mma_commit(smem_u32(&bars->q_empty[qb]));
+                    }
+                    if (h == 0 && more) {                 // the next step's values
+                        next_stage();
+                        if (!wait(&bars->full[st], st_ph)) break;
+                    }
                 }
                 if (!ok) break;
-                mma_commit(smem_u32(&bars->empty[sv]));
-                if (more) mma_commit(smem_u32(&bars->empty[st]));
-                if (j + 2 == t.steps) mma_commit(smem_u32(&bars->q_empty[qb]));
+                sv = st;
             }
-            if (ok && ++st == T::kStages) { st = 0; st_ph ^= 1u; }
+            if (ok) next_stage();
             if (++qb == T::kQBuffers) { qb = 0; q_ph ^= 1u; }
         }
         // everything issued is done before the CTA can end
