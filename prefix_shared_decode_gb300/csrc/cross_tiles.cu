@@ -383,8 +383,6 @@ cross_tiles_kernel(const __grid_constant__ CUtensorMap tmap, const CrossParams p
             if (!wait(&bars->q_full[qb], q_ph)) break;
             if (!wait(&bars->full[st], st_ph)) break;
             for (int h = 0; h < halves; ++h) scores(h, st);
-            mma_commit(smem_u32(&bars->empty[st]));
-            if (t.steps == 1) mma_commit(smem_u32(&bars->q_empty[qb]));
             // Each step: its values, then the next one's keys.  What a step waits for is
             // asked for while products are still queued: a wait takes some 150 clocks
             // even where nothing is missing, and the queue is not deep.
@@ -408,11 +406,6 @@ cross_tiles_kernel(const __grid_constant__ CUtensorMap tmap, const CrossParams p
                     for (int k = 0; k < T::kKeys / 16; ++k) mma_ts<kShapeO>(d, a + 8 * k, b + k * (2048 >> 4), j > 0 || k > 0);
                     if (more) scores(h, sk);
                     else mma_commit(smem_u32(&bars->o_full[h]));
-                    if (h + 1 == halves) {
-                        mma_commit(smem_u32(&bars->empty[sv]));
-                        if (more) mma_commit(smem_u32(&bars->empty[sk]));
-                        if (j + 2 == t.steps) mma_commit(smem_u32(&bars->q_empty[qb]));
-                    }
                     if (h == 0 && more) {                 // the next step's values
                         next_stage();
                         if (!wait(&bars->full[st], st_ph)) break;
@@ -449,6 +442,11 @@ cross_tiles_kernel(const __grid_constant__ CUtensorMap tmap, const CrossParams p
                 a[(e >> 1) & 3] = fmaxf(a[(e >> 1) & 3], fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
             return fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
         };
+        // The scores of the tile's last half being there says that every product before
+        // them is done: its first thread then gives the stages and queries back.  (A
+        // commit of the products' warp for each of them cost it 100 clocks.)
+        int first = 0, qb = 0;                            // the item's first stage, its queries' buffer
+        auto release = [&](int x) { mbar_arrive(smem_u32(&bars->empty[(first + x) % T::kStages])); };
         uint32_t s_ph = 0u, o_ph = 0u;
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -459,7 +457,15 @@ cross_tiles_kernel(const __grid_constant__ CUtensorMap tmap, const CrossParams p
         };
         for (Walk walk(p); ok && walk.more(); walk.advance()) {
             const TileItem& t = walk.t;
-            if (128 * h >= t.b.rows) continue;
+            auto pass_by = [&]() {
+                first = (first + 2 * t.steps) % T::kStages;
+                if (t.steps > 0 && ++qb == T::kQBuffers) qb = 0;
+            };
+            const bool releases = (warp & 3) == 0 && lane == 0 && (128 * (h + 1) >= t.b.rows) && 128 * h < t.b.rows;
+            if (128 * h >= t.b.rows) {
+                pass_by();
+                continue;
+            }
             // the last token that the row sees (a row past the tile's last: all)
             int last = t.n - 1;
             if (p.causal && r < t.b.rows) last = min(last, t.b.ctx - t.b.m + (t.b.row0 + r) / p.group);
@@ -468,6 +474,11 @@ cross_tiles_kernel(const __grid_constant__ CUtensorMap tmap, const CrossParams p
             for (int j = 0; j < t.steps; ++j) {
                 if (!wait(&bars->s_full[h], s_ph)) break;
                 s_ph ^= 1u;
+                if (releases) {                           // K of this step, V of the one before
+                    if (j > 0) release(2 * j - 1);
+                    release(2 * j);
+                    if (j + 1 == t.steps) mbar_arrive(smem_u32(&bars->q_empty[qb]));
+                }
                 constexpr int NC = T::kKeys / 32;         // 32 columns at a time
                 if (turned || t.b.c_begin * C + (j + 1) * T::kKeys - 1 > all_see) {
                     // few steps need it: signs turned and hidden tokens masked in place
@@ -570,6 +581,7 @@ cross_tiles_kernel(const __grid_constant__ CUtensorMap tmap, const CrossParams p
             if (t.steps > 0) {
                 if (!wait(&bars->o_full[h], o_ph)) break;
                 o_ph ^= 1u;
+                if (releases) release(2 * t.steps - 1);
             }
             const float inv = sum == 0.f ? 0.f : p.out_scale / sum;
             const size_t id = (size_t)t.b.part * p.tile_rows + r;
@@ -608,6 +620,7 @@ cross_tiles_kernel(const __grid_constant__ CUtensorMap tmap, const CrossParams p
                 __syncwarp();
             }
             if (t.b.part >= 0 && r < t.b.rows) p.part_ms[id] = make_float2(m, sum);
+            pass_by();
             tc_fence_before();                            // (the next tile's first product overwrites the outputs)
         }
     }
