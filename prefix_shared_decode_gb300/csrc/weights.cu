@@ -22,7 +22,7 @@ namespace dev {
 constexpr int kWtWarps = 4, kWtThreads = 32 * (kWtWarps + 1);
 constexpr int kWtTokens = 64;             // tokens of a stage: 16 a warp
 constexpr int kWtStages = 4;
-constexpr int kAddThreads = 256, kAddTokens = 4 * kAddThreads;
+constexpr int kAddThreads = 256, kAddPer = 4, kAddTokens = 4 * kAddPer * kAddThreads;
 
 struct WeightParams {
     AttnParams a;                 // the schedule's plan, the pool, q (part_ms: the units' (m, s))
@@ -87,63 +87,74 @@ __global__ void __launch_bounds__(kWtThreads) weight_scores_kernel(const __grid_
 
     if (warp == kWtWarps) {
         // ------------------------------ producer ------------------------------
-        if (lane != 0) return;
+        // A lane per chunk, 32 chunks of a head at a time: slots, token counts and
+        // offsets of all of them come in one round trip (chunk after chunk, each
+        // stage waited for two dependent loads: 391 us where these take 341 for
+        // eight contexts of 128 K tokens).
         if (p.test_stall) {               // test hook: a wait that nothing ends
-            if (!mbar_wait(full0, 0u)) set_status(p.status, CA_ERR_TIMEOUT);
+            if (lane == 0 && !mbar_wait(full0, 0u)) set_status(p.status, CA_ERR_TIMEOUT);
             return;
         }
         const uint64_t pol = policy_evict_first();
+        constexpr uint32_t kCopy = EB == 0 ? C * D / 2 + C * D / 16 : C * D * EB;
+        struct Refs { int slot, ntok, tok0; };
+        auto fetch = [&](int L, int end) {
+            Refs r{-1, 0, 0};
+            if (L + lane < end) {
+                const int at = base + (L + lane) % n;
+                r.slot = p.chunks[at].slot;
+                r.tok0 = p.chunk_tok0[at];
+                if (r.slot < 0 || r.slot >= p.capacity || L / n >= HK) {
+                    set_status(p.status, CA_ERR_DEVICE_BOUNDS);
+                    r.slot = -1;
+                }
+                if (r.slot >= 0) r.ntok = min(max(p.slot_ntok[r.slot], 0), C);
+            }
+            return r;
+        };
+        auto head_end = [&](int L) { return min(L1, (L / n + 1) * n); };
         int it = 0;
         bool ok = true;
+        Refs next = fetch(L0, head_end(L0));
         for (int L = L0; L < L1 && ok;) {
-            const int head = L / n, seg_end = min(L1, (head + 1) * n);
-            for (; L < seg_end && ok; ++it) {
-                const int st = it % kWtStages, cnt = min(kPer, seg_end - L);
+            const int head = L / n, batch = min(32, head_end(L) - L);
+            const Refs r = next;
+            if (L + batch < L1) next = fetch(L + batch, head_end(L + batch));
+            for (int x0 = 0; x0 < batch; x0 += kPer, ++it) {   // (32 is a multiple of kPer)
+                const int st = it % kWtStages;
                 const uint32_t fb = full0 + 8 * st;
-                if (!mbar_wait(empty0 + 8 * st, ((uint32_t)(it / kWtStages) & 1u) ^ 1u)) {
-                    set_status(p.status, CA_ERR_TIMEOUT);
+                if (!__all_sync(kFull, mbar_wait(empty0 + 8 * st, ((uint32_t)(it / kWtStages) & 1u) ^ 1u))) {
+                    if (lane == 0) set_status(p.status, CA_ERR_TIMEOUT);
                     ok = false;
                     break;
                 }
-                uint32_t bytes = 0;
-                int slots[kPer];
-#pragma unroll
-                for (int x = 0; x < kPer; ++x) {
-                    slots[x] = -1;
-                    if (x >= cnt) continue;
-                    const int at = base + (L + x) % n;
-                    const ChunkRef ch = p.chunks[at];
-                    if (ch.slot < 0 || ch.slot >= p.capacity || head >= HK) {
-                        set_status(p.status, CA_ERR_DEVICE_BOUNDS);
-                    } else {
-                        slots[x] = ch.slot;
-                        bytes += EB == 0 ? C * D / 2 + C * D / 16 : C * D * EB;
-                    }
-                    const int ntok = slots[x] >= 0 ? min(max(p.slot_ntok[slots[x]], 0), C) : 0;
-                    info[st * kPer + x].x = ntok;
-                    info[st * kPer + x].y = p.chunk_tok0[at];
+                const int x = lane - x0;
+                const bool mine = x >= 0 && x < kPer && lane < batch, there = mine && r.slot >= 0;
+                const uint32_t copies = __popc(__ballot_sync(kFull, there));
+                if (lane == 0 && copies) mbar_expect_tx_only(fb, copies * kCopy);
+                if (mine) {
+                    info[st * kPer + x].x = r.ntok;
+                    info[st * kPer + x].y = r.tok0;
                 }
-                if (bytes) mbar_expect_tx_only(fb, bytes);
-#pragma unroll
-                for (int x = 0; x < kPer; ++x) {
-                    if (slots[x] < 0) continue;
+                __syncwarp();
+                if (there) {
                     const uint32_t dst = smem_u32(smem + st * SM::kStage + x * SM::kTile);
                     if constexpr (EB == 0) {
                         using T = F4Tile<C, D>;
-                        const uint8_t* src =
-                            p.kv + (((long long)slots[x] * p.n_layers + p.layer) * HK + head) * T::kBytes;
+                        const uint8_t* src = p.kv + (((long long)r.slot * p.n_layers + p.layer) * HK + head) * T::kBytes;
                         bulk_load(dst, src, T::kCodes, fb, pol);
                         bulk_load(dst + T::kKScales, src + T::kKScales, T::kScales, fb, pol);
                     } else {
-                        const int row = ((slots[x] * p.n_layers + p.layer) * 2 * HK + head) * C;
+                        const int row = ((r.slot * p.n_layers + p.layer) * 2 * HK + head) * C;
 #pragma unroll
                         for (int bx = 0; bx < D * EB / 128; ++bx)
                             tma_load_2d(dst + bx * C * 128, &tmap, bx * (128 / (EB == 0 ? 1 : EB)), row, fb, pol);
                     }
                 }
-                mbar_arrive(fb);
-                L += cnt;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(fb);
             }
+            L += batch;
         }
         if (!ok)                          // let the copies in flight land before the CTA can end
             for (int k = max(0, it - kWtStages); k < it; ++k)
@@ -284,7 +295,8 @@ __global__ void __launch_bounds__(kWtThreads) weight_scores_kernel(const __grid_
 }
 
 // Joins the units' (m, s) of each row of a position and head, then adds the
-// rows' weights of four tokens per thread.
+// rows' weights.  A thread has four tokens of each kAddPer-th part of the block's
+// range; a row's scores and the sums are on their way before the join is through.
 __global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const WeightParams wp) {
     __shared__ float lse[kQRows];                     // log2 of each row's sum
     const AttnParams& p = wp.a;
@@ -294,18 +306,44 @@ __global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const WeightPa
     const int G = p.group, QL = p.q_len, RW = QL * G, H = p.n_heads;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long c0 = wp.tok_base[pos], tokens = (wp.tok_base[pos + 1] - c0) * wp.chunk;
-    const int t0 = blk * kAddTokens + 4 * threadIdx.x;
+    const bool apart = wp.in != wp.out;
+    const long long last = apart ? max(tokens, (long long)wp.room) : tokens;
     const size_t row = ((size_t)p.seq_perm[pos] * p.n_kv_heads + h) * wp.room;
+    const float* scores = wp.scores + c0 * wp.chunk * ((long long)QL * H) + (long long)h * RW * tokens;
+    auto token = [&](int k) { return (blk * kAddPer + k) * (4 * kAddThreads) + 4 * (int)threadIdx.x; };
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (blk * (long long)kAddTokens >= tokens && (wp.in == wp.out || blk * (long long)kAddTokens >= wp.room)) return;
+    if ((long long)blk * kAddTokens >= last) return;
+    const bool wide = (wp.room & 3) == 0 && ((reinterpret_cast<uintptr_t>(wp.in) | reinterpret_cast<uintptr_t>(wp.out)) & 15u) == 0;
+    float4 x[kAddPer], sum[kAddPer];
+    auto load_row = [&](int r) {
+#pragma unroll
+        for (int k = 0; k < kAddPer; ++k)             // (a position's tokens are a multiple of 16)
+            x[k] = token(k) < tokens ? __ldcg(reinterpret_cast<const float4*>(scores + r * tokens + token(k)))
+                                     : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    };
+    load_row(0);
+#pragma unroll
+    for (int k = 0; k < kAddPer; ++k) {
+        const int t = token(k);
+        sum[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t >= last) continue;
+        if (wide) {
+            if (t < wp.room) sum[k] = *reinterpret_cast<const float4*>(wp.in + row + t);
+        } else {
+            if (t < wp.room) sum[k].x = wp.in[row + t];
+            if (t + 1 < wp.room) sum[k].y = wp.in[row + t + 1];
+            if (t + 2 < wp.room) sum[k].z = wp.in[row + t + 2];
+            if (t + 3 < wp.room) sum[k].w = wp.in[row + t + 3];
+        }
+    }
     for (int r = warp; r < RW; r += kAddThreads / 32) {
         const size_t id = ((size_t)pos * QL + r / G) * H + h * G + r % G;
         const int a = p.pbase[id], n = p.pbase[id + 1] - a;
         float M = -INFINITY, S = 0.f;
         for (int j = lane; j < n; j += 32) {
-            const float2 x = __ldcg(&p.part_ms[a + j]);
-            const float top = fmaxf(M, x.x), mu = top == -INFINITY ? 0.f : top;
-            S = S * ex2(M - mu) + x.y * ex2(x.x - mu);
+            const float2 v = __ldcg(&p.part_ms[a + j]);
+            const float top = fmaxf(M, v.x), mu = top == -INFINITY ? 0.f : top;
+            S = S * ex2(M - mu) + v.y * ex2(v.x - mu);
             M = top;
         }
 #pragma unroll
@@ -320,24 +358,46 @@ __global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const WeightPa
         if (lane == 0) lse[r] = S > 0.f || S != S ? M + log2f(S) : INFINITY;   // (a row that sees nothing weighs nothing)
     }
     __syncthreads();
-    float w[4] = {0.f, 0.f, 0.f, 0.f};
-    if (t0 < tokens) {                                // (a position's tokens are a multiple of 16)
-        const float* x = wp.scores + c0 * wp.chunk * ((long long)QL * H) + (long long)h * RW * tokens + t0;
-        for (int r = 0; r < RW; ++r, x += tokens) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(x));
-            const float l = lse[r];
-            w[0] += ex2(v.x - l);
-            w[1] += ex2(v.y - l);
-            w[2] += ex2(v.z - l);
-            w[3] += ex2(v.w - l);
-            if (r == 0 && ((t0 >= wp.room && v.x != -INFINITY) || (t0 + 1 >= wp.room && v.y != -INFINITY) ||
-                           (t0 + 2 >= wp.room && v.z != -INFINITY) || (t0 + 3 >= wp.room && v.w != -INFINITY)))
-                set_status(p.status, CA_ERR_DEVICE_BOUNDS);   // the context has outgrown its row
+    // a context that has outgrown its row
+    bool over = false;
+#pragma unroll
+    for (int k = 0; k < kAddPer; ++k) {
+        const int t = token(k);
+        over |= (t >= wp.room && x[k].x != -INFINITY) || (t + 1 >= wp.room && x[k].y != -INFINITY) ||
+                (t + 2 >= wp.room && x[k].z != -INFINITY) || (t + 3 >= wp.room && x[k].w != -INFINITY);
+    }
+    if (over) set_status(p.status, CA_ERR_DEVICE_BOUNDS);
+    float4 w[kAddPer];
+#pragma unroll
+    for (int k = 0; k < kAddPer; ++k) w[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int r = 0; r < RW; ++r) {
+        const float l = lse[r];
+        float4 y[kAddPer];
+#pragma unroll
+        for (int k = 0; k < kAddPer; ++k) y[k] = x[k];
+        if (r + 1 < RW) load_row(r + 1);
+#pragma unroll
+        for (int k = 0; k < kAddPer; ++k) {
+            w[k].x += ex2(y[k].x - l);
+            w[k].y += ex2(y[k].y - l);
+            w[k].z += ex2(y[k].z - l);
+            w[k].w += ex2(y[k].w - l);
         }
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (t0 + j < wp.room && (t0 < tokens || wp.in != wp.out)) wp.out[row + t0 + j] = wp.in[row + t0 + j] + w[j];
+    for (int k = 0; k < kAddPer; ++k) {
+        const int t = token(k);
+        if (t >= last) continue;
+        const float4 v = make_float4(sum[k].x + w[k].x, sum[k].y + w[k].y, sum[k].z + w[k].z, sum[k].w + w[k].w);
+        if (wide) {
+            if (t < wp.room) *reinterpret_cast<float4*>(wp.out + row + t) = v;
+        } else {
+            if (t < wp.room) wp.out[row + t] = v.x;
+            if (t + 1 < wp.room) wp.out[row + t + 1] = v.y;
+            if (t + 2 < wp.room) wp.out[row + t + 2] = v.z;
+            if (t + 3 < wp.room) wp.out[row + t + 3] = v.w;
+        }
+    }
 }
 
 }  // namespace dev
