@@ -21,7 +21,6 @@ namespace dev {
 
 constexpr int kWtWarps = 4, kWtThreads = 32 * (kWtWarps + 1);
 constexpr int kWtTokens = 64;             // tokens of a stage: 16 a warp
-constexpr int kWtStages = 4;
 constexpr int kAddThreads = 256, kAddPer = 4, kAddTokens = 4 * kAddPer * kAddThreads;
 
 struct WeightParams {
@@ -40,36 +39,84 @@ struct WtSmem {
     static constexpr int kPer = kWtTokens / C;            // chunk tiles of a stage
     static constexpr int kTile = EB == 0 ? F4Tile<C, D>::kBytes : C * D * EB;
     static constexpr int kStage = kPer * kTile;
+    static constexpr int kStages = EB == 2 && D == 256 ? 4 : EB == 2 && D == 128 ? 5 : 8;   // two CTAs an SM (D 256: one)
     static constexpr int kQ = q_rows<D>() * D * 2;
-    static constexpr int kRows = kWtStages * kStage + kQ;           // score rows' addresses
-    static constexpr int kMs = kRows + kQRows * 8;                   // (m, s) of each warp's rows
+    static constexpr int kRows = kStages * kStage + kQ;              // score rows' addresses, of two pieces
+    static constexpr int kMs = kRows + 2 * kQRows * 8;               // (m, s) of each warp's rows
     static constexpr int kInfo = kMs + kWtWarps * kQRows * 8;        // ntok and first token of each chunk tile
-    static constexpr int kBars = kInfo + kWtStages * kPer * 8;
-    static constexpr int kBytes = kBars + 2 * kWtStages * 8;
+    static constexpr int kBars = kInfo + kStages * kPer * 8;
+    static constexpr int kBytes = kBars + 2 * kStages * 8;
 };
 
 __device__ __forceinline__ void wt_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWtWarps * 32) : "memory"); }
 
-// One unit per CTA.  Rows of the query tile are (position, query token, query
-// head) as in the two-phase kernel; a warp takes 16 tokens of a stage against
-// every 16 of them.  A thread keeps the running maximum and sum of its own
-// columns of each of its rows; they meet at the end of a head.
+// One head's stretch of a unit: its chunks are chunk base + L % n for L in
+// [begin, end).
+struct Piece {
+    int head, begin, end, n, base, part, q_lo, positions;
+};
+// The pieces of a CTA's units: its static ones, then every grid-th of the tail.
+struct PieceWalk {
+    const AttnParams& p;
+    int u, u_end, tail;
+    Unit U;
+    int L, L1, n;
+    __device__ __forceinline__ explicit PieceWalk(const AttnParams& p_) : p(p_), tail(p_.dyn_begin + blockIdx.x), L(0), L1(0), n(1) {
+        const int2 range = *reinterpret_cast<const int2*>(p.cta_head + blockIdx.x);
+        u = range.x;
+        u_end = range.y;
+    }
+    __device__ __forceinline__ bool next(Piece& x) {
+        while (L >= L1) {
+            int at;
+            if (u < u_end) at = u++;
+            else if (tail < p.dyn_end) {
+                at = tail;
+                tail += gridDim.x;
+            } else return false;
+            U = p.units[at];
+            const bool sf = U.kind == UNIT_SF;
+            n = sf ? U.n_per_head : U.c_end - U.c_begin;
+            L = sf ? U.c_begin : U.head * n;
+            L1 = sf ? U.c_end : (U.head + U.n_per_head) * n;
+            first = true;
+        }
+        const bool sf = U.kind == UNIT_SF;
+        x.head = L / n;
+        x.begin = L;
+        x.end = L = min(L1, (x.head + 1) * n);
+        x.n = n;
+        x.base = sf ? U.base : U.c_begin;
+        x.part = first || !sf ? U.part : U.part_next;
+        x.q_lo = U.q_lo;
+        x.positions = U.q_hi - U.q_lo;
+        first = false;
+        return true;
+    }
+    bool first = true;
+};
+
+// Rows of the query tile are (position, query token, query head) as in the
+// two-phase kernel; a warp takes 16 tokens of a stage against every 16 of them.  A
+// thread keeps the running maximum and sum of its own columns of each of its
+// rows; they meet at the end of a piece.  Pieces of at most half the tile's rows
+// use its halves in turn, so that the next one's queries come meanwhile.
 template <int C, int D, int EB>
 __global__ void __launch_bounds__(kWtThreads) weight_scores_kernel(const __grid_constant__ CUtensorMap tmap,
                                                                    const WeightParams wp) {
     using SM = WtSmem<C, D, EB>;
-    constexpr int kPer = SM::kPer;
+    constexpr int kPer = SM::kPer, kN = SM::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
     const AttnParams& p = wp.a;
-    uint8_t* qt = smem + kWtStages * SM::kStage;
+    uint8_t* qt = smem + kN * SM::kStage;
     float** row_at = reinterpret_cast<float**>(smem + SM::kRows);
     float2* ms = reinterpret_cast<float2*>(smem + SM::kMs);
     volatile int2* info = reinterpret_cast<volatile int2*>(smem + SM::kInfo);
-    const uint32_t full0 = smem_u32(smem + SM::kBars), empty0 = full0 + 8 * kWtStages;
+    const uint32_t full0 = smem_u32(smem + SM::kBars), empty0 = full0 + 8 * kN;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kWtStages; ++i) {
+        for (int i = 0; i < kN; ++i) {
             mbar_init(full0 + 8 * i, 1);
             mbar_init(empty0 + 8 * i, kWtWarps);
         }
@@ -77,12 +124,11 @@ __global__ void __launch_bounds__(kWtThreads) weight_scores_kernel(const __grid_
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     __syncthreads();
-    // the plan may be read before the dependency wait; q and the pool after it
-    const Unit U = p.units[blockIdx.x];
-    const bool sf = U.kind == UNIT_SF;
-    const int n = sf ? U.n_per_head : U.c_end - U.c_begin, base = sf ? U.base : U.c_begin;
-    const int L0 = sf ? U.c_begin : U.head * n, L1 = sf ? U.c_end : (U.head + U.n_per_head) * n;
     const int HK = p.n_kv_heads, G = p.group, QL = p.q_len, RW = QL * G, H = p.n_heads;
+    // the plan may be read before the dependency wait; q and the pool after it
+    PieceWalk walk(p);
+    Piece cur, nxt;
+    bool have = walk.next(cur);
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     if (warp == kWtWarps) {
@@ -98,13 +144,13 @@ __global__ void __launch_bounds__(kWtThreads) weight_scores_kernel(const __grid_
         const uint64_t pol = policy_evict_first();
         constexpr uint32_t kCopy = EB == 0 ? C * D / 2 + C * D / 16 : C * D * EB;
         struct Refs { int slot, ntok, tok0; };
-        auto fetch = [&](int L, int end) {
+        auto fetch = [&](const Piece& x, int L) {
             Refs r{-1, 0, 0};
-            if (L + lane < end) {
-                const int at = base + (L + lane) % n;
+            if (L + lane < x.end) {
+                const int at = x.base + (L + lane) % x.n;
                 r.slot = p.chunks[at].slot;
                 r.tok0 = p.chunk_tok0[at];
-                if (r.slot < 0 || r.slot >= p.capacity || L / n >= HK) {
+                if (r.slot < 0 || r.slot >= p.capacity || x.head >= HK) {
                     set_status(p.status, CA_ERR_DEVICE_BOUNDS);
                     r.slot = -1;
                 }
@@ -112,53 +158,58 @@ __global__ void __launch_bounds__(kWtThreads) weight_scores_kernel(const __grid_
             }
             return r;
         };
-        auto head_end = [&](int L) { return min(L1, (L / n + 1) * n); };
         int it = 0;
         bool ok = true;
-        Refs next = fetch(L0, head_end(L0));
-        for (int L = L0; L < L1 && ok;) {
-            const int head = L / n, batch = min(32, head_end(L) - L);
-            const Refs r = next;
-            if (L + batch < L1) next = fetch(L + batch, head_end(L + batch));
-            for (int x0 = 0; x0 < batch; x0 += kPer, ++it) {   // (32 is a multiple of kPer)
-                const int st = it % kWtStages;
-                const uint32_t fb = full0 + 8 * st;
-                if (!__all_sync(kFull, mbar_wait(empty0 + 8 * st, ((uint32_t)(it / kWtStages) & 1u) ^ 1u))) {
-                    if (lane == 0) set_status(p.status, CA_ERR_TIMEOUT);
-                    ok = false;
-                    break;
-                }
-                const int x = lane - x0;
-                const bool mine = x >= 0 && x < kPer && lane < batch, there = mine && r.slot >= 0;
-                const uint32_t copies = __popc(__ballot_sync(kFull, there));
-                if (lane == 0 && copies) mbar_expect_tx_only(fb, copies * kCopy);
-                if (mine) {
-                    info[st * kPer + x].x = r.ntok;
-                    info[st * kPer + x].y = r.tok0;
-                }
-                __syncwarp();
-                if (there) {
-                    const uint32_t dst = smem_u32(smem + st * SM::kStage + x * SM::kTile);
-                    if constexpr (EB == 0) {
-                        using T = F4Tile<C, D>;
-                        const uint8_t* src = p.kv + (((long long)r.slot * p.n_layers + p.layer) * HK + head) * T::kBytes;
-                        bulk_load(dst, src, T::kCodes, fb, pol);
-                        bulk_load(dst + T::kKScales, src + T::kKScales, T::kScales, fb, pol);
-                    } else {
-                        const int row = ((r.slot * p.n_layers + p.layer) * 2 * HK + head) * C;
-#pragma unroll
-                        for (int bx = 0; bx < D * EB / 128; ++bx)
-                            tma_load_2d(dst + bx * C * 128, &tmap, bx * (128 / (EB == 0 ? 1 : EB)), row, fb, pol);
+        Refs next{-1, 0, 0};
+        if (have) next = fetch(cur, cur.begin);
+        while (have && ok) {
+            const bool more = walk.next(nxt);
+            for (int L = cur.begin; L < cur.end && ok; L += 32) {
+                const int batch = min(32, cur.end - L);
+                const Refs r = next;
+                if (L + 32 < cur.end) next = fetch(cur, L + 32);
+                else if (more) next = fetch(nxt, nxt.begin);
+                for (int x0 = 0; x0 < batch; x0 += kPer, ++it) {   // (32 is a multiple of kPer)
+                    const int st = it % kN;
+                    const uint32_t fb = full0 + 8 * st;
+                    if (!__all_sync(kFull, mbar_wait(empty0 + 8 * st, ((uint32_t)(it / kN) & 1u) ^ 1u))) {
+                        if (lane == 0) set_status(p.status, CA_ERR_TIMEOUT);
+                        ok = false;
+                        break;
                     }
+                    const int x = lane - x0;
+                    const bool mine = x >= 0 && x < kPer && lane < batch, there = mine && r.slot >= 0;
+                    const uint32_t copies = __popc(__ballot_sync(kFull, there));
+                    if (lane == 0 && copies) mbar_expect_tx_only(fb, copies * kCopy);
+                    if (mine) {
+                        info[st * kPer + x].x = r.ntok;
+                        info[st * kPer + x].y = r.tok0;
+                    }
+                    __syncwarp();
+                    if (there) {
+                        const uint32_t dst = smem_u32(smem + st * SM::kStage + x * SM::kTile);
+                        if constexpr (EB == 0) {
+                            using T = F4Tile<C, D>;
+                            const uint8_t* src =
+                                p.kv + (((long long)r.slot * p.n_layers + p.layer) * HK + cur.head) * T::kBytes;
+                            bulk_load(dst, src, T::kCodes, fb, pol);
+                            bulk_load(dst + T::kKScales, src + T::kKScales, T::kScales, fb, pol);
+                        } else {
+                            const int row = ((r.slot * p.n_layers + p.layer) * 2 * HK + cur.head) * C;
+#pragma unroll
+                            for (int bx = 0; bx < D * EB / 128; ++bx)
+                                tma_load_2d(dst + bx * C * 128, &tmap, bx * (128 / (EB == 0 ? 1 : EB)), row, fb, pol);
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(fb);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(fb);
             }
-            L += batch;
+            cur = nxt;
+            have = more;
         }
         if (!ok)                          // let the copies in flight land before the CTA can end
-            for (int k = max(0, it - kWtStages); k < it; ++k)
-                mbar_wait(full0 + 8 * (k % kWtStages), (uint32_t)(k / kWtStages) & 1u);
+            for (int k = max(0, it - kN); k < it; ++k) mbar_wait(full0 + 8 * (k % kN), (uint32_t)(k / kN) & 1u);
         return;
     }
 
@@ -166,34 +217,43 @@ __global__ void __launch_bounds__(kWtThreads) weight_scores_kernel(const __grid_
     constexpr int RS = EB == 0 ? 4 : 2;               // rows of a 16-row block that a thread holds columns of
     constexpr int RB = q_rows<D>() / 16;
     const int g = lane >> 2, t = lane & 3;
-    const int m_rows = (U.q_hi - U.q_lo) * RW;
     const int sub = warp * 16 / C, tok0 = warp * 16 % C;
     auto row_of = [&](int rb, int k) { return rb * 16 + (EB == 0 ? (k >> 1) * 8 + 2 * t + (k & 1) : g + 8 * k); };
-    int lim[RB][RS];                                  // causal mask: the last token that a row sees
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-        for (int k = 0; k < RS; ++k) {
-            const int row = row_of(rb, k);
-            lim[rb][k] = p.causal && row < m_rows ? p.ctx_len[U.q_lo + row / RW] - QL + (row % RW) / G : INT_MAX;
-        }
-    int it = 0;
-    bool ok = true;                                   // (a warp whose wait ran out still meets the others at their barriers)
-    for (int L = L0; L < L1;) {
-        const int head = L / n, seg_end = min(L1, (head + 1) * n);
-        const int part = L == L0 || !sf ? U.part : U.part_next;
-        for (int i = threadIdx.x; i < m_rows * (D / 8); i += kWtWarps * 32) {
+    // a piece's queries into the tile from row `at` on, and where its rows' scores go
+    auto fetch_queries = [&](const Piece& x, int at, int which) {
+        const int rows = x.positions * RW;
+        for (int i = threadIdx.x; i < rows * (D / 8); i += kWtWarps * 32) {
             const int r = i / (D / 8), k = i % (D / 8);
-            const size_t tok = (size_t)p.seq_perm[U.q_lo + r / RW] * QL + (r % RW) / G;
-            cp_async16(smem_u32(qt + swz(r, k, q_rows<D>())), p.q + (tok * H + head * G + r % G) * D + k * 8);
+            const size_t tok = (size_t)p.seq_perm[x.q_lo + r / RW] * QL + (r % RW) / G;
+            cp_async16(smem_u32(qt + swz(at + r, k, q_rows<D>())), p.q + (tok * H + x.head * G + r % G) * D + k * 8);
         }
-        for (int r = threadIdx.x; r < m_rows; r += kWtWarps * 32) {
-            const int pos = U.q_lo + r / RW;
+        for (int r = threadIdx.x; r < rows; r += kWtWarps * 32) {
+            const int pos = x.q_lo + r / RW;
             const long long c0 = wp.tok_base[pos], tokens = (wp.tok_base[pos + 1] - c0) * C;
-            row_at[r] = wp.scores + c0 * C * ((long long)QL * H) + (long long)(head * RW + r % RW) * tokens;
+            row_at[which * kQRows + r] = wp.scores + c0 * C * ((long long)QL * H) + (long long)(x.head * RW + r % RW) * tokens;
         }
+    };
+    constexpr int kHalf = q_rows<D>() / 2;
+    int it = 0, which = 0;
+    bool ok = true, fetched = false;                  // (a warp whose wait ran out still meets the others at their barriers)
+    for (; have; cur = nxt, which ^= 1) {
+        const bool more = walk.next(nxt);
+        const int head = cur.head, part = cur.part, m_rows = cur.positions * RW;
+        const int at = m_rows <= kHalf ? which * kHalf : 0;
+        if (!fetched) fetch_queries(cur, at, which);
         cp_async_wait_all();
         wt_sync();
+        fetched = more && m_rows <= kHalf && nxt.positions * RW <= kHalf;
+        if (fetched) fetch_queries(nxt, (which ^ 1) * kHalf, which ^ 1);
+        have = more;
+        int lim[RB][RS];                              // causal mask: the last token that a row sees
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+            for (int k = 0; k < RS; ++k) {
+                const int row = row_of(rb, k);
+                lim[rb][k] = p.causal && row < m_rows ? p.ctx_len[cur.q_lo + row / RW] - QL + (row % RW) / G : INT_MAX;
+            }
         float m[RB][RS], s[RB][RS];
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb)
@@ -202,9 +262,9 @@ __global__ void __launch_bounds__(kWtThreads) weight_scores_kernel(const __grid_
                 m[rb][k] = -INFINITY;
                 s[rb][k] = 0.f;
             }
-        for (; L < seg_end; ++it) {
-            const int st = it % kWtStages, cnt = min(kPer, seg_end - L);
-            if (ok && !mbar_wait(full0 + 8 * st, (uint32_t)(it / kWtStages) & 1u)) {
+        for (int L = cur.begin; L < cur.end; ++it) {
+            const int st = it % kN, cnt = min(kPer, cur.end - L);
+            if (ok && !mbar_wait(full0 + 8 * st, (uint32_t)(it / kN) & 1u)) {
                 set_status(p.status, CA_ERR_TIMEOUT);
                 ok = false;
             }
@@ -224,11 +284,11 @@ __global__ void __launch_bounds__(kWtThreads) weight_scores_kernel(const __grid_
                         for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
                             for (int kk = 0; kk < D / 16; ++kk)
-                                lds64(smem_u32(qt) + swz(rb * 16 + nb * 8 + g, 2 * kk + (t >> 1), q_rows<D>()) + 8 * (t & 1),
+                                lds64(smem_u32(qt) + swz(at + rb * 16 + nb * 8 + g, 2 * kk + (t >> 1), q_rows<D>()) + 8 * (t & 1),
                                       qb[nb][kk][0], qb[nb][kk][1]);
                         f4_scores<C, D, 2, false>(tile, tok0 / 16, qb, acc, lane);
                     } else {
-                        cf_scores<C, D, 16, EB == 1>(smem_u32(tile), tok0, smem_u32(qt) + rb * 16 * 128, 0, D / 16, acc, lane);
+                        cf_scores<C, D, 16, EB == 1>(smem_u32(tile), tok0, smem_u32(qt) + (at + rb * 16) * 128, 0, D / 16, acc, lane);
                     }
 #pragma unroll
                     for (int k = 0; k < RS; ++k) {
@@ -250,7 +310,7 @@ __global__ void __launch_bounds__(kWtThreads) weight_scores_kernel(const __grid_
                         for (int j = 0; j < N; ++j) sum += ex2(x[j] - mu);
                         m[rb][k] = top;
                         s[rb][k] = sum;
-                        float* dst = row_at[row] + ctx0 + tok0;
+                        float* dst = row_at[which * kQRows + row] + ctx0 + tok0;
                         if constexpr (EB == 0) {
                             dst[f4_token(g)] = x[0];
                             dst[f4_token(g) + 8] = x[1];
@@ -288,7 +348,7 @@ __global__ void __launch_bounds__(kWtThreads) weight_scores_kernel(const __grid_
             const float mu = M == -INFINITY ? 0.f : M;
 #pragma unroll
             for (int w = 0; w < kWtWarps; ++w) S += ms[w * kQRows + row].y * ex2(ms[w * kQRows + row].x - mu);
-            const int pos = U.q_lo + row / RW, jq = (row % RW) / G;
+            const int pos = cur.q_lo + row / RW, jq = (row % RW) / G;
             p.part_ms[p.pbase[((size_t)pos * QL + jq) * H + head * G + row % G] + part] = make_float2(M, S);
         }
     }
@@ -300,7 +360,6 @@ __global__ void __launch_bounds__(kWtThreads) weight_scores_kernel(const __grid_
 __global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const WeightParams wp) {
     __shared__ float lse[kQRows];                     // log2 of each row's sum
     const AttnParams& p = wp.a;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int blk = blockIdx.x % wp.blocks, pair = blockIdx.x / wp.blocks;
     const int pos = pair / p.n_kv_heads, h = pair % p.n_kv_heads;
     const int G = p.group, QL = p.q_len, RW = QL * G, H = p.n_heads;
@@ -370,6 +429,9 @@ __global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const WeightPa
     float4 w[kAddPer];
 #pragma unroll
     for (int k = 0; k < kAddPer; ++k) w[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    // (not earlier: the next kernel's CTAs would take this one's registers while
+    // they wait, 64 sequences back to back 111 us)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     for (int r = 0; r < RW; ++r) {
         const float l = lse[r];
         float4 y[kAddPer];
@@ -456,17 +518,17 @@ int launch_weights(const Pool& p, const Sched& s, int32_t layer, const void* q, 
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     const CUtensorMap* map = reinterpret_cast<const CUtensorMap*>(p.tmap);
-    const unsigned units = (unsigned)s.plan.units.size();
+    const unsigned grid = (unsigned)s.plan.grid;
     int st = CA_ERR_UNSUPPORTED;
     if (c.flags & CA_KV_FP4) {
-        if (c.head_dim == 64) st = pick_scores<64, 0>(c.chunk, map, w, units, attr, cs);
-        else if (c.head_dim == 128) st = pick_scores<128, 0>(c.chunk, map, w, units, attr, cs);
+        if (c.head_dim == 64) st = pick_scores<64, 0>(c.chunk, map, w, grid, attr, cs);
+        else if (c.head_dim == 128) st = pick_scores<128, 0>(c.chunk, map, w, grid, attr, cs);
     } else if (c.flags & CA_KV_FP8) {
-        if (c.head_dim == 128) st = pick_scores<128, 1>(c.chunk, map, w, units, attr, cs);
+        if (c.head_dim == 128) st = pick_scores<128, 1>(c.chunk, map, w, grid, attr, cs);
     } else {
-        if (c.head_dim == 64) st = pick_scores<64, 2>(c.chunk, map, w, units, attr, cs);
-        else if (c.head_dim == 128) st = pick_scores<128, 2>(c.chunk, map, w, units, attr, cs);
-        else if (c.head_dim == 256) st = pick_scores<256, 2>(c.chunk, map, w, units, attr, cs);
+        if (c.head_dim == 64) st = pick_scores<64, 2>(c.chunk, map, w, grid, attr, cs);
+        else if (c.head_dim == 128) st = pick_scores<128, 2>(c.chunk, map, w, grid, attr, cs);
+        else if (c.head_dim == 256) st = pick_scores<256, 2>(c.chunk, map, w, grid, attr, cs);
     }
     if (st) return st;
     count_launch();
@@ -474,10 +536,10 @@ int launch_weights(const Pool& p, const Sched& s, int32_t layer, const void* q, 
     for (int32_t pos = 0; pos < s.t.b; ++pos)
         most = std::max<int64_t>(most, (int64_t)(s.t.tok_base[pos + 1] - s.t.tok_base[pos]) * c.chunk);
     w.blocks = (int32_t)((most + dev::kAddTokens - 1) / dev::kAddTokens);
-    const int64_t grid = (int64_t)w.blocks * s.t.b * kv_heads(c);
-    if (grid > INT32_MAX) return CA_ERR_UNSUPPORTED;
+    const int64_t adds = (int64_t)w.blocks * s.t.b * kv_heads(c);
+    if (adds > INT32_MAX) return CA_ERR_UNSUPPORTED;
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3((unsigned)grid);
+    lc.gridDim = dim3((unsigned)adds);
     lc.blockDim = dim3(dev::kAddThreads);
     lc.stream = cs;
     lc.attrs = attr;
