@@ -48,6 +48,52 @@ struct WtSmem {
     static constexpr int kBytes = kBars + 2 * kStages * 8;
 };
 
+// Fragments for m16n8k16 over the dims [128 part, 128 part + 16 KK): of 16 rows of
+// the query tile, and of the keys [tok0, tok0 + 16) of a chunk tile.  All loads of
+// a stage go out together: one after the other between the products (8 of them in
+// a chain) a stage of 64 tokens took 0.7 us, whatever the memory did.
+template <int D, int KK, bool F8>
+__device__ __forceinline__ void query_frags(uint32_t rows, int part, uint32_t (&q)[KK][4], int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int k = 0; k < KK; ++k) {
+        const int kk = 8 * part + k;
+        if constexpr (F8) {               // (dims permuted inside each step, as the keys are below)
+            lds64(rows + swz(g, 2 * kk + (t >> 1), q_rows<D>()) + 8 * (t & 1), q[k][0], q[k][2]);
+            lds64(rows + swz(g + 8, 2 * kk + (t >> 1), q_rows<D>()) + 8 * (t & 1), q[k][1], q[k][3]);
+        } else {
+            ldsm_x4(rows + swz(lane & 15, 2 * kk + (lane >> 4), q_rows<D>()), q[k][0], q[k][1], q[k][2], q[k][3]);
+        }
+    }
+}
+template <int C, int KK, bool F8>
+__device__ __forceinline__ void key_frags(uint32_t tile, int tok0, int part, uint32_t (&b)[KK][4], int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    if constexpr (F8) {
+        // a lane's four bytes of a step, dims 16 kk + 4 t + 0 .. 3: columns 2t, 2t + 1 and 2t + 8, 2t + 9
+        uint32_t w[KK][2];
+#pragma unroll
+        for (int k = 0; k < KK; ++k)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int row = tok0 + 8 * j + g;
+                w[k][j] = lds32(tile + row * 128 + (((8 * part + k) ^ (row & 7)) << 4) + 4 * t);
+            }
+#pragma unroll
+        for (int k = 0; k < KK; ++k)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                b[k][2 * j] = f16x2_from_e4m3x2(w[k][j] & 0xffffu);
+                b[k][2 * j + 1] = f16x2_from_e4m3x2(w[k][j] >> 16);
+            }
+    } else {
+#pragma unroll
+        for (int k = 0; k < KK; ++k)
+            ldsm_x4(tile + swz(tok0 + (lane & 7) + ((lane >> 4) << 3), 2 * (8 * part + k) + ((lane >> 3) & 1), C), b[k][0], b[k][1],
+                    b[k][2], b[k][3]);
+    }
+}
+
 __device__ __forceinline__ void wt_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWtWarps * 32) : "memory"); }
 
 // One head's stretch of a unit: its chunks are chunk base + L % n for L in
@@ -102,7 +148,7 @@ struct PieceWalk {
 // rows; they meet at the end of a piece.  Pieces of at most half the tile's rows
 // use its halves in turn, so that the next one's queries come meanwhile.
 template <int C, int D, int EB>
-__global__ void __launch_bounds__(kWtThreads) weight_scores_kernel(const __grid_constant__ CUtensorMap tmap,
+__global__ void __launch_bounds__(kWtThreads, D == 256 ? 1 : 2) weight_scores_kernel(const __grid_constant__ CUtensorMap tmap,
                                                                    const WeightParams wp) {
     using SM = WtSmem<C, D, EB>;
     constexpr int kPer = SM::kPer, kN = SM::kStages;
@@ -254,6 +300,11 @@ __global__ void __launch_bounds__(kWtThreads) weight_scores_kernel(const __grid_
                 const int row = row_of(rb, k);
                 lim[rb][k] = p.causal && row < m_rows ? p.ctx_len[cur.q_lo + row / RW] - QL + (row % RW) / G : INT_MAX;
             }
+        // (up to 16 rows: their fragments stay in registers for the whole piece)
+        constexpr bool kKeep = EB != 0 && D <= 128;
+        uint32_t qf[EB == 0 ? 1 : D / 16 < 8 ? D / 16 : 8][4];
+        if constexpr (kKeep)
+            if (m_rows <= 16) query_frags<D, D / 16 < 8 ? D / 16 : 8, EB == 1>(smem_u32(qt) + at * 128, 0, qf, lane);
         float m[RB][RS], s[RB][RS];
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb)
@@ -274,6 +325,9 @@ __global__ void __launch_bounds__(kWtThreads) weight_scores_kernel(const __grid_
             if (sub < cnt) {
                 const uint8_t* tile = smem + st * SM::kStage + sub * SM::kTile;
                 const int ntok = info[st * kPer + sub].x, ctx0 = info[st * kPer + sub].y;
+                constexpr int KK = D / 16 < 8 ? D / 16 : 8;
+                uint32_t kf[EB == 0 ? 1 : KK][4];
+                if constexpr (EB != 0 && D <= 128) key_frags<C, KK, EB == 1>(smem_u32(tile), tok0, 0, kf, lane);
 #pragma unroll
                 for (int rb = 0; rb < RB; ++rb) {
                     if (rb * 16 >= m_rows) break;
@@ -288,7 +342,18 @@ __global__ void __launch_bounds__(kWtThreads) weight_scores_kernel(const __grid_
                                       qb[nb][kk][0], qb[nb][kk][1]);
                         f4_scores<C, D, 2, false>(tile, tok0 / 16, qb, acc, lane);
                     } else {
-                        cf_scores<C, D, 16, EB == 1>(smem_u32(tile), tok0, smem_u32(qt) + (at + rb * 16) * 128, 0, D / 16, acc, lane);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) acc[j >> 2][j & 3] = 0.f;
+#pragma unroll
+                        for (int part = 0; part < D / 16 / KK; ++part) {
+                            if constexpr (D > 128) key_frags<C, KK, EB == 1>(smem_u32(tile), tok0, part, kf, lane);
+                            if (!kKeep || m_rows > 16) query_frags<D, KK, EB == 1>(smem_u32(qt) + (at + rb * 16) * 128, part, qf, lane);
+#pragma unroll
+                            for (int k = 0; k < KK; ++k) {
+                                mma16816(acc[0], qf[k], kf[k][0], kf[k][1]);
+                                mma16816(acc[1], qf[k], kf[k][2], kf[k][3]);
+                            }
+                        }
                     }
 #pragma unroll
                     for (int k = 0; k < RS; ++k) {
