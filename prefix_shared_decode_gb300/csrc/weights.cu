@@ -31,7 +31,7 @@ struct WeightParams {
     float* out;
     int32_t room;                 // tokens per row of in and out
     int32_t chunk;
-    int32_t blocks;               // second kernel: blocks of tokens per row
+    int32_t blocks, block_tokens; // second kernel: blocks per row, tokens of each
 };
 
 template <int C, int D, int EB>
@@ -434,15 +434,20 @@ __global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const WeightPa
     const long long last = apart ? max(tokens, (long long)wp.room) : tokens;
     const size_t row = ((size_t)p.seq_perm[pos] * p.n_kv_heads + h) * wp.room;
     const float* scores = wp.scores + c0 * wp.chunk * ((long long)QL * H) + (long long)h * RW * tokens;
-    auto token = [&](int k) { return (blk * kAddPer + k) * (4 * kAddThreads) + 4 * (int)threadIdx.x; };
+    auto token = [&](int k) { return blk * wp.block_tokens + k * (4 * kAddThreads) + 4 * (int)threadIdx.x; };
+    // this warp's first row's partials: on their way with all the rest (the plan may
+    // be read before the dependency wait)
+    auto row_id = [&](int r) { return ((size_t)pos * QL + r / G) * H + h * G + r % G; };
+    const int part0 = warp < RW ? p.pbase[row_id(warp)] : 0, part1 = warp < RW ? p.pbase[row_id(warp) + 1] : 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if ((long long)blk * kAddTokens >= last) return;
+    const long long end = min(last, (long long)(blk + 1) * wp.block_tokens);    // of this block
+    if ((long long)blk * wp.block_tokens >= last) return;
     const bool wide = (wp.room & 3) == 0 && ((reinterpret_cast<uintptr_t>(wp.in) | reinterpret_cast<uintptr_t>(wp.out)) & 15u) == 0;
     float4 x[kAddPer], sum[kAddPer];
     auto load_row = [&](int r) {
 #pragma unroll
         for (int k = 0; k < kAddPer; ++k)             // (a position's tokens are a multiple of 16)
-            x[k] = token(k) < tokens ? __ldcg(reinterpret_cast<const float4*>(scores + r * tokens + token(k)))
+            x[k] = token(k) < min(tokens, end) ? __ldcg(reinterpret_cast<const float4*>(scores + r * tokens + token(k)))
                                      : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
     };
     load_row(0);
@@ -450,7 +455,7 @@ __global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const WeightPa
     for (int k = 0; k < kAddPer; ++k) {
         const int t = token(k);
         sum[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (t >= last) continue;
+        if (t >= end) continue;
         if (wide) {
             if (t < wp.room) sum[k] = *reinterpret_cast<const float4*>(wp.in + row + t);
         } else {
@@ -461,8 +466,7 @@ __global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const WeightPa
         }
     }
     for (int r = warp; r < RW; r += kAddThreads / 32) {
-        const size_t id = ((size_t)pos * QL + r / G) * H + h * G + r % G;
-        const int a = p.pbase[id], n = p.pbase[id + 1] - a;
+        const int a = r == warp ? part0 : p.pbase[row_id(r)], n = (r == warp ? part1 : p.pbase[row_id(r) + 1]) - a;
         float M = -INFINITY, S = 0.f;
         for (int j = lane; j < n; j += 32) {
             const float2 v = __ldcg(&p.part_ms[a + j]);
@@ -514,7 +518,7 @@ __global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const WeightPa
 #pragma unroll
     for (int k = 0; k < kAddPer; ++k) {
         const int t = token(k);
-        if (t >= last) continue;
+        if (t >= end) continue;
         const float4 v = make_float4(sum[k].x + w[k].x, sum[k].y + w[k].y, sum[k].z + w[k].z, sum[k].w + w[k].w);
         if (wide) {
             if (t < wp.room) *reinterpret_cast<float4*>(wp.out + row + t) = v;
@@ -600,7 +604,10 @@ int launch_weights(const Pool& p, const Sched& s, int32_t layer, const void* q, 
     int64_t most = in == out ? 0 : room;
     for (int32_t pos = 0; pos < s.t.b; ++pos)
         most = std::max<int64_t>(most, (int64_t)(s.t.tok_base[pos + 1] - s.t.tok_base[pos]) * c.chunk);
+    // blocks of about equal length, whole rounds of the threads
+    constexpr int64_t round = 4 * dev::kAddThreads;
     w.blocks = (int32_t)((most + dev::kAddTokens - 1) / dev::kAddTokens);
+    w.block_tokens = (int32_t)(((most + w.blocks - 1) / w.blocks + round - 1) / round * round);
     const int64_t adds = (int64_t)w.blocks * s.t.b * kv_heads(c);
     if (adds > INT32_MAX) return CA_ERR_UNSUPPORTED;
     cudaLaunchConfig_t lc = {};
