@@ -14,13 +14,16 @@ namespace ca {
 namespace dev {
 
 // ---------------------------------------------------------------------------
-// Choice: one CTA per (layer, sequence, head).  The number to take from the
-// middle is known, so the smallest key taken is found digit by digit from
-// histograms; a pass in token order then takes what is above it and the first
-// of what ties with it, and writes positions and sums behind one another.
+// Choice: a cluster of CTAs per (layer, sequence, head), each with a stretch of
+// the row's sums in shared memory.  The number to take from the middle is known, so
+// the smallest key taken is found digit by digit (8 bits) from the
+// cluster's histograms; then each CTA takes, in token order, what is above it and
+// the first of what ties with it, and writes positions and sums behind those of
+// the CTAs before it.  (One CTA a row that reads it five times from L2: 64 rows
+// of 65536 took 75 us, 1024 rows of 2560 29 us.)
 // ---------------------------------------------------------------------------
-constexpr int kPickThreads = 512, kPickWarps = kPickThreads / 32, kPickPer = 4;
-constexpr int kPickBins = 2048;
+constexpr int kPickThreads = 256, kPickWarps = kPickThreads / 32, kPickPer = 16;   // a thread per digit
+constexpr int kPickCache = 53248;         // sums that fit a CTA's shared memory
 
 struct PickParams {
     const float* in;              // [L][b][Hkv][room]
@@ -31,6 +34,7 @@ struct PickParams {
     const int32_t* slot_ntok;
     int32_t* status;
     int32_t room, budget, sink, recent, chunk, b, n_heads, capacity;
+    int32_t splits, cache;        // CTAs a cluster; sums that a CTA has room for
 };
 
 // Context tokens of batch row i (every chunk but its last is full).
@@ -42,119 +46,172 @@ __device__ __forceinline__ int context_tokens(const int32_t* list_off, const int
     return (n - 1) * chunk + min(max(slot_ntok[last], 0), chunk);
 }
 
-__global__ void __launch_bounds__(kPickThreads) pick_tokens_kernel(const PickParams p) {
-    __shared__ uint32_t hist[kPickBins];
-    __shared__ uint32_t sums[kPickWarps];
-    __shared__ uint32_t found[2];                     // the digit, places left inside it
+// Exclusive sums over the block's threads (red: one word a warp); all: the total.
+__device__ __forceinline__ uint32_t sum_before(uint32_t mine, uint32_t* red, uint32_t& all) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const size_t row = blockIdx.x;
+    uint32_t at = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t o = __shfl_up_sync(kFull, at, off);
+        if (lane >= off) at += o;
+    }
+    __syncthreads();                      // earlier reads of red are done
+    if (lane == 31) red[warp] = at;
+    __syncthreads();
+    all = 0u;
+#pragma unroll
+    for (int x = 0; x < kPickWarps; ++x) {
+        if (x == warp) at += all;
+        all += red[x];
+    }
+    return at - mine;
+}
+
+// CACHED: the CTA holds its sums (else the only CTA of a row reads them each time).
+template <bool CACHED>
+__global__ void __launch_bounds__(kPickThreads, 6) pick_tokens_kernel(const PickParams p) {
+    extern __shared__ __align__(16) float held[];
+    __shared__ uint32_t hist[4][256];
+    __shared__ uint32_t red[kPickWarps];
+    __shared__ uint32_t found[2];                     // the digit, places left inside it
+    __shared__ uint32_t count[2];                     // this CTA's keys that are taken, and those that tie
+    const int cs = p.splits, rank = blockIdx.x % cs;
+    const size_t row = blockIdx.x / cs;
     const int i = (int)(row / p.n_heads % p.b);
     const float* in = p.in + row * p.room;
     float* out = p.out + row * p.room;
     int32_t* kept = p.kept + row * p.budget;
     const int n = min(context_tokens(p.list_off, p.list_slots, p.slot_ntok, i, p.chunk, p.capacity), p.room);
-    if (n <= p.budget) {
-        for (int j = threadIdx.x; j < p.budget; j += kPickThreads) kept[j] = j < n ? j : -1;
+    const int first = rank * kPickThreads + threadIdx.x, stride = cs * kPickThreads;
+    if (n <= p.budget) {                              // (the whole cluster: the same n)
+        for (int j = first; j < p.budget; j += stride) kept[j] = j < n ? j : -1;
         if (in != out)
-            for (int j = threadIdx.x; j < n; j += kPickThreads) out[j] = in[j];
-        for (int j = n + threadIdx.x; j < p.room; j += kPickThreads) out[j] = 0.f;
+            for (int j = first; j < n; j += stride) out[j] = in[j];
+        for (int j = n + first; j < p.room; j += stride) out[j] = 0.f;
+        return;
+    }
+    // this CTA's tokens [t0, t1), a multiple of 4 but for the last one's
+    const int per = ((n + cs - 1) / cs + 3) & ~3, t0 = min(n, rank * per), t1 = min(n, t0 + per);
+    if (CACHED && per > p.cache) {                    // a context longer than the host knew of (the same for the cluster)
+        if (threadIdx.x == 0) set_status(p.status, CA_ERR_DEVICE_BOUNDS);
         return;
     }
     const int lo = p.sink, hi = n - p.recent;         // the middle
     uint32_t left = (uint32_t)(p.budget - p.sink - p.recent), T = 0u, above = 0xffffffffu;   // keys > above are taken
-    if (left > 0) {
-        // the left-th largest key of the middle (which has more than left)
-        uint32_t known = 0u;                          // bits of T that are found
-#pragma unroll 1
-        for (int shift = 21; shift >= 0; shift = shift == 21 ? 10 : shift == 10 ? 0 : -1) {
-            const int bits = shift == 0 ? 10 : 11;
-            for (int j = threadIdx.x; j < kPickBins; j += kPickThreads) hist[j] = 0u;
-            __syncthreads();
-            for (int j = lo + threadIdx.x; j < hi; j += kPickThreads) {
-                const uint32_t k = order_key(in[j]);
-                if ((k & known) == T) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
-            }
-            __syncthreads();
-            // thread 0 has the largest digits
-            constexpr int kPer = kPickBins / kPickThreads;
-            uint32_t c[kPer], mine = 0u;
+    for (int j = threadIdx.x; j < 4 * 256; j += kPickThreads) hist[j >> 8][j & 255] = 0u;
+    if (CACHED) {
+        for (int from = t0 + threadIdx.x; from < t1; from += 8 * kPickThreads) {
+            float w[8];                               // (all on their way together)
 #pragma unroll
-            for (int x = 0; x < kPer; ++x) mine += c[x] = hist[kPickBins - 1 - (threadIdx.x * kPer + x)];
-            uint32_t at = mine;
+            for (int x = 0; x < 8; ++x) w[x] = from + x * kPickThreads < t1 ? in[from + x * kPickThreads] : 0.f;
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const uint32_t o = __shfl_up_sync(kFull, at, off);
-                if (lane >= off) at += o;
-            }
-            if (lane == 31) sums[warp] = at;
-            __syncthreads();
-            for (int w = 0; w < warp; ++w) at += sums[w];
-            at -= mine;                               // keys of larger digits
-            if (at < left && at + mine >= left) {
-#pragma unroll
-                for (int x = 0; x < kPer; ++x) {
-                    if (at < left && at + c[x] >= left) {
-                        found[0] = kPickBins - 1 - (threadIdx.x * kPer + x);
-                        found[1] = left - at;
-                    }
-                    at += c[x];
-                }
-            }
-            __syncthreads();
-            T |= found[0] << shift;
-            left = found[1];
-            known |= ((1u << bits) - 1u) << shift;
-            __syncthreads();
+            for (int x = 0; x < 8; ++x)
+                if (from + x * kPickThreads < t1) held[from + x * kPickThreads - t0] = w[x];
         }
-        above = T;
     }
+    __syncthreads();
+    // four sums from token t on (those from t1 on are anything)
+    auto four = [&](int t, float (&w)[4]) {
+        if constexpr (CACHED) {
+            const float4 v = *reinterpret_cast<const float4*>(held + (t - t0));
+            w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+        } else {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) w[x] = t + x < t1 ? in[t + x] : 0.f;
+        }
+    };
+    uint32_t known = 0u;                              // bits of T that are found
+#pragma unroll 1
+    for (int pass = 0; pass < 4 && left > 0u; ++pass) {
+        const int shift = 24 - 8 * pass, m0 = max(lo, t0), m1 = min(hi, t1);
+#pragma unroll 2
+        for (int t = t0 + 4 * threadIdx.x; t < m1; t += 4 * kPickThreads) {
+            float w[4];
+            four(t, w);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {             // of the keys whose digits so far are T's
+                const uint32_t k = order_key(w[x]);
+                if (t + x >= m0 && t + x < m1 && (k & known) == T) atomicAdd(&hist[pass][k >> shift & 255u], 1u);
+            }
+        }
+        if (cs > 1) cluster_sync_all();
+        else __syncthreads();
+        const uint32_t bin = 255u - threadIdx.x;      // thread 0 has the largest digit
+        uint32_t c = 0u, all;
+        if (cs == 1) c = hist[pass][bin];
+        else
+            for (int r = 0; r < cs; ++r) c += ld_peer(peer_addr(smem_u32(&hist[pass][bin]), r));
+        const uint32_t at = sum_before(c, red, all);  // keys of larger digits
+        if (at < left && at + c >= left) {
+            found[0] = bin;
+            found[1] = left - at;
+        }
+        __syncthreads();
+        T |= found[0] << shift;
+        known |= 255u << shift;
+        left = found[1];                              // (at least 1 once there is any)
+    }
+    if (left > 0u) above = T;
     // left of the keys that equal T are taken, the first ones
-    uint32_t sure0 = 0u, tie0 = 0u;                   // before this round's tokens
-    for (int t0 = 0; t0 < n; t0 += kPickThreads * kPickPer) {
-        const int t = t0 + kPickPer * threadIdx.x;
-        float w[kPickPer];
-        uint32_t sure = 0u, tie = 0u;                 // bit masks
+    auto kinds = [&](int t, const float (&w)[4], uint32_t& sure, uint32_t& tie, int bit) {
 #pragma unroll
-        for (int x = 0; x < kPickPer; ++x) {
-            w[x] = t + x < n ? in[t + x] : 0.f;
+        for (int x = 0; x < 4; ++x) {
             const uint32_t k = order_key(w[x]);
-            const bool forced = t + x < lo || t + x >= hi;
-            if (t + x < n && (forced || k > above)) sure |= 1u << x;
-            else if (t + x < n && left > 0u && k == T) tie |= 1u << x;
+            if (t + x >= t1) continue;
+            if (t + x < lo || t + x >= hi || k > above) sure |= 1u << (bit + x);
+            else if (left > 0u && k == T) tie |= 1u << (bit + x);
         }
-        // both counts of the threads before, in one scan (2048 tokens a round: 16 bits each)
-        const uint32_t mine = __popc(sure) | (__popc(tie) << 16);
-        uint32_t at = mine;
+    };
+    uint32_t sure0 = 0u, tie0 = 0u;                   // before this CTA's tokens, then before each round's
+    if (cs > 1) {
+        uint32_t both = 0u, all;                      // (53248 sums a CTA at most: 16 bits each)
+#pragma unroll 2
+        for (int t = t0 + 4 * threadIdx.x; t < t1; t += 4 * kPickThreads) {
+            float w[4];
+            uint32_t sure = 0u, tie = 0u;
+            four(t, w);
+            kinds(t, w, sure, tie, 0);
+            both += __popc(sure) | (__popc(tie) << 16);
+        }
+        sum_before(both, red, all);
+        if (threadIdx.x == 0) count[0] = all;
+        cluster_sync_all();                           // (all of the cluster's sums are held by now: in place from here on)
+        for (int r = 0; r < rank; ++r) {
+            const uint32_t v = ld_peer(peer_addr(smem_u32(&count[0]), r));
+            sure0 += v & 0xffffu;
+            tie0 += v >> 16;
+        }
+    }
+    for (int from = t0; from < t1; from += kPickThreads * kPickPer) {
+        const int t = from + kPickPer * threadIdx.x;
+        float w[kPickPer / 4][4];
+        uint32_t sure = 0u, tie = 0u, all;            // bit masks
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const uint32_t o = __shfl_up_sync(kFull, at, off);
-            if (lane >= off) at += o;
+        for (int x = 0; x < kPickPer / 4; ++x) {
+            if (t + 4 * x >= t1) break;
+            four(t + 4 * x, w[x]);
+            kinds(t + 4 * x, w[x], sure, tie, 4 * x);
         }
-        if (lane == 31) sums[warp] = at;
-        __syncthreads();                              // (this round's reads of the sums are done too)
-        uint32_t all = 0u;
-        for (int x = 0; x < kPickWarps; ++x) {
-            if (x == warp) at += all;
-            all += sums[x];
-        }
-        at -= mine;
+        // both counts of the threads before, in one scan (4096 tokens a round: 16 bits each);
+        // its barriers also part this round's reads from its writes
+        const uint32_t at = sum_before(__popc(sure) | (__popc(tie) << 16), red, all);
         uint32_t s = sure0 + (at & 0xffffu), e = tie0 + (at >> 16);
 #pragma unroll
         for (int x = 0; x < kPickPer; ++x) {
-            const bool take = (sure >> x & 1u) || ((tie >> x & 1u) && e < left);
-            if (take) {
+            if ((sure >> x & 1u) || ((tie >> x & 1u) && e < left)) {
                 const uint32_t to = s + min(e, left);
                 kept[to] = t + x;
-                out[to] = w[x];                       // (to <= t + x: in place, a place that has been read)
+                out[to] = w[x / 4][x % 4];            // (to <= t + x: in place, a place that has been read)
             }
             s += sure >> x & 1u;
             e += tie >> x & 1u;
         }
         sure0 += all & 0xffffu;
         tie0 += all >> 16;
-        __syncthreads();
     }
-    for (int j = p.budget + threadIdx.x; j < p.room; j += kPickThreads) out[j] = 0.f;
+    if (!CACHED) __syncthreads();
+    for (int j = p.budget + first; j < p.room; j += stride) out[j] = 0.f;
+    if (cs > 1) cluster_sync_all();                   // the others have read this one's counts
 }
 
 // ---------------------------------------------------------------------------
@@ -260,6 +317,42 @@ __global__ void __launch_bounds__(kMoveThreads) move_rows_kernel(const __grid_co
 
 namespace {
 
+// CTAs per row: enough that the card is full twice over, as long as each has some
+// 2048 sums, and so many that a row's sums fit their shared memories (if 8 hold
+// them; else one CTA reads them from memory).
+int run_pick(const Pool& p, dev::PickParams& a, size_t rows, const std::vector<EvictSeq>& seqs, cudaStream_t s) {
+    int64_t most = 1;
+    for (const EvictSeq& e : seqs) most = std::max<int64_t>(most, e.n);
+    int cs = 1;
+    auto share = [&](int k) { return (most + k - 1) / k; };
+    while (cs < 8 && ((rows * cs < (size_t)2 * p.sms && share(2 * cs) >= 2048) || share(cs) + 4 > dev::kPickCache)) cs *= 2;
+    const bool cached = share(cs) + 4 <= dev::kPickCache;
+    if (!cached) cs = 1;
+    a.splits = cs;
+    a.cache = cached ? (int32_t)share(cs) + 4 : 0;
+    const size_t bytes = (size_t)a.cache * sizeof(float);
+    if (rows * cs > (size_t)INT32_MAX) return CA_ERR_UNSUPPORTED;
+    if (cached && cudaFuncSetAttribute(dev::pick_tokens_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       dev::kPickCache * (int)sizeof(float)) != cudaSuccess)
+        return CA_ERR_CUDA;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cs;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3((unsigned)(rows * cs));
+    c.blockDim = dim3(dev::kPickThreads);
+    c.dynamicSmemBytes = bytes;
+    c.stream = s;
+    c.attrs = attr;
+    c.numAttrs = 1;
+    if ((cached ? cudaLaunchKernelEx(&c, dev::pick_tokens_kernel<true>, a) : cudaLaunchKernelEx(&c, dev::pick_tokens_kernel<false>, a)) !=
+        cudaSuccess)
+        return CA_ERR_CUDA;
+    count_launch();
+    return CA_OK;
+}
+
 template <int D, int EB, int N>
 bool pick_chunk(int chunk, unsigned blocks, const dev::MoveArgs<N>& a, cudaStream_t s) {
     if (chunk == 16) dev::move_rows_kernel<16, D, EB, N><<<blocks, dev::kMoveThreads, 0, s>>>(a);
@@ -352,15 +445,14 @@ int launch_evict(const Pool& p, const Sched& s, const std::vector<EvictSeq>& seq
     a.b = s.t.b;
     a.n_heads = kv_heads(c);
     a.capacity = c.capacity_slots;
-    dev::pick_tokens_kernel<<<(unsigned)(per * s.t.b), dev::kPickThreads, 0, cs>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return CA_ERR_CUDA;
-    count_launch();
+    int st = run_pick(p, a, per * s.t.b, seqs, cs);
+    if (st) return st;
     const size_t most = std::max<size_t>(1, std::min<size_t>(dev::kManyMoves, (size_t)INT32_MAX / per));
     for (size_t i = 0; i < ch.size();) {
         const size_t n = std::min(most, ch.size() - i);
-        const int st = n <= dev::kFewMoves    ? moves<dev::kFewMoves>(p, s, ch.data() + i, n, budget, kept, cs)
-                       : n <= dev::kSomeMoves ? moves<dev::kSomeMoves>(p, s, ch.data() + i, n, budget, kept, cs)
-                                              : moves<dev::kManyMoves>(p, s, ch.data() + i, n, budget, kept, cs);
+        st = n <= dev::kFewMoves    ? moves<dev::kFewMoves>(p, s, ch.data() + i, n, budget, kept, cs)
+             : n <= dev::kSomeMoves ? moves<dev::kSomeMoves>(p, s, ch.data() + i, n, budget, kept, cs)
+                                    : moves<dev::kManyMoves>(p, s, ch.data() + i, n, budget, kept, cs);
         if (st) return st;
         i += n;
     }

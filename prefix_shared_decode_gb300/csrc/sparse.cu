@@ -14,26 +14,6 @@
 namespace ca {
 namespace dev {
 
-// ---------------------------------------------------------------------------
-// Clusters: the CTAs that score one context's chunks leave their scores in
-// the first one's shared memory.
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ void cluster_arrive() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_sync_all() {
-    cluster_arrive();
-    cluster_wait();
-}
-__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ void st_peer(uint32_t addr, uint32_t v) {
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
 // What both kernels read of the schedule and the pool.
 struct ListParams {
     const uint16_t* q;            // fp16 [b][H][D]

@@ -112,6 +112,34 @@ def test_long_rows(torch_cuda, n, budget, sink, recent, kind):
     check(x, [0], [0], was, w, budget, sink, recent, kept, out)
 
 
+@pytest.mark.parametrize("n,H", [(5000, 1), (30_001, 1), (300_000, 2), (450_000, 1)])
+def test_weights_in_place_of_long_rows(torch_cuda, n, H):
+    """Rows held by one CTA, by several, and (the longest) by none."""
+    from prefix_shared_decode_gb300 import Pool
+    torch = torch_cuda
+    pool = Pool(1, H, 64, 64, -(-n // 64) + 200, n_kv_heads=H)
+    k = torch.randn(1, n, H, 64, device="cuda", dtype=torch.float16)
+    pool.insert(0, list(range(n)), k, k)
+    rows = k[0].cpu().numpy()
+    rng = np.random.default_rng(n)
+    w = np.round(rng.random((1, 1, H, n + 7)) * 1000).astype(np.float32)        # many ties
+    wd = torch.from_numpy(w).cuda()
+    mirror = [rows[:, h] for h in range(H)]
+    for budget, sink, recent in ((12_000, 5, 9), (4000, 4, 3996)):
+        if budget >= n:
+            continue
+        before = wd.cpu().numpy()
+        m = pool.seq_len(0)
+        kept, out = pool.evict(pool.schedule([0], chunk_lists=True), wd, budget, sink=sink, recent=recent, out=wd)
+        for h in range(H):
+            at = OW.kept(before[0, 0, h, :m], budget, sink, recent)
+            np.testing.assert_array_equal(kept[0, 0, h].cpu().numpy(), at)
+            np.testing.assert_array_equal(wd[0, 0, h, :budget].cpu().numpy(), before[0, 0, h, at])
+            assert not wd[0, 0, h, budget:].any()
+            mirror[h] = mirror[h][at]
+            np.testing.assert_array_equal(pool.read(0)[0][0, :, h].cpu().numpy(), mirror[h])
+
+
 def test_many_chunks_at_once(torch_cuda):
     """More new chunks than one launch lists."""
     from prefix_shared_decode_gb300 import Pool
