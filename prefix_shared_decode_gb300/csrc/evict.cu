@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kPickThreads, 6) pick_tokens_kernel(const Pick
     __shared__ uint32_t hist[4][256];
     __shared__ uint32_t red[kPickWarps];
     __shared__ uint32_t found[2];                     // the digit, places left inside it
-    __shared__ uint32_t count[2];                     // this CTA's keys that are taken, and those that tie
+    __shared__ uint32_t count[1];                     // this CTA's tokens that are taken, those that tie above
     const int cs = p.splits, rank = blockIdx.x % cs;
     const size_t row = blockIdx.x / cs;
     const int i = (int)(row / p.n_heads % p.b);
@@ -100,13 +100,36 @@ __global__ void __launch_bounds__(kPickThreads, 6) pick_tokens_kernel(const Pick
     uint32_t left = (uint32_t)(p.budget - p.sink - p.recent), T = 0u, above = 0xffffffffu;   // keys > above are taken
     for (int j = threadIdx.x; j < 4 * 256; j += kPickThreads) hist[j >> 8][j & 255] = 0u;
     if (CACHED) {
-        for (int from = t0 + threadIdx.x; from < t1; from += 8 * kPickThreads) {
-            float w[8];                               // (all on their way together)
+        // (8 loads a thread on their way together)
+        if (((reinterpret_cast<uintptr_t>(in + t0)) & 15u) == 0) {
+            for (int from = t0 + 4 * threadIdx.x; from < t1; from += 32 * kPickThreads) {
+                float4 w[8];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) w[x] = from + x * kPickThreads < t1 ? in[from + x * kPickThreads] : 0.f;
+                for (int x = 0; x < 8; ++x) {
+                    const int t = from + 4 * x * kPickThreads;
+                    w[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (t + 3 < t1) w[x] = *reinterpret_cast<const float4*>(in + t);
+                    else if (t < t1) {
+                        w[x].x = in[t];
+                        if (t + 1 < t1) w[x].y = in[t + 1];
+                        if (t + 2 < t1) w[x].z = in[t + 2];
+                    }
+                }
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-                if (from + x * kPickThreads < t1) held[from + x * kPickThreads - t0] = w[x];
+                for (int x = 0; x < 8; ++x) {
+                    const int t = from + 4 * x * kPickThreads;
+                    if (t < t1) *reinterpret_cast<float4*>(held + (t - t0)) = w[x];
+                }
+            }
+        } else {
+            for (int from = t0 + threadIdx.x; from < t1; from += 8 * kPickThreads) {
+                float w[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) w[x] = from + x * kPickThreads < t1 ? in[from + x * kPickThreads] : 0.f;
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    if (from + x * kPickThreads < t1) held[from + x * kPickThreads - t0] = w[x];
+            }
         }
     }
     __syncthreads();
@@ -121,6 +144,7 @@ __global__ void __launch_bounds__(kPickThreads, 6) pick_tokens_kernel(const Pick
         }
     };
     uint32_t known = 0u;                              // bits of T that are found
+    uint32_t larger = 0u, equal = 0u;                 // of this CTA's keys: above T (this thread's part), equal to it
 #pragma unroll 1
     for (int pass = 0; pass < 4 && left > 0u; ++pass) {
         const int shift = 24 - 8 * pass, m0 = max(lo, t0), m1 = min(hi, t1);
@@ -147,6 +171,8 @@ __global__ void __launch_bounds__(kPickThreads, 6) pick_tokens_kernel(const Pick
             found[1] = left - at;
         }
         __syncthreads();
+        if (bin > found[0]) larger += hist[pass][bin];
+        equal = hist[pass][found[0]];
         T |= found[0] << shift;
         known |= 255u << shift;
         left = found[1];                              // (at least 1 once there is any)
@@ -164,16 +190,10 @@ __global__ void __launch_bounds__(kPickThreads, 6) pick_tokens_kernel(const Pick
     };
     uint32_t sure0 = 0u, tie0 = 0u;                   // before this CTA's tokens, then before each round's
     if (cs > 1) {
-        uint32_t both = 0u, all;                      // (53248 sums a CTA at most: 16 bits each)
-#pragma unroll 2
-        for (int t = t0 + 4 * threadIdx.x; t < t1; t += 4 * kPickThreads) {
-            float w[4];
-            uint32_t sure = 0u, tie = 0u;
-            four(t, w);
-            kinds(t, w, sure, tie, 0);
-            both += __popc(sure) | (__popc(tie) << 16);
-        }
-        sum_before(both, red, all);
+        uint32_t all;
+        sum_before(larger, red, all);
+        all += max(0, min(t1, lo) - t0) + max(0, t1 - max(t0, hi));      // and the forced ones
+        if (left > 0u) all |= equal << 16;            // (53248 sums a CTA at most: 16 bits each)
         if (threadIdx.x == 0) count[0] = all;
         cluster_sync_all();                           // (all of the cluster's sums are held by now: in place from here on)
         for (int r = 0; r < rank; ++r) {
