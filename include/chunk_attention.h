@@ -502,7 +502,7 @@ int ca_sparse_attention(const ca_pool* pool, const ca_sched* sched, int32_t laye
  * refuse it (CA_ERR_INVALID).
  *
  * ca_cross_attention: q_dev / out_dev fp16 [sum of q_lens][n_heads][head_dim], block
- * after block, 16-byte aligned, not overlapping.  ws_dev as for ca_decode_attention
+ * after block, 16-byte aligned, not overlapping (CA_ERR_INVALID).  ws_dev as for ca_decode_attention
  * (ca_workspace_bytes may give 0; then it may be NULL).  One or two kernels on
  * `stream`, capturable as the decode calls are: replays see what appends have
  * put into the partial last chunks (the mask's n stays the schedule's).  The
@@ -590,8 +590,9 @@ int ca_sched_device_status(const ca_sched* sched, void* stream);
  * a host-only pool's schedule keeps a host word (ca_sched_device_status then
  * reads that one).  CA_ERR_INVALID for a non-negative or unknown code.
  *
- * ca_sched_inject_stall: the next n_calls decode or ca_sparse_attention calls
- * on this schedule run with waits that run out.  A producer warp first waits
+ * ca_sched_inject_stall: the next n_calls decode, ca_sparse_attention,
+ * ca_cross_attention or ca_accumulate_attention calls on this schedule run with
+ * waits that run out.  A producer warp first waits
  * for a barrier phase that nothing completes and issues no copy; that wait and
  * the consumers' first waits give up after their limit (~1 s).  (In CTAs of odd
  * number of ca_sparse_attention, and of the decode calls of a CA_KV_FP4 pool, one

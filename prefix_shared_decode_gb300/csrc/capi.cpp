@@ -41,6 +41,10 @@ int guard(F&& f) {
     }
 }
 
+bool overlap(const void* a, const void* b, size_t bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + bytes && y < x + bytes;
+}
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 int check_cfg(const PoolCfg* c) {
@@ -725,10 +729,8 @@ int ca_accumulate_attention(const ca_pool* pool, const ca_sched* s, int32_t laye
         return CA_ERR_INVALID;
     if (s->t.tok_base[s->t.b] < 0) return CA_ERR_UNSUPPORTED;      // more than 2^31 chunks, sharers counted
     // in place or apart
-    const size_t bytes = (size_t)s->t.b * kv_heads(pool->cfg) * room * sizeof(float);
-    const char* in = reinterpret_cast<const char*>(weights_dev);
-    const char* out = reinterpret_cast<const char*>(out_dev);
-    if (in != out && in < out + bytes && out < in + bytes) return CA_ERR_INVALID;
+    if (weights_dev != out_dev && overlap(weights_dev, out_dev, (size_t)s->t.b * kv_heads(pool->cfg) * room * sizeof(float)))
+        return CA_ERR_INVALID;
     return guard([&] {
         for (int64_t id : s->seq_ids)
             if (pool->seqs.at(id).length > room) return CA_ERR_INVALID;
@@ -749,11 +751,9 @@ int ca_evict(ca_pool* pool, const ca_sched* s, const float* weights_dev, int32_t
         if (!s->dev || room < 1 || !weights_dev || !kept_dev || !out_dev || !aligned(weights_dev, 4) ||
             !aligned(kept_dev, 4) || !aligned(out_dev, 4))
             return CA_ERR_INVALID;
-        const size_t bytes =
-            (size_t)pool->cfg.n_layers * s->t.b * kv_heads(pool->cfg) * room * sizeof(float);
-        const char* in = reinterpret_cast<const char*>(weights_dev);
-        const char* out = reinterpret_cast<const char*>(out_dev);
-        if (in != out && in < out + bytes && out < in + bytes) return CA_ERR_INVALID;
+        if (weights_dev != out_dev &&
+            overlap(weights_dev, out_dev, (size_t)pool->cfg.n_layers * s->t.b * kv_heads(pool->cfg) * room * sizeof(float)))
+            return CA_ERR_INVALID;
     } else if (weights_dev || kept_dev || out_dev) {
         return CA_ERR_INVALID;
     }
@@ -797,6 +797,8 @@ int ca_cross_attention(const ca_pool* pool, const ca_sched* s, int32_t layer, co
     if (st) return st;
     if (s->q_rows == 0) return CA_OK;
     if (!q_dev || !out_dev || !aligned(q_dev, 16) || !aligned(out_dev, 16)) return CA_ERR_INVALID;
+    // (a row's tile reads it again where its context is cut into pieces)
+    if (overlap(q_dev, out_dev, (size_t)s->q_rows * pool->cfg.n_heads * pool->cfg.head_dim * 2)) return CA_ERR_INVALID;
     return guard([&] {
         const DeviceGuard dev(pool->device);
         if (!dev.ok) return CA_ERR_CUDA;

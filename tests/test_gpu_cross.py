@@ -133,9 +133,10 @@ def test_streams_and_replays(torch_cuda):
     cross_attention(x.pool, sched, qd, out=out)
     graph = torch.cuda.CUDAGraph()
     torch.cuda.synchronize()
+    second = torch.empty_like(qd)
     with torch.cuda.graph(graph):
         cross_attention(x.pool, sched, qd, out=out)
-        cross_attention(x.pool, sched, out, out=(second := torch.empty_like(qd)))
+        cross_attention(x.pool, sched, out, out=second)
     for step in range(2):
         if step:
             x.append(0, 3)
@@ -199,6 +200,11 @@ def test_refusals(torch_cuda):
         cross_attention(x.pool, sched, qd, out=qd[:2])
     with pytest.raises(ValueError):
         cross_attention(x.pool, x.pool.schedule([0, 1]), qd)
+    with pytest.raises(CAError, match="INVALID"):          # in place
+        cross_attention(x.pool, sched, qd, out=qd)
+    four = torch.zeros(4, 4, 64, device="cuda", dtype=torch.float16)
+    with pytest.raises(CAError, match="INVALID"):          # overlapping by a row
+        cross_attention(x.pool, sched, four[:3], out=four[1:])
     with pytest.raises(CAError, match="INVALID"):
         cross_attention(x.pool, sched, qd, layer=1)
     two = torch.zeros(2, 4, 64, device="cuda", dtype=torch.float16)
@@ -251,3 +257,79 @@ def test_a_wait_that_runs_out_is_reported(torch_cuda):
     assert sched.device_status() == -8
     check(x, [0, 1], blocks, q, 0, cross_attention(x.pool, sched, qd))
     assert sched.device_status() == 0
+
+
+def test_rows_behind_the_last_block_and_unaligned_outputs(torch_cuda):
+    """Nothing is written past the blocks' rows; outputs that start 16 bytes off
+    a 32-byte boundary."""
+    from prefix_shared_decode_gb300 import cross_attention
+    torch = torch_cuda
+    for kv_dtype, D, G in (("fp16", 64, 3), ("fp16", 128, 4), ("fp8", 128, 2), ("fp16", 256, 2)):
+        x = Cache(torch, 17, kv_dtype, 16, D, G, 1, [1500, 77])
+        blocks = [131, 6]
+        sched = x.pool.schedule([0, 1], q_lens=blocks)
+        q, qd = queries(x, blocks, G)
+        n = qd.numel()
+        room = torch.full((n + 64,), 7.0, device="cuda", dtype=torch.float16)
+        for at in (8, 16):
+            room.fill_(7.0)
+            out = room[at:at + n].view(qd.shape)
+            cross_attention(x.pool, sched, qd, out=out)
+            check(x, [0, 1], blocks, q, 0, out)
+            assert bool((room[:at] == 7).all()) and bool((room[at + n:] == 7).all())
+
+
+def test_two_schedules_at_once(torch_cuda):
+    """Calls on different schedules overlap on two streams."""
+    from prefix_shared_decode_gb300 import cross_attention
+    torch = torch_cuda
+    x = Cache(torch, 23, "fp16", 64, 128, 4, 2, [5000, 3000, 700])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    plans = [([0, 2], [70, 300]), ([1, 0], [200, 33])]
+    work = []
+    for (ids, blocks) in plans:
+        sched = x.pool.schedule(ids, q_lens=blocks)
+        q, qd = queries(x, blocks, 8)
+        work.append((ids, blocks, sched, q, qd, [torch.empty_like(qd) for _ in range(6)]))
+    torch.cuda.synchronize()
+    for k in range(6):
+        for s, (_, _, sched, _, qd, outs) in zip(streams, work):
+            cross_attention(x.pool, sched, qd, out=outs[k], stream=s)
+    torch.cuda.synchronize()
+    for ids, blocks, sched, q, qd, outs in work:
+        check(x, ids, blocks, q, 0, outs[0])
+        assert all(torch.equal(outs[0], o) for o in outs[1:]) and sched.device_status() == 0
+
+
+def test_offsets_past_4_gb(torch_cuda):
+    """Slots whose tiles lie past 2^32 bytes, for every element size."""
+    from prefix_shared_decode_gb300 import Pool, accumulate_attention, cross_attention
+    torch = torch_cuda
+    for kv_dtype, slots in (("fp16", 9000), ("fp8", 18000), ("fp4", 33000)):
+        # 512 KB a slot in fp16: 16 layers of one head of 64 x 128
+        pool = Pool(16, 2, 128, 64, slots, n_kv_heads=1, kv_dtype=kv_dtype)
+        assert pool._tile_bytes() > 2**32
+        g = torch.Generator("cuda").manual_seed(1)
+        fill = slots - 12
+        row = torch.zeros(16, 1, 1, 128, device="cuda", dtype=torch.float16)
+        pool.insert(0, list(range(64 * fill)), row.expand(16, 64 * fill, 1, 128).contiguous(), row.expand(16, 64 * fill, 1, 128).contiguous())
+        k, v = (torch.randn(16, 600, 1, 128, device="cuda", dtype=torch.float16, generator=g) for _ in range(2))
+        pool.insert(1, [10**8 + j for j in range(600)], k, v)
+        pool.remove(0)
+        assert min(pool.seq_slots(1)) >= fill
+        q = torch.randn(40, 2, 128, device="cuda", dtype=torch.float16, generator=g)
+        out = cross_attention(pool, pool.schedule([1], q_lens=[40]), q, layer=15)
+        kk, vv = pool.read(1)
+        x = torch.einsum("mhd,nd->hmn", q.double(), kk[15, :, 0].double()) / 128**0.5
+        p = torch.softmax(x, -1)
+        want = torch.einsum("hmn,nd->mhd", p, vv[15, :, 0].double())
+        near(out.cpu().numpy(), want.cpu().numpy(), torch.einsum("hmn,nd->mhd", p, vv[15, :, 0].double().abs()).cpu().numpy())
+        w = torch.zeros(1, 1, 640, device="cuda")
+        accumulate_attention(pool, pool.schedule([1]), q[:1], w, layer=15)
+        assert float((w[0, 0, :600].double() - p[:, 0].sum(0)).abs().max()) < 1e-5 and not w[0, 0, 600:].any()
+        w = torch.rand(16, 1, 1, 640, device="cuda", generator=g)
+        kept, _ = pool.evict(pool.schedule([1], chunk_lists=True), w, 100, sink=3)
+        k2, v2 = pool.read(1)
+        at = kept[15, 0, 0].long().cpu()
+        assert torch.equal(k2[15, :, 0].cpu(), kk[15, :, 0].cpu()[at]) and torch.equal(v2[15, :, 0].cpu(), vv[15, :, 0].cpu()[at])
+        del pool, k, v, row
