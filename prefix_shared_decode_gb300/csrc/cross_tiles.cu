@@ -336,6 +336,10 @@ cross_tiles_kernel(const __grid_constant__ CUtensorMap tmap, const CrossParams p
                 cp_async16_or_zero(dst + r / 128 * T::kQHalf + swz(r % 128, k, 128),
                                    src + (there ? ((size_t)tok * p.n_heads + x) * D : 0), there);
             }
+            cp_async_wait_all();
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->q_full[qb]));
             if constexpr (T::kQBuffers == 1) {            // the next tile's into L2 meanwhile
                 if (walk.idx + 1 < walk.end) {
                     const BlockItem& n = walk.next.b;
@@ -344,10 +348,6 @@ cross_tiles_kernel(const __grid_constant__ CUtensorMap tmap, const CrossParams p
                         asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + block_row(p, n, i / kLines, D) + i % kLines * 64));
                 }
             }
-            cp_async_wait_all();
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars->q_full[qb]));
             if (++qb == T::kQBuffers) { qb = 0; ph ^= 1u; }
         }
     } else if (warp == kMmaWarp) {
