@@ -21,7 +21,7 @@ namespace dev {
 
 constexpr int kWtWarps = 4, kWtThreads = 32 * (kWtWarps + 1);
 constexpr int kWtTokens = 64;             // tokens of a stage: 16 a warp
-constexpr int kAddThreads = 256, kAddPer = 4, kAddTokens = 4 * kAddPer * kAddThreads;
+constexpr int kAddThreads = 128, kAddPer = 2, kAddTokens = 4 * kAddPer * kAddThreads;
 
 struct WeightParams {
     AttnParams a;                 // the schedule's plan, the pool, q (part_ms: the units' (m, s))
