@@ -8,6 +8,7 @@
 #include <algorithm>
 
 #include "ca_internal.h"
+#include "cluster.cuh"
 #include "fp4.cuh"
 
 namespace ca {

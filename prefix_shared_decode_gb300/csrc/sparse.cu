@@ -9,6 +9,7 @@
 #include <algorithm>
 
 #include "ca_internal.h"
+#include "cluster.cuh"
 #include "fp4.cuh"
 
 namespace ca {
