@@ -9,8 +9,14 @@
 //   12-15     pools of 8 and 4 bits: widen the chunks to fp16 (values in units of
 //             the pool's scales, exact), from a ring of their own
 // S, P and O stay in tensor memory; P takes the place of the scores it came from.
-// While one half is in its softmax, the other half's products run: per step of
-// 128 keys and half, 2 x 128 x 128 x D multiply-adds and 16 K exponentials.
+// While one half is in its softmax, the other half's products run: a step of 128
+// keys and a half takes the tensor cores 8 D clocks (4096 multiply-adds each) and
+// its softmax 512 of exponentials (32 a clock), some 1000 with all the rest.  So 128
+// dims and many rows are bound by the products, fed one tile's worth at a time (a
+// product of 128 x 128 x 16 takes 60 to 75 clocks where 64 are ideal, and the hand-over
+// from half to half some 200); 64 dims by the softmax's latency; few rows by DRAM.
+// 4096 queries of 32 heads over 32768 tokens (8 key/value heads): 1469 us, 1.40
+// PFLOP/s at 1670 MHz under the power limit; of 8-bit pools 20% more a step.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

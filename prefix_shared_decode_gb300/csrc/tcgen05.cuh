@@ -146,7 +146,9 @@ __host__ __device__ constexpr uint32_t f16_shape(int n, bool b_rows) {
 }
 // d (tensor memory) = a b, or d + a b (add); a and b in shared memory.  A whole
 // warp runs these with the same arguments, and one of its threads, always the
-// same, issues.
+// same, issues (with a single thread running the code around them, 4096 queries
+// over 32768 tokens took 1714 us instead of 1617: descriptors reach the
+// instruction from uniform registers).
 template <uint32_t SHAPE>
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, bool add) {
     asm volatile(

@@ -6,6 +6,13 @@
 // queries of all their sharers, then each sequence's own chunks) and leaves the
 // scores, fp32 in log2 units, and each unit's (maximum, sum) of each row; the
 // second joins those per row and adds the weights up.
+//
+// Bound by DRAM where contexts have nothing in common (eight of 128 K tokens, 4
+// rows a key/value head: 345 us for 2.28 GB, 97% of the copy rate, then 37 us for
+// the sums).  Shorter stretches of single rows are bound by the first kernel's
+// latency: 64 sequences of 4096 shared and 512 own tokens 65 us for 309 MB (two
+// CTAs an SM, eight warps; a stage of 64 tokens takes one 1100 clocks), 22 us for the
+// sums.  Stages of 128 tokens leave one CTA an SM (128 us in all instead of 87).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
