@@ -24,7 +24,7 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // fills half of its rows at most.  From traced times of items (a step of 128
 // tokens some 1.8 us, an item's start and end 3, a join 5 to 8).  With them 32
 // tiles over 16384 tokens each are cut (52 us; each into equal pieces, 160 of them
-// on 152 places, 80), and 410 tiles over some 1150 tokens are not (64 us when it was
+// on 152 places, 80), and 410 tiles over some 1220 tokens are not (64 us when it was
 // measured, cut 76).
 constexpr int32_t kPieceTokens = 256, kStepTokens = 128;
 constexpr double kItemCost = 200, kJoinCost = 500, kHalfTileCost = 0.6;
