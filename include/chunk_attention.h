@@ -531,7 +531,7 @@ int ca_cross_attention(const ca_pool* pool, const ca_sched* sched, int32_t layer
  *            as ca_decode_attention's is
  * Two kernels on `stream`; the same inputs give the same sums bit for bit.
  * Errors: as ca_decode_attention; CA_ERR_UNSUPPORTED for more than 2^31 chunks
- * of all the batch's contexts. */
+ * of all the batch's contexts, or a room above 2^31 - 4097. */
 int ca_workspace_bytes_weights(const ca_sched* sched, size_t* bytes_out);
 int ca_accumulate_attention(const ca_pool* pool, const ca_sched* sched, int32_t layer,
                             const void* q_dev, const float* weights_dev, float* out_dev,
@@ -566,7 +566,8 @@ int ca_accumulate_attention(const ca_pool* pool, const ca_sched* sched, int32_t 
  * capturable (CA_ERR_INVALID).  A host-only pool changes its tree alone (NULL
  * pointers).  Errors: CA_ERR_STALE; CA_ERR_OOM, CA_ERR_EXISTS, CA_ERR_CUDA;
  * CA_ERR_INVALID (a schedule without lists, budget < 1 or < sink + recent, a
- * room shorter than a context, repeated new ids, NULL or misaligned pointers).
+ * room shorter than a context, repeated new ids, NULL or misaligned pointers);
+ * CA_ERR_UNSUPPORTED (a budget or room above 2^31 - 4097).
  * On any error the pool is unchanged. */
 int ca_evict(ca_pool* pool, const ca_sched* sched, const float* weights_dev, int32_t room,
              int32_t budget, int32_t sink, int32_t recent, const int64_t* into_ids,

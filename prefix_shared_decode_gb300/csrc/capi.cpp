@@ -45,6 +45,10 @@ bool overlap(const void* a, const void* b, size_t bytes) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return x < y + bytes && y < x + bytes;
 }
+// The longest rows of sums and positions: kernels step past a row's end by less than
+// what is left of 32 bits.
+constexpr int32_t kMostRoom = INT32_MAX - 4096;
+
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 int check_cfg(const PoolCfg* c) {
@@ -583,7 +587,8 @@ static int decode_checks(const ca_pool* pool, const ca_sched* s, int32_t layer, 
     if (!pool || !s || !pool->kv || s->pool != pool || !s->dev || s->blocks != blocks) return CA_ERR_INVALID;
     if (s->generation != pool->generation) return CA_ERR_STALE;
     if (layer < 0 || layer >= pool->cfg.n_layers) return CA_ERR_INVALID;
-    if (need && (!ws_dev || !aligned(ws_dev, 256) || ws_bytes < need)) return CA_ERR_INVALID;
+    if (blocks && need == 0) return CA_OK;
+    if (!ws_dev || !aligned(ws_dev, 256) || ws_bytes < need) return CA_ERR_INVALID;
     return CA_OK;
 }
 
@@ -727,6 +732,7 @@ int ca_accumulate_attention(const ca_pool* pool, const ca_sched* s, int32_t laye
     if (!q_dev || !aligned(q_dev, 16) || !weights_dev || !out_dev || !aligned(weights_dev, 4) || !aligned(out_dev, 4) ||
         room < 1)
         return CA_ERR_INVALID;
+    if (room > kMostRoom) return CA_ERR_UNSUPPORTED;
     if (s->t.tok_base[s->t.b] < 0) return CA_ERR_UNSUPPORTED;      // more than 2^31 chunks, sharers counted
     // in place or apart
     if (weights_dev != out_dev && overlap(weights_dev, out_dev, (size_t)s->t.b * kv_heads(pool->cfg) * room * sizeof(float)))
@@ -747,6 +753,7 @@ int ca_evict(ca_pool* pool, const ca_sched* s, const float* weights_dev, int32_t
     if (s->generation != pool->generation) return CA_ERR_STALE;
     if (!(s->flags & CA_SCHED_CHUNK_LISTS)) return CA_ERR_INVALID;
     if (budget < 1 || sink < 0 || recent < 0 || (int64_t)sink + recent > budget) return CA_ERR_INVALID;
+    if (budget > kMostRoom || room > kMostRoom) return CA_ERR_UNSUPPORTED;
     if (pool->kv) {
         if (!s->dev || room < 1 || !weights_dev || !kept_dev || !out_dev || !aligned(weights_dev, 4) ||
             !aligned(kept_dev, 4) || !aligned(out_dev, 4))

@@ -241,3 +241,14 @@ def test_random_scripts_keep_the_books(lib):
         pool.schedule(list(live)).tables()
     pool.remove_batch(list(live))
     assert pool.stats()["free_slots"] == 400
+
+
+def test_a_budget_too_long_for_32_bits_is_refused(lib):
+    pool = make(lib, cap=12)
+    pool.insert(0, toks(0, 90))
+    lists = pool.schedule([0], chunk_lists=True)
+    was = state(pool, [0])
+    for budget in (2**31 - 4096, 2**31 - 1):
+        assert lib.ca_evict(pool.handle, lists.handle, None, 0, budget, 0, 0, None, None, None, None) == -9
+    assert lib.ca_evict(pool.handle, lists.handle, None, 2**31 - 1, 20, 0, 0, None, None, None, None) == -9
+    assert state(pool, [0]) == was

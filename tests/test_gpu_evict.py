@@ -265,3 +265,16 @@ def test_refusals(torch_cuda):
     x.pool.evict(sched, w, 20)
     with pytest.raises(CAError, match="STALE"):
         x.pool.evict(sched, w, 20)
+
+
+def test_rows_too_long_for_32_bits_are_refused(torch_cuda):
+    from prefix_shared_decode_gb300 import capi
+    torch = torch_cuda
+    x = Cache(torch, 8, "fp16", 32, 64, 1, 2, [100, 50])
+    sched = x.pool.schedule([0, 1], chunk_lists=True)
+    w, kept = torch.zeros(1, 2, 2, 100, device="cuda"), torch.zeros(1, 2, 2, 20, dtype=torch.int32, device="cuda")
+    was = x.pool.stats()
+    for room, budget in ((2**31 - 4096, 20), (2**31 - 1, 20), (100, 2**31 - 1)):
+        assert capi.lib().ca_evict(x.pool.handle, sched.handle, w.data_ptr(), room, budget, 0, 0, None, kept.data_ptr(),
+                                   w.data_ptr(), None) == -9
+    assert x.pool.stats() == was
