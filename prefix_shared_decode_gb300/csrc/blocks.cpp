@@ -111,7 +111,7 @@ int build_blocks(const Pool& p, const int64_t* seq_ids, int32_t b, const int32_t
     } else {
         // A cut falls on a whole step of the kernels, and on a tile's end where it
         // would leave a piece of fewer than kPieceTokens.
-        n_places = std::max<int64_t>(1, (int64_t)std::ceil(total / share));
+        n_places = std::clamp<int64_t>((int64_t)std::ceil(total / share), 1, most);   // (the quotient may round up)
         const int32_t grain = std::max(1, kStepTokens / c), least = std::max(1, kPieceTokens / c);
         double x = 0;
         auto next_cut = [&] { return (double)begin.size() * share; };
