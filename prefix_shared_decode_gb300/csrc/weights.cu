@@ -508,6 +508,9 @@ __global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const WeightPa
     // (not earlier: the next kernel's CTAs would take this one's registers while
     // they wait, 64 sequences back to back 111 us)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // (a token that a row does not see, or past the context, gets nothing of it even
+    // where the row's sum is not a number)
+    auto weight = [](float x, float l) { return x == -INFINITY ? 0.f : ex2(x - l); };
     for (int r = 0; r < RW; ++r) {
         const float l = lse[r];
         float4 y[kAddPer];
@@ -516,10 +519,10 @@ __global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const WeightPa
         if (r + 1 < RW) load_row(r + 1);
 #pragma unroll
         for (int k = 0; k < kAddPer; ++k) {
-            w[k].x += ex2(y[k].x - l);
-            w[k].y += ex2(y[k].y - l);
-            w[k].z += ex2(y[k].z - l);
-            w[k].w += ex2(y[k].w - l);
+            w[k].x += weight(y[k].x, l);
+            w[k].y += weight(y[k].y, l);
+            w[k].z += weight(y[k].z, l);
+            w[k].w += weight(y[k].w, l);
         }
     }
 #pragma unroll
@@ -577,17 +580,26 @@ int launch_weights(const Pool& p, const Sched& s, int32_t layer, const void* q, 
     w.a = attn_params(p, s, layer, q, nullptr, scale, ws);
     w.a.part_o = nullptr;
     w.a.part_ms = reinterpret_cast<float2*>(w8 + s.ws.weights_ms);
-    w.a.test_stall = 0;
-    if (s.stall_calls > 0) {
-        w.a.test_stall = 1;
-        --s.stall_calls;
-    }
     w.tok_base = reinterpret_cast<const int32_t*>(static_cast<unsigned char*>(s.dev) + s.layout.tok_base);
     w.scores = reinterpret_cast<float*>(w8 + s.ws.weights_scores);
     w.in = in;
     w.out = out;
     w.room = room;
     w.chunk = c.chunk;
+    int64_t most = in == out ? 0 : room;
+    for (int32_t pos = 0; pos < s.t.b; ++pos)
+        most = std::max<int64_t>(most, (int64_t)(s.t.tok_base[pos + 1] - s.t.tok_base[pos]) * c.chunk);
+    // blocks of about equal length, whole rounds of the threads
+    constexpr int64_t round = 4 * dev::kAddThreads;
+    w.blocks = (int32_t)((most + dev::kAddTokens - 1) / dev::kAddTokens);
+    w.block_tokens = (int32_t)(((most + w.blocks - 1) / w.blocks + round - 1) / round * round);
+    const int64_t adds = (int64_t)w.blocks * s.t.b * kv_heads(c);
+    if (adds > INT32_MAX) return CA_ERR_UNSUPPORTED;
+    w.a.test_stall = 0;
+    if (s.stall_calls > 0) {
+        w.a.test_stall = 1;
+        --s.stall_calls;
+    }
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     // Both are programmatic dependents of what precedes them in the stream.
     cudaLaunchAttribute attr[1];
@@ -608,15 +620,6 @@ int launch_weights(const Pool& p, const Sched& s, int32_t layer, const void* q, 
     }
     if (st) return st;
     count_launch();
-    int64_t most = in == out ? 0 : room;
-    for (int32_t pos = 0; pos < s.t.b; ++pos)
-        most = std::max<int64_t>(most, (int64_t)(s.t.tok_base[pos + 1] - s.t.tok_base[pos]) * c.chunk);
-    // blocks of about equal length, whole rounds of the threads
-    constexpr int64_t round = 4 * dev::kAddThreads;
-    w.blocks = (int32_t)((most + dev::kAddTokens - 1) / dev::kAddTokens);
-    w.block_tokens = (int32_t)(((most + w.blocks - 1) / w.blocks + round - 1) / round * round);
-    const int64_t adds = (int64_t)w.blocks * s.t.b * kv_heads(c);
-    if (adds > INT32_MAX) return CA_ERR_UNSUPPORTED;
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3((unsigned)adds);
     lc.blockDim = dim3(dev::kAddThreads);

@@ -234,3 +234,37 @@ def test_refusals(torch_cuda):
     with pytest.raises(CAError, match="STALE"):
         accumulate_attention(x.pool, sched, qd, torch.zeros(2, 2, 200, device="cuda"))
     assert float(w.abs().max()) == 0
+
+
+@pytest.mark.parametrize("kv_dtype,c,D,G,Hkv", POOLS)
+def test_a_query_that_is_no_number_stays_in_its_context(torch_cuda, kv_dtype, c, D, G, Hkv):
+    """The sums of its own sequence and head are NaN over the context; those
+    behind the context, and every other row's, are as without it."""
+    from prefix_shared_decode_gb300 import accumulate_attention
+    torch = torch_cuda
+    lens, room = [c + 3, 3 * c - 1, 1], 4 * c + 2
+    x = Cache(torch, 31, kv_dtype, c, D, G, Hkv, lens)
+    sched = x.pool.schedule([0, 1, 2])
+    q, qd = queries(x, 3, 1, Hkv * G)
+    start = x.rng.random((3, Hkv, room)).astype(np.float32)
+    clean, w, apart = x.dev(start), x.dev(start), torch.full((3, Hkv, room), -1.0, device="cuda")
+    accumulate_attention(x.pool, sched, qd, clean)
+    qd[1, G - 1, 0] = float("nan")                         # of sequence 1 and head 0
+    accumulate_attention(x.pool, sched, qd, w.clone(), out=apart)
+    accumulate_attention(x.pool, sched, qd, w)
+    want = clean.cpu().numpy()
+    want[1, 0, :lens[1]] = np.nan
+    np.testing.assert_array_equal(w.cpu().numpy(), want)
+    np.testing.assert_array_equal(apart.cpu().numpy(), want)
+
+
+def test_rows_too_long_for_32_bits_are_refused(torch_cuda):
+    from prefix_shared_decode_gb300 import capi
+    torch = torch_cuda
+    x = Cache(torch, 9, "fp16", 32, 64, 2, 2, [70, 33])
+    sched = x.pool.schedule([0, 1])
+    q, qd = queries(x, 2, 1, 4)
+    w, ws = torch.zeros(2, 2, 100, device="cuda"), torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    for room in (2**31 - 4096, 2**31 - 1):
+        assert capi.lib().ca_accumulate_attention(x.pool.handle, sched.handle, 0, qd.data_ptr(), w.data_ptr(), w.data_ptr(),
+                                                  room, 0.1, ws.data_ptr(), ws.numel(), None) == -9
