@@ -511,16 +511,11 @@ cross_tiles_kernel(const __grid_constant__ CUtensorMap tmap, const CrossParams p
                     // at most 2^-21 of the largest.  It rises by whole numbers, so that scaling
                     // the outputs rounds nothing; the step's weights are then taken again (the
                     // scores are overwritten after this check).
-                    if (j == 0) {
-                        float top = -INFINITY;
-#pragma unroll 1
-                        for (int c = 0; c < NC; ++c) {
-                            uint32_t x[32];
-                            tmem_ld32(s_at + 32 * c, x);
-                            tmem_wait_ld();
-                            top = fmaxf(top, largest(x));
-                        }
-                        top *= scale;
+                    if (j == 0) {                             // (from the first 32: what exceeds them by 7 is rare)
+                        uint32_t x[32];
+                        tmem_ld32(s_at, x);
+                        tmem_wait_ld();
+                        const float top = largest(x) * scale;
                         if (top > -INFINITY) m = ceilf(top) - 8.f;
                     }
                     uint64_t add[2] = {0ull, 0ull};
