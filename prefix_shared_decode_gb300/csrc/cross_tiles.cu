@@ -492,9 +492,10 @@ cross_tiles_kernel(const __grid_constant__ CUtensorMap tmap, const CrossParams p
                     constexpr int NC = T::kKeys / 32;         // 32 columns at a time
                     if (turned || t.b.c_begin * C + (j + 1) * T::kKeys - 1 > all_see) {
                         // few steps need it: signs turned and hidden tokens masked in place
-                        const int see = last - (t.b.c_begin * C + j * T::kKeys);
+                        // (from the first column on that some row of the warp does not see)
+                        const int at = t.b.c_begin * C + j * T::kKeys, see = last - at;
 #pragma unroll 1
-                        for (int c = 0; c < NC; ++c) {
+                        for (int c = turned ? 0 : max(0, all_see + 1 - at) / 32; c < NC; ++c) {
                             uint32_t x[32];
                             tmem_ld32(s_at + 32 * c, x);
                             tmem_wait_ld();
