@@ -14,7 +14,10 @@
 // its softmax 512 of exponentials (32 a clock), some 1000 with all the rest.  So 128
 // dims and many rows are bound by the products, fed one tile's worth at a time (a
 // product of 128 x 128 x 16 takes 60 to 75 clocks where 64 are ideal, and the hand-over
-// from half to half some 200); 64 dims by the softmax's latency; few rows by DRAM.
+// from half to half some 200); 64 dims by the hand-overs themselves (2048 queries of 32
+// heads over 8192 tokens: 148 us, 113 if the softmax's warps only pass scores on and
+// 133 with half the products; steps of 192 keys 141, but 2% more over some 1200
+// tokens, whose last step is then emptier); few rows by DRAM.
 // 4096 queries of 32 heads over 32768 tokens (8 key/value heads): 1469 us, 1.40
 // PFLOP/s at 1670 MHz under the power limit; of 8-bit pools 20% more a step.
 #include <cuda.h>
