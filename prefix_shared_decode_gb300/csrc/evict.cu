@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kPickThreads, 6) pick_tokens_kernel(const Pick
             else if (left > 0u && k == T) tie |= 1u << (bit + x);
         }
     };
-    uint32_t sure0 = 0u, tie0 = 0u;                   // before this CTA's tokens, then before each round's
+    uint32_t sure0 = 0u, tie0 = 0u;                   // before this CTA's tokens, then before each stretch's
     if (cs > 1) {
         uint32_t all;
         sum_before(larger, red, all);
@@ -217,8 +217,8 @@ __global__ void __launch_bounds__(kPickThreads, 6) pick_tokens_kernel(const Pick
             four(t + 4 * x, w[x]);
             kinds(t + 4 * x, w[x], sure, tie, 4 * x);
         }
-        // both counts of the threads before, in one scan (4096 tokens a round: 16 bits each);
-        // its barriers also part this round's reads from its writes
+        // both counts of the threads before, in one scan (4096 tokens a stretch: 16 bits each);
+        // its barriers also part this stretch's reads from its writes
         const uint32_t at = sum_before(__popc(sure) | (__popc(tie) << 16), red, all);
         uint32_t s = sure0 + (at & 0xffffu), e = tie0 + (at >> 16);
 #pragma unroll
