@@ -582,19 +582,16 @@ int ca_workspace_bytes_host(const ca_sched* s, size_t* bytes_out) {
     return CA_OK;
 }
 
-static int decode_checks(const ca_pool* pool, const ca_sched* s, int32_t layer, void* ws_dev,
-                         size_t ws_bytes, size_t need, bool blocks = false) {
-    if (!pool || !s || !pool->kv || s->pool != pool || !s->dev || s->blocks != blocks) return CA_ERR_INVALID;
-    if (s->generation != pool->generation) return CA_ERR_STALE;
-    if (layer < 0 || layer >= pool->cfg.n_layers) return CA_ERR_INVALID;
-    if (blocks && need == 0) return CA_OK;
-    if (!ws_dev || !aligned(ws_dev, 256) || ws_bytes < need) return CA_ERR_INVALID;
-    return CA_OK;
-}
-
 }  // extern "C"
 
 namespace ca {
+int attention_checks(const Pool* pool, const Sched* s, int32_t layer, bool blocks) {
+    if (!pool || !s || !pool->kv || s->pool != pool || !s->dev || s->blocks != blocks) return CA_ERR_INVALID;
+    if (s->generation != pool->generation) return CA_ERR_STALE;
+    if (layer < 0 || layer >= pool->cfg.n_layers) return CA_ERR_INVALID;
+    return CA_OK;
+}
+
 AttnParams attn_params(const Pool& pool, const Sched& s, int32_t layer, const void* q, void* out,
                        float scale, void* ws_dev) {
     unsigned char* dev = static_cast<unsigned char*>(s.dev);
@@ -634,6 +631,14 @@ AttnParams attn_params(const Pool& pool, const Sched& s, int32_t layer, const vo
 }  // namespace ca
 
 extern "C" {
+
+static int decode_checks(const ca_pool* pool, const ca_sched* s, int32_t layer, void* ws_dev,
+                         size_t ws_bytes, size_t need, bool blocks = false) {
+    const int st = attention_checks(pool, s, layer, blocks);
+    if (st || (blocks && need == 0)) return st;
+    if (!ws_dev || !aligned(ws_dev, 256) || ws_bytes < need) return CA_ERR_INVALID;
+    return CA_OK;
+}
 
 static int decode_launch(const ca_pool* pool, const ca_sched* s, int32_t layer, const void* q,
                          void* out, float scale, void* ws_dev, void* stream) {

@@ -60,9 +60,8 @@ extern "C" int ca_decode_attention_static_ws(const ca_pool* pool_, const ca_sche
                                              float scale, void* stream) {
     const ca::Pool* pool = reinterpret_cast<const ca::Pool*>(pool_);
     const ca::Sched* s = reinterpret_cast<const ca::Sched*>(sched_);
-    if (!pool || !s || !pool->kv || s->pool != pool || !s->dev) return CA_ERR_INVALID;
-    if (s->generation != pool->generation) return CA_ERR_STALE;
-    if (layer < 0 || layer >= pool->cfg.n_layers) return CA_ERR_INVALID;
+    int st = ca::attention_checks(pool, s, layer, false);
+    if (st) return st;
     if (!q_dev || !out_dev || (reinterpret_cast<uintptr_t>(q_dev) & 15) ||
         (reinterpret_cast<uintptr_t>(out_dev) & 15))
         return CA_ERR_INVALID;
@@ -71,7 +70,7 @@ extern "C" int ca_decode_attention_static_ws(const ca_pool* pool_, const ca_sche
     if (cudaGetDevice(&device) != cudaSuccess) return CA_ERR_CUDA;
     if (device != pool->device) return CA_ERR_INVALID;
     void* ws = nullptr;
-    int st = static_ws_address(device, &ws);
+    st = static_ws_address(device, &ws);
     if (st) return st;
     const ca::AttnParams a = ca::attn_params(*pool, *s, layer, q_dev, out_dev, scale, ws);
     return ca::launch_attention(*pool, *s, a, stream);

@@ -1,4 +1,8 @@
 """Schedules of query blocks on host-only pools: what is refused, and reuse."""
+import os
+import shutil
+import subprocess
+
 import pytest
 
 
@@ -49,3 +53,47 @@ def test_reuse(lib):
     with pytest.raises(Exception):
         pool.schedule([0, 9], q_lens=[300, 4], reuse=sched)
     assert sched._key() == key and sched.workspace_bytes() == need
+
+
+STATIC_WS = r"""
+// A schedule of query blocks handed to ca_decode_attention_static_ws: the pool and
+// the schedule are made to look like a device's, which nothing reads before the
+// call's checks are through.
+#include "ca_internal.h"
+#include <cstdio>
+int main() {
+    const ca_pool_config cfg{1, 4, 64, 16, 100, 0u};
+    ca_pool* pool = nullptr;
+    ca_sched* sched[2] = {nullptr, nullptr};
+    int32_t tokens[40], m = 3;
+    const int64_t id = 0;
+    for (int i = 0; i < 40; ++i) tokens[i] = i;
+    if (ca_pool_create(&cfg, nullptr, 0, &pool) || ca_insert_tokens(pool, 0, tokens, 40, nullptr, nullptr, nullptr, nullptr) ||
+        ca_build_schedule_blocks(pool, &id, 1, &m, 0, &sched[0], nullptr) || ca_build_schedule(pool, &id, 1, &sched[1], nullptr))
+        return 2;
+    alignas(1024) static unsigned char bytes[1024];
+    reinterpret_cast<ca::Pool*>(pool)->kv = bytes;
+    reinterpret_cast<ca::Pool*>(pool)->device = -1;     // no device: the call ends there at the latest
+    for (ca_sched* s : sched) {
+        reinterpret_cast<ca::Sched*>(s)->dev = bytes;
+        std::printf("%d %d\n", ca_decode_attention_static_ws(pool, s, 0, bytes, bytes + 512, 1.f, nullptr),
+                    ca_decode_attention_static_ws(pool, s, 1, bytes, bytes + 512, 1.f, nullptr));
+    }
+}
+"""
+
+
+def test_the_call_without_a_workspace_refuses_them(lib, tmp_path):
+    from prefix_shared_decode_gb300 import build, capi
+    cxx = shutil.which("g++")
+    if cxx is None:
+        pytest.skip("no C++ compiler")
+    src, exe = tmp_path / "static_ws.cpp", tmp_path / "static_ws"
+    src.write_text(STATIC_WS)
+    subprocess.run([cxx, "-std=c++17", f"-I{build.CSRC}", f"-I{build._cuda_home()}/include", str(src), "-o", str(exe),
+                    capi.LIB_PATH, f"-Wl,-rpath,{os.path.dirname(capi.LIB_PATH)}"], check=True)
+    run = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert run.returncode == 0, (run.returncode, run.stderr)
+    blocks, plain = (line.split() for line in run.stdout.splitlines())
+    assert blocks == ["-1", "-1"]
+    assert plain[0] in ("-1", "-6") and plain[1] == "-1"     # no such device, or none at all

@@ -333,3 +333,17 @@ def test_offsets_past_4_gb(torch_cuda):
         at = kept[15, 0, 0].long().cpu()
         assert torch.equal(k2[15, :, 0].cpu(), kk[15, :, 0].cpu()[at]) and torch.equal(v2[15, :, 0].cpu(), vv[15, :, 0].cpu()[at])
         del pool, k, v, row
+
+
+def test_the_call_without_a_workspace_refuses_block_schedules(torch_cuda):
+    """Whatever their pieces need; the schedule serves its own call as before."""
+    from prefix_shared_decode_gb300 import capi, cross_attention
+    torch = torch_cuda
+    x = Cache(torch, 9, "fp16", 32, 64, 2, 2, [70, 3000])
+    for blocks in ([3, 0], [2, 2]):
+        sched = x.pool.schedule([0, 1], q_lens=blocks)
+        q, qd = queries(x, blocks, 4)
+        four = torch.zeros(4, 4, 64, device="cuda", dtype=torch.float16)
+        assert capi.lib().ca_decode_attention_static_ws(x.pool.handle, sched.handle, 0, four.data_ptr(),
+                                                        torch.empty_like(four).data_ptr(), 1.0, None) == -1
+        check(x, [0, 1], blocks, q, 0, cross_attention(x.pool, sched, qd))
