@@ -97,7 +97,9 @@ extern "C" {
  * [CA §4.1, Table 3]. */
 #define CA_SCHED_NO_TPP      1u
 /* Multi-token queries (ca_build_schedule_ex): query token j of a sequence
- * whose context holds n tokens sees only tokens [0, n - q_len + j]. */
+ * whose context holds n tokens sees only tokens [0, n - q_len + j].  n is the
+ * length that the schedule found: after an append, in place or not, build it
+ * again (a call on one that was not still counts from the old length). */
 #define CA_SCHED_CAUSAL      2u
 /* Upload each sequence's chunk list with the schedule: ca_select_chunks and
  * ca_sparse_attention need it (every other call ignores it). */
@@ -228,8 +230,9 @@ int ca_insert_batch(ca_pool* pool, int32_t n_seqs, const int64_t* seq_ids,
  * holds an equal one).  k_dev / v_dev: fp16 [n_layers][n][n_kv_heads][head_dim]
  * for the n appended tokens.  Filling the partial chunk does not change the
  * tree's structure, so schedules stay valid (their exported ntok values are
- * as of their build; the kernels read current counts from the pool); growing
- * a chunk bumps the generation (schedules go stale), as the pages' "a full
+ * as of their build; the kernels read current counts from the pool), but those
+ * with CA_SCHED_CAUSAL must be built again for the mask to count from the new
+ * end; growing a chunk bumps the generation (schedules go stale), as the pages' "a full
  * chunk triggers a context copy" [CA §3.3].  n_new_chunks_out (may be NULL)
  * receives the number of chunks grown.  Errors: CA_ERR_NOT_FOUND, CA_ERR_OOM,
  * CA_ERR_INVALID, CA_ERR_CUDA; on error the pool is unchanged. */
@@ -281,9 +284,10 @@ int ca_seq_lengths(const ca_pool* pool, int32_t n_seqs, const int64_t* seq_ids,
  * (one contiguous range of a depth-first batch order), each sequence's
  * sequence-first chunks, and the merge lists; plus the kernels' work plan.
  * *inout == NULL allocates a schedule; otherwise it is reused, and when the
- * pool has not changed since it was built and the batch is identical it is
+ * tree has not changed since it was built and the batch is identical it is
  * returned untouched (the pages: context copies are cached until the tree
- * changes [CA §3.3]).  Tables are copied to a library-owned device buffer
+ * changes [CA §3.3]); one with CA_SCHED_CAUSAL only while its contexts also have
+ * the lengths they had.  Tables are copied to a library-owned device buffer
  * with cudaMemcpyAsync on `stream` (none for a host-only pool).
  * Errors: CA_ERR_NOT_FOUND (unknown seq_id), CA_ERR_INVALID (b < 1, duplicate
  * ids), CA_ERR_CUDA. */
@@ -385,7 +389,8 @@ int ca_workspace_bytes(const ca_sched* sched, size_t* bytes_out);
  * stays valid while its schedule is unchanged: appends that fit the
  * sequences' partial last chunks keep it (the kernels read each chunk's
  * token count from the pool); anything that rebuilds the schedule (a grown
- * chunk, an insert or remove, another batch) needs a new capture.  Build
+ * chunk, an insert or remove, another batch, with CA_SCHED_CAUSAL any append)
+ * needs a new capture.  Build
  * schedules outside capture (ca_build_schedule allocates).
  * Errors: CA_ERR_STALE if the pool changed after the schedule was built;
  * CA_ERR_INVALID for a host-only pool, bad layer, NULL or misaligned pointers

@@ -378,7 +378,8 @@ class Pool:
         order).  Passing the previous schedule reuses it when nothing changed.
         ``q_len`` > 1: that many query tokens per sequence (q / out become
         [b, q_len, H, D]); ``causal``: token j sees context tokens
-        [0, len - q_len + j] only.  ``chunk_lists``: also upload each
+        [0, len - q_len + j] only, ``len`` as this call finds it (call it
+        again after every append).  ``chunk_lists``: also upload each
         sequence's chunk list, for ``select_chunks``,
         ``sparse_decode_attention`` and ``evict``.  ``q_lens``: a block of
         that many queries for each sequence (0 and more; an id may repeat),

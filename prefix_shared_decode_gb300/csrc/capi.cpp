@@ -136,10 +136,13 @@ bool room_for_plan(Sched& s) {
     return true;
 }
 
-// Whether the contexts of a schedule of query blocks are as long as when it was built.
-bool same_lengths(const Pool& p, const Sched& s) {
+// Whether a schedule may be reused as far as its contexts' lengths go: a mask
+// counts from their ends, which appends in place move.  (Lengths lie in the order
+// of the call for query blocks, else in depth-first order.)
+bool lengths_stand(const Pool& p, const Sched& s) {
+    if (!(s.flags & CA_SCHED_CAUSAL)) return true;
     for (size_t i = 0; i < s.seq_ids.size(); ++i)
-        if (p.seqs.at(s.seq_ids[i]).length != s.t.ctx_len[i]) return false;
+        if (p.seqs.at(s.seq_ids[s.blocks ? i : (size_t)s.t.seq_perm[i]]).length != s.t.ctx_len[i]) return false;
     return true;
 }
 
@@ -414,7 +417,7 @@ int ca_build_schedule_ex(ca_pool* pool, const int64_t* seq_ids, int32_t b, int32
         ca_sched* s = *inout;
         if (s && s->pool == pool && !s->blocks && s->generation == pool->generation && s->flags == flags &&
             s->q_len == q_len && (int32_t)s->seq_ids.size() == b &&
-            std::equal(seq_ids, seq_ids + b, s->seq_ids.begin()))
+            std::equal(seq_ids, seq_ids + b, s->seq_ids.begin()) && lengths_stand(*pool, *s))
             return CA_OK;                   // context unchanged since the tree last changed
         if (flags & CA_SCHED_CAUSAL)
             for (int32_t i = 0; i < b; ++i) {
@@ -475,9 +478,7 @@ int ca_build_schedule_blocks(ca_pool* pool, const int64_t* seq_ids, int32_t b, c
         ca_sched* s = *inout;
         if (s && s->pool == pool && s->blocks && s->generation == pool->generation && s->flags == flags &&
             (int32_t)s->seq_ids.size() == b && std::equal(seq_ids, seq_ids + b, s->seq_ids.begin()) &&
-            std::equal(q_lens, q_lens + b, s->q_lens.begin()) &&
-            // (the mask counts from the contexts' ends, which appends in place move)
-            (!(flags & CA_SCHED_CAUSAL) || same_lengths(*pool, *s)))
+            std::equal(q_lens, q_lens + b, s->q_lens.begin()) && lengths_stand(*pool, *s))
             return CA_OK;
         std::unique_ptr<ca_sched, SchedFree> fresh;
         if (!s) {

@@ -268,3 +268,35 @@ def test_rows_too_long_for_32_bits_are_refused(torch_cuda):
     for room in (2**31 - 4096, 2**31 - 1):
         assert capi.lib().ca_accumulate_attention(x.pool.handle, sched.handle, 0, qd.data_ptr(), w.data_ptr(), w.data_ptr(),
                                                   room, 0.1, ws.data_ptr(), ws.numel(), None) == -9
+
+
+@pytest.mark.parametrize("kv_dtype,c,D,G,Hkv,q_len", [("fp16", 64, 128, 4, 2, 4), ("fp16", 16, 64, 2, 2, 3), ("fp16", 32, 256, 2, 1, 5),
+                                                      ("fp8", 64, 128, 3, 2, 5), ("fp4", 64, 128, 4, 1, 16), ("fp4", 16, 64, 1, 3, 2)])
+def test_causal_steps_that_append_in_place(torch_cuda, kv_dtype, c, D, G, Hkv, q_len):
+    """Steps that append their tokens and then ask for the schedule again: the mask
+    counts from the new ends although no chunk grew.  Sums, and the decode call on
+    the same schedule; contexts listed in another order than they lie in the tree."""
+    from oracle import cross as OC
+    from prefix_shared_decode_gb300 import accumulate_attention, decode_attention
+    from tests.test_gpu_fp4 import near
+    torch = torch_cuda
+    lens = [3 * c + 1, 2 * c + q_len, 5 * c + 2]
+    x = Cache(torch, c + q_len, kv_dtype, c, D, G, Hkv, lens, ks=0.75, vs=1.25, shared=2 * c)
+    ids = [2, 0, 1]
+    w = torch.zeros(3, Hkv, 6 * c, device="cuda")
+    sched = None
+    for step in range(3):
+        if step:
+            slots = [x.pool.seq_slots(i) for i in ids]
+            x.append(ids[step - 1], min(q_len, c // 4))
+            assert [x.pool.seq_slots(i) for i in ids] == slots
+        sched = x.pool.schedule(ids, q_len=q_len, causal=True, reuse=sched)
+        q, qd = queries(x, 3, q_len, Hkv * G)
+        before = w.cpu().numpy()
+        accumulate_attention(x.pool, sched, qd, w)
+        check(x, ids, q, 0, before, w.cpu().numpy(), causal=True)
+        out = decode_attention(x.pool, sched, qd).cpu().numpy()
+        for r, i in enumerate(ids):
+            k, v = held(x.k[i][0], x.kv_dtype, x.ks), held(x.v[i][0], x.kv_dtype, x.vs)
+            near(out[r], OC.attention(q[r], k, v, D ** -0.5, True), OC.attention(q[r], k, np.abs(v), D ** -0.5, True))
+    assert sched.device_status() == 0

@@ -259,3 +259,33 @@ def test_schedule_reuse_fast_path_and_staleness_key(lib):
     assert s._key() != key
     pool.schedule(batch, reuse=s)
     assert s._key() != key and pool.schedule(batch, reuse=s)._key() == s._key()
+
+
+def test_a_causal_schedule_is_built_again_after_an_append_in_place(lib):
+    """Its mask counts from the contexts' ends.  Tables hold the token counts as of
+    their build, which shows which ones were built again: those without a mask, and
+    those of one query token, are not."""
+    from prefix_shared_decode_gb300 import Pool
+    c = 16
+    pool = Pool(1, 8, 64, c, 100, host_only=True, n_kv_heads=2)
+    for i, n in enumerate((c + 5, 2 * c + 3, c + 9)):        # all behind a shared chunk
+        pool.insert(i, list(range(c)) + [1000 * (i + 1) + j for j in range(n - c)])
+    batch = [2, 0, 1]                                        # not the depth-first order
+
+    def last_counts(s):
+        t = s.tables()
+        ends = t["sf_chunks"][t["sf_offsets"][1:] - 1, 1]
+        return {batch[int(r)]: int(n) for r, n in zip(t["seq_perm"], ends)}
+
+    masked = pool.schedule(batch, q_len=4, causal=True)
+    full, one = pool.schedule(batch, q_len=4), pool.schedule(batch, causal=True)
+    before = last_counts(masked)
+    assert before == {0: 5, 1: 3, 2: 9} == last_counts(full) == last_counts(one)
+    for i, n in ((1, 4), (2, 1)):
+        assert pool.append(i, [7000 + 10 * i + j for j in range(n)]) == 0
+        assert last_counts(masked) == before                 # not before it is asked for
+        assert pool.schedule(batch, q_len=4, causal=True, reuse=masked) is masked
+        before[i] += n
+        assert last_counts(masked) == before
+        for s, kw in ((full, dict(q_len=4)), (one, dict(causal=True))):
+            assert last_counts(pool.schedule(batch, reuse=s, **kw)) == {0: 5, 1: 3, 2: 9}
