@@ -446,10 +446,19 @@ class Schedule:
         self._ids, self._ids_ptr, self._ids_list, self._flags = None, None, None, 0
 
     def _key(self) -> tuple:
-        """What the library's tables depend on: the batch, the flags, q_len and
-        the pool's generation (the library rebuilds them when one changes)."""
+        """What the library's tables depend on: the batch, the flags, q_len, the
+        pool's generation and, for a mask of several tokens, the contexts'
+        lengths (the library rebuilds them when one changes)."""
         return (self._ids.tobytes(), self._flags, self.q_len, None if self.q_lens is None else tuple(self.q_lens),
-                self.pool._generation())
+                self.pool._generation(), self._lengths())
+
+    def _lengths(self):
+        """The contexts' lengths now, if a mask counts from them."""
+        if not self._flags & capi.CA_SCHED_CAUSAL or (self.q_len == 1 and self.q_lens is None):
+            return None
+        lens = array("i", bytes(4 * self.b))
+        found = capi.lib().ca_seq_lengths(self.pool._h, self.b, self._ids_ptr, _at(lens)) == capi.CA_OK
+        return lens.tobytes() if found else None     # (a sequence that is gone: the generation says so)
 
     def __del__(self):
         if getattr(self, "_h", None) is not None and self._h.value:
@@ -716,7 +725,8 @@ class DecodeGraph:
     the one captured: appending tokens that fit the sequences' partial last
     chunks keeps it (the kernels read each chunk's token count from the pool),
     while anything that rebuilds the schedule (a grown chunk, an insert or
-    remove, another batch) makes ``replay`` raise; capture again then."""
+    remove, another batch, any append under a causal mask of several tokens)
+    makes ``replay`` raise; capture again then."""
 
     def __init__(self, pool: Pool, sched: Schedule, calls, workspace=None, scale: float | None = None):
         import torch

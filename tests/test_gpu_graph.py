@@ -130,3 +130,45 @@ def test_default_stream_is_torchs_current_stream(torch_cuda):
     g.replay()
     torch.cuda.synchronize()
     assert x.sum().item() == 4
+
+
+def test_a_causal_graph_is_refused_after_an_append_in_place(torch_cuda):
+    """Its mask counts from the contexts' ends: before the schedule is built again
+    and after it the old graph's replay raises, and a new one's outputs are the
+    definition's.  Without a mask the graph goes on."""
+    from prefix_shared_decode_gb300 import CAError, DecodeGraph
+    torch = torch_cuda
+    c, H, D, L, b, m = 32, 4, 128, 1, 3, 4
+    pool, trie, rng = _tree(torch, 31, b, c, H, D, L, 500)
+    batch = list(range(b))
+
+    def append(sid, n, at):
+        k, v = (rng.standard_normal((L, n, H, D), dtype=np.float32).astype(np.float16) for _ in range(2))
+        toks = [10**6 + at + j for j in range(n)]
+        assert pool.append(sid, toks, torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda()) == trie.append(sid, toks, k, v)
+    for sid in batch:                                  # room for 4 tokens in each last chunk
+        append(sid, (c - pool.seq_len(sid) % c) % c + 5, 1000 * sid)
+    q = rng.standard_normal((b, m, H, D), dtype=np.float32).astype(np.float16)
+    qd = torch.from_numpy(q).cuda()
+    out, full = torch.empty_like(qd), torch.empty_like(qd)
+    sched, unmasked = pool.schedule(batch, q_len=m, causal=True), pool.schedule(batch, q_len=m)
+    graph, other = DecodeGraph(pool, sched, [(0, qd, out)]), DecodeGraph(pool, unmasked, [(0, qd, full)])
+
+    def check():
+        graph.replay()
+        other.replay()
+        torch.cuda.synchronize()
+        for got, causal in ((out, True), (full, False)):
+            assert_close(got.cpu().numpy(), A.decode_attention_multi(trie, batch, 0, q, 1 / np.sqrt(D), causal), f"causal={causal}")
+    check()
+    chunks = [pool.seq_slots(i) for i in batch]
+    append(1, m, 50000)
+    assert [pool.seq_slots(i) for i in batch] == chunks
+    with pytest.raises(CAError, match="STALE"):
+        graph.replay()
+    assert pool.schedule(batch, q_len=m, causal=True, reuse=sched) is sched
+    with pytest.raises(CAError, match="STALE"):
+        graph.replay()
+    graph = DecodeGraph(pool, sched, [(0, qd, out)])
+    check()
+    assert sched.device_status() == 0 and unmasked.device_status() == 0

@@ -289,3 +289,27 @@ def test_a_causal_schedule_is_built_again_after_an_append_in_place(lib):
         assert last_counts(masked) == before
         for s, kw in ((full, dict(q_len=4)), (one, dict(causal=True))):
             assert last_counts(pool.schedule(batch, reuse=s, **kw)) == {0: 5, 1: 3, 2: 9}
+
+
+def test_the_staleness_key_of_a_mask_holds_the_lengths(lib):
+    """An append in place moves a causal mask of several tokens, of either kind of
+    schedule; it leaves every other schedule's key, and a removed sequence still
+    gives a key."""
+    from prefix_shared_decode_gb300 import Pool
+    c = 16
+    pool = Pool(1, 8, 64, c, 100, host_only=True, n_kv_heads=2)
+    for i in range(2):
+        pool.insert(i, [1000 * i + j for j in range(c + 5)])
+    kinds = [dict(q_len=4, causal=True), dict(q_lens=[3, 7], causal=True), dict(q_lens=[1, 0], causal=True),
+             dict(q_len=4), dict(causal=True), dict(), dict(q_lens=[3, 7])]
+    scheds = [pool.schedule([1, 0], **kw) for kw in kinds]
+    keys = [s._key() for s in scheds]
+    assert [s._key() for s in scheds] == keys
+    assert pool.append(0, [7000]) == 0
+    moved = [s._key() != key for s, key in zip(scheds, keys)]
+    assert moved == [True] * 3 + [False] * 4
+    for s, kw, key, was in zip(scheds, kinds, keys, moved):
+        assert (pool.schedule([1, 0], reuse=s, **kw)._key() != key) == was
+    keys = [s._key() for s in scheds]
+    pool.remove(0)
+    assert all(s._key() != key for s, key in zip(scheds, keys))
