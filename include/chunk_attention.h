@@ -312,6 +312,13 @@ int ca_build_schedule_ex(ca_pool* pool, const int64_t* seq_ids, int32_t b, int32
                          uint32_t flags, ca_sched** inout, void* stream);
 int ca_sched_destroy(ca_sched* sched);
 
+/* How often the schedule's tables have been built: unchanged by a call that
+ * returned it untouched or failed before it changed anything.  A captured call
+ * belongs to the build that it was captured with, whatever the schedule holds
+ * now: tables that are built again, be it for the same batch after another, may
+ * lie elsewhere.  CA_ERR_INVALID on NULL arguments. */
+int ca_sched_builds(const ca_sched* sched, int64_t* builds_out);
+
 /* Table sizes, then the tables themselves (host copies; for bit-exact tests).
  * These are the per-step context the pages describe [CA §3.2: which chunks
  * the chunk-first phase takes and for which range of sequences; CA §3.3:

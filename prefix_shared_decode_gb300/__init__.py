@@ -452,6 +452,12 @@ class Schedule:
         return (self._ids.tobytes(), self._flags, self.q_len, None if self.q_lens is None else tuple(self.q_lens),
                 self.pool._generation(), self._lengths())
 
+    def _builds(self) -> int:
+        """How often the library has built the tables."""
+        n = C.c_int64()
+        check(capi.lib().ca_sched_builds(self._h, C.byref(n)), "ca_sched_builds")
+        return n.value
+
     def _lengths(self):
         """The contexts' lengths now, if a mask counts from them."""
         if not self._flags & capi.CA_SCHED_CAUSAL or (self.q_len == 1 and self.q_lens is None):
@@ -725,8 +731,9 @@ class DecodeGraph:
     the one captured: appending tokens that fit the sequences' partial last
     chunks keeps it (the kernels read each chunk's token count from the pool),
     while anything that rebuilds the schedule (a grown chunk, an insert or
-    remove, another batch, any append under a causal mask of several tokens)
-    makes ``replay`` raise; capture again then."""
+    remove, another batch or kind, even if this one is built again afterwards, any
+    append under a causal mask of several tokens) makes ``replay`` raise;
+    capture again then."""
 
     def __init__(self, pool: Pool, sched: Schedule, calls, workspace=None, scale: float | None = None):
         import torch
@@ -734,7 +741,9 @@ class DecodeGraph:
         self.calls = [(int(layer), q, out) for layer, q, out in calls]
         self.workspace = workspace if workspace is not None else sched.workspace()
         self.scale = scale
-        self._key = sched._key()
+        # (tables that other batches have been built over may lie elsewhere, although
+        # they are built for this one again: the key alone does not tell)
+        self._key, self._built = sched._key(), sched._builds()
         with torch.cuda.device(pool._device):    # (the calls run there, whatever device is current)
             side = torch.cuda.Stream()
             side.wait_stream(torch.cuda.current_stream())
@@ -753,7 +762,7 @@ class DecodeGraph:
     def replay(self) -> None:
         """Run every recorded call on the pool's device's current stream."""
         import torch
-        if self.sched._key() != self._key:
+        if self.sched._builds() != self._built or self.sched._key() != self._key:
             raise CAError(capi.CA_ERR_STALE, "DecodeGraph: the pool or the schedule changed after capture")
         with torch.cuda.device(self.pool._device):
             self.graph.replay()
