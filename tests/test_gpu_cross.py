@@ -347,3 +347,20 @@ def test_the_call_without_a_workspace_refuses_block_schedules(torch_cuda):
         assert capi.lib().ca_decode_attention_static_ws(x.pool.handle, sched.handle, 0, four.data_ptr(),
                                                         torch.empty_like(four).data_ptr(), 1.0, None) == -1
         check(x, [0, 1], blocks, q, 0, cross_attention(x.pool, sched, qd))
+
+
+def test_a_refused_build_leaves_the_schedule(torch_cuda):
+    """Its calls go on over the tables that were there, masked or not."""
+    from prefix_shared_decode_gb300 import CAError, cross_attention
+    torch = torch_cuda
+    x = Cache(torch, 9, "fp16", 32, 64, 2, 2, [70, 300])
+    for causal in (False, True):
+        sched = x.pool.schedule([0, 1], q_lens=[300, 4], causal=causal)
+        q, qd = queries(x, [300, 4], 4)
+        out = cross_attention(x.pool, sched, qd)
+        check(x, [0, 1], [300, 4], q, 0, out, causal)
+        for ids, lens in (([0, 9], [300, 4]), ([0, 1], [2**31 - 1, 1])):
+            with pytest.raises(CAError):
+                x.pool.schedule(ids, q_lens=lens, causal=causal, reuse=sched)
+            assert torch.equal(cross_attention(x.pool, sched, qd), out)
+        assert sched.device_status() == 0
