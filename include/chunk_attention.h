@@ -510,8 +510,8 @@ int ca_sparse_attention(const ca_pool* pool, const ca_sched* sched, int32_t laye
  * each.  flags: CA_SCHED_CAUSAL or 0.  Reuse, upload and errors as
  * ca_build_schedule (CA_ERR_INVALID also for a negative length,
  * CA_ERR_UNSUPPORTED for more than 2^31 rows).  Such a schedule serves
- * ca_cross_attention, ca_workspace_bytes and the status calls alone; the others
- * refuse it (CA_ERR_INVALID).
+ * ca_cross_attention, ca_workspace_bytes, ca_sched_builds and the calls for status,
+ * failure injection and profile events; the others refuse it (CA_ERR_INVALID).
  *
  * ca_cross_attention: q_dev / out_dev fp16 [sum of q_lens][n_heads][head_dim], block
  * after block, 16-byte aligned, not overlapping (CA_ERR_INVALID).  ws_dev as for ca_decode_attention

@@ -192,7 +192,6 @@ int build_blocks(const Pool& p, const int64_t* seq_ids, int32_t b, const int32_t
     s.ws.part_o = 0;
     s.ws.part_ms = align256((size_t)parts * T * D * sizeof(float));
     s.ws.total = s.ws.part_ms + align256((size_t)parts * T * 2 * sizeof(float));
-    s.ws.total_host = s.ws.weights_total = s.ws.total;
     return CA_OK;
 }
 

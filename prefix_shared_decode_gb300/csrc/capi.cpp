@@ -587,7 +587,7 @@ int ca_workspace_bytes(const ca_sched* s, size_t* bytes_out) {
 }
 
 int ca_workspace_bytes_host(const ca_sched* s, size_t* bytes_out) {
-    if (!s || !bytes_out) return CA_ERR_INVALID;
+    if (!s || !bytes_out || s->blocks) return CA_ERR_INVALID;
     *bytes_out = s->ws.total_host;
     return CA_OK;
 }
@@ -733,7 +733,7 @@ int ca_sparse_attention(const ca_pool* pool, const ca_sched* s, int32_t layer, c
 }
 
 int ca_workspace_bytes_weights(const ca_sched* s, size_t* bytes_out) {
-    if (!s || !bytes_out) return CA_ERR_INVALID;
+    if (!s || !bytes_out || s->blocks) return CA_ERR_INVALID;
     *bytes_out = s->ws.weights_total;
     return CA_OK;
 }

@@ -1,4 +1,5 @@
 """Schedules of query blocks on host-only pools: what is refused, and reuse."""
+import ctypes as C
 import os
 import shutil
 import subprocess
@@ -123,3 +124,13 @@ def test_builds_are_counted(lib):
         # the tables that were there still stand: they are not built again
         assert pool.schedule([0, 1], reuse=sched, **kw)._builds() == n
     assert lib.ca_sched_builds(None, None) == -1
+
+
+def test_the_other_calls_workspaces_are_refused(lib):
+    pool = make(lib)
+    n = C.c_size_t(7)
+    for kw in (dict(q_lens=[300, 4]), dict()):
+        sched = pool.schedule([0, 1], **kw)
+        for call in (lib.ca_workspace_bytes_host, lib.ca_workspace_bytes_weights):
+            assert call(sched.handle, C.byref(n)) == (-1 if kw else 0)
+        assert lib.ca_workspace_bytes(sched.handle, C.byref(n)) == 0
