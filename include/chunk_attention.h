@@ -508,8 +508,11 @@ int ca_sparse_attention(const ca_pool* pool, const ca_sched* sched, int32_t laye
  *
  * ca_build_schedule_blocks: seq_ids[0..b) may repeat; q_lens[i] >= 0 query tokens
  * each.  flags: CA_SCHED_CAUSAL or 0.  Reuse, upload and errors as
- * ca_build_schedule (CA_ERR_INVALID also for a negative length,
- * CA_ERR_UNSUPPORTED for more than 2^31 rows).  Such a schedule serves
+ * ca_build_schedule; CA_ERR_INVALID also for a negative length.  A block's query
+ * tokens times the group n_heads / n_kv_heads are cut into tiles of T = 256 rows (128
+ * at head_dim 256) for each key/value head; CA_ERR_UNSUPPORTED where a block has
+ * more than 2^31 - 1 - T such rows, or all blocks more than 2^31 - 1 query tokens,
+ * 2^31 - 1 chunks of context or 2^25 - 1 tiles.  Such a schedule serves
  * ca_cross_attention, ca_workspace_bytes, ca_sched_builds and the calls for status,
  * failure injection and profile events; the others refuse it (CA_ERR_INVALID).
  *

@@ -34,7 +34,7 @@ int build_blocks(const Pool& p, const int64_t* seq_ids, int32_t b, const int32_t
     const int32_t c = p.cfg.chunk, HK = kv_heads(p.cfg), G = p.cfg.n_heads / HK, T = cross_tile_rows(p.cfg);
     const bool causal = (flags & CA_SCHED_CAUSAL) != 0;
     std::vector<const Sequence*> seq(b);
-    int64_t rows = 0, chunks = 0;
+    int64_t rows = 0, chunks = 0, n_tiles = 0;
     for (int32_t i = 0; i < b; ++i) {
         auto it = p.seqs.find(seq_ids[i]);
         if (it == p.seqs.end()) return CA_ERR_NOT_FOUND;
@@ -43,8 +43,9 @@ int build_blocks(const Pool& p, const int64_t* seq_ids, int32_t b, const int32_t
         rows += q_lens[i];
         chunks += (int64_t)it->second.path.size();
         if ((int64_t)q_lens[i] * G > INT32_MAX - T) return CA_ERR_UNSUPPORTED;
+        n_tiles += ((int64_t)q_lens[i] * G + T - 1) / T;
     }
-    if (rows > INT32_MAX || chunks > INT32_MAX) return CA_ERR_UNSUPPORTED;
+    if (rows > INT32_MAX || chunks > INT32_MAX || n_tiles * HK > INT32_MAX / 64) return CA_ERR_UNSUPPORTED;
 
     // Tiles of each sequence's rows, and the chunks that each one reads.
     struct Tile { int32_t seq, row0, rows, chunks; };
@@ -65,7 +66,6 @@ int build_blocks(const Pool& p, const int64_t* seq_ids, int32_t b, const int32_t
         list0.push_back(list0.back() + (int32_t)seq[i]->path.size());
         q_off.push_back(q_off.back() + q_lens[i]);
     }
-    if ((int64_t)tiles.size() * HK > INT32_MAX / 64) return CA_ERR_UNSUPPORTED;
 
     // Every place on the card gets a list of items.  Either whole tiles, the
     // longest first, each to the place with least work so far; or, where that

@@ -134,3 +134,24 @@ def test_the_other_calls_workspaces_are_refused(lib):
         for call in (lib.ca_workspace_bytes_host, lib.ca_workspace_bytes_weights):
             assert call(sched.handle, C.byref(n)) == (-1 if kw else 0)
         assert lib.ca_workspace_bytes(sched.handle, C.byref(n)) == 0
+
+
+def test_sizes_past_32_bits_are_refused(lib):
+    """Before anything is built over them: the last case has 42 million tiles."""
+    import resource
+    from prefix_shared_decode_gb300 import CAError, Pool
+    pools = {}
+    for G, D, T in ((64, 128, 256), (32, 256, 128), (1, 64, 256)):
+        pools[G] = pool = Pool(1, G, D, 16, 20, host_only=True, n_kv_heads=1)
+        pool.insert(0, list(range(100)))
+        most = (2**31 - 1 - T) // G
+        before = resource.getrusage(resource.RUSAGE_SELF).ru_maxrss
+        for lens in ([most + 1], [3, most + 1], [2**31 - 1], [most] * 65):
+            with pytest.raises(CAError, match="UNSUPPORTED"):
+                pool.schedule([0] * len(lens), q_lens=lens)
+        assert resource.getrusage(resource.RUSAGE_SELF).ru_maxrss - before < 64 * 1024      # KB
+    most = (2**31 - 1 - 256) // 64
+    before = resource.getrusage(resource.RUSAGE_SELF).ru_maxrss
+    with pytest.raises(CAError, match="UNSUPPORTED"):
+        pools[64].schedule([0] * 5, q_lens=[most] * 5)
+    assert resource.getrusage(resource.RUSAGE_SELF).ru_maxrss - before < 64 * 1024
