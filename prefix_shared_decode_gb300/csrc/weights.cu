@@ -525,11 +525,13 @@ __global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const WeightPa
             w[k].w += weight(y[k].w, l);
         }
     }
+    // (a weight of 0 leaves the bits of the sum: past the context they are the caller's)
+    auto add = [](float s, float x) { return x == 0.f ? s : s + x; };
 #pragma unroll
     for (int k = 0; k < kAddPer; ++k) {
         const int t = token(k);
         if (t >= end) continue;
-        const float4 v = make_float4(sum[k].x + w[k].x, sum[k].y + w[k].y, sum[k].z + w[k].z, sum[k].w + w[k].w);
+        const float4 v = make_float4(add(sum[k].x, w[k].x), add(sum[k].y, w[k].y), add(sum[k].z, w[k].z), add(sum[k].w, w[k].w));
         if (wide) {
             if (t < wp.room) *reinterpret_cast<float4*>(wp.out + row + t) = v;
         } else {

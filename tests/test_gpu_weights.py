@@ -300,3 +300,26 @@ def test_causal_steps_that_append_in_place(torch_cuda, kv_dtype, c, D, G, Hkv, q
             k, v = held(x.k[i][0], x.kv_dtype, x.ks), held(x.v[i][0], x.kv_dtype, x.vs)
             near(out[r], OC.attention(q[r], k, v, D ** -0.5, True), OC.attention(q[r], k, np.abs(v), D ** -0.5, True))
     assert sched.device_status() == 0
+
+
+@pytest.mark.parametrize("room", [96, 99])
+def test_sums_behind_the_context_keep_their_bits(torch_cuda, room):
+    """In its last chunk and past it, whatever they are: minus zero, infinities, a
+    NaN with a payload."""
+    from prefix_shared_decode_gb300 import accumulate_attention
+    torch = torch_cuda
+    x = Cache(torch, 9, "fp16", 32, 64, 2, 2, [70, 33])
+    sched = x.pool.schedule([0, 1])
+    q, qd = queries(x, 2, 1, 4)
+    bits = torch.tensor([-2**31, 0x7f800000, -0x800000, 0x7fc01234, 1, -2**31 + 1], dtype=torch.int32, device="cuda")
+    w = bits.repeat(2 * 2 * room // 6 + 1)[:2 * 2 * room].view(2, 2, room).clone()
+    w[0, :, :70] = 0
+    w[1, :, :33] = 0
+    before, sums, out = w.clone(), w.view(torch.float32), torch.full((2, 2, room), 5.0, device="cuda")
+    accumulate_attention(x.pool, sched, qd, sums, out=out)
+    assert torch.equal(w, before)
+    accumulate_attention(x.pool, sched, qd, sums)
+    assert torch.equal(out.view(torch.int32), w)
+    for r, n in ((0, 70), (1, 33)):
+        assert torch.equal(w[r, :, n:], before[r, :, n:])
+        assert float((sums[r, :, :n].sum(-1) - 2).abs().max()) < 1e-4      # two query heads a sum
