@@ -583,7 +583,8 @@ int ca_accumulate_attention(const ca_pool* pool, const ca_sched* sched, int32_t 
  * CA_ERR_INVALID (a schedule without lists, budget < 1 or < sink + recent, a
  * room shorter than a context, repeated new ids, NULL or misaligned pointers);
  * CA_ERR_UNSUPPORTED (a budget or room above 2^31 - 4097).
- * On any error the pool is unchanged. */
+ * On any error the pool is unchanged; a launch that fails (CA_ERR_CUDA) may leave
+ * kept_dev and out_dev written. */
 int ca_evict(ca_pool* pool, const ca_sched* sched, const float* weights_dev, int32_t room,
              int32_t budget, int32_t sink, int32_t recent, const int64_t* into_ids,
              int32_t* kept_dev, float* out_dev, void* stream);

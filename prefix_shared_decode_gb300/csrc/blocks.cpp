@@ -21,11 +21,12 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // read, and its partial written and joined, whatever it holds); the tokens of a
 // step of the kernels; what an item costs whatever it reads, in tokens, and the
 // joining of pieces in a kernel of its own; and what a token costs a tile that
-// fills half of its rows at most.  From traced times of items (a step of 128
-// tokens some 1.8 us, an item's start and end 3, a join 5 to 8).  With them 32
-// tiles over 16384 tokens each are cut (52 us; each into equal pieces, 160 of them
-// on 152 places, 80), and 410 tiles over some 1220 tokens are not (64 us when it was
-// measured, cut 76).
+// fills half of its rows at most.  From traced times of items over fp16 pools at 128
+// dims (a step of 128 tokens some 1.8 us, an item's start and end 3, a join 5 to 8),
+// and taken for the other dims and pools too: a choice that they make badly costs
+// time alone.  With them 32 tiles over 16384 tokens each are cut (52 us; each into
+// equal pieces, 160 of them on 152 places, 80), and 448 tiles at 64 dims over some
+// 1220 tokens are not (64 us when it was measured, cut 76).
 constexpr int32_t kPieceTokens = 256, kStepTokens = 128;
 constexpr double kItemCost = 200, kJoinCost = 500, kHalfTileCost = 0.6;
 }  // namespace
