@@ -312,12 +312,12 @@ int ca_build_schedule_ex(ca_pool* pool, const int64_t* seq_ids, int32_t b, int32
                          uint32_t flags, ca_sched** inout, void* stream);
 int ca_sched_destroy(ca_sched* sched);
 
-/* How often the schedule's tables have been built: unchanged by a call that
- * returned it untouched or failed before it changed anything.  A captured call
- * belongs to the build that it was captured with, whatever the schedule holds
- * now: tables that are built again, be it for the same batch after another, may
- * lie elsewhere.  CA_ERR_INVALID on NULL arguments. */
-int ca_sched_builds(const ca_sched* sched, int64_t* builds_out);
+/* Where the schedule's tables lie on the device: what a captured call goes on
+ * reading.  Larger tables of another batch or kind move them, and those of the first
+ * batch, built again, then lie elsewhere too; a graph of before must not be
+ * replayed.  NULL for a host-only pool, and after a build that failed when it had
+ * begun to change them.  CA_ERR_INVALID on NULL arguments. */
+int ca_sched_tables(const ca_sched* sched, const void** tables_out);
 
 /* Table sizes, then the tables themselves (host copies; for bit-exact tests).
  * These are the per-step context the pages describe [CA §3.2: which chunks
@@ -513,7 +513,7 @@ int ca_sparse_attention(const ca_pool* pool, const ca_sched* sched, int32_t laye
  * at head_dim 256) for each key/value head; CA_ERR_UNSUPPORTED where a block has
  * more than 2^31 - 1 - T such rows, or all blocks more than 2^31 - 1 query tokens,
  * 2^31 - 1 chunks of context or 2^25 - 1 tiles.  Such a schedule serves
- * ca_cross_attention, ca_workspace_bytes, ca_sched_builds and the calls for status,
+ * ca_cross_attention, ca_workspace_bytes, ca_sched_tables and the calls for status,
  * failure injection and profile events; the others refuse it (CA_ERR_INVALID).
  *
  * ca_cross_attention: q_dev / out_dev fp16 [sum of q_lens][n_heads][head_dim], block

@@ -448,15 +448,12 @@ class Schedule:
     def _key(self) -> tuple:
         """What the library's tables depend on: the batch, the flags, q_len, the
         pool's generation and, for a mask of several tokens, the contexts'
-        lengths (the library rebuilds them when one changes)."""
+        lengths (the library rebuilds them when one changes); and where they lie
+        on the device, which another batch in between may have changed."""
+        at = self.__dict__.setdefault("_tables_buf", C.c_void_p())
+        check(capi.lib().ca_sched_tables(self._h, C.byref(at)), "ca_sched_tables")
         return (self._ids.tobytes(), self._flags, self.q_len, None if self.q_lens is None else tuple(self.q_lens),
-                self.pool._generation(), self._lengths())
-
-    def _builds(self) -> int:
-        """How often the library has built the tables."""
-        n = C.c_int64()
-        check(capi.lib().ca_sched_builds(self._h, C.byref(n)), "ca_sched_builds")
-        return n.value
+                self.pool._generation(), self._lengths(), at.value)
 
     def _lengths(self):
         """The contexts' lengths now, if a mask counts from them."""
@@ -731,9 +728,8 @@ class DecodeGraph:
     the one captured: appending tokens that fit the sequences' partial last
     chunks keeps it (the kernels read each chunk's token count from the pool),
     while anything that rebuilds the schedule (a grown chunk, an insert or
-    remove, another batch or kind, even if this one is built again afterwards, any
-    append under a causal mask of several tokens) makes ``replay`` raise;
-    capture again then."""
+    remove, another batch or kind, any append under a causal mask of several
+    tokens) makes ``replay`` raise; capture again then."""
 
     def __init__(self, pool: Pool, sched: Schedule, calls, workspace=None, scale: float | None = None):
         import torch
@@ -741,9 +737,7 @@ class DecodeGraph:
         self.calls = [(int(layer), q, out) for layer, q, out in calls]
         self.workspace = workspace if workspace is not None else sched.workspace()
         self.scale = scale
-        # (tables that other batches have been built over may lie elsewhere, although
-        # they are built for this one again: the key alone does not tell)
-        self._key, self._built = sched._key(), sched._builds()
+        self._key = sched._key()
         with torch.cuda.device(pool._device):    # (the calls run there, whatever device is current)
             side = torch.cuda.Stream()
             side.wait_stream(torch.cuda.current_stream())
@@ -762,7 +756,7 @@ class DecodeGraph:
     def replay(self) -> None:
         """Run every recorded call on the pool's device's current stream."""
         import torch
-        if self.sched._builds() != self._built or self.sched._key() != self._key:
+        if self.sched._key() != self._key:
             raise CAError(capi.CA_ERR_STALE, "DecodeGraph: the pool or the schedule changed after capture")
         with torch.cuda.device(self.pool._device):
             self.graph.replay()

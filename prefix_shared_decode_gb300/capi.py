@@ -29,7 +29,7 @@ CA_SCHED_CHUNK_LISTS = 4
 # Every symbol the header declares, in header order.
 EXPORTS = [
     "ca_pool_bytes", "ca_pool_bytes_ex", "ca_pool_create", "ca_pool_create_ex", "ca_pool_destroy", "ca_match_prefix", "ca_insert_tokens",
-    "ca_insert_batch", "ca_append_tokens", "ca_read_batch", "ca_remove_seq", "ca_remove_batch", "ca_pool_stats", "ca_seq_slots", "ca_seq_lengths", "ca_build_schedule", "ca_build_schedule_ex", "ca_sched_destroy", "ca_sched_builds",
+    "ca_insert_batch", "ca_append_tokens", "ca_read_batch", "ca_remove_seq", "ca_remove_batch", "ca_pool_stats", "ca_seq_slots", "ca_seq_lengths", "ca_build_schedule", "ca_build_schedule_ex", "ca_sched_destroy", "ca_sched_tables",
     "ca_sched_counts", "ca_export_tables", "ca_export_plan", "ca_workspace_bytes", "ca_decode_attention",
     "ca_workspace_bytes_host", "ca_decode_attention_host", "ca_decode_attention_static_ws",
     "ca_select_chunks", "ca_sparse_attention", "ca_build_schedule_blocks", "ca_cross_attention", "ca_workspace_bytes_weights", "ca_accumulate_attention", "ca_evict",
@@ -96,7 +96,7 @@ def lib() -> C.CDLL:
         "ca_build_schedule": [vp, P(i64), i32, P(vp), vp],
         "ca_build_schedule_ex": [vp, vp, i32, i32, u32, P(vp), vp],     # seq_ids: int64 array address
         "ca_sched_destroy": [vp],
-        "ca_sched_builds": [vp, P(i64)],
+        "ca_sched_tables": [vp, P(vp)],
         "ca_sched_counts": [vp, P(i32)],
         "ca_export_tables": [vp] + [P(i32)] * 7,
         "ca_export_plan": [vp, P(i32), P(i32), P(i32), P(i32), P(i32)],

@@ -247,7 +247,6 @@ struct Plan {
 struct Sched {
     const Pool* pool = nullptr;
     int64_t generation = -1;
-    int64_t builds = 0;                // times that the tables were built (ca_sched_builds)
     uint32_t flags = 0;
     int32_t q_len = 1;
     bool blocks = false;               // of query blocks: q_lens, items and joins instead of q_len, t and plan

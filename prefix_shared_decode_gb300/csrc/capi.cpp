@@ -436,7 +436,6 @@ int ca_build_schedule_ex(ca_pool* pool, const int64_t* seq_ids, int32_t b, int32
         // failure from here on leaves a schedule that every later call
         // rebuilds and every decode call refuses as stale.
         s->generation = -1;
-        ++s->builds;
         s->pool = pool;
         s->flags = flags;
         s->q_len = q_len;
@@ -488,12 +487,10 @@ int ca_build_schedule_blocks(ca_pool* pool, const int64_t* seq_ids, int32_t b, c
         }
         const int64_t was = s->generation;
         s->generation = -1;                 // (as above)
-        ++s->builds;
         alloc_point(*pool);
         int st = build_blocks(*pool, seq_ids, b, q_lens, flags, *s);
         if (st) {
             s->generation = was;            // its previous tables are untouched
-            --s->builds;
             return st;
         }
         s->pool = pool;
@@ -528,9 +525,9 @@ int ca_sched_destroy(ca_sched* sched) {
     return CA_OK;
 }
 
-int ca_sched_builds(const ca_sched* s, int64_t* builds_out) {
-    if (!s || !builds_out) return CA_ERR_INVALID;
-    *builds_out = s->builds;
+int ca_sched_tables(const ca_sched* s, const void** tables_out) {
+    if (!s || !tables_out) return CA_ERR_INVALID;
+    *tables_out = s->generation < 0 ? nullptr : s->dev;
     return CA_OK;
 }
 

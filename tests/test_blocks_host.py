@@ -100,32 +100,6 @@ def test_the_call_without_a_workspace_refuses_them(lib, tmp_path):
     assert plain[0] in ("-1", "-6") and plain[1] == "-1"     # no such device, or none at all
 
 
-def test_builds_are_counted(lib):
-    """What a captured graph is checked against: a schedule that served another batch
-    or kind in between has the same key as before, but its tables were built anew
-    (and may lie elsewhere); a reused one's, and those of a build that was refused,
-    are as they were."""
-    pool = make(lib)
-    sched = pool.schedule([0, 1])
-    key, n = sched._key(), sched._builds()
-    assert n == 1 and pool.schedule([0, 1], reuse=sched)._builds() == 1
-    pool.schedule([0, 1], q_lens=[300, 4], reuse=sched)
-    pool.schedule([0, 1], reuse=sched)
-    assert sched._key() == key and sched._builds() == 3
-    pool.schedule([0], reuse=sched)
-    pool.schedule([0, 1], reuse=sched)
-    assert sched._key() == key and sched._builds() == 5
-    for kw in (dict(), dict(q_lens=[300, 4]), dict(q_lens=[300, 4], causal=True)):
-        pool.schedule([0, 1], reuse=sched, **kw)
-        n = sched._builds()
-        for bad in (dict(), dict(q_lens=[1, 1])):
-            with pytest.raises(Exception, match="NOT_FOUND"):
-                pool.schedule([0, 9], reuse=sched, **bad)
-        # the tables that were there still stand: they are not built again
-        assert pool.schedule([0, 1], reuse=sched, **kw)._builds() == n
-    assert lib.ca_sched_builds(None, None) == -1
-
-
 def test_the_other_calls_workspaces_are_refused(lib):
     pool = make(lib)
     n = C.c_size_t(7)

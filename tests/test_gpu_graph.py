@@ -174,9 +174,10 @@ def test_a_causal_graph_is_refused_after_an_append_in_place(torch_cuda):
     assert sched.device_status() == 0 and unmasked.device_status() == 0
 
 
-def test_a_graph_is_refused_once_its_schedule_served_something_else(torch_cuda):
-    """Query blocks, or another batch, between the capture and the replay: the tables
-    of the captured call may lie elsewhere although the same batch is built again."""
+def test_a_graph_after_its_schedule_served_something_else(torch_cuda):
+    """Query blocks, or another batch, between the capture and the replay: a replay
+    raises, and where the tables have moved it still does once the same batch is
+    built again; where they have not, the graph serves it again."""
     from prefix_shared_decode_gb300 import CAError, DecodeGraph
     torch = torch_cuda
     c, H, D, L, b = 32, 4, 128, 1, 6
@@ -186,16 +187,21 @@ def test_a_graph_is_refused_once_its_schedule_served_something_else(torch_cuda):
     q = rng.standard_normal((b, H, D), dtype=np.float32).astype(np.float16)
     qd = torch.from_numpy(q).cuda()
     out = torch.empty_like(qd)
-    for between in (dict(seq_ids=batch, q_lens=[2000] * b), dict(seq_ids=batch[:2]), dict(seq_ids=batch, q_len=3)):
-        graph = DecodeGraph(pool, sched, [(0, qd, out)])
-        out.zero_()
-        graph.replay()
-        torch.cuda.synchronize()
-        assert_close(out.cpu().numpy(), A.decode_attention(trie, batch, 0, q, 1 / np.sqrt(D)), str(between))
+    want = A.decode_attention(trie, batch, 0, q, 1 / np.sqrt(D))
+    for between in (dict(seq_ids=batch[:2]), dict(seq_ids=batch, q_lens=[2000] * b), dict(seq_ids=batch, q_lens=[3] * b, causal=True),
+                    dict(seq_ids=batch, q_lens=[400000] * b)):
+        graph, key = DecodeGraph(pool, sched, [(0, qd, out)]), sched._key()
         pool.schedule(reuse=sched, **between)
         with pytest.raises(CAError, match="STALE"):
             graph.replay()
         pool.schedule(batch, reuse=sched)
-        with pytest.raises(CAError, match="STALE"):
+        assert sched._key()[:-1] == key[:-1]
+        if sched._key() != key:
+            with pytest.raises(CAError, match="STALE"):
+                graph.replay()
+        else:
+            out.zero_()
             graph.replay()
+            torch.cuda.synchronize()
+            assert_close(out.cpu().numpy(), want, str(between))
     assert sched.device_status() == 0

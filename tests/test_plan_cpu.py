@@ -3,6 +3,8 @@ oracle's partial triple and merge it through the exported partial-id CSR, in
 float64, and compare with the plain definition.  Any chunk dropped or counted
 twice, or a partial written to the wrong id, changes the result
 [ChunkAttention (arXiv 2402.15220v4 summary) §3.2]."""
+import ctypes as C
+
 import numpy as np
 import pytest
 
@@ -313,3 +315,28 @@ def test_the_staleness_key_of_a_mask_holds_the_lengths(lib):
     keys = [s._key() for s in scheds]
     pool.remove(0)
     assert all(s._key() != key for s, key in zip(scheds, keys))
+
+
+def test_the_staleness_key_holds_the_tables_address(lib, monkeypatch):
+    """Tables that another batch in between has moved are others, although they are
+    built for the same batch again."""
+    from prefix_shared_decode_gb300 import Pool
+    pool = Pool(1, 2, 64, 16, 100, host_only=True)
+    for i in range(2):
+        pool.insert(i, [1000 * i + j for j in range(20)])
+    s = pool.schedule([0, 1])
+    key, at = s._key(), C.c_void_p(5)
+    assert lib.ca_sched_tables(s.handle, C.byref(at)) == 0 and at.value is None       # a host-only pool
+    assert lib.ca_sched_tables(None, C.byref(at)) == -1 and lib.ca_sched_tables(s.handle, None) == -1
+    pool.schedule([0, 1], q_lens=[300, 2], reuse=s)
+    assert pool.schedule([0, 1], reuse=s)._key() == key
+    where = [4096]
+
+    def tables(sched, out):
+        out._obj.value = where[0]
+        return 0
+    monkeypatch.setattr(lib, "ca_sched_tables", tables)
+    key = s._key()
+    assert s._key() == key
+    where[0] = 8192
+    assert s._key() != key
